@@ -88,6 +88,7 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_MXFP8 = 2 } pkv_dtype;
 #define PKV_DEVERR_BLOCK 2u    /* a block id outside [0, num_blocks)             */
 #define PKV_DEVERR_LENGTH 4u   /* a length < 0 or beyond its block table row     */
 #define PKV_DEVERR_TIMEOUT 8u  /* a bounded wait inside a kernel ran out         */
+#define PKV_DEVERR_KEEP 16u    /* a kept row out of range or out of order       */
 
 /* Shape of one paged K/V pool (host struct, passed by pointer). */
 typedef struct {
@@ -391,6 +392,149 @@ pkv_status pkv_paged_attention_decode_static(
     const void* k_cache, const void* v_cache, const int32_t* block_tables,
     int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs,
     int32_t num_q_heads, float scale, int32_t partition_size, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Drafted tokens: attention of a tree of them over the cache.
+ * (The paper has no counterpart; the layout, the block tables and the row
+ * visibility rules are those of the decode.)
+ *
+ * A speculative step appends a sequence's drafted tokens behind its committed
+ * rows (pkv_kv_append, positions ctx, ctx + 1, ...), attends them all at
+ * once with this call, and moves the accepted path's rows together with
+ * pkv_kv_compact. */
+
+/* Drafted tokens of one sequence at most (one mask bit each). */
+#define PKV_MAX_DRAFT 64
+
+/* Bytes of device workspace pkv_draft_tree_attention needs for these sizes;
+ * 0 for unsupported or invalid sizes.  Depends on the device (its SM count). */
+size_t pkv_draft_tree_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
+                                      int32_t num_q_heads, int32_t max_draft,
+                                      int32_t max_blocks_per_seq);
+
+/* Attention of every sequence's drafted tokens over its context and their
+ * drafted ancestors.  Sequence r holds ctx_lens[r] committed rows and n =
+ * draft_ptr[r + 1] - draft_ptr[r] drafted ones at positions ctx_lens[r] + 0
+ * .. n - 1.  Its i-th drafted token is query row draft_ptr[r] + i, and
+ *   out[row, h] = sum_{t in A} softmax_t(scale * q[row, h] . K_r[t]) V_r[t],
+ *   lse[row, h] = log sum_{t in A} exp(scale * q[row, h] . K_r[t]),
+ *   A = {t < ctx_lens[r]} and {ctx_lens[r] + j : j < n, bit j of masks[row]}
+ * for kv head h / (Hq / Hkv).  A row outside A contributes nothing, whatever
+ * its bytes (NaN and infinities included).  A query row that sees no row at
+ * all (no context, an empty mask) gives out = 0 and lse = -inf.
+ *   out:           [num_rows, Hq, D]; rows of no sequence are not written.
+ *   lse:           float [num_rows, Hq] natural-log LSE, or NULL.
+ *   q:             [num_rows, Hq, D].
+ *   block_tables:  int32 [num_seqs, max_blocks_per_seq]; entries past
+ *                  ceil((ctx_lens[r] + n) / P) are never read.
+ *   ctx_lens:      int32 [num_seqs], committed rows (0 allowed).
+ *   draft_ptr:     int32 [num_seqs + 1], ascending: the query rows of each
+ *                  sequence (an empty range is allowed).
+ *   masks:         uint64 [num_rows]: bit j set lets the row see drafted row
+ *                  j of its own sequence (a tree sets the bits of the row
+ *                  itself and of its ancestors), or NULL for a chain (bits 0
+ *                  .. i).  Bits at and past n are ignored.
+ *   num_rows:      query rows, >= draft_ptr[num_seqs].
+ *   max_draft:     upper bound of n over the sequences, 1 .. PKV_MAX_DRAFT.
+ *   workspace:     at least pkv_draft_tree_workspace_bytes, 256-byte aligned;
+ *                  nothing in it needs to be initialised.
+ * A sequence whose range descends, is longer than max_draft, passes num_rows,
+ * or ends beyond its block table row sets PKV_DEVERR_LENGTH and its query
+ * rows are not written.
+ * Supported: block_size 16 or a multiple of 32 up to 256; head_dim 64 or 128;
+ * Hq / Hkv in {1, 2, 4, 8}; num_seqs <= 65535; every cache dtype. */
+pkv_status pkv_draft_tree_attention(
+    const pkv_cache_desc* cache, void* out, float* lse, const void* q, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* ctx_lens, const int32_t* draft_ptr, const uint64_t* masks, int32_t num_seqs,
+    int32_t num_rows, int32_t max_draft, int32_t num_q_heads, float scale, void* workspace,
+    size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Keeping the cache inside a budget: eviction by accumulated attention weight.
+ * (The paper has no counterpart.)
+ *
+ * Decode with pkv_paged_attention_decode_weights, which keeps a running score
+ * of every cached row; when a sequence outgrows its budget, choose the rows to
+ * keep with pkv_kv_evict_select and move them together, in place, with
+ * pkv_kv_compact; the sequence then has new_lens[r] rows, and the blocks past
+ * ceil(new_lens[r] / P) are free.  Rows are chosen per kv head: after a
+ * compaction row j of two kv heads may hold different tokens. */
+
+/* Bytes of device workspace pkv_paged_attention_decode_weights needs; 0 for
+ * unsupported or invalid sizes. */
+size_t pkv_decode_weights_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
+                                          int32_t num_q_heads, int32_t max_blocks_per_seq);
+
+/* pkv_paged_attention_decode, and beside it for every kv head c and row t <
+ * seq_lens[r]
+ *   weights[r, c, t] = decay * weights[r, c, t]
+ *                      + sum_h exp(scale * q[r, h] . K_r[t] - lse[r, h])
+ * over the Hq / Hkv query heads h of c: the attention weight the row got in
+ * this step, added to its running score.
+ *   weights:        float [num_seqs, Hkv, weights_stride], read and written;
+ *                   entries at t >= seq_lens[r] are left as they are (start
+ *                   them at 0).  One buffer row per batch row, whether
+ *                   or not sequences share blocks.
+ *   weights_stride: elements between kv heads, >= 1; a sequence longer than it
+ *                   sets PKV_DEVERR_LENGTH and its rows past it are not
+ *                   weighed.
+ *   decay:          finite; 1 keeps a plain sum.
+ * A row of a block id outside the pool is not weighed.  Other arguments,
+ * support and errors as in pkv_paged_attention_decode (partition_size 0). */
+pkv_status pkv_paged_attention_decode_weights(
+    const pkv_cache_desc* cache, void* out, float* lse, float* weights, int64_t weights_stride,
+    float decay, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+    int32_t num_seqs, int32_t num_q_heads, float scale, void* workspace, size_t workspace_bytes,
+    void* stream);
+
+/* Choose the rows each (sequence, kv head) keeps within `budget`.  A sequence
+ * of T = seq_lens[r] <= budget rows keeps them all.  A longer one keeps its
+ * first num_sinks rows, its last num_recent, and of those between the budget -
+ * num_sinks - num_recent with the largest weights (equal weights: the lowest
+ * row; -0 equals 0; NaN is below every number).
+ *   weights:   float [num_seqs, num_kv_heads, weights_stride].
+ *   seq_lens:  int32 [num_seqs]; outside [0, weights_stride] it is clamped and
+ *              PKV_DEVERR_LENGTH set.
+ *   budget:    >= 1, >= num_sinks + num_recent (both >= 0).
+ *   keep:      int32 [num_seqs, num_kv_heads, budget], written whole: the kept
+ *              rows in ascending order, then -1.
+ *   new_lens:  int32 [num_seqs], written: min(T, budget).
+ * Exact and deterministic.  num_seqs and num_kv_heads <= 65535. */
+pkv_status pkv_kv_evict_select(const float* weights, int64_t weights_stride,
+                               const int32_t* seq_lens, int32_t num_seqs, int32_t num_kv_heads,
+                               int32_t budget, int32_t num_sinks, int32_t num_recent,
+                               int32_t* keep, int32_t* new_lens, void* stream);
+
+/* Move kept rows together, in place: for every sequence r, kv head c and j <
+ * keep_lens[r], row base + keep[r, c, j] of K and V (and of weights) moves to
+ * row base + j, base = base_lens[r].  After an eviction base is 0 and each kv
+ * head has its list; after a speculative step base is the committed length and
+ * one list (keep_heads = 1), the accepted path, serves every kv head.
+ *   weights:    float [num_seqs, Hkv, weights_stride] or NULL: moved alike,
+ *               and rows base + keep_lens[r] .. seq_lens[r] - 1 set to 0.
+ *   seq_lens:   int32 [num_seqs], rows before the call.  K and V rows from
+ *               base + keep_lens[r] on keep their bytes.
+ *   base_lens:  int32 [num_seqs] or NULL (0): rows below it stay.
+ *   keep:       int32 [num_seqs, keep_heads, keep_stride], ascending, so
+ *               keep[j] >= j; entries from keep_lens[r] on are never read.
+ *   keep_heads: 1 or num_kv_heads.
+ *   keep_lens:  int32 [num_seqs].
+ * The blocks written to must belong to one sequence alone: copy shared ones on
+ * write first (pkv_kv_block_copy).  An entry that is out of range or order
+ * sets PKV_DEVERR_KEEP, one in a block id outside the pool PKV_DEVERR_BLOCK;
+ * such rows are not moved.  A sequence with keep_lens[r] outside [0,
+ * seq_lens[r] - base], base outside [0, seq_lens[r]], or (with weights) more
+ * rows than weights_stride sets PKV_DEVERR_LENGTH and is skipped.
+ * Bit-exact.  Any block_size; head_dim x element a multiple of 16 bytes (MXFP8:
+ * head_dim a multiple of 32).  num_seqs and num_kv_heads <= 65535. */
+pkv_status pkv_kv_compact(const pkv_cache_desc* cache, void* k_cache, void* v_cache,
+                          float* weights, int64_t weights_stride, const int32_t* block_tables,
+                          int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                          const int32_t* base_lens, const int32_t* keep, int32_t keep_heads,
+                          int64_t keep_stride, const int32_t* keep_lens, int32_t num_seqs,
+                          void* stream);
 
 /* Read and clear the device error word of the current device.  Synchronises
  * `stream` first.  *code_out receives the PKV_DEVERR_* bits seen since the

@@ -32,6 +32,8 @@ CUDA_SOURCES = [
     "kernels/decode_tc_mx.cu",
     "kernels/prefix_tc.cu",
     "kernels/tree.cu",
+    "kernels/draft.cu",
+    "kernels/evict.cu",
 ]
 # Attention kernels take exp2/log2/division from the hardware approximations
 # (softmax in base 2, well inside the attention tolerance).
@@ -41,6 +43,8 @@ PER_SOURCE_FLAGS = {
     "kernels/decode_tc_mx.cu": ["--use_fast_math"],
     "kernels/prefix_tc.cu": ["--use_fast_math"],
     "kernels/tree.cu": ["--use_fast_math"],
+    "kernels/draft.cu": ["--use_fast_math"],
+    "kernels/evict.cu": ["--use_fast_math"],
 }
 
 LIB = os.path.join(HERE, "libpkv.so")

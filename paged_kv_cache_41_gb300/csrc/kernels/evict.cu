@@ -1,0 +1,334 @@
+// evict.cu -- keeping a paged cache inside a budget: the running attention
+// weight of every cached row, the choice of the rows to keep by it, and the
+// move of the kept rows together.
+#include <math.h>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace pkv {
+
+// ------------------------------------------------------------------ weighing
+// weights[r, c, t] = decay * weights[r, c, t] + sum over the G query heads h
+// of kv head c of exp(s_ht - lse_h), s_ht = scale q_h . k_t.  One warp per
+// cached row: its lanes hold D / 32 elements each, the G scores are summed
+// across the lanes.
+template <typename T, typename TQ, int D>
+__global__ void __launch_bounds__(256) weigh_kernel(const WeighArgs a) {
+  constexpr int EPL = D / 32;
+  pdl_wait();
+  const int r = blockIdx.z, c = blockIdx.y, P = a.block_size, Hkv = a.num_kv_heads;
+  const int G = a.num_q_heads / Hkv;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, P, a.err, false);
+  if (len > a.weights_stride && blockIdx.x == 0 && c == 0 && threadIdx.x == 0)
+    atomicOr(a.err, PKV_DEVERR_LENGTH);
+  const int64_t n = len < a.weights_stride ? len : a.weights_stride;
+  for (int64_t t = (int64_t)blockIdx.x * 8 + warp; t < n; t += (int64_t)gridDim.x * 8) {
+    const int blk = __ldg(a.block_tables + (int64_t)r * a.max_blocks + t / P);
+    if (blk < 0 || (int64_t)blk >= a.num_blocks) continue;  // the decode reports it
+    float kf[EPL];
+    const T* kp = static_cast<const T*>(a.k) + (((int64_t)blk * P + t % P) * Hkv + c) * D + lane * EPL;
+#pragma unroll
+    for (int e = 0; e < EPL; ++e) kf[e] = (float)kp[e];
+    if constexpr (sizeof(T) == 1) {
+      const float sc = e8m0_value(__ldg(a.k_scales + (((int64_t)blk * Hkv + c) * P + t % P) * (D / 32) + lane * EPL / 32));
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) kf[e] *= sc;
+    }
+    float sum = 0.f;
+    for (int g = 0; g < G; ++g) {
+      const int64_t qh = (int64_t)r * a.num_q_heads + c * G + g;
+      const TQ* qp = static_cast<const TQ*>(a.q) + qh * D + lane * EPL;
+      float s = 0.f;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) s = fmaf((float)qp[e] * a.qscale, kf[e], s);
+#pragma unroll
+      for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
+      sum += exp2f(s - __ldg(a.lse + qh) * 1.4426950408889634f);
+    }
+    if (lane == 0) {
+      float* w = a.weights + ((int64_t)r * Hkv + c) * a.weights_stride + t;
+      *w = fmaf(a.decay, *w, sum);
+    }
+  }
+}
+
+template <typename T, typename TQ>
+static cudaError_t launch_weigh_t(int head_dim, const WeighArgs& a, cudaStream_t stream) {
+  const int64_t rows = (int64_t)a.max_blocks * a.block_size;
+  const int64_t x = (rows + 63) / 64;  // eight rows per warp at least
+  const dim3 grid((unsigned)(x < 1024 ? x : 1024), (unsigned)a.num_kv_heads, (unsigned)a.num_seqs);
+  return head_dim == 128 ? launch_pdl(weigh_kernel<T, TQ, 128>, grid, dim3(256), 0, stream, a)
+                         : launch_pdl(weigh_kernel<T, TQ, 64>, grid, dim3(256), 0, stream, a);
+}
+
+cudaError_t launch_weigh(int dtype, int head_dim, const WeighArgs& a, cudaStream_t stream) {
+  switch (dtype) {
+    case PKV_F32: return launch_weigh_t<float, float>(head_dim, a, stream);
+    case PKV_BF16: return launch_weigh_t<__nv_bfloat16, __nv_bfloat16>(head_dim, a, stream);
+    default: return launch_weigh_t<__nv_fp8_e4m3, __nv_bfloat16>(head_dim, a, stream);
+  }
+}
+
+// ------------------------------------------------------------------ selection
+// Of the rows t < T of one (sequence, kv head): all where T <= budget, else
+// the first num_sinks, the last num_recent and the k = budget - sinks -
+// recent heaviest of those between, ties to the lowest index.
+//
+// The k-th largest weight is found by radix selection on an order-preserving
+// integer key, eight bits a pass; the last pass writes the kept indices in
+// ascending order, from the running counts of rows above the key and at it.
+namespace {
+
+constexpr int kSelThreads = 1024;
+
+// Larger weight, larger key: -0 counts as +0 and NaN below everything.  Takes
+// the weight's bits, and they are loaded as integers: float operations would
+// take subnormal weights for zero here.
+__device__ __forceinline__ uint32_t weight_key(uint32_t u) {
+  const uint32_t mag = u & 0x7fffffffu;
+  if (mag > 0x7f800000u) return 0u;
+  return (u & 0x80000000u) && mag ? ~u : (mag | 0x80000000u);
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectArgs a) {
+  __shared__ uint32_t hist[256];
+  __shared__ uint32_t warp_sum[32];
+  __shared__ uint32_t found[2];
+  const int c = blockIdx.x, r = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int T = __ldg(a.seq_lens + r);
+  if (T < 0 || T > a.weights_stride) {
+    if (c == 0 && tid == 0) atomicOr(a.err, PKV_DEVERR_LENGTH);
+    T = T < 0 ? 0 : (int)a.weights_stride;
+  }
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(a.weights) +
+                      ((int64_t)r * a.num_kv_heads + c) * a.weights_stride;
+  int32_t* keep = a.keep + ((int64_t)r * a.num_kv_heads + c) * a.budget;
+  const int kept = min(T, a.budget);
+  if (c == 0 && tid == 0) a.new_lens[r] = kept;
+  for (int j = kept + tid; j < a.budget; j += kSelThreads) keep[j] = -1;
+  if (T <= a.budget) {
+    for (int j = tid; j < T; j += kSelThreads) keep[j] = j;
+    return;
+  }
+  const int lo = a.num_sinks, hi = T - a.num_recent;  // candidates: [lo, hi)
+  uint32_t need = (uint32_t)(a.budget - a.num_sinks - a.num_recent);  // < hi - lo
+  uint32_t prefix = 0, mask = 0;  // the key's bits found so far
+  if (need > 0) {
+    for (int shift = 24; shift >= 0; shift -= 8) {
+      if (tid < 256) hist[tid] = 0;
+      __syncthreads();
+      for (int t = lo + tid; t < hi; t += kSelThreads) {
+        const uint32_t key = weight_key(__ldg(w + t));
+        if ((key & mask) == prefix) atomicAdd(&hist[(key >> shift) & 255u], 1u);
+      }
+      __syncthreads();
+      if (tid < 32) {  // lane l: bins 8 l .. 8 l + 7, from the top
+        uint32_t mine = 0;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) mine += hist[255 - (8 * lane + i)];
+        uint32_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        uint32_t before = inc - mine;
+        if (before < need && need <= inc) {
+#pragma unroll 1
+          for (int i = 0; i < 8; ++i) {
+            const uint32_t n = hist[255 - (8 * lane + i)];
+            if (need <= before + n) {
+              found[0] = 255 - (8 * lane + i);
+              found[1] = need - before;
+              break;
+            }
+            before += n;
+          }
+        }
+      }
+      __syncthreads();
+      prefix |= found[0] << shift;
+      mask |= 255u << shift;
+      need = found[1];
+    }
+  } else {
+    prefix = 0xffffffffu;  // no candidate is kept: no key is above this one
+  }
+  // keep every key above `prefix`, and the first `need` at it
+  uint32_t above = 0, at = 0;  // so far: kept for certain, and at the key
+  for (int base = 0; base < T; base += kSelThreads) {
+    const int t = base + tid;
+    uint32_t v = 0;
+    if (t < T) {
+      if (t < lo || t >= hi) {
+        v = 1u << 16;
+      } else {
+        const uint32_t key = weight_key(__ldg(w + t));
+        v = key > prefix ? 1u << 16 : (key == prefix ? 1u : 0u);
+      }
+    }
+    uint32_t inc = v;  // counts above in the upper half, at the key in the lower
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    uint32_t pre = 0, total = 0;
+    for (int i = 0; i < 32; ++i) {
+      const uint32_t x = warp_sum[i];
+      if (i < warp) pre += x;
+      total += x;
+    }
+    const uint32_t ex = pre + inc - v;
+    const uint32_t my_above = above + (ex >> 16), my_at = at + (ex & 0xffffu);
+    if ((v >> 16) || ((v & 1u) && my_at < need)) keep[my_above + min(my_at, need)] = t;
+    above += total >> 16;
+    at += total & 0xffffu;
+    __syncthreads();
+  }
+}
+
+cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
+  evict_select_kernel<<<dim3((unsigned)a.num_kv_heads, (unsigned)a.num_seqs), kSelThreads, 0, stream>>>(a);
+  return cudaGetLastError();
+}
+
+// ------------------------------------------------------------------ compaction
+// Row base + keep[j] moves to row base + j, keep ascending (so keep[j] >= j),
+// in place.  One CTA walks the rows of one (sequence, kv head) of K, of V or
+// of the weights in order, a tile of them at a time: all loads of a tile are
+// done before its stores.  A tile's stores reach only rows below the next
+// tile's first destination, and a later tile's sources are at or above its
+// destinations, so no load ever meets a store of another row.
+namespace {
+
+constexpr int kCmThreads = 256;
+constexpr int kCmVecs = 4;  // 16-byte vectors per thread and tile
+
+struct CompactSeq {
+  int base, n, len;  // first row, kept rows, rows in all (0: skip)
+};
+
+__device__ __forceinline__ CompactSeq compact_seq(const CompactArgs& a, int r, bool report) {
+  CompactSeq s;
+  s.len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, a.block_size, a.err, report);
+  s.base = a.base_lens ? __ldg(a.base_lens + r) : 0;
+  s.n = __ldg(a.keep_lens + r);
+  const bool ok = s.base >= 0 && s.base <= s.len && s.n >= 0 && s.n <= s.len - s.base &&
+                  s.n <= a.keep_stride && (!a.weights || s.len <= a.weights_stride);
+  if (!ok) {
+    if (report) atomicOr(a.err, PKV_DEVERR_LENGTH);
+    s.n = 0;
+    s.len = s.base = 0;
+  }
+  return s;
+}
+
+// keep[j], or -1 where it is out of range or order (reported).
+__device__ __forceinline__ int kept_row(const CompactArgs& a, const CompactSeq& s,
+                                        const int32_t* keep, int j) {
+  const int k = __ldg(keep + j);
+  const int prev = j > 0 ? __ldg(keep + j - 1) : -1;
+  if (k >= j && k > prev && k < s.len - s.base) return k;
+  atomicOr(a.err, PKV_DEVERR_KEEP);
+  return -1;
+}
+
+// Pool row of position t of sequence r, or -1 for a bad block id (reported).
+__device__ __forceinline__ int64_t pool_row(const CompactArgs& a, int r, int t) {
+  const int blk = __ldg(a.block_tables + (int64_t)r * a.max_blocks + t / a.block_size);
+  if (blk < 0 || (int64_t)blk >= a.num_blocks) {
+    atomicOr(a.err, PKV_DEVERR_BLOCK);
+    return -1;
+  }
+  return (int64_t)blk * a.block_size + t % a.block_size;
+}
+
+}  // namespace
+
+__global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArgs a) {
+  const int h = blockIdx.x, role = blockIdx.y, r = blockIdx.z;
+  const int tid = threadIdx.x, Hkv = a.num_kv_heads;
+  const CompactSeq s = compact_seq(a, r, h == 0 && role == 0 && tid == 0);
+  const int32_t* keep = a.keep + ((int64_t)r * a.keep_heads + (a.keep_heads > 1 ? h : 0)) * a.keep_stride;
+  if (role < 2) {
+    unsigned char* pool = role == 0 ? a.k : a.v;
+    const int vpr = a.row_bytes / 16;  // vectors per row
+    const int64_t total = (int64_t)s.n * vpr;
+    const int rows = kCmThreads * kCmVecs / vpr > 0 ? kCmThreads * kCmVecs / vpr : 1;
+    const int64_t step = (int64_t)rows * vpr;  // whole rows a tile
+    for (int64_t i0 = 0; i0 < total; i0 += step) {
+      // a row longer than a tile's vectors is moved in several turns
+      for (int64_t u0 = 0; u0 < step; u0 += kCmThreads * kCmVecs) {
+        uint4 x[kCmVecs];
+        int64_t dst[kCmVecs];
+#pragma unroll
+        for (int u = 0; u < kCmVecs; ++u) {
+          const int64_t off = u0 + u * kCmThreads + tid;
+          const int64_t i = i0 + off;
+          dst[u] = -1;
+          if (off >= step || i >= total) continue;
+          const int j = (int)(i / vpr), c = (int)(i % vpr);
+          const int k = kept_row(a, s, keep, j);
+          if (k < 0 || k == j) continue;
+          const int64_t from = pool_row(a, r, s.base + k), to = pool_row(a, r, s.base + j);
+          if (from < 0 || to < 0) continue;
+          x[u] = *reinterpret_cast<const uint4*>(pool + (from * Hkv + h) * a.row_bytes + c * 16);
+          dst[u] = (to * Hkv + h) * a.row_bytes + c * 16;
+        }
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kCmVecs; ++u)
+          if (dst[u] >= 0) *reinterpret_cast<uint4*>(pool + dst[u]) = x[u];
+      }
+    }
+    if (a.k_scales) {  // the rows' scales: [NB, Hkv, P, scale_bytes]
+      unsigned char* sc = role == 0 ? a.k_scales : a.v_scales;
+      const int P = a.block_size, sb = a.scale_bytes;
+      for (int64_t i0 = 0; i0 < (int64_t)s.n * sb; i0 += kCmThreads / sb * sb) {
+        const int64_t i = i0 + tid;
+        unsigned char x = 0;
+        int64_t dst = -1;
+        if (tid < kCmThreads / sb * sb && i < (int64_t)s.n * sb) {
+          const int j = (int)(i / sb), c = (int)(i % sb);
+          const int k = kept_row(a, s, keep, j);
+          if (k >= 0 && k != j) {
+            const int64_t from = pool_row(a, r, s.base + k), to = pool_row(a, r, s.base + j);
+            if (from >= 0 && to >= 0) {
+              x = sc[((from / P * Hkv + h) * P + from % P) * sb + c];
+              dst = ((to / P * Hkv + h) * P + to % P) * sb + c;
+            }
+          }
+        }
+        __syncthreads();
+        if (dst >= 0) sc[dst] = x;
+      }
+    }
+  } else {
+    float* w = a.weights + ((int64_t)r * Hkv + h) * a.weights_stride + s.base;
+    for (int j0 = 0; j0 < s.n; j0 += kCmThreads) {
+      const int j = j0 + tid;
+      const int k = j < s.n ? kept_row(a, s, keep, j) : -1;
+      const float x = k >= 0 ? w[k] : 0.f;
+      __syncthreads();
+      if (k >= 0) w[j] = x;
+    }
+    __syncthreads();  // every source has been read
+    for (int j = s.n + tid; j < s.len - s.base; j += kCmThreads) w[j] = 0.f;
+  }
+}
+
+cudaError_t launch_kv_compact(const CompactArgs& a, cudaStream_t stream) {
+  kv_compact_kernel<<<dim3((unsigned)a.num_kv_heads, a.weights ? 3u : 2u, (unsigned)a.num_seqs), kCmThreads, 0,
+                      stream>>>(a);
+  return cudaGetLastError();
+}
+
+}  // namespace pkv

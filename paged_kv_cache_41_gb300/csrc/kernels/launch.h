@@ -233,6 +233,106 @@ cudaError_t launch_prefix_attention(int head_dim, int group, int num_splits,
                                     const PrefixArgs& args, cudaStream_t stream);
 size_t prefix_smem_bytes(int head_dim, int split_len, int block_size);
 
+// Arguments of the draft-tree attention kernels (draft.cu).
+struct DraftArgs {
+  const void* q;                // [num_rows, Hq, D] (bf16 beside an MXFP8 pool)
+  const void* k;                // the pools [NB, P, Hkv, D]
+  const void* v;
+  const uint8_t* k_scales;      // MXFP8 pools: the scale planes
+  const uint8_t* v_scales;
+  const int32_t* block_tables;  // [B, max_blocks]
+  const int32_t* ctx_lens;      // [B] committed rows
+  const int32_t* draft_ptr;     // [B + 1] query rows of each sequence
+  const uint64_t* masks;        // [num_rows], or null: a chain
+  void* out;                    // [num_rows, Hq, D]
+  float* lse_out;               // [num_rows, Hq] natural log, or null
+  unsigned int* err;
+  float* rec_o;                 // split states [B, max_draft, Hq, num_splits, D]
+  float* rec_lse;               // [B, max_draft, Hq, num_splits], base 2
+  int64_t num_blocks;
+  int32_t max_blocks;
+  int32_t num_seqs;
+  int32_t num_rows;
+  int32_t max_draft;            // drafted rows of a sequence at most
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t block_size;
+  int32_t num_splits;
+  float qscale;                 // softmax scale * log2(e)
+};
+cudaError_t launch_draft_simt(int dtype, int head_dim, const DraftArgs& args, cudaStream_t stream);
+// (token, query head) rows per CTA where a kv head has `rows` of them at most.
+int draft_simt_rows(int rows);
+
+// The score update of a weighing decode (evict.cu): for every sequence r, kv
+// head c and row t < seq_lens[r],
+//   weights[r, c, t] = decay * weights[r, c, t] + sum_h exp(s_ht - lse_h)
+// over the G query heads h of c.
+struct WeighArgs {
+  const void* q;                // [B, Hq, D]
+  const void* k;                // the K pool
+  const uint8_t* k_scales;      // MXFP8 pools
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const float* lse;             // [B, Hq] natural log
+  float* weights;               // [B, Hkv, weights_stride]
+  unsigned int* err;
+  int64_t weights_stride;
+  int64_t num_blocks;
+  int32_t max_blocks;
+  int32_t num_seqs;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t block_size;
+  float qscale;                 // softmax scale * log2(e)
+  float decay;
+};
+cudaError_t launch_weigh(int dtype, int head_dim, const WeighArgs& args, cudaStream_t stream);
+
+// The choice of an eviction (evict.cu); see pkv_kv_evict_select.
+struct SelectArgs {
+  const float* weights;
+  const int32_t* seq_lens;
+  int32_t* keep;                // [B, Hkv, budget]
+  int32_t* new_lens;            // [B]
+  unsigned int* err;
+  int64_t weights_stride;
+  int32_t num_seqs;
+  int32_t num_kv_heads;
+  int32_t budget;
+  int32_t num_sinks;
+  int32_t num_recent;
+};
+cudaError_t launch_evict_select(const SelectArgs& args, cudaStream_t stream);
+
+// The move of kept rows (evict.cu); see pkv_kv_compact.  A row of one kv head
+// is row_bytes of the element plane (a multiple of 16) and, in an MXFP8 pool,
+// scale_bytes of the scale plane.
+struct CompactArgs {
+  unsigned char* k;
+  unsigned char* v;
+  unsigned char* k_scales;      // MXFP8 pools, else null
+  unsigned char* v_scales;
+  float* weights;               // [B, Hkv, weights_stride], or null
+  const int32_t* block_tables;
+  const int32_t* seq_lens;
+  const int32_t* base_lens;     // [B], or null: 0
+  const int32_t* keep;          // [B, keep_heads, keep_stride]
+  const int32_t* keep_lens;     // [B]
+  unsigned int* err;
+  int64_t weights_stride;
+  int64_t keep_stride;
+  int64_t num_blocks;
+  int32_t max_blocks;
+  int32_t num_seqs;
+  int32_t num_kv_heads;
+  int32_t block_size;
+  int32_t keep_heads;           // 1 or Hkv
+  int32_t row_bytes;
+  int32_t scale_bytes;
+};
+cudaError_t launch_kv_compact(const CompactArgs& args, cudaStream_t stream);
+
 // Stage count of the partial kernel's shared-memory ring.
 int decode_num_stages(int head_dim, int elem_bytes);
 

@@ -758,6 +758,256 @@ pkv_status pkv_prefix_attention_states(const pkv_cache_desc* cache, float* state
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+// ---------------------------------------------------------------------------
+// Drafted tokens and eviction.
+// ---------------------------------------------------------------------------
+}  // extern "C"
+
+namespace {
+
+pkv_status check_draft(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
+                       int32_t max_draft, int32_t max_blocks) {
+  if (num_seqs < 0 || max_blocks <= 0 || max_draft < 1 || max_draft > PKV_MAX_DRAFT)
+    return PKV_ERR_INVALID_ARG;
+  // the query-head groups of the decode, whatever an MXFP8 decode takes
+  pkv_cache_desc plain = *c;
+  if (plain.dtype == PKV_MXFP8) plain.dtype = PKV_BF16;
+  pkv_status st = check_attention_shape(&plain, num_q_heads);
+  if (st != PKV_OK) return st;
+  return num_seqs > 65535 ? PKV_ERR_UNSUPPORTED : PKV_OK;
+}
+
+// Key splits of the CUDA-core kernel: about four CTAs per SM in all, at
+// least 128 rows each at the table's full length.
+int32_t draft_splits(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
+                     int32_t max_draft, int32_t max_blocks) {
+  const int rows = max_draft * (num_q_heads / c->num_kv_heads);
+  const int per = pkv::draft_simt_rows(rows);
+  const int64_t ctas = (int64_t)num_seqs * c->num_kv_heads * ((rows + per - 1) / per);
+  const int64_t most = ((int64_t)max_blocks * c->block_size + 127) / 128;
+  int64_t s = (4 * (int64_t)sm_count() + ctas - 1) / ctas;
+  if (s > most) s = most;
+  return (int32_t)(s < 1 ? 1 : s);
+}
+
+struct DraftWorkspace {
+  int32_t splits;
+  size_t o_off, total;
+};
+
+DraftWorkspace draft_workspace(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
+                               int32_t max_draft, int32_t max_blocks) {
+  DraftWorkspace w{};
+  w.splits = draft_splits(c, num_seqs, num_q_heads, max_draft, max_blocks);
+  const int64_t states = w.splits > 1 ? (int64_t)num_seqs * max_draft * num_q_heads * w.splits : 0;
+  w.o_off = align256((size_t)states * 4);
+  w.total = w.o_off + align256((size_t)(states * c->head_dim) * 4) + 256;
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t pkv_draft_tree_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
+                                      int32_t num_q_heads, int32_t max_draft,
+                                      int32_t max_blocks_per_seq) {
+  if (check_cache(cache) != PKV_OK || num_seqs <= 0 ||
+      check_draft(cache, num_seqs, num_q_heads, max_draft, max_blocks_per_seq) != PKV_OK)
+    return 0;
+  return draft_workspace(cache, num_seqs, num_q_heads, max_draft, max_blocks_per_seq).total;
+}
+
+pkv_status pkv_draft_tree_attention(
+    const pkv_cache_desc* cache, void* out, float* lse, const void* q, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* ctx_lens, const int32_t* draft_ptr, const uint64_t* masks, int32_t num_seqs,
+    int32_t num_rows, int32_t max_draft, int32_t num_q_heads, float scale, void* workspace,
+    size_t workspace_bytes, void* stream) {
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (num_rows < 0 || !isfinite(scale)) return PKV_ERR_INVALID_ARG;
+  if ((st = check_draft(cache, num_seqs, num_q_heads, max_draft, max_blocks_per_seq)) != PKV_OK)
+    return st;
+  if (num_seqs == 0 || num_rows == 0) return PKV_OK;
+  if (!out || !q || !k_cache || !v_cache || !block_tables || !ctx_lens || !draft_ptr)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(q) || !aligned16(k_cache) || !aligned16(v_cache))
+    return PKV_ERR_INVALID_ARG;
+  const DraftWorkspace w =
+      draft_workspace(cache, num_seqs, num_q_heads, max_draft, max_blocks_per_seq);
+  if (workspace_bytes < w.total || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
+    return PKV_ERR_INVALID_ARG;
+  unsigned int* err = device_error_word();
+  if (!err) return PKV_ERR_CUDA;
+
+  pkv::DraftArgs a{};
+  a.q = q;
+  a.k = k_cache;
+  a.v = v_cache;
+  if (cache->dtype == PKV_MXFP8) {
+    a.k_scales = static_cast<const uint8_t*>(k_cache) + mx_plane_bytes(cache);
+    a.v_scales = static_cast<const uint8_t*>(v_cache) + mx_plane_bytes(cache);
+  }
+  a.block_tables = block_tables;
+  a.ctx_lens = ctx_lens;
+  a.draft_ptr = draft_ptr;
+  a.masks = masks;
+  a.out = out;
+  a.lse_out = lse;
+  a.err = err;
+  unsigned char* base = static_cast<unsigned char*>(workspace);
+  a.rec_lse = reinterpret_cast<float*>(base);
+  a.rec_o = reinterpret_cast<float*>(base + w.o_off);
+  a.num_blocks = cache->num_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_rows = num_rows;
+  a.max_draft = max_draft;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.block_size = cache->block_size;
+  a.num_splits = w.splits;
+  a.qscale = scale * 1.4426950408889634f;
+  cudaError_t e = pkv::launch_draft_simt(cache->dtype, cache->head_dim, a, as_stream(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+size_t pkv_decode_weights_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
+                                          int32_t num_q_heads, int32_t max_blocks_per_seq) {
+  const size_t dec =
+      pkv_decode_workspace_bytes(cache, num_seqs, num_q_heads, max_blocks_per_seq, 0);
+  return dec ? dec + align256((size_t)num_seqs * num_q_heads * 4) : 0;
+}
+
+pkv_status pkv_paged_attention_decode_weights(
+    const pkv_cache_desc* cache, void* out, float* lse, float* weights, int64_t weights_stride,
+    float decay, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+    int32_t num_seqs, int32_t num_q_heads, float scale, void* workspace, size_t workspace_bytes,
+    void* stream) {
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (num_seqs < 0 || max_blocks_per_seq <= 0 || weights_stride < 1 || !isfinite(scale) ||
+      !isfinite(decay))
+    return PKV_ERR_INVALID_ARG;
+  if ((st = check_attention_shape(cache, num_q_heads)) != PKV_OK) return st;
+  if (num_seqs == 0) return PKV_OK;
+  if (!weights || !workspace) return PKV_ERR_INVALID_ARG;
+  const size_t need =
+      pkv_decode_weights_workspace_bytes(cache, num_seqs, num_q_heads, max_blocks_per_seq);
+  const size_t lse_bytes = align256((size_t)num_seqs * num_q_heads * 4);
+  if (!need || workspace_bytes < need) return PKV_ERR_INVALID_ARG;
+  unsigned char* base = static_cast<unsigned char*>(workspace);
+  float* lse_use = lse ? lse : reinterpret_cast<float*>(base + need - lse_bytes);
+  if ((st = pkv_paged_attention_decode(cache, out, lse_use, q, k_cache, v_cache, block_tables,
+                                       max_blocks_per_seq, seq_lens, num_seqs, num_q_heads, scale,
+                                       0, workspace, need - lse_bytes, stream)) != PKV_OK)
+    return st;
+  unsigned int* err = device_error_word();
+  if (!err) return PKV_ERR_CUDA;
+  pkv::WeighArgs a{};
+  a.q = q;
+  a.k = k_cache;
+  if (cache->dtype == PKV_MXFP8)
+    a.k_scales = static_cast<const uint8_t*>(k_cache) + mx_plane_bytes(cache);
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.lse = lse_use;
+  a.weights = weights;
+  a.err = err;
+  a.weights_stride = weights_stride;
+  a.num_blocks = cache->num_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.block_size = cache->block_size;
+  a.qscale = scale * 1.4426950408889634f;
+  a.decay = decay;
+  cudaError_t e = pkv::launch_weigh(cache->dtype, cache->head_dim, a, as_stream(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_kv_evict_select(const float* weights, int64_t weights_stride,
+                               const int32_t* seq_lens, int32_t num_seqs, int32_t num_kv_heads,
+                               int32_t budget, int32_t num_sinks, int32_t num_recent,
+                               int32_t* keep, int32_t* new_lens, void* stream) {
+  if (num_seqs < 0 || num_kv_heads <= 0 || weights_stride < 1 || budget < 1 || num_sinks < 0 ||
+      num_recent < 0 || (int64_t)num_sinks + num_recent > budget)
+    return PKV_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PKV_OK;
+  if (num_seqs > 65535 || num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+  if (!weights || !seq_lens || !keep || !new_lens) return PKV_ERR_INVALID_ARG;
+  unsigned int* err = device_error_word();
+  if (!err) return PKV_ERR_CUDA;
+  pkv::SelectArgs a{};
+  a.weights = weights;
+  a.seq_lens = seq_lens;
+  a.keep = keep;
+  a.new_lens = new_lens;
+  a.err = err;
+  // a length is an int32, so nothing past INT32_MAX is ever read
+  a.weights_stride = weights_stride;
+  a.num_seqs = num_seqs;
+  a.num_kv_heads = num_kv_heads;
+  a.budget = budget;
+  a.num_sinks = num_sinks;
+  a.num_recent = num_recent;
+  cudaError_t e = pkv::launch_evict_select(a, as_stream(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_kv_compact(const pkv_cache_desc* cache, void* k_cache, void* v_cache,
+                          float* weights, int64_t weights_stride, const int32_t* block_tables,
+                          int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                          const int32_t* base_lens, const int32_t* keep, int32_t keep_heads,
+                          int64_t keep_stride, const int32_t* keep_lens, int32_t num_seqs,
+                          void* stream) {
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (num_seqs < 0 || max_blocks_per_seq <= 0 || keep_stride < 0 ||
+      (keep_heads != 1 && keep_heads != cache->num_kv_heads) || (weights && weights_stride < 1))
+    return PKV_ERR_INVALID_ARG;
+  if (num_seqs == 0 || keep_stride == 0) return PKV_OK;
+  if (!k_cache || !v_cache || !block_tables || !seq_lens || !keep || !keep_lens)
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_INVALID_ARG;
+  if (num_seqs > 65535 || cache->num_kv_heads > 65535 || cache->num_blocks > INT32_MAX)
+    return PKV_ERR_UNSUPPORTED;
+  const int64_t row_bytes = (int64_t)cache->head_dim * elem_bytes(cache->dtype);
+  if (row_bytes % 16 != 0 || row_bytes > 16384) return PKV_ERR_UNSUPPORTED;
+  if (cache->dtype == PKV_MXFP8 && cache->head_dim % 32 != 0) return PKV_ERR_UNSUPPORTED;
+  unsigned int* err = device_error_word();
+  if (!err) return PKV_ERR_CUDA;
+  pkv::CompactArgs a{};
+  a.k = static_cast<unsigned char*>(k_cache);
+  a.v = static_cast<unsigned char*>(v_cache);
+  if (cache->dtype == PKV_MXFP8) {
+    a.k_scales = a.k + mx_plane_bytes(cache);
+    a.v_scales = a.v + mx_plane_bytes(cache);
+    a.scale_bytes = cache->head_dim / 32;
+  }
+  a.weights = weights;
+  a.weights_stride = weights_stride;
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.base_lens = base_lens;
+  a.keep = keep;
+  a.keep_lens = keep_lens;
+  a.err = err;
+  a.keep_stride = keep_stride;
+  a.num_blocks = cache->num_blocks;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.num_kv_heads = cache->num_kv_heads;
+  a.block_size = cache->block_size;
+  a.keep_heads = keep_heads;
+  a.row_bytes = (int32_t)row_bytes;
+  cudaError_t e = pkv::launch_kv_compact(a, as_stream(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
 pkv_status pkv_get_device_error(int32_t* code_out, void* stream) {
   if (!code_out) return PKV_ERR_INVALID_ARG;
   unsigned int* err = device_error_word();

@@ -20,7 +20,9 @@ PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA, PKV_ERR_DEVICE, 
 # PKV_STATIC_SCRATCH_BYTES of include/pkv.h: the library-owned scratch array
 STATIC_SCRATCH_BYTES = 16 << 20
 PKV_F32, PKV_BF16, PKV_MXFP8 = 0, 1, 2
-DEVERR_SLOT, DEVERR_BLOCK, DEVERR_LENGTH, DEVERR_TIMEOUT = 1, 2, 4, 8
+DEVERR_SLOT, DEVERR_BLOCK, DEVERR_LENGTH, DEVERR_TIMEOUT, DEVERR_KEEP = 1, 2, 4, 8, 16
+# PKV_MAX_DRAFT of include/pkv.h: drafted tokens of one sequence at most
+MAX_DRAFT = 64
 
 EXPORTED = [
     "pkv_kv_append",
@@ -36,6 +38,12 @@ EXPORTED = [
     "pkv_prefix_attention_states",
     "pkv_chunk_tree_plan",
     "pkv_chunk_tree_attention",
+    "pkv_draft_tree_workspace_bytes",
+    "pkv_draft_tree_attention",
+    "pkv_decode_weights_workspace_bytes",
+    "pkv_paged_attention_decode_weights",
+    "pkv_kv_evict_select",
+    "pkv_kv_compact",
     "pkv_get_device_error",
     "pkv_status_string",
 ]
@@ -99,6 +107,20 @@ def load_library():
     lib.pkv_chunk_tree_attention.restype = ctypes.c_int
     lib.pkv_chunk_tree_attention.argtypes = [dp, vp, vp, vp, vp, vp, i32, i32, f32, vp, vp, vp,
                                              ctypes.c_size_t, vp]
+    lib.pkv_draft_tree_workspace_bytes.restype = ctypes.c_size_t
+    lib.pkv_draft_tree_workspace_bytes.argtypes = [dp, i32, i32, i32, i32]
+    lib.pkv_draft_tree_attention.restype = ctypes.c_int
+    lib.pkv_draft_tree_attention.argtypes = [dp, vp, vp, vp, vp, vp, vp, i32, vp, vp, vp, i32, i32,
+                                             i32, i32, f32, vp, ctypes.c_size_t, vp]
+    lib.pkv_decode_weights_workspace_bytes.restype = ctypes.c_size_t
+    lib.pkv_decode_weights_workspace_bytes.argtypes = [dp, i32, i32, i32]
+    lib.pkv_paged_attention_decode_weights.restype = ctypes.c_int
+    lib.pkv_paged_attention_decode_weights.argtypes = [dp, vp, vp, vp, i64, f32, vp, vp, vp, vp, i32,
+                                                       vp, i32, i32, f32, vp, ctypes.c_size_t, vp]
+    lib.pkv_kv_evict_select.restype = ctypes.c_int
+    lib.pkv_kv_evict_select.argtypes = [vp, i64, vp, i32, i32, i32, i32, i32, vp, vp, vp]
+    lib.pkv_kv_compact.restype = ctypes.c_int
+    lib.pkv_kv_compact.argtypes = [dp, vp, vp, vp, i64, vp, i32, vp, vp, vp, i32, i64, vp, i32, vp]
     lib.pkv_get_device_error.restype = ctypes.c_int
     lib.pkv_get_device_error.argtypes = [ctypes.POINTER(i32), vp]
     lib.pkv_status_string.restype = ctypes.c_char_p
@@ -132,11 +154,18 @@ class MxPool:
     followed by the E8M0 scale plane [num_blocks, num_kv_heads, block_size,
     head_dim / 32].  q, k, v and out beside it are bf16."""
 
-    def __init__(self, num_blocks, block_size, num_kv_heads, head_dim, device="cuda", fill=0):
+    def __init__(self, num_blocks, block_size, num_kv_heads, head_dim, device="cuda", fill=0,
+                 buf=None):
+        """A new pool filled with ``fill``, or a view of an existing one-dimensional
+        uint8 buffer of that layout (``buf``)."""
         self.shape = (int(num_blocks), int(block_size), int(num_kv_heads), int(head_dim))
         n = num_blocks * block_size * num_kv_heads * head_dim
         self.plane_bytes = n
-        self.buf = torch.full((n + n // 32,), fill, dtype=torch.uint8, device=device)
+        if buf is None:
+            buf = torch.full((n + n // 32,), fill, dtype=torch.uint8, device=device)
+        elif buf.dtype != torch.uint8 or buf.shape != (n + n // 32,) or not buf.is_contiguous():
+            raise ValueError("buf must be a contiguous uint8 tensor of the pool's bytes")
+        self.buf = buf
 
     @property
     def device(self):
@@ -382,6 +411,186 @@ def chunk_tree_attention(q, k_cache, v_cache, plan: ChunkTreePlan, scale, *, out
         float(scale), _ptr(plan.host), _ptr(plan.device), _ptr(workspace), ws_bytes,
         _stream(stream)), "pkv_chunk_tree_attention")
     return out
+
+
+def _dense(name, t, dtype, shape):
+    """Check a tensor argument; ``shape`` entries of None match any size."""
+    if t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or any(
+            w is not None and w != n for w, n in zip(shape, t.shape)):
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+
+
+def _pair_desc(k_cache, v_cache) -> CacheDesc:
+    """cache_desc of a K and a V pool of one shape and type."""
+    desc, v = cache_desc(k_cache), cache_desc(v_cache)
+    if any(getattr(desc, f) != getattr(v, f) for f, _ in CacheDesc._fields_):
+        raise ValueError("K and V caches must be of one shape and dtype")
+    return desc
+
+
+def _on_current_device(*tensors):
+    """Every tensor must be on the current CUDA device: the kernels are launched there."""
+    dev = tensors[0].device
+    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device, got {dev}")
+    for t in tensors:
+        if t is not None and t.device != dev:
+            raise ValueError(f"tensors must be on one device, got {t.device} and {dev}")
+
+
+def _io_dtype(desc):
+    return torch.float32 if desc.dtype == PKV_F32 else torch.bfloat16
+
+
+def _score_rows(name, weights, b, hkv):
+    """Check a score buffer [b, hkv, n] float32 (rows may be wider than n) and
+    return the elements between its rows."""
+    if weights.dtype != torch.float32 or weights.dim() != 3 or weights.shape[:2] != (b, hkv):
+        raise ValueError(f"{name} must be a float32 tensor of shape ({b}, {hkv}, n)")
+    stride = weights.stride(1) if hkv > 1 else weights.stride(0) if b > 1 else weights.shape[2]
+    if (weights.shape[2] > 1 and weights.stride(2) != 1) or stride < weights.shape[2] or (
+            b > 1 and weights.stride(0) != hkv * stride):
+        raise ValueError(f"{name}'s rows must lie one behind the other")
+    return stride
+
+
+def draft_tree_workspace_bytes(k_cache, num_seqs, num_q_heads, max_draft,
+                               max_blocks_per_seq) -> int:
+    desc = cache_desc(k_cache)
+    return load_library().pkv_draft_tree_workspace_bytes(ctypes.byref(desc), num_seqs, num_q_heads,
+                                                         max_draft, max_blocks_per_seq)
+
+
+def draft_tree_attention(q, k_cache, v_cache, block_tables, ctx_lens, draft_ptr, scale, *,
+                         max_draft, masks=None, out=None, lse=None, workspace=None, stream=None):
+    """Attention of every sequence's drafted tokens over its cached context and
+    their drafted ancestors (include/pkv.h).
+
+    q: [rows, Hq, D], sequence r's drafted tokens in rows draft_ptr[r] ..
+    draft_ptr[r + 1] - 1, their K/V already appended behind its ctx_lens[r]
+    rows; draft_ptr: int32 [B + 1]; masks: int64 [rows], bit j for drafted row
+    j of the same sequence, or None for a chain; max_draft: drafted tokens of
+    a sequence at most (<= MAX_DRAFT).  Returns out (and writes lse [rows, Hq]
+    float32 when given); rows of no sequence are not written."""
+    desc = _pair_desc(k_cache, v_cache)
+    rows, hq, d = q.shape
+    b, max_blocks = block_tables.shape
+    _dense("q", q, _io_dtype(desc), (None, None, desc.head_dim))
+    _dense("block_tables", block_tables, torch.int32, (None, None))
+    _dense("ctx_lens", ctx_lens, torch.int32, (b,))
+    _dense("draft_ptr", draft_ptr, torch.int32, (b + 1,))
+    if masks is not None:
+        _dense("masks", masks, torch.int64, (rows,))
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _dense("out", out, q.dtype, (rows, hq, d))
+    if lse is not None:
+        _dense("lse", lse, torch.float32, (rows, hq))
+    _on_current_device(q, k_cache, v_cache, block_tables, ctx_lens, draft_ptr, masks, out, lse,
+                       workspace)
+    lib = load_library()
+    if workspace is None and b:
+        need = lib.pkv_draft_tree_workspace_bytes(ctypes.byref(desc), b, hq, max_draft, max_blocks)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib.pkv_draft_tree_attention(
+        ctypes.byref(desc), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), max_blocks,
+        ctx_lens.data_ptr(), draft_ptr.data_ptr(), masks.data_ptr() if masks is not None else None,
+        b, rows, max_draft, hq, scale, workspace.data_ptr() if workspace is not None else None,
+        ws_bytes, _stream(stream)), "pkv_draft_tree_attention")
+    return out
+
+
+def decode_weights_workspace_bytes(k_cache, num_seqs, num_q_heads, max_blocks_per_seq) -> int:
+    desc = cache_desc(k_cache)
+    return load_library().pkv_decode_weights_workspace_bytes(ctypes.byref(desc), num_seqs,
+                                                             num_q_heads, max_blocks_per_seq)
+
+
+def paged_attention_decode_weights(q, k_cache, v_cache, block_tables, seq_lens, weights, scale, *,
+                                   decay=1.0, out=None, lse=None, workspace=None, stream=None):
+    """The paged decode, which also updates every cached row's running score
+    (include/pkv.h): weights [B, Hkv, n] float32, in place, becomes decay *
+    weights + the row's attention weight summed over the query heads of its kv
+    head.  Returns out (and writes lse [B, Hq] float32 when given)."""
+    desc = _pair_desc(k_cache, v_cache)
+    b, hq, d = q.shape
+    max_blocks = block_tables.shape[1]
+    _dense("q", q, _io_dtype(desc), (None, None, desc.head_dim))
+    _dense("block_tables", block_tables, torch.int32, (b, None))
+    _dense("seq_lens", seq_lens, torch.int32, (b,))
+    stride = _score_rows("weights", weights, b, desc.num_kv_heads)
+    if out is None:
+        out = torch.empty_like(q)
+    else:
+        _dense("out", out, q.dtype, (b, hq, d))
+    if lse is not None:
+        _dense("lse", lse, torch.float32, (b, hq))
+    _on_current_device(q, k_cache, v_cache, block_tables, seq_lens, weights, out, lse, workspace)
+    lib = load_library()
+    if workspace is None and b:
+        need = lib.pkv_decode_weights_workspace_bytes(ctypes.byref(desc), b, hq, max_blocks)
+        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib.pkv_paged_attention_decode_weights(
+        ctypes.byref(desc), out.data_ptr(), lse.data_ptr() if lse is not None else None,
+        weights.data_ptr(), stride, decay, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        block_tables.data_ptr(), max_blocks, seq_lens.data_ptr(), b, hq, scale,
+        workspace.data_ptr() if workspace is not None else None, ws_bytes, _stream(stream)),
+        "pkv_paged_attention_decode_weights")
+    return out
+
+
+def kv_evict_select(weights, seq_lens, budget, *, num_sinks=0, num_recent=0, keep=None,
+                    new_lens=None, stream=None):
+    """Choose the rows each sequence and kv head keeps within ``budget``
+    (include/pkv.h): its first num_sinks, its last num_recent and the heaviest
+    others.  weights: [B, Hkv, n] float32; seq_lens: int32 [B].  Returns (keep
+    int32 [B, Hkv, budget], ascending and -1 padded, new_lens int32 [B])."""
+    b, hkv, _ = weights.shape
+    _dense("seq_lens", seq_lens, torch.int32, (b,))
+    stride = _score_rows("weights", weights, b, hkv)
+    if keep is None:
+        keep = torch.empty(b, hkv, max(int(budget), 0), dtype=torch.int32, device=weights.device)
+    else:
+        _dense("keep", keep, torch.int32, (b, hkv, budget))
+    if new_lens is None:
+        new_lens = torch.empty_like(seq_lens)
+    else:
+        _dense("new_lens", new_lens, torch.int32, (b,))
+    _on_current_device(weights, seq_lens, keep, new_lens)
+    _check(load_library().pkv_kv_evict_select(
+        weights.data_ptr(), stride, seq_lens.data_ptr(), b, hkv, budget, num_sinks, num_recent,
+        keep.data_ptr(), new_lens.data_ptr(), _stream(stream)), "pkv_kv_evict_select")
+    return keep, new_lens
+
+
+def kv_compact(k_cache, v_cache, block_tables, seq_lens, keep, keep_lens, *, base_lens=None,
+               weights=None, stream=None) -> None:
+    """Move kept rows together in place (include/pkv.h): row base + keep[r, c,
+    j] of K, V and, when given, of weights [B, Hkv, n] goes to row base + j.
+    keep: int32 [B, Hkv, k], ascending, or [B, 1, k] for one list for every kv
+    head; keep_lens: int32 [B]; base_lens: int32 [B] or None (0)."""
+    desc = _pair_desc(k_cache, v_cache)
+    b, max_blocks = block_tables.shape
+    _dense("block_tables", block_tables, torch.int32, (None, None))
+    _dense("seq_lens", seq_lens, torch.int32, (b,))
+    _dense("keep", keep, torch.int32, (b, None, None))
+    _dense("keep_lens", keep_lens, torch.int32, (b,))
+    if base_lens is not None:
+        _dense("base_lens", base_lens, torch.int32, (b,))
+    stride = _score_rows("weights", weights, b, desc.num_kv_heads) if weights is not None else 0
+    _on_current_device(k_cache, v_cache, block_tables, seq_lens, keep, keep_lens, base_lens,
+                       weights)
+    _check(load_library().pkv_kv_compact(
+        ctypes.byref(desc), k_cache.data_ptr(), v_cache.data_ptr(),
+        weights.data_ptr() if weights is not None else None, stride, block_tables.data_ptr(),
+        max_blocks, seq_lens.data_ptr(), base_lens.data_ptr() if base_lens is not None else None,
+        keep.data_ptr(), keep.shape[1], keep.shape[2], keep_lens.data_ptr(), b, _stream(stream)),
+        "pkv_kv_compact")
 
 
 def get_device_error(stream=None) -> int:

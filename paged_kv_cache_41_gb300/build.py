@@ -33,6 +33,7 @@ CUDA_SOURCES = [
     "kernels/prefix_tc.cu",
     "kernels/tree.cu",
     "kernels/draft.cu",
+    "kernels/draft_tc.cu",
     "kernels/evict.cu",
 ]
 # Attention kernels take exp2/log2/division from the hardware approximations
@@ -43,6 +44,7 @@ PER_SOURCE_FLAGS = {
     "kernels/decode_tc_mx.cu": ["--use_fast_math"],
     "kernels/prefix_tc.cu": ["--use_fast_math"],
     "kernels/tree.cu": ["--use_fast_math"],
+    "kernels/draft_tc.cu": ["--use_fast_math"],
     "kernels/draft.cu": ["--use_fast_math"],
     "kernels/evict.cu": ["--use_fast_math"],
 }

@@ -40,4 +40,13 @@ __device__ __forceinline__ uint64_t draft_mask(const DraftArgs& a, const DraftSe
   return m & all;
 }
 
+// The work list of plan.cuh: a sequence's rows, and its segments.
+__device__ __forceinline__ int plan_len(const DraftArgs& a, int r, bool report) {
+  const DraftSeq s = draft_seq(a, r, report);
+  return s.n > 0 ? s.ctx + s.n : 0;
+}
+__device__ __forceinline__ int plan_heads(const DraftArgs& a) {
+  return a.num_kv_heads * a.row_tiles;
+}
+
 }  // namespace pkv

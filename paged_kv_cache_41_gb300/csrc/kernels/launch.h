@@ -233,7 +233,7 @@ cudaError_t launch_prefix_attention(int head_dim, int group, int num_splits,
                                     const PrefixArgs& args, cudaStream_t stream);
 size_t prefix_smem_bytes(int head_dim, int split_len, int block_size);
 
-// Arguments of the draft-tree attention kernels (draft.cu).
+// Arguments of the draft-tree attention kernels (draft.cu, draft_tc.cu).
 struct DraftArgs {
   const void* q;                // [num_rows, Hq, D] (bf16 beside an MXFP8 pool)
   const void* k;                // the pools [NB, P, Hkv, D]
@@ -247,8 +247,9 @@ struct DraftArgs {
   void* out;                    // [num_rows, Hq, D]
   float* lse_out;               // [num_rows, Hq] natural log, or null
   unsigned int* err;
-  float* rec_o;                 // split states [B, max_draft, Hq, num_splits, D]
-  float* rec_lse;               // [B, max_draft, Hq, num_splits], base 2
+  float* rec_o;                 // states: draft.cu [B, max_draft, Hq, num_splits, D],
+  float* rec_lse;               // draft_tc.cu [2 num_ctas, rows, D]; their LSEs, base 2
+  int64_t* plan_pre;            // draft_tc.cu: [B + 1], the work split of plan.cuh
   int64_t num_blocks;
   int32_t max_blocks;
   int32_t num_seqs;
@@ -258,8 +259,26 @@ struct DraftArgs {
   int32_t num_kv_heads;
   int32_t block_size;
   int32_t num_splits;
+  int32_t num_ctas;             // draft_tc.cu, as in DecodeArgs:
+  int32_t stage_units;
+  int32_t piece_units;
+  int32_t row_tiles;            // segments of a (sequence, kv head): its rows / 256 rounded up
+  int32_t q_tokens;             // drafted rows of one 128-row query tile that are loaded
   float qscale;                 // softmax scale * log2(e)
 };
+
+// Draft-tree attention on the tensor cores (draft_tc.cu): bf16 pools.  A
+// segment is one kv head of a sequence against up to `tiles` 128-row tiles of
+// its (drafted row, head) rows; stages are 128 keys.  tmk / tmv: row-group
+// maps whose box is draft_tc_box_rows rows; tmq: a 128-byte-swizzled map over
+// q whose box is 64 columns x G heads x q_tokens rows.
+constexpr int kDraftKeys = 128;
+constexpr int kDraftRows = 128;
+__host__ __device__ constexpr int draft_tc_box_rows(int block_size) {
+  return kDraftKeys % block_size == 0 ? block_size : block_size % kDraftKeys == 0 ? kDraftKeys : 32;
+}
+cudaError_t launch_draft_tc(int head_dim, int tiles, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                            const CUtensorMap& tmv, const DraftArgs& args, cudaStream_t stream);
 cudaError_t launch_draft_simt(int dtype, int head_dim, const DraftArgs& args, cudaStream_t stream);
 // (token, query head) rows per CTA where a kv head has `rows` of them at most.
 int draft_simt_rows(int rows);

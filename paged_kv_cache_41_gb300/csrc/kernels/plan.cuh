@@ -29,6 +29,13 @@ __host__ __device__ __forceinline__ long long units_per_cta(long long S, int C, 
   return w > stage_units ? w : stage_units;
 }
 
+// What the split asks of a work list: a sequence's rows (0: no segment) and its
+// segments.
+__device__ __forceinline__ int plan_len(const DecodeArgs& a, int r, bool report) {
+  return effective_len(__ldg(a.seq_lens + r), a.max_blocks, a.block_size, a.err, report);
+}
+__device__ __forceinline__ int plan_heads(const DecodeArgs& a) { return a.num_kv_heads; }
+
 // Every CTA scans the lengths (all kThreads threads must call this): units
 // per sequence, their total S (times Hkv), this CTA's range, and the
 // (sequence, kv head, stage in segment) of its first stage in *d0 -- whose
@@ -41,12 +48,12 @@ __host__ __device__ __forceinline__ long long units_per_cta(long long S, int C, 
 // to one pass, the lengths are read once and kept in registers.  `wsum` is
 // shared scratch of at least 2 * (kThreads / 32) + 4 long longs.  Returns the
 // number of stages of this CTA (<= 0: none; the caller leaves).
-template <int kThreads, int kRows, int kPer = 8>
-__device__ __forceinline__ int plan_cta_stages(const DecodeArgs& a, long long* wsum, int4* d0) {
+template <int kThreads, int kRows, int kPer = 8, class Args>
+__device__ __forceinline__ int plan_cta_stages(const Args& a, long long* wsum, int4* d0) {
   constexpr int kWarps = kThreads / 32;
   constexpr int kChunk = kThreads * kPer;
   const int c = blockIdx.x, C = a.num_ctas;
-  const int B = a.num_seqs, P = a.block_size, Hkv = a.num_kv_heads;
+  const int B = a.num_seqs, Hkv = plan_heads(a);
   const long long su = a.stage_units, pu = a.piece_units;
   const bool weighted = su != 1 || pu != 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -62,9 +69,7 @@ __device__ __forceinline__ int plan_cta_stages(const DecodeArgs& a, long long* w
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int r = base + threadIdx.x * kPer + j;
-      nt[j] = r < B ? (effective_len(__ldg(a.seq_lens + r), a.max_blocks, P, a.err, report) +
-                       kRows - 1) / kRows
-                    : 0;
+      nt[j] = r < B ? (plan_len(a, r, report) + kRows - 1) / kRows : 0;
       mu += nt[j] > 0 ? su * nt[j] + pu : 0;
       ms += nt[j];
     }

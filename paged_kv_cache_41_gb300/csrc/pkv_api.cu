@@ -790,14 +790,39 @@ int32_t draft_splits(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_he
   return (int32_t)(s < 1 ? 1 : s);
 }
 
+// bf16 pools run on the tensor cores (row groups addressed with int32
+// coordinates), the others on the CUDA cores.
+bool draft_on_tc(const pkv_cache_desc* c) {
+  return c->dtype == PKV_BF16 &&
+         (int64_t)c->num_blocks * (c->block_size / pkv::kRowGroup) <= INT32_MAX;
+}
+
 struct DraftWorkspace {
-  int32_t splits;
-  size_t o_off, total;
+  int32_t splits;             // CUDA cores
+  int32_t tiles, row_tiles;   // tensor cores: 128-row tiles of a segment, segments per kv head
+  int32_t ctas;
+  size_t lse_off, o_off, total;
 };
 
 DraftWorkspace draft_workspace(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
                                int32_t max_draft, int32_t max_blocks) {
   DraftWorkspace w{};
+  if (draft_on_tc(c)) {
+    const int rows = max_draft * (num_q_heads / c->num_kv_heads);
+    w.tiles = rows > pkv::kDraftRows ? 2 : 1;
+    const int per = w.tiles * pkv::kDraftRows;
+    w.row_tiles = (rows + per - 1) / per;
+    const int64_t keys = (int64_t)max_blocks * c->block_size;
+    const int64_t stages = (int64_t)num_seqs * c->num_kv_heads * w.row_tiles *
+                           ((keys + pkv::kDraftKeys - 1) / pkv::kDraftKeys);
+    const int64_t sms = sm_count();
+    w.ctas = (int32_t)(stages < sms ? stages : sms);
+    const int64_t recs = 2 * (int64_t)w.ctas * per;
+    w.lse_off = align256((size_t)(num_seqs + 1) * 8);
+    w.o_off = w.lse_off + align256((size_t)recs * 4);
+    w.total = w.o_off + align256((size_t)(recs * c->head_dim) * 4);
+    return w;
+  }
   w.splits = draft_splits(c, num_seqs, num_q_heads, max_draft, max_blocks);
   const int64_t states = w.splits > 1 ? (int64_t)num_seqs * max_draft * num_q_heads * w.splits : 0;
   w.o_off = align256((size_t)states * 4);
@@ -857,7 +882,8 @@ pkv_status pkv_draft_tree_attention(
   a.lse_out = lse;
   a.err = err;
   unsigned char* base = static_cast<unsigned char*>(workspace);
-  a.rec_lse = reinterpret_cast<float*>(base);
+  a.plan_pre = reinterpret_cast<int64_t*>(base);
+  a.rec_lse = reinterpret_cast<float*>(base + w.lse_off);
   a.rec_o = reinterpret_cast<float*>(base + w.o_off);
   a.num_blocks = cache->num_blocks;
   a.max_blocks = max_blocks_per_seq;
@@ -869,7 +895,24 @@ pkv_status pkv_draft_tree_attention(
   a.block_size = cache->block_size;
   a.num_splits = w.splits;
   a.qscale = scale * 1.4426950408889634f;
-  cudaError_t e = pkv::launch_draft_simt(cache->dtype, cache->head_dim, a, as_stream(stream));
+  cudaError_t e;
+  if (draft_on_tc(cache)) {
+    const int G = num_q_heads / cache->num_kv_heads;
+    a.num_ctas = w.ctas;
+    a.row_tiles = w.row_tiles;
+    a.stage_units = 2;
+    a.piece_units = 3;
+    a.q_tokens = max_draft < pkv::kDraftRows / G ? max_draft : pkv::kDraftRows / G;
+    const int box = pkv::draft_tc_box_rows(cache->block_size);
+    CUtensorMap tmq, tmk, tmv;
+    if ((st = encode_q_map_sw128(&tmq, q, num_rows, num_q_heads, cache->head_dim, G, a.q_tokens)) != PKV_OK ||
+        (st = encode_cache_map_rg(&tmk, cache, k_cache, box)) != PKV_OK ||
+        (st = encode_cache_map_rg(&tmv, cache, v_cache, box)) != PKV_OK)
+      return st;
+    e = pkv::launch_draft_tc(cache->head_dim, w.tiles, tmq, tmk, tmv, a, as_stream(stream));
+  } else {
+    e = pkv::launch_draft_simt(cache->dtype, cache->head_dim, a, as_stream(stream));
+  }
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

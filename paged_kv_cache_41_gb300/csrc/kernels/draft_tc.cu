@@ -17,13 +17,17 @@
 //     the stages of every (sequence, kv head, 256-row) segment, writes whole
 //     segments directly and leaves one (O, LSE) record per cut piece, which
 //     draft_tc_reduce_kernel merges;
-//   * two softmax warpgroups, each with its own S and O in TMEM (512 columns).
+//   * two softmax groups, each with its own S and O in TMEM (512 columns).
 //     A piece of more than 128 rows gives each of them one row tile, both
 //     against every stage; a piece of up to 128 rows gives them alternate
 //     stages of the same rows, merged at its end.  Either way one group's
 //     softmax runs while the tensor pipe works for the other;
-//   * thread t of a group owns row t of its tile (TMEM lane t): no cross-thread
-//     reduction.  Warps whose 32 rows hold no drafted row skip the arithmetic;
+//   * a group is two warpgroups: a thread takes one row (its TMEM lane) and 64
+//     of the 128 keys, and meets the row's other thread once a stage, over its
+//     maximum.  (One warpgroup a group, 128 keys a thread: the softmax's
+//     latency, 4,500 cycles a stage, held the tensor pipe; 700 us for 64
+//     requests with trees of 64.)  Warps whose 32 rows hold no drafted row
+//     skip the arithmetic;
 //   * P is rounded to bf16 (half a step, 2^-8 of each weight, is the size of the
 //     output's own rounding) and overlays its S in TMEM, from where
 //     the PV MMA reads it; the row sums are taken before the rounding;
@@ -49,7 +53,8 @@ namespace pkv {
 
 namespace {
 
-constexpr int kDtThreads = 10 * 32;  // two softmax groups, MMA, producer
+constexpr int kDtSoftWarps = 16;     // two groups of eight
+constexpr int kDtThreads = (kDtSoftWarps + 2) * 32;  // ..., MMA, producer
 constexpr int kDtDescs = 8;          // stage descriptors in flight
 constexpr float kDtLn2 = 0.6931471805599453f;
 
@@ -78,10 +83,10 @@ struct DtSmem {
   static constexpr int kItems = D == 128 ? 7 - kTiles : 12;  // ring tiles
   static constexpr int q_off = 0;
   static constexpr int ring_off = kTiles * kTile;
-  static constexpr int exch_off = ring_off + kItems * kTile;  // [2][128] (m, l); the plan's scratch
-  static constexpr int desc_off = exch_off + 2 * 128 * 8;
+  static constexpr int exch_off = ring_off + kItems * kTile;  // [4][128] floats; the plan's scratch
+  static constexpr int desc_off = exch_off + 4 * 128 * 4;
   static constexpr int bar_off = desc_off + kDtDescs * (int)sizeof(DtDesc);
-  static constexpr int bad_off = bar_off + (2 * kItems + kDtDescs + 9) * 8;
+  static constexpr int bad_off = bar_off + (2 * kItems + kDtDescs + 17) * 8;
   static constexpr int tmem_off = bad_off + 65 * 4;
   static constexpr int total = tmem_off + 4;
   static_assert(total <= 227 * 1024, "shared memory of one CTA");
@@ -112,7 +117,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
   unsigned char* sm = dt_smem;
   unsigned char* qs = sm + L::q_off;
   unsigned char* ring = sm + L::ring_off;
-  float2* exch = reinterpret_cast<float2*>(sm + L::exch_off);
+  float* exch = reinterpret_cast<float*>(sm + L::exch_off);
   DtDesc* descs = reinterpret_cast<DtDesc*>(sm + L::desc_off);
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::bar_off);  // a ring tile landed
   uint64_t* freeb = full + kItems;    // its MMAs completed
@@ -124,6 +129,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
   uint64_t* oend = pfull + 2;         // a piece's MMAs completed
   uint64_t* ofree = oend + 1;         // both groups read its O
   uint64_t* xsync = ofree + 1;        // the groups meet at a piece's end
+  uint64_t* psync = xsync + 1;        // [8] the two warps of the same rows meet
   // a piece's drafted rows with non-finite V: [0] the last such piece, [1 + j]
   // the last piece whose row j was one (pieces count from 1)
   volatile int* bad = reinterpret_cast<volatile int*>(sm + L::bad_off);
@@ -142,15 +148,16 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     mbar_init(qfree, 1);
     for (int x = 0; x < 2; ++x) {
       mbar_init(&sfull[x], 1);
-      mbar_init(&pfull[x], 4);
+      mbar_init(&pfull[x], 8);
     }
     mbar_init(oend, 1);
-    mbar_init(ofree, 8);
-    mbar_init(xsync, 8);
+    mbar_init(ofree, kDtSoftWarps);
+    mbar_init(xsync, kDtSoftWarps);
+    for (int i = 0; i < 8; ++i) mbar_init(&psync[i], 2);
     fence_barrier_init();
   }
   if (t < 65) bad[t] = 0;
-  if (warp == 9 && lane == 0) {
+  if (warp == kDtSoftWarps + 1 && lane == 0) {
     prefetch_tensormap(&tmq);
     prefetch_tensormap(&tmk);
     prefetch_tensormap(&tmv);
@@ -167,7 +174,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
 
   if (n <= 0) {
     // nothing to do: only the TMEM to give back
-  } else if (warp == 9) {
+  } else if (warp == kDtSoftWarps + 1) {
     // ============================================================ producer
     const int TB = draft_tc_box_rows(P);  // rows per box
     const int j = lane;                   // this lane's box
@@ -216,38 +223,40 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       q_wanted = false;
       return true;
     };
-    // all lanes: wait until ring slot `it % kItems` may be written
-    auto wait_slot = [&](int it) -> bool {
+    // all lanes: wait until the next ring slot may be written
+    int slot = 0;
+    uint32_t round = 0;
+    auto wait_slot = [&]() -> bool {
       int good = 1;
       if (lane == 0) {
-        uint64_t* b = &freeb[it % kItems];
-        const uint32_t par = ((it / kItems) - 1) & 1;
         try_q(false);
-        if (it >= kItems && !mbar_try_wait(b, par)) {
+        if (round > 0 && !mbar_try_wait(&freeb[slot], (round - 1) & 1)) {
           const uint64_t t0 = global_timer_ns();
-          while (!mbar_try_wait(b, par)) {
-            try_q(false);
-            if (global_timer_ns() - t0 > kWaitLimitNs) {
-              good = 0;
-              break;
+          good = 0;
+          do {
+            for (int i_ = 0; i_ < 64 && !good; ++i_) {
+              try_q(false);
+              good = mbar_try_wait(&freeb[slot], (round - 1) & 1);
             }
-          }
+          } while (!good && global_timer_ns() - t0 <= kWaitLimitNs);
         }
       }
       return __shfl_sync(0xffffffffu, good, 0) != 0;
     };
     struct Boxes {
-      int blk, brow, n, head;
+      int group, n, head;  // first row group, boxes, kv head
     };
     auto load = [&](const CUtensorMap* tm, const Boxes& x) -> bool {
-      if (!wait_slot(item)) return false;
-      const int sl = item % kItems;
-      if (lane == 0) mbar_arrive_expect_tx(&full[sl], (uint32_t)(x.n * TB * D * 2));
+      if (!wait_slot()) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(x.n * TB * D * 2));
       __syncwarp();
       if (j < x.n)
-        tma_load_5d(ring + (size_t)sl * L::kTile + j * TB * H * 128, tm, 0, 0, 0, x.head,
-                    (int)((int64_t)x.blk * (P / kRowGroup) + x.brow / kRowGroup), &full[sl]);
+        tma_load_5d(ring + slot * L::kTile + j * TB * H * 128, tm, 0, 0, 0, x.head, x.group, &full[slot]);
       ++item;
+      if (++slot == kItems) {
+        slot = 0;
+        ++round;
+      }
       return true;
     };
     int emitted = 0;
@@ -286,15 +295,13 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         q_two = pair;
       }
       Boxes b;
-      b.blk = blk_next;
       b.n = (nvalid + TB - 1) / TB;
-      b.brow = (t0 + j * TB) % P;
       b.head = kvh;
-      const bool badid = j < b.n && (b.blk < 0 || (int64_t)b.blk >= a.num_blocks);
-      if (badid) {
+      if (j < b.n && (blk_next < 0 || (int64_t)blk_next >= a.num_blocks)) {
         atomicOr(a.err, PKV_DEVERR_BLOCK);
-        b.blk = (int)a.num_blocks;  // zero-filled out-of-range box
-        b.brow = 0;
+        b.group = (int)a.num_blocks * (P / kRowGroup);  // zero-filled out-of-range box
+      } else {
+        b.group = blk_next * (P / kRowGroup) + (t0 + j * TB) % P / kRowGroup;
       }
       if (lane == 0) {
         DtDesc* d = &descs[emitted % kDtDescs];
@@ -327,34 +334,38 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         if (pieces > 0 && !q_wanted) mbar_wait(qfull, (pieces - 1) & 1);
       }
     }
-  } else if (warp == 8) {
+  } else if (warp == kDtSoftWarps) {
     // ============================================================ MMA issue
     if (lane == 0) {
       const uint32_t idqk = tc::idesc_bf16_f32(kDraftRows, kDraftKeys, 0, 0) |
                             (a.qscale < 0.f ? tc::kIdescNegateA : 0u);
       constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kDraftRows, D, 0, 1);
-      // Jobs alternate between the groups: job j is group j & 1's.
-      struct Job {
-        int vitem;  // ring item of its V
-        bool first, piece_first, piece_last, frees;  // of its group in the piece; of the piece; V's last use
-      };
-      Job pend[2] = {};
+      // Jobs alternate between the groups: job j is group j & 1's.  What a PV
+      // needs of its job is kept for the two jobs at most between their QK and
+      // their PV, in registers: its V's ring slot and phase, and the flags.
+      constexpr int kFirst = 1, kPieceFirst = 2, kPieceLast = 4, kFrees = 8;
+      uint32_t info0 = 0, info1 = 0;  // flags, phase << 4, slot << 5
       int jn = 0, pv = 0, pieces = 0, pieces_done = 0;  // QKs and PVs issued, pieces begun and finished
-      bool fresh[2] = {true, true};
+      uint32_t fresh = 3;             // bit x: no job of group x in this piece yet
+      // descriptors differ in their address field alone
+      const uint64_t kdesc = tc::smem_desc_sw128(smem_u32(ring), 16, kGroupBytes);
+      const uint64_t vdesc = tc::smem_desc_sw128(smem_u32(ring), 1024, kGroupBytes);
+      const uint64_t qdesc = tc::smem_desc_sw128(smem_u32(qs), 16, 1024);
       auto issue_pv = [&]() -> bool {  // of job pv
-        const Job q = pend[pv & 1];
-        const int x = pv & 1, sl = q.vitem % kItems;
-        if (!mbar_wait(&pfull[x], (pv >> 1) & 1) || !mbar_wait(&full[sl], (q.vitem / kItems) & 1)) return false;
-        if (q.piece_first && pieces_done > 0 && !mbar_wait(ofree, (pieces_done - 1) & 1)) return false;
+        const int x = pv & 1;
+        const uint32_t q = x ? info1 : info0;
+        const uint32_t sl = q >> 5;
+        if (!mbar_wait(&pfull[x], (pv >> 1) & 1) || !mbar_wait(&full[sl], (q >> 4) & 1)) return false;
+        if ((q & kPieceFirst) && pieces_done > 0 && !mbar_wait(ofree, (pieces_done - 1) & 1)) return false;
         tc::fence_after_sync();
-        const uint32_t vb = smem_u32(ring + (size_t)sl * L::kTile);
+        const uint64_t vd = vdesc + sl * (L::kTile >> 4);
+        const uint32_t tO = tmem + 256 + x * 128, tP = tmem + x * 128;
 #pragma unroll
         for (int k = 0; k < kDraftKeys / 16; ++k)
-          tc::mma_bf16_ta(tmem + 256 + x * 128, tmem + x * 128 + k * 8,
-                          tc::smem_desc_sw128(vb + k * 2 * kGroupBytes, 1024, kGroupBytes), kIdPV,
-                          (k > 0 || !q.first) ? 1u : 0u);
-        if (q.frees) tc::commit(&freeb[sl]);
-        if (q.piece_last) {
+          tc::mma_bf16_ta(tO, tP + (k >> 1) * 32 + (k & 1) * 8, vd + ((k * 2 * kGroupBytes) >> 4), kIdPV,
+                          (k > 0 || !(q & kFirst)) ? 1u : 0u);
+        if (q & kFrees) tc::commit(&freeb[sl]);
+        if (q & kPieceLast) {
           tc::commit(oend);
           ++pieces_done;
         }
@@ -362,39 +373,51 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         return true;
       };
       bool ok = true;
+      uint32_t slot = 0, phase = 0;  // of the ring item that comes next
+      auto advance = [&]() {
+        if (++slot == kItems) {
+          slot = 0;
+          phase ^= 1u;
+        }
+      };
       for (int e = 0; ok; ++e) {
         if (pv + 1 < jn && !(ok = issue_pv())) break;
         if (!(ok = mbar_wait(&dfull[e % kDtDescs], (e / kDtDescs) & 1))) break;
         const int fl = descs[e % kDtDescs].a.w;
         if (fl & kDtDone) break;
         if (fl & kDtStart) {
-          fresh[0] = fresh[1] = true;
+          fresh = 3;
           if (!(ok = mbar_wait(qfull, pieces & 1))) break;
           ++pieces;
         }
-        const int kitem = 2 * e, sl = kitem % kItems;
-        if (!(ok = mbar_wait(&full[sl], (kitem / kItems) & 1))) break;
+        const uint32_t ksl = slot;
+        if (!(ok = mbar_wait(&full[ksl], phase))) break;
+        advance();
+        const uint32_t vinfo = (slot << 5) | (phase << 4);
+        advance();
         const int uses = (kTiles > 1 && (fl & kDtPair)) ? 2 : 1;
         for (int u = 0; u < uses; ++u) {
           if (pv + 1 < jn && !(ok = issue_pv())) break;
           const int x = jn & 1;
           tc::fence_after_sync();
-          const uint32_t kb = smem_u32(ring + (size_t)sl * L::kTile);
-          const uint32_t qb = smem_u32(qs + u * L::kTile);
+          const uint64_t kd = kdesc + ksl * (L::kTile >> 4), qd = qdesc + u * (L::kTile >> 4);
+          const uint32_t tS = tmem + x * 128;
 #pragma unroll
           for (int k = 0; k < D / 16; ++k)
-            tc::mma_bf16(tmem + x * 128,
-                         tc::smem_desc_sw128(qb + (k >> 2) * L::kHalf + (k & 3) * 32, 16, 1024),
-                         tc::smem_desc_sw128(kb + (k >> 2) * 1024 + (k & 3) * 32, 16, kGroupBytes), idqk,
-                         k > 0 ? 1u : 0u);
+            tc::mma_bf16(tS, qd + (((k >> 2) * L::kHalf + (k & 3) * 32) >> 4),
+                         kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idqk, k > 0 ? 1u : 0u);
           tc::commit(&sfull[x]);
           const bool last = u == uses - 1;
           if (last) {
-            tc::commit(&freeb[sl]);
+            tc::commit(&freeb[ksl]);
             if (fl & kDtEnd) tc::commit(qfree);
           }
-          pend[jn & 1] = {kitem + 1, fresh[x], (fl & kDtStart) && u == 0, (fl & kDtEnd) && last, last};
-          fresh[x] = false;
+          const uint32_t q = vinfo | ((fresh >> x) & 1u ? kFirst : 0) |
+                             ((fl & kDtStart) && u == 0 ? kPieceFirst : 0) |
+                             ((fl & kDtEnd) && last ? kPieceLast : 0) | (last ? kFrees : 0);
+          if (x) info1 = q;
+          else info0 = q;
+          fresh &= ~(1u << x);
           ++jn;
         }
       }
@@ -403,20 +426,31 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     }
   } else {
     // ============================================================ softmax
-    const int x = warp >> 2;
+    const int x = warp >> 3, half = (warp >> 2) & 1;
     const int row = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;
-    const uint32_t tS = tmem + x * 128 + lane_base;
+    // this thread's 64 columns of S; the weights of each 32 overlay their first 16
+    const uint32_t tS = tmem + x * 128 + half * 64 + lane_base;
+    float* mine = exch + (warp >> 2) * kDraftRows + row;
+    const float* other = exch + ((warp >> 2) ^ 1) * kDraftRows + row;
+    uint64_t* pair_bar = &psync[(warp >> 3) * 4 + (warp & 3)];
     // the sign of the scale is in the QK; 1e-37 keeps a hidden score -inf
     // where the scale is 0
     const float cs = fmaxf(fabsf(a.qscale), 1e-37f);
     float m = -INFINITY, l = 0.f;
     uint64_t mask = 0;
-    bool live = false, warp_live = false, fresh = true;
-    int rowg = 0, jobs = 0, syncs = 0;
+    bool live = false, warp_live = false;
+    bool fresh = true, newpiece = true;  // no job of this group in the piece yet
+    int rowg = 0, jobs = 0, syncs = 0, meets = 0;
     bool ok = true;
     auto wait = [&](uint64_t* b, uint32_t parity) -> bool {
       return __all_sync(0xffffffffu, mbar_wait(b, parity));
+    };
+    // the two warps of the same rows: what they wrote before is read after
+    auto meet = [&]() -> bool {
+      __syncwarp();
+      if (lane == 0) mbar_arrive(pair_bar);
+      return wait(pair_bar, meets++ & 1);
     };
     for (int e = 0;; ++e) {
       if (!(ok = wait(&dfull[e % kDtDescs], (e / kDtDescs) & 1))) break;
@@ -429,7 +463,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       if (fl & kDtStart) {
         m = -INFINITY;
         l = 0.f;
-        fresh = true;
+        fresh = newpiece = true;
         rowg = (pair ? x ^ first_group : 0) * kDraftRows + row;
         live = rowg < db.z;
         warp_live = __any_sync(0xffffffffu, live);
@@ -444,81 +478,89 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         ++jobs;
         tc::fence_after_sync();
         if (warp_live) {
-          uint32_t v[kDraftKeys];
+          // 32 columns at a time (all 64 in registers would spill): both for
+          // the maximum, then the second's weights, then the first's, read again
+          uint32_t v[32];
+          auto hide = [&](int w) {
+            if (!(fl & kDtTail)) return;
+            const uint32_t bits = mask_word(mask, mb, 2 * half + w);
 #pragma unroll
-          for (int c0 = 0; c0 < kDraftKeys; c0 += 32)
-            tc::tmem_ld32(tS + c0, *reinterpret_cast<uint32_t(*)[32]>(v + c0));
-          tc::wait_ld();
-          if (fl & kDtTail) {
+            for (int i = 0; i < 32; ++i)
+              if (!((bits >> i) & 1u)) v[i] = __float_as_uint(-INFINITY);
+          };
+          float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int w = 0; w < 4; ++w) {
-              const uint32_t bits = mask_word(mask, mb, w);
+          for (int w = 0; w < 2; ++w) {
+            tc::tmem_ld32(tS + 32 * w, v);
+            tc::wait_ld32(v);
+            hide(w);
 #pragma unroll
-              for (int i = 0; i < 32; ++i)
-                if (!((bits >> i) & 1u)) v[32 * w + i] = __float_as_uint(-INFINITY);
-            }
+            for (int i = 0; i < 32; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(v[i]));
           }
-          float mx8[8];
-#pragma unroll
-          for (int u = 0; u < 8; ++u) mx8[u] = __uint_as_float(v[u]);
-#pragma unroll
-          for (int i = 8; i < kDraftKeys; ++i) mx8[i & 7] = fmaxf(mx8[i & 7], __uint_as_float(v[i]));
-          const float mx = cs * fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                                      fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          float mx = fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+          // the exchange slots were last read at the previous piece's end
+          if (newpiece && db.w > 1 && !(ok = wait(ofree, (db.w - 2) & 1))) break;
+          *mine = mx;
+          if (!(ok = meet())) break;
+          mx = cs * fmaxf(mx, *other);
           const float m_new = fmaxf(m, mx);
           const bool need = live && m_new > m + 8.0f;
           const float alpha = need ? exp2f(m - m_new) : 1.f;
           if (need) m = m_new;
           const float nm = m == -INFINITY ? 0.f : -m;  // nothing seen yet: every weight is 0
           // ---- P = exp2(c s - m) in bf16 pairs; the sums take it unrounded
-          uint32_t pw[kDraftKeys / 2];
-          float2 ls4[4];
+          float2 ls2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
-          for (int u = 0; u < 4; ++u) ls4[u] = make_float2(0.f, 0.f);
+          for (int w = 1; w >= 0; --w) {
+            if (w == 0) {
+              tc::tmem_ld32(tS, v);
+              tc::wait_ld32(v);
+              hide(0);
+            }
+            uint32_t pw[16];
 #pragma unroll
-          for (int i = 0; i < kDraftKeys / 2; ++i) {
-            const float p0 = exp2f(fmaf(__uint_as_float(v[2 * i]), cs, nm));
-            const float p1 = exp2f(fmaf(__uint_as_float(v[2 * i + 1]), cs, nm));
-            ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(p0, p1));
-            const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
-            pw[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            for (int i = 0; i < 16; ++i) {
+              const float p0 = exp2f(fmaf(__uint_as_float(v[2 * i]), cs, nm));
+              const float p1 = exp2f(fmaf(__uint_as_float(v[2 * i + 1]), cs, nm));
+              ls2[i & 1] = __fadd2_rn(ls2[i & 1], make_float2(p0, p1));
+              const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+              pw[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            }
+            tc::tmem_st16(tS + 32 * w, pw);
           }
-          const float2 ls2 = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
-          l = l * alpha + (ls2.x + ls2.y);
+          const float2 ls = __fadd2_rn(ls2[0], ls2[1]);
+          l = l * alpha + (ls.x + ls.y);
           // O holds every PV of this group but this job's: its S was computed
-          // after them
+          // after them.  The row's two threads rescale half of it each.
           if (!fresh && __any_sync(0xffffffffu, need)) {
-            const uint32_t tO = tmem + 256 + x * 128 + lane_base;
+            const uint32_t tO = tmem + 256 + x * 128 + half * (D / 2) + lane_base;
 #pragma unroll 1
-            for (int c0 = 0; c0 < D; c0 += 32) {
-              uint32_t o[32];
-              tc::tmem_ld32(tO + c0, o);
+            for (int c0 = 0; c0 < D / 2; c0 += 16) {
+              uint32_t o[16];
+              tc::tmem_ld16(tO + c0, o);
               tc::wait_ld();
 #pragma unroll
-              for (int i = 0; i < 32; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
-              tc::tmem_st32(tO + c0, o);
+              for (int i = 0; i < 16; ++i) o[i] = __float_as_uint(__uint_as_float(o[i]) * alpha);
+              tc::tmem_st16(tO + c0, o);
             }
           }
-          tc::tmem_st32(tS, *reinterpret_cast<const uint32_t(*)[32]>(pw));
-          tc::tmem_st32(tS + 32, *reinterpret_cast<const uint32_t(*)[32]>(pw + 32));
           tc::wait_st();
         }
-        fresh = false;
+        fresh = newpiece = false;
         // The stage's first job clears what the PVs must not multiply: V rows
         // past the last one (weight 0, any bytes), and non-finite elements of
         // drafted rows, which some row may not see.
         if ((fl & kDtTail) && x == first_group) {
-          const int vitem = 2 * e + 1;
+          const int vitem = 2 * e + 1;  // K and V of a stage are ring items 2 e and 2 e + 1
           if (!(ok = wait(&full[vitem % kItems], (vitem / kItems) & 1))) break;
           if (row >= mb) {
             unsigned char* vr = ring + (size_t)(vitem % kItems) * L::kTile + (row / kRowGroup) * kGroupBytes +
                                 (row % kRowGroup) * 128;
             bool found = false;
-#pragma unroll
-            for (int hf = 0; hf < H; ++hf)
-#pragma unroll
+            if (half < H) {  // 64 columns a thread
+#pragma unroll 2
               for (int ch = 0; ch < 8; ++ch) {
-                uint4* at = reinterpret_cast<uint4*>(vr + hf * 1024 + ch * 16);
+                uint4* at = reinterpret_cast<uint4*>(vr + half * 1024 + ch * 16);
                 if (row >= nvalid) {
                   *at = make_uint4(0u, 0u, 0u, 0u);
                   continue;
@@ -540,6 +582,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
                 if (any) *at = make_uint4(q[0], q[1], q[2], q[3]);
                 found |= any;
               }
+            }
             if (found) {
               bad[1 + row - mb] = db.w;
               bad[0] = db.w;
@@ -555,7 +598,18 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         // ---- a piece's end: O / l and the LSE of each row
         if (!(ok = wait(oend, (db.w - 1) & 1))) break;
         tc::fence_after_sync();
-        if (!pair) exch[x * kDraftRows + row] = make_float2(m, l);
+        float M = m, Ls = l, f0 = 1.f, f1 = 1.f;
+        bool has0 = x == 0, has1 = x == 1;  // accumulators that hold this row's outputs
+        if (warp_live) {
+          // the row's sum: its two threads'
+          *mine = l;
+          if (!(ok = meet())) break;
+          Ls = half == 0 ? l + *other : *other + l;
+          if (!pair) {  // then the groups' states: (m, sum) of each
+            if (!(ok = meet())) break;
+            *mine = half == 0 ? m : Ls;
+          }
+        }
         if (!pair || (fl & kDtTail)) {  // the groups' states, and `bad`
           __syncwarp();
           if (lane == 0) mbar_arrive(xsync);
@@ -563,23 +617,18 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           ++syncs;
         }
         if (warp_live) {
-          float f0 = 0.f, f1 = 0.f, M = m, Ls = l;
-          bool has0 = x == 0, has1 = x == 1;  // accumulators that hold this row's outputs
           if (!pair) {
-            const float2 s0 = exch[row], s1 = exch[kDraftRows + row];
-            const bool only = (fl & kDtStart) != 0;  // one stage: one group's work
-            has0 = !only || first_group == 0;
-            has1 = !only || first_group == 1;
-            M = fmaxf(s0.x, s1.x);
+            const float mo = exch[2 * (x ^ 1) * kDraftRows + row], lo = exch[(2 * (x ^ 1) + 1) * kDraftRows + row];
+            const float m0 = x == 0 ? m : mo, m1 = x == 0 ? mo : m, l0 = x == 0 ? Ls : lo, l1 = x == 0 ? lo : Ls;
+            M = fmaxf(m0, m1);
             const float base = M == -INFINITY ? 0.f : M;
-            f0 = exp2f(s0.x - base);
-            f1 = exp2f(s1.x - base);
-            // an empty state adds nothing (its l is 0, its factor 0 or 1)
-            Ls = f0 * s0.y + f1 * s1.y;
-            has0 = has0 && s0.y != 0.f;
-            has1 = has1 && s1.y != 0.f;
-          } else {
-            f0 = f1 = 1.f;
+            f0 = exp2f(m0 - base);
+            f1 = exp2f(m1 - base);
+            Ls = f0 * l0 + f1 * l1;
+            // a group without a job in the piece (one stage), or without a
+            // seen key, has nothing in its O
+            has0 = l0 != 0.f;
+            has1 = l1 != 0.f;
           }
           const float inv = Ls == 0.f ? 0.f : 1.f / Ls;
           f0 *= inv;
@@ -590,23 +639,33 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           const int64_t qh = (int64_t)(db.y + tok) * a.num_q_heads + kvh * G + g;
           const int64_t rec = (2 * (int64_t)c + ((fl & kDtSlot1) ? 1 : 0)) * kRecRows + rowg;
           const bool whole = (fl & kDtWhole) != 0;
-          if (live && (pair || x == 0)) {
+          if (live && half == 0 && (pair || x == 0)) {
             if (!whole) a.rec_lse[rec] = lse2;
             else if (a.lse_out) a.lse_out[qh] = lse2 * kDtLn2;
           }
           const bool fix = bad[0] == db.w;
-          const int c_lo = pair ? 0 : x * (D / 2), c_hi = pair ? D : c_lo + D / 2;
+          // columns: half of them each in a pair, a quarter otherwise, 16 at a time
+          const int span = pair ? D / 2 : D / 4;
+          const int c_lo = pair ? half * (D / 2) : (x * 2 + half) * (D / 4);
 #pragma unroll 1
-          for (int c0 = c_lo; c0 < c_hi; c0 += 32) {
-            float o[32];
-            uint32_t w0[32], w1[32];
-            if (!pair || x == 0) tc::tmem_ld32(tmem + 256 + lane_base + c0, w0);
-            if (!pair || x == 1) tc::tmem_ld32(tmem + 384 + lane_base + c0, w1);
-            tc::wait_ld();
+          for (int c0 = c_lo; c0 < c_lo + span; c0 += 16) {
+            float o[16];
+            uint32_t w[16];
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              o[i] = has0 ? __uint_as_float(w0[i]) * f0 : 0.f;
-              if (has1) o[i] = fmaf(__uint_as_float(w1[i]), f1, o[i]);
+            for (int i = 0; i < 16; ++i) o[i] = 0.f;
+            if (!pair || x == 0) {
+              tc::tmem_ld16(tmem + 256 + lane_base + c0, w);
+              tc::wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (has0) o[i] = __uint_as_float(w[i]) * f0;
+            }
+            if (!pair || x == 1) {
+              tc::tmem_ld16(tmem + 384 + lane_base + c0, w);
+              tc::wait_ld();
+#pragma unroll
+              for (int i = 0; i < 16; ++i)
+                if (has1) o[i] = fmaf(__uint_as_float(w[i]), f1, o[i]);
             }
             if (fix && live) {  // non-finite elements that this row does see
               for (uint64_t left = mask; left; left &= left - 1) {
@@ -618,7 +677,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
                 const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) +
                                           (((int64_t)blk * P + pos % P) * Hkv + kvh) * D + c0;
 #pragma unroll
-                for (int i = 0; i < 32; ++i) {
+                for (int i = 0; i < 16; ++i) {
                   const uint32_t u = __bfloat16_as_ushort(vp[i]);
                   if ((u & 0x7f80u) == 0x7f80u) o[i] += __uint_as_float(u << 16);
                 }
@@ -628,19 +687,19 @@ __global__ void __launch_bounds__(kDtThreads, 1)
               if (whole) {
                 uint4* dst = reinterpret_cast<uint4*>(static_cast<__nv_bfloat16*>(a.out) + qh * D + c0);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  uint32_t w[4];
+                for (int i = 0; i < 2; ++i) {
+                  uint32_t b[4];
 #pragma unroll
                   for (int u = 0; u < 4; ++u) {
                     const __nv_bfloat162 b2 = __floats2bfloat162_rn(o[8 * i + 2 * u], o[8 * i + 2 * u + 1]);
-                    w[u] = *reinterpret_cast<const uint32_t*>(&b2);
+                    b[u] = *reinterpret_cast<const uint32_t*>(&b2);
                   }
-                  dst[i] = make_uint4(w[0], w[1], w[2], w[3]);
+                  dst[i] = make_uint4(b[0], b[1], b[2], b[3]);
                 }
               } else {
                 float4* dst = reinterpret_cast<float4*>(a.rec_o + rec * D + c0);
 #pragma unroll
-                for (int i = 0; i < 8; ++i)
+                for (int i = 0; i < 4; ++i)
                   dst[i] = make_float4(o[4 * i], o[4 * i + 1], o[4 * i + 2], o[4 * i + 3]);
               }
             }

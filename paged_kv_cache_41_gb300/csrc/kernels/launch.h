@@ -250,6 +250,7 @@ struct DraftArgs {
   float* rec_o;                 // states: draft.cu [B, max_draft, Hq, num_splits, D],
   float* rec_lse;               // draft_tc.cu [2 num_ctas, rows, D]; their LSEs, base 2
   int64_t* plan_pre;            // draft_tc.cu: [B + 1], the work split of plan.cuh
+  int2* cut_segs;               // draft_tc.cu: [num_ctas] (sequence, segment) cut at a CTA's end, or -1
   int64_t num_blocks;
   int32_t max_blocks;
   int32_t num_seqs;

@@ -801,7 +801,7 @@ struct DraftWorkspace {
   int32_t splits;             // CUDA cores
   int32_t tiles, row_tiles;   // tensor cores: 128-row tiles of a segment, segments per kv head
   int32_t ctas;
-  size_t lse_off, o_off, total;
+  size_t cut_off, lse_off, o_off, total;
 };
 
 DraftWorkspace draft_workspace(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
@@ -818,7 +818,8 @@ DraftWorkspace draft_workspace(const pkv_cache_desc* c, int32_t num_seqs, int32_
     const int64_t sms = sm_count();
     w.ctas = (int32_t)(stages < sms ? stages : sms);
     const int64_t recs = 2 * (int64_t)w.ctas * per;
-    w.lse_off = align256((size_t)(num_seqs + 1) * 8);
+    w.cut_off = align256((size_t)(num_seqs + 1) * 8);
+    w.lse_off = w.cut_off + align256((size_t)w.ctas * 8);
     w.o_off = w.lse_off + align256((size_t)recs * 4);
     w.total = w.o_off + align256((size_t)(recs * c->head_dim) * 4);
     return w;
@@ -883,6 +884,7 @@ pkv_status pkv_draft_tree_attention(
   a.err = err;
   unsigned char* base = static_cast<unsigned char*>(workspace);
   a.plan_pre = reinterpret_cast<int64_t*>(base);
+  a.cut_segs = reinterpret_cast<int2*>(base + w.cut_off);
   a.rec_lse = reinterpret_cast<float*>(base + w.lse_off);
   a.rec_o = reinterpret_cast<float*>(base + w.o_off);
   a.num_blocks = cache->num_blocks;

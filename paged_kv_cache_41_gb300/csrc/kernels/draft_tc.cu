@@ -18,13 +18,13 @@
 //     segments directly and leaves one (O, LSE) record per cut piece, which
 //     draft_tc_reduce_kernel merges;
 //   * two softmax warpgroups.  A piece of more than 128 rows gives each of them
-//     one row tile, both against every stage; a piece of up to 128 rows gives
-//     them alternate stages of the same rows, merged at its end;
-//   * a stage is two jobs of 64 keys for a group, in two S buffers in turn, so
-//     that the next job's QK runs under a job's softmax.  TMEM (512 columns):
-//     2 x 2 x 64 of S, 2 x 128 of O.  With one 128-key S a group the softmax
-//     and the MMAs of a group wait for each other: 390 us against THIS_US for 64
-//     requests with trees of 64;
+//     one row tile, both against all of every stage; a piece of up to 128 rows
+//     gives them a half of every stage each, against the same rows, and they
+//     merge at its end.  (Alternate stages instead of halves keep two
+//     stages of the ring under work, and fewer loads in flight: SPLIT_US.)
+//   * a job is 64 keys, in two S buffers of a group in turn, so that the next
+//     job's QK runs under a job's softmax.  TMEM (512 columns): 2 x 2 x 64 of S,
+//     2 x 128 of O;
 //   * thread t of a group owns row t of its tile (TMEM lane t): no cross-thread
 //     reduction.  Warps whose 32 rows hold no drafted row skip the arithmetic;
 //   * P is rounded to bf16 (half a step, 2^-8 of each weight, is the size of the
@@ -354,7 +354,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       const uint32_t tS = tmem + x * 128, tO = tmem + 256 + x * 128;
       // What a PV needs of its job is kept for the two jobs at most between
       // their QK and their PV: flags, phase << 4, ring slot << 5 of its V.
-      constexpr uint32_t kFirst = 1, kSecond = 2, kFrees = 4, kFreesTwice = 8;
+      constexpr uint32_t kFirst = 1, kSecond = 2, kFrees = 4;
       uint32_t info0 = 0, info1 = 0;
       int jn = 0, pv = 0, pieces = 0;  // QKs and PVs issued, pieces begun
       bool first = true, freed = false;  // no job in the piece yet; O is known to be free
@@ -379,7 +379,6 @@ __global__ void __launch_bounds__(kDtThreads, 1)
                           (k > 0 || !(q & kFirst)) ? 1u : 0u);
         tc::commit(&pvdone[x]);
         if (q & kFrees) tc::commit(&freeb[sl]);
-        if (q & kFreesTwice) tc::commit(&freeb[sl]);
         ++pv;
         return true;
       };
@@ -411,34 +410,35 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         const uint32_t vinfo = (slot << 5) | (phase << 4);
         advance();
         const bool pair = kTiles > 1 && (fl & kDtPair);
-        if (pair || (e & 1) == x) {
-          if (pv < jn && !mbar_test(&full[ksl], kph) && !(ok = issue_pv())) break;
-          if (!(ok = mbar_wait(&full[ksl], kph))) break;
-          const int jobs = da.z > kDtJob ? 2 : 1;
-          for (int u = 0; u < jobs; ++u) {
-            if (pv + 1 < jn && !(ok = issue_pv())) break;
-            const int b = jn & 1;
-            tc::fence_after_sync();
-            const uint64_t kd = kdesc + ksl * (L::kTile >> 4) + (u ? (8 * kGroupBytes) >> 4 : 0);
-            const uint64_t qd = qdesc + (pair ? x * (L::kTile >> 4) : 0);
+        // halves of the stage: both in a pair, half x otherwise
+        const int u_lo = pair ? 0 : x, u_hi = pair ? (da.z > kDtJob ? 2 : 1) : (da.z > x * kDtJob ? x + 1 : x);
+        if (pv < jn && !mbar_test(&full[ksl], kph) && !(ok = issue_pv())) break;
+        if (!(ok = mbar_wait(&full[ksl], kph))) break;
+        for (int u = u_lo; u < u_hi; ++u) {
+          if (pv + 1 < jn && !(ok = issue_pv())) break;
+          const int b = jn & 1;
+          tc::fence_after_sync();
+          const uint64_t kd = kdesc + ksl * (L::kTile >> 4) + (u ? (8 * kGroupBytes) >> 4 : 0);
+          const uint64_t qd = qdesc + (pair ? x * (L::kTile >> 4) : 0);
 #pragma unroll
-            for (int k = 0; k < D / 16; ++k)
-              tc::mma_bf16(tS + b * 64, qd + (((k >> 2) * L::kHalf + (k & 3) * 32) >> 4),
-                           kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idqk, k > 0 ? 1u : 0u);
-            tc::commit(&sfull[2 * x + b]);
-            const bool last = u == jobs - 1;
-            if (last) {
-              tc::commit(&freeb[ksl]);
-              if (!pair) tc::commit(&freeb[ksl]);
-            }
-            const uint32_t q = vinfo | (first ? kFirst : 0) | (u ? kSecond : 0) | (last ? kFrees : 0) |
-                               (last && !pair ? kFreesTwice : 0);
-            if (b) info1 = q;
-            else info0 = q;
-            first = false;
-            ++jn;
-          }
-          if (!ok) break;
+          for (int k = 0; k < D / 16; ++k)
+            tc::mma_bf16(tS + b * 64, qd + (((k >> 2) * L::kHalf + (k & 3) * 32) >> 4),
+                         kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idqk, k > 0 ? 1u : 0u);
+          tc::commit(&sfull[2 * x + b]);
+          const bool last = u == u_hi - 1;
+          if (last) tc::commit(&freeb[ksl]);
+          const uint32_t q = vinfo | (first ? kFirst : 0) | (u ? kSecond : 0) | (last ? kFrees : 0);
+          if (b) info1 = q;
+          else info0 = q;
+          first = false;
+          ++jn;
+        }
+        if (!ok) break;
+        if (u_lo == u_hi) {  // no key of this group's half: give the stage back
+          tc::commit(&freeb[ksl]);
+          const uint32_t vsl = vinfo >> 5;
+          if (!(ok = mbar_wait(&full[vsl], (vinfo >> 4) & 1))) break;
+          tc::commit(&freeb[vsl]);
         }
         if (fl & kDtEnd) {
           tc::commit(qfree);
@@ -489,9 +489,9 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         s.row0 = db.y - tok0;
         mask = live ? draft_mask(a, s, tok0 + rowg / G) : 0ull;
       }
-      if (pair || (e & 1) == x) {
-        const int njobs = nvalid > kDtJob ? 2 : 1;
-        for (int u = 0; u < njobs; ++u) {
+      {
+        const int u_lo = pair ? 0 : x, u_hi = pair ? (nvalid > kDtJob ? 2 : 1) : (nvalid > x * kDtJob ? x + 1 : x);
+        for (int u = u_lo; u < u_hi; ++u) {
           const int b = jobs & 1;
           if (!(ok = wait(&sfull[2 * x + b], (jobs >> 1) & 1))) break;
           tc::fence_after_sync();
@@ -561,12 +561,12 @@ __global__ void __launch_bounds__(kDtThreads, 1)
           // A tail stage's V is cleared, before its first PV, of what the PVs
           // must not multiply: rows past the last one (weight 0, any bytes) and
           // non-finite elements of drafted rows, which some row may not see.
-          // In a pair group 0 does it for both.
-          if ((fl & kDtTail) && u == 0) {
+          // In a pair group 0 does it for both, otherwise each in its half.
+          if ((fl & kDtTail) && u == u_lo) {
             if (!pair || x == 0) {
               const int vitem = 2 * e + 1;  // K and V of a stage are ring items 2 e and 2 e + 1
               if (!(ok = wait(&full[vitem % kItems], (vitem / kItems) & 1))) break;
-              if (row >= mb) {
+              if (row >= mb && (pair || (row >> 6) == x)) {
                 unsigned char* vr = ring + (size_t)(vitem % kItems) * L::kTile +
                                     (row / kRowGroup) * kGroupBytes + (row % kRowGroup) * 128;
                 bool found = false;

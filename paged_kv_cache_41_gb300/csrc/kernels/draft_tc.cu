@@ -142,7 +142,8 @@ __global__ void __launch_bounds__(kDtThreads, 1)
   volatile int* bad = reinterpret_cast<volatile int*>(sm + L::bad_off);
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(sm + L::tmem_off);
 
-  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  // the warp number as a warp-uniform value, for the branches on it
+  const int t = threadIdx.x, warp = __shfl_sync(0xffffffffu, t >> 5, 0), lane = t & 31;
   const int c = blockIdx.x, P = a.block_size;
   const int Hkv = a.num_kv_heads, G = a.num_q_heads / Hkv;
   if (t == 0) {
@@ -347,7 +348,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
   } else if (warp >= kDtSoftWarps) {
     // ============================================================ MMA issue
     const int x = warp - kDtSoftWarps;  // of this group's jobs; job j uses S buffer j & 1
-    if (lane == 0) {
+    if (tc::elect_one()) {
       const uint32_t idqk = tc::idesc_bf16_f32(kDraftRows, kDtJob, 0, 0) |
                             (a.qscale < 0.f ? tc::kIdescNegateA : 0u);
       constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kDraftRows, D, 0, 1);

@@ -106,6 +106,13 @@ __device__ __forceinline__ void wait_ld32(uint32_t (&r)[32]) {
                  "+r"(r[31])::"memory");
 }
 
+// True in one thread of the (converged) warp.
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+
 // ---------------------------------------------------------------- descriptors
 // Shared-memory matrix descriptor, 128-byte swizzle.  K-major operands: rows
 // of 128 B (64 bf16 of the reduction dimension), 8-row groups `sbo` bytes

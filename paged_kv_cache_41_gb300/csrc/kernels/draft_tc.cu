@@ -91,6 +91,12 @@ struct DtSmem {
   static_assert(total <= 227 * 1024, "shared memory of one CTA");
 };
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // Eight floats to a 32-byte aligned address: one whole sector a thread.
 __device__ __forceinline__ void store_sector(float* p, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
@@ -367,11 +373,12 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         const int b = pv & 1;
         const uint32_t q = b ? info1 : info0;
         const uint32_t sl = q >> 5;
-        if (!mbar_wait(&pfull[2 * x + b], (pv >> 1) & 1) || !mbar_wait(&full[sl], (q >> 4) & 1)) return false;
-        if (!freed) {
+        if (!mbar_wait(&full[sl], (q >> 4) & 1)) return false;
+        if (!freed) {  // the piece's first PV: the previous piece's O has been read
           if (pieces > 1 && !mbar_wait(ofree, (pieces - 2) & 1)) return false;
           freed = true;
         }
+        if (!mbar_wait(&pfull[2 * x + b], (pv >> 1) & 1)) return false;
         tc::fence_after_sync();
         const uint64_t vd = vdesc + sl * (L::kTile >> 4) + ((q & kSecond) ? (8 * kGroupBytes) >> 4 : 0);
 #pragma unroll
@@ -393,12 +400,13 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       };
       for (int e = 0; ok; ++e) {
         uint64_t* db = &dfull[e % kDtDescs];
-        if (pv + 1 < jn && !(ok = issue_pv())) break;
-        // no QK can be issued ahead of the last PV: issue it first
-        if (pv < jn && !mbar_test(db, (e / kDtDescs) & 1) && !(ok = issue_pv())) break;
-        if (!(ok = mbar_wait(db, (e / kDtDescs) & 1))) break;
-        const int4 da = descs[e % kDtDescs].a;
-        const int fl = da.w;
+        if (!mbar_test(db, (e / kDtDescs) & 1)) {
+          // no QK can be issued ahead of the PVs that are due: issue them first
+          while (pv < jn && (ok = issue_pv())) {
+          }
+          if (!ok || !(ok = mbar_wait(db, (e / kDtDescs) & 1))) break;
+        }
+        const int nvalid = descs[e % kDtDescs].a.z, fl = descs[e % kDtDescs].a.w;
         if (fl & kDtDone) break;
         if (fl & kDtStart) {
           first = true;
@@ -412,9 +420,12 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         advance();
         const bool pair = kTiles > 1 && (fl & kDtPair);
         // halves of the stage: both in a pair, half x otherwise
-        const int u_lo = pair ? 0 : x, u_hi = pair ? (da.z > kDtJob ? 2 : 1) : (da.z > x * kDtJob ? x + 1 : x);
-        if (pv < jn && !mbar_test(&full[ksl], kph) && !(ok = issue_pv())) break;
-        if (!(ok = mbar_wait(&full[ksl], kph))) break;
+        const int u_lo = pair ? 0 : x, u_hi = pair ? (nvalid > kDtJob ? 2 : 1) : (nvalid > x * kDtJob ? x + 1 : x);
+        if (!mbar_test(&full[ksl], kph)) {
+          while (pv < jn && (ok = issue_pv())) {
+          }
+          if (!ok || !(ok = mbar_wait(&full[ksl], kph))) break;
+        }
         for (int u = u_lo; u < u_hi; ++u) {
           if (pv + 1 < jn && !(ok = issue_pv())) break;
           const int b = jn & 1;
@@ -514,12 +525,11 @@ __global__ void __launch_bounds__(kDtThreads, 1)
                   if (!((bits >> i) & 1u)) v[32 * w + i] = __float_as_uint(-INFINITY);
               }
             }
-            float mx4[4];
+            float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) mx4[i] = __uint_as_float(v[i]);
-#pragma unroll
-            for (int i = 4; i < 64; ++i) mx4[i & 3] = fmaxf(mx4[i & 3], __uint_as_float(v[i]));
-            const float mx = cs * fmaxf(fmaxf(mx4[0], mx4[1]), fmaxf(mx4[2], mx4[3]));
+            for (int i = 0; i < 64; i += 2)
+              mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            const float mx = cs * fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
             const float m_new = fmaxf(m, mx);
             const bool need = live && m_new > m + 8.0f;
             const float alpha = need ? exp2f(m - m_new) : 1.f;

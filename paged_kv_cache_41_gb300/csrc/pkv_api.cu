@@ -902,8 +902,12 @@ pkv_status pkv_draft_tree_attention(
     const int G = num_q_heads / cache->num_kv_heads;
     a.num_ctas = w.ctas;
     a.row_tiles = w.row_tiles;
+    // Work units (kernels/plan.cuh).  A least-squares fit of the CTAs' times
+    // gave a piece (its Q, the drained pipeline, its outputs) 0.8 stages with
+    // one row tile (16 requests, trees of 5 to 27) and 3.4 with two (64
+    // requests, trees of 64).
     a.stage_units = 2;
-    a.piece_units = 3;
+    a.piece_units = w.tiles > 1 ? 7 : 2;
     a.q_tokens = max_draft < pkv::kDraftRows / G ? max_draft : pkv::kDraftRows / G;
     const int box = pkv::draft_tc_box_rows(cache->block_size);
     CUtensorMap tmq, tmk, tmv;

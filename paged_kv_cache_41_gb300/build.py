@@ -28,6 +28,7 @@ CUDA_SOURCES = [
     "pkv_api.cu",
     "kernels/append_copy.cu",
     "kernels/decode.cu",
+    "kernels/decode_scores.cu",
     "kernels/decode_tc.cu",
     "kernels/decode_tc_mx.cu",
     "kernels/prefix_tc.cu",
@@ -40,6 +41,7 @@ CUDA_SOURCES = [
 # (softmax in base 2, well inside the attention tolerance).
 PER_SOURCE_FLAGS = {
     "kernels/decode.cu": ["--use_fast_math"],
+    "kernels/decode_scores.cu": ["--use_fast_math"],
     "kernels/decode_tc.cu": ["--use_fast_math"],
     "kernels/decode_tc_mx.cu": ["--use_fast_math"],
     "kernels/prefix_tc.cu": ["--use_fast_math"],

@@ -75,7 +75,7 @@ constexpr int kStart = 1, kEnd = 2, kWholeSeg = 4, kSlotOne = 8;
 
 }  // namespace
 
-template <int G>
+template <int G, bool kScores = false>
 __global__ void __launch_bounds__(kTcThreads, 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv,
@@ -233,7 +233,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int qb = (pieces - 1) % kQBufs;
       const int flags = (start ? kStart : 0) | (end ? kEnd : 0) |
                         (end && i == nt - 1 && dseg >= 0 ? kWholeSeg : 0) |
-                        (dseg > 0 ? kSlotOne : 0) | (qb << 4);
+                        (dseg > 0 ? kSlotOne : 0) | (qb << 4) | (kScores ? i << 6 : 0);
       const int nbox = (nvalid + TB - 1) / TB;  // per tensor
       int brow = (t0 + j * TB) % P;
       const bool bad = j < nbox && (blk < 0 || (int64_t)blk >= a.num_blocks);
@@ -398,6 +398,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       for (int g = 0; g < G; ++g) {
         sg[g] = row < nvalid ? __uint_as_float(v[g]) * cs : -INFINITY;
         pass |= sg[g] > m[g] + 8.0f;
+      }
+      if constexpr (kScores) {  // stage flags >> 6 of its segment
+        static_assert(G == 8, "two vectors of four");
+        if (row < nvalid) {
+          float4* at = reinterpret_cast<float4*>(
+              a.scores + (((int64_t)dsc.x * a.num_kv_heads + dsc.y) * a.scores_rows +
+                          (int64_t)(flags >> 6) * kTcRows + row) * G);
+          at[0] = make_float4(sg[0], sg[1], sg[2], sg[3]);
+          at[1] = make_float4(sg[4], sg[5], sg[6], sg[7]);
+        }
       }
       const bool wpass = __any_sync(0xffffffffu, pass);
       if (lane == 0) reinterpret_cast<int*>(&redf[b])[q4] = wpass ? 1 : 0;
@@ -579,9 +589,9 @@ int decode_tc_resident_ctas() {
 cudaError_t launch_paged_decode_tc(const CUtensorMap& tmk, const CUtensorMap& tmv,
                                    const CUtensorMap& tmq, const DecodeArgs& a,
                                    cudaStream_t stream) {
-  auto kern = decode_tc_kernel<8>;
-  static SmemAttrCache attr_cache;
-  cudaError_t e = ensure_smem_limit(kern, kTcSmem, attr_cache);
+  auto kern = a.scores ? decode_tc_kernel<8, true> : decode_tc_kernel<8>;
+  static SmemAttrCache attr_cache[2];
+  cudaError_t e = ensure_smem_limit(kern, kTcSmem, attr_cache[a.scores ? 1 : 0]);
   if (e != cudaSuccess) return e;
   e = launch_pdl(kern, dim3((unsigned)a.num_ctas), dim3(kTcThreads), kTcSmem, stream, tmk, tmv,
                  tmq, a);

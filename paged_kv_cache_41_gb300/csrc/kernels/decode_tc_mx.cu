@@ -109,7 +109,7 @@ __device__ __forceinline__ void scale_factors(uint32_t sc, int g, __nv_bfloat162
 
 }  // namespace
 
-template <int G>
+template <int G, bool kScores = false>
 __global__ void __launch_bounds__(kMxThreads, 1)
     decode_tc_mx_kernel(const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv,
@@ -227,7 +227,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       const int qb = (pieces - 1) % kQBufsMx;
       const int flags = (start ? kStart : 0) | (end ? kEnd : 0) |
                         (end && i == nt - 1 && dseg >= 0 ? kWholeSeg : 0) |
-                        (dseg > 0 ? kSlotOne : 0) | (qb << 4);
+                        (dseg > 0 ? kSlotOne : 0) | (qb << 4) | (kScores ? i << 6 : 0);
       const int nbox = (nvalid + TB - 1) / TB;  // per tensor, <= 8
       int blk = 0, brow = 0;
       if (j < nbox) {
@@ -455,6 +455,16 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         sg[g] = row < nvalid ? __uint_as_float(v[g]) * cs : -INFINITY;
         pass |= sg[g] > m[g] + 8.0f;
       }
+      if constexpr (kScores) {  // stage flags >> 6 of its segment
+        static_assert(G == 8, "two vectors of four");
+        if (row < nvalid) {
+          float4* at = reinterpret_cast<float4*>(
+              a.scores + (((int64_t)dsc.x * a.num_kv_heads + dsc.y) * a.scores_rows +
+                          (int64_t)(flags >> 6) * kMxRows + row) * G);
+          at[0] = make_float4(sg[0], sg[1], sg[2], sg[3]);
+          at[1] = make_float4(sg[4], sg[5], sg[6], sg[7]);
+        }
+      }
       const bool wpass = __any_sync(0xffffffffu, pass);
       if (lane == 0) reinterpret_cast<int*>(&redf[b])[q4] = wpass ? 1 : 0;
       if (!group_sync()) break;
@@ -590,9 +600,9 @@ bool decode_tc_mx_supported(int dtype, int head_dim, int group, int block_size) 
 template <int G>
 static cudaError_t launch_mx_t(const CUtensorMap& tmk, const CUtensorMap& tmv,
                                const CUtensorMap& tmq, const DecodeArgs& a, cudaStream_t stream) {
-  auto kern = decode_tc_mx_kernel<G>;
-  static SmemAttrCache attr_cache;
-  cudaError_t e = ensure_smem_limit(kern, kMxSmem, attr_cache);
+  auto kern = a.scores ? decode_tc_mx_kernel<G, true> : decode_tc_mx_kernel<G>;
+  static SmemAttrCache attr_cache[2];
+  cudaError_t e = ensure_smem_limit(kern, kMxSmem, attr_cache[a.scores ? 1 : 0]);
   if (e != cudaSuccess) return e;
   return launch_pdl(kern, dim3((unsigned)a.num_ctas), dim3(kMxThreads), kMxSmem, stream, tmk, tmv,
                     tmq, a);

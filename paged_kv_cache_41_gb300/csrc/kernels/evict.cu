@@ -10,64 +10,74 @@ namespace pkv {
 
 // ------------------------------------------------------------------ weighing
 // weights[r, c, t] = decay * weights[r, c, t] + sum over the G query heads h
-// of kv head c of exp(s_ht - lse_h), s_ht = scale q_h . k_t.  One warp per
-// cached row: its lanes hold D / 32 elements each, the G scores are summed
-// across the lanes.
-template <typename T, typename TQ, int D>
-__global__ void __launch_bounds__(256) weigh_kernel(const WeighArgs a) {
-  constexpr int EPL = D / 32;
+// of kv head c of 2^(s_ht - lse_h), from the base-2 scores s that the decode
+// left and the LSEs of its merge.  A thread per row, four rows in flight.
+// Bound by its bytes: 4 G + 8 a row, beside the 4 D of K and V that the decode
+// read for it (bf16), and partly still in L2.
+namespace {
+
+constexpr int kWeighThreads = 256;
+constexpr int kWeighRows = 4;  // rows of a thread
+
+}  // namespace
+
+template <int G>
+__global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const WeighArgs a) {
   pdl_wait();
-  const int r = blockIdx.z, c = blockIdx.y, P = a.block_size, Hkv = a.num_kv_heads;
-  const int G = a.num_q_heads / Hkv;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, P, a.err, false);
+  const int r = blockIdx.z, c = blockIdx.y, Hkv = a.num_kv_heads;
+  const int len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, a.block_size, a.err, false);
   if (len > a.weights_stride && blockIdx.x == 0 && c == 0 && threadIdx.x == 0)
     atomicOr(a.err, PKV_DEVERR_LENGTH);
   const int64_t n = len < a.weights_stride ? len : a.weights_stride;
-  for (int64_t t = (int64_t)blockIdx.x * 8 + warp; t < n; t += (int64_t)gridDim.x * 8) {
-    const int blk = __ldg(a.block_tables + (int64_t)r * a.max_blocks + t / P);
-    if (blk < 0 || (int64_t)blk >= a.num_blocks) continue;  // the decode reports it
-    float kf[EPL];
-    const T* kp = static_cast<const T*>(a.k) + (((int64_t)blk * P + t % P) * Hkv + c) * D + lane * EPL;
+  const int64_t t0 = (int64_t)blockIdx.x * (kWeighThreads * kWeighRows) + threadIdx.x;
+  if (t0 - threadIdx.x >= n) return;
+  const int64_t rc = (int64_t)r * Hkv + c;
+  float lse2[G];
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) kf[e] = (float)kp[e];
-    if constexpr (sizeof(T) == 1) {
-      const float sc = e8m0_value(__ldg(a.k_scales + (((int64_t)blk * Hkv + c) * P + t % P) * (D / 32) + lane * EPL / 32));
+  for (int g = 0; g < G; ++g) lse2[g] = __ldg(a.lse + rc * G + g) * 1.4426950408889634f;
+  const float* s = a.scores + rc * a.scores_rows * G;
+  float* w = a.weights + rc * a.weights_stride;
+  float x[kWeighRows][G], old[kWeighRows];
 #pragma unroll
-      for (int e = 0; e < EPL; ++e) kf[e] *= sc;
-    }
+  for (int i = 0; i < kWeighRows; ++i) {
+    const int64_t t = t0 + i * kWeighThreads;
+    if (t >= n) continue;
+    if constexpr (G == 1)
+      x[i][0] = s[t];
+    else
+      VecLoad<float, G>::run(s + t * G, x[i]);
+    old[i] = w[t];
+  }
+#pragma unroll
+  for (int i = 0; i < kWeighRows; ++i) {
+    const int64_t t = t0 + i * kWeighThreads;
+    if (t >= n) continue;
     float sum = 0.f;
+#pragma unroll
     for (int g = 0; g < G; ++g) {
-      const int64_t qh = (int64_t)r * a.num_q_heads + c * G + g;
-      const TQ* qp = static_cast<const TQ*>(a.q) + qh * D + lane * EPL;
-      float s = 0.f;
-#pragma unroll
-      for (int e = 0; e < EPL; ++e) s = fmaf((float)qp[e] * a.qscale, kf[e], s);
-#pragma unroll
-      for (int o = 16; o >= 1; o >>= 1) s += __shfl_xor_sync(0xffffffffu, s, o);
-      sum += exp2f(s - __ldg(a.lse + qh) * 1.4426950408889634f);
+      // a row that was not attended (a bad block) has score -inf and weight 0;
+      // a head without an LSE (NaN scores) has no weights
+      if (x[i][g] != -INFINITY) sum += lse2[g] == -INFINITY ? nanf("") : exp2f(x[i][g] - lse2[g]);
     }
-    if (lane == 0) {
-      float* w = a.weights + ((int64_t)r * Hkv + c) * a.weights_stride + t;
-      *w = fmaf(a.decay, *w, sum);
-    }
+    w[t] = fmaf(a.decay, old[i], sum);
   }
 }
 
-template <typename T, typename TQ>
-static cudaError_t launch_weigh_t(int head_dim, const WeighArgs& a, cudaStream_t stream) {
-  const int64_t rows = (int64_t)a.max_blocks * a.block_size;
-  const int64_t x = (rows + 63) / 64;  // eight rows per warp at least
-  const dim3 grid((unsigned)(x < 1024 ? x : 1024), (unsigned)a.num_kv_heads, (unsigned)a.num_seqs);
-  return head_dim == 128 ? launch_pdl(weigh_kernel<T, TQ, 128>, grid, dim3(256), 0, stream, a)
-                         : launch_pdl(weigh_kernel<T, TQ, 64>, grid, dim3(256), 0, stream, a);
+template <int G>
+static cudaError_t launch_weigh_t(const WeighArgs& a, cudaStream_t stream) {
+  const int64_t rows = (int64_t)a.max_blocks * a.block_size, per = kWeighThreads * kWeighRows;
+  return launch_pdl(weigh_kernel<G>,
+                    dim3((unsigned)((rows + per - 1) / per), (unsigned)a.num_kv_heads, (unsigned)a.num_seqs),
+                    dim3(kWeighThreads), 0, stream, a);
 }
 
-cudaError_t launch_weigh(int dtype, int head_dim, const WeighArgs& a, cudaStream_t stream) {
-  switch (dtype) {
-    case PKV_F32: return launch_weigh_t<float, float>(head_dim, a, stream);
-    case PKV_BF16: return launch_weigh_t<__nv_bfloat16, __nv_bfloat16>(head_dim, a, stream);
-    default: return launch_weigh_t<__nv_fp8_e4m3, __nv_bfloat16>(head_dim, a, stream);
+cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t stream) {
+  switch (a.num_q_heads / a.num_kv_heads) {
+    case 1: return launch_weigh_t<1>(a, stream);
+    case 2: return launch_weigh_t<2>(a, stream);
+    case 4: return launch_weigh_t<4>(a, stream);
+    case 8: return launch_weigh_t<8>(a, stream);
+    default: return cudaErrorInvalidValue;
   }
 }
 

@@ -120,12 +120,21 @@ struct DecodeArgs {
   // them, or, for the plain decode, as its interface documents.
   int32_t plan_before_wait;
   float qscale;          // softmax scale * log2(e)
+  // Weighing decode: every row's base-2 scores, [B, Hkv, scores_rows, G] (G
+  // query heads of the kv head), or null.
+  float* scores;
+  int64_t scores_rows;
 };
 
 // Partial kernel, then the LSE reduction of cut segments, on one stream.
 cudaError_t launch_paged_decode(int dtype, int head_dim, int group, const CUtensorMap& tmk,
                                 const CUtensorMap& tmv, const DecodeArgs& args,
                                 cudaStream_t stream);
+
+// The partial kernel alone, leaving scores (args.scores; decode_scores.cu).
+cudaError_t launch_decode_partial_scores(int dtype, int head_dim, int group, const CUtensorMap& tmk,
+                                         const CUtensorMap& tmv, const DecodeArgs& args,
+                                         cudaStream_t stream);
 
 // CTAs of one wave of the partial kernel (resident CTAs per SM x SMs).
 int decode_resident_ctas(int dtype, int head_dim, int group);
@@ -287,27 +296,23 @@ int draft_simt_rows(int rows);
 // The score update of a weighing decode (evict.cu): for every sequence r, kv
 // head c and row t < seq_lens[r],
 //   weights[r, c, t] = decay * weights[r, c, t] + sum_h exp(s_ht - lse_h)
-// over the G query heads h of c.
+// over the G query heads h of c, from the scores the decode left.
 struct WeighArgs {
-  const void* q;                // [B, Hq, D]
-  const void* k;                // the K pool
-  const uint8_t* k_scales;      // MXFP8 pools
-  const int32_t* block_tables;
+  const float* scores;          // [B, Hkv, scores_rows, G], base 2
   const int32_t* seq_lens;
   const float* lse;             // [B, Hq] natural log
   float* weights;               // [B, Hkv, weights_stride]
   unsigned int* err;
+  int64_t scores_rows;
   int64_t weights_stride;
-  int64_t num_blocks;
   int32_t max_blocks;
   int32_t num_seqs;
   int32_t num_q_heads;
   int32_t num_kv_heads;
   int32_t block_size;
-  float qscale;                 // softmax scale * log2(e)
   float decay;
 };
-cudaError_t launch_weigh(int dtype, int head_dim, const WeighArgs& args, cudaStream_t stream);
+cudaError_t launch_weigh(const WeighArgs& args, cudaStream_t stream);
 
 // The choice of an eviction (evict.cu); see pkv_kv_evict_select.
 struct SelectArgs {

@@ -519,12 +519,17 @@ size_t pkv_decode_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
   return decode_workspace(num_seqs, C, num_q_heads / cache->num_kv_heads, cache->head_dim).total;
 }
 
-pkv_status pkv_paged_attention_decode(const pkv_cache_desc* cache, void* out, float* lse,
-                                      const void* q, const void* k_cache, const void* v_cache,
-                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
-                                      const int32_t* seq_lens, int32_t num_seqs,
-                                      int32_t num_q_heads, float scale, int32_t partition_size,
-                                      void* workspace, size_t workspace_bytes, void* stream) {
+}  // extern "C"
+
+namespace {
+
+// The paged decode; with `scores` it also leaves every row's base-2 scores
+// (DecodeArgs::scores).
+pkv_status decode_checked(const pkv_cache_desc* cache, void* out, float* lse, const void* q,
+                          const void* k_cache, const void* v_cache, const int32_t* block_tables,
+                          int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs,
+                          int32_t num_q_heads, float scale, int32_t partition_size, void* workspace,
+                          size_t workspace_bytes, void* stream, float* scores, int64_t scores_rows) {
   pkv_status st = check_cache(cache);
   if (st != PKV_OK) return st;
   if (num_seqs < 0 || max_blocks_per_seq <= 0 || partition_size < 0 || !isfinite(scale))
@@ -566,7 +571,24 @@ pkv_status pkv_paged_attention_decode(const pkv_cache_desc* cache, void* out, fl
   // The length scan runs under the preceding kernel's tail where that kernel
   // lets its dependents start early (kv_append: it writes rows, never lengths)
   a.plan_before_wait = 1;
+  a.scores = scores;
+  a.scores_rows = scores_rows;
   return launch_decode(cache, G, q, k_cache, v_cache, a, as_stream(stream));
+}
+
+}  // namespace
+
+extern "C" {
+
+pkv_status pkv_paged_attention_decode(const pkv_cache_desc* cache, void* out, float* lse,
+                                      const void* q, const void* k_cache, const void* v_cache,
+                                      const int32_t* block_tables, int32_t max_blocks_per_seq,
+                                      const int32_t* seq_lens, int32_t num_seqs,
+                                      int32_t num_q_heads, float scale, int32_t partition_size,
+                                      void* workspace, size_t workspace_bytes, void* stream) {
+  return decode_checked(cache, out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                        seq_lens, num_seqs, num_q_heads, scale, partition_size, workspace,
+                        workspace_bytes, stream, nullptr, 0);
 }
 
 // Shared-prefix workspace: prefix states plus the suffix's whole-segment
@@ -922,11 +944,33 @@ pkv_status pkv_draft_tree_attention(
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
+}  // extern "C"
+
+namespace {
+
+// Weighing-decode workspace: the decode's, then the LSEs [B, Hq] (for a caller
+// that wants none) and the scores [B, Hkv, rows, G], rows the table's.
+struct WeightsWorkspace {
+  size_t lse_off, score_off, total;
+};
+
+WeightsWorkspace weights_workspace(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
+                                   int32_t max_blocks) {
+  WeightsWorkspace w{};
+  w.lse_off = pkv_decode_workspace_bytes(c, num_seqs, num_q_heads, max_blocks, 0);
+  if (!w.lse_off) return w;
+  w.score_off = w.lse_off + align256((size_t)num_seqs * num_q_heads * 4);
+  w.total = w.score_off + align256((size_t)num_seqs * num_q_heads * max_blocks * c->block_size * 4);
+  return w;
+}
+
+}  // namespace
+
+extern "C" {
+
 size_t pkv_decode_weights_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
                                           int32_t num_q_heads, int32_t max_blocks_per_seq) {
-  const size_t dec =
-      pkv_decode_workspace_bytes(cache, num_seqs, num_q_heads, max_blocks_per_seq, 0);
-  return dec ? dec + align256((size_t)num_seqs * num_q_heads * 4) : 0;
+  return weights_workspace(cache, num_seqs, num_q_heads, max_blocks_per_seq).total;
 }
 
 pkv_status pkv_paged_attention_decode_weights(
@@ -943,38 +987,35 @@ pkv_status pkv_paged_attention_decode_weights(
   if ((st = check_attention_shape(cache, num_q_heads)) != PKV_OK) return st;
   if (num_seqs == 0) return PKV_OK;
   if (!weights || !workspace) return PKV_ERR_INVALID_ARG;
-  const size_t need =
-      pkv_decode_weights_workspace_bytes(cache, num_seqs, num_q_heads, max_blocks_per_seq);
-  const size_t lse_bytes = align256((size_t)num_seqs * num_q_heads * 4);
-  if (!need || workspace_bytes < need) return PKV_ERR_INVALID_ARG;
+  const WeightsWorkspace w =
+      weights_workspace(cache, num_seqs, num_q_heads, max_blocks_per_seq);
+  if (!w.total || workspace_bytes < w.total) return PKV_ERR_INVALID_ARG;
+  const int64_t rows = (int64_t)max_blocks_per_seq * cache->block_size;
+  if (rows > (int64_t)INT32_MAX * 1024) return PKV_ERR_UNSUPPORTED;
   unsigned char* base = static_cast<unsigned char*>(workspace);
-  float* lse_use = lse ? lse : reinterpret_cast<float*>(base + need - lse_bytes);
-  if ((st = pkv_paged_attention_decode(cache, out, lse_use, q, k_cache, v_cache, block_tables,
-                                       max_blocks_per_seq, seq_lens, num_seqs, num_q_heads, scale,
-                                       0, workspace, need - lse_bytes, stream)) != PKV_OK)
+  float* lse_use = lse ? lse : reinterpret_cast<float*>(base + w.lse_off);
+  float* scores = reinterpret_cast<float*>(base + w.score_off);
+  if ((st = decode_checked(cache, out, lse_use, q, k_cache, v_cache, block_tables,
+                           max_blocks_per_seq, seq_lens, num_seqs, num_q_heads, scale, 0, workspace,
+                           w.lse_off, stream, scores, rows)) != PKV_OK)
     return st;
   unsigned int* err = device_error_word();
   if (!err) return PKV_ERR_CUDA;
   pkv::WeighArgs a{};
-  a.q = q;
-  a.k = k_cache;
-  if (cache->dtype == PKV_MXFP8)
-    a.k_scales = static_cast<const uint8_t*>(k_cache) + mx_plane_bytes(cache);
-  a.block_tables = block_tables;
+  a.scores = scores;
   a.seq_lens = seq_lens;
   a.lse = lse_use;
   a.weights = weights;
   a.err = err;
+  a.scores_rows = rows;
   a.weights_stride = weights_stride;
-  a.num_blocks = cache->num_blocks;
   a.max_blocks = max_blocks_per_seq;
   a.num_seqs = num_seqs;
   a.num_q_heads = num_q_heads;
   a.num_kv_heads = cache->num_kv_heads;
   a.block_size = cache->block_size;
-  a.qscale = scale * 1.4426950408889634f;
   a.decay = decay;
-  cudaError_t e = pkv::launch_weigh(cache->dtype, cache->head_dim, a, as_stream(stream));
+  cudaError_t e = pkv::launch_weigh(a, as_stream(stream));
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 

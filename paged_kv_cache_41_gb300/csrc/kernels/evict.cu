@@ -1,6 +1,7 @@
 // evict.cu -- keeping a paged cache inside a budget: the running attention
 // weight of every cached row, the choice of the rows to keep by it, and the
 // move of the kept rows together.
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include "common.cuh"
@@ -87,8 +88,13 @@ cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t stream) {
 // recent heaviest of those between, ties to the lowest index.
 //
 // The k-th largest weight is found by radix selection on an order-preserving
-// integer key, eight bits a pass; the last pass writes the kept indices in
-// ascending order, from the running counts of rows above the key and at it.
+// integer key; then the kept indices are written in ascending order, from
+// running counts.  The data is small (4 bytes a row), so latency bounds it: one
+// CTA takes a row of weights (a cluster of up to eight where it does not fit)
+// and reads it once, into shared memory.  A histogram of the keys' upper 11
+// bits leaves the rows of one bin (3% of a lognormal row); where they are few
+// they are ranked against each other, else histograms of the next 11 and the
+// last 10 bits follow.
 namespace {
 
 constexpr int kSelThreads = 1024;
@@ -104,6 +110,261 @@ __device__ __forceinline__ uint32_t weight_key(uint32_t u) {
 
 }  // namespace
 
+namespace {
+
+namespace cg = cooperative_groups;
+
+constexpr int kScBins = 2048;
+constexpr int kScList = 256;         // rows ranked against each other at most
+constexpr int kScSlice = 48 * 1024;  // keys of a CTA at most (192 KiB)
+constexpr uint32_t kScForced = 0xffffffffu;  // the key of a row kept for certain: no weight has it
+
+}  // namespace
+
+// Warp w of the cluster's CTA `rank` holds a contiguous run of its slice, 128
+// consecutive rows at a time, four a lane.
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) evict_select_cluster_kernel(const SelectArgs a) {
+  constexpr int kWarps = kThreads / 32;
+  extern __shared__ __align__(16) uint32_t keys[];  // this CTA's slice, padded with key 0
+  __shared__ __align__(16) uint32_t hist[kScBins];  // of its keys, largest digit first
+  __shared__ __align__(8) uint2 list[kScList];      // in CTA 0: (key, row) of the threshold's bin
+  __shared__ uint32_t listed;
+  __shared__ uint32_t warp_sum[kWarps], warp_above[kWarps], warp_at[kWarps];
+  __shared__ uint32_t found[3];    // digit, rows wanted of its bin, rows in it
+  __shared__ uint2 last;           // in CTA 0: the last kept candidate
+  __shared__ uint32_t counts[2];   // this CTA's rows above the threshold, and at it
+  cg::cluster_group cluster = cg::this_cluster();
+  const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int c = blockIdx.x / cs, r = blockIdx.y;
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  int T = __ldg(a.seq_lens + r);
+  if (T < 0 || T > a.weights_stride) {
+    if (c == 0 && rank == 0 && tid == 0) atomicOr(a.err, PKV_DEVERR_LENGTH);
+    T = T < 0 ? 0 : (int)a.weights_stride;
+  }
+  int32_t* keep = a.keep + ((int64_t)r * a.num_kv_heads + c) * a.budget;
+  const int kept = min(T, a.budget);
+  if (c == 0 && rank == 0 && tid == 0) a.new_lens[r] = kept;
+  const int me = rank * kThreads + tid, all = cs * kThreads;
+  for (int j = kept + me; j < a.budget; j += all) keep[j] = -1;
+  if (T <= a.budget) {  // the same for the whole cluster
+    for (int j = me; j < T; j += all) keep[j] = j;
+    return;
+  }
+  // every CTA of the cluster meets; one alone only needs its own threads
+  auto meet = [&]() {
+    if (cs > 1) cluster.sync();
+    else __syncthreads();
+  };
+  const int slice = ((T + cs - 1) / cs + 3) & ~3;          // <= kScSlice
+  const int n = (slice + 4 * kThreads - 1) / (4 * kThreads);  // fours of a thread
+  const int first = rank * slice, len = min(T - first, slice);  // this CTA's rows (len may be <= 0)
+  const int at0 = warp * 128 * n + lane * 4;               // this thread's: at0 + 128 i ..+3 of them
+  const int lo = a.num_sinks, hi = T - a.num_recent;       // candidates: [lo, hi)
+  const uint32_t* w = reinterpret_cast<const uint32_t*>(a.weights) +
+                      ((int64_t)r * a.num_kv_heads + c) * a.weights_stride + first;
+  const bool wide = (reinterpret_cast<uintptr_t>(w) & 15u) == 0;
+  auto clear = [&]() {
+    for (int i = tid; i < kScBins / 4; i += kThreads) reinterpret_cast<uint4*>(hist)[i] = make_uint4(0u, 0u, 0u, 0u);
+  };
+  clear();
+  if (tid == 0) listed = 0;
+  __syncthreads();
+  uint32_t need = (uint32_t)(a.budget - a.num_sinks - a.num_recent);  // < hi - lo
+  uint32_t prefix = kScForced - 1;  // the key's digits found so far; need 0: only forced rows are above
+  uint32_t last_row = 0xffffffffu;  // of the rows at the key, keep those up to here ...
+  bool ranked = false;              // ... where the candidates were ranked; else the first `need`
+  // A thread reads only the keys it wrote.
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const int at = at0 + 128 * i;
+    if (at >= len) break;
+    uint4 x;
+    if (wide && at + 3 < len) {
+      x = __ldg(reinterpret_cast<const uint4*>(w + at));
+    } else {
+      x.x = __ldg(w + at);
+      x.y = at + 1 < len ? __ldg(w + at + 1) : 0u;
+      x.z = at + 2 < len ? __ldg(w + at + 2) : 0u;
+      x.w = at + 3 < len ? __ldg(w + at + 3) : 0u;
+    }
+    uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const int t = first + at + q;
+      v[q] = at + q >= len ? 0u : t < lo || t >= hi ? kScForced : weight_key(v[q]);
+      if (at + q < len && v[q] != kScForced) atomicAdd(&hist[kScBins - 1 - (v[q] >> 21)], 1u);
+    }
+    *reinterpret_cast<uint4*>(keys + at) = make_uint4(v[0], v[1], v[2], v[3]);
+  }
+  // f(key, index in the slice) for this thread's keys whose upper bits are
+  // `prefix`; a padding key passes as well, its index being >= len
+  auto matching = [&](int shift, auto f) {
+#pragma unroll 4
+    for (int i = 0; i < n; ++i) {
+      const int at = at0 + 128 * i;
+      if (at >= len) break;
+      const uint4 x = *reinterpret_cast<const uint4*>(keys + at);
+      const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if ((v[q] >> shift) == prefix && at + q < len) f(v[q], at + q);
+    }
+  };
+  int bits_left = 21;
+  for (int pass = 0; need > 0 && pass < 3; ++pass) {
+    const int bits = pass == 2 ? 10 : 11;
+    if (pass > 0) {
+      bits_left -= bits;
+      meet();  // the others have read this CTA's histogram
+      clear();
+      __syncthreads();
+      matching(bits_left + bits, [&](uint32_t key, int) {
+        atomicAdd(&hist[kScBins - 1 - ((key >> bits_left) & ((1u << bits) - 1u))], 1u);
+      });
+    }
+    meet();
+    // the bin that holds the need-th largest digit, over the whole cluster:
+    // thread t adds up bins kPer t ..
+    constexpr int kPer = kScBins / kThreads;
+    uint32_t v[kPer];
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) v[q] = 0;
+    for (int q = 0; q < cs; ++q) {
+      const uint32_t* h = (cs > 1 ? cluster.map_shared_rank(hist, q) : hist) + tid * kPer;
+#pragma unroll
+      for (int p = 0; p < kPer / 2; ++p) {
+        const uint2 x = reinterpret_cast<const uint2*>(h)[p];
+        v[2 * p] += x.x;
+        v[2 * p + 1] += x.y;
+      }
+    }
+    uint32_t mine = 0;
+#pragma unroll
+    for (int q = 0; q < kPer; ++q) mine += v[q];
+    uint32_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    if (lane == 31) warp_sum[warp] = inc;
+    __syncthreads();
+    uint32_t before = inc - mine + __reduce_add_sync(0xffffffffu, lane < warp ? warp_sum[lane] : 0u);
+    if (before < need && need <= before + mine) {
+#pragma unroll
+      for (int q = 0; q < kPer; ++q) {
+        if (before < need && need <= before + v[q]) {
+          found[0] = (uint32_t)(kScBins - 1 - (kPer * tid + q));
+          found[1] = need - before;
+          found[2] = v[q];
+        }
+        before += v[q];
+      }
+    }
+    __syncthreads();
+    prefix = pass == 0 ? found[0] : (prefix << bits) | found[0];
+    need = found[1];
+    const uint32_t in_bin = found[2];
+    if (in_bin <= (uint32_t)kScList) {
+      // rank the bin's rows by (key, lowest row first), in CTA 0
+      ranked = true;
+      uint2* to = cs > 1 ? cluster.map_shared_rank(list, 0) : list;
+      uint32_t* nl = cs > 1 ? cluster.map_shared_rank(&listed, 0) : &listed;
+      matching(bits_left, [&](uint32_t key, int at) { to[atomicAdd(nl, 1u)] = make_uint2(key, first + at); });
+      meet();
+      if (rank == 0 && tid < in_bin) {
+        const uint2 x = list[tid];
+        uint32_t above = 0;
+#pragma unroll 8
+        for (uint32_t q = 0; q < in_bin; ++q) {
+          const uint2 y = list[q];
+          above += y.x > x.x || (y.x == x.x && y.y < x.y) ? 1u : 0u;
+        }
+        if (above == need - 1) last = x;
+      }
+      meet();
+      const uint2 x = cs > 1 ? *cluster.map_shared_rank(&last, 0) : last;
+      prefix = x.x;
+      last_row = x.y;
+      break;
+    }
+  }
+  // ---- keep every key above `prefix`, and of those at it the rows up to
+  // last_row or the first `need`: counts by warp, by CTA, by row
+  // above and at of four rows: bits 0-3 and 4-7
+  auto kinds = [&](int at) -> uint32_t {
+    uint32_t m = 0;
+    if (at < len) {
+      const uint4 x = *reinterpret_cast<const uint4*>(keys + at);
+      const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const bool eq = v[q] == prefix && at + q < len;
+        const bool in = eq && ranked && (uint32_t)(first + at + q) <= last_row;
+        if (v[q] > prefix || in) m |= 1u << q;
+        if (eq && !ranked) m |= 16u << q;
+      }
+    }
+    return m;
+  };
+  uint32_t n_above = 0, n_at = 0;
+#pragma unroll 4
+  for (int i = 0; i < n; ++i) {
+    const uint32_t m = kinds(at0 + 128 * i);
+    n_above += __popc(m & 15u);
+    n_at += __popc(m >> 4);
+  }
+  n_above = __reduce_add_sync(0xffffffffu, n_above);
+  n_at = __reduce_add_sync(0xffffffffu, n_at);
+  if (lane == 0) {
+    warp_above[warp] = n_above;
+    warp_at[warp] = n_at;
+  }
+  __syncthreads();
+  uint32_t my_above = __reduce_add_sync(0xffffffffu, lane < warp ? warp_above[lane] : 0u);
+  uint32_t my_at = __reduce_add_sync(0xffffffffu, lane < warp ? warp_at[lane] : 0u);
+  if (cs > 1) {
+    if (tid == kThreads - 1) {
+      counts[0] = my_above + n_above;
+      counts[1] = my_at + n_at;
+    }
+    cluster.sync();
+    for (int q = 0; q < rank; ++q) {
+      const uint32_t* x = cluster.map_shared_rank(counts, q);
+      my_above += x[0];
+      my_at += x[1];
+    }
+  }
+#pragma unroll 2
+  for (int i = 0; i < n; ++i) {
+    const int at = at0 + 128 * i;
+    const uint32_t m = kinds(at);
+    const uint32_t mine = __popc(m & 15u) | (__popc(m >> 4) << 16);
+    uint32_t inc = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += y;
+    }
+    const uint32_t total = __shfl_sync(0xffffffffu, inc, 31);
+    uint32_t pa = my_above + ((inc - mine) & 0xffffu), pq = my_at + ((inc - mine) >> 16);
+#pragma unroll
+    for (int q = 0; q < 4; ++q) {
+      const bool ab = (m >> q) & 1u, eq = (m >> (4 + q)) & 1u;
+      if (ab || (eq && pq < need)) keep[pa + min(pq, need)] = first + at + q;
+      pa += ab ? 1u : 0u;
+      pq += eq ? 1u : 0u;
+    }
+    my_above += total & 0xffffu;
+    my_at += total >> 16;
+  }
+  if (cs > 1) cluster.sync();  // the others may still read this CTA's shared memory
+}
+
+// Any length: one CTA a row of weights, which it reads again in each of four
+// passes over eight bits.
 __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectArgs a) {
   __shared__ uint32_t hist[256];
   __shared__ uint32_t warp_sum[32];
@@ -205,7 +466,37 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
   }
 }
 
+template <int kThreads>
+static cudaError_t launch_select_cluster(const SelectArgs& a, int cs, cudaStream_t stream) {
+  const int smem = (int)(((a.weights_stride + cs - 1) / cs + 3) & ~(int64_t)3) * 4;
+  auto kern = evict_select_cluster_kernel<kThreads>;
+  static SmemAttrCache attr_cache;
+  cudaError_t e = ensure_smem_limit(kern, smem, attr_cache);
+  if (e != cudaSuccess) return e;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.num_kv_heads * cs), (unsigned)a.num_seqs);
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = (size_t)smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)cs;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, kern, a);
+}
+
 cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
+  // No length passes weights_stride: the smallest cluster whose CTAs hold it.
+  const int64_t most = a.weights_stride;
+  if (most <= 8 * kScSlice) {
+    int cs = 1;
+    while (most > (int64_t)cs * kScSlice) cs *= 2;
+    return most <= 8192 ? launch_select_cluster<256>(a, cs, stream)
+                        : launch_select_cluster<1024>(a, cs, stream);
+  }
   evict_select_kernel<<<dim3((unsigned)a.num_kv_heads, (unsigned)a.num_seqs), kSelThreads, 0, stream>>>(a);
   return cudaGetLastError();
 }

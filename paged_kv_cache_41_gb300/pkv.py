@@ -171,6 +171,9 @@ class MxPool:
     def device(self):
         return self.buf.device
 
+    def get_device(self) -> int:
+        return self.buf.get_device()
+
     def data_ptr(self) -> int:
         return self.buf.data_ptr()
 
@@ -415,28 +418,33 @@ def chunk_tree_attention(q, k_cache, v_cache, plan: ChunkTreePlan, scale, *, out
 
 def _dense(name, t, dtype, shape):
     """Check a tensor argument; ``shape`` entries of None match any size."""
-    if t.dtype != dtype or t.dim() != len(shape) or not t.is_contiguous() or any(
-            w is not None and w != n for w, n in zip(shape, t.shape)):
+    if t.dtype != dtype or not t.is_contiguous() or (t.shape != shape and (
+            t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)))):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, "
                          f"got {t.dtype} {tuple(t.shape)}")
 
 
 def _pair_desc(k_cache, v_cache) -> CacheDesc:
     """cache_desc of a K and a V pool of one shape and type."""
-    desc, v = cache_desc(k_cache), cache_desc(v_cache)
-    if any(getattr(desc, f) != getattr(v, f) for f, _ in CacheDesc._fields_):
-        raise ValueError("K and V caches must be of one shape and dtype")
-    return desc
+    if type(k_cache) is not type(v_cache) or k_cache.shape != v_cache.shape or (
+            not isinstance(v_cache, MxPool)
+            and (v_cache.dtype != k_cache.dtype or not v_cache.is_contiguous())):
+        raise ValueError("K and V caches must be of one shape and dtype, and contiguous")
+    return cache_desc(k_cache)
 
 
-def _on_current_device(*tensors):
-    """Every tensor must be on the current CUDA device: the kernels are launched there."""
-    dev = tensors[0].device
-    if dev.type != "cuda" or dev.index != torch.cuda.current_device():
-        raise ValueError(f"tensors must be on the current CUDA device, got {dev}")
+def _launch_place(stream, *tensors):
+    """The stream to launch on (an address).  Every tensor must be on the
+    current CUDA device: the kernels are launched there."""
+    dev = tensors[0].get_device()
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"tensors must be on the current CUDA device, got {tensors[0].device}")
     for t in tensors:
-        if t is not None and t.device != dev:
-            raise ValueError(f"tensors must be on one device, got {t.device} and {dev}")
+        if t is not None and t.get_device() != dev:
+            raise ValueError(f"tensors must be on the current CUDA device, got one on {t.device}")
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _io_dtype(desc):
@@ -488,8 +496,8 @@ def draft_tree_attention(q, k_cache, v_cache, block_tables, ctx_lens, draft_ptr,
         _dense("out", out, q.dtype, (rows, hq, d))
     if lse is not None:
         _dense("lse", lse, torch.float32, (rows, hq))
-    _on_current_device(q, k_cache, v_cache, block_tables, ctx_lens, draft_ptr, masks, out, lse,
-                       workspace)
+    where = _launch_place(stream, q, k_cache, v_cache, block_tables, ctx_lens, draft_ptr, masks,
+                          out, lse, workspace)
     lib = load_library()
     if workspace is None and b:
         need = lib.pkv_draft_tree_workspace_bytes(ctypes.byref(desc), b, hq, max_draft, max_blocks)
@@ -500,7 +508,7 @@ def draft_tree_attention(q, k_cache, v_cache, block_tables, ctx_lens, draft_ptr,
         q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), max_blocks,
         ctx_lens.data_ptr(), draft_ptr.data_ptr(), masks.data_ptr() if masks is not None else None,
         b, rows, max_draft, hq, scale, workspace.data_ptr() if workspace is not None else None,
-        ws_bytes, _stream(stream)), "pkv_draft_tree_attention")
+        ws_bytes, where), "pkv_draft_tree_attention")
     return out
 
 
@@ -529,7 +537,8 @@ def paged_attention_decode_weights(q, k_cache, v_cache, block_tables, seq_lens, 
         _dense("out", out, q.dtype, (b, hq, d))
     if lse is not None:
         _dense("lse", lse, torch.float32, (b, hq))
-    _on_current_device(q, k_cache, v_cache, block_tables, seq_lens, weights, out, lse, workspace)
+    where = _launch_place(stream, q, k_cache, v_cache, block_tables, seq_lens, weights, out, lse,
+                          workspace)
     lib = load_library()
     if workspace is None and b:
         need = lib.pkv_decode_weights_workspace_bytes(ctypes.byref(desc), b, hq, max_blocks)
@@ -539,7 +548,7 @@ def paged_attention_decode_weights(q, k_cache, v_cache, block_tables, seq_lens, 
         ctypes.byref(desc), out.data_ptr(), lse.data_ptr() if lse is not None else None,
         weights.data_ptr(), stride, decay, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         block_tables.data_ptr(), max_blocks, seq_lens.data_ptr(), b, hq, scale,
-        workspace.data_ptr() if workspace is not None else None, ws_bytes, _stream(stream)),
+        workspace.data_ptr() if workspace is not None else None, ws_bytes, where),
         "pkv_paged_attention_decode_weights")
     return out
 
@@ -561,10 +570,10 @@ def kv_evict_select(weights, seq_lens, budget, *, num_sinks=0, num_recent=0, kee
         new_lens = torch.empty_like(seq_lens)
     else:
         _dense("new_lens", new_lens, torch.int32, (b,))
-    _on_current_device(weights, seq_lens, keep, new_lens)
+    where = _launch_place(stream, weights, seq_lens, keep, new_lens)
     _check(load_library().pkv_kv_evict_select(
         weights.data_ptr(), stride, seq_lens.data_ptr(), b, hkv, budget, num_sinks, num_recent,
-        keep.data_ptr(), new_lens.data_ptr(), _stream(stream)), "pkv_kv_evict_select")
+        keep.data_ptr(), new_lens.data_ptr(), where), "pkv_kv_evict_select")
     return keep, new_lens
 
 
@@ -583,13 +592,13 @@ def kv_compact(k_cache, v_cache, block_tables, seq_lens, keep, keep_lens, *, bas
     if base_lens is not None:
         _dense("base_lens", base_lens, torch.int32, (b,))
     stride = _score_rows("weights", weights, b, desc.num_kv_heads) if weights is not None else 0
-    _on_current_device(k_cache, v_cache, block_tables, seq_lens, keep, keep_lens, base_lens,
-                       weights)
+    where = _launch_place(stream, k_cache, v_cache, block_tables, seq_lens, keep, keep_lens,
+                          base_lens, weights)
     _check(load_library().pkv_kv_compact(
         ctypes.byref(desc), k_cache.data_ptr(), v_cache.data_ptr(),
         weights.data_ptr() if weights is not None else None, stride, block_tables.data_ptr(),
         max_blocks, seq_lens.data_ptr(), base_lens.data_ptr() if base_lens is not None else None,
-        keep.data_ptr(), keep.shape[1], keep.shape[2], keep_lens.data_ptr(), b, _stream(stream)),
+        keep.data_ptr(), keep.shape[1], keep.shape[2], keep_lens.data_ptr(), b, where),
         "pkv_kv_compact")
 
 

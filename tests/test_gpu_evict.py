@@ -214,7 +214,8 @@ def run_select(w, lens, budget, sinks=0, recent=0, err=0, **kw):
 @pytest.mark.parametrize("n,budget,sinks,recent", [
     (1, 1, 0, 0), (5, 3, 1, 1), (64, 63, 4, 8), (1023, 100, 0, 10), (1024, 1000, 16, 0),
     (1025, 1, 0, 0), (1025, 512, 256, 256), (5000, 2048, 4, 128), (40001, 16384, 16, 1000),
-    (70000, 65536, 0, 1)])
+    (70000, 65536, 0, 1), (131072, 5000, 3, 7), (131073, 70000, 2, 9), (8192, 1000, 4, 4),
+    (8193, 8000, 0, 0), (16385, 300, 5, 5), (32769, 32768, 1, 1), (65537, 40000, 0, 100)])
 def test_select_sizes(n, budget, sinks, recent):
     rng = np.random.default_rng(n)
     w = np.exp(2 * rng.standard_normal((3, 2, n))).astype(np.float32)

@@ -124,15 +124,17 @@ constexpr uint32_t kScForced = 0xffffffffu;  // the key of a row kept for certai
 // Warp w of the cluster's CTA `rank` holds a contiguous run of its slice, 128
 // consecutive rows at a time, four a lane.
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads) evict_select_cluster_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, 2048 / kThreads) evict_select_cluster_kernel(const SelectArgs a) {
   constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint32_t keys[];  // this CTA's slice, padded with key 0
   __shared__ __align__(16) uint32_t hist[kScBins];  // of its keys, largest digit first
-  __shared__ __align__(8) uint2 list[kScList];      // in CTA 0: (key, row) of the threshold's bin
+  // in CTA 0: key << 32 | ~row of the rows in the threshold's bin, so that a
+  // larger word comes first
+  __shared__ unsigned long long list[kScList];
   __shared__ uint32_t listed;
   __shared__ uint32_t warp_sum[kWarps], warp_above[kWarps], warp_at[kWarps];
   __shared__ uint32_t found[3];    // digit, rows wanted of its bin, rows in it
-  __shared__ uint2 last;           // in CTA 0: the last kept candidate
+  __shared__ unsigned long long last;  // in CTA 0: the last kept candidate's word
   __shared__ uint32_t counts[2];   // this CTA's rows above the threshold, and at it
   cg::cluster_group cluster = cg::this_cluster();
   const int cs = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
@@ -176,7 +178,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_cluster_kernel(const Se
   uint32_t last_row = 0xffffffffu;  // of the rows at the key, keep those up to here ...
   bool ranked = false;              // ... where the candidates were ranked; else the first `need`
   // A thread reads only the keys it wrote.
-#pragma unroll 4
+#pragma unroll 2
   for (int i = 0; i < n; ++i) {
     const int at = at0 + 128 * i;
     if (at >= len) break;
@@ -201,7 +203,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_cluster_kernel(const Se
   // f(key, index in the slice) for this thread's keys whose upper bits are
   // `prefix`; a padding key passes as well, its index being >= len
   auto matching = [&](int shift, auto f) {
-#pragma unroll 4
+#pragma unroll 1
     for (int i = 0; i < n; ++i) {
       const int at = at0 + 128 * i;
       if (at >= len) break;
@@ -270,24 +272,47 @@ __global__ void __launch_bounds__(kThreads) evict_select_cluster_kernel(const Se
     if (in_bin <= (uint32_t)kScList) {
       // rank the bin's rows by (key, lowest row first), in CTA 0
       ranked = true;
-      uint2* to = cs > 1 ? cluster.map_shared_rank(list, 0) : list;
+      unsigned long long* to = cs > 1 ? cluster.map_shared_rank(list, 0) : list;
       uint32_t* nl = cs > 1 ? cluster.map_shared_rank(&listed, 0) : &listed;
-      matching(bits_left, [&](uint32_t key, int at) { to[atomicAdd(nl, 1u)] = make_uint2(key, first + at); });
+#pragma unroll 1
+      for (int i = 0; i < n; ++i) {  // a warp claims its places of 128 rows at once
+        const int at = at0 + 128 * i;
+        uint32_t m = 0, v[4] = {0, 0, 0, 0};
+        if (at < len) {
+          const uint4 x = *reinterpret_cast<const uint4*>(keys + at);
+          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if ((v[q] >> bits_left) == prefix && at + q < len) m |= 1u << q;
+        }
+        if (!__any_sync(0xffffffffu, m != 0)) continue;
+        const uint32_t mine = __popc(m);
+        uint32_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+          const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
+          if (lane >= o) inc += y;
+        }
+        uint32_t place = 0;
+        if (lane == 31) place = atomicAdd(nl, inc);
+        place = __shfl_sync(0xffffffffu, place, 31) + inc - mine;
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if ((m >> q) & 1u)
+            to[place++] = ((unsigned long long)v[q] << 32) | (uint32_t)~(first + at + q);
+      }
       meet();
       if (rank == 0 && tid < in_bin) {
-        const uint2 x = list[tid];
+        const unsigned long long x = list[tid];
         uint32_t above = 0;
-#pragma unroll 8
-        for (uint32_t q = 0; q < in_bin; ++q) {
-          const uint2 y = list[q];
-          above += y.x > x.x || (y.x == x.x && y.y < x.y) ? 1u : 0u;
-        }
+#pragma unroll 4
+        for (uint32_t q = 0; q < in_bin; ++q) above += list[q] > x ? 1u : 0u;
         if (above == need - 1) last = x;
       }
       meet();
-      const uint2 x = cs > 1 ? *cluster.map_shared_rank(&last, 0) : last;
-      prefix = x.x;
-      last_row = x.y;
+      const unsigned long long x = cs > 1 ? *cluster.map_shared_rank(&last, 0) : last;
+      prefix = (uint32_t)(x >> 32);
+      last_row = ~(uint32_t)x;
       break;
     }
   }
@@ -310,7 +335,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_cluster_kernel(const Se
     return m;
   };
   uint32_t n_above = 0, n_at = 0;
-#pragma unroll 4
+#pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const uint32_t m = kinds(at0 + 128 * i);
     n_above += __popc(m & 15u);
@@ -337,7 +362,7 @@ __global__ void __launch_bounds__(kThreads) evict_select_cluster_kernel(const Se
       my_at += x[1];
     }
   }
-#pragma unroll 2
+#pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const int at = at0 + 128 * i;
     const uint32_t m = kinds(at);

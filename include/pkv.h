@@ -527,8 +527,9 @@ pkv_status pkv_kv_evict_select(const float* weights, int64_t weights_stride,
  * such rows are not moved.  A sequence with keep_lens[r] outside [0,
  * seq_lens[r] - base], base outside [0, seq_lens[r]], or (with weights) more
  * rows than weights_stride sets PKV_DEVERR_LENGTH and is skipped.
- * Bit-exact.  Any block_size; head_dim x element a multiple of 16 bytes (MXFP8:
- * head_dim a multiple of 32).  num_seqs and num_kv_heads <= 65535. */
+ * Bit-exact.  Any block_size; head_dim x element a multiple of 16 bytes, 16 KiB
+ * at most (MXFP8: head_dim a multiple of 32); fewer than 2^32 - 1 pool rows.
+ * num_seqs and num_kv_heads <= 65535. */
 pkv_status pkv_kv_compact(const pkv_cache_desc* cache, void* k_cache, void* v_cache,
                           float* weights, int64_t weights_stride, const int32_t* block_tables,
                           int32_t max_blocks_per_seq, const int32_t* seq_lens,

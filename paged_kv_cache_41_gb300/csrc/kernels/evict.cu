@@ -528,15 +528,26 @@ cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
 
 // ------------------------------------------------------------------ compaction
 // Row base + keep[j] moves to row base + j, keep ascending (so keep[j] >= j),
-// in place.  One CTA walks the rows of one (sequence, kv head) of K, of V or
-// of the weights in order, a tile of them at a time: all loads of a tile are
-// done before its stores.  A tile's stores reach only rows below the next
-// tile's first destination, and a later tile's sources are at or above its
-// destinations, so no load ever meets a store of another row.
+// in place.  One CTA walks the rows of one chain -- one (sequence, kv head) of
+// K or of V, or some columns of it -- in order, a tile of them at a time.  The
+// order that has to hold: a tile's loads, and those of the tiles before it,
+// are done before its stores, since its destinations may be their sources.
+// Later tiles' loads may run ahead freely: their sources are at or above their
+// own destinations, which this tile's stores do not reach.
+//
+// So each CTA keeps a ring of 8 KiB tiles in shared memory filled by
+// cp.async (a plain load would have to arrive before the barrier that orders
+// the stores), several tiles ahead, and works out the rows' places further
+// ahead still.  Bound by the bytes: every moved row read once and written
+// once.  Where the chains are few, a row's columns are dealt to several CTAs
+// and the ring is deeper.
 namespace {
 
 constexpr int kCmThreads = 256;
-constexpr int kCmVecs = 4;  // 16-byte vectors per thread and tile
+constexpr int kCmVecs = 2;                            // 16-byte vectors per thread and tile
+constexpr int kCmTileVecs = kCmThreads * kCmVecs;     // 8 KiB
+constexpr uint32_t kCmSkip = 0xffffffffu;             // no row to move here
+constexpr int kCmSmall = 8;                           // weights or scales per thread and turn
 
 struct CompactSeq {
   int base, n, len;  // first row, kept rows, rows in all (0: skip)
@@ -567,94 +578,193 @@ __device__ __forceinline__ int kept_row(const CompactArgs& a, const CompactSeq& 
   return -1;
 }
 
-// Pool row of position t of sequence r, or -1 for a bad block id (reported).
-__device__ __forceinline__ int64_t pool_row(const CompactArgs& a, int r, int t) {
-  const int blk = __ldg(a.block_tables + (int64_t)r * a.max_blocks + t / a.block_size);
-  if (blk < 0 || (int64_t)blk >= a.num_blocks) {
-    atomicOr(a.err, PKV_DEVERR_BLOCK);
-    return -1;
-  }
-  return (int64_t)blk * a.block_size + t % a.block_size;
+__device__ __forceinline__ int table_entry(const CompactArgs& a, int r, int t) {
+  return __ldg(a.block_tables + (int64_t)r * a.max_blocks + t / a.block_size);
+}
+
+// Pool row of offset `off` of block `blk`, or kCmSkip for a bad id (reported).
+// Pool rows are below 2^32 - 1 (the host checks).
+__device__ __forceinline__ uint32_t pool_row(const CompactArgs& a, int blk, int off) {
+  if (blk >= 0 && (int64_t)blk < a.num_blocks) return (uint32_t)((int64_t)blk * a.block_size + off);
+  atomicOr(a.err, PKV_DEVERR_BLOCK);
+  return kCmSkip;
+}
+
+__device__ __forceinline__ void cp_async16(uint32_t smem, const void* g) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem), "l"(g) : "memory");
 }
 
 }  // namespace
 
+// kRing: tiles of the ring.  kPlaces: entries of the ring of places, a power of
+// two >= kRing tiles + 2 batches.
+template <int kRing, int kPlaces>
 __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArgs a) {
-  const int h = blockIdx.x, role = blockIdx.y, r = blockIdx.z;
-  const int tid = threadIdx.x, Hkv = a.num_kv_heads;
-  const CompactSeq s = compact_seq(a, r, h == 0 && role == 0 && tid == 0);
+  extern __shared__ __align__(128) unsigned char cm_smem[];
+  uint4* ring = reinterpret_cast<uint4*>(cm_smem);                               // [kRing][kCmTileVecs]
+  uint2* places = reinterpret_cast<uint2*>(cm_smem + kRing * kCmTileVecs * 16);  // (from, to) by row
+  const int h = blockIdx.x, y = blockIdx.y, r = blockIdx.z;
+  const int tid = threadIdx.x, Hkv = a.num_kv_heads, P = a.block_size;
+  const CompactSeq s = compact_seq(a, r, h == 0 && y == 0 && tid == 0);
   const int32_t* keep = a.keep + ((int64_t)r * a.keep_heads + (a.keep_heads > 1 ? h : 0)) * a.keep_stride;
-  if (role < 2) {
-    unsigned char* pool = role == 0 ? a.k : a.v;
-    const int vpr = a.row_bytes / 16;  // vectors per row
-    const int64_t total = (int64_t)s.n * vpr;
-    const int rows = kCmThreads * kCmVecs / vpr > 0 ? kCmThreads * kCmVecs / vpr : 1;
-    const int64_t step = (int64_t)rows * vpr;  // whole rows a tile
-    for (int64_t i0 = 0; i0 < total; i0 += step) {
-      // a row longer than a tile's vectors is moved in several turns
-      for (int64_t u0 = 0; u0 < step; u0 += kCmThreads * kCmVecs) {
-        uint4 x[kCmVecs];
-        int64_t dst[kCmVecs];
+  if (y < 2 * a.parts) {
+    if (s.n == 0) return;
+    unsigned char* pool = y < a.parts ? a.k : a.v;
+    // this CTA's columns: `vecs` vectors from c0 on, `rows` (a power of two) rows a tile
+    const int per = (a.row_bytes / 16 + a.parts - 1) / a.parts, c0 = (y % a.parts) * per;
+    const int vecs = min(per, a.row_bytes / 16 - c0);
+    if (vecs <= 0) return;
+    const int rows = 1 << (31 - __clz(min(kCmTileVecs / vecs, kCmThreads)));
+    const int tiles = (s.n + rows - 1) / rows;
+    int my_row[kCmVecs], my_c[kCmVecs];  // this thread's vectors of a tile
+#pragma unroll
+    for (int u = 0; u < kCmVecs; ++u) {
+      const int i = tid + u * kCmThreads;
+      my_row[u] = i < rows * vecs ? i / vecs : -1;
+      my_c[u] = i % vecs;
+    }
+    // ---- places, in batches of kCmThreads rows, a row a thread: the kept rows
+    // of the batch after next and the block ids of the next one are on their
+    // way while a batch is used
+    int k_next = -1, k_now = -1, b_from = 0, b_to = 0;  // kept rows, block ids
+    auto load_keep = [&](int j) { return j < s.n ? kept_row(a, s, keep, j) : -1; };
+    auto load_blocks = [&](int j) {
+      if (k_now >= 0) {
+        b_from = table_entry(a, r, s.base + k_now);
+        b_to = table_entry(a, r, s.base + j);
+      }
+    };
+    int filled = 0;  // rows whose places are known
+    k_now = load_keep(tid);
+    k_next = load_keep(kCmThreads + tid);
+    load_blocks(tid);
+    auto fill = [&]() {
+      const int j = filled + tid;
+      uint2 at = make_uint2(kCmSkip, kCmSkip);
+      if (k_now >= 0 && k_now != j) {  // a row already in its place stays
+        const uint32_t from = pool_row(a, b_from, (s.base + k_now) % P), to = pool_row(a, b_to, (s.base + j) % P);
+        if (from != kCmSkip && to != kCmSkip) at = make_uint2(from, to);
+      }
+      places[j & (kPlaces - 1)] = at;
+      filled += kCmThreads;
+      k_now = k_next;
+      load_blocks(filled + tid);
+      k_next = load_keep(filled + kCmThreads + tid);
+    };
+    auto issue = [&](int t) {  // this thread's loads of tile t (an empty group past the last)
+      if (t < tiles) {
 #pragma unroll
         for (int u = 0; u < kCmVecs; ++u) {
-          const int64_t off = u0 + u * kCmThreads + tid;
-          const int64_t i = i0 + off;
-          dst[u] = -1;
-          if (off >= step || i >= total) continue;
-          const int j = (int)(i / vpr), c = (int)(i % vpr);
-          const int k = kept_row(a, s, keep, j);
-          if (k < 0 || k == j) continue;
-          const int64_t from = pool_row(a, r, s.base + k), to = pool_row(a, r, s.base + j);
-          if (from < 0 || to < 0) continue;
-          x[u] = *reinterpret_cast<const uint4*>(pool + (from * Hkv + h) * a.row_bytes + c * 16);
-          dst[u] = (to * Hkv + h) * a.row_bytes + c * 16;
+          if (my_row[u] < 0) continue;
+          const int j = t * rows + my_row[u];
+          const uint32_t from = j < s.n ? places[j & (kPlaces - 1)].x : kCmSkip;
+          if (from != kCmSkip)
+            cp_async16(smem_u32(ring + (t % kRing) * kCmTileVecs + u * kCmThreads + tid),
+                       pool + ((int64_t)from * Hkv + h) * a.row_bytes + (c0 + my_c[u]) * 16);
         }
-        __syncthreads();
-#pragma unroll
-        for (int u = 0; u < kCmVecs; ++u)
-          if (dst[u] >= 0) *reinterpret_cast<uint4*>(pool + dst[u]) = x[u];
       }
-    }
-    if (a.k_scales) {  // the rows' scales: [NB, Hkv, P, scale_bytes]
-      unsigned char* sc = role == 0 ? a.k_scales : a.v_scales;
-      const int P = a.block_size, sb = a.scale_bytes;
-      for (int64_t i0 = 0; i0 < (int64_t)s.n * sb; i0 += kCmThreads / sb * sb) {
-        const int64_t i = i0 + tid;
-        unsigned char x = 0;
-        int64_t dst = -1;
-        if (tid < kCmThreads / sb * sb && i < (int64_t)s.n * sb) {
-          const int j = (int)(i / sb), c = (int)(i % sb);
-          const int k = kept_row(a, s, keep, j);
-          if (k >= 0 && k != j) {
-            const int64_t from = pool_row(a, r, s.base + k), to = pool_row(a, r, s.base + j);
-            if (from >= 0 && to >= 0) {
-              x = sc[((from / P * Hkv + h) * P + from % P) * sb + c];
-              dst = ((to / P * Hkv + h) * P + to % P) * sb + c;
-            }
-          }
-        }
-        __syncthreads();
-        if (dst >= 0) sc[dst] = x;
-      }
-    }
-  } else {
-    float* w = a.weights + ((int64_t)r * Hkv + h) * a.weights_stride + s.base;
-    for (int j0 = 0; j0 < s.n; j0 += kCmThreads) {
-      const int j = j0 + tid;
-      const int k = j < s.n ? kept_row(a, s, keep, j) : -1;
-      const float x = k >= 0 ? w[k] : 0.f;
+      asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    const int ahead = kRing - 1;
+    while (filled < min(ahead * rows, s.n)) fill();
+    __syncthreads();
+    for (int t = 0; t < ahead; ++t) issue(t);
+    for (int t = 0; t < tiles; ++t) {
+      asm volatile("cp.async.wait_group %0;" ::"n"(kRing - 2) : "memory");
+      while (filled < min((t + kRing) * rows, s.n)) fill();
+      // tile t has landed for every thread, the places of tile t + kRing - 1
+      // are known, and the stores of tile t - 1 have left its ring slot
       __syncthreads();
-      if (k >= 0) w[j] = x;
+      issue(t + ahead);
+#pragma unroll
+      for (int u = 0; u < kCmVecs; ++u) {
+        if (my_row[u] < 0) continue;
+        const int j = t * rows + my_row[u];
+        const uint32_t to = j < s.n ? places[j & (kPlaces - 1)].y : kCmSkip;
+        if (to != kCmSkip)
+          *reinterpret_cast<uint4*>(pool + ((int64_t)to * Hkv + h) * a.row_bytes + (c0 + my_c[u]) * 16) =
+              ring[(t % kRing) * kCmTileVecs + u * kCmThreads + tid];
+      }
+    }
+    return;
+  }
+  // ---- weights, and an MXFP8 pool's scales: a few bytes a row
+  constexpr int kTurn = kCmThreads * kCmSmall;
+  if (y == 2 * a.parts && a.weights) {
+    float* w = a.weights + ((int64_t)r * Hkv + h) * a.weights_stride + s.base;
+    for (int j0 = 0; j0 < s.n; j0 += kTurn) {
+      float x[kCmSmall];
+      int k[kCmSmall];
+#pragma unroll
+      for (int u = 0; u < kCmSmall; ++u) {
+        const int j = j0 + u * kCmThreads + tid;
+        k[u] = j < s.n ? kept_row(a, s, keep, j) : -1;
+      }
+#pragma unroll
+      for (int u = 0; u < kCmSmall; ++u) x[u] = k[u] >= 0 ? w[k[u]] : 0.f;
+      __syncthreads();  // the turn's loads are done
+#pragma unroll
+      for (int u = 0; u < kCmSmall; ++u)
+        if (k[u] >= 0) w[j0 + u * kCmThreads + tid] = x[u];
     }
     __syncthreads();  // every source has been read
     for (int j = s.n + tid; j < s.len - s.base; j += kCmThreads) w[j] = 0.f;
+  } else {
+    // scales of K, then of V: [NB, Hkv, P, scale_bytes], scale_bytes a row
+    const int v = y - 2 * a.parts - (a.weights ? 1 : 0), sb = a.scale_bytes;
+    unsigned char* sc = v == 0 ? a.k_scales : a.v_scales;
+    for (int j0 = 0; j0 < s.n; j0 += kTurn) {
+      uint32_t from[kCmSmall], to[kCmSmall];
+#pragma unroll
+      for (int u = 0; u < kCmSmall; ++u) {
+        const int j = j0 + u * kCmThreads + tid;
+        const int k = j < s.n ? kept_row(a, s, keep, j) : -1;
+        from[u] = to[u] = kCmSkip;
+        if (k >= 0 && k != j) {
+          from[u] = pool_row(a, table_entry(a, r, s.base + k), (s.base + k) % P);
+          to[u] = pool_row(a, table_entry(a, r, s.base + j), (s.base + j) % P);
+          if (from[u] == kCmSkip) to[u] = kCmSkip;
+        }
+      }
+      auto at = [&](uint32_t row) {
+        return sc + (((int64_t)(row / P) * Hkv + h) * P + row % P) * sb;
+      };
+      for (int b = 0; b < sb; ++b) {  // a byte of every row at a time
+        unsigned char x[kCmSmall];
+#pragma unroll
+        for (int u = 0; u < kCmSmall; ++u)
+          if (to[u] != kCmSkip) x[u] = at(from[u])[b];
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < kCmSmall; ++u)
+          if (to[u] != kCmSkip) at(to[u])[b] = x[u];
+      }
+    }
   }
 }
 
-cudaError_t launch_kv_compact(const CompactArgs& a, cudaStream_t stream) {
-  kv_compact_kernel<<<dim3((unsigned)a.num_kv_heads, a.weights ? 3u : 2u, (unsigned)a.num_seqs), kCmThreads, 0,
-                      stream>>>(a);
+template <int kRing, int kPlaces>
+static cudaError_t launch_compact_t(const CompactArgs& a, unsigned y, cudaStream_t stream) {
+  constexpr int smem = kRing * kCmTileVecs * 16 + kPlaces * 8;
+  auto kern = kv_compact_kernel<kRing, kPlaces>;
+  static SmemAttrCache attr_cache;
+  cudaError_t e = ensure_smem_limit(kern, smem, attr_cache);
+  if (e != cudaSuccess) return e;
+  kern<<<dim3((unsigned)a.num_kv_heads, y, (unsigned)a.num_seqs), kCmThreads, smem, stream>>>(a);
   return cudaGetLastError();
+}
+
+cudaError_t launch_kv_compact(const CompactArgs& args, cudaStream_t stream) {
+  CompactArgs a = args;
+  // Columns: at most 64 vectors a CTA, and while the chains are fewer than two
+  // a SM, halves of at least four vectors (64 bytes).
+  const int vecs = a.row_bytes / 16;
+  const int64_t chains = (int64_t)a.num_seqs * a.num_kv_heads * 2;
+  a.parts = (vecs + 63) / 64;
+  while (chains * a.parts < 304 && vecs % (2 * a.parts) == 0 && vecs / (2 * a.parts) >= 4) a.parts *= 2;
+  const unsigned y = 2u * a.parts + (a.weights ? 1u : 0u) + (a.k_scales ? 2u : 0u);
+  return chains * a.parts < 456 ? launch_compact_t<12, 4096>(a, y, stream)
+                                : launch_compact_t<4, 2048>(a, y, stream);
 }
 
 }  // namespace pkv

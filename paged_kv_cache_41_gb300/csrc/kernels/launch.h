@@ -355,6 +355,7 @@ struct CompactArgs {
   int32_t keep_heads;           // 1 or Hkv
   int32_t row_bytes;
   int32_t scale_bytes;
+  int32_t parts;                // CTAs a row's columns are dealt to (the launcher sets it)
 };
 cudaError_t launch_kv_compact(const CompactArgs& args, cudaStream_t stream);
 

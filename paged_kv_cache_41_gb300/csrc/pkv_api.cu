@@ -1067,6 +1067,7 @@ pkv_status pkv_kv_compact(const pkv_cache_desc* cache, void* k_cache, void* v_ca
     return PKV_ERR_UNSUPPORTED;
   const int64_t row_bytes = (int64_t)cache->head_dim * elem_bytes(cache->dtype);
   if (row_bytes % 16 != 0 || row_bytes > 16384) return PKV_ERR_UNSUPPORTED;
+  if (cache->num_blocks * cache->block_size >= (int64_t)UINT32_MAX) return PKV_ERR_UNSUPPORTED;
   if (cache->dtype == PKV_MXFP8 && cache->head_dim % 32 != 0) return PKV_ERR_UNSUPPORTED;
   unsigned int* err = device_error_word();
   if (!err) return PKV_ERR_CUDA;

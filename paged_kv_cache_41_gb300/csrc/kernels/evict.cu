@@ -535,7 +535,7 @@ cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
 // Later tiles' loads may run ahead freely: their sources are at or above their
 // own destinations, which this tile's stores do not reach.
 //
-// So each CTA keeps a ring of 8 KiB tiles in shared memory filled by
+// So each CTA keeps a ring of tiles in shared memory filled by
 // cp.async (a plain load would have to arrive before the barrier that orders
 // the stores), several tiles ahead, and works out the rows' places further
 // ahead still.  Bound by the bytes: every moved row read once and written
@@ -544,8 +544,6 @@ cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
 namespace {
 
 constexpr int kCmThreads = 256;
-constexpr int kCmVecs = 2;                            // 16-byte vectors per thread and tile
-constexpr int kCmTileVecs = kCmThreads * kCmVecs;     // 8 KiB
 constexpr uint32_t kCmSkip = 0xffffffffu;             // no row to move here
 constexpr int kCmSmall = 8;                           // weights or scales per thread and turn
 
@@ -596,13 +594,16 @@ __device__ __forceinline__ void cp_async16(uint32_t smem, const void* g) {
 
 }  // namespace
 
-// kRing: tiles of the ring.  kPlaces: entries of the ring of places, a power of
-// two >= kRing tiles + 2 batches.
-template <int kRing, int kPlaces>
+// kVecs: 16-byte vectors per thread and tile.  kRing: tiles of the ring.
+// kPlaces: entries of the ring of places, a power of two >= the rows of kRing +
+// 1 tiles (a tile has kCmThreads at most) and a batch.
+template <int kVecs, int kRing, int kPlaces>
 __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArgs a) {
+  static_assert(kPlaces >= (kRing + 2) * kCmThreads, "the ring of places");
+  constexpr int kTileVecs = kCmThreads * kVecs;
   extern __shared__ __align__(128) unsigned char cm_smem[];
-  uint4* ring = reinterpret_cast<uint4*>(cm_smem);                               // [kRing][kCmTileVecs]
-  uint2* places = reinterpret_cast<uint2*>(cm_smem + kRing * kCmTileVecs * 16);  // (from, to) by row
+  uint4* ring = reinterpret_cast<uint4*>(cm_smem);                               // [kRing][kTileVecs]
+  uint2* places = reinterpret_cast<uint2*>(cm_smem + kRing * kTileVecs * 16);  // (from, to) by row
   const int h = blockIdx.x, y = blockIdx.y, r = blockIdx.z;
   const int tid = threadIdx.x, Hkv = a.num_kv_heads, P = a.block_size;
   const CompactSeq s = compact_seq(a, r, h == 0 && y == 0 && tid == 0);
@@ -614,11 +615,11 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
     const int per = (a.row_bytes / 16 + a.parts - 1) / a.parts, c0 = (y % a.parts) * per;
     const int vecs = min(per, a.row_bytes / 16 - c0);
     if (vecs <= 0) return;
-    const int rows = 1 << (31 - __clz(min(kCmTileVecs / vecs, kCmThreads)));
+    const int rows = 1 << (31 - __clz(min(kTileVecs / vecs, kCmThreads)));
     const int tiles = (s.n + rows - 1) / rows;
-    int my_row[kCmVecs], my_c[kCmVecs];  // this thread's vectors of a tile
+    int my_row[kVecs], my_c[kVecs];  // this thread's vectors of a tile
 #pragma unroll
-    for (int u = 0; u < kCmVecs; ++u) {
+    for (int u = 0; u < kVecs; ++u) {
       const int i = tid + u * kCmThreads;
       my_row[u] = i < rows * vecs ? i / vecs : -1;
       my_c[u] = i % vecs;
@@ -654,12 +655,12 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
     auto issue = [&](int t) {  // this thread's loads of tile t (an empty group past the last)
       if (t < tiles) {
 #pragma unroll
-        for (int u = 0; u < kCmVecs; ++u) {
+        for (int u = 0; u < kVecs; ++u) {
           if (my_row[u] < 0) continue;
           const int j = t * rows + my_row[u];
           const uint32_t from = j < s.n ? places[j & (kPlaces - 1)].x : kCmSkip;
           if (from != kCmSkip)
-            cp_async16(smem_u32(ring + (t % kRing) * kCmTileVecs + u * kCmThreads + tid),
+            cp_async16(smem_u32(ring + (t % kRing) * kTileVecs + u * kCmThreads + tid),
                        pool + ((int64_t)from * Hkv + h) * a.row_bytes + (c0 + my_c[u]) * 16);
         }
       }
@@ -677,13 +678,13 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
       __syncthreads();
       issue(t + ahead);
 #pragma unroll
-      for (int u = 0; u < kCmVecs; ++u) {
+      for (int u = 0; u < kVecs; ++u) {
         if (my_row[u] < 0) continue;
         const int j = t * rows + my_row[u];
         const uint32_t to = j < s.n ? places[j & (kPlaces - 1)].y : kCmSkip;
         if (to != kCmSkip)
           *reinterpret_cast<uint4*>(pool + ((int64_t)to * Hkv + h) * a.row_bytes + (c0 + my_c[u]) * 16) =
-              ring[(t % kRing) * kCmTileVecs + u * kCmThreads + tid];
+              ring[(t % kRing) * kTileVecs + u * kCmThreads + tid];
       }
     }
     return;
@@ -743,10 +744,10 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
   }
 }
 
-template <int kRing, int kPlaces>
+template <int kVecs, int kRing, int kPlaces>
 static cudaError_t launch_compact_t(const CompactArgs& a, unsigned y, cudaStream_t stream) {
-  constexpr int smem = kRing * kCmTileVecs * 16 + kPlaces * 8;
-  auto kern = kv_compact_kernel<kRing, kPlaces>;
+  constexpr int smem = kRing * kCmThreads * kVecs * 16 + kPlaces * 8;
+  auto kern = kv_compact_kernel<kVecs, kRing, kPlaces>;
   static SmemAttrCache attr_cache;
   cudaError_t e = ensure_smem_limit(kern, smem, attr_cache);
   if (e != cudaSuccess) return e;
@@ -757,14 +758,18 @@ static cudaError_t launch_compact_t(const CompactArgs& a, unsigned y, cudaStream
 cudaError_t launch_kv_compact(const CompactArgs& args, cudaStream_t stream) {
   CompactArgs a = args;
   // Columns: at most 64 vectors a CTA, and while the chains are fewer than two
-  // a SM, halves of at least four vectors (64 bytes).
+  // a SM, halves of at least two vectors (32 bytes; three long fp32 sequences
+  // take 52 us with at least four, 44 us with two).
   const int vecs = a.row_bytes / 16;
   const int64_t chains = (int64_t)a.num_seqs * a.num_kv_heads * 2;
   a.parts = (vecs + 63) / 64;
-  while (chains * a.parts < 304 && vecs % (2 * a.parts) == 0 && vecs / (2 * a.parts) >= 4) a.parts *= 2;
+  while (chains * a.parts < 304 && vecs % (2 * a.parts) == 0 && vecs / (2 * a.parts) >= 2) a.parts *= 2;
   const unsigned y = 2u * a.parts + (a.weights ? 1u : 0u) + (a.k_scales ? 2u : 0u);
-  return chains * a.parts < 456 ? launch_compact_t<12, 4096>(a, y, stream)
-                                : launch_compact_t<4, 2048>(a, y, stream);
+  // A drafted path is one batch of rows at most: a small ring, and more CTAs a
+  // SM (64 requests 6.2 us, with four tiles 7.1 us).  Few chains: a deep ring.
+  if (a.keep_stride <= kCmThreads) return launch_compact_t<2, 2, 1024>(a, y, stream);
+  return chains * a.parts < 456 ? launch_compact_t<4, 8, 4096>(a, y, stream)
+                                : launch_compact_t<2, 4, 2048>(a, y, stream);
 }
 
 }  // namespace pkv

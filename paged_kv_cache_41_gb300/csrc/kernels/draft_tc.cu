@@ -1,5 +1,5 @@
-// draft_tc.cu -- attention of drafted tokens over a paged bf16 cache on the
-// tcgen05 tensor cores.
+// draft_tc.cu -- attention of drafted tokens over a paged bf16 or MXFP8 cache on
+// the tcgen05 tensor cores.
 //
 // What it computes: draft.cu's formula.  For each kv head the n drafted rows'
 // G query heads are n G rows of one matrix Q against the same keys, so
@@ -34,6 +34,10 @@
 //     launch.h) through a ring of tiles, K0, V0, K1, V1, ..., and each piece's
 //     Q as soon as the previous piece's QKs have read theirs; a thread per
 //     group issues its MMAs: QK(0), QK(1), PV(0), QK(2), PV(1), ...;
+//   * an MXFP8 pool's tiles are filled by four more warps instead of TMA: they
+//     read codes and scales with plain loads, one tile ahead, and store the
+//     widened bf16 rows into the ring in the same layout (exact: a code has
+//     four significant bits).  No raw copy in shared memory is needed;
 //   * only stages that hold drafted rows apply masks: a row's 64-bit mask is
 //     shifted into place and selects the scores.  Drafted rows hidden from
 //     some rows may hold anything, and 0 * NaN is not 0, so those stages also
@@ -45,6 +49,7 @@
 #include <math.h>
 
 #include "draft.cuh"
+#include "mx_widen.cuh"
 #include "plan.cuh"
 #include "tcgen05.cuh"
 
@@ -53,7 +58,9 @@ namespace pkv {
 namespace {
 
 constexpr int kDtSoftWarps = 8;      // two groups of four
-constexpr int kDtThreads = (kDtSoftWarps + 3) * 32;  // ..., an MMA warp for each, producer
+constexpr int kDtWidenWarps = 4;     // MXFP8 pools
+// ..., an MMA warp for each, producer, and for MXFP8 the widening warps
+constexpr int dt_threads(bool mx) { return (kDtSoftWarps + 3 + (mx ? kDtWidenWarps : 0)) * 32; }
 constexpr int kDtJob = 64;           // keys of a job
 constexpr int kDtDescs = 8;          // stage descriptors in flight
 constexpr float kDtLn2 = 0.6931471805599453f;
@@ -97,6 +104,24 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
+// Whether any of 16 E4M3 codes is a NaN: its lower seven bits are all set.
+__device__ __forceinline__ bool nan_codes(const uint4& x) {
+  constexpr uint32_t kLow = 0x7f7f7f7fu, kOne = 0x01010101u;
+  return ((((x.x & kLow) + kOne) | ((x.y & kLow) + kOne) | ((x.z & kLow) + kOne) | ((x.w & kLow) + kOne)) &
+          0x80808080u) != 0;
+}
+
+// The bf16 values v of eight codes (two words), with NaN where a code is one.
+__device__ __noinline__ uint4 nan_at(uint4 v, uint32_t w0, uint32_t w1) {
+  uint32_t o[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const uint32_t code = ((i < 4 ? w0 : w1) >> (8 * (i & 3))) & 0x7fu;
+    if (code == 0x7fu) o[i >> 1] |= (i & 1) ? 0x7fff0000u : 0x7fffu;
+  }
+  return make_uint4(o[0], o[1], o[2], o[3]);
+}
+
 // Eight floats to a 32-byte aligned address: one whole sector a thread.
 __device__ __forceinline__ void store_sector(float* p, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
@@ -116,8 +141,8 @@ __device__ __forceinline__ uint32_t mask_word(uint64_t mask, int mb, int i) {
 
 }  // namespace
 
-template <int D, int kTiles>
-__global__ void __launch_bounds__(kDtThreads, 1)
+template <int D, int kTiles, bool kMx>
+__global__ void __launch_bounds__(dt_threads(kMx), 1)
     draft_tc_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
                     const __grid_constant__ CUtensorMap tmv, const DraftArgs a) {
   using L = DtSmem<D, kTiles>;
@@ -154,7 +179,7 @@ __global__ void __launch_bounds__(kDtThreads, 1)
   const int Hkv = a.num_kv_heads, G = a.num_q_heads / Hkv;
   if (t == 0) {
     for (int i = 0; i < kItems; ++i) {
-      mbar_init(&full[i], 1);
+      mbar_init(&full[i], kMx ? kDtWidenWarps : 1);
       mbar_init(&freeb[i], 2);
     }
     for (int i = 0; i < kDtDescs; ++i) mbar_init(&dfull[i], 1);
@@ -176,15 +201,17 @@ __global__ void __launch_bounds__(kDtThreads, 1)
   if (t < 65) bad[t] = 0;
   if (warp == kDtSoftWarps + 2 && lane == 0) {
     prefetch_tensormap(&tmq);
-    prefetch_tensormap(&tmk);
-    prefetch_tensormap(&tmv);
+    if constexpr (!kMx) {
+      prefetch_tensormap(&tmk);
+      prefetch_tensormap(&tmv);
+    }
   }
   if (warp == 0) tc::tmem_alloc(tmem_base, 512);
   pdl_wait();
   pdl_launch_dependents();
   int4 d0;
   const int n =
-      plan_cta_stages<kDtThreads, kDraftKeys, 1>(a, reinterpret_cast<long long*>(exch), &d0);
+      plan_cta_stages<dt_threads(kMx), kDraftKeys, 1>(a, reinterpret_cast<long long*>(exch), &d0);
   tc::fence_before_sync();
   __syncthreads();
   tc::fence_after_sync();
@@ -266,11 +293,13 @@ __global__ void __launch_bounds__(kDtThreads, 1)
     struct Boxes {
       int group, n, head;  // first row group, boxes, kv head
     };
+    // fill the next ring slot; for MXFP8, only see that it may be written
     auto load = [&](const CUtensorMap* tm, const Boxes& x) -> bool {
       if (!wait_slot()) return false;
-      if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(x.n * TB * D * 2));
+      if (kMx) {
+      } else if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(x.n * TB * D * 2));
       __syncwarp();
-      if (j < x.n)
+      if (!kMx && j < x.n)
         tma_load_5d(ring + slot * L::kTile + j * TB * H * 128, tm, 0, 0, 0, x.head, x.group, &full[slot]);
       ++item;
       if (++slot == kItems) {
@@ -314,18 +343,22 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       Boxes b;
       b.n = (nvalid + TB - 1) / TB;
       b.head = kvh;
-      if (j < b.n && (blk_next < 0 || (int64_t)blk_next >= a.num_blocks)) {
+      if (!kMx && j < b.n && (blk_next < 0 || (int64_t)blk_next >= a.num_blocks)) {
         atomicOr(a.err, PKV_DEVERR_BLOCK);
         b.group = (int)a.num_blocks * (P / kRowGroup);  // zero-filled out-of-range box
       } else {
         b.group = blk_next * (P / kRowGroup) + (t0 + j * TB) % P / kRowGroup;
       }
-      if (lane == 0) {
-        DtDesc* d = &descs[emitted % kDtDescs];
-        d->a = make_int4(r, h, nvalid, flags);
-        d->b = make_int4(s.ctx - t0, row0, rows, pieces);
-        mbar_arrive(&dfull[emitted % kDtDescs]);
-      }
+      auto describe = [&](int seq, int seg, int mb) {
+        if (lane == 0) {
+          DtDesc* d = &descs[emitted % kDtDescs];
+          d->a = make_int4(seq, seg, nvalid, flags);
+          d->b = make_int4(mb, row0, rows, pieces);
+          mbar_arrive(&dfull[emitted % kDtDescs]);
+        }
+      };
+      const int seq = r, seg = h, mb = s.ctx - t0;
+      if (!kMx) describe(seq, seg, mb);
       ++k;
       if (k < n) {  // the next stage's block ids, under this one's waits
         if (++i == nt) next_segment();
@@ -335,6 +368,8 @@ __global__ void __launch_bounds__(kDtThreads, 1)
         ok = false;
         break;
       }
+      // the widening warps fill a stage's slots once they see it
+      if (kMx) describe(seq, seg, mb);
       ++emitted;
     }
     if (lane == 0) {
@@ -346,11 +381,113 @@ __global__ void __launch_bounds__(kDtThreads, 1)
       } else {
         atomicOr(a.err, PKV_DEVERR_TIMEOUT);
         // copies may still be in flight into the ring and Q: wait for them
-        for (int it = item > kItems ? item - kItems : 0; it < item; ++it)
-          mbar_wait(&full[it % kItems], (it / kItems) & 1);
+        if (!kMx)
+          for (int it = item > kItems ? item - kItems : 0; it < item; ++it)
+            mbar_wait(&full[it % kItems], (it / kItems) & 1);
         if (pieces > 0 && !q_wanted) mbar_wait(qfull, (pieces - 1) & 1);
       }
     }
+  } else if (kMx && warp > kDtSoftWarps + 2) {
+    // ============================================================ widening
+    // A row is kPerRow 16-byte chunks of codes, a chunk a thread: step i of a
+    // tile covers rows kStep i .. of it.  The next tile's loads are out while
+    // a tile is widened.
+    constexpr int kPerRow = D / 16, kStep = kDtWidenWarps * 32 / kPerRow, kSteps = kDraftKeys / kStep;
+    const int wt = t - (kDtSoftWarps + 3) * 32, cc = wt % kPerRow, row0 = wt / kPerRow;
+    int64_t at[kSteps];  // pool row (of all heads) of this thread's rows, -1: none
+    int scale_at[kSteps];
+    uint4 kx[kSteps], vx[kSteps];
+    uint32_t ksc[kSteps], vsc[kSteps];
+    int seq = -1, ctx = 0, kvh = 0;
+    auto places = [&](const int4& da, const int4& db) {
+      if (da.x != seq) {
+        seq = da.x;
+        ctx = __ldg(a.ctx_lens + seq);
+      }
+      kvh = a.row_tiles > 1 ? da.y / a.row_tiles : da.y;
+      const int t0 = ctx - db.x;
+      const int32_t* table = a.block_tables + (int64_t)seq * a.max_blocks;
+      int blk[kSteps];
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int row = i * kStep + row0;
+        blk[i] = row < da.z ? __ldg(table + (t0 + row) / P) : -2;
+      }
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int off = (t0 + i * kStep + row0) % P;
+        if (blk[i] >= 0 && (int64_t)blk[i] < a.num_blocks) {
+          at[i] = (int64_t)blk[i] * P + off;
+          scale_at[i] = off;
+        } else {
+          at[i] = -1;
+          if (blk[i] != -2 && cc == 0) atomicOr(a.err, PKV_DEVERR_BLOCK);
+        }
+      }
+    };
+    auto fetch = [&](const void* pool, const uint8_t* scales, uint4 (&x)[kSteps], uint32_t (&sc)[kSteps]) {
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        x[i] = make_uint4(0u, 0u, 0u, 0u);  // rows past the last one, and of bad blocks
+        sc[i] = 0;
+        if (at[i] >= 0) {
+          x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) +
+                                                      (at[i] * Hkv + kvh) * D + cc * 16));
+          sc[i] = __ldg(scales + (((at[i] - scale_at[i]) * Hkv + (int64_t)kvh * P) + scale_at[i]) * (D / 32) +
+                        cc / 2);
+        }
+      }
+    };
+    auto widen = [&](int item, const uint4 (&x)[kSteps], const uint32_t (&sc)[kSteps]) {
+      unsigned char* tile = ring + (size_t)(item % kItems) * L::kTile;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        const int row = i * kStep + row0;
+        __nv_bfloat162 s1, s2;
+        scale_factors(sc[i], 0, s1, s2);
+        const bool big = sc[i] > 134u;
+        uint4 lo = widen8(make_uint2(x[i].x, x[i].y), s1, s2, big);
+        uint4 hi = widen8(make_uint2(x[i].z, x[i].w), s1, s2, big);
+        // widen8 takes the NaN codes s.1111.111 for numbers
+        if (nan_codes(x[i])) {
+          lo = nan_at(lo, x[i].x, x[i].y);
+          hi = nan_at(hi, x[i].z, x[i].w);
+        }
+        // 16-byte chunks 2 cc and 2 cc + 1 of the bf16 row, eight to a half;
+        // threads of the second half store theirs the other way round, so
+        // that eight threads' stores fall into eight bank groups
+        unsigned char* d = tile + (row / kRowGroup) * kGroupBytes + (cc >> 2) * 1024 + (row & 7) * 128;
+        const int c0 = (cc & 3) * 2, turn = cc >> 2;
+        *reinterpret_cast<uint4*>(d + (((c0 + turn) ^ (row & 7)) << 4)) = turn ? hi : lo;
+        *reinterpret_cast<uint4*>(d + (((c0 + 1 - turn) ^ (row & 7)) << 4)) = turn ? lo : hi;
+      }
+      tc::fence_proxy_async_smem();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&full[item % kItems]);
+    };
+    bool ok = true, have = false;
+    for (int e = 0;; ++e) {
+      if (!have) {
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&dfull[e % kDtDescs], (e / kDtDescs) & 1)))) break;
+        const DtDesc& d = descs[e % kDtDescs];
+        if (d.a.w & kDtDone) break;
+        places(d.a, d.b);
+        fetch(a.k, a.k_scales, kx, ksc);
+      }
+      fetch(a.v, a.v_scales, vx, vsc);
+      widen(2 * e, kx, ksc);
+      have = __all_sync(0xffffffffu, mbar_test(&dfull[(e + 1) % kDtDescs], ((e + 1) / kDtDescs) & 1));
+      if (have) {
+        const DtDesc& d = descs[(e + 1) % kDtDescs];
+        have = !(d.a.w & kDtDone);
+        if (have) {
+          places(d.a, d.b);
+          fetch(a.k, a.k_scales, kx, ksc);
+        }
+      }
+      widen(2 * e + 1, vx, vsc);
+    }
+    if (!ok && lane == 0) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
   } else if (warp >= kDtSoftWarps) {
     // ============================================================ MMA issue
     const int x = warp - kDtSoftWarps;  // of this group's jobs; job j uses S buffer j & 1
@@ -688,12 +825,23 @@ __global__ void __launch_bounds__(kDtThreads, 1)
                 const int pos = __ldg(a.ctx_lens + da.x) + jd;
                 const int blk = __ldg(a.block_tables + (int64_t)da.x * a.max_blocks + pos / P);
                 if (blk < 0 || (int64_t)blk >= a.num_blocks) continue;
-                const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) +
-                                          (((int64_t)blk * P + pos % P) * Hkv + kvh) * D + c0;
+                const int64_t vrow = (int64_t)blk * P + pos % P;
+                if constexpr (kMx) {
+                  const __nv_fp8_e4m3* vp = static_cast<const __nv_fp8_e4m3*>(a.v) + (vrow * Hkv + kvh) * D + c0;
+                  const float sc = e8m0_value(__ldg(a.v_scales + (((int64_t)blk * Hkv + kvh) * P + pos % P) * (D / 32) +
+                                                    c0 / 32));
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                  const uint32_t u = __bfloat16_as_ushort(vp[i]);
-                  if ((u & 0x7f80u) == 0x7f80u) o[i] += __uint_as_float(u << 16);
+                  for (int i = 0; i < 16; ++i) {
+                    const float x = __bfloat162float(__float2bfloat16_rn((float)vp[i] * sc));
+                    if ((__float_as_uint(x) & 0x7f800000u) == 0x7f800000u) o[i] += x;
+                  }
+                } else {
+                  const __nv_bfloat16* vp = static_cast<const __nv_bfloat16*>(a.v) + (vrow * Hkv + kvh) * D + c0;
+#pragma unroll
+                  for (int i = 0; i < 16; ++i) {
+                    const uint32_t u = __bfloat16_as_ushort(vp[i]);
+                    if ((u & 0x7f80u) == 0x7f80u) o[i] += __uint_as_float(u << 16);
+                  }
                 }
               }
             }
@@ -824,15 +972,15 @@ __global__ void __launch_bounds__(256) draft_tc_reduce_kernel(const DraftArgs a)
   }
 }
 
-template <int D, int kTiles>
+template <int D, int kTiles, bool kMx>
 static cudaError_t launch_draft_tc_t(const CUtensorMap& tmq, const CUtensorMap& tmk, const CUtensorMap& tmv,
                                      const DraftArgs& a, cudaStream_t stream) {
   constexpr int smem = DtSmem<D, kTiles>::total;
-  auto kern = draft_tc_kernel<D, kTiles>;
+  auto kern = draft_tc_kernel<D, kTiles, kMx>;
   static SmemAttrCache attr_cache;
   cudaError_t e = ensure_smem_limit(kern, smem, attr_cache);
   if (e != cudaSuccess) return e;
-  e = launch_pdl(kern, dim3((unsigned)a.num_ctas), dim3(kDtThreads), smem, stream, tmq, tmk, tmv, a);
+  e = launch_pdl(kern, dim3((unsigned)a.num_ctas), dim3(dt_threads(kMx)), smem, stream, tmq, tmk, tmv, a);
   if (e != cudaSuccess || a.num_ctas == 1) return e;  // one CTA cuts nothing
   const int rows = a.max_draft * (a.num_q_heads / a.num_kv_heads);
   const int blocks = ((rows < kTiles * kDraftRows ? rows : kTiles * kDraftRows) + 31) / 32;
@@ -840,13 +988,21 @@ static cudaError_t launch_draft_tc_t(const CUtensorMap& tmq, const CUtensorMap& 
                     0, stream, a);
 }
 
-cudaError_t launch_draft_tc(int head_dim, int tiles, const CUtensorMap& tmq, const CUtensorMap& tmk,
-                            const CUtensorMap& tmv, const DraftArgs& a, cudaStream_t stream) {
-  if (head_dim == 128)
-    return tiles > 1 ? launch_draft_tc_t<128, 2>(tmq, tmk, tmv, a, stream)
-                     : launch_draft_tc_t<128, 1>(tmq, tmk, tmv, a, stream);
-  return tiles > 1 ? launch_draft_tc_t<64, 2>(tmq, tmk, tmv, a, stream)
-                   : launch_draft_tc_t<64, 1>(tmq, tmk, tmv, a, stream);
+template <int D, bool kMx>
+static cudaError_t launch_draft_tc_d(int tiles, const CUtensorMap& tmq, const CUtensorMap& tmk,
+                                     const CUtensorMap& tmv, const DraftArgs& a, cudaStream_t stream) {
+  return tiles > 1 ? launch_draft_tc_t<D, 2, kMx>(tmq, tmk, tmv, a, stream)
+                   : launch_draft_tc_t<D, 1, kMx>(tmq, tmk, tmv, a, stream);
+}
+
+cudaError_t launch_draft_tc(int dtype, int head_dim, int tiles, const CUtensorMap& tmq,
+                            const CUtensorMap& tmk, const CUtensorMap& tmv, const DraftArgs& a,
+                            cudaStream_t stream) {
+  if (dtype == PKV_MXFP8)
+    return head_dim == 128 ? launch_draft_tc_d<128, true>(tiles, tmq, tmk, tmv, a, stream)
+                           : launch_draft_tc_d<64, true>(tiles, tmq, tmk, tmv, a, stream);
+  return head_dim == 128 ? launch_draft_tc_d<128, false>(tiles, tmq, tmk, tmv, a, stream)
+                         : launch_draft_tc_d<64, false>(tiles, tmq, tmk, tmv, a, stream);
 }
 
 }  // namespace pkv

@@ -277,7 +277,8 @@ struct DraftArgs {
   float qscale;                 // softmax scale * log2(e)
 };
 
-// Draft-tree attention on the tensor cores (draft_tc.cu): bf16 pools.  A
+// Draft-tree attention on the tensor cores (draft_tc.cu): bf16 and MXFP8 pools
+// (tmk and tmv are of no use to the latter).  A
 // segment is one kv head of a sequence against up to `tiles` 128-row tiles of
 // its (drafted row, head) rows; stages are 128 keys.  tmk / tmv: row-group
 // maps whose box is draft_tc_box_rows rows; tmq: a 128-byte-swizzled map over
@@ -287,8 +288,9 @@ constexpr int kDraftRows = 128;
 __host__ __device__ constexpr int draft_tc_box_rows(int block_size) {
   return kDraftKeys % block_size == 0 ? block_size : block_size % kDraftKeys == 0 ? kDraftKeys : 32;
 }
-cudaError_t launch_draft_tc(int head_dim, int tiles, const CUtensorMap& tmq, const CUtensorMap& tmk,
-                            const CUtensorMap& tmv, const DraftArgs& args, cudaStream_t stream);
+cudaError_t launch_draft_tc(int dtype, int head_dim, int tiles, const CUtensorMap& tmq,
+                            const CUtensorMap& tmk, const CUtensorMap& tmv, const DraftArgs& args,
+                            cudaStream_t stream);
 cudaError_t launch_draft_simt(int dtype, int head_dim, const DraftArgs& args, cudaStream_t stream);
 // (token, query head) rows per CTA where a kv head has `rows` of them at most.
 int draft_simt_rows(int rows);

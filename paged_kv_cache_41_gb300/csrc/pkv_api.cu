@@ -812,9 +812,10 @@ int32_t draft_splits(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_he
   return (int32_t)(s < 1 ? 1 : s);
 }
 
-// bf16 pools run on the tensor cores (row groups addressed with int32
-// coordinates), the others on the CUDA cores.
+// fp32 pools run on the CUDA cores, the others on the tensor cores (a bf16
+// pool's row groups are addressed with int32 coordinates).
 bool draft_on_tc(const pkv_cache_desc* c) {
+  if (c->dtype == PKV_MXFP8) return true;
   return c->dtype == PKV_BF16 &&
          (int64_t)c->num_blocks * (c->block_size / pkv::kRowGroup) <= INT32_MAX;
 }
@@ -933,11 +934,14 @@ pkv_status pkv_draft_tree_attention(
     a.q_tokens = max_draft < pkv::kDraftRows / G ? max_draft : pkv::kDraftRows / G;
     const int box = pkv::draft_tc_box_rows(cache->block_size);
     CUtensorMap tmq, tmk, tmv;
-    if ((st = encode_q_map_sw128(&tmq, q, num_rows, num_q_heads, cache->head_dim, G, a.q_tokens)) != PKV_OK ||
-        (st = encode_cache_map_rg(&tmk, cache, k_cache, box)) != PKV_OK ||
-        (st = encode_cache_map_rg(&tmv, cache, v_cache, box)) != PKV_OK)
+    if ((st = encode_q_map_sw128(&tmq, q, num_rows, num_q_heads, cache->head_dim, G, a.q_tokens)) != PKV_OK)
       return st;
-    e = pkv::launch_draft_tc(cache->head_dim, w.tiles, tmq, tmk, tmv, a, as_stream(stream));
+    tmk = tmv = tmq;
+    if (cache->dtype == PKV_BF16 &&
+        ((st = encode_cache_map_rg(&tmk, cache, k_cache, box)) != PKV_OK ||
+         (st = encode_cache_map_rg(&tmv, cache, v_cache, box)) != PKV_OK))
+      return st;
+    e = pkv::launch_draft_tc(cache->dtype, cache->head_dim, w.tiles, tmq, tmk, tmv, a, as_stream(stream));
   } else {
     e = pkv::launch_draft_simt(cache->dtype, cache->head_dim, a, as_stream(stream));
   }

@@ -91,7 +91,7 @@ def test_types_and_heads(dtype, hq, hkv, d):
 
 
 @pytest.mark.parametrize("p", [16, 32, 64, 96, 128, 160, 256])
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "mxfp8"])
 def test_block_sizes(p, dtype):
     Draft([p - 1, 3 * p + 5, 0, 700, 2 * p], [2, 64, p % 60 + 1, 9, 30], dtype=dtype, p=p, d=128,
           hq=8, hkv=2, seed=p).run()
@@ -105,13 +105,15 @@ def test_masks(masks, dtype):
 
 
 @pytest.mark.parametrize("n", [1, 2, 4, 8, 16, 17, 32, 33, 64])
-def test_draft_lengths(n):
+@pytest.mark.parametrize("dtype", ["bf16", "mxfp8"])
+def test_draft_lengths(n, dtype):
     # every sequence alike: one to eight row tiles of the largest group
-    Draft([250, 0, 1000], [n] * 3, hq=16, hkv=2, d=128, seed=n).run()
+    Draft([250, 0, 1000], [n] * 3, dtype=dtype, hq=16, hkv=2, d=128, seed=n).run()
 
 
-def test_one_sequence_many_splits():
-    Draft([9001], [13], hq=8, hkv=2, d=128, seed=5).run()
+@pytest.mark.parametrize("dtype", ["bf16", "mxfp8"])
+def test_one_sequence_many_splits(dtype):
+    Draft([9001], [13], dtype=dtype, hq=8, hkv=2, d=128, seed=5).run()
 
 
 def test_many_sequences():
@@ -163,7 +165,34 @@ def test_hidden_rows_with_nan_and_inf(dtype, value, ctx):
         assert torch.isnan(out[seers].float()).all()
 
 
-@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("ctx", [3, 60, 125])
+def test_nan_codes_of_a_quantized_pool(d, ctx):
+    # drafted row 2 holds NaN codes: whoever sees it gets NaN there, nobody else
+    dr = Draft([ctx], [9], dtype="mxfp8", hq=8, hkv=2, d=d, seed=21)
+    words = [1 | 1 << i for i in range(9)]
+    words[6] |= 4
+    words[2] = 1
+    dr.words, dr.masks = [words], su.as_int64(words).cuda()
+    want, want_lse = dr.call()
+    slot = int(dr.cache.slots(0, [ctx + 2])[0])
+    dr.cache.v.elements.view(-1, 2, d)[slot, :, 5:40:3] = 0x7F
+    dr.cache.v.elements.view(-1, 2, d)[slot, :, 6] = 0xFF
+    out, lse = dr.call()
+    assert pkv.get_device_error() == 0
+    dr.check(out, lse)
+    dr.cache.k.elements.view(-1, 2, d)[slot, 1, 9] = 0x7F
+    out, lse = dr.call()
+    hidden = [i for i in range(9) if i != 6]
+    assert torch.equal(out[hidden], want[hidden]) and torch.equal(lse[hidden], want_lse[hidden])
+    assert torch.isnan(out[6, 4:].float()).all() and torch.isnan(lse[6, 4:]).all()
+    # in the context every row sees them
+    dr.cache.v.elements.view(-1, 2, d)[int(dr.cache.slots(0, [0])[0]), :, 1] = 0x7F
+    out, _ = dr.call()
+    assert torch.isnan(out[:, :, 1].float()).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "mxfp8"])
 def test_large_scores(dtype):
     # scores far apart: the running maximum moves in every tile
     dr = Draft([700, 3], [9, 9], dtype=dtype, hq=4, hkv=2, d=64, seed=10)

@@ -111,17 +111,6 @@ __device__ __forceinline__ bool nan_codes(const uint4& x) {
           0x80808080u) != 0;
 }
 
-// The bf16 values v of eight codes (two words), with NaN where a code is one.
-__device__ __noinline__ uint4 nan_at(uint4 v, uint32_t w0, uint32_t w1) {
-  uint32_t o[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-  for (int i = 0; i < 8; ++i) {
-    const uint32_t code = ((i < 4 ? w0 : w1) >> (8 * (i & 3))) & 0x7fu;
-    if (code == 0x7fu) o[i >> 1] |= (i & 1) ? 0x7fff0000u : 0x7fffu;
-  }
-  return make_uint4(o[0], o[1], o[2], o[3]);
-}
-
 // Eight floats to a 32-byte aligned address: one whole sector a thread.
 __device__ __forceinline__ void store_sector(float* p, const float* v) {
   asm volatile("st.global.v8.f32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "f"(v[0]), "f"(v[1]),
@@ -389,14 +378,14 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
     }
   } else if (kMx && warp > kDtSoftWarps + 2) {
     // ============================================================ widening
-    // A row is kPerRow 16-byte chunks of codes, a chunk a thread: step i of a
-    // tile covers rows kStep i .. of it.  The next tile's loads are out while
-    // a tile is widened.
-    constexpr int kPerRow = D / 16, kStep = kDtWidenWarps * 32 / kPerRow, kSteps = kDraftKeys / kStep;
-    const int wt = t - (kDtSoftWarps + 3) * 32, cc = wt % kPerRow, row0 = wt / kPerRow;
-    int64_t at[kSteps];  // pool row (of all heads) of this thread's rows, -1: none
-    int scale_at[kSteps];
-    uint4 kx[kSteps], vx[kSteps];
+    // A thread takes a scale group, 32 codes, of a row: step i of a tile covers
+    // rows kStep i .. of it.  The next tile's loads are out while a tile is
+    // widened.
+    constexpr int kPerRow = D / 32, kStep = kDtWidenWarps * 32 / kPerRow, kSteps = kDraftKeys / kStep;
+    const int wt = t - (kDtSoftWarps + 3) * 32, g = wt % kPerRow, row0 = wt / kPerRow;
+    const int shift = (P & (P - 1)) == 0 ? 31 - __clz(P) : -1;  // of a power-of-two block size
+    int blk[kSteps], off[kSteps];  // of this thread's rows; blk -1: none
+    uint4 kx[kSteps][2], vx[kSteps][2];
     uint32_t ksc[kSteps], vsc[kSteps];
     int seq = -1, ctx = 0, kvh = 0;
     auto places = [&](const int4& da, const int4& db) {
@@ -407,38 +396,35 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
       kvh = a.row_tiles > 1 ? da.y / a.row_tiles : da.y;
       const int t0 = ctx - db.x;
       const int32_t* table = a.block_tables + (int64_t)seq * a.max_blocks;
-      int blk[kSteps];
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const int row = i * kStep + row0;
-        blk[i] = row < da.z ? __ldg(table + (t0 + row) / P) : -2;
+        const int row = t0 + i * kStep + row0, bi = shift >= 0 ? row >> shift : row / P;
+        off[i] = row - bi * P;
+        blk[i] = i * kStep + row0 < da.z ? __ldg(table + bi) : -2;
       }
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        const int off = (t0 + i * kStep + row0) % P;
-        if (blk[i] >= 0 && (int64_t)blk[i] < a.num_blocks) {
-          at[i] = (int64_t)blk[i] * P + off;
-          scale_at[i] = off;
-        } else {
-          at[i] = -1;
-          if (blk[i] != -2 && cc == 0) atomicOr(a.err, PKV_DEVERR_BLOCK);
+      for (int i = 0; i < kSteps; ++i)
+        if (blk[i] < 0 || (int64_t)blk[i] >= a.num_blocks) {
+          if (blk[i] != -2 && g == 0) atomicOr(a.err, PKV_DEVERR_BLOCK);
+          blk[i] = -1;
         }
-      }
     };
-    auto fetch = [&](const void* pool, const uint8_t* scales, uint4 (&x)[kSteps], uint32_t (&sc)[kSteps]) {
+    auto fetch = [&](const void* pool, const uint8_t* scales, uint4 (&x)[kSteps][2], uint32_t (&sc)[kSteps]) {
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        x[i] = make_uint4(0u, 0u, 0u, 0u);  // rows past the last one, and of bad blocks
+        x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);  // rows past the last one, and of bad blocks
         sc[i] = 0;
-        if (at[i] >= 0) {
-          x[i] = __ldg(reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) +
-                                                      (at[i] * Hkv + kvh) * D + cc * 16));
-          sc[i] = __ldg(scales + (((at[i] - scale_at[i]) * Hkv + (int64_t)kvh * P) + scale_at[i]) * (D / 32) +
-                        cc / 2);
+        if (blk[i] >= 0) {
+          const int64_t row = (int64_t)blk[i] * P * Hkv;  // rows of one head before the block
+          const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) +
+                                                           (row + off[i] * Hkv + kvh) * D + g * 32);
+          x[i][0] = __ldg(at);
+          x[i][1] = __ldg(at + 1);
+          sc[i] = __ldg(scales + (row + kvh * P + off[i]) * (D / 32) + g);
         }
       }
     };
-    auto widen = [&](int item, const uint4 (&x)[kSteps], const uint32_t (&sc)[kSteps]) {
+    auto widen = [&](int item, const uint4 (&x)[kSteps][2], const uint32_t (&sc)[kSteps]) {
       unsigned char* tile = ring + (size_t)(item % kItems) * L::kTile;
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
@@ -446,20 +432,30 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
         __nv_bfloat162 s1, s2;
         scale_factors(sc[i], 0, s1, s2);
         const bool big = sc[i] > 134u;
-        uint4 lo = widen8(make_uint2(x[i].x, x[i].y), s1, s2, big);
-        uint4 hi = widen8(make_uint2(x[i].z, x[i].w), s1, s2, big);
-        // widen8 takes the NaN codes s.1111.111 for numbers
-        if (nan_codes(x[i])) {
-          lo = nan_at(lo, x[i].x, x[i].y);
-          hi = nan_at(hi, x[i].z, x[i].w);
+        // four 16-byte chunks of the bf16 row, from chunk 4 (g % 2) of its half
+        // g / 2 on; threads of the second half store theirs in another order,
+        // so that eight threads' stores fall into eight bank groups
+        unsigned char* d = tile + (row / kRowGroup) * kGroupBytes + (g >> 1) * 1024 + (row & 7) * 128;
+        const int flip = (g >> 1) << 1;
+        const uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w,
+                               x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
+        uint4 v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = widen8(make_uint2(w[2 * q], w[2 * q + 1]), s1, s2, big);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int ch = (g & 1) * 4 + (q ^ flip);
+          *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) << 4)) = flip ? v[q ^ 2] : v[q];
         }
-        // 16-byte chunks 2 cc and 2 cc + 1 of the bf16 row, eight to a half;
-        // threads of the second half store theirs the other way round, so
-        // that eight threads' stores fall into eight bank groups
-        unsigned char* d = tile + (row / kRowGroup) * kGroupBytes + (cc >> 2) * 1024 + (row & 7) * 128;
-        const int c0 = (cc & 3) * 2, turn = cc >> 2;
-        *reinterpret_cast<uint4*>(d + (((c0 + turn) ^ (row & 7)) << 4)) = turn ? hi : lo;
-        *reinterpret_cast<uint4*>(d + (((c0 + 1 - turn) ^ (row & 7)) << 4)) = turn ? lo : hi;
+        if (nan_codes(x[i][0]) || nan_codes(x[i][1])) {  // widen8 takes the NaN codes s.1111.111 for numbers
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+#pragma unroll 1
+            for (int b = 0; b < 4; ++b)
+              if (((w[q] >> (8 * b)) & 0x7fu) == 0x7fu)
+                *reinterpret_cast<uint16_t*>(d + ((((g & 1) * 4 + (q >> 1)) ^ (row & 7)) << 4) +
+                                             ((q & 1) * 4 + b) * 2) = 0x7fffu;
+        }
       }
       tc::fence_proxy_async_smem();
       __syncwarp();

@@ -34,7 +34,7 @@
 //     launch.h) through a ring of tiles, K0, V0, K1, V1, ..., and each piece's
 //     Q as soon as the previous piece's QKs have read theirs; a thread per
 //     group issues its MMAs: QK(0), QK(1), PV(0), QK(2), PV(1), ...;
-//   * an MXFP8 pool's tiles are filled by four more warps instead of TMA: they
+//   * an MXFP8 pool's tiles are filled by eight more warps instead of TMA: they
 //     read codes and scales with plain loads, one tile ahead, and store the
 //     widened bf16 rows into the ring in the same layout (exact: a code has
 //     four significant bits).  No raw copy in shared memory is needed;
@@ -58,10 +58,14 @@ namespace pkv {
 namespace {
 
 constexpr int kDtSoftWarps = 8;      // two groups of four
-constexpr int kDtWidenWarps = 4;     // MXFP8 pools
+constexpr int kDtWidenWarps = 8;     // MXFP8 pools
 // ..., an MMA warp for each, producer, and for MXFP8 the widening warps
 constexpr int dt_threads(bool mx) { return (kDtSoftWarps + 3 + (mx ? kDtWidenWarps : 0)) * 32; }
 constexpr int kDtJob = 64;           // keys of a job
+// Columns of S that a softmax thread holds at once: a job's 64, or 32 (the
+// second 32's weights come first then, and the first 32 are read again) where
+// the widening warps leave fewer registers.
+constexpr int dt_chunk(bool mx) { return mx ? 32 : 64; }
 constexpr int kDtDescs = 8;          // stage descriptors in flight
 constexpr float kDtLn2 = 0.6931471805599453f;
 
@@ -516,7 +520,8 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
         const uint64_t vd = vdesc + sl * (L::kTile >> 4) + ((q & kSecond) ? (8 * kGroupBytes) >> 4 : 0);
 #pragma unroll
         for (int k = 0; k < kDtJob / 16; ++k)
-          tc::mma_bf16_ta(tO, tS + b * 64 + k * 8, vd + ((k * 2 * kGroupBytes) >> 4), kIdPV,
+          tc::mma_bf16_ta(tO, tS + b * 64 + (dt_chunk(kMx) == 64 ? k * 8 : (k >> 1) * 32 + (k & 1) * 8),
+                          vd + ((k * 2 * kGroupBytes) >> 4), kIdPV,
                           (k > 0 || !(q & kFirst)) ? 1u : 0u);
         tc::commit(&pvdone[x]);
         if (q & kFrees) tc::commit(&freeb[sl]);
@@ -642,46 +647,58 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
           tc::fence_after_sync();
           if (warp_live) {
             const uint32_t tS = tSx + b * 64;
-            uint32_t v[64];
-            auto& v0 = *reinterpret_cast<uint32_t(*)[32]>(v);
-            auto& v1 = *reinterpret_cast<uint32_t(*)[32]>(v + 32);
-            tc::tmem_ld32(tS, v0);
-            tc::tmem_ld32(tS + 32, v1);
-            tc::wait_ld32(v0);
-            tc::wait_ld32(v1);
-            if (fl & kDtTail) {
+            constexpr int kChunk = dt_chunk(kMx), kChunks = kDtJob / kChunk;
+            uint32_t v[kChunk];
+            auto read = [&](int w) {
 #pragma unroll
-              for (int w = 0; w < 2; ++w) {
-                const uint32_t bits = mask_word(mask, mb, 2 * u + w);
+              for (int q = 0; q < kChunk / 32; ++q)
+                tc::tmem_ld32(tS + kChunk * w + 32 * q, *reinterpret_cast<uint32_t(*)[32]>(v + 32 * q));
 #pragma unroll
-                for (int i = 0; i < 32; ++i)
-                  if (!((bits >> i) & 1u)) v[32 * w + i] = __float_as_uint(-INFINITY);
+              for (int q = 0; q < kChunk / 32; ++q) tc::wait_ld32(*reinterpret_cast<uint32_t(*)[32]>(v + 32 * q));
+              if (fl & kDtTail) {
+#pragma unroll
+                for (int q = 0; q < kChunk / 32; ++q) {
+                  const uint32_t bits = mask_word(mask, mb, 2 * u + w * (kChunk / 32) + q);
+#pragma unroll
+                  for (int i = 0; i < 32; ++i)
+                    if (!((bits >> i) & 1u)) v[32 * q + i] = __float_as_uint(-INFINITY);
+                }
               }
-            }
+            };
             float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int i = 0; i < 64; i += 2)
-              mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            for (int w = 0; w < kChunks; ++w) {
+              read(w);
+#pragma unroll
+              for (int i = 0; i < kChunk; i += 2)
+                mx4[(i >> 1) & 3] = max3(mx4[(i >> 1) & 3], __uint_as_float(v[i]), __uint_as_float(v[i + 1]));
+            }
             const float mx = cs * fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
             const float m_new = fmaxf(m, mx);
             const bool need = live && m_new > m + 8.0f;
             const float alpha = need ? exp2f(m - m_new) : 1.f;
             if (need) m = m_new;
             const float nm = m == -INFINITY ? 0.f : -m;  // nothing seen yet: every weight is 0
-            // ---- P = exp2(c s - m) in bf16 pairs; the sums take it unrounded
-            uint32_t pw[32];
+            // ---- P = exp2(c s - m) in bf16 pairs, over the first half of its
+            // S's columns; the sums take it unrounded
             float2 ls4[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) ls4[i] = make_float2(0.f, 0.f);
 #pragma unroll
-            for (int i = 0; i < 32; ++i) {
-              const float p0 = exp2f(fmaf(__uint_as_float(v[2 * i]), cs, nm));
-              const float p1 = exp2f(fmaf(__uint_as_float(v[2 * i + 1]), cs, nm));
-              ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(p0, p1));
-              const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
-              pw[i] = *reinterpret_cast<const uint32_t*>(&b2);
+            for (int w = kChunks - 1; w >= 0; --w) {
+              if (w < kChunks - 1) read(w);
+              uint32_t pw[kChunk / 2];
+#pragma unroll
+              for (int i = 0; i < kChunk / 2; ++i) {
+                const float p0 = exp2f(fmaf(__uint_as_float(v[2 * i]), cs, nm));
+                const float p1 = exp2f(fmaf(__uint_as_float(v[2 * i + 1]), cs, nm));
+                ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(p0, p1));
+                const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
+                pw[i] = *reinterpret_cast<const uint32_t*>(&b2);
+              }
+              if constexpr (kChunk == 64) tc::tmem_st32(tS, pw);
+              else tc::tmem_st16(tS + 32 * w, pw);
             }
-            tc::tmem_st32(tS, pw);
             const float2 ls2 = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
             l = l * alpha + (ls2.x + ls2.y);
             // a new base: once the group's previous PV has added to O under the

@@ -108,11 +108,25 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   return d;
 }
 
-// Whether any of 16 E4M3 codes is a NaN: its lower seven bits are all set.
-__device__ __forceinline__ bool nan_codes(const uint4& x) {
+// A scale group's E4M3 codes.
+struct Codes {
+  uint32_t w[8];
+};
+
+// Whether any of them is a NaN: its lower seven bits are all set.
+__device__ __forceinline__ bool nan_codes(const Codes& x) {
   constexpr uint32_t kLow = 0x7f7f7f7fu, kOne = 0x01010101u;
-  return ((((x.x & kLow) + kOne) | ((x.y & kLow) + kOne) | ((x.z & kLow) + kOne) | ((x.w & kLow) + kOne)) &
-          0x80808080u) != 0;
+  uint32_t any = 0;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) any |= (x.w[i] & kLow) + kOne;
+  return (any & 0x80808080u) != 0;
+}
+
+// A group's codes (16-byte aligned), the second half before the first if `turned`.
+__device__ __forceinline__ Codes load_codes(const uint8_t* p, int turned) {
+  const uint4 lo = __ldg(reinterpret_cast<const uint4*>(p) + turned);
+  const uint4 hi = __ldg(reinterpret_cast<const uint4*>(p) + (turned ^ 1));
+  return Codes{{lo.x, lo.y, lo.z, lo.w, hi.x, hi.y, hi.z, hi.w}};
 }
 
 // Eight floats to a 32-byte aligned address: one whole sector a thread.
@@ -270,15 +284,12 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
       int good = 1;
       if (lane == 0) {
         try_q(false);
-        if (round > 0 && !mbar_test(&freeb[slot], (round - 1) & 1)) {
+        if (round > 0) {
           const uint64_t t0 = global_timer_ns();
-          good = 0;
-          do {
-            for (int i_ = 0; i_ < 64 && !good; ++i_) {
-              try_q(false);
-              good = mbar_test(&freeb[slot], (round - 1) & 1);
-            }
-          } while (!good && global_timer_ns() - t0 <= kWaitLimitNs);
+          while (q_wanted && !(good = mbar_test(&freeb[slot], (round - 1) & 1)) &&
+                 global_timer_ns() - t0 <= kWaitLimitNs)
+            try_q(false);
+          good = mbar_wait(&freeb[slot], (round - 1) & 1);
         }
       }
       return __shfl_sync(0xffffffffu, good, 0) != 0;
@@ -383,82 +394,93 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
   } else if (kMx && warp > kDtSoftWarps + 2) {
     // ============================================================ widening
     // A thread takes a scale group, 32 codes, of a row: step i of a tile covers
-    // rows kStep i .. of it.  The next tile's loads are out while a tile is
-    // widened.
+    // rows kStep i .. of it.  It takes its four chunks of eight codes in an
+    // order, `turn`, that puts the stores of eight threads in a row into eight
+    // bank groups.  The next tile's loads are out while a tile is widened.
     constexpr int kPerRow = D / 32, kStep = kDtWidenWarps * 32 / kPerRow, kSteps = kDraftKeys / kStep;
-    const int wt = t - (kDtSoftWarps + 3) * 32, g = wt % kPerRow, row0 = wt / kPerRow;
+    const int wt = t - (kDtSoftWarps + 3) * 32;
+    const int g = wt % kPerRow, row0 = wt / kPerRow, half = g >> 1, turn = (row0 & 3) ^ (2 * half);
     const int shift = (P & (P - 1)) == 0 ? 31 - __clz(P) : -1;  // of a power-of-two block size
-    int blk[kSteps], off[kSteps];  // of this thread's rows; blk -1: none
-    uint4 kx[kSteps][2], vx[kSteps][2];
+    int64_t at[kSteps], sat[kSteps];  // this thread's groups in the code planes (-1: none) and the scale planes
+    Codes kx[kSteps], vx[kSteps];
     uint32_t ksc[kSteps], vsc[kSteps];
-    int seq = -1, ctx = 0, kvh = 0;
+    int seq = -1, ctx = 0;
     auto places = [&](const int4& da, const int4& db) {
       if (da.x != seq) {
         seq = da.x;
         ctx = __ldg(a.ctx_lens + seq);
       }
-      kvh = a.row_tiles > 1 ? da.y / a.row_tiles : da.y;
-      const int t0 = ctx - db.x;
+      const int kvh = a.row_tiles > 1 ? da.y / a.row_tiles : da.y;
+      const int t0 = ctx - db.x + row0;
       const int32_t* table = a.block_tables + (int64_t)seq * a.max_blocks;
+      int blk[kSteps], off[kSteps];
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const int row = t0 + i * kStep + row0, bi = shift >= 0 ? row >> shift : row / P;
+        const int row = t0 + i * kStep, bi = shift >= 0 ? row >> shift : row / P;
         off[i] = row - bi * P;
         blk[i] = i * kStep + row0 < da.z ? __ldg(table + bi) : -2;
       }
 #pragma unroll
-      for (int i = 0; i < kSteps; ++i)
+      for (int i = 0; i < kSteps; ++i) {
+        const int64_t base = (int64_t)blk[i] * P * Hkv;  // rows of one head before the block
+        at[i] = (base + off[i] * Hkv + kvh) * (D / 32) + g;
+        sat[i] = (base + kvh * P + off[i]) * (D / 32) + g;
         if (blk[i] < 0 || (int64_t)blk[i] >= a.num_blocks) {
           if (blk[i] != -2 && g == 0) atomicOr(a.err, PKV_DEVERR_BLOCK);
-          blk[i] = -1;
-        }
-    };
-    auto fetch = [&](const void* pool, const uint8_t* scales, uint4 (&x)[kSteps][2], uint32_t (&sc)[kSteps]) {
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) {
-        x[i][0] = x[i][1] = make_uint4(0u, 0u, 0u, 0u);  // rows past the last one, and of bad blocks
-        sc[i] = 0;
-        if (blk[i] >= 0) {
-          const int64_t row = (int64_t)blk[i] * P * Hkv;  // rows of one head before the block
-          const uint4* at = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(pool) +
-                                                           (row + off[i] * Hkv + kvh) * D + g * 32);
-          x[i][0] = __ldg(at);
-          x[i][1] = __ldg(at + 1);
-          sc[i] = __ldg(scales + (row + kvh * P + off[i]) * (D / 32) + g);
+          at[i] = -1;
         }
       }
     };
-    auto widen = [&](int item, const uint4 (&x)[kSteps][2], const uint32_t (&sc)[kSteps]) {
-      unsigned char* tile = ring + (size_t)(item % kItems) * L::kTile;
+    auto fetch = [&](const void* pool, const uint8_t* scales, Codes (&x)[kSteps], uint32_t (&sc)[kSteps]) {
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
-        const int row = i * kStep + row0;
+        if (at[i] >= 0) {
+          x[i] = load_codes(static_cast<const uint8_t*>(pool) + at[i] * 32, half);
+          sc[i] = __ldg(scales + sat[i]);
+        } else {  // rows past the last one, and of bad blocks
+          x[i] = Codes{};
+          sc[i] = 0;
+        }
+      }
+    };
+    // its chunks' place in a tile: chunk q it takes goes to (q ^ turn) 16 from here on
+    const uint32_t dst = (row0 / kRowGroup) * kGroupBytes + half * 1024 + (row0 & 7) * 128 +
+                         ((((g & 1) * 4) ^ (row0 & 4)) << 4);
+    auto widen = [&](int item, const Codes (&x)[kSteps], const uint32_t (&sc)[kSteps]) {
+      unsigned char* tile = ring + (size_t)(item % kItems) * L::kTile + dst;
+      bool rare = false;
+#pragma unroll
+      for (int i = 0; i < kSteps; ++i) {
+        unsigned char* d = tile + i * (kStep / kRowGroup) * kGroupBytes;
         __nv_bfloat162 s1, s2;
         scale_factors(sc[i], 0, s1, s2);
-        const bool big = sc[i] > 134u;
-        // four 16-byte chunks of the bf16 row, from chunk 4 (g % 2) of its half
-        // g / 2 on; threads of the second half store theirs in another order,
-        // so that eight threads' stores fall into eight bank groups
-        unsigned char* d = tile + (row / kRowGroup) * kGroupBytes + (g >> 1) * 1024 + (row & 7) * 128;
-        const int flip = (g >> 1) << 1;
-        const uint32_t w[8] = {x[i][0].x, x[i][0].y, x[i][0].z, x[i][0].w,
-                               x[i][1].x, x[i][1].y, x[i][1].z, x[i][1].w};
-        uint4 v[4];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) v[q] = widen8(make_uint2(w[2 * q], w[2 * q + 1]), s1, s2, big);
+        for (int q = 0; q < 4; ++q)
+          *reinterpret_cast<uint4*>(d + ((q ^ turn) << 4)) =
+              widen8(make_uint2(x[i].w[2 * q], x[i].w[2 * q + 1]), s1, s2, false);
+        rare |= sc[i] > 134u || nan_codes(x[i]);
+      }
+      // Rare: the second factor of scales past 2^7, and the NaN codes
+      // s.1111.111, which widen8 takes for numbers, code by code, in few
+      // instructions: the warps' loops have to fit the instruction cache.
+      if (rare) {
+        Codes y[kSteps];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int ch = (g & 1) * 4 + (q ^ flip);
-          *reinterpret_cast<uint4*>(d + ((ch ^ (row & 7)) << 4)) = flip ? v[q ^ 2] : v[q];
-        }
-        if (nan_codes(x[i][0]) || nan_codes(x[i][1])) {  // widen8 takes the NaN codes s.1111.111 for numbers
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
+        for (int i = 0; i < kSteps; ++i) y[i] = x[i];
 #pragma unroll 1
-            for (int b = 0; b < 4; ++b)
-              if (((w[q] >> (8 * b)) & 0x7fu) == 0x7fu)
-                *reinterpret_cast<uint16_t*>(d + ((((g & 1) * 4 + (q >> 1)) ^ (row & 7)) << 4) +
-                                             ((q & 1) * 4 + b) * 2) = 0x7fffu;
+        for (int n = 0; n < 32; ++n) {
+#pragma unroll
+          for (int i = 0; i < kSteps; ++i) {
+            const uint32_t code = y[i].w[0] & 0xffu, at16 = place2(code);
+            __nv_bfloat162 s1, s2;
+            scale_factors(sc[i], 0, s1, s2);
+            const __nv_bfloat162 v = __hmul2(__hmul2(*reinterpret_cast<const __nv_bfloat162*>(&at16), s1), s2);
+            *reinterpret_cast<uint16_t*>(tile + i * (kStep / kRowGroup) * kGroupBytes +
+                                         (((n >> 3) ^ turn) << 4) + (n & 7) * 2) =
+                (code & 0x7fu) == 0x7fu ? (uint16_t)0x7fffu : __bfloat16_as_ushort(__low2bfloat16(v));
+#pragma unroll
+            for (int w = 0; w < 8; ++w) y[i].w[w] = __funnelshift_r(y[i].w[w], w < 7 ? y[i].w[w + 1] : 0u, 8);
+          }
         }
       }
       tc::fence_proxy_async_smem();

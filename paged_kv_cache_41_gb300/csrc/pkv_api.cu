@@ -930,7 +930,7 @@ pkv_status pkv_draft_tree_attention(
     // one row tile (16 requests, trees of 5 to 27) and 3.4 with two (64
     // requests, trees of 64).
     a.stage_units = 2;
-    a.piece_units = w.tiles > 1 ? 7 : 2;
+    a.piece_units = cache->dtype == PKV_MXFP8 ? 1 : w.tiles > 1 ? 7 : 2;
     a.q_tokens = max_draft < pkv::kDraftRows / G ? max_draft : pkv::kDraftRows / G;
     const int box = pkv::draft_tc_box_rows(cache->block_size);
     CUtensorMap tmq, tmk, tmv;

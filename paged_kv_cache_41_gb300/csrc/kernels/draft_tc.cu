@@ -757,7 +757,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
                 for (int hf = 0; hf < H; ++hf)
 #pragma unroll 2
                   for (int ch = 0; ch < 8; ++ch) {
-                    uint4* at = reinterpret_cast<uint4*>(vr + hf * 1024 + ch * 16);
+                    uint4* at = reinterpret_cast<uint4*>(vr + hf * 1024 + (ch ^ (row & 7)) * 16);  // other banks than the next rows'
                     if (row >= nvalid) {
                       *at = make_uint4(0u, 0u, 0u, 0u);
                       continue;

@@ -824,6 +824,7 @@ struct DraftWorkspace {
   int32_t splits;             // CUDA cores
   int32_t tiles, row_tiles;   // tensor cores: 128-row tiles of a segment, segments per kv head
   int32_t ctas;
+  int32_t stage_units, piece_units;
   size_t cut_off, lse_off, o_off, total;
 };
 
@@ -835,11 +836,20 @@ DraftWorkspace draft_workspace(const pkv_cache_desc* c, int32_t num_seqs, int32_
     w.tiles = rows > pkv::kDraftRows ? 2 : 1;
     const int per = w.tiles * pkv::kDraftRows;
     w.row_tiles = (rows + per - 1) / per;
+    // Work units (kernels/plan.cuh).  A least-squares fit of the CTAs' times
+    // gave a piece (its Q, the drained pipeline, its outputs) 0.8 stages with
+    // one row tile (16 requests, trees of 5 to 27) and 3.4 with two (64
+    // requests, trees of 64); an MXFP8 pool's stages take five times as long.
+    w.stage_units = 2;
+    w.piece_units = c->dtype == PKV_MXFP8 ? 1 : w.tiles > 1 ? 7 : 2;
+    // As many CTAs as make a share one stage, where that is fewer than the SMs:
+    // a CTA less gives some two (one sequence of 304 rows: 14.7 us, 13.0 so).
     const int64_t keys = (int64_t)max_blocks * c->block_size;
-    const int64_t stages = (int64_t)num_seqs * c->num_kv_heads * w.row_tiles *
-                           ((keys + pkv::kDraftKeys - 1) / pkv::kDraftKeys);
+    const int64_t nt = (keys + pkv::kDraftKeys - 1) / pkv::kDraftKeys;
+    const int64_t shares = (int64_t)num_seqs * c->num_kv_heads * w.row_tiles *
+                           ((nt * w.stage_units + w.piece_units + w.stage_units - 1) / w.stage_units);
     const int64_t sms = sm_count();
-    w.ctas = (int32_t)(stages < sms ? stages : sms);
+    w.ctas = (int32_t)(shares < sms ? shares : sms);
     const int64_t recs = 2 * (int64_t)w.ctas * per;
     w.cut_off = align256((size_t)(num_seqs + 1) * 8);
     w.lse_off = w.cut_off + align256((size_t)w.ctas * 8);
@@ -925,12 +935,8 @@ pkv_status pkv_draft_tree_attention(
     const int G = num_q_heads / cache->num_kv_heads;
     a.num_ctas = w.ctas;
     a.row_tiles = w.row_tiles;
-    // Work units (kernels/plan.cuh).  A least-squares fit of the CTAs' times
-    // gave a piece (its Q, the drained pipeline, its outputs) 0.8 stages with
-    // one row tile (16 requests, trees of 5 to 27) and 3.4 with two (64
-    // requests, trees of 64).
-    a.stage_units = 2;
-    a.piece_units = cache->dtype == PKV_MXFP8 ? 1 : w.tiles > 1 ? 7 : 2;
+    a.stage_units = w.stage_units;
+    a.piece_units = w.piece_units;
     a.q_tokens = max_draft < pkv::kDraftRows / G ? max_draft : pkv::kDraftRows / G;
     const int box = pkv::draft_tc_box_rows(cache->block_size);
     CUtensorMap tmq, tmk, tmv;

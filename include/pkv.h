@@ -58,6 +58,8 @@
  *     and Hq / Hkv <= 4, on the tensor cores (tiles widened to bf16 in shared
  *     memory) for head_dim 128 and Hq / Hkv = 8 with block_size 16, 32, 64,
  *     128 or 256; other group sizes return PKV_ERR_UNSUPPORTED.  The
+ *     decode that weighs rows goes with the decode; the attention of drafted
+ *     tokens and the compaction take them in every shape.  The
  *     shared-prefix kernel and the chunk-first phase take bf16 only (a tree
  *     over MXFP8 pools runs sequence-first).
  *   - Pointers to the caches, q, k, v and out must be 16-byte aligned.
@@ -442,7 +444,8 @@ size_t pkv_draft_tree_workspace_bytes(const pkv_cache_desc* cache, int32_t num_s
  * or ends beyond its block table row sets PKV_DEVERR_LENGTH and its query
  * rows are not written.
  * Supported: block_size 16 or a multiple of 32 up to 256; head_dim 64 or 128;
- * Hq / Hkv in {1, 2, 4, 8}; num_seqs <= 65535; every cache dtype. */
+ * Hq / Hkv in {1, 2, 4, 8}; num_seqs <= 65535; every cache dtype (bf16: num_blocks
+ * * block_size / 8 within int32). */
 pkv_status pkv_draft_tree_attention(
     const pkv_cache_desc* cache, void* out, float* lse, const void* q, const void* k_cache,
     const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
@@ -462,7 +465,8 @@ pkv_status pkv_draft_tree_attention(
  * compaction row j of two kv heads may hold different tokens. */
 
 /* Bytes of device workspace pkv_paged_attention_decode_weights needs; 0 for
- * unsupported or invalid sizes. */
+ * unsupported or invalid sizes.  Beside the decode's it holds a score for
+ * every row and query head: 4 Hq bytes a row of the table's full length. */
 size_t pkv_decode_weights_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
                                           int32_t num_q_heads, int32_t max_blocks_per_seq);
 
@@ -480,8 +484,8 @@ size_t pkv_decode_weights_workspace_bytes(const pkv_cache_desc* cache, int32_t n
  *                   sets PKV_DEVERR_LENGTH and its rows past it are not
  *                   weighed.
  *   decay:          finite; 1 keeps a plain sum.
- * A row of a block id outside the pool is not weighed.  Other arguments,
- * support and errors as in pkv_paged_attention_decode (partition_size 0). */
+ * What the rows of a block id outside the pool (PKV_DEVERR_BLOCK) add to their
+ * own scores is unspecified.  Other arguments, support and errors as in pkv_paged_attention_decode (partition_size 0). */
 pkv_status pkv_paged_attention_decode_weights(
     const pkv_cache_desc* cache, void* out, float* lse, float* weights, int64_t weights_stride,
     float decay, const void* q, const void* k_cache, const void* v_cache,
@@ -521,11 +525,11 @@ pkv_status pkv_kv_evict_select(const float* weights, int64_t weights_stride,
  *               keep[j] >= j; entries from keep_lens[r] on are never read.
  *   keep_heads: 1 or num_kv_heads.
  *   keep_lens:  int32 [num_seqs].
- * The blocks written to must belong to one sequence alone: copy shared ones on
- * write first (pkv_kv_block_copy).  An entry that is out of range or order
+ * The K and V pools must not overlap, and the blocks written to must belong to
+ * one sequence alone: copy shared ones on write first (pkv_kv_block_copy).  An entry that is out of range or order
  * sets PKV_DEVERR_KEEP, one in a block id outside the pool PKV_DEVERR_BLOCK;
  * such rows are not moved.  A sequence with keep_lens[r] outside [0,
- * seq_lens[r] - base], base outside [0, seq_lens[r]], or (with weights) more
+ * min(keep_stride, seq_lens[r] - base)], base outside [0, seq_lens[r]], or (with weights) more
  * rows than weights_stride sets PKV_DEVERR_LENGTH and is skipped.
  * Bit-exact.  Any block_size; head_dim x element a multiple of 16 bytes, 16 KiB
  * at most (MXFP8: head_dim a multiple of 32); fewer than 2^32 - 1 pool rows.

@@ -1,5 +1,5 @@
-// draft.cu -- attention of drafted tokens over a paged cache, on the CUDA
-// cores (every cache type).
+// draft.cu -- attention of drafted tokens over a paged fp32 cache, on the CUDA
+// cores.  (bf16 and MXFP8 pools: draft_tc.cu, on the tensor cores.)
 //
 // What it computes: sequence r holds ctx committed token rows and n drafted
 // ones behind them (positions ctx .. ctx + n - 1, already in the cache).
@@ -12,7 +12,7 @@
 // Design:
 //   * a CTA takes kRT * 8 (token, query head) rows of one kv head -- all the
 //     G heads of a token share its K/V -- and one contiguous split of the
-//     sequence's rows, 32 at a time, widened to fp32 in shared memory;
+//     sequence's rows, 32 at a time, in shared memory;
 //   * thread (rg, kg) of 8 x 16 holds the scores of rows rg kRT .. and keys
 //     kg, kg + 16, and the outputs of those rows at D / 16 columns;
 //   * splits leave (O, LSE) states that a second kernel merges by
@@ -20,8 +20,8 @@
 //   * a hidden row's weight is stored as -1 and skipped, not multiplied, so
 //     an infinity or NaN in it cannot leak; rows past the last drafted one
 //     are never read.
-// The fp32 FMAs bound it: 256 per (row, key) at head_dim 128, where the
-// tensor cores would need bf16 operands.
+// The fp32 FMAs bound it, 256 per (row, key) at head_dim 128: fp32 operands
+// would lose 16 bits on the tensor cores.  SIMT_US
 #include <math.h>
 
 #include "draft.cuh"
@@ -34,21 +34,6 @@ constexpr int kDsThreads = 128;
 constexpr int kDsKeys = 32;  // keys per tile
 constexpr float kDsLn2 = 0.6931471805599453f;
 
-// Eight consecutive elements of a cache row as fp32.
-template <typename T>
-__device__ __forceinline__ void load8(const T* p, float (&f)[8]) {
-  VecLoad<T, 8>::run(p, f);
-}
-
-template <typename T>
-struct DraftIo {
-  using type = T;
-};
-template <>
-struct DraftIo<__nv_fp8_e4m3> {
-  using type = __nv_bfloat16;
-};
-
 template <int D, int kRT>
 constexpr int draft_simt_smem() {
   return (8 * kRT * (D + 4) + kDsKeys * (D + 4) + kDsKeys * D + 8 * kRT * (kDsKeys + 1)) * 4 +
@@ -57,10 +42,8 @@ constexpr int draft_simt_smem() {
 
 }  // namespace
 
-template <typename T, int D, int kRT>
+template <int D, int kRT>
 __global__ void __launch_bounds__(kDsThreads) draft_simt_kernel(const DraftArgs a) {
-  using TQ = typename DraftIo<T>::type;
-  constexpr bool kMx = sizeof(T) == 1;
   constexpr int R = 8 * kRT;       // query rows per CTA
   constexpr int LD = D + 4;        // padded shared rows of Q and K
   constexpr int CPT = D / 16;      // output columns per thread
@@ -92,7 +75,8 @@ __global__ void __launch_bounds__(kDsThreads) draft_simt_kernel(const DraftArgs 
     float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
     if (row < rows) {
       const int tok = (row_lo + row) / G, g = (row_lo + row) % G;
-      load8(static_cast<const TQ*>(a.q) + ((int64_t)(s.row0 + tok) * a.num_q_heads + h * G + g) * D + c, f);
+      VecLoad<float, 8>::run(static_cast<const float*>(a.q) + ((int64_t)(s.row0 + tok) * a.num_q_heads + h * G + g) * D + c,
+                            f);
     }
 #pragma unroll
     for (int e = 0; e < 8; ++e) qs[row * LD + c + e] = f[e] * a.qscale;
@@ -116,17 +100,8 @@ __global__ void __launch_bounds__(kDsThreads) draft_simt_kernel(const DraftArgs 
         const int blk = __ldg(a.block_tables + (int64_t)r * a.max_blocks + t / P);
         if (blk >= 0 && (int64_t)blk < a.num_blocks) {
           const int64_t at = (((int64_t)blk * P + t % P) * Hkv + h) * D + c;
-          load8(static_cast<const T*>(a.k) + at, kf);
-          load8(static_cast<const T*>(a.v) + at, vf);
-          if constexpr (kMx) {
-            const int64_t sc = (((int64_t)blk * Hkv + h) * P + t % P) * (D / 32) + c / 32;
-            const float ks_ = e8m0_value(__ldg(a.k_scales + sc)), vs_ = e8m0_value(__ldg(a.v_scales + sc));
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-              kf[e] *= ks_;
-              vf[e] *= vs_;
-            }
-          }
+          VecLoad<float, 8>::run(static_cast<const float*>(a.k) + at, kf);
+          VecLoad<float, 8>::run(static_cast<const float*>(a.v) + at, vf);
         } else if (c == 0) {
           atomicOr(a.err, PKV_DEVERR_BLOCK);
         }
@@ -211,7 +186,7 @@ __global__ void __launch_bounds__(kDsThreads) draft_simt_kernel(const DraftArgs 
     if (a.num_splits == 1) {
 #pragma unroll
       for (int c = 0; c < CPT; ++c)
-        store_out(static_cast<TQ*>(a.out) + qh * D + c * 16 + kg, o[i][c] * inv);
+        static_cast<float*>(a.out)[qh * D + c * 16 + kg] = o[i][c] * inv;
       if (kg == 0 && a.lse_out) a.lse_out[qh] = lse2 * kDsLn2;
     } else {
       // states by (sequence, drafted row, head), whatever query row that is
@@ -224,7 +199,7 @@ __global__ void __launch_bounds__(kDsThreads) draft_simt_kernel(const DraftArgs 
 }
 
 // One warp per (sequence, drafted row, head): merge the row's split states.
-template <typename TQ, int D>
+template <int D>
 __global__ void __launch_bounds__(128) draft_simt_merge_kernel(const DraftArgs a) {
   constexpr int EPL = D / 32;
   pdl_wait();
@@ -255,15 +230,14 @@ __global__ void __launch_bounds__(128) draft_simt_merge_kernel(const DraftArgs a
   const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll
   for (int e = 0; e < EPL; ++e)
-    store_out(static_cast<TQ*>(a.out) + qh * D + lane * EPL + e, acc[e] * inv);
+    static_cast<float*>(a.out)[qh * D + lane * EPL + e] = acc[e] * inv;
   if (lane == 0 && a.lse_out) a.lse_out[qh] = L == 0.f ? -INFINITY : (M + log2f(L)) * kDsLn2;
 }
 
-template <typename T, int D, int kRT>
+template <int D, int kRT>
 static cudaError_t launch_draft_simt_t(const DraftArgs& a, cudaStream_t stream) {
-  using TQ = typename DraftIo<T>::type;
   constexpr int smem = draft_simt_smem<D, kRT>() + 16;
-  auto kern = draft_simt_kernel<T, D, kRT>;
+  auto kern = draft_simt_kernel<D, kRT>;
   static SmemAttrCache attr_cache;
   cudaError_t e = ensure_smem_limit(kern, smem, attr_cache);
   if (e != cudaSuccess) return e;
@@ -272,27 +246,17 @@ static cudaError_t launch_draft_simt_t(const DraftArgs& a, cudaStream_t stream) 
   e = launch_pdl(kern, dim3((unsigned)a.num_splits, (unsigned)(a.num_kv_heads * tiles), (unsigned)a.num_seqs),
                  dim3(kDsThreads), smem, stream, a);
   if (e != cudaSuccess || a.num_splits == 1) return e;
-  return launch_pdl(draft_simt_merge_kernel<TQ, D>,
+  return launch_pdl(draft_simt_merge_kernel<D>,
                     dim3((unsigned)((a.max_draft * a.num_q_heads + 3) / 4), (unsigned)a.num_seqs), dim3(128), 0,
                     stream, a);
 }
 
-template <typename T>
-static cudaError_t launch_draft_simt_d(int head_dim, const DraftArgs& a, cudaStream_t stream) {
-  const int rows = a.max_draft * (a.num_q_heads / a.num_kv_heads);
-  if (head_dim == 128)
-    return rows <= 8 ? launch_draft_simt_t<T, 128, 1>(a, stream) : launch_draft_simt_t<T, 128, 4>(a, stream);
-  return rows <= 8 ? launch_draft_simt_t<T, 64, 1>(a, stream) : launch_draft_simt_t<T, 64, 4>(a, stream);
-}
-
 int draft_simt_rows(int rows) { return rows <= 8 ? 8 : 32; }
 
-cudaError_t launch_draft_simt(int dtype, int head_dim, const DraftArgs& a, cudaStream_t stream) {
-  switch (dtype) {
-    case PKV_F32: return launch_draft_simt_d<float>(head_dim, a, stream);
-    case PKV_BF16: return launch_draft_simt_d<__nv_bfloat16>(head_dim, a, stream);
-    default: return launch_draft_simt_d<__nv_fp8_e4m3>(head_dim, a, stream);
-  }
+cudaError_t launch_draft_simt(int head_dim, const DraftArgs& a, cudaStream_t stream) {
+  const int rows = a.max_draft * (a.num_q_heads / a.num_kv_heads);
+  if (head_dim == 128) return rows <= 8 ? launch_draft_simt_t<128, 1>(a, stream) : launch_draft_simt_t<128, 4>(a, stream);
+  return rows <= 8 ? launch_draft_simt_t<64, 1>(a, stream) : launch_draft_simt_t<64, 4>(a, stream);
 }
 
 }  // namespace pkv

@@ -291,7 +291,7 @@ __host__ __device__ constexpr int draft_tc_box_rows(int block_size) {
 cudaError_t launch_draft_tc(int dtype, int head_dim, int tiles, const CUtensorMap& tmq,
                             const CUtensorMap& tmk, const CUtensorMap& tmv, const DraftArgs& args,
                             cudaStream_t stream);
-cudaError_t launch_draft_simt(int dtype, int head_dim, const DraftArgs& args, cudaStream_t stream);
+cudaError_t launch_draft_simt(int head_dim, const DraftArgs& args, cudaStream_t stream);
 // (token, query head) rows per CTA where a kv head has `rows` of them at most.
 int draft_simt_rows(int rows);
 

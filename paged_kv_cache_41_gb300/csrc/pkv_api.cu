@@ -796,6 +796,9 @@ pkv_status check_draft(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_
   if (plain.dtype == PKV_MXFP8) plain.dtype = PKV_BF16;
   pkv_status st = check_attention_shape(&plain, num_q_heads);
   if (st != PKV_OK) return st;
+  // a bf16 pool's row groups are addressed with int32 coordinates
+  if (c->dtype == PKV_BF16 && (int64_t)c->num_blocks * (c->block_size / pkv::kRowGroup) > INT32_MAX)
+    return PKV_ERR_UNSUPPORTED;
   return num_seqs > 65535 ? PKV_ERR_UNSUPPORTED : PKV_OK;
 }
 
@@ -812,13 +815,8 @@ int32_t draft_splits(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_he
   return (int32_t)(s < 1 ? 1 : s);
 }
 
-// fp32 pools run on the CUDA cores, the others on the tensor cores (a bf16
-// pool's row groups are addressed with int32 coordinates).
-bool draft_on_tc(const pkv_cache_desc* c) {
-  if (c->dtype == PKV_MXFP8) return true;
-  return c->dtype == PKV_BF16 &&
-         (int64_t)c->num_blocks * (c->block_size / pkv::kRowGroup) <= INT32_MAX;
-}
+// fp32 pools run on the CUDA cores, the others on the tensor cores.
+bool draft_on_tc(const pkv_cache_desc* c) { return c->dtype != PKV_F32; }
 
 struct DraftWorkspace {
   int32_t splits;             // CUDA cores
@@ -949,7 +947,7 @@ pkv_status pkv_draft_tree_attention(
       return st;
     e = pkv::launch_draft_tc(cache->dtype, cache->head_dim, w.tiles, tmq, tmk, tmv, a, as_stream(stream));
   } else {
-    e = pkv::launch_draft_simt(cache->dtype, cache->head_dim, a, as_stream(stream));
+    e = pkv::launch_draft_simt(cache->head_dim, a, as_stream(stream));
   }
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
@@ -1069,8 +1067,8 @@ pkv_status pkv_kv_compact(const pkv_cache_desc* cache, void* k_cache, void* v_ca
   if (num_seqs < 0 || max_blocks_per_seq <= 0 || keep_stride < 0 ||
       (keep_heads != 1 && keep_heads != cache->num_kv_heads) || (weights && weights_stride < 1))
     return PKV_ERR_INVALID_ARG;
-  if (num_seqs == 0 || keep_stride == 0) return PKV_OK;
-  if (!k_cache || !v_cache || !block_tables || !seq_lens || !keep || !keep_lens)
+  if (num_seqs == 0 || (keep_stride == 0 && !weights)) return PKV_OK;  // else weights to clear
+  if (!k_cache || !v_cache || !block_tables || !seq_lens || (!keep && keep_stride > 0) || !keep_lens)
     return PKV_ERR_INVALID_ARG;
   if (!aligned16(k_cache) || !aligned16(v_cache)) return PKV_ERR_INVALID_ARG;
   if (num_seqs > 65535 || cache->num_kv_heads > 65535 || cache->num_blocks > INT32_MAX)
@@ -1079,6 +1077,11 @@ pkv_status pkv_kv_compact(const pkv_cache_desc* cache, void* k_cache, void* v_ca
   if (row_bytes % 16 != 0 || row_bytes > 16384) return PKV_ERR_UNSUPPORTED;
   if (cache->num_blocks * cache->block_size >= (int64_t)UINT32_MAX) return PKV_ERR_UNSUPPORTED;
   if (cache->dtype == PKV_MXFP8 && cache->head_dim % 32 != 0) return PKV_ERR_UNSUPPORTED;
+  // chains of K and of V run side by side: in one place they would race
+  const uintptr_t k_at = reinterpret_cast<uintptr_t>(k_cache), v_at = reinterpret_cast<uintptr_t>(v_cache);
+  const uintptr_t pool_bytes = (uintptr_t)cache->num_blocks * cache->block_size * cache->num_kv_heads *
+                               (row_bytes + (cache->dtype == PKV_MXFP8 ? cache->head_dim / 32 : 0));
+  if ((k_at > v_at ? k_at - v_at : v_at - k_at) < pool_bytes) return PKV_ERR_INVALID_ARG;
   unsigned int* err = device_error_word();
   if (!err) return PKV_ERR_CUDA;
   pkv::CompactArgs a{};

@@ -246,6 +246,24 @@ def test_select_ties_and_special_values(kind, n):
         run_select(w, [n, n - 5], budget, min(2, budget // 2), min(5, budget // 2))
 
 
+@pytest.mark.parametrize("n,budget,sinks,recent", [
+    (196609, 9000, 4, 64), (393216, 200000, 0, 1000), (393217, 20000, 16, 64), (500001, 499999, 1, 1)])
+def test_select_lengths_past_one_cta_and_past_a_cluster(n, budget, sinks, recent):
+    rng = np.random.default_rng(n)
+    w = np.exp(2 * rng.standard_normal((2, 2, n))).astype(np.float32)
+    run_select(w, [n, n - 3], budget, sinks, recent)
+
+
+@pytest.mark.parametrize("kind", ["equal", "special"])
+def test_select_ties_past_a_cluster(kind):
+    n = 400003
+    rng = np.random.default_rng(15)
+    w = (np.full((1, 2, n), 0.5) if kind == "equal" else
+         rng.choice([np.nan, np.inf, -np.inf, 0.0, -0.0, 1e-42, -1e-42, 1.0, 3.4e38], (1, 2, n)))
+    for budget in (1, n // 3, n - 1):
+        run_select(np.ascontiguousarray(w, dtype=np.float32), [n], budget, min(2, budget // 2), min(5, budget // 2))
+
+
 def test_select_forced_rows_fill_the_budget():
     w = np.random.default_rng(6).random((2, 2, 400)).astype(np.float32)
     run_select(w, [400, 21], 20, 13, 7)
@@ -411,6 +429,12 @@ def test_compact_accepted_paths():
     Compact((base + n).tolist(), acc, base=base, per_head=False, d=128, hkv=4, weights=False,
             seed=3).run()
     Compact((base + n).tolist(), acc, base=base, per_head=True, d=128, hkv=4, seed=3).run()
+
+
+def test_compact_to_nothing_clears_the_scores():
+    for pad in (0, 2):  # a list with no room, and one of which nothing is used
+        Compact([50, 7], [0, 0], pad=pad, seed=11).run()
+        Compact([50, 7], [0, 0], pad=pad, base=[20, 7], seed=11).run()
 
 
 def test_compact_long():

@@ -116,6 +116,20 @@ def test_compact_arguments(lib, kw, want):
     assert compact(lib, **kw) == want
 
 
+def test_compact_refuses_pools_that_overlap(lib):
+    c = desc()  # 64 * 16 * 2 * 64 bf16 elements: 262144 bytes a pool
+    for off in (0, 16, 262144 - 16):
+        assert compact(lib, c=c, k=A, v=P((1 << 20) + off)) == BAD
+        assert compact(lib, c=c, k=P((1 << 20) + off), v=A) == BAD
+    mx = desc(dtype=pkv.PKV_MXFP8)  # 131072 codes, 4096 scales
+    assert compact(lib, c=mx, k=A, v=P((1 << 20) + 131072)) == BAD
+
+
+def test_draft_refuses_a_bf16_pool_past_its_coordinates(lib):
+    assert draft(lib, c=desc(nb=2**30 + 8)) == UNSUP
+    assert lib.pkv_draft_tree_workspace_bytes(ctypes.byref(desc(nb=2**30 + 8)), 2, 4, 3, 4) == 0
+
+
 # ------------------------------------------------------------ the binding
 def host(nb=8, p=16, hkv=2, d=64, dtype=torch.bfloat16):
     return torch.zeros(nb, p, hkv, d, dtype=dtype)

@@ -275,31 +275,21 @@ __global__ void __launch_bounds__(kThreads, 2048 / kThreads) evict_select_cluste
       unsigned long long* to = cs > 1 ? cluster.map_shared_rank(list, 0) : list;
       uint32_t* nl = cs > 1 ? cluster.map_shared_rank(&listed, 0) : &listed;
 #pragma unroll 1
-      for (int i = 0; i < n; ++i) {  // a warp claims its places of 128 rows at once
+      for (int i = 0; i < n; ++i) {
         const int at = at0 + 128 * i;
-        uint32_t m = 0, v[4] = {0, 0, 0, 0};
-        if (at < len) {
-          const uint4 x = *reinterpret_cast<const uint4*>(keys + at);
-          v[0] = x.x, v[1] = x.y, v[2] = x.z, v[3] = x.w;
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if ((v[q] >> bits_left) == prefix && at + q < len) m |= 1u << q;
-        }
-        if (!__any_sync(0xffffffffu, m != 0)) continue;
-        const uint32_t mine = __popc(m);
-        uint32_t inc = mine;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t y = __shfl_up_sync(0xffffffffu, inc, o);
-          if (lane >= o) inc += y;
-        }
-        uint32_t place = 0;
-        if (lane == 31) place = atomicAdd(nl, inc);
-        place = __shfl_sync(0xffffffffu, place, 31) + inc - mine;
+        if (at >= len) break;
+        const uint4 x = *reinterpret_cast<const uint4*>(keys + at);
+        const uint32_t v[4] = {x.x, x.y, x.z, x.w};
+        uint32_t m = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if ((m >> q) & 1u)
-            to[place++] = ((unsigned long long)v[q] << 32) | (uint32_t)~(first + at + q);
+          if ((v[q] >> bits_left) == prefix && at + q < len) m |= 1u << q;
+        if (m) {
+          uint32_t place = atomicAdd(nl, (uint32_t)__popc(m));
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if ((m >> q) & 1u) to[place++] = ((unsigned long long)v[q] << 32) | (uint32_t)~(first + at + q);
+        }
       }
       meet();
       if (rank == 0 && tid < in_bin) {

@@ -124,7 +124,7 @@ constexpr uint32_t kScForced = 0xffffffffu;  // the key of a row kept for certai
 // Warp w of the cluster's CTA `rank` holds a contiguous run of its slice, 128
 // consecutive rows at a time, four a lane.
 template <int kThreads>
-__global__ void __launch_bounds__(kThreads, 2048 / kThreads) evict_select_cluster_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kThreads, kThreads == 256 ? 5 : 2) evict_select_cluster_kernel(const SelectArgs a) {
   constexpr int kWarps = kThreads / 32;
   extern __shared__ __align__(16) uint32_t keys[];  // this CTA's slice, padded with key 0
   __shared__ __align__(16) uint32_t hist[kScBins];  // of its keys, largest digit first
@@ -182,6 +182,15 @@ __global__ void __launch_bounds__(kThreads, 2048 / kThreads) evict_select_cluste
   for (int i = 0; i < n; ++i) {
     const int at = at0 + 128 * i;
     if (at >= len) break;
+    const int run = first + at - 4 * lane;  // the warp's 128 rows: all of them candidates, as a rule
+    if (wide && run >= lo && run + 128 <= hi && run + 128 <= first + len) {
+      const uint4 x = __ldg(reinterpret_cast<const uint4*>(w + at));
+      const uint32_t v[4] = {weight_key(x.x), weight_key(x.y), weight_key(x.z), weight_key(x.w)};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) atomicAdd(&hist[kScBins - 1 - (v[q] >> 21)], 1u);
+      *reinterpret_cast<uint4*>(keys + at) = make_uint4(v[0], v[1], v[2], v[3]);
+      continue;
+    }
     uint4 x;
     if (wide && at + 3 < len) {
       x = __ldg(reinterpret_cast<const uint4*>(w + at));
@@ -283,7 +292,8 @@ __global__ void __launch_bounds__(kThreads, 2048 / kThreads) evict_select_cluste
         uint32_t m = 0;
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          if ((v[q] >> bits_left) == prefix && at + q < len) m |= 1u << q;
+          if ((v[q] >> bits_left) == prefix) m |= 1u << q;
+        if (at + 3 >= len) m &= (1u << (len - at)) - 1u;  // not the padding
         if (m) {
           uint32_t place = atomicAdd(nl, (uint32_t)__popc(m));
 #pragma unroll
@@ -307,7 +317,10 @@ __global__ void __launch_bounds__(kThreads, 2048 / kThreads) evict_select_cluste
     }
   }
   // ---- keep every key above `prefix`, and of those at it the rows up to
-  // last_row or the first `need`: counts by warp, by CTA, by row
+  // last_row (ranked) or the first `need`: counts by warp, by CTA, by row.
+  // Ranked: one bit a row says it all (padding lies past last_row), and a
+  // thread's 4 n <= 48 of them wait in a register for the counts.
+  uint64_t kept_bits = 0;
   // above and at of four rows: bits 0-3 and 4-7
   auto kinds = [&](int at) -> uint32_t {
     uint32_t m = 0;
@@ -316,10 +329,12 @@ __global__ void __launch_bounds__(kThreads, 2048 / kThreads) evict_select_cluste
       const uint32_t v[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const bool eq = v[q] == prefix && at + q < len;
-        const bool in = eq && ranked && (uint32_t)(first + at + q) <= last_row;
-        if (v[q] > prefix || in) m |= 1u << q;
-        if (eq && !ranked) m |= 16u << q;
+        if (ranked) {
+          if (v[q] > prefix || (v[q] == prefix && (uint32_t)(first + at + q) <= last_row)) m |= 1u << q;
+        } else {
+          if (v[q] > prefix) m |= 1u << q;
+          if (v[q] == prefix && at + q < len) m |= 16u << q;
+        }
       }
     }
     return m;
@@ -328,6 +343,7 @@ __global__ void __launch_bounds__(kThreads, 2048 / kThreads) evict_select_cluste
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {
     const uint32_t m = kinds(at0 + 128 * i);
+    kept_bits |= (uint64_t)(m & 15u) << (4 * i);
     n_above += __popc(m & 15u);
     n_at += __popc(m >> 4);
   }
@@ -351,6 +367,26 @@ __global__ void __launch_bounds__(kThreads, 2048 / kThreads) evict_select_cluste
       my_above += x[0];
       my_at += x[1];
     }
+  }
+  if (ranked) {
+    const uint32_t below = (1u << lane) - 1u;
+#pragma unroll 1
+    for (int i = 0; i < n; ++i) {
+      const int row = first + at0 + 128 * i;
+      const uint32_t m = (uint32_t)(kept_bits >> (4 * i)) & 15u;
+      uint32_t pa = my_above;
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const uint32_t all = __ballot_sync(0xffffffffu, (m >> q) & 1u);
+        pa += __popc(all & below);
+        my_above += __popc(all);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        if ((m >> q) & 1u) keep[pa++] = row + q;
+    }
+    if (cs > 1) cluster.sync();  // the others may still read this CTA's shared memory
+    return;
   }
 #pragma unroll 1
   for (int i = 0; i < n; ++i) {

@@ -592,18 +592,25 @@ __device__ __forceinline__ CompactSeq compact_seq(const CompactArgs& a, int r, b
   return s;
 }
 
-// keep[j], or -1 where it is out of range or order (reported).
-__device__ __forceinline__ int kept_row(const CompactArgs& a, const CompactSeq& s,
-                                        const int32_t* keep, int j) {
-  const int k = __ldg(keep + j);
-  const int prev = j > 0 ? __ldg(keep + j - 1) : -1;
+// Kept row j, keep[j] = k after keep[j - 1] = prev (-1: none), or -1 where it
+// is out of range or order (reported).
+__device__ __forceinline__ int kept_row(const CompactArgs& a, const CompactSeq& s, int k, int prev, int j) {
   if (k >= j && k > prev && k < s.len - s.base) return k;
   atomicOr(a.err, PKV_DEVERR_KEEP);
   return -1;
 }
+__device__ __forceinline__ int kept_before(const int32_t* keep, int j) { return j > 0 ? __ldg(keep + j - 1) : -1; }
+
+// Row t's block, in its table, and place in that block.
+__device__ __forceinline__ int block_of(const CompactArgs& a, int t) {
+  return a.block_shift >= 0 ? t >> a.block_shift : t / a.block_size;
+}
+__device__ __forceinline__ int offset_of(const CompactArgs& a, int t) {
+  return a.block_shift >= 0 ? t & (a.block_size - 1) : t % a.block_size;
+}
 
 __device__ __forceinline__ int table_entry(const CompactArgs& a, int r, int t) {
-  return __ldg(a.block_tables + (int64_t)r * a.max_blocks + t / a.block_size);
+  return __ldg(a.block_tables + (int64_t)r * a.max_blocks + block_of(a, t));
 }
 
 // Pool row of offset `off` of block `blk`, or kCmSkip for a bad id (reported).
@@ -643,18 +650,26 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
     if (vecs <= 0) return;
     const int rows = 1 << (31 - __clz(min(kTileVecs / vecs, kCmThreads)));
     const int tiles = (s.n + rows - 1) / rows;
-    int my_row[kVecs], my_c[kVecs];  // this thread's vectors of a tile
+    int my_row[kVecs];          // this thread's vectors of a tile: rows,
+    unsigned char* col[kVecs];  // and columns in pool row 0
+    const uint32_t pitch = (uint32_t)Hkv * a.row_bytes;
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
       const int i = tid + u * kCmThreads;
       my_row[u] = i < rows * vecs ? i / vecs : -1;
-      my_c[u] = i % vecs;
+      col[u] = pool + (int64_t)h * a.row_bytes + (c0 + i % vecs) * 16;
     }
     // ---- places, in batches of kCmThreads rows, a row a thread: the kept rows
     // of the batch after next and the block ids of the next one are on their
     // way while a batch is used
-    int k_next = -1, k_now = -1, b_from = 0, b_to = 0;  // kept rows, block ids
-    auto load_keep = [&](int j) { return j < s.n ? kept_row(a, s, keep, j) : -1; };
+    int k_next = -1, k_prev = -1, k_now = -1, b_from = 0, b_to = 0;  // kept rows, block ids
+    auto load_keep = [&](int j) {  // looked at a batch later
+      if (j < s.n) {
+        k_next = __ldg(keep + j);
+        k_prev = kept_before(keep, j);
+      }
+    };
+    auto next_keep = [&](int j) { k_now = j < s.n ? kept_row(a, s, k_next, k_prev, j) : -1; };
     auto load_blocks = [&](int j) {
       if (k_now >= 0) {
         b_from = table_entry(a, r, s.base + k_now);
@@ -662,21 +677,25 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
       }
     };
     int filled = 0;  // rows whose places are known
-    k_now = load_keep(tid);
-    k_next = load_keep(kCmThreads + tid);
+    if (tid * 32 < min(s.n, (kRing + 2) * kCmThreads))  // the first of them ahead of their turns
+      asm volatile("prefetch.global.L2 [%0];" ::"l"(keep + tid * 32));
+    load_keep(tid);
+    next_keep(tid);
+    load_keep(kCmThreads + tid);
     load_blocks(tid);
     auto fill = [&]() {
       const int j = filled + tid;
       uint2 at = make_uint2(kCmSkip, kCmSkip);
       if (k_now >= 0 && k_now != j) {  // a row already in its place stays
-        const uint32_t from = pool_row(a, b_from, (s.base + k_now) % P), to = pool_row(a, b_to, (s.base + j) % P);
+        const uint32_t from = pool_row(a, b_from, offset_of(a, s.base + k_now));
+        const uint32_t to = pool_row(a, b_to, offset_of(a, s.base + j));
         if (from != kCmSkip && to != kCmSkip) at = make_uint2(from, to);
       }
       places[j & (kPlaces - 1)] = at;
       filled += kCmThreads;
-      k_now = k_next;
+      next_keep(filled + tid);
       load_blocks(filled + tid);
-      k_next = load_keep(filled + kCmThreads + tid);
+      load_keep(filled + kCmThreads + tid);
     };
     auto issue = [&](int t) {  // this thread's loads of tile t (an empty group past the last)
       if (t < tiles) {
@@ -687,7 +706,7 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
           const uint32_t from = j < s.n ? places[j & (kPlaces - 1)].x : kCmSkip;
           if (from != kCmSkip)
             cp_async16(smem_u32(ring + (t % kRing) * kTileVecs + u * kCmThreads + tid),
-                       pool + ((int64_t)from * Hkv + h) * a.row_bytes + (c0 + my_c[u]) * 16);
+                       col[u] + (uint64_t)from * pitch);
         }
       }
       asm volatile("cp.async.commit_group;" ::: "memory");
@@ -709,7 +728,7 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
         const int j = t * rows + my_row[u];
         const uint32_t to = j < s.n ? places[j & (kPlaces - 1)].y : kCmSkip;
         if (to != kCmSkip)
-          *reinterpret_cast<uint4*>(pool + ((int64_t)to * Hkv + h) * a.row_bytes + (c0 + my_c[u]) * 16) =
+          *reinterpret_cast<uint4*>(col[u] + (uint64_t)to * pitch) =
               ring[(t % kRing) * kTileVecs + u * kCmThreads + tid];
       }
     }
@@ -725,7 +744,7 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
 #pragma unroll
       for (int u = 0; u < kCmSmall; ++u) {
         const int j = j0 + u * kCmThreads + tid;
-        k[u] = j < s.n ? kept_row(a, s, keep, j) : -1;
+        k[u] = j < s.n ? kept_row(a, s, __ldg(keep + j), kept_before(keep, j), j) : -1;
       }
 #pragma unroll
       for (int u = 0; u < kCmSmall; ++u) x[u] = k[u] >= 0 ? w[k[u]] : 0.f;
@@ -745,11 +764,11 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
 #pragma unroll
       for (int u = 0; u < kCmSmall; ++u) {
         const int j = j0 + u * kCmThreads + tid;
-        const int k = j < s.n ? kept_row(a, s, keep, j) : -1;
+        const int k = j < s.n ? kept_row(a, s, __ldg(keep + j), kept_before(keep, j), j) : -1;
         from[u] = to[u] = kCmSkip;
         if (k >= 0 && k != j) {
-          from[u] = pool_row(a, table_entry(a, r, s.base + k), (s.base + k) % P);
-          to[u] = pool_row(a, table_entry(a, r, s.base + j), (s.base + j) % P);
+          from[u] = pool_row(a, table_entry(a, r, s.base + k), offset_of(a, s.base + k));
+          to[u] = pool_row(a, table_entry(a, r, s.base + j), offset_of(a, s.base + j));
           if (from[u] == kCmSkip) to[u] = kCmSkip;
         }
       }
@@ -789,6 +808,9 @@ cudaError_t launch_kv_compact(const CompactArgs& args, cudaStream_t stream) {
   const int vecs = a.row_bytes / 16;
   const int64_t chains = (int64_t)a.num_seqs * a.num_kv_heads * 2;
   a.parts = (vecs + 63) / 64;
+  a.block_shift = -1;
+  for (int i = 0; i < 31; ++i)
+    if (a.block_size == 1 << i) a.block_shift = i;
   while (chains * a.parts < 304 && vecs % (2 * a.parts) == 0 && vecs / (2 * a.parts) >= 2) a.parts *= 2;
   const unsigned y = 2u * a.parts + (a.weights ? 1u : 0u) + (a.k_scales ? 2u : 0u);
   // A drafted path is one batch of rows at most: a small ring, and more CTAs a

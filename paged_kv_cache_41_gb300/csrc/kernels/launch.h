@@ -358,6 +358,7 @@ struct CompactArgs {
   int32_t row_bytes;
   int32_t scale_bytes;
   int32_t parts;                // CTAs a row's columns are dealt to (the launcher sets it)
+  int32_t block_shift;          // block_size = 1 << block_shift, or -1 (the launcher sets it)
 };
 cudaError_t launch_kv_compact(const CompactArgs& args, cudaStream_t stream);
 

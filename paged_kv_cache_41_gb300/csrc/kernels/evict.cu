@@ -569,7 +569,6 @@ cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
 // and the ring is deeper.
 namespace {
 
-constexpr int kCmThreads = 256;
 constexpr uint32_t kCmSkip = 0xffffffffu;             // no row to move here
 constexpr int kCmSmall = 8;                           // weights or scales per thread and turn
 
@@ -629,11 +628,11 @@ __device__ __forceinline__ void cp_async16(uint32_t smem, const void* g) {
 
 // kVecs: 16-byte vectors per thread and tile.  kRing: tiles of the ring.
 // kPlaces: entries of the ring of places, a power of two >= the rows of kRing +
-// 1 tiles (a tile has kCmThreads at most) and a batch.
-template <int kVecs, int kRing, int kPlaces>
-__global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArgs a) {
-  static_assert(kPlaces >= (kRing + 2) * kCmThreads, "the ring of places");
-  constexpr int kTileVecs = kCmThreads * kVecs;
+// 1 tiles (a tile has kThreads at most) and a batch.
+template <int kThreads, int kVecs, int kRing, int kPlaces>
+__global__ void __launch_bounds__(kThreads) kv_compact_kernel(const CompactArgs a) {
+  static_assert(kPlaces >= (kRing + 2) * kThreads, "the ring of places");
+  constexpr int kTileVecs = kThreads * kVecs;
   extern __shared__ __align__(128) unsigned char cm_smem[];
   uint4* ring = reinterpret_cast<uint4*>(cm_smem);                               // [kRing][kTileVecs]
   uint2* places = reinterpret_cast<uint2*>(cm_smem + kRing * kTileVecs * 16);  // (from, to) by row
@@ -648,18 +647,18 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
     const int per = (a.row_bytes / 16 + a.parts - 1) / a.parts, c0 = (y % a.parts) * per;
     const int vecs = min(per, a.row_bytes / 16 - c0);
     if (vecs <= 0) return;
-    const int rows = 1 << (31 - __clz(min(kTileVecs / vecs, kCmThreads)));
+    const int rows = 1 << (31 - __clz(min(kTileVecs / vecs, kThreads)));
     const int tiles = (s.n + rows - 1) / rows;
     int my_row[kVecs];          // this thread's vectors of a tile: rows,
     unsigned char* col[kVecs];  // and columns in pool row 0
     const uint32_t pitch = (uint32_t)Hkv * a.row_bytes;
 #pragma unroll
     for (int u = 0; u < kVecs; ++u) {
-      const int i = tid + u * kCmThreads;
+      const int i = tid + u * kThreads;
       my_row[u] = i < rows * vecs ? i / vecs : -1;
       col[u] = pool + (int64_t)h * a.row_bytes + (c0 + i % vecs) * 16;
     }
-    // ---- places, in batches of kCmThreads rows, a row a thread: the kept rows
+    // ---- places, in batches of kThreads rows, a row a thread: the kept rows
     // of the batch after next and the block ids of the next one are on their
     // way while a batch is used
     int k_next = -1, k_prev = -1, k_now = -1, b_from = 0, b_to = 0;  // kept rows, block ids
@@ -677,11 +676,11 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
       }
     };
     int filled = 0;  // rows whose places are known
-    if (tid * 32 < min(s.n, (kRing + 2) * kCmThreads))  // the first of them ahead of their turns
+    if (tid * 32 < min(s.n, (kRing + 2) * kThreads))  // the first of them ahead of their turns
       asm volatile("prefetch.global.L2 [%0];" ::"l"(keep + tid * 32));
     load_keep(tid);
     next_keep(tid);
-    load_keep(kCmThreads + tid);
+    load_keep(kThreads + tid);
     load_blocks(tid);
     auto fill = [&]() {
       const int j = filled + tid;
@@ -692,10 +691,10 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
         if (from != kCmSkip && to != kCmSkip) at = make_uint2(from, to);
       }
       places[j & (kPlaces - 1)] = at;
-      filled += kCmThreads;
+      filled += kThreads;
       next_keep(filled + tid);
       load_blocks(filled + tid);
-      load_keep(filled + kCmThreads + tid);
+      load_keep(filled + kThreads + tid);
     };
     auto issue = [&](int t) {  // this thread's loads of tile t (an empty group past the last)
       if (t < tiles) {
@@ -705,7 +704,7 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
           const int j = t * rows + my_row[u];
           const uint32_t from = j < s.n ? places[j & (kPlaces - 1)].x : kCmSkip;
           if (from != kCmSkip)
-            cp_async16(smem_u32(ring + (t % kRing) * kTileVecs + u * kCmThreads + tid),
+            cp_async16(smem_u32(ring + (t % kRing) * kTileVecs + u * kThreads + tid),
                        col[u] + (uint64_t)from * pitch);
         }
       }
@@ -729,13 +728,13 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
         const uint32_t to = j < s.n ? places[j & (kPlaces - 1)].y : kCmSkip;
         if (to != kCmSkip)
           *reinterpret_cast<uint4*>(col[u] + (uint64_t)to * pitch) =
-              ring[(t % kRing) * kTileVecs + u * kCmThreads + tid];
+              ring[(t % kRing) * kTileVecs + u * kThreads + tid];
       }
     }
     return;
   }
   // ---- weights, and an MXFP8 pool's scales: a few bytes a row
-  constexpr int kTurn = kCmThreads * kCmSmall;
+  constexpr int kTurn = kThreads * kCmSmall;
   if (y == 2 * a.parts && a.weights) {
     float* w = a.weights + ((int64_t)r * Hkv + h) * a.weights_stride + s.base;
     for (int j0 = 0; j0 < s.n; j0 += kTurn) {
@@ -743,7 +742,7 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
       int k[kCmSmall];
 #pragma unroll
       for (int u = 0; u < kCmSmall; ++u) {
-        const int j = j0 + u * kCmThreads + tid;
+        const int j = j0 + u * kThreads + tid;
         k[u] = j < s.n ? kept_row(a, s, __ldg(keep + j), kept_before(keep, j), j) : -1;
       }
 #pragma unroll
@@ -751,10 +750,10 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
       __syncthreads();  // the turn's loads are done
 #pragma unroll
       for (int u = 0; u < kCmSmall; ++u)
-        if (k[u] >= 0) w[j0 + u * kCmThreads + tid] = x[u];
+        if (k[u] >= 0) w[j0 + u * kThreads + tid] = x[u];
     }
     __syncthreads();  // every source has been read
-    for (int j = s.n + tid; j < s.len - s.base; j += kCmThreads) w[j] = 0.f;
+    for (int j = s.n + tid; j < s.len - s.base; j += kThreads) w[j] = 0.f;
   } else {
     // scales of K, then of V: [NB, Hkv, P, scale_bytes], scale_bytes a row
     const int v = y - 2 * a.parts - (a.weights ? 1 : 0), sb = a.scale_bytes;
@@ -763,7 +762,7 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
       uint32_t from[kCmSmall], to[kCmSmall];
 #pragma unroll
       for (int u = 0; u < kCmSmall; ++u) {
-        const int j = j0 + u * kCmThreads + tid;
+        const int j = j0 + u * kThreads + tid;
         const int k = j < s.n ? kept_row(a, s, __ldg(keep + j), kept_before(keep, j), j) : -1;
         from[u] = to[u] = kCmSkip;
         if (k >= 0 && k != j) {
@@ -789,14 +788,14 @@ __global__ void __launch_bounds__(kCmThreads) kv_compact_kernel(const CompactArg
   }
 }
 
-template <int kVecs, int kRing, int kPlaces>
+template <int kThreads, int kVecs, int kRing, int kPlaces>
 static cudaError_t launch_compact_t(const CompactArgs& a, unsigned y, cudaStream_t stream) {
-  constexpr int smem = kRing * kCmThreads * kVecs * 16 + kPlaces * 8;
-  auto kern = kv_compact_kernel<kVecs, kRing, kPlaces>;
+  constexpr int smem = kRing * kThreads * kVecs * 16 + kPlaces * 8;
+  auto kern = kv_compact_kernel<kThreads, kVecs, kRing, kPlaces>;
   static SmemAttrCache attr_cache;
   cudaError_t e = ensure_smem_limit(kern, smem, attr_cache);
   if (e != cudaSuccess) return e;
-  kern<<<dim3((unsigned)a.num_kv_heads, y, (unsigned)a.num_seqs), kCmThreads, smem, stream>>>(a);
+  kern<<<dim3((unsigned)a.num_kv_heads, y, (unsigned)a.num_seqs), kThreads, smem, stream>>>(a);
   return cudaGetLastError();
 }
 
@@ -815,9 +814,9 @@ cudaError_t launch_kv_compact(const CompactArgs& args, cudaStream_t stream) {
   const unsigned y = 2u * a.parts + (a.weights ? 1u : 0u) + (a.k_scales ? 2u : 0u);
   // A drafted path is one batch of rows at most: a small ring, and more CTAs a
   // SM (64 requests 6.2 us, with four tiles 7.1 us).  Few chains: a deep ring.
-  if (a.keep_stride <= kCmThreads) return launch_compact_t<2, 2, 1024>(a, y, stream);
-  return chains * a.parts < 456 ? launch_compact_t<4, 8, 4096>(a, y, stream)
-                                : launch_compact_t<2, 4, 2048>(a, y, stream);
+  if (a.keep_stride <= 256) return launch_compact_t<256, 2, 2, 1024>(a, y, stream);
+  return chains * a.parts < 456 ? launch_compact_t<512, 2, 8, 8192>(a, y, stream)
+                                : launch_compact_t<256, 2, 4, 2048>(a, y, stream);
 }
 
 }  // namespace pkv

@@ -815,7 +815,7 @@ cudaError_t launch_kv_compact(const CompactArgs& args, cudaStream_t stream) {
   // A drafted path is one batch of rows at most: a small ring, and more CTAs a
   // SM (64 requests 6.2 us, with four tiles 7.1 us).  Few chains: a deep ring.
   if (a.keep_stride <= 256) return launch_compact_t<256, 2, 2, 1024>(a, y, stream);
-  return chains * a.parts < 456 ? launch_compact_t<512, 2, 8, 8192>(a, y, stream)
+  return chains * a.parts < 456 ? launch_compact_t<1024, 1, 6, 8192>(a, y, stream)
                                 : launch_compact_t<256, 2, 4, 2048>(a, y, stream);
 }
 

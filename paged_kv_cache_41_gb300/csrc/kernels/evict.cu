@@ -802,8 +802,7 @@ static cudaError_t launch_compact_t(const CompactArgs& a, unsigned y, cudaStream
 cudaError_t launch_kv_compact(const CompactArgs& args, cudaStream_t stream) {
   CompactArgs a = args;
   // Columns: at most 64 vectors a CTA, and while the chains are fewer than two
-  // a SM, halves of at least two vectors (32 bytes; three long fp32 sequences
-  // take 52 us with at least four, 44 us with two).
+  // a SM, halves of at least two vectors (32 bytes, a sector).
   const int vecs = a.row_bytes / 16;
   const int64_t chains = (int64_t)a.num_seqs * a.num_kv_heads * 2;
   a.parts = (vecs + 63) / 64;
@@ -813,9 +812,12 @@ cudaError_t launch_kv_compact(const CompactArgs& args, cudaStream_t stream) {
   while (chains * a.parts < 304 && vecs % (2 * a.parts) == 0 && vecs / (2 * a.parts) >= 2) a.parts *= 2;
   const unsigned y = 2u * a.parts + (a.weights ? 1u : 0u) + (a.k_scales ? 2u : 0u);
   // A drafted path is one batch of rows at most: a small ring, and more CTAs a
-  // SM (64 requests 6.2 us, with four tiles 7.1 us).  Few chains: a deep ring.
+  // SM (64 requests 6.2 us, with four tiles 7.1 us).  Otherwise four CTAs a SM,
+  // or one that keeps more on its way where there is no second for every SM
+  // (three long fp32 sequences, 96 CTAs: 44 us and 20 us; 14 bf16 ones, 448
+  // CTAs: 23.7 us and 29.5 us).
   if (a.keep_stride <= 256) return launch_compact_t<256, 2, 2, 1024>(a, y, stream);
-  return chains * a.parts < 456 ? launch_compact_t<1024, 1, 6, 8192>(a, y, stream)
+  return chains * a.parts < 304 ? launch_compact_t<1024, 1, 6, 8192>(a, y, stream)
                                 : launch_compact_t<256, 2, 4, 2048>(a, y, stream);
 }
 

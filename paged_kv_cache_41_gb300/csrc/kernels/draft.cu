@@ -10,19 +10,24 @@
 // in one pass over the rows with a running maximum and sum (base 2, fp32).
 //
 // Design:
-//   * a CTA takes kRT * 8 (token, query head) rows of one kv head -- all the
+//   * a CTA takes 16 kRT (token, query head) rows of one kv head -- all the
 //     G heads of a token share its K/V -- and one contiguous split of the
-//     sequence's rows, 32 at a time, in shared memory;
-//   * thread (rg, kg) of 8 x 16 holds the scores of rows rg kRT .. and keys
-//     kg, kg + 16, and the outputs of those rows at D / 16 columns;
+//     sequence's rows, 32 at a time, through two buffers that cp.async fills;
+//   * thread (rg, kg) of 16 x 16 holds the scores of rows rg kRT .. and keys
+//     kg, kg + 16, and the outputs of those rows at columns 4 kg .. + 3 of
+//     every 64: three shared-memory wavefronts for every eight FMAs;
 //   * splits leave (O, LSE) states that a second kernel merges by
 //     log-sum-exp; one split writes the result directly;
 //   * a hidden row's weight is stored as -1 and skipped, not multiplied, so
 //     an infinity or NaN in it cannot leak; rows past the last drafted one
-//     are never read.
+//     are never read.  Tiles without hidden rows look at no weight's sign.
 // The fp32 FMAs bound it, 256 per (row, key) at head_dim 128: fp32 operands
-// would lose 16 bits on the tensor cores.  SIMT_US
+// would lose 13 bits or more on the tensor cores.  16 requests with trees of 5
+// to 27, 32 query and 8 kv heads: 747 us, 24 TFLOP/s, of the 74 that the FMAs
+// can do.
 #include <math.h>
+
+#include <type_traits>
 
 #include "draft.cuh"
 
@@ -30,30 +35,36 @@ namespace pkv {
 
 namespace {
 
-constexpr int kDsThreads = 128;
+constexpr int kDsThreads = 256;
 constexpr int kDsKeys = 32;  // keys per tile
+constexpr int kDsPs = kDsKeys + 4;  // padded shared rows of weights
 constexpr float kDsLn2 = 0.6931471805599453f;
 
 template <int D, int kRT>
 constexpr int draft_simt_smem() {
-  return (8 * kRT * (D + 4) + kDsKeys * (D + 4) + kDsKeys * D + 8 * kRT * (kDsKeys + 1)) * 4 +
-         8 * kRT * 8;
+  return (16 * kRT * (D + 4) + 2 * kDsKeys * (D + 4) + 2 * kDsKeys * D + 16 * kRT * kDsPs) * 4 + 16 * kRT * 8;
+}
+
+// 16 bytes, or zeros.
+__device__ __forceinline__ void cp_async16_or_zero(void* smem, const void* g, bool valid) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(smem_u32(smem)), "l"(g), "r"(valid ? 16 : 0)
+               : "memory");
 }
 
 }  // namespace
 
 template <int D, int kRT>
-__global__ void __launch_bounds__(kDsThreads) draft_simt_kernel(const DraftArgs a) {
-  constexpr int R = 8 * kRT;       // query rows per CTA
+__global__ void __launch_bounds__(kDsThreads, 2) draft_simt_kernel(const DraftArgs a) {
+  constexpr int R = 16 * kRT;      // query rows per CTA
   constexpr int LD = D + 4;        // padded shared rows of Q and K
-  constexpr int CPT = D / 16;      // output columns per thread
-  constexpr int kVec = D / 8;      // 8-element vectors per row
+  constexpr int NQ = D / 64;       // quads of output columns per thread
+  constexpr int kVec = D / 4;      // 16-byte vectors per row
   extern __shared__ __align__(16) float sm[];
   float* qs = sm;                           // [R][LD], scaled
-  float* ks = qs + R * LD;                  // [keys][LD]
-  float* vs = ks + kDsKeys * LD;            // [keys][D]
-  float* ps = vs + kDsKeys * D;             // [R][keys + 1]
-  uint64_t* mk = reinterpret_cast<uint64_t*>(ps + ((R * (kDsKeys + 1) + 1) & ~1));
+  float* ks = qs + R * LD;                  // [2][keys][LD]
+  float* vs = ks + 2 * kDsKeys * LD;        // [2][keys][D]
+  float* ps = vs + 2 * kDsKeys * D;         // [R][kDsPs]
+  uint64_t* mk = reinterpret_cast<uint64_t*>(ps + R * kDsPs);
   pdl_wait();
   pdl_launch_dependents();
   const int r = blockIdx.z, split = blockIdx.x;
@@ -70,57 +81,62 @@ __global__ void __launch_bounds__(kDsThreads) draft_simt_kernel(const DraftArgs 
   const int t_lo = lo64 < T_all ? (int)lo64 : T_all, t_hi = min(T_all - t_lo, per) + t_lo;
 
   const int tid = threadIdx.x, rg = tid >> 4, kg = tid & 15;
+  auto load = [&](int t0, int buf) {  // the tile's K and V; zeros past the split and for bad blocks
+#pragma unroll
+    for (int n = 0; n < kDsKeys * kVec / kDsThreads; ++n) {
+      const int i = tid + n * kDsThreads, key = i / kVec, c = (i % kVec) * 4, t = t0 + key;
+      bool valid = t < t_hi;
+      int64_t at = 0;
+      if (valid) {
+        const int blk = __ldg(a.block_tables + (int64_t)r * a.max_blocks + t / P);
+        valid = blk >= 0 && (int64_t)blk < a.num_blocks;
+        if (valid) at = (((int64_t)blk * P + t % P) * Hkv + h) * D + c;
+        else if (c == 0) atomicOr(a.err, PKV_DEVERR_BLOCK);
+      }
+      cp_async16_or_zero(ks + (buf * kDsKeys + key) * LD + c, static_cast<const float*>(a.k) + at, valid);
+      cp_async16_or_zero(vs + (buf * kDsKeys + key) * D + c, static_cast<const float*>(a.v) + at, valid);
+    }
+  };
+  if (t_lo < t_hi) load(t_lo, 0);
+  asm volatile("cp.async.commit_group;" ::: "memory");
   for (int i = tid; i < R * kVec; i += kDsThreads) {
-    const int row = i / kVec, c = (i % kVec) * 8;
-    float f[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+    const int row = i / kVec, c = (i % kVec) * 4;
+    float4 f = make_float4(0.f, 0.f, 0.f, 0.f);
     if (row < rows) {
       const int tok = (row_lo + row) / G, g = (row_lo + row) % G;
-      VecLoad<float, 8>::run(static_cast<const float*>(a.q) + ((int64_t)(s.row0 + tok) * a.num_q_heads + h * G + g) * D + c,
-                            f);
+      f = __ldg(reinterpret_cast<const float4*>(static_cast<const float*>(a.q) +
+                                                ((int64_t)(s.row0 + tok) * a.num_q_heads + h * G + g) * D + c));
     }
-#pragma unroll
-    for (int e = 0; e < 8; ++e) qs[row * LD + c + e] = f[e] * a.qscale;
+    *reinterpret_cast<float4*>(qs + row * LD + c) =
+        make_float4(f.x * a.qscale, f.y * a.qscale, f.z * a.qscale, f.w * a.qscale);
   }
   for (int i = tid; i < R; i += kDsThreads) mk[i] = i < rows ? draft_mask(a, s, (row_lo + i) / G) : 0;
 
-  float m[kRT], l[kRT], o[kRT][CPT];
+  float m[kRT], l[kRT], o[kRT][4 * NQ];
 #pragma unroll
   for (int i = 0; i < kRT; ++i) {
     m[i] = -INFINITY;
     l[i] = 0.f;
 #pragma unroll
-    for (int c = 0; c < CPT; ++c) o[i][c] = 0.f;
+    for (int c = 0; c < 4 * NQ; ++c) o[i][c] = 0.f;
   }
-  for (int t0 = t_lo; t0 < t_hi; t0 += kDsKeys) {
-    __syncthreads();  // the previous tile has been used
-    for (int i = tid; i < kDsKeys * kVec; i += kDsThreads) {
-      const int key = i / kVec, c = (i % kVec) * 8, t = t0 + key;
-      float kf[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, vf[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (t < t_hi) {
-        const int blk = __ldg(a.block_tables + (int64_t)r * a.max_blocks + t / P);
-        if (blk >= 0 && (int64_t)blk < a.num_blocks) {
-          const int64_t at = (((int64_t)blk * P + t % P) * Hkv + h) * D + c;
-          VecLoad<float, 8>::run(static_cast<const float*>(a.k) + at, kf);
-          VecLoad<float, 8>::run(static_cast<const float*>(a.v) + at, vf);
-        } else if (c == 0) {
-          atomicOr(a.err, PKV_DEVERR_BLOCK);
-        }
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        ks[key * LD + c + e] = kf[e];
-        vs[key * D + c + e] = vf[e];
-      }
-    }
-    __syncthreads();
+  int buf = 0;
+  for (int t0 = t_lo; t0 < t_hi; t0 += kDsKeys, buf ^= 1) {
+    asm volatile("cp.async.wait_group 0;" ::: "memory");
+    __syncthreads();  // this tile is here, and the previous one has been used
+    if (t0 + kDsKeys < t_hi) load(t0 + kDsKeys, buf ^ 1);
+    asm volatile("cp.async.commit_group;" ::: "memory");
+    if ((tid >> 5) * 2 * kRT >= rows) continue;  // a warp without rows only loads
+    const float* kt = ks + buf * kDsKeys * LD;
+    const float* vt = vs + buf * kDsKeys * D + kg * 4;
     // ---- scores of rows rg kRT + i, keys kg and kg + 16
     float x[kRT][2];
 #pragma unroll
     for (int i = 0; i < kRT; ++i) x[i][0] = x[i][1] = 0.f;
 #pragma unroll 4
     for (int c = 0; c < D; c += 4) {
-      const float4 k0 = *reinterpret_cast<const float4*>(ks + kg * LD + c);
-      const float4 k1 = *reinterpret_cast<const float4*>(ks + (kg + 16) * LD + c);
+      const float4 k0 = *reinterpret_cast<const float4*>(kt + kg * LD + c);
+      const float4 k1 = *reinterpret_cast<const float4*>(kt + (kg + 16) * LD + c);
 #pragma unroll
       for (int i = 0; i < kRT; ++i) {
         const float4 q = *reinterpret_cast<const float4*>(qs + (rg * kRT + i) * LD + c);
@@ -128,6 +144,7 @@ __global__ void __launch_bounds__(kDsThreads) draft_simt_kernel(const DraftArgs 
         x[i][1] = fmaf(q.x, k1.x, fmaf(q.y, k1.y, fmaf(q.z, k1.z, fmaf(q.w, k1.w, x[i][1]))));
       }
     }
+    const bool clean = t0 + kDsKeys <= min(s.ctx, t_hi);  // every row sees every key
 #pragma unroll
     for (int i = 0; i < kRT; ++i) {
       const int row = rg * kRT + i;
@@ -136,7 +153,7 @@ __global__ void __launch_bounds__(kDsThreads) draft_simt_kernel(const DraftArgs 
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int t = t0 + kg + 16 * j, d = t - s.ctx;
-        seen[j] = t < t_hi && (d < 0 || ((mk[row] >> d) & 1));  // d < n <= 64 where t < t_hi
+        seen[j] = clean || (t < t_hi && (d < 0 || ((mk[row] >> d) & 1)));  // d < n <= 64 where t < t_hi
         if (seen[j]) mx = fmaxf(mx, x[i][j]);
       }
 #pragma unroll
@@ -149,30 +166,44 @@ __global__ void __launch_bounds__(kDsThreads) draft_simt_kernel(const DraftArgs 
       for (int j = 0; j < 2; ++j) {
         const float p = exp2f(x[i][j] - base);
         if (seen[j]) sum += p;
-        ps[row * (kDsKeys + 1) + kg + 16 * j] = seen[j] ? p : -1.f;
+        ps[row * kDsPs + kg + 16 * j] = seen[j] ? p : -1.f;
       }
 #pragma unroll
       for (int w = 8; w >= 1; w >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, w);
       l[i] = l[i] * alpha + sum;
       m[i] = m_new;
 #pragma unroll
-      for (int c = 0; c < CPT; ++c) o[i][c] *= alpha;
+      for (int c = 0; c < 4 * NQ; ++c) o[i][c] *= alpha;
     }
     __syncwarp();  // a row's weights are written and read by one half-warp
-    const int nk = min(kDsKeys, t_hi - t0);
-    for (int key = 0; key < nk; ++key) {
-      float v[CPT];
+    auto add = [&](auto hidden) {
+#pragma unroll 2
+      for (int key = 0; key < kDsKeys; key += 4) {
+        float4 p4[kRT];
 #pragma unroll
-      for (int c = 0; c < CPT; ++c) v[c] = vs[key * D + c * 16 + kg];
+        for (int i = 0; i < kRT; ++i) p4[i] = *reinterpret_cast<const float4*>(ps + (rg * kRT + i) * kDsPs + key);
 #pragma unroll
-      for (int i = 0; i < kRT; ++i) {
-        const float p = ps[(rg * kRT + i) * (kDsKeys + 1) + key];
-        if (!(p < 0.f)) {  // a NaN weight counts
+        for (int k = 0; k < 4; ++k) {
+          float4 v[NQ];
 #pragma unroll
-          for (int c = 0; c < CPT; ++c) o[i][c] = fmaf(p, v[c], o[i][c]);
+          for (int c = 0; c < NQ; ++c) v[c] = *reinterpret_cast<const float4*>(vt + (key + k) * D + c * 64);
+#pragma unroll
+          for (int i = 0; i < kRT; ++i) {
+            const float p = k == 0 ? p4[i].x : k == 1 ? p4[i].y : k == 2 ? p4[i].z : p4[i].w;
+            if (decltype(hidden)::value && p < 0.f) continue;  // a NaN weight counts
+#pragma unroll
+            for (int c = 0; c < NQ; ++c) {
+              o[i][4 * c] = fmaf(p, v[c].x, o[i][4 * c]);
+              o[i][4 * c + 1] = fmaf(p, v[c].y, o[i][4 * c + 1]);
+              o[i][4 * c + 2] = fmaf(p, v[c].z, o[i][4 * c + 2]);
+              o[i][4 * c + 3] = fmaf(p, v[c].w, o[i][4 * c + 3]);
+            }
+          }
         }
       }
-    }
+    };
+    if (clean) add(std::false_type{});
+    else add(std::true_type{});
     __syncwarp();
   }
 #pragma unroll
@@ -183,17 +214,16 @@ __global__ void __launch_bounds__(kDsThreads) draft_simt_kernel(const DraftArgs 
     const int64_t qh = (int64_t)(s.row0 + tok) * a.num_q_heads + h * G + g;
     const float inv = l[i] == 0.f ? 0.f : 1.f / l[i];
     const float lse2 = l[i] == 0.f ? -INFINITY : m[i] + log2f(l[i]);
-    if (a.num_splits == 1) {
+    // states by (sequence, drafted row, head), whatever query row that is
+    const int64_t st = (((int64_t)r * a.max_draft + tok) * a.num_q_heads + h * G + g) * a.num_splits + split;
+    float* dst = (a.num_splits == 1 ? static_cast<float*>(a.out) + qh * D : a.rec_o + st * D) + kg * 4;
 #pragma unroll
-      for (int c = 0; c < CPT; ++c)
-        static_cast<float*>(a.out)[qh * D + c * 16 + kg] = o[i][c] * inv;
-      if (kg == 0 && a.lse_out) a.lse_out[qh] = lse2 * kDsLn2;
-    } else {
-      // states by (sequence, drafted row, head), whatever query row that is
-      const int64_t st = (((int64_t)r * a.max_draft + tok) * a.num_q_heads + h * G + g) * a.num_splits + split;
-#pragma unroll
-      for (int c = 0; c < CPT; ++c) a.rec_o[st * D + c * 16 + kg] = o[i][c] * inv;
-      if (kg == 0) a.rec_lse[st] = lse2;
+    for (int c = 0; c < NQ; ++c)
+      *reinterpret_cast<float4*>(dst + c * 64) =
+          make_float4(o[i][4 * c] * inv, o[i][4 * c + 1] * inv, o[i][4 * c + 2] * inv, o[i][4 * c + 3] * inv);
+    if (kg == 0) {
+      if (a.num_splits > 1) a.rec_lse[st] = lse2;
+      else if (a.lse_out) a.lse_out[qh] = lse2 * kDsLn2;
     }
   }
 }
@@ -236,13 +266,13 @@ __global__ void __launch_bounds__(128) draft_simt_merge_kernel(const DraftArgs a
 
 template <int D, int kRT>
 static cudaError_t launch_draft_simt_t(const DraftArgs& a, cudaStream_t stream) {
-  constexpr int smem = draft_simt_smem<D, kRT>() + 16;
+  constexpr int smem = draft_simt_smem<D, kRT>();
   auto kern = draft_simt_kernel<D, kRT>;
   static SmemAttrCache attr_cache;
   cudaError_t e = ensure_smem_limit(kern, smem, attr_cache);
   if (e != cudaSuccess) return e;
   const int G = a.num_q_heads / a.num_kv_heads;
-  const int tiles = (a.max_draft * G + 8 * kRT - 1) / (8 * kRT);
+  const int tiles = (a.max_draft * G + 16 * kRT - 1) / (16 * kRT);
   e = launch_pdl(kern, dim3((unsigned)a.num_splits, (unsigned)(a.num_kv_heads * tiles), (unsigned)a.num_seqs),
                  dim3(kDsThreads), smem, stream, a);
   if (e != cudaSuccess || a.num_splits == 1) return e;
@@ -251,12 +281,12 @@ static cudaError_t launch_draft_simt_t(const DraftArgs& a, cudaStream_t stream) 
                     stream, a);
 }
 
-int draft_simt_rows(int rows) { return rows <= 8 ? 8 : 32; }
+int draft_simt_rows(int rows) { return rows <= 16 ? 16 : 64; }
 
 cudaError_t launch_draft_simt(int head_dim, const DraftArgs& a, cudaStream_t stream) {
-  const int rows = a.max_draft * (a.num_q_heads / a.num_kv_heads);
-  if (head_dim == 128) return rows <= 8 ? launch_draft_simt_t<128, 1>(a, stream) : launch_draft_simt_t<128, 4>(a, stream);
-  return rows <= 8 ? launch_draft_simt_t<64, 1>(a, stream) : launch_draft_simt_t<64, 4>(a, stream);
+  const bool few = draft_simt_rows(a.max_draft * (a.num_q_heads / a.num_kv_heads)) == 16;
+  if (head_dim == 128) return few ? launch_draft_simt_t<128, 1>(a, stream) : launch_draft_simt_t<128, 4>(a, stream);
+  return few ? launch_draft_simt_t<64, 1>(a, stream) : launch_draft_simt_t<64, 4>(a, stream);
 }
 
 }  // namespace pkv

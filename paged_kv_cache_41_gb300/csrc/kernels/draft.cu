@@ -243,19 +243,30 @@ __global__ void __launch_bounds__(128) draft_simt_merge_kernel(const DraftArgs a
   const int64_t st0 = ((int64_t)r * a.max_draft * a.num_q_heads + w) * S;
   const float* lse = a.rec_lse + st0;
   float M = -INFINITY;
-  for (int i = 0; i < S; ++i) M = fmaxf(M, lse[i]);
+  for (int i = lane; i < S; i += 32) M = fmaxf(M, lse[i]);
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float acc[EPL], L = 0.f;
 #pragma unroll
   for (int e = 0; e < EPL; ++e) acc[e] = 0.f;
-  for (int i = 0; i < S; ++i) {
-    const float x = lse[i];
-    if (x == -INFINITY) continue;  // an empty state
-    const float wt = exp2f(x - M);  // NaN stays NaN
-    L += wt;
-    float f[EPL];
-    VecLoad<float, EPL>::run(a.rec_o + (st0 + i) * D + lane * EPL, f);
+  constexpr int kBatch = 8;  // states loaded at once
+  for (int i0 = 0; i0 < S; i0 += kBatch) {
+    float x[kBatch], f[kBatch][EPL];
 #pragma unroll
-    for (int e = 0; e < EPL; ++e) acc[e] = fmaf(wt, f[e], acc[e]);
+    for (int i = 0; i < kBatch; ++i) {
+      x[i] = -INFINITY;
+      if (i0 + i >= S) continue;
+      x[i] = lse[i0 + i];
+      VecLoad<float, EPL>::run(a.rec_o + (st0 + i0 + i) * D + lane * EPL, f[i]);
+    }
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      if (x[i] == -INFINITY) continue;  // an empty state
+      const float wt = exp2f(x[i] - M);  // NaN stays NaN
+      L += wt;
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) acc[e] = fmaf(wt, f[i][e], acc[e]);
+    }
   }
   const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll

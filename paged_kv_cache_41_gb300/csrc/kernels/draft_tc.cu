@@ -21,7 +21,8 @@
 //     one row tile, both against all of every stage; a piece of up to 128 rows
 //     gives them a half of every stage each, against the same rows, and they
 //     merge at its end.  (Alternate stages instead of halves keep two
-//     stages of the ring under work, and fewer loads in flight: SPLIT_US.)
+//     stages of the ring under work, and fewer loads in flight: 76 us for 16
+//     requests with trees where halves took 71.)
 //   * a job is 64 keys, in two S buffers of a group in turn, so that the next
 //     job's QK runs under a job's softmax.  TMEM (512 columns): 2 x 2 x 64 of S,
 //     2 x 128 of O;
@@ -915,13 +916,13 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
 
 // Merge the pieces of the segment that starts in CTA blockIdx.x and runs on
 // into later ones, by log-sum-exp: a block per 32 rows, a warp per four of
-// them, whose pieces' outputs are loaded together.  (A warp per row, one piece
-// after another: 21 us for 64 requests with trees of 64, MERGE_US so.)
-template <int D, int kTiles>
+// them, whose pieces' outputs are loaded together; or, with kShare, a block
+// per four rows, whose warps share the pieces.
+template <int D, int kTiles, bool kShare>
 __global__ void __launch_bounds__(256) draft_tc_reduce_kernel(const DraftArgs a) {
   constexpr int EPL = D / 32;
   constexpr int kRecRows = kTiles * kDraftRows;
-  constexpr int kRows = 4, kBatch = 2;  // rows of a warp; pieces loaded at once for each
+  constexpr int kRows = 4, kBatch = kShare ? 4 : 2;  // rows of a warp; pieces loaded at once for each
   pdl_wait();  // the records and the plan are complete
   const int2 seg = a.cut_segs[blockIdx.x];
   if (seg.x < 0) return;
@@ -931,7 +932,7 @@ __global__ void __launch_bounds__(256) draft_tc_reduce_kernel(const DraftArgs a)
   const DraftSeq s = draft_seq(a, r, false);
   const int G = a.num_q_heads / a.num_kv_heads;
   const int mt = h % a.row_tiles, kvh = h / a.row_tiles;
-  const int row0 = (blockIdx.y * 8 + warp) * kRows;  // of the segment
+  const int row0 = (kShare ? blockIdx.y : blockIdx.y * 8 + warp) * kRows;  // of the segment
   const int rows = min(kRows, s.n * G - mt * kRecRows - row0);
   if (rows <= 0) return;
   const int heads = plan_heads(a);
@@ -954,7 +955,7 @@ __global__ void __launch_bounds__(256) draft_tc_reduce_kernel(const DraftArgs a)
 #pragma unroll
     for (int e = 0; e < EPL; ++e) acc[k][e] = 0.f;
   }
-  for (int i0 = 0; i0 < np; i0 += kBatch) {
+  for (int i0 = kShare ? warp * kBatch : 0; i0 < np; i0 += kShare ? 8 * kBatch : kBatch) {
     float ls[kBatch][kRows], f[kBatch][kRows][EPL];
 #pragma unroll
     for (int i = 0; i < kBatch; ++i)
@@ -987,9 +988,34 @@ __global__ void __launch_bounds__(256) draft_tc_reduce_kernel(const DraftArgs a)
         for (int e = 0; e < EPL; ++e) acc[k][e] = fmaf(w1, f[i][k][e], acc[k][e] * w0);
       }
   }
+  if constexpr (kShare) {  // warp k adds the warps' sums of row k to its own
+    __shared__ float2 state[8][kRows];
+    __shared__ float sums[8][kRows][D];
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (lane == 0) state[warp][k] = make_float2(M[k], Ls[k]);
+#pragma unroll
+      for (int e = 0; e < EPL; ++e) sums[warp][k][e * 32 + lane] = acc[k][e];
+    }
+    __syncthreads();
+#pragma unroll
+    for (int k = 0; k < kRows; ++k) {
+      if (warp != k) continue;
+#pragma unroll 1
+      for (int w = 0; w < 8; ++w) {
+        const float2 x = state[w][k];
+        if (w == warp || x.y == 0.f) continue;  // its own, or nothing
+        const float m = fmaxf(M[k], x.x), w0 = M[k] == m ? 1.f : exp2f(M[k] - m), w1 = exp2f(x.x - m);
+        M[k] = m;
+        Ls[k] = Ls[k] * w0 + x.y * w1;
+#pragma unroll
+        for (int e = 0; e < EPL; ++e) acc[k][e] = fmaf(w1, sums[w][k][e * 32 + lane], acc[k][e] * w0);
+      }
+    }
+  }
 #pragma unroll
   for (int k = 0; k < kRows; ++k) {
-    if (k >= rows) continue;
+    if (k >= rows || (kShare && warp != k)) continue;
     const float inv = Ls[k] == 0.f ? 0.f : 1.f / Ls[k];
     const int rowg = mt * kRecRows + row0 + k;
     const int64_t qh = (int64_t)(s.row0 + rowg / G) * a.num_q_heads + kvh * G + rowg % G;
@@ -1018,9 +1044,15 @@ static cudaError_t launch_draft_tc_t(const CUtensorMap& tmq, const CUtensorMap& 
   e = launch_pdl(kern, dim3((unsigned)a.num_ctas), dim3(dt_threads(kMx)), smem, stream, tmq, tmk, tmv, a);
   if (e != cudaSuccess || a.num_ctas == 1) return e;  // one CTA cuts nothing
   const int rows = a.max_draft * (a.num_q_heads / a.num_kv_heads);
-  const int blocks = ((rows < kTiles * kDraftRows ? rows : kTiles * kDraftRows) + 31) / 32;
-  return launch_pdl(draft_tc_reduce_kernel<D, kTiles>, dim3((unsigned)a.num_ctas, (unsigned)blocks), dim3(256),
-                    0, stream, a);
+  const int most = rows < kTiles * kDraftRows ? rows : kTiles * kDraftRows;
+  // Segments of eight pieces or more: one block would merge them one after
+  // another (one sequence of 21000 rows, one kv head, 152 pieces: 48.5 us, and
+  // 20.1 us shared).
+  if (a.num_ctas >= 8ll * a.num_seqs * a.num_kv_heads * a.row_tiles)
+    return launch_pdl(draft_tc_reduce_kernel<D, kTiles, true>, dim3((unsigned)a.num_ctas, (unsigned)((most + 3) / 4)),
+                      dim3(256), 0, stream, a);
+  return launch_pdl(draft_tc_reduce_kernel<D, kTiles, false>,
+                    dim3((unsigned)a.num_ctas, (unsigned)((most + 31) / 32)), dim3(256), 0, stream, a);
 }
 
 template <int D, bool kMx>

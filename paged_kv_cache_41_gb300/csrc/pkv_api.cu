@@ -1038,7 +1038,11 @@ pkv_status pkv_kv_evict_select(const float* weights, int64_t weights_stride,
     return PKV_ERR_INVALID_ARG;
   if (num_seqs == 0) return PKV_OK;
   if (num_seqs > 65535 || num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
+  // row numbers past the last, up to a CTA's stride, stay in 32 bits
+  if (weights_stride > 0x7fff0000 || budget > 0x7fff0000) return PKV_ERR_UNSUPPORTED;
   if (!weights || !seq_lens || !keep || !new_lens) return PKV_ERR_INVALID_ARG;
+  // the lengths are read by every CTA while one writes the new ones
+  if (new_lens < seq_lens + num_seqs && seq_lens < new_lens + num_seqs) return PKV_ERR_INVALID_ARG;
   unsigned int* err = device_error_word();
   if (!err) return PKV_ERR_CUDA;
   pkv::SelectArgs a{};
@@ -1047,7 +1051,6 @@ pkv_status pkv_kv_evict_select(const float* weights, int64_t weights_stride,
   a.keep = keep;
   a.new_lens = new_lens;
   a.err = err;
-  // a length is an int32, so nothing past INT32_MAX is ever read
   a.weights_stride = weights_stride;
   a.num_seqs = num_seqs;
   a.num_kv_heads = num_kv_heads;

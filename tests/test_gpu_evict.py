@@ -501,6 +501,19 @@ def test_compact_refuses_bad_lengths():
         assert lens == c.cache.lens
 
 
+def test_compact_refuses_a_length_near_the_end_of_32_bits():
+    # a table of 2^31 rows, of which the one kept row is in its place already
+    k, v = [torch.randn(4, 256, 1, 8, device="cuda").bfloat16() for _ in range(2)]
+    k0, v0 = k.clone(), v.clone()
+    tables = torch.zeros(1, 2**23, dtype=torch.int32, device="cuda")
+    one = torch.ones(1, dtype=torch.int32, device="cuda")
+    for n, err in ((2**31 - 2**16, 0), (2**31 - 2**16 + 1, pkv.DEVERR_LENGTH)):
+        pkv.kv_compact(k, v, tables, torch.tensor([n], dtype=torch.int32, device="cuda"),
+                       torch.zeros(1, 1, 1, dtype=torch.int32, device="cuda"), one)
+        assert pkv.get_device_error() == err
+    assert torch.equal(k, k0) and torch.equal(v, v0)
+
+
 def test_compact_bad_block():
     c = Compact([200, 60], [50, 20], seed=8, pattern="last", weights=False)
     good = c.cache.tables_np[0, 1]

@@ -98,6 +98,14 @@ def test_select_arguments(lib, kw, want):
     assert select(lib, **kw) == want
 
 
+def test_select_refuses_new_lengths_over_the_old_and_rows_past_32_bits(lib):
+    for off in (-4, 0, 4):  # two sequences: eight bytes each
+        assert select(lib, new=P((1 << 20) + off)) == BAD
+    far = P(1 << 21)
+    assert select(lib, stride=2**31 - 2**16 + 1, new=far) == UNSUP
+    assert select(lib, budget=2**31 - 2**16 + 1, new=far) == UNSUP
+
+
 def compact(lib, c=None, k=A, v=A, w=None, stride=0, tables=A, mb=4, lens=A, base=None, keep=A, heads=2,
             ks=10, kl=A, b=2):
     c = c or desc()

@@ -447,6 +447,16 @@ def _launch_place(stream, *tensors):
     return torch._C._cuda_getCurrentRawStream(dev)
 
 
+def _empty(stream, shape, dtype, device):
+    """torch.empty for a launch on ``stream`` (None: the current one): memory
+    that another stream's allocator pool owned could be taken back, or still be
+    in use there, while the launch runs."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=device)
+
+
 def _io_dtype(desc):
     return torch.float32 if desc.dtype == PKV_F32 else torch.bfloat16
 
@@ -491,7 +501,7 @@ def draft_tree_attention(q, k_cache, v_cache, block_tables, ctx_lens, draft_ptr,
     if masks is not None:
         _dense("masks", masks, torch.int64, (rows,))
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(stream, q.shape, q.dtype, q.device)
     else:
         _dense("out", out, q.dtype, (rows, hq, d))
     if lse is not None:
@@ -501,7 +511,7 @@ def draft_tree_attention(q, k_cache, v_cache, block_tables, ctx_lens, draft_ptr,
     lib = load_library()
     if workspace is None and b:
         need = lib.pkv_draft_tree_workspace_bytes(ctypes.byref(desc), b, hq, max_draft, max_blocks)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        workspace = _empty(stream, need, torch.uint8, q.device) if need else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib.pkv_draft_tree_attention(
         ctypes.byref(desc), out.data_ptr(), lse.data_ptr() if lse is not None else None,
@@ -532,7 +542,7 @@ def paged_attention_decode_weights(q, k_cache, v_cache, block_tables, seq_lens, 
     _dense("seq_lens", seq_lens, torch.int32, (b,))
     stride = _score_rows("weights", weights, b, desc.num_kv_heads)
     if out is None:
-        out = torch.empty_like(q)
+        out = _empty(stream, q.shape, q.dtype, q.device)
     else:
         _dense("out", out, q.dtype, (b, hq, d))
     if lse is not None:
@@ -542,7 +552,7 @@ def paged_attention_decode_weights(q, k_cache, v_cache, block_tables, seq_lens, 
     lib = load_library()
     if workspace is None and b:
         need = lib.pkv_decode_weights_workspace_bytes(ctypes.byref(desc), b, hq, max_blocks)
-        workspace = torch.empty(need, dtype=torch.uint8, device=q.device) if need else None
+        workspace = _empty(stream, need, torch.uint8, q.device) if need else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
     _check(lib.pkv_paged_attention_decode_weights(
         ctypes.byref(desc), out.data_ptr(), lse.data_ptr() if lse is not None else None,
@@ -563,11 +573,11 @@ def kv_evict_select(weights, seq_lens, budget, *, num_sinks=0, num_recent=0, kee
     _dense("seq_lens", seq_lens, torch.int32, (b,))
     stride = _score_rows("weights", weights, b, hkv)
     if keep is None:
-        keep = torch.empty(b, hkv, max(int(budget), 0), dtype=torch.int32, device=weights.device)
+        keep = _empty(stream, (b, hkv, max(int(budget), 0)), torch.int32, weights.device)
     else:
         _dense("keep", keep, torch.int32, (b, hkv, budget))
     if new_lens is None:
-        new_lens = torch.empty_like(seq_lens)
+        new_lens = _empty(stream, (b,), torch.int32, seq_lens.device)
     else:
         _dense("new_lens", new_lens, torch.int32, (b,))
     where = _launch_place(stream, weights, seq_lens, keep, new_lens)

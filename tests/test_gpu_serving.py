@@ -98,3 +98,77 @@ def test_speculate_commit_weigh_evict(dtype, hq, hkv, d):
                 assert np.array_equal(x, y)
         lens = [int(x) for x in new]
         assert pkv.get_device_error() == 0
+
+
+class Small:
+    """Inputs of every operator over one small cache."""
+
+    def __init__(self, seed, dtype="bf16"):
+        lens, n = [300, 33, 700], [5, 0, 17]
+        self.c = su.Cache([t + m for t, m in zip(lens, n)], dtype=dtype, hkv=2, d=128, p=16, seed=seed)
+        self.lens = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        self.ptr = torch.tensor(np.concatenate([[0], np.cumsum(n)]), dtype=torch.int32, device="cuda")
+        rng = np.random.default_rng(seed)
+        self.masks = su.as_int64(sum((su.tree_masks(m, rng) for m in n if m), [])).cuda()
+        self.q = self.c.randn(sum(n), 8, 128)
+        self.q1 = self.c.randn(3, 8, 128)
+        self.w0 = torch.rand(3, 2, 720, device="cuda")
+        self.scale = su.softmax_scale(128)
+
+    def run(self, stream=None, ws=(None, None)):
+        c, w = self.c, self.w0.clone()
+        if stream is not None:
+            stream.wait_stream(torch.cuda.current_stream())
+        out = pkv.draft_tree_attention(self.q, c.k, c.v, c.tables, self.lens, self.ptr, self.scale, max_draft=17,
+                                       masks=self.masks, workspace=ws[0], stream=stream)
+        out1 = pkv.paged_attention_decode_weights(self.q1, c.k, c.v, c.tables, self.lens, w, self.scale,
+                                                  workspace=ws[1], stream=stream)
+        keep, new = pkv.kv_evict_select(w, self.lens, 200, num_sinks=4, num_recent=20, stream=stream)
+        return out, out1, keep, new, w
+
+    def workspaces(self):
+        k, nb = self.c.k, self.c.tables.shape[1]
+        return [torch.empty(n, dtype=torch.uint8, device="cuda") for n in
+                (pkv.draft_tree_workspace_bytes(k, 3, 8, 17, nb), pkv.decode_weights_workspace_bytes(k, 3, 8, nb))]
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "mxfp8"])
+def test_results_belong_to_the_launching_stream(dtype):
+    x = Small(4, dtype)
+    want = x.run()
+    torch.cuda.synchronize()
+    s = torch.cuda.Stream()
+    got = x.run(s)
+    owners = {}
+    for seg in torch.cuda.memory_snapshot():
+        for t in got[:4]:
+            if seg["address"] <= t.data_ptr() < seg["address"] + seg["total_size"]:
+                owners[t.data_ptr()] = seg["stream"]
+    s.synchronize()
+    assert sorted(owners) == sorted(t.data_ptr() for t in got[:4])
+    assert set(owners.values()) == {s.cuda_stream}
+    for a, b in zip(want, got):
+        assert torch.equal(a, b)
+
+
+def test_two_graphs_replayed_at_once():
+    xs = [Small(5), Small(6, "mxfp8")]
+    want = [x.run() for x in xs]
+    torch.cuda.synchronize()
+    graphs, got = [], []
+    for x in xs:
+        ws = x.workspaces()  # one for each graph
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            got.append(x.run(ws=ws))
+        graphs.append((g, ws))
+    streams = [torch.cuda.Stream() for _ in xs]
+    for _ in range(20):
+        for (g, _), s in zip(graphs, streams):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    assert pkv.get_device_error() == 0
+    for a, b in zip(want, got):
+        for t, u in zip(a, b):
+            assert torch.equal(t, u)

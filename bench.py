@@ -488,10 +488,10 @@ def run_pkv(args, rank, world, local):
 
     peak, peak_kind = load_peaks()
     achieved = kv_bytes / (decode_ms * 1e-3) / 1e9
-    summaries = {"llama": ("decode.cu", "decode_partial_llama.md"),
-                 "llama_mxfp8": ("decode.cu", "decode_partial_mxfp8.md"),
-                 "long_bs16": ("decode.cu", "decode_partial_long_bs16.md"),
-                 "long_bs64": ("decode.cu", "decode_partial_long_bs64.md"),
+    summaries = {"llama": ("decode_partial.cuh", "decode_partial_llama.md"),
+                 "llama_mxfp8": ("decode_partial.cuh", "decode_partial_mxfp8.md"),
+                 "long_bs16": ("decode_partial.cuh", "decode_partial_long_bs16.md"),
+                 "long_bs64": ("decode_partial.cuh", "decode_partial_long_bs64.md"),
                  "gqa8": ("decode_tc.cu", "decode_tc_gqa8.md"),
                  "gqa8_mxfp8": ("decode_tc_mx.cu", "decode_tc_mx_gqa8.md")}
     traffic = (kernel_traffic(*summaries[args.workload]) if args.workload in summaries and

@@ -417,9 +417,8 @@ def chunk_tree_attention(q, k_cache, v_cache, plan: ChunkTreePlan, scale, *, out
 
 
 def _dense(name, t, dtype, shape):
-    """Check a tensor argument; ``shape`` entries of None match any size."""
-    if t.dtype != dtype or not t.is_contiguous() or (t.shape != shape and (
-            t.dim() != len(shape) or any(w is not None and w != n for w, n in zip(shape, t.shape)))):
+    """Check a tensor argument."""
+    if t.dtype != dtype or t.shape != shape or not t.is_contiguous():
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of shape {shape}, "
                          f"got {t.dtype} {tuple(t.shape)}")
 
@@ -494,8 +493,8 @@ def draft_tree_attention(q, k_cache, v_cache, block_tables, ctx_lens, draft_ptr,
     desc = _pair_desc(k_cache, v_cache)
     rows, hq, d = q.shape
     b, max_blocks = block_tables.shape
-    _dense("q", q, _io_dtype(desc), (None, None, desc.head_dim))
-    _dense("block_tables", block_tables, torch.int32, (None, None))
+    _dense("q", q, _io_dtype(desc), (rows, hq, desc.head_dim))
+    _dense("block_tables", block_tables, torch.int32, (b, max_blocks))
     _dense("ctx_lens", ctx_lens, torch.int32, (b,))
     _dense("draft_ptr", draft_ptr, torch.int32, (b + 1,))
     if masks is not None:
@@ -536,9 +535,9 @@ def paged_attention_decode_weights(q, k_cache, v_cache, block_tables, seq_lens, 
     head.  Returns out (and writes lse [B, Hq] float32 when given)."""
     desc = _pair_desc(k_cache, v_cache)
     b, hq, d = q.shape
-    max_blocks = block_tables.shape[1]
-    _dense("q", q, _io_dtype(desc), (None, None, desc.head_dim))
-    _dense("block_tables", block_tables, torch.int32, (b, None))
+    _, max_blocks = block_tables.shape
+    _dense("q", q, _io_dtype(desc), (b, hq, desc.head_dim))
+    _dense("block_tables", block_tables, torch.int32, (b, max_blocks))
     _dense("seq_lens", seq_lens, torch.int32, (b,))
     stride = _score_rows("weights", weights, b, desc.num_kv_heads)
     if out is None:
@@ -595,9 +594,10 @@ def kv_compact(k_cache, v_cache, block_tables, seq_lens, keep, keep_lens, *, bas
     head; keep_lens: int32 [B]; base_lens: int32 [B] or None (0)."""
     desc = _pair_desc(k_cache, v_cache)
     b, max_blocks = block_tables.shape
-    _dense("block_tables", block_tables, torch.int32, (None, None))
+    _, keep_heads, places = keep.shape
+    _dense("block_tables", block_tables, torch.int32, (b, max_blocks))
     _dense("seq_lens", seq_lens, torch.int32, (b,))
-    _dense("keep", keep, torch.int32, (b, None, None))
+    _dense("keep", keep, torch.int32, (b, keep_heads, places))
     _dense("keep_lens", keep_lens, torch.int32, (b,))
     if base_lens is not None:
         _dense("base_lens", base_lens, torch.int32, (b,))
@@ -608,7 +608,7 @@ def kv_compact(k_cache, v_cache, block_tables, seq_lens, keep, keep_lens, *, bas
         ctypes.byref(desc), k_cache.data_ptr(), v_cache.data_ptr(),
         weights.data_ptr() if weights is not None else None, stride, block_tables.data_ptr(),
         max_blocks, seq_lens.data_ptr(), base_lens.data_ptr() if base_lens is not None else None,
-        keep.data_ptr(), keep.shape[1], keep.shape[2], keep_lens.data_ptr(), b, where),
+        keep.data_ptr(), keep_heads, places, keep_lens.data_ptr(), b, where),
         "pkv_kv_compact")
 
 

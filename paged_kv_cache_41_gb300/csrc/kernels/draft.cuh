@@ -41,7 +41,7 @@ __device__ __forceinline__ uint64_t draft_mask(const DraftArgs& a, const DraftSe
 }
 
 // The work list of plan.cuh: a sequence's rows, and its segments.
-__device__ __forceinline__ int plan_len(const DraftArgs& a, int r, bool report) {
+__device__ __forceinline__ int plan_len(const DraftArgs& a, int r, int, bool report) {
   const DraftSeq s = draft_seq(a, r, report);
   return s.n > 0 ? s.ctx + s.n : 0;
 }

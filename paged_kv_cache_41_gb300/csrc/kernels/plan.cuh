@@ -31,8 +31,8 @@ __host__ __device__ __forceinline__ long long units_per_cta(long long S, int C, 
 
 // What the split asks of a work list: a sequence's rows (0: no segment) and its
 // segments.
-__device__ __forceinline__ int plan_len(const DecodeArgs& a, int r, bool report) {
-  return effective_len(__ldg(a.seq_lens + r), a.max_blocks, a.block_size, a.err, report);
+__device__ __forceinline__ int plan_len(const DecodeArgs& a, int r, int block_size, bool report) {
+  return effective_len(__ldg(a.seq_lens + r), a.max_blocks, block_size, a.err, report);
 }
 __device__ __forceinline__ int plan_heads(const DecodeArgs& a) { return a.num_kv_heads; }
 
@@ -53,7 +53,7 @@ __device__ __forceinline__ int plan_cta_stages(const Args& a, long long* wsum, i
   constexpr int kWarps = kThreads / 32;
   constexpr int kChunk = kThreads * kPer;
   const int c = blockIdx.x, C = a.num_ctas;
-  const int B = a.num_seqs, Hkv = plan_heads(a);
+  const int B = a.num_seqs, P = a.block_size, Hkv = plan_heads(a);
   const long long su = a.stage_units, pu = a.piece_units;
   const bool weighted = su != 1 || pu != 0;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -69,7 +69,9 @@ __device__ __forceinline__ int plan_cta_stages(const Args& a, long long* wsum, i
 #pragma unroll
     for (int j = 0; j < kPer; ++j) {
       const int r = base + threadIdx.x * kPer + j;
-      nt[j] = r < B ? (plan_len(a, r, report) + kRows - 1) / kRows : 0;
+      nt[j] = r < B ? (plan_len(a, r, P, report) +
+                       kRows - 1) / kRows
+                    : 0;
       mu += nt[j] > 0 ? su * nt[j] + pu : 0;
       ms += nt[j];
     }

@@ -71,7 +71,16 @@ constexpr int kDtJob = 64;           // keys of a job
 // second 32's weights come first then, and the first 32 are read again) where
 // the widening warps leave fewer registers.
 constexpr int dt_chunk(bool mx) { return mx ? 32 : 64; }
-constexpr int kDtDescs = 8;          // stage descriptors in flight
+// Stage descriptors in flight.  A bf16 stage is described when its ring tiles
+// are free.  An MXFP8 one is described once the stage kDtAhead before it has
+// been widened; the widening warps send for its codes and then wait for the
+// tiles themselves (12 requests, 64 query heads: 90.7 us, described as bf16's 96).  So when stage n is
+// described, stage n - 2 has been widened, into a ring of 12 tiles at most: the
+// PVs of stage n - 8 are done, and a softmax group, which may be a stage without
+// a job of its own behind (the end of a piece, where the groups meet), has read
+// stage n - 10's descriptor.
+constexpr int dt_descs(bool mx) { return mx ? 10 : 8; }
+constexpr int kDtAhead = 2;
 constexpr float kDtLn2 = 0.6931471805599453f;
 
 // Stage descriptor flags.
@@ -100,8 +109,8 @@ struct DtSmem {
   static constexpr int ring_off = kTiles * kTile;
   static constexpr int exch_off = ring_off + kItems * kTile;  // [2][128] (m, l); the plan's scratch
   static constexpr int desc_off = exch_off + 2 * 128 * 8;
-  static constexpr int bar_off = desc_off + kDtDescs * (int)sizeof(DtDesc);
-  static constexpr int bad_off = bar_off + (2 * kItems + kDtDescs + 17) * 8;
+  static constexpr int bar_off = desc_off + dt_descs(true) * (int)sizeof(DtDesc);
+  static constexpr int bad_off = bar_off + (2 * kItems + dt_descs(true) + 17 + kDtAhead) * 8;
   static constexpr int tmem_off = bad_off + 65 * 4;
   static constexpr int total = tmem_off + 4;
   static_assert(total <= 227 * 1024, "shared memory of one CTA");
@@ -160,6 +169,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
   using L = DtSmem<D, kTiles>;
   constexpr int H = D / 64;
   constexpr int kItems = L::kItems;
+  constexpr int kDescs = dt_descs(kMx);
   constexpr int kGroupBytes = kRowGroup * H * 128;  // one 8-row group of a K/V tile
   constexpr int kRecRows = kTiles * kDraftRows;
   extern __shared__ __align__(1024) unsigned char dt_smem[];
@@ -171,7 +181,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
   uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::bar_off);  // a ring tile landed
   uint64_t* freeb = full + kItems;    // its MMAs completed (two commits)
   uint64_t* dfull = freeb + kItems;   // a descriptor was written
-  uint64_t* qfull = dfull + kDtDescs; // a piece's Q landed
+  uint64_t* qfull = dfull + kDescs;   // a piece's Q landed
   uint64_t* qfree = qfull + 1;        // its QKs completed (a commit per group)
   uint64_t* sfull = qfree + 1;        // [group][buffer] S written
   uint64_t* pfull = sfull + 4;        // [group][buffer] P written
@@ -180,6 +190,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
   uint64_t* ofree = oend + 1;         // both groups read its O
   uint64_t* xsync = ofree + 1;        // the groups meet at a piece's end
   uint64_t* vclean = xsync + 1;       // [2] group 0 cleared a tail stage's V for both
+  uint64_t* widened = vclean + 2;     // [kDtAhead] MXFP8: a stage has been widened
   // a piece's drafted rows with non-finite V: [0] the last such piece, [1 + j]
   // the last piece whose row j was one (pieces count from 1)
   volatile int* bad = reinterpret_cast<volatile int*>(sm + L::bad_off);
@@ -194,7 +205,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
       mbar_init(&full[i], kMx ? kDtWidenWarps : 1);
       mbar_init(&freeb[i], 2);
     }
-    for (int i = 0; i < kDtDescs; ++i) mbar_init(&dfull[i], 1);
+    for (int i = 0; i < kDescs; ++i) mbar_init(&dfull[i], 1);
     mbar_init(qfull, 1);
     mbar_init(qfree, 2);
     for (int i = 0; i < 4; ++i) {
@@ -205,6 +216,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
       mbar_init(&pvdone[x], 1);
       mbar_init(&vclean[x], 4);
     }
+    for (int i = 0; i < kDtAhead; ++i) mbar_init(&widened[i], kDtWidenWarps);
     mbar_init(oend, 2);
     mbar_init(ofree, kDtSoftWarps);
     mbar_init(xsync, kDtSoftWarps);
@@ -282,19 +294,18 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
       q_wanted = false;
       return true;
     };
-    // all lanes: wait until the next ring slot may be written
+    // all lanes: wait for a barrier, and load the wanted Q meanwhile
     int slot = 0;
     uint32_t round = 0;
-    auto wait_slot = [&]() -> bool {
+    auto wait_for = [&](uint64_t* bar, uint32_t n) -> bool {  // the barrier's phase n - 1, none for 0
       int good = 1;
       if (lane == 0) {
         try_q(false);
-        if (round > 0) {
+        if (n > 0) {
           const uint64_t t0 = global_timer_ns();
-          while (q_wanted && !(good = mbar_test(&freeb[slot], (round - 1) & 1)) &&
-                 global_timer_ns() - t0 <= kWaitLimitNs)
+          while (q_wanted && !(good = mbar_test(bar, (n - 1) & 1)) && global_timer_ns() - t0 <= kWaitLimitNs)
             try_q(false);
-          good = mbar_wait(&freeb[slot], (round - 1) & 1);
+          good = mbar_wait(bar, (n - 1) & 1);
         }
       }
       return __shfl_sync(0xffffffffu, good, 0) != 0;
@@ -302,13 +313,12 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
     struct Boxes {
       int group, n, head;  // first row group, boxes, kv head
     };
-    // fill the next ring slot; for MXFP8, only see that it may be written
+    // fill the next ring slot
     auto load = [&](const CUtensorMap* tm, const Boxes& x) -> bool {
-      if (!wait_slot()) return false;
-      if (kMx) {
-      } else if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(x.n * TB * D * 2));
+      if (!wait_for(&freeb[slot], round)) return false;
+      if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(x.n * TB * D * 2));
       __syncwarp();
-      if (!kMx && j < x.n)
+      if (j < x.n)
         tma_load_5d(ring + slot * L::kTile + j * TB * H * 128, tm, 0, 0, 0, x.head, x.group, &full[slot]);
       ++item;
       if (++slot == kItems) {
@@ -360,10 +370,10 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
       }
       auto describe = [&](int seq, int seg, int mb) {
         if (lane == 0) {
-          DtDesc* d = &descs[emitted % kDtDescs];
+          DtDesc* d = &descs[emitted % kDescs];
           d->a = make_int4(seq, seg, nvalid, flags);
           d->b = make_int4(mb, row0, rows, pieces);
-          mbar_arrive(&dfull[emitted % kDtDescs]);
+          mbar_arrive(&dfull[emitted % kDescs]);
         }
       };
       const int seq = r, seg = h, mb = s.ctx - t0;
@@ -373,20 +383,21 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
         if (++i == nt) next_segment();
         blk_next = box_block();
       }
-      if (!load(&tmk, b) || !load(&tmv, b)) {
-        ok = false;
-        break;
+      if constexpr (kMx) {
+        ok = wait_for(&widened[emitted % kDtAhead], (uint32_t)emitted / kDtAhead);
+        if (ok) describe(seq, seg, mb);
+      } else {
+        ok = load(&tmk, b) && load(&tmv, b);
       }
-      // the widening warps fill a stage's slots once they see it
-      if (kMx) describe(seq, seg, mb);
+      if (!ok) break;
       ++emitted;
     }
     if (lane == 0) {
       a.cut_segs[c] = cut;
       if (ok) ok = try_q(true);
       if (ok) {
-        descs[emitted % kDtDescs].a = make_int4(0, 0, 0, kDtDone);
-        mbar_arrive(&dfull[emitted % kDtDescs]);
+        descs[emitted % kDescs].a = make_int4(0, 0, 0, kDtDone);
+        mbar_arrive(&dfull[emitted % kDescs]);
       } else {
         atomicOr(a.err, PKV_DEVERR_TIMEOUT);
         // copies may still be in flight into the ring and Q: wait for them
@@ -451,7 +462,10 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
     // its chunks' place in a tile: chunk q it takes goes to (q ^ turn) 16 from here on
     const uint32_t dst = (row0 / kRowGroup) * kGroupBytes + half * 1024 + (row0 & 7) * 128 +
                          ((((g & 1) * 4) ^ (row0 & 4)) << 4);
-    auto widen = [&](int item, const Codes (&x)[kSteps], const uint32_t (&sc)[kSteps]) {
+    auto widen = [&](int item, const Codes (&x)[kSteps], const uint32_t (&sc)[kSteps]) -> bool {
+      // the tile's last MMAs have read it
+      if (item >= kItems && !__all_sync(0xffffffffu, mbar_wait(&freeb[item % kItems], (item / kItems - 1) & 1)))
+        return false;
       unsigned char* tile = ring + (size_t)(item % kItems) * L::kTile + dst;
       bool rare = false;
 #pragma unroll
@@ -491,28 +505,30 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
       tc::fence_proxy_async_smem();
       __syncwarp();
       if (lane == 0) mbar_arrive(&full[item % kItems]);
+      return true;
     };
     bool ok = true, have = false;
     for (int e = 0;; ++e) {
       if (!have) {
-        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&dfull[e % kDtDescs], (e / kDtDescs) & 1)))) break;
-        const DtDesc& d = descs[e % kDtDescs];
+        if (!(ok = __all_sync(0xffffffffu, mbar_wait(&dfull[e % kDescs], (e / kDescs) & 1)))) break;
+        const DtDesc& d = descs[e % kDescs];
         if (d.a.w & kDtDone) break;
         places(d.a, d.b);
         fetch(a.k, a.k_scales, kx, ksc);
       }
       fetch(a.v, a.v_scales, vx, vsc);
-      widen(2 * e, kx, ksc);
-      have = __all_sync(0xffffffffu, mbar_test(&dfull[(e + 1) % kDtDescs], ((e + 1) / kDtDescs) & 1));
+      if (!(ok = widen(2 * e, kx, ksc))) break;
+      have = __all_sync(0xffffffffu, mbar_test(&dfull[(e + 1) % kDescs], ((e + 1) / kDescs) & 1));
       if (have) {
-        const DtDesc& d = descs[(e + 1) % kDtDescs];
+        const DtDesc& d = descs[(e + 1) % kDescs];
         have = !(d.a.w & kDtDone);
         if (have) {
           places(d.a, d.b);
           fetch(a.k, a.k_scales, kx, ksc);
         }
       }
-      widen(2 * e + 1, vx, vsc);
+      if (!(ok = widen(2 * e + 1, vx, vsc))) break;
+      if (lane == 0) mbar_arrive(&widened[e % kDtAhead]);
     }
     if (!ok && lane == 0) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
   } else if (warp >= kDtSoftWarps) {
@@ -564,14 +580,14 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
         }
       };
       for (int e = 0; ok; ++e) {
-        uint64_t* db = &dfull[e % kDtDescs];
-        if (!mbar_test(db, (e / kDtDescs) & 1)) {
+        uint64_t* db = &dfull[e % kDescs];
+        if (!mbar_test(db, (e / kDescs) & 1)) {
           // no QK can be issued ahead of the PVs that are due: issue them first
           while (pv < jn && (ok = issue_pv())) {
           }
-          if (!ok || !(ok = mbar_wait(db, (e / kDtDescs) & 1))) break;
+          if (!ok || !(ok = mbar_wait(db, (e / kDescs) & 1))) break;
         }
-        const int nvalid = descs[e % kDtDescs].a.z, fl = descs[e % kDtDescs].a.w;
+        const int nvalid = descs[e % kDescs].a.z, fl = descs[e % kDescs].a.w;
         if (fl & kDtDone) break;
         if (fl & kDtStart) {
           first = true;
@@ -647,8 +663,8 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
       return __all_sync(0xffffffffu, mbar_wait(b, parity));
     };
     for (int e = 0;; ++e) {
-      if (!(ok = wait(&dfull[e % kDtDescs], (e / kDtDescs) & 1))) break;
-      const int4 da = descs[e % kDtDescs].a, db = descs[e % kDtDescs].b;
+      if (!(ok = wait(&dfull[e % kDescs], (e / kDescs) & 1))) break;
+      const int4 da = descs[e % kDescs].a, db = descs[e % kDescs].b;
       const int fl = da.w;
       if (fl & kDtDone) break;
       const bool pair = kTiles > 1 && (fl & kDtPair);

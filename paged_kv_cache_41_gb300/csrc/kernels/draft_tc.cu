@@ -64,8 +64,16 @@ namespace {
 
 constexpr int kDtSoftWarps = 8;      // two groups of four
 constexpr int kDtWidenWarps = 8;     // MXFP8 pools
-// ..., an MMA warp for each, producer, and for MXFP8 the widening warps
-constexpr int dt_threads(bool mx) { return (kDtSoftWarps + 3 + (mx ? kDtWidenWarps : 0)) * 32; }
+// ..., an MMA warp for each, producer, and for MXFP8 an idle warp (registers
+// move between whole warpgroups) and the widening warps
+constexpr int kDtWidenFirst = kDtSoftWarps + 4;
+constexpr int dt_threads(bool mx) { return (mx ? kDtWidenFirst + kDtWidenWarps : kDtSoftWarps + 3) * 32; }
+// Registers a thread of the MXFP8 kernel: 96 at launch (20 warps), of which the
+// others give some to the softmax warps, whose loop spilled into L2 (the L1 is
+// shared memory here; 12 requests: 90.7 us, 73.7 so): 128 x 64 + 256 x 120 + 256 x 88 = 640 x 96.
+constexpr int kDtMxRegs = 96, kDtMxIssueRegs = 64, kDtMxWidenRegs = 88, kDtMxSoftRegs = 120;
+static_assert(128 * kDtMxIssueRegs + 256 * kDtMxSoftRegs + 256 * kDtMxWidenRegs <= dt_threads(true) * kDtMxRegs,
+              "the warpgroups' registers come from the launch's");
 constexpr int kDtJob = 64;           // keys of a job
 // Columns of S that a softmax thread holds at once: a job's 64, or 32 (the
 // second 32's weights come first then, and the first 32 are read again) where
@@ -120,6 +128,16 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// All warps of a warpgroup: from now on each thread has kRegs registers.
+template <int kRegs>
+__device__ __forceinline__ void give_registers() {
+  asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kRegs));
+}
+template <int kRegs>
+__device__ __forceinline__ void take_registers() {
+  asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kRegs));
 }
 
 // A scale group's E4M3 codes.
@@ -243,7 +261,10 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
 
   if (n <= 0) {
     if (t == 0) a.cut_segs[c] = make_int2(-1, 0);  // nothing to do
+  } else if (kMx && warp == kDtSoftWarps + 3) {
+    give_registers<kDtMxIssueRegs>();
   } else if (warp == kDtSoftWarps + 2) {
+    if (kMx) give_registers<kDtMxIssueRegs>();
     // ============================================================ producer
     const int TB = draft_tc_box_rows(P);  // rows per box
     const int j = lane;                   // this lane's box
@@ -407,14 +428,15 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
         if (pieces > 0 && !q_wanted) mbar_wait(qfull, (pieces - 1) & 1);
       }
     }
-  } else if (kMx && warp > kDtSoftWarps + 2) {
+  } else if (kMx && warp >= kDtWidenFirst) {
     // ============================================================ widening
+    give_registers<kDtMxWidenRegs>();
     // A thread takes a scale group, 32 codes, of a row: step i of a tile covers
     // rows kStep i .. of it.  It takes its four chunks of eight codes in an
     // order, `turn`, that puts the stores of eight threads in a row into eight
     // bank groups.  The next tile's loads are out while a tile is widened.
     constexpr int kPerRow = D / 32, kStep = kDtWidenWarps * 32 / kPerRow, kSteps = kDraftKeys / kStep;
-    const int wt = t - (kDtSoftWarps + 3) * 32;
+    const int wt = t - kDtWidenFirst * 32;
     const int g = wt % kPerRow, row0 = wt / kPerRow, half = g >> 1, turn = (row0 & 3) ^ (2 * half);
     const int shift = (P & (P - 1)) == 0 ? 31 - __clz(P) : -1;  // of a power-of-two block size
     int64_t at[kSteps], sat[kSteps];  // this thread's groups in the code planes (-1: none) and the scale planes
@@ -533,6 +555,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
     if (!ok && lane == 0) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
   } else if (warp >= kDtSoftWarps) {
     // ============================================================ MMA issue
+    if (kMx) give_registers<kDtMxIssueRegs>();
     const int x = warp - kDtSoftWarps;  // of this group's jobs; job j uses S buffer j & 1
     if (tc::elect_one()) {
       const uint32_t idqk = tc::idesc_bf16_f32(kDraftRows, kDtJob, 0, 0) |
@@ -647,6 +670,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
     }
   } else {
     // ============================================================ softmax
+    if (kMx) take_registers<kDtMxSoftRegs>();
     const int x = warp >> 2;
     const int row = (warp & 3) * 32 + lane;  // row of the tile = TMEM lane
     const uint32_t lane_base = (uint32_t)((warp & 3) * 32) << 16;

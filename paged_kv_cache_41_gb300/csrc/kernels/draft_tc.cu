@@ -13,7 +13,8 @@
 // query and 8 kv heads: 16 requests with trees of 5 to 27 67 us (4.3 TB/s over
 // the call, 6.4 in the steady state); 64 requests with trees of 64 283 us (1046
 // TFLOP/s), where the exponentials beside the MMAs bound it; MXFP8, 64 query
-// heads, 12 requests 96 us, where the widening warps do.
+// heads, 12 requests 72 us, where the widening and the softmax warps' latencies
+// do.
 //
 // Design:
 //   * the work split, the pieces and their records are the decode's
@@ -439,7 +440,8 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
     const int wt = t - kDtWidenFirst * 32;
     const int g = wt % kPerRow, row0 = wt / kPerRow, half = g >> 1, turn = (row0 & 3) ^ (2 * half);
     const int shift = (P & (P - 1)) == 0 ? 31 - __clz(P) : -1;  // of a power-of-two block size
-    int64_t at[kSteps], sat[kSteps];  // this thread's groups in the code planes (-1: none) and the scale planes
+    int64_t at[kSteps];  // this thread's groups in the code planes (-1: none), and
+    int sat[kSteps];     // how much further on they are in the scale planes
     Codes kx[kSteps], vx[kSteps];
     uint32_t ksc[kSteps], vsc[kSteps];
     int seq = -1, ctx = 0;
@@ -462,7 +464,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
       for (int i = 0; i < kSteps; ++i) {
         const int64_t base = (int64_t)blk[i] * P * Hkv;  // rows of one head before the block
         at[i] = (base + off[i] * Hkv + kvh) * (D / 32) + g;
-        sat[i] = (base + kvh * P + off[i]) * (D / 32) + g;
+        sat[i] = (kvh * P + off[i] - (off[i] * Hkv + kvh)) * (D / 32);
         if (blk[i] < 0 || (int64_t)blk[i] >= a.num_blocks) {
           if (blk[i] != -2 && g == 0) atomicOr(a.err, PKV_DEVERR_BLOCK);
           at[i] = -1;
@@ -474,7 +476,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
       for (int i = 0; i < kSteps; ++i) {
         if (at[i] >= 0) {
           x[i] = load_codes(static_cast<const uint8_t*>(pool) + at[i] * 32, half);
-          sc[i] = __ldg(scales + sat[i]);
+          sc[i] = __ldg(scales + at[i] + sat[i]);
         } else {  // rows past the last one, and of bad blocks
           x[i] = Codes{};
           sc[i] = 0;

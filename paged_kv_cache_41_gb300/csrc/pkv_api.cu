@@ -839,9 +839,10 @@ DraftWorkspace draft_workspace(const pkv_cache_desc* c, int32_t num_seqs, int32_
     // Work units (kernels/plan.cuh).  A least-squares fit of the CTAs' times
     // gave a piece (its Q, the drained pipeline, its outputs) 0.8 stages with
     // one row tile (16 requests, trees of 5 to 27) and 3.4 with two (64
-    // requests, trees of 64); an MXFP8 pool's stages take five times as long.
+    // requests, trees of 64).  An MXFP8 pool's stages take several times as
+    // long: 12 requests, two row tiles, 73.3, 71.9 and 72.3 us for 1, 2 and 3.
     w.stage_units = 2;
-    w.piece_units = c->dtype == PKV_MXFP8 ? 1 : w.tiles > 1 ? 7 : 2;
+    w.piece_units = w.tiles > 1 && c->dtype != PKV_MXFP8 ? 7 : 2;
     // As many CTAs as make a share one stage, where that is fewer than the SMs:
     // a CTA less gives some two (one sequence of 304 rows: 14.7 us, 13.0 so).
     const int64_t keys = (int64_t)max_blocks * c->block_size;

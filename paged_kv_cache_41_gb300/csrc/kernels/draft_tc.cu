@@ -71,7 +71,8 @@ constexpr int kDtWidenFirst = kDtSoftWarps + 4;
 constexpr int dt_threads(bool mx) { return (mx ? kDtWidenFirst + kDtWidenWarps : kDtSoftWarps + 3) * 32; }
 // Registers a thread of the MXFP8 kernel: 96 at launch (20 warps), of which the
 // others give some to the softmax warps, whose loop spilled into L2 (the L1 is
-// shared memory here; 12 requests: 90.7 us, 73.7 so): 128 x 64 + 256 x 120 + 256 x 88 = 640 x 96.
+// shared memory here; 12 requests: 90.7 us, 73.7 so): 128 x 64 + 256 x 120 +
+// 256 x 88 = 640 x 96.
 constexpr int kDtMxRegs = 96, kDtMxIssueRegs = 64, kDtMxWidenRegs = 88, kDtMxSoftRegs = 120;
 static_assert(128 * kDtMxIssueRegs + 256 * kDtMxSoftRegs + 256 * kDtMxWidenRegs <= dt_threads(true) * kDtMxRegs,
               "the warpgroups' registers come from the launch's");
@@ -83,11 +84,11 @@ constexpr int dt_chunk(bool mx) { return mx ? 32 : 64; }
 // Stage descriptors in flight.  A bf16 stage is described when its ring tiles
 // are free.  An MXFP8 one is described once the stage kDtAhead before it has
 // been widened; the widening warps send for its codes and then wait for the
-// tiles themselves (12 requests, 64 query heads: 90.7 us, described as bf16's 96).  So when stage n is
-// described, stage n - 2 has been widened, into a ring of 12 tiles at most: the
-// PVs of stage n - 8 are done, and a softmax group, which may be a stage without
-// a job of its own behind (the end of a piece, where the groups meet), has read
-// stage n - 10's descriptor.
+// tiles themselves (12 requests, 64 query heads: 90.7 us, described as bf16's
+// 96).  So when stage n is described, stage n - 2 has been widened, into a ring
+// of 12 tiles at most: the PVs of stage n - 8 are done, and a softmax group,
+// which may be a stage without a job of its own behind (the end of a piece,
+// where the groups meet), has read stage n - 10's descriptor.
 constexpr int dt_descs(bool mx) { return mx ? 10 : 8; }
 constexpr int kDtAhead = 2;
 constexpr float kDtLn2 = 0.6931471805599453f;
@@ -1084,6 +1085,13 @@ static cudaError_t launch_draft_tc_t(const CUtensorMap& tmq, const CUtensorMap& 
                                      const DraftArgs& a, cudaStream_t stream) {
   constexpr int smem = DtSmem<D, kTiles>::total;
   auto kern = draft_tc_kernel<D, kTiles, kMx>;
+  if constexpr (kMx) {  // with fewer registers at launch the softmax warps would wait for theirs for ever
+    static const bool enough = [&] {
+      cudaFuncAttributes f;
+      return cudaFuncGetAttributes(&f, kern) == cudaSuccess && f.numRegs >= kDtMxRegs;
+    }();
+    if (!enough) return cudaErrorInvalidConfiguration;
+  }
   static SmemAttrCache attr_cache;
   cudaError_t e = ensure_smem_limit(kern, smem, attr_cache);
   if (e != cudaSuccess) return e;

@@ -263,171 +263,287 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
 
   if (n <= 0) {
     if (t == 0) a.cut_segs[c] = make_int2(-1, 0);  // nothing to do
-  } else if (kMx && warp == kDtSoftWarps + 3) {
-    give_registers<kDtMxIssueRegs>();
-  } else if (warp == kDtSoftWarps + 2) {
+  } else if (warp >= kDtSoftWarps && warp < kDtWidenFirst) {
+    // setmaxnreg is one instruction of a whole warpgroup: this one takes it
+    // together, and then its warps part (MXFP8: the fourth only for this)
     if (kMx) give_registers<kDtMxIssueRegs>();
-    // ============================================================ producer
-    const int TB = draft_tc_box_rows(P);  // rows per box
-    const int j = lane;                   // this lane's box
-    const int heads = plan_heads(a);
-    int r = d0.x, h = d0.y, i = d0.z;
-    DraftSeq s = draft_seq(a, r, false);
-    auto stages = [&]() { return s.n > 0 ? (s.ctx + s.n + kDraftKeys - 1) / kDraftKeys : 0; };
-    int nt = stages();
-    auto next_segment = [&]() {
-      i = 0;
-      if (++h == heads) {
-        h = 0;
-        do {
-          ++r;
-          s = draft_seq(a, r, false);
-          nt = stages();
-        } while (nt == 0);
-      }
-    };
-    while (i >= nt) {  // the plan may name a segment's end
-      const int over = i - nt;
-      next_segment();
-      i = over;
-    }
-    auto box_block = [&]() -> int {
-      const int row = i * kDraftKeys + j * TB;
-      return row < s.ctx + s.n && j * TB < kDraftKeys
-                 ? __ldg(a.block_tables + (int64_t)r * a.max_blocks + row / P)
-                 : 0;
-    };
-    int item = 0, pieces = 0;
-    bool q_wanted = false;  // a piece's Q is still to be loaded
-    int q_row = 0, q_head = 0, q_two = 0;
-    int2 cut = make_int2(-1, 0);  // the segment that starts here and runs on into the next CTA
-    bool ok = true;
-    // lane 0: issue the wanted Q once the previous piece's QKs have read theirs
-    auto try_q = [&](bool wait) -> bool {
-      if (!q_wanted) return true;
-      if (pieces > 1 && !(wait ? mbar_wait(qfree, (pieces - 2) & 1) : mbar_test(qfree, (pieces - 2) & 1)))
-        return !wait;
-      const int tiles = q_two ? 2 : 1;
-      mbar_arrive_expect_tx(qfull, (uint32_t)(tiles * H * a.q_tokens * G * 128));
-      for (int x = 0; x < tiles; ++x)
-#pragma unroll
-        for (int hf = 0; hf < H; ++hf)
-          tma_load_3d(qs + x * L::kTile + hf * L::kHalf, &tmq, hf * 64, q_head, q_row + x * (kDraftRows / G),
-                      qfull);
-      q_wanted = false;
-      return true;
-    };
-    // all lanes: wait for a barrier, and load the wanted Q meanwhile
-    int slot = 0;
-    uint32_t round = 0;
-    auto wait_for = [&](uint64_t* bar, uint32_t n) -> bool {  // the barrier's phase n - 1, none for 0
-      int good = 1;
-      if (lane == 0) {
-        try_q(false);
-        if (n > 0) {
-          const uint64_t t0 = global_timer_ns();
-          while (q_wanted && !(good = mbar_test(bar, (n - 1) & 1)) && global_timer_ns() - t0 <= kWaitLimitNs)
-            try_q(false);
-          good = mbar_wait(bar, (n - 1) & 1);
-        }
-      }
-      return __shfl_sync(0xffffffffu, good, 0) != 0;
-    };
-    struct Boxes {
-      int group, n, head;  // first row group, boxes, kv head
-    };
-    // fill the next ring slot
-    auto load = [&](const CUtensorMap* tm, const Boxes& x) -> bool {
-      if (!wait_for(&freeb[slot], round)) return false;
-      if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(x.n * TB * D * 2));
-      __syncwarp();
-      if (j < x.n)
-        tma_load_5d(ring + slot * L::kTile + j * TB * H * 128, tm, 0, 0, 0, x.head, x.group, &full[slot]);
-      ++item;
-      if (++slot == kItems) {
-        slot = 0;
-        ++round;
-      }
-      return true;
-    };
-    int emitted = 0;
-    int blk_next = box_block();
-    for (int k = 0; k < n;) {
-      const int mt = a.row_tiles > 1 ? h % a.row_tiles : 0;
-      const int rows = min(s.n * G - mt * kRecRows, kRecRows);
-      if (rows <= 0) {  // the sequence has no rows in this tile: pass its stages over
-        k += nt - i;
-        if (k >= n) break;
-        next_segment();
-        blk_next = box_block();
-        continue;
-      }
-      const int kvh = a.row_tiles > 1 ? h / a.row_tiles : h;
-      const int t0 = i * kDraftKeys, nvalid = min(kDraftKeys, s.ctx + s.n - t0);
-      const int dseg = k - i;  // the CTA's stage that starts the segment
-      const bool start = k == 0 || i == 0, end = k == n - 1 || i == nt - 1;
-      const bool pair = kTiles > 1 && rows > kDraftRows;
-      const int flags = (start ? kDtStart : 0) | (end ? kDtEnd : 0) |
-                        (end && i == nt - 1 && dseg >= 0 ? kDtWhole : 0) | (dseg > 0 ? kDtSlot1 : 0) |
-                        (pair ? kDtPair : 0) | (t0 + nvalid > s.ctx ? kDtTail : 0) | (s.n << kDtDraftShift);
-      const int row0 = s.row0 + mt * (kRecRows / G);
-      if (i == 0 && n - k < nt) cut = make_int2(r, h);
-      if (start) {
-        if (lane == 0 && !try_q(true)) ok = false;  // the piece before this one's, if it still waits
-        ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
-        if (!ok) break;
-        ++pieces;
-        q_wanted = true;
-        q_row = row0;
-        q_head = kvh * G;
-        q_two = pair;
-      }
-      Boxes b;
-      b.n = (nvalid + TB - 1) / TB;
-      b.head = kvh;
-      if (!kMx && j < b.n && (blk_next < 0 || (int64_t)blk_next >= a.num_blocks)) {
-        atomicOr(a.err, PKV_DEVERR_BLOCK);
-        b.group = (int)a.num_blocks * (P / kRowGroup);  // zero-filled out-of-range box
-      } else {
-        b.group = blk_next * (P / kRowGroup) + (t0 + j * TB) % P / kRowGroup;
-      }
-      auto describe = [&](int seq, int seg, int mb) {
-        if (lane == 0) {
-          DtDesc* d = &descs[emitted % kDescs];
-          d->a = make_int4(seq, seg, nvalid, flags);
-          d->b = make_int4(mb, row0, rows, pieces);
-          mbar_arrive(&dfull[emitted % kDescs]);
+    if (warp == kDtSoftWarps + 2) {
+      // ============================================================ producer
+      const int TB = draft_tc_box_rows(P);  // rows per box
+      const int j = lane;                   // this lane's box
+      const int heads = plan_heads(a);
+      int r = d0.x, h = d0.y, i = d0.z;
+      DraftSeq s = draft_seq(a, r, false);
+      auto stages = [&]() { return s.n > 0 ? (s.ctx + s.n + kDraftKeys - 1) / kDraftKeys : 0; };
+      int nt = stages();
+      auto next_segment = [&]() {
+        i = 0;
+        if (++h == heads) {
+          h = 0;
+          do {
+            ++r;
+            s = draft_seq(a, r, false);
+            nt = stages();
+          } while (nt == 0);
         }
       };
-      const int seq = r, seg = h, mb = s.ctx - t0;
-      if (!kMx) describe(seq, seg, mb);
-      ++k;
-      if (k < n) {  // the next stage's block ids, under this one's waits
-        if (++i == nt) next_segment();
-        blk_next = box_block();
+      while (i >= nt) {  // the plan may name a segment's end
+        const int over = i - nt;
+        next_segment();
+        i = over;
       }
-      if constexpr (kMx) {
-        ok = wait_for(&widened[emitted % kDtAhead], (uint32_t)emitted / kDtAhead);
-        if (ok) describe(seq, seg, mb);
-      } else {
-        ok = load(&tmk, b) && load(&tmv, b);
+      auto box_block = [&]() -> int {
+        const int row = i * kDraftKeys + j * TB;
+        return row < s.ctx + s.n && j * TB < kDraftKeys
+                   ? __ldg(a.block_tables + (int64_t)r * a.max_blocks + row / P)
+                   : 0;
+      };
+      int item = 0, pieces = 0;
+      bool q_wanted = false;  // a piece's Q is still to be loaded
+      int q_row = 0, q_head = 0, q_two = 0;
+      int2 cut = make_int2(-1, 0);  // the segment that starts here and runs on into the next CTA
+      bool ok = true;
+      // lane 0: issue the wanted Q once the previous piece's QKs have read theirs
+      auto try_q = [&](bool wait) -> bool {
+        if (!q_wanted) return true;
+        if (pieces > 1 && !(wait ? mbar_wait(qfree, (pieces - 2) & 1) : mbar_test(qfree, (pieces - 2) & 1)))
+          return !wait;
+        const int tiles = q_two ? 2 : 1;
+        mbar_arrive_expect_tx(qfull, (uint32_t)(tiles * H * a.q_tokens * G * 128));
+        for (int x = 0; x < tiles; ++x)
+#pragma unroll
+          for (int hf = 0; hf < H; ++hf)
+            tma_load_3d(qs + x * L::kTile + hf * L::kHalf, &tmq, hf * 64, q_head, q_row + x * (kDraftRows / G),
+                        qfull);
+        q_wanted = false;
+        return true;
+      };
+      // all lanes: wait for a barrier, and load the wanted Q meanwhile
+      int slot = 0;
+      uint32_t round = 0;
+      auto wait_for = [&](uint64_t* bar, uint32_t n) -> bool {  // the barrier's phase n - 1, none for 0
+        int good = 1;
+        if (lane == 0) {
+          try_q(false);
+          if (n > 0) {
+            const uint64_t t0 = global_timer_ns();
+            while (q_wanted && !(good = mbar_test(bar, (n - 1) & 1)) && global_timer_ns() - t0 <= kWaitLimitNs)
+              try_q(false);
+            good = mbar_wait(bar, (n - 1) & 1);
+          }
+        }
+        return __shfl_sync(0xffffffffu, good, 0) != 0;
+      };
+      struct Boxes {
+        int group, n, head;  // first row group, boxes, kv head
+      };
+      // fill the next ring slot
+      auto load = [&](const CUtensorMap* tm, const Boxes& x) -> bool {
+        if (!wait_for(&freeb[slot], round)) return false;
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], (uint32_t)(x.n * TB * D * 2));
+        __syncwarp();
+        if (j < x.n)
+          tma_load_5d(ring + slot * L::kTile + j * TB * H * 128, tm, 0, 0, 0, x.head, x.group, &full[slot]);
+        ++item;
+        if (++slot == kItems) {
+          slot = 0;
+          ++round;
+        }
+        return true;
+      };
+      int emitted = 0;
+      int blk_next = box_block();
+      for (int k = 0; k < n;) {
+        const int mt = a.row_tiles > 1 ? h % a.row_tiles : 0;
+        const int rows = min(s.n * G - mt * kRecRows, kRecRows);
+        if (rows <= 0) {  // the sequence has no rows in this tile: pass its stages over
+          k += nt - i;
+          if (k >= n) break;
+          next_segment();
+          blk_next = box_block();
+          continue;
+        }
+        const int kvh = a.row_tiles > 1 ? h / a.row_tiles : h;
+        const int t0 = i * kDraftKeys, nvalid = min(kDraftKeys, s.ctx + s.n - t0);
+        const int dseg = k - i;  // the CTA's stage that starts the segment
+        const bool start = k == 0 || i == 0, end = k == n - 1 || i == nt - 1;
+        const bool pair = kTiles > 1 && rows > kDraftRows;
+        const int flags = (start ? kDtStart : 0) | (end ? kDtEnd : 0) |
+                          (end && i == nt - 1 && dseg >= 0 ? kDtWhole : 0) | (dseg > 0 ? kDtSlot1 : 0) |
+                          (pair ? kDtPair : 0) | (t0 + nvalid > s.ctx ? kDtTail : 0) | (s.n << kDtDraftShift);
+        const int row0 = s.row0 + mt * (kRecRows / G);
+        if (i == 0 && n - k < nt) cut = make_int2(r, h);
+        if (start) {
+          if (lane == 0 && !try_q(true)) ok = false;  // the piece before this one's, if it still waits
+          ok = __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
+          if (!ok) break;
+          ++pieces;
+          q_wanted = true;
+          q_row = row0;
+          q_head = kvh * G;
+          q_two = pair;
+        }
+        Boxes b;
+        b.n = (nvalid + TB - 1) / TB;
+        b.head = kvh;
+        if (!kMx && j < b.n && (blk_next < 0 || (int64_t)blk_next >= a.num_blocks)) {
+          atomicOr(a.err, PKV_DEVERR_BLOCK);
+          b.group = (int)a.num_blocks * (P / kRowGroup);  // zero-filled out-of-range box
+        } else {
+          b.group = blk_next * (P / kRowGroup) + (t0 + j * TB) % P / kRowGroup;
+        }
+        auto describe = [&](int seq, int seg, int mb) {
+          if (lane == 0) {
+            DtDesc* d = &descs[emitted % kDescs];
+            d->a = make_int4(seq, seg, nvalid, flags);
+            d->b = make_int4(mb, row0, rows, pieces);
+            mbar_arrive(&dfull[emitted % kDescs]);
+          }
+        };
+        const int seq = r, seg = h, mb = s.ctx - t0;
+        if (!kMx) describe(seq, seg, mb);
+        ++k;
+        if (k < n) {  // the next stage's block ids, under this one's waits
+          if (++i == nt) next_segment();
+          blk_next = box_block();
+        }
+        if constexpr (kMx) {
+          ok = wait_for(&widened[emitted % kDtAhead], (uint32_t)emitted / kDtAhead);
+          if (ok) describe(seq, seg, mb);
+        } else {
+          ok = load(&tmk, b) && load(&tmv, b);
+        }
+        if (!ok) break;
+        ++emitted;
       }
-      if (!ok) break;
-      ++emitted;
-    }
-    if (lane == 0) {
-      a.cut_segs[c] = cut;
-      if (ok) ok = try_q(true);
-      if (ok) {
-        descs[emitted % kDescs].a = make_int4(0, 0, 0, kDtDone);
-        mbar_arrive(&dfull[emitted % kDescs]);
-      } else {
-        atomicOr(a.err, PKV_DEVERR_TIMEOUT);
-        // copies may still be in flight into the ring and Q: wait for them
-        if (!kMx)
-          for (int it = item > kItems ? item - kItems : 0; it < item; ++it)
-            mbar_wait(&full[it % kItems], (it / kItems) & 1);
-        if (pieces > 0 && !q_wanted) mbar_wait(qfull, (pieces - 1) & 1);
+      if (lane == 0) {
+        a.cut_segs[c] = cut;
+        if (ok) ok = try_q(true);
+        if (ok) {
+          descs[emitted % kDescs].a = make_int4(0, 0, 0, kDtDone);
+          mbar_arrive(&dfull[emitted % kDescs]);
+        } else {
+          atomicOr(a.err, PKV_DEVERR_TIMEOUT);
+          // copies may still be in flight into the ring and Q: wait for them
+          if (!kMx)
+            for (int it = item > kItems ? item - kItems : 0; it < item; ++it)
+              mbar_wait(&full[it % kItems], (it / kItems) & 1);
+          if (pieces > 0 && !q_wanted) mbar_wait(qfull, (pieces - 1) & 1);
+        }
+      }
+    } else if (warp < kDtSoftWarps + 2) {
+      // ============================================================ MMA issue
+      const int x = warp - kDtSoftWarps;  // of this group's jobs; job j uses S buffer j & 1
+      if (tc::elect_one()) {
+        const uint32_t idqk = tc::idesc_bf16_f32(kDraftRows, kDtJob, 0, 0) |
+                              (a.qscale < 0.f ? tc::kIdescNegateA : 0u);
+        constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kDraftRows, D, 0, 1);
+        const uint32_t tS = tmem + x * 128, tO = tmem + 256 + x * 128;
+        // What a PV needs of its job is kept for the two jobs at most between
+        // their QK and their PV: flags, phase << 4, ring slot << 5 of its V.
+        constexpr uint32_t kFirst = 1, kSecond = 2, kFrees = 4;
+        uint32_t info0 = 0, info1 = 0;
+        int jn = 0, pv = 0, pieces = 0;  // QKs and PVs issued, pieces begun
+        bool first = true, freed = false;  // no job in the piece yet; O is known to be free
+        // descriptors differ in their address field alone
+        const uint64_t kdesc = tc::smem_desc_sw128(smem_u32(ring), 16, kGroupBytes);
+        const uint64_t vdesc = tc::smem_desc_sw128(smem_u32(ring), 1024, kGroupBytes);
+        const uint64_t qdesc = tc::smem_desc_sw128(smem_u32(qs), 16, 1024);
+        auto issue_pv = [&]() -> bool {  // of job pv
+          const int b = pv & 1;
+          const uint32_t q = b ? info1 : info0;
+          const uint32_t sl = q >> 5;
+          if (!mbar_wait(&full[sl], (q >> 4) & 1)) return false;
+          if (!freed) {  // the piece's first PV: the previous piece's O has been read
+            if (pieces > 1 && !mbar_wait(ofree, (pieces - 2) & 1)) return false;
+            freed = true;
+          }
+          if (!mbar_wait(&pfull[2 * x + b], (pv >> 1) & 1)) return false;
+          tc::fence_after_sync();
+          const uint64_t vd = vdesc + sl * (L::kTile >> 4) + ((q & kSecond) ? (8 * kGroupBytes) >> 4 : 0);
+#pragma unroll
+          for (int k = 0; k < kDtJob / 16; ++k)
+            tc::mma_bf16_ta(tO, tS + b * 64 + (dt_chunk(kMx) == 64 ? k * 8 : (k >> 1) * 32 + (k & 1) * 8),
+                            vd + ((k * 2 * kGroupBytes) >> 4), kIdPV,
+                            (k > 0 || !(q & kFirst)) ? 1u : 0u);
+          tc::commit(&pvdone[x]);
+          if (q & kFrees) tc::commit(&freeb[sl]);
+          ++pv;
+          return true;
+        };
+        bool ok = true;
+        uint32_t slot = 0, phase = 0;  // of the ring item that comes next
+        auto advance = [&]() {
+          if (++slot == kItems) {
+            slot = 0;
+            phase ^= 1u;
+          }
+        };
+        for (int e = 0; ok; ++e) {
+          uint64_t* db = &dfull[e % kDescs];
+          if (!mbar_test(db, (e / kDescs) & 1)) {
+            // no QK can be issued ahead of the PVs that are due: issue them first
+            while (pv < jn && (ok = issue_pv())) {
+            }
+            if (!ok || !(ok = mbar_wait(db, (e / kDescs) & 1))) break;
+          }
+          const int nvalid = descs[e % kDescs].a.z, fl = descs[e % kDescs].a.w;
+          if (fl & kDtDone) break;
+          if (fl & kDtStart) {
+            first = true;
+            freed = false;
+            if (!(ok = mbar_wait(qfull, pieces & 1))) break;
+            ++pieces;
+          }
+          const uint32_t ksl = slot, kph = phase;
+          advance();
+          const uint32_t vinfo = (slot << 5) | (phase << 4);
+          advance();
+          const bool pair = kTiles > 1 && (fl & kDtPair);
+          // halves of the stage: both in a pair, half x otherwise
+          const int u_lo = pair ? 0 : x, u_hi = pair ? (nvalid > kDtJob ? 2 : 1) : (nvalid > x * kDtJob ? x + 1 : x);
+          if (!mbar_test(&full[ksl], kph)) {
+            while (pv < jn && (ok = issue_pv())) {
+            }
+            if (!ok || !(ok = mbar_wait(&full[ksl], kph))) break;
+          }
+          for (int u = u_lo; u < u_hi; ++u) {
+            if (pv + 1 < jn && !(ok = issue_pv())) break;
+            const int b = jn & 1;
+            tc::fence_after_sync();
+            const uint64_t kd = kdesc + ksl * (L::kTile >> 4) + (u ? (8 * kGroupBytes) >> 4 : 0);
+            const uint64_t qd = qdesc + (pair ? x * (L::kTile >> 4) : 0);
+#pragma unroll
+            for (int k = 0; k < D / 16; ++k)
+              tc::mma_bf16(tS + b * 64, qd + (((k >> 2) * L::kHalf + (k & 3) * 32) >> 4),
+                           kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idqk, k > 0 ? 1u : 0u);
+            tc::commit(&sfull[2 * x + b]);
+            const bool last = u == u_hi - 1;
+            if (last) tc::commit(&freeb[ksl]);
+            const uint32_t q = vinfo | (first ? kFirst : 0) | (u ? kSecond : 0) | (last ? kFrees : 0);
+            if (b) info1 = q;
+            else info0 = q;
+            first = false;
+            ++jn;
+          }
+          if (!ok) break;
+          if (u_lo == u_hi) {  // no key of this group's half: give the stage back
+            tc::commit(&freeb[ksl]);
+            const uint32_t vsl = vinfo >> 5;
+            if (!(ok = mbar_wait(&full[vsl], (vinfo >> 4) & 1))) break;
+            tc::commit(&freeb[vsl]);
+          }
+          if (fl & kDtEnd) {
+            tc::commit(qfree);
+            while (pv < jn && (ok = issue_pv())) {
+            }
+            if (!ok) break;
+            // a piece without a job of this group must not run ahead either
+            if (!freed && pieces > 1 && !(ok = mbar_wait(ofree, (pieces - 2) & 1))) break;
+            tc::commit(oend);
+          }
+        }
+        if (!ok) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
       }
     }
   } else if (kMx && warp >= kDtWidenFirst) {
@@ -556,121 +672,6 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
       if (lane == 0) mbar_arrive(&widened[e % kDtAhead]);
     }
     if (!ok && lane == 0) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
-  } else if (warp >= kDtSoftWarps) {
-    // ============================================================ MMA issue
-    if (kMx) give_registers<kDtMxIssueRegs>();
-    const int x = warp - kDtSoftWarps;  // of this group's jobs; job j uses S buffer j & 1
-    if (tc::elect_one()) {
-      const uint32_t idqk = tc::idesc_bf16_f32(kDraftRows, kDtJob, 0, 0) |
-                            (a.qscale < 0.f ? tc::kIdescNegateA : 0u);
-      constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kDraftRows, D, 0, 1);
-      const uint32_t tS = tmem + x * 128, tO = tmem + 256 + x * 128;
-      // What a PV needs of its job is kept for the two jobs at most between
-      // their QK and their PV: flags, phase << 4, ring slot << 5 of its V.
-      constexpr uint32_t kFirst = 1, kSecond = 2, kFrees = 4;
-      uint32_t info0 = 0, info1 = 0;
-      int jn = 0, pv = 0, pieces = 0;  // QKs and PVs issued, pieces begun
-      bool first = true, freed = false;  // no job in the piece yet; O is known to be free
-      // descriptors differ in their address field alone
-      const uint64_t kdesc = tc::smem_desc_sw128(smem_u32(ring), 16, kGroupBytes);
-      const uint64_t vdesc = tc::smem_desc_sw128(smem_u32(ring), 1024, kGroupBytes);
-      const uint64_t qdesc = tc::smem_desc_sw128(smem_u32(qs), 16, 1024);
-      auto issue_pv = [&]() -> bool {  // of job pv
-        const int b = pv & 1;
-        const uint32_t q = b ? info1 : info0;
-        const uint32_t sl = q >> 5;
-        if (!mbar_wait(&full[sl], (q >> 4) & 1)) return false;
-        if (!freed) {  // the piece's first PV: the previous piece's O has been read
-          if (pieces > 1 && !mbar_wait(ofree, (pieces - 2) & 1)) return false;
-          freed = true;
-        }
-        if (!mbar_wait(&pfull[2 * x + b], (pv >> 1) & 1)) return false;
-        tc::fence_after_sync();
-        const uint64_t vd = vdesc + sl * (L::kTile >> 4) + ((q & kSecond) ? (8 * kGroupBytes) >> 4 : 0);
-#pragma unroll
-        for (int k = 0; k < kDtJob / 16; ++k)
-          tc::mma_bf16_ta(tO, tS + b * 64 + (dt_chunk(kMx) == 64 ? k * 8 : (k >> 1) * 32 + (k & 1) * 8),
-                          vd + ((k * 2 * kGroupBytes) >> 4), kIdPV,
-                          (k > 0 || !(q & kFirst)) ? 1u : 0u);
-        tc::commit(&pvdone[x]);
-        if (q & kFrees) tc::commit(&freeb[sl]);
-        ++pv;
-        return true;
-      };
-      bool ok = true;
-      uint32_t slot = 0, phase = 0;  // of the ring item that comes next
-      auto advance = [&]() {
-        if (++slot == kItems) {
-          slot = 0;
-          phase ^= 1u;
-        }
-      };
-      for (int e = 0; ok; ++e) {
-        uint64_t* db = &dfull[e % kDescs];
-        if (!mbar_test(db, (e / kDescs) & 1)) {
-          // no QK can be issued ahead of the PVs that are due: issue them first
-          while (pv < jn && (ok = issue_pv())) {
-          }
-          if (!ok || !(ok = mbar_wait(db, (e / kDescs) & 1))) break;
-        }
-        const int nvalid = descs[e % kDescs].a.z, fl = descs[e % kDescs].a.w;
-        if (fl & kDtDone) break;
-        if (fl & kDtStart) {
-          first = true;
-          freed = false;
-          if (!(ok = mbar_wait(qfull, pieces & 1))) break;
-          ++pieces;
-        }
-        const uint32_t ksl = slot, kph = phase;
-        advance();
-        const uint32_t vinfo = (slot << 5) | (phase << 4);
-        advance();
-        const bool pair = kTiles > 1 && (fl & kDtPair);
-        // halves of the stage: both in a pair, half x otherwise
-        const int u_lo = pair ? 0 : x, u_hi = pair ? (nvalid > kDtJob ? 2 : 1) : (nvalid > x * kDtJob ? x + 1 : x);
-        if (!mbar_test(&full[ksl], kph)) {
-          while (pv < jn && (ok = issue_pv())) {
-          }
-          if (!ok || !(ok = mbar_wait(&full[ksl], kph))) break;
-        }
-        for (int u = u_lo; u < u_hi; ++u) {
-          if (pv + 1 < jn && !(ok = issue_pv())) break;
-          const int b = jn & 1;
-          tc::fence_after_sync();
-          const uint64_t kd = kdesc + ksl * (L::kTile >> 4) + (u ? (8 * kGroupBytes) >> 4 : 0);
-          const uint64_t qd = qdesc + (pair ? x * (L::kTile >> 4) : 0);
-#pragma unroll
-          for (int k = 0; k < D / 16; ++k)
-            tc::mma_bf16(tS + b * 64, qd + (((k >> 2) * L::kHalf + (k & 3) * 32) >> 4),
-                         kd + (((k >> 2) * 1024 + (k & 3) * 32) >> 4), idqk, k > 0 ? 1u : 0u);
-          tc::commit(&sfull[2 * x + b]);
-          const bool last = u == u_hi - 1;
-          if (last) tc::commit(&freeb[ksl]);
-          const uint32_t q = vinfo | (first ? kFirst : 0) | (u ? kSecond : 0) | (last ? kFrees : 0);
-          if (b) info1 = q;
-          else info0 = q;
-          first = false;
-          ++jn;
-        }
-        if (!ok) break;
-        if (u_lo == u_hi) {  // no key of this group's half: give the stage back
-          tc::commit(&freeb[ksl]);
-          const uint32_t vsl = vinfo >> 5;
-          if (!(ok = mbar_wait(&full[vsl], (vinfo >> 4) & 1))) break;
-          tc::commit(&freeb[vsl]);
-        }
-        if (fl & kDtEnd) {
-          tc::commit(qfree);
-          while (pv < jn && (ok = issue_pv())) {
-          }
-          if (!ok) break;
-          // a piece without a job of this group must not run ahead either
-          if (!freed && pieces > 1 && !(ok = mbar_wait(ofree, (pieces - 2) & 1))) break;
-          tc::commit(oend);
-        }
-      }
-      if (!ok) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
-    }
   } else {
     // ============================================================ softmax
     if (kMx) take_registers<kDtMxSoftRegs>();

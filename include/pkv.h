@@ -423,7 +423,9 @@ size_t pkv_draft_tree_workspace_bytes(const pkv_cache_desc* cache, int32_t num_s
  *   A = {t < ctx_lens[r]} and {ctx_lens[r] + j : j < n, bit j of masks[row]}
  * for kv head h / (Hq / Hkv).  A row outside A contributes nothing, whatever
  * its bytes (NaN and infinities included).  A query row that sees no row at
- * all (no context, an empty mask) gives out = 0 and lse = -inf.
+ * all (no context, an empty mask) gives out = 0 and lse = -inf.  Weights and
+ * their sums are held in fp32; on the tensor cores (bf16 and MXFP8 pools) a
+ * weight meets its V in two bf16 terms, within 2^-14 of itself.
  *   out:           [num_rows, Hq, D]; rows of no sequence are not written.
  *   lse:           float [num_rows, Hq] natural-log LSE, or NULL.
  *   q:             [num_rows, Hq, D].

@@ -8,13 +8,12 @@
 // fp32 per row; a stage is 128 keys, K and V read once for up to 256 rows.
 //
 // What bounds it: at head_dim 128 a stage is 64 KiB, 1.47 us of one SM's share
-// of the measured copy bandwidth, and 8.4 MFLOP per 128 rows, 0.67 us of its
-// share of the measured bf16 rate: the bytes, up to 256 rows.  Measured, 32
-// query and 8 kv heads: 16 requests with trees of 5 to 27 67 us (4.3 TB/s over
-// the call, 6.4 in the steady state); 64 requests with trees of 64 283 us (1046
-// TFLOP/s), where the exponentials beside the MMAs bound it; MXFP8, 64 query
-// heads, 12 requests 72 us, where the widening and the softmax warps' latencies
-// do.
+// of the measured copy bandwidth, and 12.6 MFLOP per 128 rows (P in two terms:
+// 4.2 of QK, 8.4 of PV), 1.0 us of its share of the measured bf16 rate: the
+// bytes up to 128 rows, the MMAs past them.  Measured, 32 query and 8 kv heads:
+// 16 requests with trees of 5 to 27 75 us (3.9 TB/s over the call; P in one term
+// 66); 64 requests with trees of 64 345 us (1.29 PFLOP/s of MMAs; one term 288);
+// MXFP8, 64 query heads, 12 requests 75 us (one term 72).
 //
 // Design:
 //   * the work split, the pieces and their records are the decode's
@@ -33,9 +32,10 @@
 //     2 x 128 of O;
 //   * thread t of a group owns row t of its tile (TMEM lane t): no cross-thread
 //     reduction.  Warps whose 32 rows hold no drafted row skip the arithmetic;
-//   * P is rounded to bf16 (half a step, 2^-8 of each weight, is the size of the
-//     output's own rounding) and overlays its S in TMEM, from where
-//     the PV MMA reads it; the row sums are taken before the rounding;
+//   * P goes into the PV as two bf16 terms (one alone errs by up to half a step
+//     of each weight, 2^-8, which a few keys of opposite values can lift to the
+//     size of the output's own rounding and past it), which overlay its S in
+//     TMEM; the row sums take it whole;
 //   * one warp streams K and V (TMA, 128-byte swizzle, row-group tiles of
 //     launch.h) through a ring of tiles, K0, V0, K1, V1, ..., and each piece's
 //     Q as soon as the previous piece's QKs have read theirs; a thread per
@@ -77,9 +77,9 @@ constexpr int kDtMxRegs = 96, kDtMxIssueRegs = 64, kDtMxWidenRegs = 88, kDtMxSof
 static_assert(128 * kDtMxIssueRegs + 256 * kDtMxSoftRegs + 256 * kDtMxWidenRegs <= dt_threads(true) * kDtMxRegs,
               "the warpgroups' registers come from the launch's");
 constexpr int kDtJob = 64;           // keys of a job
-// Columns of S that a softmax thread holds at once: a job's 64, or 32 (the
-// second 32's weights come first then, and the first 32 are read again) where
-// the widening warps leave fewer registers.
+// Columns of S that a softmax thread holds at once: a job's 64, or 32 (each 32
+// are read again for their weights) where the widening warps leave fewer
+// registers.
 constexpr int dt_chunk(bool mx) { return mx ? 32 : 64; }
 // Stage descriptors in flight.  A bf16 stage is described when its ring tiles
 // are free.  An MXFP8 one is described once the stage kDtAhead before it has
@@ -130,6 +130,19 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
   asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
+}
+
+// Two weights as bf16 pairs, p = hi + lo to 2^-14.9 of p.  hi is p cut off and lo
+// what is left, of p (1 + 2^-20): neither is ever negative, nor 0 unless p is,
+// so that an infinity of V stays one in hi V + lo V.
+__device__ __forceinline__ void split_weights(float p0, float p1, uint32_t& hi, uint32_t& lo) {
+  const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
+  hi = __byte_perm(b0, b1, 0x7632);
+  const float2 minus = make_float2(__uint_as_float((b0 & 0xffff0000u) | 0x80000000u),
+                                   __uint_as_float((b1 & 0xffff0000u) | 0x80000000u));
+  const float2 left = __ffma2_rn(make_float2(p0, p1), make_float2(1.f + 0x1p-20f, 1.f + 0x1p-20f), minus);
+  const __nv_bfloat162 b2 = __floats2bfloat162_rn(left.x, left.y);
+  lo = *reinterpret_cast<const uint32_t*>(&b2);
 }
 
 // All warps of a warpgroup: from now on each thread has kRegs registers.
@@ -462,10 +475,11 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
           tc::fence_after_sync();
           const uint64_t vd = vdesc + sl * (L::kTile >> 4) + ((q & kSecond) ? (8 * kGroupBytes) >> 4 : 0);
 #pragma unroll
-          for (int k = 0; k < kDtJob / 16; ++k)
-            tc::mma_bf16_ta(tO, tS + b * 64 + (dt_chunk(kMx) == 64 ? k * 8 : (k >> 1) * 32 + (k & 1) * 8),
-                            vd + ((k * 2 * kGroupBytes) >> 4), kIdPV,
-                            (k > 0 || !(q & kFirst)) ? 1u : 0u);
+          for (int k = 0; k < kDtJob / 16; ++k) {  // 16 keys: their hi, then their lo
+            const uint32_t tP = tS + b * 64 + 16 * k;
+            tc::mma_bf16_ta(tO, tP, vd + ((k * 2 * kGroupBytes) >> 4), kIdPV, (k > 0 || !(q & kFirst)) ? 1u : 0u);
+            tc::mma_bf16_ta(tO, tP + 8, vd + ((k * 2 * kGroupBytes) >> 4), kIdPV, 1u);
+          }
           tc::commit(&pvdone[x]);
           if (q & kFrees) tc::commit(&freeb[sl]);
           ++pv;
@@ -750,25 +764,27 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
             const float alpha = need ? exp2f(m - m_new) : 1.f;
             if (need) m = m_new;
             const float nm = m == -INFINITY ? 0.f : -m;  // nothing seen yet: every weight is 0
-            // ---- P = exp2(c s - m) in bf16 pairs, over the first half of its
-            // S's columns; the sums take it unrounded
+            // ---- P = exp2(c s - m) in bf16 pairs, hi and lo, over the columns
+            // of the S that it came from; the sums take it whole
             float2 ls4[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) ls4[i] = make_float2(0.f, 0.f);
-#pragma unroll
+            // (not unrolled: MXFP8's two chunks at once spill, 98 us and 75)
+#pragma unroll 1
             for (int w = kChunks - 1; w >= 0; --w) {
-              if (w < kChunks - 1) read(w);
-              uint32_t pw[kChunk / 2];
+              if (kChunks > 1) read(w);
 #pragma unroll
-              for (int i = 0; i < kChunk / 2; ++i) {
-                const float p0 = exp2f(fmaf(__uint_as_float(v[2 * i]), cs, nm));
-                const float p1 = exp2f(fmaf(__uint_as_float(v[2 * i + 1]), cs, nm));
-                ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(p0, p1));
-                const __nv_bfloat162 b2 = __floats2bfloat162_rn(p0, p1);
-                pw[i] = *reinterpret_cast<const uint32_t*>(&b2);
+              for (int q = 0; q < kChunk / 32; ++q) {
+                uint32_t pw[32];  // of 16 keys hi, then lo, and of the next 16
+#pragma unroll
+                for (int i = 0; i < 16; ++i) {
+                  const float p0 = exp2f(fmaf(__uint_as_float(v[32 * q + 2 * i]), cs, nm));
+                  const float p1 = exp2f(fmaf(__uint_as_float(v[32 * q + 2 * i + 1]), cs, nm));
+                  ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(p0, p1));
+                  split_weights(p0, p1, pw[(i & 7) + 16 * (i >> 3)], pw[8 + (i & 7) + 16 * (i >> 3)]);
+                }
+                tc::tmem_st32(tS + kChunk * w + 32 * q, pw);
               }
-              if constexpr (kChunk == 64) tc::tmem_st32(tS, pw);
-              else tc::tmem_st16(tS + 32 * w, pw);
             }
             const float2 ls2 = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
             l = l * alpha + (ls2.x + ls2.y);

@@ -110,6 +110,16 @@ struct DtDesc {
            // row, rows of the segment, piece number (from 1)
 };
 
+// What a piece notes of its drafted rows with non-finite V: [0] the last such
+// piece, [1 + j] the last piece whose row j was one (pieces count from 1).  Two
+// of them by the piece's parity: some warps may clear a piece's V while others
+// still read what the piece before noted.  The piece after that cannot be
+// reached before they have: its clearing follows the end of the piece between
+// (oend), whose MMAs wait until every softmax warp has left this one (ofree).
+// The numbers in 16 bits: one that comes round again has a row looked at once
+// more, whose finite elements add nothing.
+constexpr int kDtBad = 1 + 64;
+
 template <int D, int kTiles>
 struct DtSmem {
   static constexpr int kHalf = kDraftRows * 128;          // 64 columns of a Q tile
@@ -121,7 +131,7 @@ struct DtSmem {
   static constexpr int desc_off = exch_off + 2 * 128 * 8;
   static constexpr int bar_off = desc_off + dt_descs(true) * (int)sizeof(DtDesc);
   static constexpr int bad_off = bar_off + (2 * kItems + dt_descs(true) + 17 + kDtAhead) * 8;
-  static constexpr int tmem_off = bad_off + 65 * 4;
+  static constexpr int tmem_off = bad_off + 2 * kDtBad * 2;
   static constexpr int total = tmem_off + 4;
   static_assert(total <= 227 * 1024, "shared memory of one CTA");
 };
@@ -224,9 +234,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
   uint64_t* xsync = ofree + 1;        // the groups meet at a piece's end
   uint64_t* vclean = xsync + 1;       // [2] group 0 cleared a tail stage's V for both
   uint64_t* widened = vclean + 2;     // [kDtAhead] MXFP8: a stage has been widened
-  // a piece's drafted rows with non-finite V: [0] the last such piece, [1 + j]
-  // the last piece whose row j was one (pieces count from 1)
-  volatile int* bad = reinterpret_cast<volatile int*>(sm + L::bad_off);
+  volatile uint16_t* bad_rows = reinterpret_cast<volatile uint16_t*>(sm + L::bad_off);  // [2][kDtBad]
   uint32_t* tmem_base = reinterpret_cast<uint32_t*>(sm + L::tmem_off);
 
   // the warp number as a warp-uniform value, for the branches on it
@@ -255,7 +263,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
     mbar_init(xsync, kDtSoftWarps);
     fence_barrier_init();
   }
-  if (t < 65) bad[t] = 0;
+  if (t < 2 * kDtBad) bad_rows[t] = 0;
   if (warp == kDtSoftWarps + 2 && lane == 0) {
     prefetch_tensormap(&tmq);
     if constexpr (!kMx) {
@@ -766,9 +774,9 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
             const float nm = m == -INFINITY ? 0.f : -m;  // nothing seen yet: every weight is 0
             // ---- P = exp2(c s - m) in bf16 pairs, hi and lo, over the columns
             // of the S that it came from; the sums take it whole
-            float2 ls4[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ls4[i] = make_float2(0.f, 0.f);
+            // (two pairs of sums: with four of them the pair form spills, 353 us
+            // for 64 trees of 64 and 342)
+            float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             // (not unrolled: MXFP8's two chunks at once spill, 98 us and 75)
 #pragma unroll 1
             for (int w = kChunks - 1; w >= 0; --w) {
@@ -780,13 +788,13 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
                 for (int i = 0; i < 16; ++i) {
                   const float p0 = exp2f(fmaf(__uint_as_float(v[32 * q + 2 * i]), cs, nm));
                   const float p1 = exp2f(fmaf(__uint_as_float(v[32 * q + 2 * i + 1]), cs, nm));
-                  ls4[i & 3] = __fadd2_rn(ls4[i & 3], make_float2(p0, p1));
+                  ls[i & 1] = __fadd2_rn(ls[i & 1], make_float2(p0, p1));
                   split_weights(p0, p1, pw[(i & 7) + 16 * (i >> 3)], pw[8 + (i & 7) + 16 * (i >> 3)]);
                 }
                 tc::tmem_st32(tS + kChunk * w + 32 * q, pw);
               }
             }
-            const float2 ls2 = __fadd2_rn(__fadd2_rn(ls4[0], ls4[1]), __fadd2_rn(ls4[2], ls4[3]));
+            const float2 ls2 = __fadd2_rn(ls[0], ls[1]);
             l = l * alpha + (ls2.x + ls2.y);
             // a new base: once the group's previous PV has added to O under the
             // old one (and no later one has begun), rescale the row
@@ -845,8 +853,9 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
                     found |= any;
                   }
                 if (found) {
-                  bad[1 + row - mb] = db.w;
-                  bad[0] = db.w;
+                  volatile uint16_t* bad = bad_rows + (db.w & 1) * kDtBad;
+                  bad[1 + row - mb] = (uint16_t)db.w;
+                  bad[0] = (uint16_t)db.w;
                 }
               }
               tc::fence_proxy_async_smem();
@@ -903,7 +912,8 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
             if (!whole) a.rec_lse[rec] = lse2;
             else if (a.lse_out) a.lse_out[qh] = lse2 * kDtLn2;
           }
-          const bool fix = bad[0] == db.w;
+          volatile uint16_t* bad = bad_rows + (db.w & 1) * kDtBad;
+          const bool fix = bad[0] == (uint16_t)db.w;
           // columns: all in a pair, this group's half otherwise, 16 at a time
           const int c_lo = pair ? 0 : x * (D / 2), c_hi = pair ? D : c_lo + D / 2;
 #pragma unroll 1
@@ -921,7 +931,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
             if (fix && live) {  // non-finite elements that this row does see
               for (uint64_t left = mask; left; left &= left - 1) {
                 const int jd = __ffsll((long long)left) - 1;
-                if (bad[1 + jd] != db.w) continue;
+                if (bad[1 + jd] != (uint16_t)db.w) continue;
                 const int pos = __ldg(a.ctx_lens + da.x) + jd;
                 const int blk = __ldg(a.block_tables + (int64_t)da.x * a.max_blocks + pos / P);
                 if (blk < 0 || (int64_t)blk >= a.num_blocks) continue;

@@ -490,13 +490,37 @@ size_t pkv_decode_weights_workspace_bytes(const pkv_cache_desc* cache, int32_t n
  *   workspace:      at least pkv_decode_weights_workspace_bytes, 256-byte
  *                   aligned; calls that may overlap on the GPU need one each.
  * What the rows of a block id outside the pool (PKV_DEVERR_BLOCK) add to their
- * own scores is unspecified.  Other arguments, support and errors as in pkv_paged_attention_decode (partition_size 0). */
+ * own scores is unspecified.  Other arguments, support and errors as in
+ * pkv_paged_attention_decode (partition_size 0). */
 pkv_status pkv_paged_attention_decode_weights(
     const pkv_cache_desc* cache, void* out, float* lse, float* weights, int64_t weights_stride,
     float decay, const void* q, const void* k_cache, const void* v_cache,
     const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
     int32_t num_seqs, int32_t num_q_heads, float scale, void* workspace, size_t workspace_bytes,
     void* stream);
+
+/* The three calls that take scores, on a part of a wider buffer: each row holds
+ * weights_rows scores (0 .. weights_stride), and no length reaches the ones
+ * behind them.  weights_rows stands where the plain calls' bounds name
+ * weights_stride (a longer sequence sets PKV_DEVERR_LENGTH); the plain calls are
+ * these with weights_rows = weights_stride. */
+pkv_status pkv_paged_attention_decode_weights_view(
+    const pkv_cache_desc* cache, void* out, float* lse, float* weights, int64_t weights_stride,
+    int64_t weights_rows, float decay, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+    int32_t num_seqs, int32_t num_q_heads, float scale, void* workspace, size_t workspace_bytes,
+    void* stream);
+pkv_status pkv_kv_evict_select_view(const float* weights, int64_t weights_stride,
+                                    int64_t weights_rows, const int32_t* seq_lens,
+                                    int32_t num_seqs, int32_t num_kv_heads, int32_t budget,
+                                    int32_t num_sinks, int32_t num_recent, int32_t* keep,
+                                    int32_t* new_lens, void* stream);
+pkv_status pkv_kv_compact_view(const pkv_cache_desc* cache, void* k_cache, void* v_cache,
+                               float* weights, int64_t weights_stride, int64_t weights_rows,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, const int32_t* base_lens,
+                               const int32_t* keep, int32_t keep_heads, int64_t keep_stride,
+                               const int32_t* keep_lens, int32_t num_seqs, void* stream);
 
 /* Choose the rows each (sequence, kv head) keeps within `budget`.  A sequence
  * of T = seq_lens[r] <= budget rows keeps them all.  A longer one keeps its

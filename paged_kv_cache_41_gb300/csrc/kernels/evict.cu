@@ -29,9 +29,9 @@ __global__ void __launch_bounds__(kWeighThreads) weigh_kernel(const WeighArgs a)
   pdl_wait();
   const int r = blockIdx.z, c = blockIdx.y, Hkv = a.num_kv_heads;
   const int len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, a.block_size, a.err, false);
-  if (len > a.weights_stride && blockIdx.x == 0 && c == 0 && threadIdx.x == 0)
+  if (len > a.weights_rows && blockIdx.x == 0 && c == 0 && threadIdx.x == 0)
     atomicOr(a.err, PKV_DEVERR_LENGTH);
-  const int64_t n = len < a.weights_stride ? len : a.weights_stride;
+  const int64_t n = len < a.weights_rows ? len : a.weights_rows;
   const int64_t t0 = (int64_t)blockIdx.x * (kWeighThreads * kWeighRows) + threadIdx.x;
   if (t0 - threadIdx.x >= n) return;
   const int64_t rc = (int64_t)r * Hkv + c;
@@ -145,9 +145,9 @@ __global__ void __launch_bounds__(kThreads, kThreads == 256 ? 5 : 2) evict_selec
   const int c = blockIdx.x / cs, r = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int T = __ldg(a.seq_lens + r);
-  if (T < 0 || T > a.weights_stride) {
+  if (T < 0 || T > a.weights_rows) {
     if (c == 0 && rank == 0 && tid == 0) atomicOr(a.err, PKV_DEVERR_LENGTH);
-    T = T < 0 ? 0 : (int)a.weights_stride;
+    T = T < 0 ? 0 : (int)a.weights_rows;
   }
   int32_t* keep = a.keep + ((int64_t)r * a.num_kv_heads + c) * a.budget;
   const int kept = min(T, a.budget);
@@ -427,9 +427,9 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
   const int c = blockIdx.x, r = blockIdx.y;
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   int T = __ldg(a.seq_lens + r);
-  if (T < 0 || T > a.weights_stride) {
+  if (T < 0 || T > a.weights_rows) {
     if (c == 0 && tid == 0) atomicOr(a.err, PKV_DEVERR_LENGTH);
-    T = T < 0 ? 0 : (int)a.weights_stride;
+    T = T < 0 ? 0 : (int)a.weights_rows;
   }
   const uint32_t* w = reinterpret_cast<const uint32_t*>(a.weights) +
                       ((int64_t)r * a.num_kv_heads + c) * a.weights_stride;
@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kSelThreads) evict_select_kernel(const SelectA
 
 template <int kThreads>
 static cudaError_t launch_select_cluster(const SelectArgs& a, int cs, cudaStream_t stream) {
-  const int smem = (int)(((a.weights_stride + cs - 1) / cs + 3) & ~(int64_t)3) * 4;
+  const int smem = (int)(((a.weights_rows + cs - 1) / cs + 3) & ~(int64_t)3) * 4;
   auto kern = evict_select_cluster_kernel<kThreads>;
   static SmemAttrCache attr_cache;
   cudaError_t e = ensure_smem_limit(kern, smem, attr_cache);
@@ -544,10 +544,10 @@ static cudaError_t launch_select_cluster(const SelectArgs& a, int cs, cudaStream
 }
 
 cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
-  // No length passes weights_stride: the smallest cluster whose CTAs hold it.
+  // No length passes weights_rows: the smallest cluster whose CTAs hold it.
   // Small CTAs for rows of up to 8192, several to a SM (64 requests: 22.6 us,
   // with 1024 threads 25.6).
-  const int64_t most = a.weights_stride;
+  const int64_t most = a.weights_rows;
   if (most <= 8 * kScSlice) {
     int cs = 1;
     while (most > (int64_t)cs * kScSlice) cs *= 2;
@@ -591,7 +591,7 @@ __device__ __forceinline__ CompactSeq compact_seq(const CompactArgs& a, int r, b
   s.base = a.base_lens ? __ldg(a.base_lens + r) : 0;
   s.n = __ldg(a.keep_lens + r);
   const bool ok = s.len <= kCmMaxLen && s.base >= 0 && s.base <= s.len && s.n >= 0 && s.n <= s.len - s.base &&
-                  s.n <= a.keep_stride && (!a.weights || s.len <= a.weights_stride);
+                  s.n <= a.keep_stride && (!a.weights || s.len <= a.weights_rows);
   if (!ok) {
     if (report) atomicOr(a.err, PKV_DEVERR_LENGTH);
     s.n = 0;

@@ -307,6 +307,7 @@ struct WeighArgs {
   unsigned int* err;
   int64_t scores_rows;
   int64_t weights_stride;
+  int64_t weights_rows;         // scores a row of weights holds, <= weights_stride
   int32_t max_blocks;
   int32_t num_seqs;
   int32_t num_q_heads;
@@ -324,6 +325,7 @@ struct SelectArgs {
   int32_t* new_lens;            // [B]
   unsigned int* err;
   int64_t weights_stride;
+  int64_t weights_rows;         // scores a row of weights holds, <= weights_stride
   int32_t num_seqs;
   int32_t num_kv_heads;
   int32_t budget;
@@ -348,6 +350,7 @@ struct CompactArgs {
   const int32_t* keep_lens;     // [B]
   unsigned int* err;
   int64_t weights_stride;
+  int64_t weights_rows;         // scores a row of weights holds, <= weights_stride
   int64_t keep_stride;
   int64_t num_blocks;
   int32_t max_blocks;

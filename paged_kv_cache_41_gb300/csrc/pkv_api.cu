@@ -959,6 +959,9 @@ pkv_status pkv_draft_tree_attention(
 
 namespace {
 
+// Rows of scores, `rows` of them used of each `stride`.
+bool score_rows_ok(int64_t stride, int64_t rows) { return stride >= 1 && rows >= 0 && rows <= stride; }
+
 // Weighing-decode workspace: the decode's, then the LSEs [B, Hq] (for a caller
 // that wants none) and the scores [B, Hkv, rows, G], rows the table's.
 struct WeightsWorkspace {
@@ -984,16 +987,16 @@ size_t pkv_decode_weights_workspace_bytes(const pkv_cache_desc* cache, int32_t n
   return weights_workspace(cache, num_seqs, num_q_heads, max_blocks_per_seq).total;
 }
 
-pkv_status pkv_paged_attention_decode_weights(
+pkv_status pkv_paged_attention_decode_weights_view(
     const pkv_cache_desc* cache, void* out, float* lse, float* weights, int64_t weights_stride,
-    float decay, const void* q, const void* k_cache, const void* v_cache,
+    int64_t weights_rows, float decay, const void* q, const void* k_cache, const void* v_cache,
     const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
     int32_t num_seqs, int32_t num_q_heads, float scale, void* workspace, size_t workspace_bytes,
     void* stream) {
   pkv_status st = check_cache(cache);
   if (st != PKV_OK) return st;
-  if (num_seqs < 0 || max_blocks_per_seq <= 0 || weights_stride < 1 || !isfinite(scale) ||
-      !isfinite(decay))
+  if (num_seqs < 0 || max_blocks_per_seq <= 0 || !score_rows_ok(weights_stride, weights_rows) ||
+      !isfinite(scale) || !isfinite(decay))
     return PKV_ERR_INVALID_ARG;
   if ((st = check_attention_shape(cache, num_q_heads)) != PKV_OK) return st;
   if (num_seqs == 0) return PKV_OK;
@@ -1020,6 +1023,7 @@ pkv_status pkv_paged_attention_decode_weights(
   a.err = err;
   a.scores_rows = rows;
   a.weights_stride = weights_stride;
+  a.weights_rows = weights_rows;
   a.max_blocks = max_blocks_per_seq;
   a.num_seqs = num_seqs;
   a.num_q_heads = num_q_heads;
@@ -1030,17 +1034,30 @@ pkv_status pkv_paged_attention_decode_weights(
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-pkv_status pkv_kv_evict_select(const float* weights, int64_t weights_stride,
-                               const int32_t* seq_lens, int32_t num_seqs, int32_t num_kv_heads,
-                               int32_t budget, int32_t num_sinks, int32_t num_recent,
-                               int32_t* keep, int32_t* new_lens, void* stream) {
-  if (num_seqs < 0 || num_kv_heads <= 0 || weights_stride < 1 || budget < 1 || num_sinks < 0 ||
-      num_recent < 0 || (int64_t)num_sinks + num_recent > budget)
+pkv_status pkv_paged_attention_decode_weights(
+    const pkv_cache_desc* cache, void* out, float* lse, float* weights, int64_t weights_stride,
+    float decay, const void* q, const void* k_cache, const void* v_cache,
+    const int32_t* block_tables, int32_t max_blocks_per_seq, const int32_t* seq_lens,
+    int32_t num_seqs, int32_t num_q_heads, float scale, void* workspace, size_t workspace_bytes,
+    void* stream) {
+  return pkv_paged_attention_decode_weights_view(
+      cache, out, lse, weights, weights_stride, weights_stride, decay, q, k_cache, v_cache,
+      block_tables, max_blocks_per_seq, seq_lens, num_seqs, num_q_heads, scale, workspace,
+      workspace_bytes, stream);
+}
+
+pkv_status pkv_kv_evict_select_view(const float* weights, int64_t weights_stride,
+                                    int64_t weights_rows, const int32_t* seq_lens,
+                                    int32_t num_seqs, int32_t num_kv_heads, int32_t budget,
+                                    int32_t num_sinks, int32_t num_recent, int32_t* keep,
+                                    int32_t* new_lens, void* stream) {
+  if (num_seqs < 0 || num_kv_heads <= 0 || !score_rows_ok(weights_stride, weights_rows) ||
+      budget < 1 || num_sinks < 0 || num_recent < 0 || (int64_t)num_sinks + num_recent > budget)
     return PKV_ERR_INVALID_ARG;
   if (num_seqs == 0) return PKV_OK;
   if (num_seqs > 65535 || num_kv_heads > 65535) return PKV_ERR_UNSUPPORTED;
   // row numbers past the last, up to a CTA's stride, stay in 32 bits
-  if (weights_stride > 0x7fff0000 || budget > 0x7fff0000) return PKV_ERR_UNSUPPORTED;
+  if (weights_rows > 0x7fff0000 || budget > 0x7fff0000) return PKV_ERR_UNSUPPORTED;
   if (!weights || !seq_lens || !keep || !new_lens) return PKV_ERR_INVALID_ARG;
   // the lengths are read by every CTA while one writes the new ones
   if (new_lens < seq_lens + num_seqs && seq_lens < new_lens + num_seqs) return PKV_ERR_INVALID_ARG;
@@ -1053,6 +1070,7 @@ pkv_status pkv_kv_evict_select(const float* weights, int64_t weights_stride,
   a.new_lens = new_lens;
   a.err = err;
   a.weights_stride = weights_stride;
+  a.weights_rows = weights_rows;
   a.num_seqs = num_seqs;
   a.num_kv_heads = num_kv_heads;
   a.budget = budget;
@@ -1062,16 +1080,25 @@ pkv_status pkv_kv_evict_select(const float* weights, int64_t weights_stride,
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
-pkv_status pkv_kv_compact(const pkv_cache_desc* cache, void* k_cache, void* v_cache,
-                          float* weights, int64_t weights_stride, const int32_t* block_tables,
-                          int32_t max_blocks_per_seq, const int32_t* seq_lens,
-                          const int32_t* base_lens, const int32_t* keep, int32_t keep_heads,
-                          int64_t keep_stride, const int32_t* keep_lens, int32_t num_seqs,
-                          void* stream) {
+pkv_status pkv_kv_evict_select(const float* weights, int64_t weights_stride,
+                               const int32_t* seq_lens, int32_t num_seqs, int32_t num_kv_heads,
+                               int32_t budget, int32_t num_sinks, int32_t num_recent,
+                               int32_t* keep, int32_t* new_lens, void* stream) {
+  return pkv_kv_evict_select_view(weights, weights_stride, weights_stride, seq_lens, num_seqs,
+                                  num_kv_heads, budget, num_sinks, num_recent, keep, new_lens,
+                                  stream);
+}
+
+pkv_status pkv_kv_compact_view(const pkv_cache_desc* cache, void* k_cache, void* v_cache,
+                               float* weights, int64_t weights_stride, int64_t weights_rows,
+                               const int32_t* block_tables, int32_t max_blocks_per_seq,
+                               const int32_t* seq_lens, const int32_t* base_lens,
+                               const int32_t* keep, int32_t keep_heads, int64_t keep_stride,
+                               const int32_t* keep_lens, int32_t num_seqs, void* stream) {
   pkv_status st = check_cache(cache);
   if (st != PKV_OK) return st;
   if (num_seqs < 0 || max_blocks_per_seq <= 0 || keep_stride < 0 ||
-      (keep_heads != 1 && keep_heads != cache->num_kv_heads) || (weights && weights_stride < 1))
+      (keep_heads != 1 && keep_heads != cache->num_kv_heads) || (weights && !score_rows_ok(weights_stride, weights_rows)))
     return PKV_ERR_INVALID_ARG;
   if (num_seqs == 0 || (keep_stride == 0 && !weights)) return PKV_OK;  // else weights to clear
   if (!k_cache || !v_cache || !block_tables || !seq_lens || (!keep && keep_stride > 0) || !keep_lens)
@@ -1100,6 +1127,7 @@ pkv_status pkv_kv_compact(const pkv_cache_desc* cache, void* k_cache, void* v_ca
   }
   a.weights = weights;
   a.weights_stride = weights_stride;
+  a.weights_rows = weights_rows;
   a.block_tables = block_tables;
   a.seq_lens = seq_lens;
   a.base_lens = base_lens;
@@ -1116,6 +1144,17 @@ pkv_status pkv_kv_compact(const pkv_cache_desc* cache, void* k_cache, void* v_ca
   a.row_bytes = (int32_t)row_bytes;
   cudaError_t e = pkv::launch_kv_compact(a, as_stream(stream));
   return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_kv_compact(const pkv_cache_desc* cache, void* k_cache, void* v_cache,
+                          float* weights, int64_t weights_stride, const int32_t* block_tables,
+                          int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                          const int32_t* base_lens, const int32_t* keep, int32_t keep_heads,
+                          int64_t keep_stride, const int32_t* keep_lens, int32_t num_seqs,
+                          void* stream) {
+  return pkv_kv_compact_view(cache, k_cache, v_cache, weights, weights_stride, weights_stride,
+                             block_tables, max_blocks_per_seq, seq_lens, base_lens, keep,
+                             keep_heads, keep_stride, keep_lens, num_seqs, stream);
 }
 
 pkv_status pkv_get_device_error(int32_t* code_out, void* stream) {

@@ -42,8 +42,11 @@ EXPORTED = [
     "pkv_draft_tree_attention",
     "pkv_decode_weights_workspace_bytes",
     "pkv_paged_attention_decode_weights",
+    "pkv_paged_attention_decode_weights_view",
     "pkv_kv_evict_select",
+    "pkv_kv_evict_select_view",
     "pkv_kv_compact",
+    "pkv_kv_compact_view",
     "pkv_get_device_error",
     "pkv_status_string",
 ]
@@ -117,10 +120,17 @@ def load_library():
     lib.pkv_paged_attention_decode_weights.restype = ctypes.c_int
     lib.pkv_paged_attention_decode_weights.argtypes = [dp, vp, vp, vp, i64, f32, vp, vp, vp, vp, i32,
                                                        vp, i32, i32, f32, vp, ctypes.c_size_t, vp]
+    lib.pkv_paged_attention_decode_weights_view.restype = ctypes.c_int
+    lib.pkv_paged_attention_decode_weights_view.argtypes = [dp, vp, vp, vp, i64, i64, f32, vp, vp, vp, vp,
+                                                            i32, vp, i32, i32, f32, vp, ctypes.c_size_t, vp]
     lib.pkv_kv_evict_select.restype = ctypes.c_int
     lib.pkv_kv_evict_select.argtypes = [vp, i64, vp, i32, i32, i32, i32, i32, vp, vp, vp]
+    lib.pkv_kv_evict_select_view.restype = ctypes.c_int
+    lib.pkv_kv_evict_select_view.argtypes = [vp, i64, i64, vp, i32, i32, i32, i32, i32, vp, vp, vp]
     lib.pkv_kv_compact.restype = ctypes.c_int
     lib.pkv_kv_compact.argtypes = [dp, vp, vp, vp, i64, vp, i32, vp, vp, vp, i32, i64, vp, i32, vp]
+    lib.pkv_kv_compact_view.restype = ctypes.c_int
+    lib.pkv_kv_compact_view.argtypes = [dp, vp, vp, vp, i64, i64, vp, i32, vp, vp, vp, i32, i64, vp, i32, vp]
     lib.pkv_get_device_error.restype = ctypes.c_int
     lib.pkv_get_device_error.argtypes = [ctypes.POINTER(i32), vp]
     lib.pkv_status_string.restype = ctypes.c_char_p
@@ -461,15 +471,16 @@ def _io_dtype(desc):
 
 
 def _score_rows(name, weights, b, hkv):
-    """Check a score buffer [b, hkv, n] float32 (rows may be wider than n) and
-    return the elements between its rows."""
+    """Check a score buffer [b, hkv, n] float32 (a view of wider rows, perhaps)
+    and return the elements between its rows and those of a row, which alone
+    the kernels touch."""
     if weights.dtype != torch.float32 or weights.dim() != 3 or weights.shape[:2] != (b, hkv):
         raise ValueError(f"{name} must be a float32 tensor of shape ({b}, {hkv}, n)")
     stride = weights.stride(1) if hkv > 1 else weights.stride(0) if b > 1 else weights.shape[2]
     if (weights.shape[2] > 1 and weights.stride(2) != 1) or stride < weights.shape[2] or (
             b > 1 and weights.stride(0) != hkv * stride):
         raise ValueError(f"{name}'s rows must lie one behind the other")
-    return stride
+    return stride, weights.shape[2]
 
 
 def draft_tree_workspace_bytes(k_cache, num_seqs, num_q_heads, max_draft,
@@ -539,7 +550,7 @@ def paged_attention_decode_weights(q, k_cache, v_cache, block_tables, seq_lens, 
     _dense("q", q, _io_dtype(desc), (b, hq, desc.head_dim))
     _dense("block_tables", block_tables, torch.int32, (b, max_blocks))
     _dense("seq_lens", seq_lens, torch.int32, (b,))
-    stride = _score_rows("weights", weights, b, desc.num_kv_heads)
+    stride, n = _score_rows("weights", weights, b, desc.num_kv_heads)
     if out is None:
         out = _empty(stream, q.shape, q.dtype, q.device)
     else:
@@ -553,9 +564,9 @@ def paged_attention_decode_weights(q, k_cache, v_cache, block_tables, seq_lens, 
         need = lib.pkv_decode_weights_workspace_bytes(ctypes.byref(desc), b, hq, max_blocks)
         workspace = _empty(stream, need, torch.uint8, q.device) if need else None
     ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
-    _check(lib.pkv_paged_attention_decode_weights(
+    _check(lib.pkv_paged_attention_decode_weights_view(
         ctypes.byref(desc), out.data_ptr(), lse.data_ptr() if lse is not None else None,
-        weights.data_ptr(), stride, decay, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
+        weights.data_ptr(), stride, n, decay, q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(),
         block_tables.data_ptr(), max_blocks, seq_lens.data_ptr(), b, hq, scale,
         workspace.data_ptr() if workspace is not None else None, ws_bytes, where),
         "pkv_paged_attention_decode_weights")
@@ -570,7 +581,7 @@ def kv_evict_select(weights, seq_lens, budget, *, num_sinks=0, num_recent=0, kee
     int32 [B, Hkv, budget], ascending and -1 padded, new_lens int32 [B])."""
     b, hkv, _ = weights.shape
     _dense("seq_lens", seq_lens, torch.int32, (b,))
-    stride = _score_rows("weights", weights, b, hkv)
+    stride, n = _score_rows("weights", weights, b, hkv)
     if keep is None:
         keep = _empty(stream, (b, hkv, max(int(budget), 0)), torch.int32, weights.device)
     else:
@@ -580,8 +591,8 @@ def kv_evict_select(weights, seq_lens, budget, *, num_sinks=0, num_recent=0, kee
     else:
         _dense("new_lens", new_lens, torch.int32, (b,))
     where = _launch_place(stream, weights, seq_lens, keep, new_lens)
-    _check(load_library().pkv_kv_evict_select(
-        weights.data_ptr(), stride, seq_lens.data_ptr(), b, hkv, budget, num_sinks, num_recent,
+    _check(load_library().pkv_kv_evict_select_view(
+        weights.data_ptr(), stride, n, seq_lens.data_ptr(), b, hkv, budget, num_sinks, num_recent,
         keep.data_ptr(), new_lens.data_ptr(), where), "pkv_kv_evict_select")
     return keep, new_lens
 
@@ -601,12 +612,12 @@ def kv_compact(k_cache, v_cache, block_tables, seq_lens, keep, keep_lens, *, bas
     _dense("keep_lens", keep_lens, torch.int32, (b,))
     if base_lens is not None:
         _dense("base_lens", base_lens, torch.int32, (b,))
-    stride = _score_rows("weights", weights, b, desc.num_kv_heads) if weights is not None else 0
+    stride, n = _score_rows("weights", weights, b, desc.num_kv_heads) if weights is not None else (0, 0)
     where = _launch_place(stream, k_cache, v_cache, block_tables, seq_lens, keep, keep_lens,
                           base_lens, weights)
-    _check(load_library().pkv_kv_compact(
+    _check(load_library().pkv_kv_compact_view(
         ctypes.byref(desc), k_cache.data_ptr(), v_cache.data_ptr(),
-        weights.data_ptr() if weights is not None else None, stride, block_tables.data_ptr(),
+        weights.data_ptr() if weights is not None else None, stride, n, block_tables.data_ptr(),
         max_blocks, seq_lens.data_ptr(), base_lens.data_ptr() if base_lens is not None else None,
         keep.data_ptr(), keep_heads, places, keep_lens.data_ptr(), b, where),
         "pkv_kv_compact")

@@ -597,7 +597,7 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
       for (int i = 0; i < kSteps; ++i) {
         const int row = t0 + i * kStep, bi = shift >= 0 ? row >> shift : row / P;
         off[i] = row - bi * P;
-        blk[i] = i * kStep + row0 < da.z ? __ldg(table + bi) : -2;
+        blk[i] = i * kStep + row0 < da.z ? __ldg(table + bi) : -1;
       }
 #pragma unroll
       for (int i = 0; i < kSteps; ++i) {
@@ -605,7 +605,8 @@ __global__ void __launch_bounds__(dt_threads(kMx), 1)
         at[i] = (base + off[i] * Hkv + kvh) * (D / 32) + g;
         sat[i] = (kvh * P + off[i] - (off[i] * Hkv + kvh)) * (D / 32);
         if (blk[i] < 0 || (int64_t)blk[i] >= a.num_blocks) {
-          if (blk[i] != -2 && g == 0) atomicOr(a.err, PKV_DEVERR_BLOCK);
+          // any id may stand in the table: a row is one by its number
+          if (i * kStep + row0 < da.z && g == 0) atomicOr(a.err, PKV_DEVERR_BLOCK);
           at[i] = -1;
         }
       }

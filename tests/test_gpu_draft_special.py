@@ -54,3 +54,19 @@ def test_non_finite_rows_of_many_short_sequences(dtype, d, b, hq, n, ctx):
     for _ in range(20):  # the warps' order differs from call to call
         o, l = dr.call()
         assert same(o, out) and torch.equal(l, lse)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "mxfp8"])
+@pytest.mark.parametrize("bad", [-2, -3, -2**31, 2**31 - 2])
+@pytest.mark.parametrize("place", [0, 3, 12])
+def test_any_bad_block_sets_the_error(dtype, bad, place):
+    # in the first block, in one of the context, and in the drafted rows' own
+    dr = Draft([190, 30], [14, 5], dtype=dtype, hq=8, hkv=2, d=128, seed=13)
+    dr.cache.tables[0, place] = bad
+    dr.call()
+    assert pkv.get_device_error() == pkv.DEVERR_BLOCK
+    # a table that is right where rows are, and anything behind them
+    dr = Draft([190, 30], [14, 5], dtype=dtype, hq=8, hkv=2, d=128, width=20, seed=13)
+    dr.cache.tables[0, 13:] = bad
+    dr.cache.tables[1, 3:] = bad
+    dr.run()

@@ -558,11 +558,13 @@ pkv_status pkv_kv_evict_select(const float* weights, int64_t weights_stride,
  *   keep_heads: 1 or num_kv_heads.
  *   keep_lens:  int32 [num_seqs].
  * The K and V pools must not overlap, and the blocks written to must belong to
- * one sequence alone: copy shared ones on write first (pkv_kv_block_copy).  An entry that is out of range or order
- * sets PKV_DEVERR_KEEP, one in a block id outside the pool PKV_DEVERR_BLOCK;
- * such rows are not moved.  A sequence with keep_lens[r] outside [0,
- * min(keep_stride, seq_lens[r] - base)], base outside [0, seq_lens[r]], or (with weights) more
- * rows than weights_stride sets PKV_DEVERR_LENGTH and is skipped.
+ * one sequence alone: copy shared ones on write first (pkv_kv_block_copy).  An
+ * entry that is out of range or order sets PKV_DEVERR_KEEP, one that would move
+ * from or to a block id outside the pool PKV_DEVERR_BLOCK; such rows are not
+ * moved, nor are their weights.  A sequence with keep_lens[r] outside [0,
+ * min(keep_stride, seq_lens[r] - base)], base outside [0, seq_lens[r]], or
+ * (with weights) more rows than weights_stride sets PKV_DEVERR_LENGTH and is
+ * skipped.
  * Bit-exact.  Any block_size; head_dim x element a multiple of 16 bytes, 16 KiB
  * at most (MXFP8: head_dim a multiple of 32); fewer than 2^32 - 1 pool rows.
  * num_seqs and num_kv_heads <= 65535. */

@@ -753,6 +753,14 @@ __global__ void __launch_bounds__(kThreads) kv_compact_kernel(const CompactArgs 
       for (int u = 0; u < kCmSmall; ++u) {
         const int j = j0 + u * kThreads + tid;
         k[u] = j < s.n ? kept_row(a, s, __ldg(keep + j), kept_before(keep, j), j) : -1;
+        if (k[u] == j) k[u] = -1;  // in its place already
+      }
+#pragma unroll
+      for (int u = 0; u < kCmSmall; ++u) {  // a row that K and V do not move: nor its weight
+        if (k[u] < 0) continue;
+        const int from = table_entry(a, r, s.base + k[u]);
+        const int to = table_entry(a, r, s.base + j0 + u * kThreads + tid);
+        if (pool_row(a, from, 0) == kCmSkip || pool_row(a, to, 0) == kCmSkip) k[u] = -1;
       }
 #pragma unroll
       for (int u = 0; u < kCmSmall; ++u) x[u] = k[u] >= 0 ? w[k[u]] : 0.f;

@@ -54,6 +54,8 @@
 //     than 2^8 (exact), by a TMEM load/multiply/store of the row's O.
 #include <math.h>
 
+#include <atomic>
+
 #include "draft.cuh"
 #include "mx_widen.cuh"
 #include "plan.cuh"
@@ -1114,11 +1116,14 @@ static cudaError_t launch_draft_tc_t(const CUtensorMap& tmq, const CUtensorMap& 
   constexpr int smem = DtSmem<D, kTiles>::total;
   auto kern = draft_tc_kernel<D, kTiles, kMx>;
   if constexpr (kMx) {  // with fewer registers at launch the softmax warps would wait for theirs for ever
-    static const bool enough = [&] {
+    static std::atomic<int> regs{0};  // once known; a query that fails is asked again
+    if (regs.load(std::memory_order_relaxed) == 0) {
       cudaFuncAttributes f;
-      return cudaFuncGetAttributes(&f, kern) == cudaSuccess && f.numRegs >= kDtMxRegs;
-    }();
-    if (!enough) return cudaErrorInvalidConfiguration;
+      cudaError_t e = cudaFuncGetAttributes(&f, kern);
+      if (e != cudaSuccess) return e;
+      regs.store(f.numRegs, std::memory_order_relaxed);
+    }
+    if (regs.load(std::memory_order_relaxed) < kDtMxRegs) return cudaErrorInvalidConfiguration;
   }
   static SmemAttrCache attr_cache;
   cudaError_t e = ensure_smem_limit(kern, smem, attr_cache);

@@ -21,3 +21,13 @@ def test_each_warpgroup_moves_its_registers_by_one_instruction():
     assert warps["kDtSoftWarps"] % 4 == warps["kDtWidenWarps"] % 4 == int(first.group(1)) % 4 == 0
     before = text[:text.index("give_registers<kDtMxIssueRegs>()")]
     assert re.search(r"else if \(warp >= kDtSoftWarps && warp < kDtWidenFirst\) \{\s*if \(kMx\)\s*$", before)
+
+
+def test_a_failed_query_is_not_kept():
+    # the launcher may keep what the attribute query said, not that it failed:
+    # no initialiser of a static holds the query
+    path = os.path.join(ROOT, "paged_kv_cache_41_gb300", "csrc", "kernels", "draft_tc.cu")
+    text = re.sub(r"//[^\n]*", "", open(path).read())
+    assert "cudaFuncGetAttributes" in text
+    for m in re.finditer(r"static [^;]*?=\s*\[&\]\s*\{.*?\}\(\);", text, flags=re.S):
+        assert "cudaFuncGetAttributes" not in m.group(0)

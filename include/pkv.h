@@ -465,7 +465,8 @@ pkv_status pkv_draft_tree_attention(
  * keep with pkv_kv_evict_select and move them together, in place, with
  * pkv_kv_compact; the sequence then has new_lens[r] rows, and the blocks past
  * ceil(new_lens[r] / P) are free.  Rows are chosen per kv head: after a
- * compaction row j of two kv heads may hold different tokens. */
+ * compaction row j of two kv heads may hold different tokens.  (A sequence of
+ * pkv_pool.h gives those blocks back by pkv_seq_truncate.) */
 
 /* Bytes of device workspace pkv_paged_attention_decode_weights needs; 0 for
  * unsupported or invalid sizes.  Beside the decode's it holds a score for

@@ -80,6 +80,13 @@ int pkv_seq_append_tokens(pkv_pool* pool, pkv_seq* seq, int64_t n,
                           int64_t* slots_out, int64_t* cow_pair_out,
                           int32_t* cow_count);
 
+/* Shorten seq to its first `len` tokens (0 .. its length): after an eviction
+ * (pkv_kv_compact moved the kept rows to the front) or for drafted tokens that
+ * were not accepted.  The blocks past ceil(len / block_size) lose this
+ * reference; the next append goes to position len.  Returns -1 for a length
+ * outside that range. */
+int pkv_seq_truncate(pkv_pool* pool, pkv_seq* seq, int64_t len);
+
 /* Dense [num_seqs, max_blocks] int32 table, padded with -1, and the int32
  * context lengths.  Returns -1 if a sequence has more than max_blocks
  * blocks. */

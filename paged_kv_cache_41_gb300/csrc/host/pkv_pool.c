@@ -188,6 +188,15 @@ int pkv_seq_append_tokens(pkv_pool* pool, pkv_seq* seq, int64_t n,
   return 0;
 }
 
+int pkv_seq_truncate(pkv_pool* pool, pkv_seq* seq, int64_t len) {
+  if (len < 0 || len > seq->len) return -1;
+  const int32_t keep = (int32_t)((len + pool->block_size - 1) / pool->block_size);
+  for (int32_t j = keep; j < seq->nblocks; ++j) pkv_pool_decref(pool, seq->blocks[j]);
+  seq->nblocks = keep;
+  seq->len = len;
+  return 0;
+}
+
 int pkv_build_block_tables(pkv_seq* const* seqs, int32_t num_seqs,
                            int32_t max_blocks, int32_t* tables_out,
                            int32_t* lens_out) {

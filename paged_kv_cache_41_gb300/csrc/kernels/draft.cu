@@ -21,10 +21,10 @@
 //   * a hidden row's weight is stored as -1 and skipped, not multiplied, so
 //     an infinity or NaN in it cannot leak; rows past the last drafted one
 //     are never read.  Tiles without hidden rows look at no weight's sign.
-// The fp32 FMAs bound it, 256 per (row, key) at head_dim 128: fp32 operands
-// would lose 13 bits or more on the tensor cores.  16 requests with trees of 5
-// to 27, 32 query and 8 kv heads: 747 us, 24 TFLOP/s, of the 74 that the FMAs
-// can do.
+// The fp32 FMAs bound it, 256 per (row, key) at head_dim 128.  (One TF32 term on
+// the tensor cores would lose 13 bits of an operand; sums of several terms, and
+// packed FMAs here, are untried.)  16 requests with trees of 5 to 27, 32 query
+// and 8 kv heads: 748 us, 24 TFLOP/s, of the 74 that the FMAs can do.
 #include <math.h>
 
 #include <type_traits>

@@ -11,9 +11,11 @@
 // of the measured copy bandwidth, and 12.6 MFLOP per 128 rows (P in two terms:
 // 4.2 of QK, 8.4 of PV), 1.0 us of its share of the measured bf16 rate: the
 // bytes up to 128 rows, the MMAs past them.  Measured, 32 query and 8 kv heads:
-// 16 requests with trees of 5 to 27 75 us (3.9 TB/s over the call; P in one term
-// 66); 64 requests with trees of 64 345 us (1.29 PFLOP/s of MMAs; one term 288);
-// MXFP8, 64 query heads, 12 requests 75 us (one term 72).
+// 16 requests with trees of 5 to 27 76 us (3.8 TB/s over the call; P in one term
+// 66); 64 requests with trees of 64 342 us (1.30 PFLOP/s of MMAs; one term 288);
+// MXFP8, 64 query heads, 12 requests 75 us (one term 72).  No pipe is full in any
+// of them (64 trees: tensor 58% of its cycles, issue 0.50, DRAM 46%): what is
+// left is the latency between the steps of a job, and of a stage's widening.
 //
 // Design:
 //   * the work split, the pieces and their records are the decode's
@@ -73,8 +75,8 @@ constexpr int kDtWidenFirst = kDtSoftWarps + 4;
 constexpr int dt_threads(bool mx) { return (mx ? kDtWidenFirst + kDtWidenWarps : kDtSoftWarps + 3) * 32; }
 // Registers a thread of the MXFP8 kernel: 96 at launch (20 warps), of which the
 // others give some to the softmax warps, whose loop spilled into L2 (the L1 is
-// shared memory here; 12 requests: 90.7 us, 73.7 so): 128 x 64 + 256 x 120 +
-// 256 x 88 = 640 x 96.
+// shared memory here; 12 requests, P in one term: 90.7 us, 73.7 so): 128 x 64 +
+// 256 x 120 + 256 x 88 = 640 x 96.
 constexpr int kDtMxRegs = 96, kDtMxIssueRegs = 64, kDtMxWidenRegs = 88, kDtMxSoftRegs = 120;
 static_assert(128 * kDtMxIssueRegs + 256 * kDtMxSoftRegs + 256 * kDtMxWidenRegs <= dt_threads(true) * kDtMxRegs,
               "the warpgroups' registers come from the launch's");
@@ -86,7 +88,8 @@ constexpr int dt_chunk(bool mx) { return mx ? 32 : 64; }
 // Stage descriptors in flight.  A bf16 stage is described when its ring tiles
 // are free.  An MXFP8 one is described once the stage kDtAhead before it has
 // been widened; the widening warps send for its codes and then wait for the
-// tiles themselves (12 requests, 64 query heads: 90.7 us, described as bf16's
+// tiles themselves (12 requests, 64 query heads, before the registers moved and
+// with P in one term: 90.7 us, described as bf16's
 // 96).  So when stage n is described, stage n - 2 has been widened, into a ring
 // of 12 tiles at most: the PVs of stage n - 8 are done, and a softmax group,
 // which may be a stage without a job of its own behind (the end of a piece,
@@ -145,8 +148,8 @@ __device__ __forceinline__ float max3(float a, float b, float c) {
 }
 
 // Two weights as bf16 pairs, p = hi + lo to 2^-14.9 of p.  hi is p cut off and lo
-// what is left, of p (1 + 2^-20): neither is ever negative, nor 0 unless p is,
-// so that an infinity of V stays one in hi V + lo V.
+// what is left, of p (1 + 2^-20): neither is ever negative, nor 0 (above 2^-106)
+// unless p is, so that an infinity of V stays one in hi V + lo V.
 __device__ __forceinline__ void split_weights(float p0, float p1, uint32_t& hi, uint32_t& lo) {
   const uint32_t b0 = __float_as_uint(p0), b1 = __float_as_uint(p1);
   hi = __byte_perm(b0, b1, 0x7632);

@@ -571,7 +571,7 @@ cudaError_t launch_evict_select(const SelectArgs& a, cudaStream_t stream) {
 // cp.async (a plain load would have to arrive before the barrier that orders
 // the stores), several tiles ahead, and works out the rows' places further
 // ahead still.  Bound by the bytes: every moved row read once and written
-// once (64 bf16 requests, 253 MB kept: 83.4 us, 6.06 TB/s read + written).
+// once (64 bf16 requests, 253 MB kept: 85 us, 5.95 TB/s read + written).
 // Where the chains are few, a row's columns are dealt to several CTAs and the
 // ring is deeper (three fp32 sequences, 7777 rows kept: 20 us, 2.4 TB/s; then
 // the order of a chain's tiles bounds it).

@@ -836,11 +836,12 @@ DraftWorkspace draft_workspace(const pkv_cache_desc* c, int32_t num_seqs, int32_
     w.tiles = rows > pkv::kDraftRows ? 2 : 1;
     const int per = w.tiles * pkv::kDraftRows;
     w.row_tiles = (rows + per - 1) / per;
-    // Work units (kernels/plan.cuh).  A least-squares fit of the CTAs' times
-    // gave a piece (its Q, the drained pipeline, its outputs) 0.8 stages with
-    // one row tile (16 requests, trees of 5 to 27) and 3.4 with two (64
-    // requests, trees of 64).  An MXFP8 pool's stages take several times as
-    // long: 12 requests, two row tiles, 73.3, 71.9 and 72.3 us for 1, 2 and 3.
+    // Work units (kernels/plan.cuh): a piece (its Q, the drained pipeline, its
+    // outputs) costs one stage with one row tile (16 requests, trees of 5 to 27:
+    // 75.7, 75.5 and 76.0 us for 1, 2 and 3 units) and three and a half with two
+    // (64 requests, trees of 64: 348, 342 and 345 us for 5, 7 and 9).  An MXFP8
+    // pool's stages take several times as long: 12 requests, two row tiles, 78.1,
+    // 75.3 and 75.4 us for 1, 2 and 3.
     w.stage_units = 2;
     w.piece_units = w.tiles > 1 && c->dtype != PKV_MXFP8 ? 7 : 2;
     // As many CTAs as make a share one stage, where that is fewer than the SMs:

@@ -543,7 +543,7 @@ def paged_attention_decode_weights(q, k_cache, v_cache, block_tables, seq_lens, 
     """The paged decode, which also updates every cached row's running score
     (include/pkv.h): weights [B, Hkv, n] float32, in place, becomes decay *
     weights + the row's attention weight summed over the query heads of its kv
-    head.  Returns out (and writes lse [B, Hq] float32 when given)."""
+    head (n bounds the lengths; it may be a view of wider rows).  Returns out (and writes lse [B, Hq] float32 when given)."""
     desc = _pair_desc(k_cache, v_cache)
     b, hq, d = q.shape
     _, max_blocks = block_tables.shape
@@ -578,7 +578,9 @@ def kv_evict_select(weights, seq_lens, budget, *, num_sinks=0, num_recent=0, kee
     """Choose the rows each sequence and kv head keeps within ``budget``
     (include/pkv.h): its first num_sinks, its last num_recent and the heaviest
     others.  weights: [B, Hkv, n] float32; seq_lens: int32 [B].  Returns (keep
-    int32 [B, Hkv, budget], ascending and -1 padded, new_lens int32 [B])."""
+    int32 [B, Hkv, budget], ascending and -1 padded, new_lens int32 [B]).  n sizes
+    the launch: of a buffer at the cache's capacity pass the view of as many
+    columns as the longest sequence may have."""
     b, hkv, _ = weights.shape
     _dense("seq_lens", seq_lens, torch.int32, (b,))
     stride, n = _score_rows("weights", weights, b, hkv)

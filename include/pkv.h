@@ -445,7 +445,8 @@ size_t pkv_draft_tree_workspace_bytes(const pkv_cache_desc* cache, int32_t num_s
  *                  overlap on the GPU need one each.
  * A sequence whose range descends, is longer than max_draft, passes num_rows,
  * or ends beyond its block table row sets PKV_DEVERR_LENGTH and its query
- * rows are not written.
+ * rows are not written.  A block id outside the pool sets PKV_DEVERR_BLOCK and is
+ * not followed; what its sequence's query rows then hold is unspecified.
  * Supported: block_size 16 or a multiple of 32 up to 256; head_dim 64 or 128;
  * Hq / Hkv in {1, 2, 4, 8}; num_seqs <= 65535; every cache dtype (bf16: num_blocks
  * * block_size / 8 within int32). */

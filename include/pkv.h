@@ -91,6 +91,9 @@ typedef enum { PKV_F32 = 0, PKV_BF16 = 1, PKV_MXFP8 = 2 } pkv_dtype;
 #define PKV_DEVERR_LENGTH 4u   /* a length < 0 or beyond its block table row     */
 #define PKV_DEVERR_TIMEOUT 8u  /* a bounded wait inside a kernel ran out         */
 #define PKV_DEVERR_KEEP 16u    /* a kept row out of range or out of order       */
+#define PKV_DEVERR_POSITION 32u /* a position past the table of angles         */
+#define PKV_DEVERR_TOKEN 64u   /* a drafted token outside the vocabulary         */
+#define PKV_DEVERR_POOL 128u   /* a request that needs more blocks than are free */
 
 /* Shape of one paged K/V pool (host struct, passed by pointer). */
 typedef struct {
@@ -578,6 +581,169 @@ pkv_status pkv_kv_compact(const pkv_cache_desc* cache, void* k_cache, void* v_ca
                           const int32_t* base_lens, const int32_t* keep, int32_t keep_heads,
                           int64_t keep_stride, const int32_t* keep_lens, int32_t num_seqs,
                           void* stream);
+
+/* ------------------------------------------------------------------------
+ * The step around the cache: blocks and slots, the rows that go into them, and
+ * the verdict on what was drafted, all on the GPU.
+ * (The paper has no counterpart but for the slot arithmetic, M5.3 0x03D, and
+ * the append, 0x04E.)
+ *
+ * A step takes blocks and slots for its new rows (pkv_kv_blocks_update),
+ * normalises, rotates and appends them (pkv_qk_norm_rope_append), attends, and
+ * where tokens were drafted verifies them (pkv_draft_verify), moves the accepted
+ * rows together (pkv_kv_compact) and gives the other rows' blocks back
+ * (pkv_kv_blocks_update again). */
+
+/* Bring every request from seq_lens[r] rows to new = base + add[r] (base =
+ * base_lens[r], or 0): its block table, and slots and positions of its new rows.
+ * A shorter request gives the blocks past ceil(new / P) back, a longer one takes
+ * what it lacks.  A speculative step grows by add = the drafted rows (base_lens =
+ * seq_lens), then goes to base_lens = the committed lengths and add = the keep
+ * lengths; an eviction goes to add = its new_lens; add = 0 without base_lens
+ * ends a request.
+ *   block_tables:  int32 [num_seqs, max_blocks_per_seq], read and written:
+ *                  entries taken get ids, entries given back -1; no other entry
+ *                  is touched.  Every block belongs to one sequence alone.
+ *   seq_lens, base_lens, add: int32 [num_seqs]; base_lens may be NULL.
+ *   free_ids:      int32 [num_blocks], read and written: the free ids, a stack
+ *                  whose top is free_ids[count - 1].  Ids go onto it in
+ *                  descending order of (request, block), then come off it in
+ *                  ascending order, so growing and shrinking back leaves it as
+ *                  it was.  Entries past the count keep stale ids.
+ *   free_count:    int32 [1], read; free_count_out: int32 [1], written (the two
+ *                  may be one).
+ *   window, num_sinks: where window > 0, blocks that no decode over
+ *                  min(seq_lens[r], new) rows or more sees
+ *                  (pkv_paged_attention_decode_window) are given back too, behind the
+ *                  sinks: from the window
+ *                  downwards to the first entry that is negative already.
+ *                  0: none.
+ *   out_lens:      int32 [num_seqs], written: the new lengths; must not overlap
+ *                  seq_lens, base_lens or add.
+ *   row_ptr:       int32 [num_seqs + 1], written: request r's new rows are rows
+ *                  row_ptr[r] .. row_ptr[r + 1] - 1 of the step (none where it
+ *                  shrinks), as pkv_draft_tree_attention's draft_ptr.
+ *   slots:         int64 [num_rows], written whole: the new rows' slots for the
+ *                  appends, then -1.
+ *   positions:     int32 [num_rows] or NULL, written whole: their positions
+ *                  seq_lens[r], seq_lens[r] + 1, ..., then -1 (the rows of a drafted
+ *                  tree are rotated by their depth instead).
+ * A request whose growth does not find free blocks (requests are served in
+ * order; those that need none always are), or whose rows pass num_rows, keeps its length
+ * and table, its rows (below num_rows) get -1, and PKV_DEVERR_POOL or
+ * PKV_DEVERR_LENGTH is set; so does one whose lengths are negative or pass its
+ * table row (PKV_DEVERR_LENGTH; it has no rows).  An id outside the pool sets
+ * PKV_DEVERR_BLOCK: given back it is dropped, taken it becomes -1.
+ * Exact and deterministic.  Any block_size; num_blocks and num_rows <= INT32_MAX;
+ * num_seqs <= 65535. */
+pkv_status pkv_kv_blocks_update(const pkv_cache_desc* cache, int32_t* block_tables,
+                                int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                const int32_t* base_lens, const int32_t* add, int32_t num_seqs,
+                                int32_t num_sinks, int32_t window, int32_t* free_ids,
+                                const int32_t* free_count, int32_t* free_count_out,
+                                int32_t* out_lens, int32_t* row_ptr, int64_t* slots,
+                                int32_t* positions, int64_t num_rows, void* stream);
+
+/* Bytes of device workspace pkv_paged_attention_decode_window needs; 0 for
+ * unsupported or invalid sizes.  Depends on the device (its SM count). */
+size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
+                                         int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                         int32_t window, int32_t num_sinks);
+
+/* pkv_paged_attention_decode under a sliding window with sinks: of a sequence of
+ * T = seq_lens[r] rows, row t is seen where t < num_sinks or t >= T - window; out
+ * and lse are over the rows that are seen.  Blocks without a seen row are not
+ * read, and neither are their table entries' ids: they may be -1
+ * (pkv_kv_blocks_update gives such blocks back).
+ *   window:        >= 1: the newest row is always seen.
+ *   num_sinks:     >= 0.
+ *   workspace:     at least pkv_decode_window_workspace_bytes bytes, 256-byte
+ *                  aligned; nothing in it needs to be initialised.  Calls that may
+ *                  overlap on the GPU need one each.
+ * Other arguments, support and errors as in pkv_paged_attention_decode
+ * (partition_size 0). */
+pkv_status pkv_paged_attention_decode_window(
+    const pkv_cache_desc* cache, void* out, float* lse, const void* q, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* seq_lens, int32_t num_seqs, int32_t num_q_heads, float scale, int32_t window,
+    int32_t num_sinks, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Norms of queries and keys, their rotation, and the append.  For token i and
+ * every head row x of q and k (fp32 arithmetic, one rounding at the end):
+ *   x <- x * rsqrt(mean(x^2) + eps) * weight          (where a weight is given)
+ *   (x_a, x_b) <- (x_a c - x_b s, x_b c + x_a s)      for the pairs j < rot / 2:
+ * (a, b) = (j, j + rot / 2), or (2 j, 2 j + 1) where interleaved; c and s are
+ * cos_sin[p, j] and cos_sin[p, rot / 2 + j] at the token's position p on the axis
+ * of pair j.  q goes to out; k, and v as it is, go to slot slots[i] of the pools
+ * (an MXFP8 pool: quantised from the fp32 values, as pkv_kv_append does).
+ *   q, k, v:       [num_tokens, Hq or Hkv, D], head rows contiguous and *_stride
+ *                  elements from token to token (a packed projection's parts).
+ *   out:           [num_tokens, Hq, D], contiguous; q itself where q is.
+ *   slots:         int64 [num_tokens], as pkv_kv_append's: a negative one appends
+ *                  nothing (q is still rotated), one past the pool sets
+ *                  PKV_DEVERR_SLOT too.  Distinct.
+ *   positions:     int32, axis x of token i at [x * pos_stride + i].  A negative
+ *                  one marks a row of no token: nothing of it is written.  One at
+ *                  or past max_positions does the same and sets
+ *                  PKV_DEVERR_POSITION.
+ *   num_axes:      1 to 3 (time, or time, height and width).
+ *   axis_of:       HOST uint8 [rot / 2], the axis of each pair, below num_axes;
+ *                  NULL: axis 0.
+ *   cos_sin:       float [max_positions, rot]; may be NULL where rot is 0.
+ *   rot:           rotated elements of a head, the first ones: a multiple of 16
+ *                  in 0 .. D.
+ *   q_weight, k_weight: float [D], or NULL: no norm.
+ * q, k, v and out are bf16 (fp32 with a PKV_F32 cache); pointers 16-byte aligned,
+ * strides whole multiples of 16 bytes.  head_dim 64 or 128; any block_size. */
+pkv_status pkv_qk_norm_rope_append(
+    const pkv_cache_desc* cache, void* out, void* k_cache, void* v_cache, const void* q,
+    int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+    const int64_t* slots, const int32_t* positions, int64_t pos_stride, int32_t num_axes,
+    const uint8_t* axis_of, const float* cos_sin, int32_t max_positions, int32_t rot,
+    int32_t interleaved, const float* q_weight, const float* k_weight, float eps,
+    int64_t num_tokens, int32_t num_q_heads, void* stream);
+
+/* Verify drafted tokens against the target's probabilities, so that what is
+ * emitted is distributed as the target's own samples.  Sequence r's drafted rows
+ * are those of pkv_draft_tree_attention: n = draft_ptr[r + 1] - draft_ptr[r], row
+ * 0 the root (the last token emitted, accepted by definition), the others a tree
+ * below it given by masks.  A row's parent is the highest bit of its mask below
+ * its own; rows whose parents do not lead to the root are never reached.  From
+ * node i (first the root) its children are tried in ascending order:
+ *   with draft_probs (tokens sampled, one after the other, from row i of it):
+ *     child x is accepted where u q(x) R < r(x), r(v) = max(p(v) - c q(v), 0), with
+ *     p, q row i of target_probs and draft_probs, c = 0, R = 1 and r = p for the first child;
+ *     turned down, c grows by R, and R becomes the sum of the new r;
+ *   without (tokens the draft chose outright): child x is accepted where u R <
+ *     p(x), R = 1 less the p of the children turned down before it (a token
+ *     turned down before: p = 0).
+ * u is uniforms[x's row].  An accepted child becomes node i.  At a node where no
+ * child is accepted the next token is the first v whose running sum of r (without draft_probs:
+ * of p with the tokens turned down at this node taken out) passes
+ * uniforms[the root's row] times the whole; p itself where nothing is left.
+ *   target_probs, draft_probs: float [num_rows, vocab], target_stride and
+ *                  draft_stride elements from row to row; row i follows drafted
+ *                  row i.  Each in [0, 1] and summing to about 1 (held there: NaN
+ *                  and below as 0, above as 1); multiples of 2^-60 below that are cut.
+ *                  draft_probs may be NULL.
+ *   draft_tokens:  int32 [num_rows]; one outside the vocabulary is never accepted
+ *                  and sets PKV_DEVERR_TOKEN (the root's is not read as a token).
+ *   draft_ptr, masks, num_rows, max_draft: as in pkv_draft_tree_attention.
+ *   uniforms:      float [num_rows] in [0, 1) (held there; NaN as 0).
+ *   keep:          int32 [num_seqs, max_draft], written whole: the accepted rows,
+ *                  0 first, ascending, then -1: pkv_kv_compact's list with keep_heads 1.
+ *   keep_lens:     int32 [num_seqs], written; 0 for a sequence without rows.
+ *   next_tokens:   int32 [num_seqs], written; -1 for a sequence without rows or
+ *                  a row of p without any mass.
+ * A sequence whose range descends, is longer than max_draft or passes num_rows
+ * sets PKV_DEVERR_LENGTH and counts as one without rows.
+ * Sums are exact and the result does not depend on the launch.  num_seqs <= 65535. */
+pkv_status pkv_draft_verify(const float* target_probs, int64_t target_stride,
+                            const float* draft_probs, int64_t draft_stride, int32_t vocab,
+                            const int32_t* draft_tokens, const int32_t* draft_ptr,
+                            const uint64_t* masks, const float* uniforms, int32_t num_seqs,
+                            int32_t num_rows, int32_t max_draft, int32_t* keep,
+                            int32_t* keep_lens, int32_t* next_tokens, void* stream);
 
 /* Read and clear the device error word of the current device.  Synchronises
  * `stream` first.  *code_out receives the PKV_DEVERR_* bits seen since the

@@ -29,6 +29,7 @@ CUDA_SOURCES = [
     "kernels/append_copy.cu",
     "kernels/decode.cu",
     "kernels/decode_scores.cu",
+    "kernels/decode_window.cu",
     "kernels/decode_tc.cu",
     "kernels/decode_tc_mx.cu",
     "kernels/prefix_tc.cu",
@@ -36,12 +37,16 @@ CUDA_SOURCES = [
     "kernels/draft.cu",
     "kernels/draft_tc.cu",
     "kernels/evict.cu",
+    "kernels/blocks.cu",
+    "kernels/rope_append.cu",
+    "kernels/verify.cu",
 ]
 # Attention kernels take exp2/log2/division from the hardware approximations
 # (softmax in base 2, well inside the attention tolerance).
 PER_SOURCE_FLAGS = {
     "kernels/decode.cu": ["--use_fast_math"],
     "kernels/decode_scores.cu": ["--use_fast_math"],
+    "kernels/decode_window.cu": ["--use_fast_math"],
     "kernels/decode_tc.cu": ["--use_fast_math"],
     "kernels/decode_tc_mx.cu": ["--use_fast_math"],
     "kernels/prefix_tc.cu": ["--use_fast_math"],

@@ -60,9 +60,7 @@ cudaError_t launch_kv_append(void* k_cache, void* v_cache, const void* k, const 
 // MXFP8 append: one warp per (token, kv head) row of D bf16 elements, each
 // lane EPL = D / 32 consecutive ones, so a 32-element scale group is 32 / EPL
 // lanes.  The group's scale is the smallest power of two X with
-// max |x| / X <= 448 (E4M3's largest finite value): for max |x| = (1 + f)
-// 2^E (fp32 fields), X = 2^(E - 8), or 2^(E - 7) when 1 + f > 1.75; zero and
-// subnormal maxima take the smallest scale.  Elements are x / X (exact: a
+// max |x| / X <= 448 (mx_scale_exponent).  Elements are x / X (exact: a
 // power-of-two multiply) rounded to the nearest E4M3 code, ties to even.
 template <int D>
 __global__ void __launch_bounds__(256) kv_append_mxfp8_kernel(
@@ -107,12 +105,9 @@ __global__ void __launch_bounds__(256) kv_append_mxfp8_kernel(
     for (int i = 0; i < EPL; ++i) amax = fmaxf(amax, fabsf(x[i]));
 #pragma unroll
     for (int o = 1; o < LPG; o <<= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const uint32_t bits = __float_as_uint(amax);
-    const int E = (int)(bits >> 23) - 127;
-    int e = E - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
-    if ((bits >> 23) == 0 || e < -127) e = -127;  // zero or tiny group
+    const int e = mx_scale_exponent(amax);
     const uint32_t sbyte = (uint32_t)(e + 127);
-    const float inv = __uint_as_float((uint32_t)(127 - e) << 23);  // 2^-e, e in [-127, 126]
+    const float inv = mx_inverse_scale(e);
     uint32_t packed = 0;
 #pragma unroll
     for (int i = 0; i < EPL; i += 2) {

@@ -279,6 +279,21 @@ __device__ __forceinline__ float e8m0_value(uint32_t s) {
   return __uint_as_float(s ? s << 23 : 0x00400000u);
 }
 
+// The exponent e of an MXFP8 group's scale 2^e: the smallest with amax / 2^e <=
+// 448, E4M3's largest finite value.  For amax = (1 + f) 2^E (fp32 fields) that
+// is E - 8, or E - 7 when 1 + f > 1.75; zero and subnormal maxima take -127.
+__device__ __forceinline__ int mx_scale_exponent(float amax) {
+  const uint32_t bits = __float_as_uint(amax);
+  const int E = (int)(bits >> 23) - 127;
+  const int e = E - 8 + ((bits & 0x7fffffu) > 0x600000u ? 1 : 0);
+  return (bits >> 23) == 0 || e < -127 ? -127 : e;
+}
+
+// 2^-e for such an exponent, e in [-127, 126].
+__device__ __forceinline__ float mx_inverse_scale(int e) {
+  return __uint_as_float((uint32_t)(127 - e) << 23);
+}
+
 __device__ __forceinline__ void store_out(float* p, float v) { *p = v; }
 __device__ __forceinline__ void store_out(__nv_bfloat16* p, float v) { *p = __float2bfloat16_rn(v); }
 

@@ -1,6 +1,7 @@
 // decode_partial.cuh -- the partial kernel of the paged decode on CUDA cores:
 // decode.cu has its design and launches the decode with it, decode_scores.cu
-// the variant that also leaves every row's scores.
+// the variant that also leaves every row's scores, decode_window.cu the one
+// under a sliding window.
 #pragma once
 
 #include <math.h>
@@ -144,12 +145,14 @@ __device__ __forceinline__ void store_vec(__nv_bfloat16* p, const float (&o)[N])
 
 //
 // With kScores the base-2 score of every row and head also goes to srow[row *
-// G + head] (see DecodeArgs::scores).
-template <typename T, int D, int G, bool kTail, bool kScores>
+// G + head] (see DecodeArgs::scores).  With kWin the rows [hide_lo, hide_hi) are
+// masked too (kTail only).
+template <typename T, int D, int G, bool kTail, bool kScores, bool kWin>
 __device__ __forceinline__ void decode_chunk(const T* __restrict__ kt, const T* __restrict__ vt,
                                              const uint8_t* __restrict__ ksc,
                                              const uint8_t* __restrict__ vsc, int row0,
-                                             int nvalid, const float2 (&q2)[G][D / 32],
+                                             int nvalid, int hide_lo, int hide_hi,
+                                             const float2 (&q2)[G][D / 32],
                                              float2 (&acc)[G][D / 32], float& m_used,
                                              float& l_run, float* __restrict__ red, int hw, int l16,
                                              float* __restrict__ srow) {
@@ -157,6 +160,10 @@ __device__ __forceinline__ void decode_chunk(const T* __restrict__ kt, const T* 
   constexpr int EP2 = EPL / 2;
   constexpr int NV = 2 * G;    // values per half-warp and chunk
   constexpr int LPV = 16 / NV; // lanes summing one value
+  auto seen = [&](int row) {
+    if constexpr (!kTail) return true;
+    return kWin ? row_seen(row, nvalid, hide_lo, hide_hi) : row < nvalid;
+  };
   // MXFP8: this lane's EPL elements lie in one 32-element scale group; its
   // V scale multiplies the weights (a power of two).  The K scales are
   // applied in the cross-lane sum, once per group of partials.
@@ -215,7 +222,7 @@ __device__ __forceinline__ void decode_chunk(const T* __restrict__ kt, const T* 
     if (sub == 0 && (!kTail || row0 + (l16 >> 3) < nvalid)) srow[row0 * G + j] = s2;
   }
   // ---- online softmax over the warp's 4 rows (rows differ in lane bits 3, 4)
-  const float sc = (!kTail || row0 + (l16 >> 3) < nvalid) ? s2 : -INFINITY;
+  const float sc = seen(row0 + (l16 >> 3)) ? s2 : -INFINITY;
   // The exponent base of a head moves only when one of its scores passes it
   // by more than 2^8 (m_used = -inf before a piece's first row), so most
   // chunks need neither the cross-row max nor a rescale.
@@ -245,7 +252,7 @@ __device__ __forceinline__ void decode_chunk(const T* __restrict__ kt, const T* 
     for (int g = 0; g < G; ++g) pg[tk][g] = __shfl_sync(0xffffffffu, p, (tk * G + g) * LPV, 16);
 #pragma unroll
   for (int tk = 0; tk < 2; ++tk) {
-    if (!kTail || row0 + tk < nvalid) {
+    if (seen(row0 + tk)) {
       float vf[EPL];
       VecLoad<T, EPL>::run(vt + (row0 + tk) * D + l16 * EPL, vf);
 #pragma unroll
@@ -260,10 +267,11 @@ __device__ __forceinline__ void decode_chunk(const T* __restrict__ kt, const T* 
   }
 }
 
-template <typename T, int D, int G, bool kScores = false>
+template <typename T, int D, int G, bool kScores = false, bool kWin = false>
 __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
     decode_partial_kernel(const __grid_constant__ CUtensorMap tmk,
-                          const __grid_constant__ CUtensorMap tmv, const DecodeArgs a) {
+                          const __grid_constant__ CUtensorMap tmv, const DecodeArgsOf<kWin> a) {
+  static_assert(!(kScores && kWin), "the descriptor's flags hold one of the two");
   using TQ = typename IoOf<T>::type;  // q and out
   constexpr int EPL = D / 16;  // head_dim elements per lane
   constexpr int EP2 = EPL / 2;
@@ -393,13 +401,14 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
           h = 0;
           do {
             ++r;
-            len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, P, a.err, false);
+            len = plan_len(a, r, P, false);
             pnt = (len + kStageRows - 1) / kStageRows;
           } while (pnt == 0);
         }
       }
-      const int k = kb + lane, row0 = i * kStageRows;
-      const int nvalid = min(kStageRows, len - row0);
+      const int k = kb + lane;
+      const StageRows sr = stage_rows<kStageRows>(a, r, len, i);
+      const int row0 = sr.row0, nvalid = sr.nvalid;
       const int b0 = row0 / P;
       const int nbox = (nvalid + TB - 1) / TB;  // 1 or 2 (two only when P < 32)
       const int32_t* tbl = a.block_tables + (int64_t)r * a.max_blocks + b0;
@@ -413,11 +422,20 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
         prefetch_l2_bulk(static_cast<const TQ*>(a.q) + (qr * a.num_q_heads + (int64_t)h * G) * D,
                          (uint32_t)(G * D * sizeof(TQ)));
       }
-      // the piece's q row rides in the box-count word (nbox is 1 or 2)
+      // the piece's q row rides in the box-count word (nbox is 1 or 2; 3: the
+      // second box alone, the first one's rows are hidden)
+      int code = nbox;
+      if constexpr (kWin) {
+        if (nbox == 2 && sr.hide_lo == 0 && sr.hide_hi >= TB) code = 3;
+      }
       const int qrow = a.q_rows ? __ldg(a.q_rows + r) : r;
-      dA[k & 63] = make_int4(id0, id1, row0 - b0 * P, nbox | (qrow << 2));
-      // with scores, the stage's index in its segment rides above the flags
-      dB[k & 63] = make_int4(r, h, nvalid, kScores ? flags | (i << 4) : flags);
+      dA[k & 63] = make_int4(id0, id1, row0 - b0 * P, code | (qrow << 2));
+      // with scores, the stage's index in its segment rides above the flags;
+      // under a window, its hidden rows
+      dB[k & 63] = make_int4(r, h, nvalid,
+                             kScores ? flags | (i << 4)
+                             : kWin  ? flags | (sr.hide_lo << 8) | (sr.hide_hi << 16)
+                                     : flags);
     }
     // the cursor moves to the stage after lane 31's
     cr = __shfl_sync(0xffffffffu, r, 31);
@@ -431,8 +449,9 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
   auto issue_stage = [&](int st, int k) {
     const int4 da = dA[k & 63];
     const int4 db = dB[k & 63];
-    const int nbox = da.w & 3;
-    const bool valid = da.x >= 0 && (int64_t)da.x < a.num_blocks &&
+    const int nbox = kWin && (da.w & 3) == 3 ? 2 : da.w & 3;
+    const int box0 = kWin && (da.w & 3) == 3 ? 1 : 0;  // the first box to load
+    const bool valid = (box0 == 1 || (da.x >= 0 && (int64_t)da.x < a.num_blocks)) &&
                        (nbox < 2 || (da.y >= 0 && (int64_t)da.y < a.num_blocks));
     if (lane == 0) sdesc[st] = db;
     if ((db.w & kPieceStart) && lane == 31)  // refresh the piece's q in L2 shortly before use
@@ -448,21 +467,21 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
     } else {
       if (lane == 0) {
         stage_ok[st] = 1;
-        mbar_arrive_expect_tx(&full[st], 2u * (box_bytes + (kIsMx<T> ? scale_box : 0u)) * (uint32_t)nbox);
+        mbar_arrive_expect_tx(&full[st], 2u * (box_bytes + (kIsMx<T> ? scale_box : 0u)) * (uint32_t)(nbox - box0));
       }
       __syncwarp();
       // one box per lane: lanes 0..nbox-1 load K, lanes 16..16+nbox-1 load V;
       // MXFP8: lanes 8.. and 24.. copy the same boxes' scale rows, which lie
       // contiguously in the head-major scale plane
       const int j = lane & 15;
-      if (j < nbox) {
+      if (j >= box0 && j < nbox) {
         T* dst = tiles + (size_t)st * 2 * L.tile_elems + (lane < 16 ? 0 : L.tile_elems) + j * TB * D;
         tma_load_4d(dst, lane < 16 ? &tmk : &tmv, 0, db.y, j == 0 ? da.z : 0, j == 0 ? da.x : da.y,
                     &full[st]);
       }
       if constexpr (kIsMx<T>) {
         const int js = j - 8;
-        if (js >= 0 && js < nbox) {
+        if (js >= box0 && js < nbox) {
           const int64_t blk = js == 0 ? da.x : da.y;
           const int row = js == 0 ? da.z : 0;
           const uint8_t* src = (lane < 16 ? a.k_scales : a.v_scales) +
@@ -487,7 +506,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
       prefetch_tensormap(&tmk);
       prefetch_tensormap(&tmv);
     }
-    cT = effective_len(__ldg(a.seq_lens + cr), a.max_blocks, P, a.err, false);
+    cT = plan_len(a, cr, P, false);
     cpnt = (cT + kStageRows - 1) / kStageRows;
     compute_batch(0);  // lengths, block tables and q rows only
   }
@@ -550,15 +569,16 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
         for (int i = threadIdx.x; i < nvalid * G; i += kDecodeThreads) srow[i] = -INFINITY;
     }
     if (stage_ok[s]) {
-      if (nvalid == kStageRows) {
+      const int hide_lo = kWin ? (flags >> 8) & 255 : 0, hide_hi = kWin ? flags >> 16 : 0;
+      if (nvalid == kStageRows && hide_hi == 0) {
 #pragma unroll 1
         for (int cc = 0; cc < kStageRows / kChunk; ++cc)
-          decode_chunk<T, D, G, false, kScores>(kt, vt, ksc, vsc, cc * kChunk + rbase, kStageRows, q2, acc,
-                                                m_used, l_run, red, hw, l16, srow);
+          decode_chunk<T, D, G, false, kScores, kWin>(kt, vt, ksc, vsc, cc * kChunk + rbase, kStageRows, 0, 0,
+                                                      q2, acc, m_used, l_run, red, hw, l16, srow);
       } else {
-        for (int cc = 0; cc * kChunk < nvalid; ++cc)
-          decode_chunk<T, D, G, true, kScores>(kt, vt, ksc, vsc, cc * kChunk + rbase, nvalid, q2, acc, m_used,
-                                               l_run, red, hw, l16, srow);
+        for (int cc = kWin && hide_lo == 0 ? hide_hi / kChunk : 0; cc * kChunk < nvalid; ++cc)
+          decode_chunk<T, D, G, true, kScores, kWin>(kt, vt, ksc, vsc, cc * kChunk + rbase, nvalid, hide_lo,
+                                                     hide_hi, q2, acc, m_used, l_run, red, hw, l16, srow);
       }
     }
     if (flags & kPieceEnd) {
@@ -670,11 +690,11 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
   }
 }
 
-template <typename T, int D, int G, bool kScores = false>
-cudaError_t launch_partial(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeArgs& a,
+template <typename T, int D, int G, bool kScores = false, bool kWin = false>
+cudaError_t launch_partial(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeArgsOf<kWin>& a,
                            cudaStream_t stream) {
   const size_t smem = decode_smem_layout(D, (int)sizeof(T), G, a.num_stages).total;
-  auto kern = decode_partial_kernel<T, D, G, kScores>;
+  auto kern = decode_partial_kernel<T, D, G, kScores, kWin>;
   static SmemAttrCache attr_cache;
   cudaError_t e = ensure_smem_limit(kern, (int)smem, attr_cache);
   if (e != cudaSuccess) return e;

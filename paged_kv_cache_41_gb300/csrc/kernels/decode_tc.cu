@@ -75,11 +75,12 @@ constexpr int kStart = 1, kEnd = 2, kWholeSeg = 4, kSlotOne = 8;
 
 }  // namespace
 
-template <int G, bool kScores = false>
+template <int G, bool kScores = false, bool kWin = false>
 __global__ void __launch_bounds__(kTcThreads, 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv,
-                     const __grid_constant__ CUtensorMap tmq, const DecodeArgs a) {
+                     const __grid_constant__ CUtensorMap tmq, const DecodeArgsOf<kWin> a) {
+  static_assert(!(kScores && kWin), "the descriptor's flags hold one of the two");
   static_assert(G <= kTcN, "at most 16 query heads per kv head");
   constexpr uint32_t kIdQK = tc::idesc_bf16_f32(kTcRows, kTcN, 0, 0);
   constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kTcD, kTcN, 1, 0);
@@ -161,7 +162,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       prefetch_tensormap(&tmq);
     }
     int r = d0.x, h = d0.y, i = d0.z;
-    int len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, P, a.err, false);
+    int len = plan_len(a, r, P, false);
     int nt = (len + kTcRows - 1) / kTcRows;
     while (i >= nt) {  // the plan may name a segment's end: its next non-empty one
       i -= nt;
@@ -169,7 +170,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         h = 0;
         do {
           ++r;
-          len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, P, a.err, false);
+          len = plan_len(a, r, P, false);
           nt = (len + kTcRows - 1) / kTcRows;
         } while (nt == 0);
       }
@@ -179,8 +180,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // table read then overlaps the wait for a free slot
     const int j = lane & 15;
     auto box_block = [&](int r_, int i_, int len_) -> int {
-      const int row = i_ * kTcRows + j * TB;
-      return row < len_ && j * TB < kTcRows
+      const StageRows sr_ = stage_rows<kTcRows>(a, r_, len_, i_);
+      const int row = sr_.row0 + j * TB;
+      return j * TB < sr_.nvalid
                  ? __ldg(a.block_tables + (int64_t)r_ * a.max_blocks + row / P)
                  : 0;
     };
@@ -188,8 +190,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     if (a.plan_before_wait) pdl_wait();  // the K/V rows and q are read from here on
     int pieces = 0;
     // the previous stage's V boxes: this lane's block and first row, the box
-    // count and the kv head
-    int v_blk = 0, v_brow = 0, v_nbox = 0, v_h = 0;
+    // count and the kv head; under a window, the boxes without a seen row
+    int v_blk = 0, v_brow = 0, v_nbox = 0, v_h = 0, v_hide0 = 0, v_hide1 = 0;
     auto issue_v = [&](int kv) -> bool {
       const int sv = kv % kTcStages;
       if (kv >= kTcStages) {
@@ -200,9 +202,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
       }
-      if (lane == 0) mbar_arrive_expect_tx(&vfull[sv], (uint32_t)(v_nbox * TB * kTcD * 2));
+      if (lane == 0) mbar_arrive_expect_tx(&vfull[sv], (uint32_t)((v_nbox - (v_hide1 - v_hide0)) * TB * kTcD * 2));
       __syncwarp();
-      if (lane >= 16 && j < v_nbox)
+      if (lane >= 16 && j < v_nbox && (j < v_hide0 || j >= v_hide1))
         tma_load_5d(ring + (size_t)sv * 2 * kTcTile + kTcTile + j * TB * kTcD * 2, &tmv, 0, 0, 0, v_h,
                     (int)((int64_t)v_blk * (P / kRowGroup) + v_brow / kRowGroup), &vfull[sv]);
       issued_v = kv + 1;
@@ -224,8 +226,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           break;
         }
       }
-      const int t0 = i * kTcRows;
-      const int nvalid = min(kTcRows, len - t0);
+      const StageRows sr = stage_rows<kTcRows>(a, r, len, i);
+      const int t0 = sr.row0, nvalid = sr.nvalid;
+      int hide0 = 0, hide1 = 0;  // boxes that are not loaded
+      if constexpr (kWin) hidden_boxes(sr, TB, &hide0, &hide1);
       const int dseg = k - i;  // CTA stage index of the segment's first stage
       const bool start = k == 0 || i == 0;
       const bool end = k == n - 1 || i == nt - 1;
@@ -233,10 +237,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int qb = (pieces - 1) % kQBufs;
       const int flags = (start ? kStart : 0) | (end ? kEnd : 0) |
                         (end && i == nt - 1 && dseg >= 0 ? kWholeSeg : 0) |
-                        (dseg > 0 ? kSlotOne : 0) | (qb << 4) | (kScores ? i << 6 : 0);
+                        (dseg > 0 ? kSlotOne : 0) | (qb << 4) |
+                        (kScores ? i << 6 : kWin ? (sr.hide_lo << 8) | (sr.hide_hi << 16) : 0);
       const int nbox = (nvalid + TB - 1) / TB;  // per tensor
       int brow = (t0 + j * TB) % P;
-      const bool bad = j < nbox && (blk < 0 || (int64_t)blk >= a.num_blocks);
+      const bool load = j < nbox && (j < hide0 || j >= hide1);
+      const bool bad = load && (blk < 0 || (int64_t)blk >= a.num_blocks);
       if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.err, PKV_DEVERR_BLOCK);
       if (bad) {
         blk = (int)a.num_blocks;  // zero-filled out-of-range box
@@ -244,10 +250,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (lane == 0) {
         sdesc[s] = make_int4(r, h, nvalid, flags);
-        mbar_arrive_expect_tx(&kfull[s], (uint32_t)(nbox * TB * kTcD * 2 + (start ? 2 * G * 128 : 0)));
+        mbar_arrive_expect_tx(&kfull[s], (uint32_t)((nbox - (hide1 - hide0)) * TB * kTcD * 2 + (start ? 2 * G * 128 : 0)));
       }
       __syncwarp();
-      if (lane < 16 && j < nbox)
+      if (lane < 16 && load)
         tma_load_5d(ring + (size_t)s * 2 * kTcTile + j * TB * kTcD * 2, &tmk, 0, 0, 0, h,
                     (int)((int64_t)blk * (P / kRowGroup) + brow / kRowGroup), &kfull[s]);
       if (start && lane == 0) {
@@ -264,6 +270,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       v_blk = blk;
       v_brow = brow;
       v_nbox = nbox;
+      v_hide0 = hide0;
+      v_hide1 = hide1;
       v_h = h;
       if (k + 1 < n && ++i == nt) {  // on to the next non-empty segment
         i = 0;
@@ -271,7 +279,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           h = 0;
           do {
             ++r;
-            len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, P, a.err, false);
+            len = plan_len(a, r, P, false);
             nt = (len + kTcRows - 1) / kTcRows;
           } while (nt == 0);
         }
@@ -372,6 +380,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc::fence_after_sync();
       const int4 dsc = sdesc[s];
       const int nvalid = dsc.z, flags = dsc.w;
+      const int hide_lo = kWin ? (flags >> 8) & 255 : 0, hide_hi = kWin ? flags >> 16 : 0;
+      const bool seen = row_seen(row, nvalid, hide_lo, hide_hi);  // this thread's key row
       if (flags & kStart) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -396,7 +406,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool pass = false;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        sg[g] = row < nvalid ? __uint_as_float(v[g]) * cs : -INFINITY;
+        sg[g] = seen ? __uint_as_float(v[g]) * cs : -INFINITY;
         pass |= sg[g] > m[g] + 8.0f;
       }
       if constexpr (kScores) {  // stage flags >> 6 of its segment
@@ -479,14 +489,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           *reinterpret_cast<__nv_bfloat16*>(at + kQBytes) = lo;
         }
       }
-      // zero the rows of V past the tail (weight 0, bytes maybe NaN), once
+      // zero the rows of V that are not seen (weight 0, bytes maybe NaN), once
       // the stage's V has landed
-      if (nvalid < kTcRows &&
+      if ((nvalid < kTcRows || hide_hi > 0) &&
           !__all_sync(0xffffffffu, mbar_wait(&vfull[s], (k / kTcStages) & 1))) {
         if (lane == 0) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
         break;
       }
-      if (row >= nvalid) {
+      if (!seen) {
         unsigned char* vrow = ring + (size_t)s * 2 * kTcTile + kTcTile +
                               (row / kRowGroup) * kTcGroup + (row % kRowGroup) * 128;
 #pragma unroll
@@ -589,6 +599,16 @@ int decode_tc_resident_ctas() {
 cudaError_t launch_paged_decode_tc(const CUtensorMap& tmk, const CUtensorMap& tmv,
                                    const CUtensorMap& tmq, const DecodeArgs& a,
                                    cudaStream_t stream) {
+  if (a.window) {
+    auto kern = decode_tc_kernel<8, false, true>;
+    static SmemAttrCache window_cache;
+    cudaError_t e = ensure_smem_limit(kern, kTcSmem, window_cache);
+    if (e != cudaSuccess) return e;
+    e = launch_pdl(kern, dim3((unsigned)a.num_ctas), dim3(kTcThreads), kTcSmem, stream, tmk, tmv, tmq,
+                   WindowArgs(a, kTcRows));
+    if (e != cudaSuccess) return e;
+    return launch_decode_reduce(PKV_BF16, kTcD, a, stream);
+  }
   auto kern = a.scores ? decode_tc_kernel<8, true> : decode_tc_kernel<8>;
   static SmemAttrCache attr_cache[2];
   cudaError_t e = ensure_smem_limit(kern, kTcSmem, attr_cache[a.scores ? 1 : 0]);

@@ -124,6 +124,18 @@ struct DecodeArgs {
   // query heads of the kv head), or null.
   float* scores;
   int64_t scores_rows;
+  // Sliding window: a row is seen among the first num_sinks or the last window
+  // ones.  0: every row is.
+  int32_t window;
+  int32_t num_sinks;
+};
+
+// Arguments of the kernels of a windowed decode: a type of its own, so that
+// the work split counts what is seen (plan.cuh).
+struct WindowArgs : DecodeArgs {
+  int32_t stage_rows = 0;       // rows of one stage
+  WindowArgs() = default;
+  WindowArgs(const DecodeArgs& a, int rows) : DecodeArgs(a), stage_rows(rows) {}
 };
 
 // Partial kernel, then the LSE reduction of cut segments, on one stream.
@@ -133,6 +145,11 @@ cudaError_t launch_paged_decode(int dtype, int head_dim, int group, const CUtens
 
 // The partial kernel alone, leaving scores (args.scores; decode_scores.cu).
 cudaError_t launch_decode_partial_scores(int dtype, int head_dim, int group, const CUtensorMap& tmk,
+                                         const CUtensorMap& tmv, const DecodeArgs& args,
+                                         cudaStream_t stream);
+
+// The partial kernel alone, under a window (decode_window.cu).
+cudaError_t launch_decode_partial_window(int dtype, int head_dim, int group, const CUtensorMap& tmk,
                                          const CUtensorMap& tmv, const DecodeArgs& args,
                                          cudaStream_t stream);
 
@@ -364,6 +381,87 @@ struct CompactArgs {
   int32_t block_shift;          // block_size = 1 << block_shift, or -1 (the launcher sets it)
 };
 cudaError_t launch_kv_compact(const CompactArgs& args, cudaStream_t stream);
+
+// Block tables and slot maps from request lengths (blocks.cu); see
+// pkv_kv_blocks_update.
+struct BlocksArgs {
+  int32_t* block_tables;        // [B, max_blocks]
+  const int32_t* seq_lens;      // [B] rows held
+  const int32_t* base_lens;     // [B], or null: 0
+  const int32_t* add;           // [B]
+  int32_t* free_ids;            // [num_blocks], a stack
+  const int32_t* count_in;      // [1] ids on it
+  int32_t* count_out;           // [1], may be count_in
+  int32_t* out_lens;            // [B]
+  int32_t* row_ptr;             // [B + 1]
+  int64_t* slots;               // [num_rows]
+  int32_t* positions;           // [num_rows], or null
+  unsigned int* err;
+  int64_t num_blocks;
+  int64_t num_rows;
+  int32_t max_blocks;
+  int32_t num_seqs;
+  int32_t block_size;
+  int32_t num_sinks;
+  int32_t window;               // 0: none
+};
+cudaError_t launch_blocks_update(const BlocksArgs& args, cudaStream_t stream);
+
+// Norm, rotation and append (rope_append.cu); see pkv_qk_norm_rope_append.
+constexpr int kMaxAxes = 3;
+struct RopeArgs {
+  const void* q;                // [num_tokens, Hq, D], tokens q_stride elements apart
+  const void* k;                // [num_tokens, Hkv, D]
+  const void* v;
+  void* out;                    // [num_tokens, Hq, D]
+  void* k_cache;
+  void* v_cache;
+  const int64_t* slots;         // [num_tokens]
+  const int32_t* positions;     // [axes], pos_stride apart
+  const float* cos_sin;         // [max_positions, rot]
+  const float* q_weight;        // [D], or null
+  const float* k_weight;
+  unsigned int* err;
+  int64_t q_stride, k_stride, v_stride;
+  int64_t pos_stride;
+  int64_t num_tokens;
+  int64_t num_slots;
+  int64_t plane_bytes;          // MXFP8 pools: the element plane's size
+  int32_t max_positions;
+  int32_t num_q_heads;
+  int32_t num_kv_heads;
+  int32_t block_size;
+  int32_t rot;                  // elements of a head that are rotated
+  int32_t axes;
+  float eps;
+  uint32_t uniform;             // bit i: the pairs of a lane's i-th stretch are on one axis
+  uint8_t axis_of[64];          // the axis of each pair
+};
+cudaError_t launch_rope_append(int dtype, int head_dim, bool interleaved, const RopeArgs& args,
+                               cudaStream_t stream);
+// Pairs of one lane's stretch (RopeArgs::uniform).
+constexpr int rope_stretch(bool interleaved) { return interleaved ? 4 : 8; }
+
+// Verification of drafted tokens (verify.cu); see pkv_draft_verify.
+struct VerifyArgs {
+  const float* target;          // [num_rows, vocab], rows target_stride apart
+  const float* draft;           // or null
+  const int32_t* tokens;        // [num_rows]
+  const int32_t* draft_ptr;     // [B + 1]
+  const uint64_t* masks;        // [num_rows], or null: a chain
+  const float* uniforms;        // [num_rows]
+  int32_t* keep;                // [B, max_draft]
+  int32_t* keep_lens;           // [B]
+  int32_t* next_tokens;         // [B]
+  unsigned int* err;
+  int64_t target_stride;
+  int64_t draft_stride;
+  int32_t vocab;
+  int32_t num_seqs;
+  int32_t num_rows;
+  int32_t max_draft;
+};
+cudaError_t launch_draft_verify(const VerifyArgs& args, cudaStream_t stream);
 
 // Stage count of the partial kernel's shared-memory ring.
 int decode_num_stages(int head_dim, int elem_bytes);

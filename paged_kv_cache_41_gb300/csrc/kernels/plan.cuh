@@ -17,6 +17,8 @@
 
 #include <limits.h>
 
+#include <type_traits>
+
 #include "common.cuh"
 #include "launch.h"
 
@@ -35,6 +37,64 @@ __device__ __forceinline__ int plan_len(const DecodeArgs& a, int r, int block_si
   return effective_len(__ldg(a.seq_lens + r), a.max_blocks, block_size, a.err, report);
 }
 __device__ __forceinline__ int plan_heads(const DecodeArgs& a) { return a.num_kv_heads; }
+
+// Under a window a sequence of T rows shows rows t < S (the sinks) and t >= lo =
+// T - W.  Its stages are those that hold a row that is seen: the first ceil(S /
+// R), then, `skip` stages later, those from row lo's on.  They are counted, dealt
+// out and walked like the stages of T - skip R rows; only where a stage's rows
+// lie, and which of them are seen, asks for the window again.
+__device__ __forceinline__ int window_skip(const DecodeArgs& a, int T, int R) {
+  const int lo = T - a.window;
+  if (lo <= a.num_sinks) return 0;  // every row is seen
+  return max(lo / R - (a.num_sinks + R - 1) / R, 0);
+}
+__device__ __forceinline__ int plan_len(const WindowArgs& a, int r, int block_size, bool report) {
+  const int T = effective_len(__ldg(a.seq_lens + r), a.max_blocks, block_size, a.err, report);
+  return T - window_skip(a, T, a.stage_rows) * a.stage_rows;
+}
+
+// The rows of a stage: the first one's place in the sequence, how many there
+// are, and the hidden ones among them, [hide_lo, hide_hi) (none: 0, 0).
+struct StageRows {
+  int row0, nvalid, hide_lo, hide_hi;
+};
+// Stage i of a sequence r of `len` rows as plan_len counts them.
+template <int R>
+__device__ __forceinline__ StageRows stage_rows(const DecodeArgs& a, int r, int len, int i) {
+  return {i * R, min(R, len - i * R), 0, 0};
+}
+template <int R>
+__device__ __forceinline__ StageRows stage_rows(const WindowArgs& a, int r, int len, int i) {
+  const int T = effective_len(__ldg(a.seq_lens + r), a.max_blocks, a.block_size, a.err, false);
+  const int lo = T - a.window, S = a.num_sinks;
+  StageRows s = {i * R, 0, 0, 0};
+  if (lo > S && i >= (S + R - 1) / R) s.row0 += window_skip(a, T, R) * R;
+  s.nvalid = min(R, T - s.row0);
+  if (lo > S) {
+    const int hs = min(max(S - s.row0, 0), R), he = min(max(lo - s.row0, 0), R);
+    if (hs < he) {
+      if (he >= s.nvalid) {
+        s.nvalid = hs;  // nothing is seen behind the sinks
+      } else {
+        s.hide_lo = hs;
+        s.hide_hi = he;
+      }
+    }
+  }
+  return s;
+}
+// Whether row `row` of a stage is seen; the boxes of TB rows that hold no seen
+// row of a stage, [*lo, *hi).
+__device__ __forceinline__ bool row_seen(int row, int nvalid, int hide_lo, int hide_hi) {
+  return row < nvalid && (row < hide_lo || row >= hide_hi);
+}
+__device__ __forceinline__ void hidden_boxes(const StageRows& s, int TB, int* lo, int* hi) {
+  *lo = (s.hide_lo + TB - 1) / TB;
+  *hi = max(*lo, s.hide_hi / TB);
+}
+
+template <bool kWin>
+using DecodeArgsOf = std::conditional_t<kWin, WindowArgs, DecodeArgs>;
 
 // Every CTA scans the lengths (all kThreads threads must call this): units
 // per sequence, their total S (times Hkv), this CTA's range, and the

@@ -1,0 +1,381 @@
+// verify.cu -- drafted tokens against the target's probabilities.
+//
+// What it computes (pkv_draft_verify): a walk down a request's tree of drafted
+// tokens.  At node i with target row p and draft row q the children are tried
+// in ascending order, with weights
+//   r(v) = max(p(v) - c q(v), 0),   R = sum_v r(v),   c = 0 before the first
+// child and R = 1 there: child x with number u is accepted where u q(x) R <
+// r(x), else c grows by R and the next child is tried.  (Turning x down leaves
+// the distribution max(p' - q, 0) / sum of it, p' = r / R; r's closed form
+// follows because q >= 0: max(max(p - a q, 0) - b q, 0) = max(p - (a + b) q, 0).)
+// Tokens that the draft chose outright (no q) are tried at their mass among
+// what is left, u R < p(x), and their mass is taken out of p.  Where the walk
+// ends the next token is the first v whose running sum of r passes u R.
+//
+// Design (GB300): the bytes are one row of p (and of q) a request, the rest is
+// a chain of dependent steps.  A cluster of CTAs takes a request: each walks
+// the tree by itself (64 nodes in shared memory), and where a sum over the
+// vocabulary is wanted each warp of the cluster sums one segment, the sums are
+// read through distributed shared memory, and the warp whose segment holds the
+// wanted place reads that segment once more.
+//   * Sums are whole numbers: a probability is held as a multiple of 2^-60
+//     (exact from 2^-37 up, cut below), so they are exact, do not depend on
+//     how the row was cut, and a segment's second reading meets the place that
+//     its sum promised.  Sums in fp32 would move the borders between tokens by
+//     more than the smallest of them.
+//   * The tests of single tokens are in 64 bits, u q < p exactly.
+#include <cooperative_groups.h>
+
+#include "common.cuh"
+#include "launch.h"
+
+namespace cg = cooperative_groups;
+
+namespace pkv {
+
+namespace {
+
+constexpr int kVfThreads = 512;
+constexpr int kVfWarps = kVfThreads / 32;
+constexpr int kVfMaxCluster = 8;
+constexpr int kVfNodes = 64;  // PKV_MAX_DRAFT
+typedef unsigned long long u64;
+
+// x held to [0, 1]; NaN counts as 0.
+__device__ __forceinline__ float as_prob(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
+
+// x of [0, 1] as a multiple of 2^-60.
+__device__ __forceinline__ u64 fixed60(float x) {
+  const uint32_t b = __float_as_uint(x);
+  const int e = (int)(b >> 23);  // x = m 2^(e - 150), m the 24 bits below
+  if (e == 0) return 0;
+  const u64 m = (u64)((b & 0x7fffffu) | 0x800000u);
+  const int s = e - 90;
+  return s >= 0 ? m << s : (s > -24 ? m >> -s : 0);
+}
+
+// u of [0, 1) as a multiple of 2^-64.
+__device__ __forceinline__ u64 fixed64(float u) {
+  const uint32_t b = __float_as_uint(u);
+  const int e = (int)(b >> 23);
+  if (e == 0) return 0;
+  const u64 m = (u64)((b & 0x7fffffu) | 0x800000u);
+  const int s = e - 86;
+  return s >= 0 ? m << s : (s > -24 ? m >> -s : 0);
+}
+
+// max(P - c Q, 0) of fixed numbers, c a multiple of 2^-56.
+template <bool kOne>
+__device__ __forceinline__ u64 rest(u64 p, u64 q, u64 c) {
+  u64 cq = q;
+  if constexpr (!kOne) {
+    const u64 top = __umul64hi(q, c);
+    cq = top >> 56 ? ~0ull : (top << 8) | ((q * c) >> 56);
+  }
+  return p > cq ? p - cq : 0;
+}
+
+// One row's weights of a request: p, and q where there is one.
+struct VfRow {
+  const float* p;
+  const float* q;  // null: none is taken off
+  u64 c;           // 2^56: once
+};
+
+// Elements v .. v + 3 of the row as weights (0 past the end).
+template <bool kVec, bool kQ, bool kOne>
+__device__ __forceinline__ void weights4(const VfRow& row, int v, int end, u64 (&w)[4]) {
+  float p[4], q[4];
+  if (kVec && v + 4 <= end) {
+    const float4 x = __ldg(reinterpret_cast<const float4*>(row.p + v));
+    p[0] = x.x, p[1] = x.y, p[2] = x.z, p[3] = x.w;
+    if constexpr (kQ) {
+      const float4 y = __ldg(reinterpret_cast<const float4*>(row.q + v));
+      q[0] = y.x, q[1] = y.y, q[2] = y.z, q[3] = y.w;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      p[i] = v + i < end ? __ldg(row.p + v + i) : 0.f;
+      if constexpr (kQ) q[i] = v + i < end ? __ldg(row.q + v + i) : 0.f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = fixed60(as_prob(p[i]));
+    if constexpr (kQ) w[i] = rest<kOne>(w[i], fixed60(as_prob(q[i])), row.c);
+  }
+}
+
+template <bool kVec, bool kQ, bool kOne>
+__device__ __forceinline__ u64 segment_sum(const VfRow& row, int lo, int hi, int lane) {
+  u64 sum = 0;
+#pragma unroll 4
+  for (int v = lo + lane * 4; v < hi; v += 128) {
+    u64 w[4];
+    weights4<kVec, kQ, kOne>(row, v, hi, w);
+    sum += (w[0] + w[1]) + (w[2] + w[3]);
+  }
+  return sum;
+}
+
+// First element of [lo, hi) whose running sum passes `want`, the tokens of
+// `out` (n of them) counting nothing; hi - 1 if none does.  A warp.
+template <bool kVec, bool kQ, bool kOne>
+__device__ __forceinline__ int segment_find(const VfRow& row, int lo, int hi, int lane, u64 want,
+                                            const int* out, int n) {
+  u64 before = 0;
+  for (int v0 = lo; v0 < hi; v0 += 128) {
+    const int v = v0 + lane * 4;
+    u64 w[4];
+    weights4<kVec, kQ, kOne>(row, v, hi, w);
+    for (int k = 0; k < n; ++k) {
+      const int d = out[k] - v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (d == i) w[i] = 0;
+    }
+    const u64 mine = (w[0] + w[1]) + (w[2] + w[3]);
+    u64 upto = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned hit = __ballot_sync(0xffffffffu, before + upto > want);
+    if (hit) {
+      const int l = __ffs(hit) - 1;
+      u64 run = before + upto - mine;
+      int at = v;
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        run += w[i];
+        if (run <= want) at = v + i + 1;
+      }
+      return __shfl_sync(0xffffffffu, at, l);
+    }
+    before += __shfl_sync(0xffffffffu, upto, 31);
+  }
+  return hi - 1;
+}
+
+}  // namespace
+
+template <bool kVec>
+__global__ void __launch_bounds__(kVfThreads) draft_verify_kernel(const VerifyArgs a) {
+  cg::cluster_group cluster = cg::this_cluster();
+  __shared__ int s_tok[kVfNodes], s_out[kVfNodes];
+  __shared__ float s_u[kVfNodes], s_p[kVfNodes], s_q[kVfNodes];
+  __shared__ u64 s_kids[kVfNodes];
+  __shared__ u64 s_ok;                    // children that pass their first trial
+  __shared__ u64 seg[2][kVfWarps];        // this CTA's segments, by sum
+  __shared__ u64 all[kVfWarps * kVfMaxCluster];
+  const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
+  const int r = blockIdx.x / C;
+  const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
+  const int S = C * kVfWarps;             // segments of the row
+  const int V = a.vocab;
+
+  // ---- the request's nodes
+  const int p0 = a.draft_ptr[r], p1 = a.draft_ptr[r + 1];
+  const bool bad = p0 < 0 || p1 < p0 || p1 - p0 > a.max_draft || p1 > a.num_rows;
+  const int n = bad ? 0 : p1 - p0;
+  if (bad && rank == 0 && t == 0) atomicOr(a.err, PKV_DEVERR_LENGTH);
+  if (n == 0) {  // the whole cluster leaves
+    if (rank == 0) {
+      for (int i = t; i < a.max_draft; i += kVfThreads) a.keep[(int64_t)r * a.max_draft + i] = -1;
+      if (t == 0) {
+        a.keep_lens[r] = 0;
+        a.next_tokens[r] = -1;
+      }
+    }
+    return;
+  }
+  if (t < kVfNodes) s_kids[t] = 0;
+  if (t == 0) s_ok = 0;
+  __syncthreads();
+  if (t < n) {
+    const int64_t row = (int64_t)p0 + t;
+    const u64 mask = a.masks ? a.masks[row] : 0;
+    // the parent: the last ancestor in the node's mask, or the node before
+    const u64 older = a.masks ? mask & ((1ull << t) - 1) : t > 0 ? 1ull << (t - 1) : 0;
+    const int up = older ? 63 - __clzll((long long)older) : -1;
+    const int tok = a.tokens[row];
+    float u = a.uniforms[row];
+    u = u >= 0.f ? fminf(u, 0x1.fffffep-1f) : 0.f;
+    const bool known = tok >= 0 && tok < V;
+    if (t > 0 && !known && rank == 0) atomicOr(a.err, PKV_DEVERR_TOKEN);
+    float p = 0.f, q = 1.f;
+    if (known && up >= 0) {
+      p = as_prob(__ldg(a.target + (p0 + up) * a.target_stride + tok));
+      if (a.draft) q = as_prob(__ldg(a.draft + (p0 + up) * a.draft_stride + tok));
+    }
+    s_tok[t] = tok;
+    s_u[t] = u;
+    s_p[t] = p;
+    s_q[t] = q;
+    if (known && up >= 0) {  // any other is never reached
+      atomicOr(&s_kids[up], 1ull << t);
+      if ((double)u * (double)q < (double)p) atomicOr(&s_ok, 1ull << t);
+    }
+  }
+  __syncthreads();
+
+  // ---- sums over the vocabulary, the whole cluster: every thread gets R
+  const int per = (((V + S - 1) / S) + 127) & ~127;
+  const int my_seg = rank * kVfWarps + warp;
+  const int lo = (int)min((int64_t)my_seg * per, (int64_t)V), hi = min(lo + per, V);
+  const u64 one = 1ull << 56;
+  int sums = 0;
+  auto total_of = [&](const VfRow& row) -> u64 {
+    u64 sum = !row.q          ? segment_sum<kVec, false, true>(row, lo, hi, lane)
+              : row.c == one ? segment_sum<kVec, true, true>(row, lo, hi, lane)
+                             : segment_sum<kVec, true, false>(row, lo, hi, lane);
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    // two buffers in turn: one is written again only after every CTA has
+    // passed the next sum's barrier, so has read this one's
+    u64* mine = seg[sums & 1];
+    if (lane == 0) mine[warp] = sum;
+    ++sums;
+    cluster.sync();
+    if (t < S) all[t] = cluster.map_shared_rank(mine, t / kVfWarps)[t % kVfWarps];
+    __syncthreads();
+    u64 total = 0;
+    for (int s = lane; s < S; s += 32) total += all[s];
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+    return total;
+  };
+  auto row_at = [&](int node, u64 c) {
+    VfRow row;
+    row.p = a.target + (p0 + node) * a.target_stride;
+    row.q = a.draft && c ? a.draft + (p0 + node) * a.draft_stride : nullptr;
+    row.c = c;
+    return row;
+  };
+
+  // ---- the walk, the same in every thread of the cluster
+  u64 kept = 1;       // accepted nodes
+  int at = 0, n_out = 0;
+  double c = 0.0, mass = 1.0;
+  u64 kids = s_kids[0];
+  auto fixed_c = [&](double x) { return (u64)(x * 0x1p56); };
+  while (kids) {
+    const int x = __ffsll((long long)kids) - 1;
+    kids &= kids - 1;
+    bool yes;
+    double part = 0.0;
+    if (n_out == 0) {
+      yes = s_ok >> x & 1;
+      part = s_p[x];
+    } else if (a.draft) {
+      part = fmax((double)s_p[x] - c * (double)s_q[x], 0.0);
+      yes = (double)s_u[x] * (double)s_q[x] * mass < part;
+    } else {
+      bool twice = false;
+      for (int k = 0; k < n_out; ++k) twice |= s_out[k] == s_tok[x];
+      part = twice ? 0.0 : (double)s_p[x];
+      yes = (double)s_u[x] * mass < part;
+    }
+    if (yes) {
+      kept |= 1ull << x;
+      at = x;
+      n_out = 0;
+      c = 0.0;
+      mass = 1.0;
+      kids = s_kids[x];
+      continue;
+    }
+    __syncthreads();  // s_out is read above
+    if (t == 0) s_out[n_out] = s_tok[x];
+    __syncthreads();
+    ++n_out;
+    if (a.draft) {
+      c += mass;
+      if (kids) mass = (double)total_of(row_at(at, fixed_c(c))) * 0x1p-60;
+    } else {
+      mass -= part;
+    }
+  }
+
+  // ---- the next token
+  VfRow row = row_at(at, a.draft ? fixed_c(c) : 0);
+  int taken_out = a.draft ? 0 : n_out;  // tokens whose mass counts nothing
+  u64 total = total_of(row);
+  auto without = [&](int s) -> u64 {  // a segment's sum but for those tokens
+    u64 sum = all[s];
+    for (int k = 0; k < taken_out; ++k) {
+      const int tok = s_out[k];
+      bool twice = false;
+      for (int m = 0; m < k; ++m) twice |= s_out[m] == tok;
+      if (!twice && tok / per == s) sum -= fixed60(as_prob(__ldg(row.p + tok)));
+    }
+    return sum;
+  };
+  if (taken_out) {
+    const u64 mine = t < S ? without(t) : 0;
+    __syncthreads();
+    if (t < S) all[t] = mine;
+    __syncthreads();
+    total = 0;
+    for (int s = lane; s < S; s += 32) total += all[s];
+#pragma unroll
+    for (int o = 16; o >= 1; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+  }
+  if (total == 0 && n_out > 0) {  // nothing is left: the target's own distribution
+    row = row_at(at, 0);
+    taken_out = 0;
+    total = total_of(row);
+  }
+  const u64 want = __umul64hi(fixed64(s_u[0]), total);  // below total
+  // the segment that holds it: this warp's own, if so
+  u64 before = 0;
+  for (int s = lane; s < my_seg; s += 32) before += all[s];
+#pragma unroll
+  for (int o = 16; o >= 1; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
+  if (total > 0 && before <= want && want < before + all[my_seg]) {
+    int v;
+    if (!row.q)
+      v = segment_find<kVec, false, true>(row, lo, hi, lane, want - before, s_out, taken_out);
+    else if (row.c == one)
+      v = segment_find<kVec, true, true>(row, lo, hi, lane, want - before, s_out, 0);
+    else
+      v = segment_find<kVec, true, false>(row, lo, hi, lane, want - before, s_out, 0);
+    if (lane == 0) a.next_tokens[r] = v;
+  }
+  if (rank == 0) {
+    if (t == 0 && total == 0) a.next_tokens[r] = -1;
+    for (int i = t; i < a.max_draft; i += kVfThreads)
+      if (i >= __popcll(kept)) a.keep[(int64_t)r * a.max_draft + i] = -1;
+    if (t < kVfNodes && (kept >> t & 1))
+      a.keep[(int64_t)r * a.max_draft + __popcll(kept & ((1ull << t) - 1))] = t;
+    if (t == 0) a.keep_lens[r] = __popcll(kept);
+  }
+  cluster.sync();  // every CTA's sums have been read
+}
+
+cudaError_t launch_draft_verify(const VerifyArgs& a, cudaStream_t stream) {
+  // CTAs of a request: enough to fill the GPU about three times over with few
+  // requests, but no segment below a warp's four loads
+  int C = 1;
+  while (C < kVfMaxCluster && (int64_t)a.num_seqs * C * 2 <= 512 && (int64_t)C * kVfThreads * 8 < a.vocab)
+    C *= 2;
+  const bool vec = a.target_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(a.target) & 15u) == 0 &&
+                   (!a.draft || (a.draft_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(a.draft) & 15u) == 0));
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(a.num_seqs * C));
+  cfg.blockDim = dim3(kVfThreads);
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)C;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  return vec ? cudaLaunchKernelEx(&cfg, draft_verify_kernel<true>, a)
+             : cudaLaunchKernelEx(&cfg, draft_verify_kernel<false>, a);
+}
+
+}  // namespace pkv

@@ -523,13 +523,26 @@ size_t pkv_decode_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
 
 namespace {
 
+// Blocks of a sequence that a windowed decode's work list can hold at most
+// (window 0: all).  Its stages are those of the sinks and, the window beginning
+// anywhere in one, those of window + 1 stage's rows.
+int32_t seen_blocks(const pkv_cache_desc* c, int32_t num_q_heads, int32_t max_blocks, int32_t window,
+                    int32_t num_sinks) {
+  if (window <= 0) return max_blocks;
+  const int64_t R = decode_stage_rows(c, num_q_heads / c->num_kv_heads);
+  const int64_t rows = ((int64_t)num_sinks + R - 1) / R * R + ((int64_t)window + 2 * R - 1) / R * R;
+  const int64_t blocks = (rows + c->block_size - 1) / c->block_size;
+  return blocks < max_blocks ? (int32_t)blocks : max_blocks;
+}
+
 // The paged decode; with `scores` it also leaves every row's base-2 scores
-// (DecodeArgs::scores).
+// (DecodeArgs::scores); with a window it sees the rows under it alone.
 pkv_status decode_checked(const pkv_cache_desc* cache, void* out, float* lse, const void* q,
                           const void* k_cache, const void* v_cache, const int32_t* block_tables,
                           int32_t max_blocks_per_seq, const int32_t* seq_lens, int32_t num_seqs,
                           int32_t num_q_heads, float scale, int32_t partition_size, void* workspace,
-                          size_t workspace_bytes, void* stream, float* scores, int64_t scores_rows) {
+                          size_t workspace_bytes, void* stream, float* scores, int64_t scores_rows,
+                          int32_t window = 0, int32_t num_sinks = 0) {
   pkv_status st = check_cache(cache);
   if (st != PKV_OK) return st;
   if (num_seqs < 0 || max_blocks_per_seq <= 0 || partition_size < 0 || !isfinite(scale))
@@ -542,7 +555,9 @@ pkv_status decode_checked(const pkv_cache_desc* cache, void* out, float* lse, co
     return PKV_ERR_INVALID_ARG;
   if (partition_size % cache->block_size != 0) return PKV_ERR_INVALID_ARG;
   const int G = num_q_heads / cache->num_kv_heads;
-  const int64_t C = decode_ctas(cache, num_seqs, num_q_heads, max_blocks_per_seq, partition_size);
+  const int64_t C =
+      decode_ctas(cache, num_seqs, num_q_heads,
+                  seen_blocks(cache, num_q_heads, max_blocks_per_seq, window, num_sinks), partition_size);
   if (C > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   const DecodeWorkspace w = decode_workspace(num_seqs, C, G, cache->head_dim);
   if (workspace_bytes < w.total || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
@@ -573,6 +588,8 @@ pkv_status decode_checked(const pkv_cache_desc* cache, void* out, float* lse, co
   a.plan_before_wait = 1;
   a.scores = scores;
   a.scores_rows = scores_rows;
+  a.window = window;
+  a.num_sinks = num_sinks;
   return launch_decode(cache, G, q, k_cache, v_cache, a, as_stream(stream));
 }
 
@@ -589,6 +606,29 @@ pkv_status pkv_paged_attention_decode(const pkv_cache_desc* cache, void* out, fl
   return decode_checked(cache, out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
                         seq_lens, num_seqs, num_q_heads, scale, partition_size, workspace,
                         workspace_bytes, stream, nullptr, 0);
+}
+
+size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
+                                         int32_t num_q_heads, int32_t max_blocks_per_seq,
+                                         int32_t window, int32_t num_sinks) {
+  if (check_cache(cache) != PKV_OK || num_seqs <= 0 || num_q_heads <= 0 ||
+      max_blocks_per_seq <= 0 || window <= 0 || num_sinks < 0 ||
+      check_attention_shape(cache, num_q_heads) != PKV_OK)
+    return 0;
+  return pkv_decode_workspace_bytes(
+      cache, num_seqs, num_q_heads,
+      seen_blocks(cache, num_q_heads, max_blocks_per_seq, window, num_sinks), 0);
+}
+
+pkv_status pkv_paged_attention_decode_window(
+    const pkv_cache_desc* cache, void* out, float* lse, const void* q, const void* k_cache,
+    const void* v_cache, const int32_t* block_tables, int32_t max_blocks_per_seq,
+    const int32_t* seq_lens, int32_t num_seqs, int32_t num_q_heads, float scale, int32_t window,
+    int32_t num_sinks, void* workspace, size_t workspace_bytes, void* stream) {
+  if (window <= 0 || num_sinks < 0) return PKV_ERR_INVALID_ARG;
+  return decode_checked(cache, out, lse, q, k_cache, v_cache, block_tables, max_blocks_per_seq,
+                        seq_lens, num_seqs, num_q_heads, scale, 0, workspace, workspace_bytes, stream,
+                        nullptr, 0, window, num_sinks);
 }
 
 // Shared-prefix workspace: prefix states plus the suffix's whole-segment
@@ -1156,6 +1196,165 @@ pkv_status pkv_kv_compact(const pkv_cache_desc* cache, void* k_cache, void* v_ca
   return pkv_kv_compact_view(cache, k_cache, v_cache, weights, weights_stride, weights_stride,
                              block_tables, max_blocks_per_seq, seq_lens, base_lens, keep,
                              keep_heads, keep_stride, keep_lens, num_seqs, stream);
+}
+
+pkv_status pkv_kv_blocks_update(const pkv_cache_desc* cache, int32_t* block_tables,
+                                int32_t max_blocks_per_seq, const int32_t* seq_lens,
+                                const int32_t* base_lens, const int32_t* add, int32_t num_seqs,
+                                int32_t num_sinks, int32_t window, int32_t* free_ids,
+                                const int32_t* free_count, int32_t* free_count_out,
+                                int32_t* out_lens, int32_t* row_ptr, int64_t* slots,
+                                int32_t* positions, int64_t num_rows, void* stream) {
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (num_seqs < 0 || max_blocks_per_seq <= 0 || num_sinks < 0 || window < 0 || num_rows < 0)
+    return PKV_ERR_INVALID_ARG;
+  if (!free_ids || !free_count || !free_count_out || !row_ptr || (num_rows > 0 && !slots) ||
+      (num_seqs > 0 && (!block_tables || !seq_lens || !add || !out_lens)))
+    return PKV_ERR_INVALID_ARG;
+  if (num_seqs > 65535 || cache->num_blocks > INT32_MAX || num_rows > INT32_MAX)
+    return PKV_ERR_UNSUPPORTED;
+  // the slots are written from the lengths before and after
+  auto overlaps = [&](const int32_t* x) {
+    return x && num_seqs > 0 && x < out_lens + num_seqs && out_lens < x + num_seqs;
+  };
+  if (overlaps(seq_lens) || overlaps(base_lens) || overlaps(add)) return PKV_ERR_INVALID_ARG;
+  unsigned int* err = device_error_word();
+  if (!err) return PKV_ERR_CUDA;
+  pkv::BlocksArgs a{};
+  a.block_tables = block_tables;
+  a.seq_lens = seq_lens;
+  a.base_lens = base_lens;
+  a.add = add;
+  a.free_ids = free_ids;
+  a.count_in = free_count;
+  a.count_out = free_count_out;
+  a.out_lens = out_lens;
+  a.row_ptr = row_ptr;
+  a.slots = slots;
+  a.positions = positions;
+  a.err = err;
+  a.num_blocks = cache->num_blocks;
+  a.num_rows = num_rows;
+  a.max_blocks = max_blocks_per_seq;
+  a.num_seqs = num_seqs;
+  a.block_size = cache->block_size;
+  a.num_sinks = num_sinks;
+  a.window = window;
+  cudaError_t e = pkv::launch_blocks_update(a, as_stream(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_qk_norm_rope_append(
+    const pkv_cache_desc* cache, void* out, void* k_cache, void* v_cache, const void* q,
+    int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,
+    const int64_t* slots, const int32_t* positions, int64_t pos_stride, int32_t num_axes,
+    const uint8_t* axis_of, const float* cos_sin, int32_t max_positions, int32_t rot,
+    int32_t interleaved, const float* q_weight, const float* k_weight, float eps,
+    int64_t num_tokens, int32_t num_q_heads, void* stream) {
+  pkv_status st = check_cache(cache);
+  if (st != PKV_OK) return st;
+  if (num_tokens < 0 || num_q_heads <= 0 || num_axes < 1 || rot < 0 || rot > cache->head_dim ||
+      !isfinite(eps) || eps < 0.f)
+    return PKV_ERR_INVALID_ARG;
+  if ((cache->head_dim != 64 && cache->head_dim != 128) || num_axes > pkv::kMaxAxes || rot % 16 != 0)
+    return PKV_ERR_UNSUPPORTED;
+  if (num_tokens == 0) return PKV_OK;
+  if (!out || !k_cache || !v_cache || !q || !k || !v || !slots || !positions ||
+      (rot > 0 && (!cos_sin || max_positions <= 0)))
+    return PKV_ERR_INVALID_ARG;
+  const int D = cache->head_dim, Hkv = cache->num_kv_heads;
+  const int per16 = cache->dtype == PKV_F32 ? 4 : 8;  // elements of 16 bytes
+  if (q_stride < (int64_t)num_q_heads * D || k_stride < (int64_t)Hkv * D ||
+      v_stride < (int64_t)Hkv * D || q_stride % per16 || k_stride % per16 || v_stride % per16 ||
+      (num_axes > 1 && pos_stride < num_tokens))
+    return PKV_ERR_INVALID_ARG;
+  if (!aligned16(out) || !aligned16(k_cache) || !aligned16(v_cache) || !aligned16(q) ||
+      !aligned16(k) || !aligned16(v) || !aligned16(cos_sin) || !aligned16(q_weight) ||
+      !aligned16(k_weight))
+    return PKV_ERR_INVALID_ARG;
+  const int64_t heads = num_q_heads + 2 * (int64_t)Hkv;
+  if (num_tokens > ((int64_t)1 << 40) / heads || num_tokens * heads / 16 > INT32_MAX - 1)
+    return PKV_ERR_UNSUPPORTED;
+  pkv::RopeArgs a{};
+  if (axis_of)
+    for (int j = 0; j < rot / 2; ++j) {
+      if (axis_of[j] >= num_axes) return PKV_ERR_INVALID_ARG;
+      a.axis_of[j] = axis_of[j];
+    }
+  const int run = pkv::rope_stretch(interleaved != 0);
+  for (int i = 0; i * run < rot / 2; ++i) {
+    bool same = true;
+    for (int j = 1; j < run; ++j) same = same && a.axis_of[i * run + j] == a.axis_of[i * run];
+    if (same) a.uniform |= 1u << i;
+  }
+  unsigned int* err = device_error_word();
+  if (!err) return PKV_ERR_CUDA;
+  a.q = q;
+  a.k = k;
+  a.v = v;
+  a.out = out;
+  a.k_cache = k_cache;
+  a.v_cache = v_cache;
+  a.slots = slots;
+  a.positions = positions;
+  a.cos_sin = cos_sin;
+  a.q_weight = q_weight;
+  a.k_weight = k_weight;
+  a.err = err;
+  a.q_stride = q_stride;
+  a.k_stride = k_stride;
+  a.v_stride = v_stride;
+  a.pos_stride = pos_stride;
+  a.num_tokens = num_tokens;
+  a.num_slots = cache->num_blocks * cache->block_size;
+  a.plane_bytes = mx_plane_bytes(cache);
+  a.max_positions = rot > 0 ? max_positions : INT32_MAX;
+  a.num_q_heads = num_q_heads;
+  a.num_kv_heads = Hkv;
+  a.block_size = cache->block_size;
+  a.rot = rot;
+  a.axes = num_axes;
+  a.eps = eps;
+  cudaError_t e = pkv::launch_rope_append(cache->dtype, D, interleaved != 0, a, as_stream(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+}
+
+pkv_status pkv_draft_verify(const float* target_probs, int64_t target_stride,
+                            const float* draft_probs, int64_t draft_stride, int32_t vocab,
+                            const int32_t* draft_tokens, const int32_t* draft_ptr,
+                            const uint64_t* masks, const float* uniforms, int32_t num_seqs,
+                            int32_t num_rows, int32_t max_draft, int32_t* keep,
+                            int32_t* keep_lens, int32_t* next_tokens, void* stream) {
+  if (num_seqs < 0 || num_rows < 0 || vocab <= 0 || max_draft < 1 || max_draft > PKV_MAX_DRAFT ||
+      target_stride < vocab || (draft_probs && draft_stride < vocab))
+    return PKV_ERR_INVALID_ARG;
+  if (num_seqs == 0) return PKV_OK;
+  if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
+  if (!draft_ptr || !keep || !keep_lens || !next_tokens ||
+      (num_rows > 0 && (!target_probs || !draft_tokens || !uniforms)))
+    return PKV_ERR_INVALID_ARG;
+  unsigned int* err = device_error_word();
+  if (!err) return PKV_ERR_CUDA;
+  pkv::VerifyArgs a{};
+  a.target = target_probs;
+  a.draft = draft_probs;
+  a.tokens = draft_tokens;
+  a.draft_ptr = draft_ptr;
+  a.masks = masks;
+  a.uniforms = uniforms;
+  a.keep = keep;
+  a.keep_lens = keep_lens;
+  a.next_tokens = next_tokens;
+  a.err = err;
+  a.target_stride = target_stride;
+  a.draft_stride = draft_stride;
+  a.vocab = vocab;
+  a.num_seqs = num_seqs;
+  a.num_rows = num_rows;
+  a.max_draft = max_draft;
+  cudaError_t e = pkv::launch_draft_verify(a, as_stream(stream));
+  return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
 }
 
 pkv_status pkv_get_device_error(int32_t* code_out, void* stream) {

@@ -21,6 +21,7 @@ PKV_OK, PKV_ERR_INVALID_ARG, PKV_ERR_UNSUPPORTED, PKV_ERR_CUDA, PKV_ERR_DEVICE, 
 STATIC_SCRATCH_BYTES = 16 << 20
 PKV_F32, PKV_BF16, PKV_MXFP8 = 0, 1, 2
 DEVERR_SLOT, DEVERR_BLOCK, DEVERR_LENGTH, DEVERR_TIMEOUT, DEVERR_KEEP = 1, 2, 4, 8, 16
+DEVERR_POSITION, DEVERR_TOKEN, DEVERR_POOL = 32, 64, 128
 # PKV_MAX_DRAFT of include/pkv.h: drafted tokens of one sequence at most
 MAX_DRAFT = 64
 
@@ -47,6 +48,11 @@ EXPORTED = [
     "pkv_kv_evict_select_view",
     "pkv_kv_compact",
     "pkv_kv_compact_view",
+    "pkv_kv_blocks_update",
+    "pkv_decode_window_workspace_bytes",
+    "pkv_paged_attention_decode_window",
+    "pkv_qk_norm_rope_append",
+    "pkv_draft_verify",
     "pkv_get_device_error",
     "pkv_status_string",
 ]
@@ -131,6 +137,19 @@ def load_library():
     lib.pkv_kv_compact.argtypes = [dp, vp, vp, vp, i64, vp, i32, vp, vp, vp, i32, i64, vp, i32, vp]
     lib.pkv_kv_compact_view.restype = ctypes.c_int
     lib.pkv_kv_compact_view.argtypes = [dp, vp, vp, vp, i64, i64, vp, i32, vp, vp, vp, i32, i64, vp, i32, vp]
+    lib.pkv_kv_blocks_update.restype = ctypes.c_int
+    lib.pkv_kv_blocks_update.argtypes = [dp, vp, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp, vp, vp, vp,
+                                         i64, vp]
+    lib.pkv_decode_window_workspace_bytes.restype = ctypes.c_size_t
+    lib.pkv_decode_window_workspace_bytes.argtypes = [dp, i32, i32, i32, i32, i32]
+    lib.pkv_paged_attention_decode_window.restype = ctypes.c_int
+    lib.pkv_paged_attention_decode_window.argtypes = [dp, vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, f32, i32,
+                                                      i32, vp, ctypes.c_size_t, vp]
+    lib.pkv_qk_norm_rope_append.restype = ctypes.c_int
+    lib.pkv_qk_norm_rope_append.argtypes = [dp, vp, vp, vp, vp, i64, vp, i64, vp, i64, vp, vp, i64, i32,
+                                            ctypes.c_char_p, vp, i32, i32, i32, vp, vp, f32, i64, i32, vp]
+    lib.pkv_draft_verify.restype = ctypes.c_int
+    lib.pkv_draft_verify.argtypes = [vp, i64, vp, i64, i32, vp, vp, vp, vp, i32, i32, i32, vp, vp, vp, vp]
     lib.pkv_get_device_error.restype = ctypes.c_int
     lib.pkv_get_device_error.argtypes = [ctypes.POINTER(i32), vp]
     lib.pkv_status_string.restype = ctypes.c_char_p
@@ -623,6 +642,219 @@ def kv_compact(k_cache, v_cache, block_tables, seq_lens, keep, keep_lens, *, bas
         max_blocks, seq_lens.data_ptr(), base_lens.data_ptr() if base_lens is not None else None,
         keep.data_ptr(), keep_heads, places, keep_lens.data_ptr(), b, where),
         "pkv_kv_compact")
+
+
+def kv_blocks_update(k_cache, block_tables, seq_lens, add, free_ids, free_count, *, base_lens=None,
+                     num_sinks=0, window=0, num_rows=None, out_lens=None, row_ptr=None, slots=None,
+                     positions=None, free_count_out=None, stream=None):
+    """Bring every request from seq_lens to base_lens + add rows (base_lens None:
+    0): blocks given back to and taken from the stack of free ids, and the new
+    rows' slots and positions (include/pkv.h).
+
+    k_cache: a pool, for its shape; block_tables: int32 [B, max_blocks], updated in
+    place; seq_lens, base_lens, add: int32 [B]; free_ids: int32 [num_blocks] with
+    free_count (int32 [1]) ids on it, both updated in place (or the count to
+    free_count_out).  num_rows: new rows of the step at most (the sum of growths,
+    or more in a padded batch); not needed where slots is given.  window,
+    num_sinks: give back what lies behind a sliding window.  Returns (out_lens int32
+    [B], row_ptr int32 [B + 1], slots int64 [num_rows], positions int32
+    [num_rows]); out_lens must not be one of the inputs."""
+    desc = cache_desc(k_cache)
+    b, max_blocks = block_tables.shape
+    _dense("block_tables", block_tables, torch.int32, (b, max_blocks))
+    _dense("seq_lens", seq_lens, torch.int32, (b,))
+    _dense("add", add, torch.int32, (b,))
+    _dense("free_ids", free_ids, torch.int32, (desc.num_blocks,))
+    _dense("free_count", free_count, torch.int32, (1,))
+    if base_lens is not None:
+        _dense("base_lens", base_lens, torch.int32, (b,))
+    if free_count_out is None:
+        free_count_out = free_count
+    else:
+        _dense("free_count_out", free_count_out, torch.int32, (1,))
+    if out_lens is None:
+        out_lens = _empty(stream, (b,), torch.int32, seq_lens.device)
+    else:
+        _dense("out_lens", out_lens, torch.int32, (b,))
+    if row_ptr is None:
+        row_ptr = _empty(stream, (b + 1,), torch.int32, seq_lens.device)
+    else:
+        _dense("row_ptr", row_ptr, torch.int32, (b + 1,))
+    if slots is None:
+        if num_rows is None:
+            raise ValueError("num_rows is needed where no slots are given")
+        slots = _empty(stream, (num_rows,), torch.int64, seq_lens.device)
+    else:
+        if num_rows is None:
+            num_rows = slots.shape[0]
+        _dense("slots", slots, torch.int64, (num_rows,))
+    if positions is None:
+        positions = _empty(stream, (num_rows,), torch.int32, seq_lens.device)
+    else:
+        _dense("positions", positions, torch.int32, (num_rows,))
+    where = _launch_place(stream, block_tables, seq_lens, add, base_lens, free_ids, free_count,
+                          free_count_out, out_lens, row_ptr, slots, positions)
+    _check(load_library().pkv_kv_blocks_update(
+        ctypes.byref(desc), block_tables.data_ptr(), max_blocks, seq_lens.data_ptr(),
+        base_lens.data_ptr() if base_lens is not None else None, add.data_ptr(), b, num_sinks, window,
+        free_ids.data_ptr(), free_count.data_ptr(), free_count_out.data_ptr(), out_lens.data_ptr(),
+        row_ptr.data_ptr(), slots.data_ptr(), positions.data_ptr(), num_rows, where),
+        "pkv_kv_blocks_update")
+    return out_lens, row_ptr, slots, positions
+
+
+def decode_window_workspace_bytes(k_cache, num_seqs, num_q_heads, max_blocks_per_seq, window,
+                                  num_sinks=0) -> int:
+    desc = cache_desc(k_cache)
+    return load_library().pkv_decode_window_workspace_bytes(
+        ctypes.byref(desc), num_seqs, num_q_heads, max_blocks_per_seq, window, num_sinks)
+
+
+def paged_attention_decode_window(q, k_cache, v_cache, block_tables, seq_lens, scale, *, window,
+                                  num_sinks=0, out=None, lse=None, workspace=None, stream=None):
+    """The paged decode under a sliding window with sinks (include/pkv.h): of a
+    sequence's T rows the first num_sinks and the last window are seen; blocks
+    without one may have been given back.  Returns out (and writes lse [B, Hq] float32 when
+    given)."""
+    desc = _pair_desc(k_cache, v_cache)
+    b, hq, d = q.shape
+    _, max_blocks = block_tables.shape
+    _dense("q", q, _io_dtype(desc), (b, hq, desc.head_dim))
+    _dense("block_tables", block_tables, torch.int32, (b, max_blocks))
+    _dense("seq_lens", seq_lens, torch.int32, (b,))
+    if out is None:
+        out = _empty(stream, q.shape, q.dtype, q.device)
+    else:
+        _dense("out", out, q.dtype, (b, hq, d))
+    if lse is not None:
+        _dense("lse", lse, torch.float32, (b, hq))
+    where = _launch_place(stream, q, k_cache, v_cache, block_tables, seq_lens, out, lse, workspace)
+    lib = load_library()
+    if workspace is None and b:
+        need = lib.pkv_decode_window_workspace_bytes(ctypes.byref(desc), b, hq, max_blocks, window,
+                                                     num_sinks)
+        workspace = _empty(stream, need, torch.uint8, q.device) if need else None
+    ws_bytes = workspace.numel() * workspace.element_size() if workspace is not None else 0
+    _check(lib.pkv_paged_attention_decode_window(
+        ctypes.byref(desc), out.data_ptr(), lse.data_ptr() if lse is not None else None, q.data_ptr(),
+        k_cache.data_ptr(), v_cache.data_ptr(), block_tables.data_ptr(), max_blocks, seq_lens.data_ptr(),
+        b, hq, scale, window, num_sinks, workspace.data_ptr() if workspace is not None else None, ws_bytes,
+        where), "pkv_paged_attention_decode_window")
+    return out
+
+
+def _head_rows(name, t, dtype, n, heads, d):
+    """Check [n, heads, d] head rows that are contiguous within a token and return
+    the elements from token to token."""
+    if t.dtype != dtype or t.shape != (n, heads, d):
+        raise ValueError(f"{name} must be a {dtype} tensor of shape {(n, heads, d)}, "
+                         f"got {t.dtype} {tuple(t.shape)}")
+    token, row, one = t.stride()
+    if (one != 1 and d > 1) or (row != d and heads > 1):
+        raise ValueError(f"{name}'s head rows must be contiguous and lie one behind the other")
+    return token if n > 1 else max(token, heads * d)
+
+
+def qk_norm_rope_append(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, *, q_weight=None,
+                        k_weight=None, eps=1e-6, axis_of=None, interleaved=False, out=None,
+                        stream=None):
+    """Normalise (where a weight is given) and rotate the queries and keys of a
+    step, and append the keys and the values as they are (include/pkv.h).
+
+    q: [N, Hq, D], k and v: [N, Hkv, D], perhaps parts of one packed projection;
+    slot_mapping: int64 [N]; positions: int32 [N], or [axes, N] with axis_of[j] the
+    axis of pair j (a sequence of rot / 2 integers); cos_sin: float32 [positions,
+    rot], the cosines then the sines of the rot / 2 pairs, or None: no rotation.
+    Returns the rotated queries [N, Hq, D]; rows of negative positions are left
+    as they are."""
+    desc = _pair_desc(k_cache, v_cache)
+    n, hq, d = q.shape
+    hkv, io = desc.num_kv_heads, _io_dtype(desc)
+    q_stride = _head_rows("q", q, io, n, hq, desc.head_dim)
+    k_stride = _head_rows("k", k, io, n, hkv, desc.head_dim)
+    v_stride = _head_rows("v", v, io, n, hkv, desc.head_dim)
+    _dense("slot_mapping", slot_mapping, torch.int64, (n,))
+    axes = 1 if positions.dim() == 1 else positions.shape[0]
+    if positions.dtype != torch.int32 or positions.dim() > 2 or positions.shape[-1] != n or (
+            n > 1 and positions.stride(-1) != 1):
+        raise ValueError(f"positions must be an int32 tensor of shape ({n},) or (axes, {n})")
+    rot = 0
+    if cos_sin is not None:
+        rot = cos_sin.shape[-1]
+        _dense("cos_sin", cos_sin, torch.float32, (cos_sin.shape[0], rot))
+    if axis_of is not None:
+        axis_of = bytes(axis_of)
+        if len(axis_of) != rot // 2:
+            raise ValueError(f"axis_of must name an axis for each of the {rot // 2} pairs")
+    for name, w in (("q_weight", q_weight), ("k_weight", k_weight)):
+        if w is not None:
+            _dense(name, w, torch.float32, (d,))
+    if out is None:
+        out = _empty(stream, (n, hq, d), q.dtype, q.device)
+    else:
+        _dense("out", out, q.dtype, (n, hq, d))
+    where = _launch_place(stream, q, k, v, k_cache, v_cache, slot_mapping, positions, cos_sin, q_weight,
+                          k_weight, out)
+    _check(load_library().pkv_qk_norm_rope_append(
+        ctypes.byref(desc), out.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), q.data_ptr(),
+        q_stride, k.data_ptr(), k_stride, v.data_ptr(), v_stride, slot_mapping.data_ptr(),
+        positions.data_ptr(), positions.stride(0) if axes > 1 else n, axes, axis_of,
+        cos_sin.data_ptr() if rot else None, cos_sin.shape[0] if rot else 0, rot, 1 if interleaved else 0,
+        q_weight.data_ptr() if q_weight is not None else None,
+        k_weight.data_ptr() if k_weight is not None else None, eps, n, hq, where),
+        "pkv_qk_norm_rope_append")
+    return out
+
+
+def _prob_rows(name, t, rows, vocab):
+    """Check probabilities [rows, vocab] float32 and return the elements from row
+    to row."""
+    if t.dtype != torch.float32 or t.shape != (rows, vocab) or (vocab > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} must be a float32 tensor of shape {(rows, vocab)} with contiguous rows")
+    return max(t.stride(0), vocab) if rows <= 1 else t.stride(0)
+
+
+def draft_verify(target_probs, draft_tokens, draft_ptr, uniforms, *, max_draft, draft_probs=None,
+                 masks=None, keep=None, keep_lens=None, next_tokens=None, stream=None):
+    """Verify drafted tokens against the target's probabilities from given random
+    numbers (include/pkv.h).
+
+    target_probs: float32 [rows, vocab], row i the target's distribution after
+    drafted row i (a view of wider rows, perhaps); draft_probs: the draft's, from
+    which the children of each row were sampled, or None where it chose them
+    outright; draft_tokens: int32 [rows]; draft_ptr: int32 [B + 1]; masks: int64 [rows], as
+    draft_tree_attention's, or None for chains; uniforms: float32 [rows] in
+    [0, 1).  Returns (keep int32 [B, 1, max_draft], the accepted rows, -1 padded, for
+    kv_compact; keep_lens int32 [B]; next_tokens int32 [B])."""
+    rows, vocab = target_probs.shape
+    b = draft_ptr.shape[0] - 1
+    target_stride = _prob_rows("target_probs", target_probs, rows, vocab)
+    draft_stride = 0 if draft_probs is None else _prob_rows("draft_probs", draft_probs, rows, vocab)
+    _dense("draft_tokens", draft_tokens, torch.int32, (rows,))
+    _dense("draft_ptr", draft_ptr, torch.int32, (b + 1,))
+    _dense("uniforms", uniforms, torch.float32, (rows,))
+    if masks is not None:
+        _dense("masks", masks, torch.int64, (rows,))
+    if keep is None:
+        keep = _empty(stream, (b, 1, max_draft), torch.int32, draft_ptr.device)
+    else:
+        _dense("keep", keep, torch.int32, (b, 1, max_draft))
+    if keep_lens is None:
+        keep_lens = _empty(stream, (b,), torch.int32, draft_ptr.device)
+    else:
+        _dense("keep_lens", keep_lens, torch.int32, (b,))
+    if next_tokens is None:
+        next_tokens = _empty(stream, (b,), torch.int32, draft_ptr.device)
+    else:
+        _dense("next_tokens", next_tokens, torch.int32, (b,))
+    where = _launch_place(stream, target_probs, draft_probs, draft_tokens, draft_ptr, masks, uniforms,
+                          keep, keep_lens, next_tokens)
+    _check(load_library().pkv_draft_verify(
+        target_probs.data_ptr(), target_stride, draft_probs.data_ptr() if draft_probs is not None else None,
+        draft_stride, vocab, draft_tokens.data_ptr(), draft_ptr.data_ptr(),
+        masks.data_ptr() if masks is not None else None, uniforms.data_ptr(), b, rows, max_draft,
+        keep.data_ptr(), keep_lens.data_ptr(), next_tokens.data_ptr(), where), "pkv_draft_verify")
+    return keep, keep_lens, next_tokens
 
 
 def get_device_error(stream=None) -> int:

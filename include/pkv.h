@@ -724,7 +724,7 @@ pkv_status pkv_qk_norm_rope_append(
  *   target_probs, draft_probs: float [num_rows, vocab], target_stride and
  *                  draft_stride elements from row to row; row i follows drafted
  *                  row i.  Each in [0, 1] and summing to about 1 (held there: NaN
- *                  and below as 0, above as 1); multiples of 2^-60 below that are cut.
+ *                  and below as 0, above as 1), rounded to multiples of 2^-60.
  *                  draft_probs may be NULL.
  *   draft_tokens:  int32 [num_rows]; one outside the vocabulary is never accepted
  *                  and sets PKV_DEVERR_TOKEN (the root's is not read as a token).

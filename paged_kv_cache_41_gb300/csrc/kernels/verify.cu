@@ -19,7 +19,7 @@
 // read through distributed shared memory, and the warp whose segment holds the
 // wanted place reads that segment once more.
 //   * Sums are whole numbers: a probability is held as a multiple of 2^-60
-//     (exact from 2^-37 up, cut below), so they are exact, do not depend on
+//     (exact from 2^-37 up, rounded below), so they are exact, do not depend on
 //     how the row was cut, and a segment's second reading meets the place that
 //     its sum promised.  Sums in fp32 would move the borders between tokens by
 //     more than the smallest of them.
@@ -35,24 +35,37 @@ namespace pkv {
 
 namespace {
 
-constexpr int kVfThreads = 512;
+constexpr int kVfThreads = 256;
 constexpr int kVfWarps = kVfThreads / 32;
 constexpr int kVfMaxCluster = 8;
 constexpr int kVfNodes = 64;  // PKV_MAX_DRAFT
 typedef unsigned long long u64;
 
 // x held to [0, 1]; NaN counts as 0.
-__device__ __forceinline__ float as_prob(float x) { return fminf(fmaxf(x, 0.f), 1.f); }
+__device__ __forceinline__ float as_prob(float x) { return __saturatef(x); }
 
-// x of [0, 1] as a multiple of 2^-60.
-__device__ __forceinline__ u64 fixed60(float x) {
-  const uint32_t b = __float_as_uint(x);
-  const int e = (int)(b >> 23);  // x = m 2^(e - 150), m the 24 bits below
-  if (e == 0) return 0;
-  const u64 m = (u64)((b & 0x7fffffu) | 0x800000u);
-  const int s = e - 90;
-  return s >= 0 ? m << s : (s > -24 ? m >> -s : 0);
+// A number of [0, 1] as a 2^-20 + b 2^-40 + c 2^-60, rounded to the nearest
+// multiple of 2^-60.  Adding 8 leaves x as a multiple of 2^-20 in the low bits
+// of the sum; what that left out is exact in fp32 and goes on in the same way.
+// Seven additions and three integer ones a number, all at full rate: shifting
+// the mantissa to its place instead made the whole kernel twice as slow.
+struct Limbs {
+  int a, b, c;
+};
+constexpr float kLimb1 = 8.0f, kLimb2 = 12.0f * 0x1p-20f, kLimb3 = 12.0f * 0x1p-40f;
+__device__ __forceinline__ Limbs limbs(float x) {
+  const float t1 = __fadd_rn(x, kLimb1);
+  const float r1 = __fsub_rn(x, __fsub_rn(t1, kLimb1));
+  const float t2 = __fadd_rn(r1, kLimb2);
+  const float r2 = __fsub_rn(r1, __fsub_rn(t2, kLimb2));
+  const float t3 = __fadd_rn(r2, kLimb3);
+  return {__float_as_int(t1) - __float_as_int(kLimb1), __float_as_int(t2) - __float_as_int(kLimb2),
+          __float_as_int(t3) - __float_as_int(kLimb3)};
 }
+__device__ __forceinline__ u64 whole(const Limbs& x) {
+  return (u64)(x.a * (1ll << 40) + x.b * (1ll << 20) + x.c);
+}
+__device__ __forceinline__ u64 fixed60(float x) { return whole(limbs(x)); }
 
 // u of [0, 1) as a multiple of 2^-64.
 __device__ __forceinline__ u64 fixed64(float u) {
@@ -82,10 +95,9 @@ struct VfRow {
   u64 c;           // 2^56: once
 };
 
-// Elements v .. v + 3 of the row as weights (0 past the end).
-template <bool kVec, bool kQ, bool kOne>
-__device__ __forceinline__ void weights4(const VfRow& row, int v, int end, u64 (&w)[4]) {
-  float p[4], q[4];
+// Elements v .. v + 3 of the row, held to [0, 1] (0 past the end).
+template <bool kVec, bool kQ>
+__device__ __forceinline__ void load4(const VfRow& row, int v, int end, float (&p)[4], float (&q)[4]) {
   if (kVec && v + 4 <= end) {
     const float4 x = __ldg(reinterpret_cast<const float4*>(row.p + v));
     p[0] = x.x, p[1] = x.y, p[2] = x.z, p[3] = x.w;
@@ -102,19 +114,62 @@ __device__ __forceinline__ void weights4(const VfRow& row, int v, int end, u64 (
   }
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    w[i] = fixed60(as_prob(p[i]));
-    if constexpr (kQ) w[i] = rest<kOne>(w[i], fixed60(as_prob(q[i])), row.c);
+    p[i] = as_prob(p[i]);
+    if constexpr (kQ) q[i] = as_prob(q[i]);
   }
 }
 
+// ... and as weights.
+template <bool kVec, bool kQ, bool kOne>
+__device__ __forceinline__ void weights4(const VfRow& row, int v, int end, u64 (&w)[4]) {
+  float p[4], q[4];
+  load4<kVec, kQ>(row, v, end, p, q);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    w[i] = fixed60(p[i]);
+    if constexpr (kQ) w[i] = rest<kOne>(w[i], fixed60(q[i]), row.c);
+  }
+}
+
+// The sum of the weights of [lo, hi), this lane's share.
 template <bool kVec, bool kQ, bool kOne>
 __device__ __forceinline__ u64 segment_sum(const VfRow& row, int lo, int hi, int lane) {
   u64 sum = 0;
+  if constexpr (kQ && !kOne) {
+#pragma unroll 2
+    for (int v = lo + lane * 4; v < hi; v += 128) {
+      u64 w[4];
+      weights4<kVec, true, false>(row, v, hi, w);
+      sum += (w[0] + w[1]) + (w[2] + w[3]);
+    }
+  } else {
+    // limbs apart, in 32 bits: kRun numbers of 2^20 at most
+    constexpr int kRun = 1024;
+    for (int v0 = lo + lane * 4; v0 < hi; v0 += kRun / 4 * 128) {
+      Limbs s = {0, 0, 0};
+      const int stop = min(hi, v0 + kRun / 4 * 128);
 #pragma unroll 4
-  for (int v = lo + lane * 4; v < hi; v += 128) {
-    u64 w[4];
-    weights4<kVec, kQ, kOne>(row, v, hi, w);
-    sum += (w[0] + w[1]) + (w[2] + w[3]);
+      for (int v = v0; v < stop; v += 128) {
+        float p[4], q[4];
+        load4<kVec, kQ>(row, v, hi, p, q);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          if constexpr (kQ) {  // max(p - q, 0), the two apart
+            const bool over = p[i] > q[i];
+            const Limbs x = limbs(over ? p[i] : 0.f), y = limbs(over ? q[i] : 0.f);
+            s.a += x.a - y.a;
+            s.b += x.b - y.b;
+            s.c += x.c - y.c;
+          } else {
+            const Limbs x = limbs(p[i]);
+            s.a += x.a;
+            s.b += x.b;
+            s.c += x.c;
+          }
+        }
+      }
+      sum += whole(s);
+    }
   }
   return sum;
 }
@@ -162,7 +217,7 @@ __device__ __forceinline__ int segment_find(const VfRow& row, int lo, int hi, in
 }  // namespace
 
 template <bool kVec>
-__global__ void __launch_bounds__(kVfThreads) draft_verify_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kVfThreads, 4) draft_verify_kernel(const VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
   __shared__ int s_tok[kVfNodes], s_out[kVfNodes];
   __shared__ float s_u[kVfNodes], s_p[kVfNodes], s_q[kVfNodes];

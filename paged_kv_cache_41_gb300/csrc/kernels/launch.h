@@ -434,13 +434,11 @@ struct RopeArgs {
   int32_t rot;                  // elements of a head that are rotated
   int32_t axes;
   float eps;
-  uint32_t uniform;             // bit i: the pairs of a lane's i-th stretch are on one axis
+  uint32_t uniform;             // bit i: pairs 4 i .. 4 i + 3 are on one axis
   uint8_t axis_of[64];          // the axis of each pair
 };
 cudaError_t launch_rope_append(int dtype, int head_dim, bool interleaved, const RopeArgs& args,
                                cudaStream_t stream);
-// Pairs of one lane's stretch (RopeArgs::uniform).
-constexpr int rope_stretch(bool interleaved) { return interleaved ? 4 : 8; }
 
 // Verification of drafted tokens (verify.cu); see pkv_draft_verify.
 struct VerifyArgs {

@@ -10,11 +10,14 @@
 //
 // Design (GB300): the bytes are those of q, k and v once in and once out, so
 // the whole is one kernel bound by memory.  A head row is held by head_dim / 8
-// lanes, eight elements (a 16-byte load of bf16) each: the mean is three or
-// four shuffles, and a pair's other half is eight shuffles away (or in the same
-// lane, where pairs are interleaved).  Angles come from a table, so that far
-// positions lose nothing: a lane reads its eight cosines and sines once for
-// the kRows head rows of its token that it takes.
+// lanes, two stretches of four elements each, laid out so that both halves of a
+// pair lie in one lane (split pairs: elements 4 l and rot / 2 + 4 l on; those
+// that are not rotated follow, eight a lane): the only shuffles are the three or four of
+// the mean.  A group of lanes takes kRows head rows of one token and one kind
+// (q, k or v), so that weight and angle are multiplied into four coefficients a
+// pair once for all of them.  Angles come from a table, so that far positions lose
+// nothing.  K rows of an MXFP8 pool are brought into order by shuffles before their
+// groups of 32 are quantised; they are few beside the queries.
 #include "common.cuh"
 #include "launch.h"
 
@@ -24,21 +27,32 @@ namespace {
 
 constexpr int kRopeThreads = 256;
 
-template <int N>
-__device__ __forceinline__ void store_row(float* p, const float (&y)[N]) {
-#pragma unroll
-  for (int i = 0; i < N / 4; ++i)
-    reinterpret_cast<float4*>(p)[i] = make_float4(y[4 * i], y[4 * i + 1], y[4 * i + 2], y[4 * i + 3]);
-}
-__device__ __forceinline__ void store_row(__nv_bfloat16* p, const float (&y)[8]) {
-  uint32_t w[4];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const __nv_bfloat162 b = __floats2bfloat162_rn(y[2 * i], y[2 * i + 1]);
-    w[i] = *reinterpret_cast<const uint32_t*>(&b);
+// Four consecutive elements as they lie in memory.
+template <typename T>
+struct Raw4;
+template <>
+struct Raw4<float> {
+  float4 w;
+  __device__ __forceinline__ void load(const float* p) { w = __ldg(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void store(float* p) const { *reinterpret_cast<float4*>(p) = w; }
+  __device__ __forceinline__ void get(float (&x)[4]) const { x[0] = w.x, x[1] = w.y, x[2] = w.z, x[3] = w.w; }
+  __device__ __forceinline__ void set(const float (&x)[4]) { w = make_float4(x[0], x[1], x[2], x[3]); }
+};
+template <>
+struct Raw4<__nv_bfloat16> {
+  uint2 w;
+  __device__ __forceinline__ void load(const __nv_bfloat16* p) {
+    w = __ldg(reinterpret_cast<const uint2*>(p));
   }
-  *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
-}
+  __device__ __forceinline__ void store(__nv_bfloat16* p) const { *reinterpret_cast<uint2*>(p) = w; }
+  __device__ __forceinline__ void get(float (&x)[4]) const {
+    x[0] = bf16lo(w.x), x[1] = bf16hi(w.x), x[2] = bf16lo(w.y), x[3] = bf16hi(w.y);
+  }
+  __device__ __forceinline__ void set(const float (&x)[4]) {
+    const __nv_bfloat162 a = __floats2bfloat162_rn(x[0], x[1]), b = __floats2bfloat162_rn(x[2], x[3]);
+    w = make_uint2(*reinterpret_cast<const uint32_t*>(&a), *reinterpret_cast<const uint32_t*>(&b));
+  }
+};
 
 // Four values as E4M3 codes of the scale 2^e.
 __device__ __forceinline__ uint32_t mx_codes4(float a, float b, float c, float d, int e) {
@@ -50,148 +64,204 @@ __device__ __forceinline__ uint32_t mx_codes4(float a, float b, float c, float d
 
 }  // namespace
 
-// Group of D / 8 lanes g takes head rows g % parts + parts * i (i < kRows) of
-// token g / parts; rows 0 .. Hq - 1 are q's, then k's, then v's.
+// Quantise eight consecutive values a lane (lane l: elements 8 l ..), groups of
+// 32 being four lanes, into row `hk` of slot `slot`.
+template <int D>
+__device__ __forceinline__ void store_mx(const RopeArgs& a, void* cache, const float (&y)[8], int64_t slot,
+                                         int hk, int l, unsigned lanes) {
+  float amax = 0.f;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));
+  amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, 1));
+  amax = fmaxf(amax, __shfl_xor_sync(lanes, amax, 2));
+  if (slot < 0) return;
+  const int ex = mx_scale_exponent(amax), Hkv = a.num_kv_heads;
+  uint8_t* pool = static_cast<uint8_t*>(cache);
+  const int64_t blk = slot / a.block_size, off = slot - blk * a.block_size;
+  *reinterpret_cast<uint2*>(pool + (slot * Hkv + hk) * D + l * 8) =
+      make_uint2(mx_codes4(y[0], y[1], y[2], y[3], ex), mx_codes4(y[4], y[5], y[6], y[7], ex));
+  if (l % 4 == 0)
+    pool[a.plane_bytes + ((blk * Hkv + hk) * a.block_size + off) * (D / 32) + l / 4] = (uint8_t)(ex + 127);
+}
+
+// Group g of D / 8 lanes takes up to kRows head rows of token g / parts: of
+// its parts, the first ceil(Hq / kRows) are q's, then come k's and v's.
 template <typename T, bool kMx, int D, bool kInter, int kRows>
 __global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs a) {
   constexpr int LPR = D / 8;  // lanes of a head row
   pdl_launch_dependents();    // a decode after this append may be scheduled now
-  const int Hq = a.num_q_heads, Hkv = a.num_kv_heads, H = Hq + 2 * Hkv;
-  const int parts = (H + kRows - 1) / kRows;
+  const int Hq = a.num_q_heads, Hkv = a.num_kv_heads;
+  const int qparts = (Hq + kRows - 1) / kRows, kparts = (Hkv + kRows - 1) / kRows;
+  const int parts = qparts + 2 * kparts;
   const int64_t g = ((int64_t)blockIdx.x * kRopeThreads + threadIdx.x) / LPR;
-  const int l = threadIdx.x % LPR;  // elements 8 l .. 8 l + 7
+  const int l = threadIdx.x % LPR;
+  const unsigned lanes = (LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1)) << ((threadIdx.x & 31) / LPR * LPR);
   const int64_t tok = g / parts;
-  const int part = (int)(g - tok * parts);
-  bool on = tok < a.num_tokens;
+  if (tok >= a.num_tokens) return;  // a group leaves together
+  int part = (int)(g - tok * parts);
+  const int kind = part < qparts ? 0 : part < qparts + kparts ? 1 : 2;  // q, k, v
+  part -= kind == 0 ? 0 : kind == 1 ? qparts : qparts + kparts;
+  const int heads = kind == 0 ? Hq : Hkv;
+  const int h0 = part * kRows, nrows = min(kRows, heads - h0);
+  const T* src = kind == 0   ? static_cast<const T*>(a.q) + tok * a.q_stride
+                 : kind == 1 ? static_cast<const T*>(a.k) + tok * a.k_stride
+                             : static_cast<const T*>(a.v) + tok * a.v_stride;
+  src += (int64_t)h0 * D;
+  // this lane's elements: o0 .. o0 + 3 and o1 .. o1 + 3
+  const int half = a.rot / 2;
+  const bool turned = 8 * l < a.rot && kind != 2;
+  const bool split = !kInter && turned;
+  const int o0 = split ? 4 * l : 8 * l, o1 = split ? half + 4 * l : 8 * l + 4;
 
   // ---- the rows, and where they go
-  float x[kRows][8];
+  Raw4<T> x[kRows][2];
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int h = part + i * parts;
-#pragma unroll
-    for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-    if (on && h < H) {
-      const T* src = h < Hq ? static_cast<const T*>(a.q) + tok * a.q_stride + (int64_t)h * D
-                     : h < Hq + Hkv
-                         ? static_cast<const T*>(a.k) + tok * a.k_stride + (int64_t)(h - Hq) * D
-                         : static_cast<const T*>(a.v) + tok * a.v_stride + (int64_t)(h - Hq - Hkv) * D;
-      VecLoad<T, 8>::run(src + l * 8, x[i]);
-    }
+    const int h = min(i, nrows - 1);  // past the last: it again, not stored
+    x[i][0].load(src + h * D + o0);
+    x[i][1].load(src + h * D + o1);
   }
-  int64_t slot = on ? a.slots[tok] : -1;
+  int64_t slot = a.slots[tok];
   // positions: a negative one marks a row of no token
-  int pos[kMaxAxes];
-#pragma unroll
-  for (int ax = 0; ax < kMaxAxes; ++ax) {
-    pos[ax] = on && ax < a.axes ? a.positions[ax * a.pos_stride + tok] : 0;
-  }
+  int pos[kMaxAxes] = {};
   bool skip = false, far = false;
 #pragma unroll
-  for (int ax = 0; ax < kMaxAxes; ++ax) {
-    skip |= pos[ax] < 0;
-    far |= pos[ax] >= a.max_positions;
+  for (int ax = 0; ax < kMaxAxes; ++ax)
+    if (ax < a.axes) {
+      pos[ax] = a.positions[ax * a.pos_stride + tok];
+      skip |= pos[ax] < 0;
+      far |= pos[ax] >= a.max_positions;
+    }
+  if (skip || far) {
+    if (!skip && g == tok * parts && l == 0) atomicOr(a.err, PKV_DEVERR_POSITION);
+    return;
   }
-  if (on && far && !skip && part == 0 && l == 0) atomicOr(a.err, PKV_DEVERR_POSITION);
-  on = on && !skip && !far;
   if (slot >= a.num_slots) {
-    if (on && part == 0 && l == 0) atomicOr(a.err, PKV_DEVERR_SLOT);
+    if (g == tok * parts && l == 0) atomicOr(a.err, PKV_DEVERR_SLOT);
     slot = -1;
   }
-
-  // ---- this lane's cosines and sines
-  constexpr int NP = kInter ? 4 : 8;  // pairs that its elements belong to
-  const int half = a.rot / 2;
-  const bool turned = 8 * l < a.rot;            // rot is a multiple of 16
-  const bool second = !kInter && 8 * l >= half;  // its elements are the pairs' second ones
-  const int j0 = kInter ? 4 * l : second ? 8 * l - half : 8 * l;
-  float cs[NP], sn[NP];
+  void* cache = kind == 1 ? a.k_cache : a.v_cache;
+  if (kind != 0 && slot < 0) return;
+  if (kind == 2) {  // values go as they are
 #pragma unroll
-  for (int j = 0; j < NP; ++j) {
-    cs[j] = 1.f;
-    sn[j] = 0.f;
+    for (int i = 0; i < kRows; ++i) {
+      if (i >= nrows) break;
+      if constexpr (kMx) {
+        float y[8], z[4];
+        x[i][0].get(z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = z[e];
+        x[i][1].get(z);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[4 + e] = z[e];
+        store_mx<D>(a, cache, y, slot, h0 + i, l, lanes);
+      } else {
+        T* dst = static_cast<T*>(cache) + (slot * Hkv + h0 + i) * D;
+        x[i][0].store(dst + o0);
+        x[i][1].store(dst + o1);
+      }
+    }
+    return;
   }
-  if (on && turned) {
-    const int ax0 = a.axis_of[j0];
-    if (a.uniform >> (j0 / NP) & 1) {  // one axis for all of them
-      const int p = ax0 == 0 ? pos[0] : ax0 == 1 ? pos[1] : pos[2];
-      const float* row = a.cos_sin + (int64_t)p * a.rot + j0;
-      VecLoad<float, NP>::run(row, cs);
-      VecLoad<float, NP>::run(row + half, sn);
+
+  // ---- coefficients: with w the weights of a pair (a, b), c and s its angle,
+  //   y_a = x_a (w_a c) - x_b (w_b s),   y_b = x_b (w_b c) + x_a (w_a s)
+  float cs[4] = {1.f, 1.f, 1.f, 1.f}, sn[4] = {0.f, 0.f, 0.f, 0.f};
+  if (turned) {
+    const int j0 = 4 * l;
+    if (a.uniform >> l & 1) {  // one axis for all four
+      const int ax = a.axis_of[j0];
+      const float* row = a.cos_sin + (int64_t)(ax == 0 ? pos[0] : ax == 1 ? pos[1] : pos[2]) * a.rot + j0;
+      VecLoad<float, 4>::run(row, cs);
+      VecLoad<float, 4>::run(row + half, sn);
     } else {
 #pragma unroll
-      for (int j = 0; j < NP; ++j) {
+      for (int j = 0; j < 4; ++j) {
         const int ax = a.axis_of[j0 + j];
-        const int p = ax == 0 ? pos[0] : ax == 1 ? pos[1] : pos[2];
-        const float* row = a.cos_sin + (int64_t)p * a.rot + j0 + j;
+        const float* row = a.cos_sin + (int64_t)(ax == 0 ? pos[0] : ax == 1 ? pos[1] : pos[2]) * a.rot + j0 + j;
         cs[j] = row[0];
         sn[j] = row[half];
       }
     }
   }
+  // element pairs of the lane: (first, second) of pair j
+  auto first = [](int j) { return kInter ? 2 * j : j; };
+  auto second = [](int j) { return kInter ? 2 * j + 1 : 4 + j; };
+  float aa[4], ab[4], bb[4], ba[4];
+  const float* w = kind == 0 ? a.q_weight : a.k_weight;
+  {
+    float wt[8] = {1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f, 1.f};
+    if (w) {
+      const float4 u = __ldg(reinterpret_cast<const float4*>(w + o0)), v = __ldg(reinterpret_cast<const float4*>(w + o1));
+      wt[0] = u.x, wt[1] = u.y, wt[2] = u.z, wt[3] = u.w;
+      wt[4] = v.x, wt[5] = v.y, wt[6] = v.z, wt[7] = v.w;
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      aa[j] = wt[first(j)] * cs[j];
+      ab[j] = -wt[second(j)] * sn[j];
+      bb[j] = wt[second(j)] * cs[j];
+      ba[j] = wt[first(j)] * sn[j];
+    }
+  }
 
 #pragma unroll
   for (int i = 0; i < kRows; ++i) {
-    const int h = part + i * parts;
-    const bool is_q = h < Hq, is_v = h >= Hq + Hkv;
-    // ---- norm
-    const float* w = is_q ? a.q_weight : a.k_weight;
-    const bool normed = !is_v && w != nullptr;
-    float ss = 0.f;
+    if (i >= nrows) break;
+    float v[8];
+    {
+      float z[4];
+      x[i][0].get(z);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(x[i][e], x[i][e], ss);
+      for (int e = 0; e < 4; ++e) v[e] = z[e];
+      x[i][1].get(z);
 #pragma unroll
-    for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (normed) {
-      const float inv = rsqrtf(ss * (1.f / D) + a.eps);
-      float wf[8];
-      VecLoad<float, 8>::run(w + l * 8, wf);
-#pragma unroll
-      for (int e = 0; e < 8; ++e) x[i][e] *= inv * wf[e];
+      for (int e = 0; e < 4; ++e) v[4 + e] = z[e];
     }
-    // ---- rotation
-    float y[8];
-    if constexpr (kInter) {
+    float inv = 1.f;
+    if (w) {
+      float ss = 0.f;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        y[2 * j] = x[i][2 * j] * cs[j] - x[i][2 * j + 1] * sn[j];
-        y[2 * j + 1] = x[i][2 * j + 1] * cs[j] + x[i][2 * j] * sn[j];
-      }
-    } else {
-      const int other = second ? l - half / 8 : l + half / 8;
+      for (int e = 0; e < 8; ++e) ss = fmaf(v[e], v[e], ss);
+#pragma unroll
+      for (int o = LPR / 2; o >= 1; o >>= 1) ss += __shfl_xor_sync(lanes, ss, o);
+      inv = rsqrtf(ss * (1.f / D) + a.eps);
+    }
+    float y[8];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const float p = v[first(j)] * inv, q = v[second(j)] * inv;
+      y[first(j)] = fmaf(p, aa[j], q * ab[j]);
+      y[second(j)] = fmaf(q, bb[j], p * ba[j]);
+    }
+    if (kMx && kind == 1) {
+      // into order: lane l wants elements 8 l .., the stretches 2 l and 2 l + 1
       float z[8];
 #pragma unroll
-      for (int e = 0; e < 8; ++e) z[e] = __shfl_sync(0xffffffffu, x[i][e], other & (LPR - 1), LPR);
+      for (int c = 0; c < 2; ++c) {
+        const int u = 2 * l + c;
+        int from = l, which = c;  // interleaved, or not rotated: in order already
+        if (!kInter && 4 * u < a.rot) {
+          which = 4 * u >= half;
+          from = which ? u - half / 4 : u;
+        }
 #pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = x[i][e] * cs[e] + (second ? z[e] * sn[e] : -z[e] * sn[e]);
-    }
-    if (is_v || !turned) {
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] = x[i][e];
-    }
-    // ---- to where it belongs
-    const int hk = is_v ? h - Hq - Hkv : h - Hq;  // kv head
-    if constexpr (kMx) {
-      // the scale of a group of 32: four lanes
-      float amax = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) amax = fmaxf(amax, fabsf(y[e]));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
-      amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
-      if (!is_q && on && h < H && slot >= 0) {
-        const int ex = mx_scale_exponent(amax);
-        uint8_t* pool = static_cast<uint8_t*>(is_v ? a.v_cache : a.k_cache);
-        const int64_t blk = slot / a.block_size, off = slot - blk * a.block_size;
-        *reinterpret_cast<uint2*>(pool + (slot * Hkv + hk) * D + l * 8) =
-            make_uint2(mx_codes4(y[0], y[1], y[2], y[3], ex), mx_codes4(y[4], y[5], y[6], y[7], ex));
-        if (l % 4 == 0)
-          pool[a.plane_bytes + ((blk * Hkv + hk) * a.block_size + off) * (D / 32) + l / 4] =
-              (uint8_t)(ex + 127);
+        for (int e = 0; e < 4; ++e) {
+          const float s0 = __shfl_sync(lanes, y[e], from, LPR), s1 = __shfl_sync(lanes, y[4 + e], from, LPR);
+          z[4 * c + e] = which ? s1 : s0;
+        }
       }
-    } else if (!is_q && on && h < H && slot >= 0) {
-      store_row(static_cast<T*>(is_v ? a.v_cache : a.k_cache) + (slot * Hkv + hk) * D + l * 8, y);
+      store_mx<D>(a, cache, z, slot, h0 + i, l, lanes);
+    } else {
+      T* dst = kind == 0 ? static_cast<T*>(a.out) + (tok * Hq + h0 + i) * D
+                         : static_cast<T*>(cache) + (slot * Hkv + h0 + i) * D;
+      Raw4<T> o;
+      const float lo[4] = {y[0], y[1], y[2], y[3]}, hi[4] = {y[4], y[5], y[6], y[7]};
+      o.set(lo);
+      o.store(dst + o0);
+      o.set(hi);
+      o.store(dst + o1);
     }
-    if (is_q && on) store_row(static_cast<T*>(a.out) + (tok * Hq + h) * D + l * 8, y);
   }
 }
 
@@ -202,7 +272,8 @@ static cudaError_t launch_rope_t(const RopeArgs& a, cudaStream_t stream) {
   // Few rows: one a group, so that every SM has some.  Many: four, so that a
   // token's angles are read once for four.
   const bool few = a.num_tokens * H <= 20000;
-  const int64_t groups = a.num_tokens * (few ? H : (H + 3) / 4);
+  const int64_t groups =
+      a.num_tokens * (few ? H : (a.num_q_heads + 3) / 4 + 2 * ((a.num_kv_heads + 3) / 4));
   const unsigned grid = (unsigned)((groups + per_cta - 1) / per_cta);
   if (few)
     rope_append_kernel<T, kMx, D, kInter, 1><<<grid, kRopeThreads, 0, stream>>>(a);

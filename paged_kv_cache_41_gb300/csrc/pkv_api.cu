@@ -1274,7 +1274,7 @@ pkv_status pkv_qk_norm_rope_append(
       !aligned16(k_weight))
     return PKV_ERR_INVALID_ARG;
   const int64_t heads = num_q_heads + 2 * (int64_t)Hkv;
-  if (num_tokens > ((int64_t)1 << 40) / heads || num_tokens * heads / 16 > INT32_MAX - 1)
+  if (num_tokens > ((int64_t)1 << 40) / heads || num_tokens * heads / 16 > INT32_MAX - 2)
     return PKV_ERR_UNSUPPORTED;
   pkv::RopeArgs a{};
   if (axis_of)
@@ -1282,11 +1282,9 @@ pkv_status pkv_qk_norm_rope_append(
       if (axis_of[j] >= num_axes) return PKV_ERR_INVALID_ARG;
       a.axis_of[j] = axis_of[j];
     }
-  const int run = pkv::rope_stretch(interleaved != 0);
-  for (int i = 0; i * run < rot / 2; ++i) {
-    bool same = true;
-    for (int j = 1; j < run; ++j) same = same && a.axis_of[i * run + j] == a.axis_of[i * run];
-    if (same) a.uniform |= 1u << i;
+  for (int i = 0; 4 * i < rot / 2; ++i) {
+    const uint8_t* ax = a.axis_of + 4 * i;
+    if (ax[1] == ax[0] && ax[2] == ax[0] && ax[3] == ax[0]) a.uniform |= 1u << i;
   }
   unsigned int* err = device_error_word();
   if (!err) return PKV_ERR_CUDA;

@@ -10,12 +10,14 @@
 // slot table[position / P] * P + position % P.
 //
 // Design (GB300): one CTA.  A batch is a few thousand integers, and everything
-// depends on running sums over the requests, so the time is that of a few
-// block-wide scans one behind the other, not of bytes; a grid would need a
-// launch (or a grid barrier) between them.  Requests are taken 1024 at a time,
-// one a thread.  The ids of a chunk's requests are one flat list (a prefix sum
-// of their counts): a thread finds its entry's request by bisection, so that
-// one request with a thousand blocks costs what a thousand with one do.  The
+// depends on running sums over the requests, so the time is that of a chain of
+// loads, scans and barriers, not of bytes; a grid would need a launch (or a
+// grid barrier) between its links.  Requests are taken one a thread, as many at
+// a time as there are threads: 128, whose barriers and scans are short, where
+// the batch and its rows are small, else 1024.  A batch that fits one pass takes its three running sums (ids given
+// back, ids taken, rows) in one scan.  The ids of a pass are one flat list: a
+// thread finds its entries' request by bisection of the running sums, so that one
+// request with a thousand blocks costs what a thousand with one do.  The
 // slots of many rows (a prompt's) are a second launch over the whole GPU.
 #include "common.cuh"
 #include "launch.h"
@@ -24,32 +26,47 @@ namespace pkv {
 
 namespace {
 
-constexpr int kBlThreads = 1024;
-constexpr int kBlWarps = kBlThreads / 32;
+constexpr int kBlRowThreads = 256;
 // Rows whose slots the one CTA writes itself.
 constexpr int64_t kBlOwnRows = 4096;
 
-// Inclusive sum over the CTA's threads; *total receives the sum of all.  `ws`:
-// kBlWarps long longs of shared memory, free again when the call returns.
-__device__ __forceinline__ long long block_scan(long long x, long long* ws, long long* total) {
+struct Sum3 {
+  long long a, b, c;
+};
+// Inclusive sums over the CTA's threads; *total receives the sums of all.  `ws`:
+// kThreads / 32 entries of shared memory, free again when the call returns.
+template <int kThreads>
+__device__ __forceinline__ Sum3 block_scan(Sum3 x, Sum3* ws, Sum3* total) {
+  constexpr int kWarps = kThreads / 32;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long y = __shfl_up_sync(0xffffffffu, x, o);
-    if (lane >= o) x += y;
+    const long long ya = __shfl_up_sync(0xffffffffu, x.a, o), yb = __shfl_up_sync(0xffffffffu, x.b, o),
+                    yc = __shfl_up_sync(0xffffffffu, x.c, o);
+    if (lane >= o) {
+      x.a += ya;
+      x.b += yb;
+      x.c += yc;
+    }
   }
   if (lane == 31) ws[warp] = x;
   __syncthreads();
-  long long before = 0, all = 0;
-#pragma unroll
-  for (int w = 0; w < kBlWarps; ++w) {
-    const long long t = ws[w];
-    before += w < warp ? t : 0;
-    all += t;
+  Sum3 before = {0, 0, 0}, all = {0, 0, 0};
+#pragma unroll 8
+  for (int w = 0; w < kWarps; ++w) {
+    const Sum3 t = ws[w];
+    if (w < warp) {
+      before.a += t.a;
+      before.b += t.b;
+      before.c += t.c;
+    }
+    all.a += t.a;
+    all.b += t.b;
+    all.c += t.c;
   }
   __syncthreads();
   *total = all;
-  return before + x;
+  return {before.a + x.a, before.b + x.b, before.c + x.c};
 }
 
 // First index i of the ascending a[0 .. n) with a[i] > x (n: none).
@@ -81,41 +98,56 @@ __device__ __forceinline__ Ask read_ask(const BlocksArgs& a, int r, long long ca
   return k;
 }
 
-// Slot and position of row i: those of its request, or -1.
-__device__ __forceinline__ void write_row(const BlocksArgs& a, int64_t i) {
-  const int32_t* ptr = a.row_ptr;
+__device__ __forceinline__ int blocks_of(int len, int P) { return (int)(((long long)len + P - 1) / P); }
+
+// Slot and position of row i, row e of the new ones of request r, which goes
+// from old_len to new_len rows (none: r < 0, or not grown).
+__device__ __forceinline__ void write_row(const BlocksArgs& a, int64_t i, int r, int e, int old_len,
+                                          int new_len) {
   int64_t slot = -1;
   int pos = -1;
-  if (a.num_seqs > 0 && i < ptr[a.num_seqs]) {
-    const int r = first_above(ptr + 1, a.num_seqs, i);
-    const int old_len = a.seq_lens[r];
-    if (a.out_lens[r] != old_len) {  // it has grown
-      pos = old_len + (int)(i - ptr[r]);
-      const int b = pos / a.block_size;
-      const int32_t id = a.block_tables[(int64_t)r * a.max_blocks + b];
-      if (id >= 0 && id < a.num_blocks)
-        slot = (int64_t)id * a.block_size + (pos - b * a.block_size);
-      else
-        pos = -1;
-    }
+  if (r >= 0 && new_len != old_len) {
+    pos = old_len + e;
+    const int b = pos / a.block_size;
+    const int32_t id = a.block_tables[(int64_t)r * a.max_blocks + b];
+    if (id >= 0 && id < a.num_blocks)
+      slot = (int64_t)id * a.block_size + (pos - b * a.block_size);
+    else
+      pos = -1;
   }
   a.slots[i] = slot;
   if (a.positions) a.positions[i] = pos;
 }
+// The same from what the update has left in global memory.
+__device__ __forceinline__ void write_row(const BlocksArgs& a, int64_t i) {
+  const int32_t* ptr = a.row_ptr;
+  if (a.num_seqs == 0 || i >= ptr[a.num_seqs]) {
+    write_row(a, i, -1, 0, 0, 0);
+    return;
+  }
+  const int r = first_above(ptr + 1, a.num_seqs, i);
+  write_row(a, i, r, (int)(i - ptr[r]), a.seq_lens[r], a.out_lens[r]);
+}
 
-__global__ void __launch_bounds__(kBlThreads) blocks_rows_kernel(const BlocksArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * kBlThreads + threadIdx.x;
+__global__ void __launch_bounds__(kBlRowThreads) blocks_rows_kernel(const BlocksArgs a) {
+  pdl_wait();  // the update's tables, lengths and row ranges
+  const int64_t i = (int64_t)blockIdx.x * kBlRowThreads + threadIdx.x;
   if (i < a.num_rows) write_row(a, i);
 }
 
-__global__ void __launch_bounds__(kBlThreads) blocks_update_kernel(const BlocksArgs a, int own_rows) {
-  __shared__ long long ws[kBlWarps];
-  __shared__ long long upto[kBlThreads];  // running count of a chunk's ids, by thread
-  __shared__ int s_first[kBlThreads], s_next[kBlThreads], s_split[kBlThreads];
+template <int kThreads>
+__global__ void __launch_bounds__(kThreads) blocks_update_kernel(const BlocksArgs a, int own_rows) {
+  __shared__ Sum3 ws[kThreads / 32];
+  // running sums by request: of the ids that go, then of those that come; of rows
+  __shared__ long long ids_to[kThreads], rows_to[kThreads];
+  // what goes: s_cut ids from block s_want on, before them those from block
+  // s_wlo on; what comes: from block s_held on, where served
+  __shared__ int s_cut[kThreads], s_want[kThreads], s_wlo[kThreads], s_held[kThreads], s_old[kThreads],
+      s_new[kThreads];
   const int t = threadIdx.x, lane = t & 31;
   const int B = a.num_seqs, P = a.block_size;
   const long long cap = (long long)a.max_blocks * P;
-  auto blocks_of = [&](int len) { return (int)(((long long)len + P - 1) / P); };
+  const bool single = B <= kThreads;
 
   long long avail = a.count_in[0];
   if (avail < 0 || avail > a.num_blocks) {
@@ -123,22 +155,27 @@ __global__ void __launch_bounds__(kBlThreads) blocks_update_kernel(const BlocksA
     avail = avail < 0 ? 0 : a.num_blocks;
   }
 
-  // ---------------------------------------------------------- blocks that go
-  // Chunks from the last request to the first; thread t of a chunk takes its
-  // request 1023 - t, so that ascending threads are descending requests.
-  for (int base = (B - 1) / kBlThreads * kBlThreads; base >= 0 && B > 0; base -= kBlThreads) {
-    const int r = base + kBlThreads - 1 - t;
-    int hi = 0, n_cut = 0, w_hi = 0, w_lo = 0;
+  Ask k;
+  int n_go = 0, n_come = 0, n_rows = 0;  // of this thread's request in the pass
+  // Read request base + t: what goes (with kGo), what comes.
+  auto read = [&](int base, bool report) {
+    const int r = base + t;
+    n_go = n_come = n_rows = 0;
+    int cut = 0, want = 0, held = 0, w_lo = 0, w_hi = 0;
+    k = {0, 0, true};
     if (r < B) {
-      const Ask k = read_ask(a, r, cap);
-      if (k.bad) atomicOr(a.err, PKV_DEVERR_LENGTH);
+      k = read_ask(a, r, cap);
+      if (k.bad && report) atomicOr(a.err, PKV_DEVERR_LENGTH);
       if (!k.bad) {
-        hi = blocks_of(k.old_len);
-        n_cut = max(0, hi - blocks_of(k.new_len));
+        held = blocks_of(k.old_len, P);
+        want = blocks_of(k.new_len, P);
+        cut = max(0, held - want);
+        n_come = max(0, want - held);
+        n_rows = max(0, k.new_len - k.old_len);
         if (a.window > 0) {
           // the first row behind the sinks that a decode from here on sees
           const long long lo = (long long)min(k.old_len, k.new_len) - a.window;
-          w_lo = blocks_of(a.num_sinks);
+          w_lo = blocks_of(a.num_sinks, P);
           w_hi = lo > 0 ? (int)(lo / P) : 0;
           if (w_hi <= w_lo) w_hi = w_lo = 0;
         }
@@ -150,8 +187,7 @@ __global__ void __launch_bounds__(kBlThreads) blocks_update_kernel(const BlocksA
     if (a.window > 0) {
       const int32_t* row = a.block_tables + (int64_t)(r < B ? r : 0) * a.max_blocks;
       unsigned todo = __ballot_sync(0xffffffffu, w_hi > w_lo && row[w_hi > 0 ? w_hi - 1 : 0] >= 0);
-      const int found = __popc(todo & (1u << lane));  // whether this thread's request has some
-      if (!found) w_lo = w_hi;
+      if (!(todo >> lane & 1)) w_lo = w_hi;
       while (todo) {
         const int l = __ffs(todo) - 1;
         todo &= todo - 1;
@@ -161,9 +197,9 @@ __global__ void __launch_bounds__(kBlThreads) blocks_update_kernel(const BlocksA
         int at = top;  // blocks at .. top - 1 are still held
         while (at > bottom) {
           const int j = at - 1 - lane;
-          const unsigned gone = __ballot_sync(0xffffffffu, j < bottom || rrow[j] < 0);
-          if (gone) {
-            at -= __ffs(gone) - 1;
+          const unsigned away = __ballot_sync(0xffffffffu, j < bottom || rrow[j] < 0);
+          if (away) {
+            at -= __ffs(away) - 1;
             break;
           }
           at -= 32;
@@ -171,107 +207,171 @@ __global__ void __launch_bounds__(kBlThreads) blocks_update_kernel(const BlocksA
         if (lane == l) w_lo = at;
       }
     }
-    long long total;
-    const int mine = n_cut + (w_hi - w_lo);
-    const long long sum = block_scan(mine, ws, &total);
-    upto[t] = sum;
-    s_first[t] = hi - 1;   // its topmost block, then downwards
-    s_split[t] = n_cut;    // after so many, on from behind the window
-    s_next[t] = w_hi - 1;
-    __syncthreads();
-    for (long long f0 = 0; f0 < total; f0 += kBlThreads) {
-      const long long f = f0 + t;
-      int32_t id = -1;
-      if (f < total) {
-        const int o = first_above(upto, kBlThreads, f);
-        const int e = (int)(f - (o ? upto[o - 1] : 0));
-        const int blk = e < s_split[o] ? s_first[o] - e : s_next[o] - (e - s_split[o]);
-        int32_t* at = a.block_tables + (int64_t)(base + kBlThreads - 1 - o) * a.max_blocks + blk;
-        id = *at;
+    n_go = cut + (w_hi - w_lo);
+    s_cut[t] = cut;
+    s_want[t] = want;
+    s_wlo[t] = w_lo;
+    s_held[t] = held;
+  };
+  // The ids of a pass that go, `total` of them: entry f of the list (ascending
+  // request and block) goes onto the stack behind those after it.
+  auto go = [&](int base, long long total) {
+    for (long long f0 = total; f0 > 0; f0 -= 4 * kThreads) {
+      // entries f0 - 1 - 4 t and the three before it
+      int32_t id[4];
+      bool all = true;
+      int o = -1;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const long long f = f0 - 1 - 4 * t - e;
+        id[e] = -1;
+        if (f < 0) continue;
+        if (o < 0) o = first_above(ids_to, kThreads, f);
+        while (o > 0 && ids_to[o - 1] > f) --o;
+        const int x = (int)(f - (o ? ids_to[o - 1] : 0));
+        const int w = (int)(ids_to[o] - (o ? ids_to[o - 1] : 0)) - s_cut[o];  // of them behind the window
+        int32_t* at = a.block_tables + (int64_t)(base + o) * a.max_blocks +
+                      (x < w ? s_wlo[o] + x : s_want[o] + (x - w));
+        id[e] = *at;
         *at = -1;
-        if (id >= a.num_blocks) {
+        if (id[e] >= a.num_blocks) {
+          atomicOr(a.err, PKV_DEVERR_BLOCK);
+          id[e] = -1;
+        }
+        all = all && id[e] >= 0;
+      }
+      const long long here = min(f0, (long long)4 * kThreads);
+      if (__syncthreads_and(all)) {
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const long long place = avail + 4 * t + e;
+          if (id[e] < 0) continue;
+          if (place < a.num_blocks)
+            a.free_ids[place] = id[e];
+          else
+            atomicOr(a.err, PKV_DEVERR_BLOCK);  // more ids than the pool has blocks
+        }
+        avail += here;
+      } else {
+        int mine = 0;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) mine += id[e] >= 0;
+        Sum3 pushed;
+        long long place = avail + block_scan<kThreads>({mine, 0, 0}, ws, &pushed).a - mine;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          if (id[e] < 0) continue;
+          if (place < a.num_blocks)
+            a.free_ids[place] = id[e];
+          else
+            atomicOr(a.err, PKV_DEVERR_BLOCK);
+          ++place;
+        }
+        avail += pushed.a;
+      }
+      avail = min(avail, (long long)a.num_blocks);
+    }
+  };
+
+  long long rows = 0, taken = 0, used = 0;  // of the passes before: rows, ids asked for, ids given
+  if (t == 0) a.row_ptr[0] = 0;
+  // Ids and rows that come in a pass, from their running sums in it.
+  auto grow = [&](int base, Sum3 upto, Sum3 total) {
+    const int r = base + t;
+    const bool crowded = rows + total.c > a.num_rows;  // some rows have no room
+    if (crowded) {
+      if (n_rows > 0 && rows + upto.c > a.num_rows) {
+        atomicOr(a.err, PKV_DEVERR_LENGTH);
+        k.new_len = k.old_len;
+        n_come = 0;
+      }
+      Sum3 again;
+      upto.b = block_scan<kThreads>({0, n_come, 0}, ws, &again).b;
+      total.b = again.b;
+    }
+    bool served = true;
+    if (taken + total.b > avail && n_come > 0 && taken + upto.b > avail) {  // not enough free blocks
+      atomicOr(a.err, PKV_DEVERR_POOL);
+      k.new_len = k.old_len;
+      served = false;
+    }
+    if (r < B) {
+      a.out_lens[r] = k.new_len;
+      a.row_ptr[r + 1] = (int32_t)min(rows + upto.c, (long long)a.num_rows);
+    }
+    ids_to[t] = upto.b;
+    rows_to[t] = upto.c;
+    s_old[t] = k.old_len;
+    s_new[t] = k.new_len;
+    // those that are served stand in front of those that are not
+    long long got = taken + total.b;
+    if (got > avail) {
+      Sum3 given;
+      block_scan<kThreads>({served ? n_come : 0, 0, 0}, ws, &given);
+      got = given.a > 0 ? taken + given.a : 0;
+    }
+    used = max(used, got);
+    __syncthreads();
+    const int per = (int)((total.b + kThreads - 1) / kThreads);
+    long long f = (long long)t * per;
+    const long long end = min(f + per, total.b);
+    if (f < end) {
+      int o = first_above(ids_to, kThreads, f);
+      for (; f < end; ++f) {
+        while (ids_to[o] <= f) ++o;
+        if (s_new[o] == s_old[o]) continue;  // not served
+        int32_t id = a.free_ids[avail - 1 - (taken + f)];
+        if (id < 0 || id >= a.num_blocks) {
           atomicOr(a.err, PKV_DEVERR_BLOCK);
           id = -1;
         }
+        const int e = (int)(f - (o ? ids_to[o - 1] : 0));
+        a.block_tables[(int64_t)(base + o) * a.max_blocks + s_held[o] + e] = id;
       }
-      long long pushed;
-      const long long place = avail + block_scan(id >= 0, ws, &pushed) - 1;
-      if (id >= 0) {
-        if (place < a.num_blocks)
-          a.free_ids[place] = id;
-        else
-          atomicOr(a.err, PKV_DEVERR_BLOCK);  // more ids than the pool has blocks
-      }
-      avail = min(avail + pushed, (long long)a.num_blocks);
     }
+    rows += total.c;
+    taken += total.b;
     __syncthreads();
-  }
+  };
 
-  // -------------------------------------------------------- blocks that come
-  long long rows = 0, taken = 0;  // of the chunks before; taken: asked for so far
-  long long used = 0;             // ... and given
-  if (t == 0) a.row_ptr[0] = 0;
-  for (int base = 0; base < B; base += kBlThreads) {
-    const int r = base + t;
-    int held = 0, want = 0, n = 0, old_len = 0, new_len = 0;
-    if (r < B) {
-      const Ask k = read_ask(a, r, cap);
-      old_len = k.old_len;
-      new_len = k.new_len;
-      if (!k.bad && new_len > old_len) {
-        n = new_len - old_len;
-        held = blocks_of(old_len);
-        want = blocks_of(new_len);
-      }
+  if (single) {
+    Sum3 total;
+    read(0, true);
+    const Sum3 upto = block_scan<kThreads>({n_go, n_come, n_rows}, ws, &total);
+    if (total.a > 0) {
+      ids_to[t] = upto.a;
+      __syncthreads();
+      go(0, total.a);
+      __syncthreads();
     }
-    long long total;
-    const long long row_end = rows + block_scan(n, ws, &total);
-    rows += total;
-    if (n > 0 && row_end > a.num_rows) {  // no room for its rows
-      atomicOr(a.err, PKV_DEVERR_LENGTH);
-      new_len = old_len;
-      want = held;
+    grow(0, upto, total);
+  } else {
+    Sum3 total;
+    for (int base = (B - 1) / kThreads * kThreads; base >= 0; base -= kThreads) {
+      read(base, true);
+      ids_to[t] = block_scan<kThreads>({n_go, 0, 0}, ws, &total).a;
+      __syncthreads();
+      go(base, total.a);
+      __syncthreads();
     }
-    if (r < B) a.row_ptr[r + 1] = (int32_t)min(row_end, (long long)a.num_rows);
-    int demand = want - held;
-    const long long sum = taken + block_scan(demand, ws, &total);
-    if (demand > 0 && sum > avail) {  // not enough free blocks
-      atomicOr(a.err, PKV_DEVERR_POOL);
-      new_len = old_len;
+    for (int base = 0; base < B; base += kThreads) {
+      read(base, false);
+      const Sum3 upto = block_scan<kThreads>({0, n_come, n_rows}, ws, &total);
+      grow(base, upto, total);
     }
-    if (r < B) a.out_lens[r] = new_len;
-    const bool served = demand > 0 && sum <= avail;
-    upto[t] = sum - taken;
-    s_first[t] = held;
-    s_split[t] = served ? 1 : 0;
-    __syncthreads();
-    for (long long f = t; f < total; f += kBlThreads) {
-      const int o = first_above(upto, kBlThreads, f);
-      if (!s_split[o]) continue;
-      const int e = (int)(f - (o ? upto[o - 1] : 0));
-      int32_t id = a.free_ids[avail - 1 - (taken + f)];
-      if (id < 0 || id >= a.num_blocks) {
-        atomicOr(a.err, PKV_DEVERR_BLOCK);
-        id = -1;
-      }
-      a.block_tables[(int64_t)(base + o) * a.max_blocks + s_first[o] + e] = id;
-    }
-    // what the last request served has reached
-    long long last = served ? sum : 0;
-#pragma unroll
-    for (int o = 16; o >= 1; o >>= 1) last = max(last, __shfl_xor_sync(0xffffffffu, last, o));
-    __syncthreads();
-    if (lane == 0) ws[t >> 5] = last;
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kBlWarps; ++w) used = max(used, ws[w]);
-    taken += total;
-    __syncthreads();
   }
   if (t == 0) a.count_out[0] = (int32_t)(avail - used);
-  if (own_rows) {
-    __syncthreads();
-    for (int64_t i = t; i < a.num_rows; i += kBlThreads) write_row(a, i);
+  if (!own_rows) return;
+  if (single) {
+    for (int64_t i = t; i < a.num_rows; i += kThreads) {
+      const int o = first_above(rows_to, kThreads, i);
+      if (o < B)
+        write_row(a, i, o, (int)(i - (o ? rows_to[o - 1] : 0)), s_old[o], s_new[o]);
+      else
+        write_row(a, i, -1, 0, 0, 0);
+    }
+  } else {
+    for (int64_t i = t; i < a.num_rows; i += kThreads) write_row(a, i);
   }
 }
 
@@ -279,11 +379,14 @@ __global__ void __launch_bounds__(kBlThreads) blocks_update_kernel(const BlocksA
 
 cudaError_t launch_blocks_update(const BlocksArgs& a, cudaStream_t stream) {
   const int own = a.num_rows <= kBlOwnRows ? 1 : 0;
-  blocks_update_kernel<<<1, kBlThreads, 0, stream>>>(a, own);
+  if (a.num_seqs <= 128 && a.num_rows <= 1024)
+    blocks_update_kernel<128><<<1, 128, 0, stream>>>(a, own);
+  else
+    blocks_update_kernel<1024><<<1, 1024, 0, stream>>>(a, own);
   cudaError_t e = cudaGetLastError();
   if (e != cudaSuccess || own) return e;
-  blocks_rows_kernel<<<(unsigned)((a.num_rows + kBlThreads - 1) / kBlThreads), kBlThreads, 0, stream>>>(a);
-  return cudaGetLastError();
+  const int64_t grid = (a.num_rows + kBlRowThreads - 1) / kBlRowThreads;
+  return launch_pdl(blocks_rows_kernel, dim3((unsigned)grid), dim3(kBlRowThreads), 0, stream, a);
 }
 
 }  // namespace pkv

@@ -15,9 +15,11 @@
 // Design (GB300): the bytes are one row of p (and of q) a request, the rest is
 // a chain of dependent steps.  A cluster of CTAs takes a request: each walks
 // the tree by itself (64 nodes in shared memory), and where a sum over the
-// vocabulary is wanted each warp of the cluster sums one segment, the sums are
-// read through distributed shared memory, and the warp whose segment holds the
-// wanted place reads that segment once more.
+// vocabulary is wanted each warp of the cluster sums one segment and the sums are
+// read through distributed shared memory.  The CTA whose segment holds the
+// wanted place sums that segment again in eighths, one a warp, until what is left
+// is two steps of a warp (one warp walking its segment alone, a step behind
+// the other, took 8 us of 26 with 64 requests).
 //   * Sums are whole numbers: a probability is held as a multiple of 2^-60
 //     (exact from 2^-37 up, rounded below), so they are exact, do not depend on
 //     how the row was cut, and a segment's second reading meets the place that
@@ -39,6 +41,7 @@ constexpr int kVfThreads = 256;
 constexpr int kVfWarps = kVfThreads / 32;
 constexpr int kVfMaxCluster = 8;
 constexpr int kVfNodes = 64;  // PKV_MAX_DRAFT
+static_assert(kVfWarps * kVfMaxCluster <= 64, "a warp holds two segments' sums a lane");
 typedef unsigned long long u64;
 
 // x held to [0, 1]; NaN counts as 0.
@@ -219,12 +222,14 @@ __device__ __forceinline__ int segment_find(const VfRow& row, int lo, int hi, in
 template <bool kVec>
 __global__ void __launch_bounds__(kVfThreads, 4) draft_verify_kernel(const VerifyArgs a) {
   cg::cluster_group cluster = cg::this_cluster();
-  __shared__ int s_tok[kVfNodes], s_out[kVfNodes];
+  __shared__ int s_tok[kVfNodes], s_out[kVfNodes];  // tokens; those turned down here
+  __shared__ u64 s_outw[kVfNodes];                   // ... and their mass, once each
   __shared__ float s_u[kVfNodes], s_p[kVfNodes], s_q[kVfNodes];
   __shared__ u64 s_kids[kVfNodes];
   __shared__ u64 s_ok;                    // children that pass their first trial
   __shared__ u64 seg[2][kVfWarps];        // this CTA's segments, by sum
   __shared__ u64 all[kVfWarps * kVfMaxCluster];
+  __shared__ u64 part_sum[2][kVfWarps];
   const int C = (int)cluster.num_blocks(), rank = (int)cluster.block_rank();
   const int r = blockIdx.x / C;
   const int t = threadIdx.x, warp = t >> 5, lane = t & 31;
@@ -278,16 +283,19 @@ __global__ void __launch_bounds__(kVfThreads, 4) draft_verify_kernel(const Verif
 
   // ---- sums over the vocabulary, the whole cluster: every thread gets R
   const int per = (((V + S - 1) / S) + 127) & ~127;
-  const int my_seg = rank * kVfWarps + warp;
-  const int lo = (int)min((int64_t)my_seg * per, (int64_t)V), hi = min(lo + per, V);
+  const int lo = (int)min((int64_t)(rank * kVfWarps + warp) * per, (int64_t)V), hi = min(lo + per, V);
   const u64 one = 1ull << 56;
   int sums = 0;
-  auto total_of = [&](const VfRow& row) -> u64 {
-    u64 sum = !row.q          ? segment_sum<kVec, false, true>(row, lo, hi, lane)
-              : row.c == one ? segment_sum<kVec, true, true>(row, lo, hi, lane)
-                             : segment_sum<kVec, true, false>(row, lo, hi, lane);
+  auto range_sum = [&](const VfRow& row, int from, int to) -> u64 {  // a warp
+    u64 sum = !row.q          ? segment_sum<kVec, false, true>(row, from, to, lane)
+              : row.c == one ? segment_sum<kVec, true, true>(row, from, to, lane)
+                             : segment_sum<kVec, true, false>(row, from, to, lane);
 #pragma unroll
     for (int o = 16; o >= 1; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    return sum;
+  };
+  auto total_of = [&](const VfRow& row) -> u64 {
+    const u64 sum = range_sum(row, lo, hi);
     // two buffers in turn: one is written again only after every CTA has
     // passed the next sum's barrier, so has read this one's
     u64* mine = seg[sums & 1];
@@ -343,7 +351,12 @@ __global__ void __launch_bounds__(kVfThreads, 4) draft_verify_kernel(const Verif
       continue;
     }
     __syncthreads();  // s_out is read above
-    if (t == 0) s_out[n_out] = s_tok[x];
+    if (t == 0) {
+      bool twice = false;
+      for (int k = 0; k < n_out; ++k) twice |= s_out[k] == s_tok[x];
+      s_out[n_out] = s_tok[x];
+      s_outw[n_out] = twice ? 0 : fixed60(s_p[x]);
+    }
     __syncthreads();
     ++n_out;
     if (a.draft) {
@@ -358,20 +371,18 @@ __global__ void __launch_bounds__(kVfThreads, 4) draft_verify_kernel(const Verif
   VfRow row = row_at(at, a.draft ? fixed_c(c) : 0);
   int taken_out = a.draft ? 0 : n_out;  // tokens whose mass counts nothing
   u64 total = total_of(row);
-  auto without = [&](int s) -> u64 {  // a segment's sum but for those tokens
-    u64 sum = all[s];
-    for (int k = 0; k < taken_out; ++k) {
-      const int tok = s_out[k];
-      bool twice = false;
-      for (int m = 0; m < k; ++m) twice |= s_out[m] == tok;
-      if (!twice && tok / per == s) sum -= fixed60(as_prob(__ldg(row.p + tok)));
-    }
+  // the mass in [from, to) of the tokens that count nothing
+  auto out_of = [&](int from, int to) -> u64 {
+    u64 sum = 0;
+    for (int k = 0; k < taken_out; ++k)
+      if (s_out[k] >= from && s_out[k] < to) sum += s_outw[k];
     return sum;
   };
   if (taken_out) {
-    const u64 mine = t < S ? without(t) : 0;
-    __syncthreads();
-    if (t < S) all[t] = mine;
+    if (t < S) {
+      const int from = (int)min((int64_t)t * per, (int64_t)V);
+      all[t] -= out_of(from, min(from + per, V));
+    }
     __syncthreads();
     total = 0;
     for (int s = lane; s < S; s += 32) total += all[s];
@@ -384,20 +395,49 @@ __global__ void __launch_bounds__(kVfThreads, 4) draft_verify_kernel(const Verif
     total = total_of(row);
   }
   const u64 want = __umul64hi(fixed64(s_u[0]), total);  // below total
-  // the segment that holds it: this warp's own, if so
-  u64 before = 0;
-  for (int s = lane; s < my_seg; s += 32) before += all[s];
+  // The part that holds `want`, of n <= 64 parts one behind the other; what
+  // stands before it is taken off.  The same in every lane.
+  auto part_of = [&](const u64* sums_, int n_, u64& want_) -> int {
+    const u64 x0 = 2 * lane < n_ ? sums_[2 * lane] : 0, x1 = 2 * lane + 1 < n_ ? sums_[2 * lane + 1] : 0;
+    u64 upto = x0 + x1;
 #pragma unroll
-  for (int o = 16; o >= 1; o >>= 1) before += __shfl_xor_sync(0xffffffffu, before, o);
-  if (total > 0 && before <= want && want < before + all[my_seg]) {
-    int v;
-    if (!row.q)
-      v = segment_find<kVec, false, true>(row, lo, hi, lane, want - before, s_out, taken_out);
-    else if (row.c == one)
-      v = segment_find<kVec, true, true>(row, lo, hi, lane, want - before, s_out, 0);
-    else
-      v = segment_find<kVec, true, false>(row, lo, hi, lane, want - before, s_out, 0);
-    if (lane == 0) a.next_tokens[r] = v;
+    for (int o = 1; o < 32; o <<= 1) {
+      const u64 y = __shfl_up_sync(0xffffffffu, upto, o);
+      if (lane >= o) upto += y;
+    }
+    const unsigned above = __ballot_sync(0xffffffffu, upto > want_);
+    const int l = above ? __ffs(above) - 1 : 31;  // none: the rows have changed in between
+    const u64 before = __shfl_sync(0xffffffffu, upto - x0 - x1, l), first = __shfl_sync(0xffffffffu, x0, l);
+    const bool in_first = want_ - before < first;
+    want_ -= in_first ? before : before + first;
+    return min(2 * l + (in_first ? 0 : 1), n_ - 1);
+  };
+  if (total > 0) {
+    u64 left = want;
+    const int s = part_of(all, S, left);
+    if (s / kVfWarps == rank) {
+      int from = (int)min((int64_t)s * per, (int64_t)V), to = min(from + per, V);
+      for (int b = 0; to - from > 256; b ^= 1) {
+        const int sub = ((to - from + kVfWarps - 1) / kVfWarps + 127) & ~127;
+        const int a0 = min(from + warp * sub, to), a1 = min(a0 + sub, to);
+        const u64 sum = range_sum(row, a0, a1) - out_of(a0, a1);
+        if (lane == 0) part_sum[b][warp] = sum;
+        __syncthreads();
+        const int w = part_of(part_sum[b], kVfWarps, left);
+        from = min(from + w * sub, to);
+        to = min(from + sub, to);
+      }
+      if (warp == 0) {
+        int v;
+        if (!row.q)
+          v = segment_find<kVec, false, true>(row, from, to, lane, left, s_out, taken_out);
+        else if (row.c == one)
+          v = segment_find<kVec, true, true>(row, from, to, lane, left, s_out, 0);
+        else
+          v = segment_find<kVec, true, false>(row, from, to, lane, left, s_out, 0);
+        if (lane == 0) a.next_tokens[r] = max(v, 0);
+      }
+    }
   }
   if (rank == 0) {
     if (t == 0 && total == 0) a.next_tokens[r] = -1;

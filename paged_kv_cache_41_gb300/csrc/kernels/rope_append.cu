@@ -25,7 +25,7 @@ namespace pkv {
 
 namespace {
 
-constexpr int kRopeThreads = 256;
+constexpr int kRopeThreads = 128;
 
 // Four consecutive elements as they lie in memory.
 template <typename T>
@@ -87,7 +87,8 @@ __device__ __forceinline__ void store_mx(const RopeArgs& a, void* cache, const f
 // Group g of D / 8 lanes takes up to kRows head rows of token g / parts: of
 // its parts, the first ceil(Hq / kRows) are q's, then come k's and v's.
 template <typename T, bool kMx, int D, bool kInter, int kRows>
-__global__ void __launch_bounds__(kRopeThreads) rope_append_kernel(const RopeArgs a) {
+// 56 registers where there are four rows of 16-bit elements: nine CTAs an SM.
+__global__ void __launch_bounds__(kRopeThreads, kRows == 4 && sizeof(T) == 2 ? 9 : 1) rope_append_kernel(const RopeArgs a) {
   constexpr int LPR = D / 8;  // lanes of a head row
   pdl_launch_dependents();    // a decode after this append may be scheduled now
   const int Hq = a.num_q_heads, Hkv = a.num_kv_heads;

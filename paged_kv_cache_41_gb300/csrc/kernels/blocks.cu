@@ -33,12 +33,8 @@ constexpr int64_t kBlOwnRows = 4096;
 struct Sum3 {
   long long a, b, c;
 };
-// Inclusive sums over the CTA's threads; *total receives the sums of all.  `ws`:
-// kThreads / 32 entries of shared memory, free again when the call returns.
-template <int kThreads>
-__device__ __forceinline__ Sum3 block_scan(Sum3 x, Sum3* ws, Sum3* total) {
-  constexpr int kWarps = kThreads / 32;
-  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+__device__ __forceinline__ Sum3 warp_scan(Sum3 x) {
+  const int lane = threadIdx.x & 31;
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const long long ya = __shfl_up_sync(0xffffffffu, x.a, o), yb = __shfl_up_sync(0xffffffffu, x.b, o),
@@ -49,24 +45,46 @@ __device__ __forceinline__ Sum3 block_scan(Sum3 x, Sum3* ws, Sum3* total) {
       x.c += yc;
     }
   }
+  return x;
+}
+// Inclusive sums over the CTA's threads; *total receives the sums of all.  `ws`:
+// kThreads / 32 entries of shared memory, free again when the call returns.
+template <int kThreads>
+__device__ __forceinline__ Sum3 block_scan(Sum3 x, Sum3* ws, Sum3* total) {
+  constexpr int kWarps = kThreads / 32;
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  x = warp_scan(x);
   if (lane == 31) ws[warp] = x;
   __syncthreads();
-  Sum3 before = {0, 0, 0}, all = {0, 0, 0};
-#pragma unroll 8
-  for (int w = 0; w < kWarps; ++w) {
-    const Sum3 t = ws[w];
-    if (w < warp) {
-      before.a += t.a;
-      before.b += t.b;
-      before.c += t.c;
+  if constexpr (kWarps <= 4) {
+    Sum3 all = {0, 0, 0};
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const Sum3 y = ws[w];
+      if (w == warp) x = {x.a + all.a, x.b + all.b, x.c + all.c};
+      all = {all.a + y.a, all.b + y.b, all.c + y.c};
     }
-    all.a += t.a;
-    all.b += t.b;
-    all.c += t.c;
+    __syncthreads();
+    *total = all;
+    return x;
+  }
+  // the sums of more warps by one of them: all warps reading all sums is a
+  // thousand loads of shared memory
+  if (warp == 0) {
+    const Sum3 y = warp_scan(lane < kWarps ? ws[lane] : Sum3{0, 0, 0});
+    __syncwarp();
+    if (lane < kWarps) ws[lane] = y;
   }
   __syncthreads();
-  *total = all;
-  return {before.a + x.a, before.b + x.b, before.c + x.c};
+  *total = ws[kWarps - 1];
+  if (warp > 0) {
+    const Sum3 before = ws[warp - 1];
+    x.a += before.a;
+    x.b += before.b;
+    x.c += before.c;
+  }
+  __syncthreads();
+  return x;
 }
 
 // First index i of the ascending a[0 .. n) with a[i] > x (n: none).
@@ -144,6 +162,7 @@ __global__ void __launch_bounds__(kThreads) blocks_update_kernel(const BlocksArg
   // s_wlo on; what comes: from block s_held on, where served
   __shared__ int s_cut[kThreads], s_want[kThreads], s_wlo[kThreads], s_held[kThreads], s_old[kThreads],
       s_new[kThreads];
+  constexpr int kPer = kThreads == 128 ? 1 : 2;  // ids of a thread at a time
   const int t = threadIdx.x, lane = t & 31;
   const int B = a.num_seqs, P = a.block_size;
   const long long cap = (long long)a.max_blocks * P;
@@ -216,35 +235,40 @@ __global__ void __launch_bounds__(kThreads) blocks_update_kernel(const BlocksArg
   // The ids of a pass that go, `total` of them: entry f of the list (ascending
   // request and block) goes onto the stack behind those after it.
   auto go = [&](int base, long long total) {
-    for (long long f0 = total; f0 > 0; f0 -= 4 * kThreads) {
-      // entries f0 - 1 - 4 t and the three before it
-      int32_t id[4];
+    for (long long f0 = total; f0 > 0; f0 -= kPer * kThreads) {
+      // entries f0 - 1 - kPer t and those before it, together on their way
+      int32_t id[kPer], *at[kPer];
       bool all = true;
       int o = -1;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const long long f = f0 - 1 - 4 * t - e;
-        id[e] = -1;
+      for (int e = 0; e < kPer; ++e) {
+        const long long f = f0 - 1 - kPer * t - e;
+        at[e] = nullptr;
         if (f < 0) continue;
         if (o < 0) o = first_above(ids_to, kThreads, f);
         while (o > 0 && ids_to[o - 1] > f) --o;
         const int x = (int)(f - (o ? ids_to[o - 1] : 0));
         const int w = (int)(ids_to[o] - (o ? ids_to[o - 1] : 0)) - s_cut[o];  // of them behind the window
-        int32_t* at = a.block_tables + (int64_t)(base + o) * a.max_blocks +
-                      (x < w ? s_wlo[o] + x : s_want[o] + (x - w));
-        id[e] = *at;
-        *at = -1;
+        at[e] = a.block_tables + (int64_t)(base + o) * a.max_blocks +
+                (x < w ? s_wlo[o] + x : s_want[o] + (x - w));
+      }
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) id[e] = at[e] ? *at[e] : -1;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        if (!at[e]) continue;
+        *at[e] = -1;
         if (id[e] >= a.num_blocks) {
           atomicOr(a.err, PKV_DEVERR_BLOCK);
           id[e] = -1;
         }
         all = all && id[e] >= 0;
       }
-      const long long here = min(f0, (long long)4 * kThreads);
+      const long long here = min(f0, (long long)kPer * kThreads);
       if (__syncthreads_and(all)) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const long long place = avail + 4 * t + e;
+        for (int e = 0; e < kPer; ++e) {
+          const long long place = avail + kPer * t + e;
           if (id[e] < 0) continue;
           if (place < a.num_blocks)
             a.free_ids[place] = id[e];
@@ -255,11 +279,11 @@ __global__ void __launch_bounds__(kThreads) blocks_update_kernel(const BlocksArg
       } else {
         int mine = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) mine += id[e] >= 0;
+        for (int e = 0; e < kPer; ++e) mine += id[e] >= 0;
         Sum3 pushed;
         long long place = avail + block_scan<kThreads>({mine, 0, 0}, ws, &pushed).a - mine;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < kPer; ++e) {
           if (id[e] < 0) continue;
           if (place < a.num_blocks)
             a.free_ids[place] = id[e];
@@ -312,21 +336,30 @@ __global__ void __launch_bounds__(kThreads) blocks_update_kernel(const BlocksArg
     }
     used = max(used, got);
     __syncthreads();
-    const int per = (int)((total.b + kThreads - 1) / kThreads);
-    long long f = (long long)t * per;
-    const long long end = min(f + per, total.b);
-    if (f < end) {
-      int o = first_above(ids_to, kThreads, f);
-      for (; f < end; ++f) {
+    for (long long f0 = 0; f0 < total.b; f0 += kPer * kThreads) {
+      // entries f0 + kPer t and those behind it
+      int32_t id[kPer], *at[kPer];
+      int o = -1;
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        const long long f = f0 + kPer * t + e;
+        at[e] = nullptr;
+        if (f >= total.b) continue;
+        if (o < 0) o = first_above(ids_to, kThreads, f);
         while (ids_to[o] <= f) ++o;
         if (s_new[o] == s_old[o]) continue;  // not served
-        int32_t id = a.free_ids[avail - 1 - (taken + f)];
-        if (id < 0 || id >= a.num_blocks) {
+        at[e] = a.block_tables + (int64_t)(base + o) * a.max_blocks + s_held[o] +
+                (int)(f - (o ? ids_to[o - 1] : 0));
+        id[e] = a.free_ids[avail - 1 - (taken + f)];
+      }
+#pragma unroll
+      for (int e = 0; e < kPer; ++e) {
+        if (!at[e]) continue;
+        if (id[e] < 0 || id[e] >= a.num_blocks) {
           atomicOr(a.err, PKV_DEVERR_BLOCK);
-          id = -1;
+          id[e] = -1;
         }
-        const int e = (int)(f - (o ? ids_to[o - 1] : 0));
-        a.block_tables[(int64_t)(base + o) * a.max_blocks + s_held[o] + e] = id;
+        *at[e] = id[e];
       }
     }
     rows += total.c;
@@ -379,7 +412,9 @@ __global__ void __launch_bounds__(kThreads) blocks_update_kernel(const BlocksArg
 
 cudaError_t launch_blocks_update(const BlocksArgs& a, cudaStream_t stream) {
   const int own = a.num_rows <= kBlOwnRows ? 1 : 0;
-  if (a.num_seqs <= 128 && a.num_rows <= 1024)
+  // a step of few requests and rows; a call without rows gives ids back, of
+  // which there may be thousands
+  if (a.num_seqs <= 128 && a.num_rows > 0 && a.num_rows <= 1024)
     blocks_update_kernel<128><<<1, 128, 0, stream>>>(a, own);
   else
     blocks_update_kernel<1024><<<1, 1024, 0, stream>>>(a, own);

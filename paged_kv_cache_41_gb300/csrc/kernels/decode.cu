@@ -255,9 +255,8 @@ cudaError_t launch_paged_decode(int dtype, int head_dim, int group, const CUtens
                                 const CUtensorMap& tmv, const DecodeArgs& a,
                                 cudaStream_t stream) {
   cudaError_t e;
-  if (a.window)
-    e = launch_decode_partial_window(dtype, head_dim, group, tmk, tmv, a, stream);
-  else if (a.scores)
+  if (a.window) return launch_decode_window(dtype, head_dim, group, tmk, tmv, a, stream);
+  if (a.scores)
     e = launch_decode_partial_scores(dtype, head_dim, group, tmk, tmv, a, stream);
   else if (dtype == PKV_MXFP8)
     e = head_dim == 128 ? dispatch_group<__nv_fp8_e4m3, 128>(group, tmk, tmv, a, stream)

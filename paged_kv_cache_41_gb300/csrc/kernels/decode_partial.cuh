@@ -267,11 +267,12 @@ __device__ __forceinline__ void decode_chunk(const T* __restrict__ kt, const T* 
   }
 }
 
-template <typename T, int D, int G, bool kScores = false, bool kWin = false>
+template <typename T, int D, int G, bool kScores = false, bool kWin = false, bool kDirect = false>
 __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
     decode_partial_kernel(const __grid_constant__ CUtensorMap tmk,
                           const __grid_constant__ CUtensorMap tmv, const DecodeArgsOf<kWin> a) {
   static_assert(!(kScores && kWin), "the descriptor's flags hold one of the two");
+  static_assert(kWin || !kDirect, "segments of any length want the balanced split");
   using TQ = typename IoOf<T>::type;  // q and out
   constexpr int EPL = D / 16;  // head_dim elements per lane
   constexpr int EP2 = EPL / 2;
@@ -305,8 +306,20 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
   if (!a.plan_before_wait) pdl_wait();  // inputs written by earlier kernels are visible
   pdl_launch_dependents();   // the reduction may be scheduled as CTAs retire
   int4 d0;
-  const int n = plan_cta_stages<kDecodeThreads, kStageRows>(
-      a, reinterpret_cast<long long*>(scratch), &d0);
+  int n;
+  if constexpr (kDirect)
+    n = direct_stages<kStageRows>(a, &d0);
+  else
+    n = plan_cta_stages<kDecodeThreads, kStageRows>(a, reinterpret_cast<long long*>(scratch), &d0);
+  if constexpr (kDirect) {
+    if (n < 0) {  // an empty sequence: its output, by the first CTA of each segment
+      if (a.plan_before_wait) pdl_wait();
+      const int64_t rh = (int64_t)d0.x * a.num_q_heads + (int64_t)d0.y * G;
+      for (int i = threadIdx.x; i < G * D; i += kDecodeThreads)
+        store_out(static_cast<TQ*>(a.out) + rh * D + i, 0.f);
+      if (a.lse_out && threadIdx.x < G) a.lse_out[rh + threadIdx.x] = -INFINITY;
+    }
+  }
   if (n <= 0) return;  // no stages: the whole CTA leaves before any barrier
   const int hw = lane >> 4, l16 = lane & 15;
   float2 q2[G][EP2];
@@ -368,7 +381,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
       }
     }
   };
-  const bool d0_exact = a.stage_units == 1 && a.piece_units == 0;
+  const bool d0_exact = kDirect || (a.stage_units == 1 && a.piece_units == 0);
   if (d0_exact && !a.plan_before_wait) load_q(d0.x, d0.y);
 
   if (threadIdx.x == 0) {
@@ -387,12 +400,14 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
   // two-batch descriptor ring in shared memory: block ids of the stage's
   // boxes, first row in the block, box count, and (sequence, kv head, valid
   // rows, flags).  The cursor (cr, ch, ci) is the position of the next
-  // batch's first stage, cpnt / cT the stages and length of sequence cr.
-  int cr = d0.x, ch = d0.y, ci = d0.z, cpnt = 0, cT = 0;
+  // batch's first stage, cpnt / cT the stages and rows of sequence cr.
+  int cr = d0.x, ch = d0.y, ci = d0.z, cpnt = 0;
+  SegRows cT = {0, 0};
   const uint32_t box_bytes = (uint32_t)(TB * D * sizeof(T));
   const uint32_t scale_box = (uint32_t)(TB * kScaleRow);  // MXFP8 scale bytes of one box
   auto compute_batch = [&](int kb) {
-    int r = cr, h = ch, i = ci + lane, pnt = cpnt, len = cT;
+    int r = cr, h = ch, i = ci + lane, pnt = cpnt;
+    SegRows seg = cT;
     const bool act = kb + lane < n;
     if (act) {
       while (i >= pnt) {  // crossed into a later segment (rare)
@@ -401,18 +416,19 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
           h = 0;
           do {
             ++r;
-            len = plan_len(a, r, P, false);
-            pnt = (len + kStageRows - 1) / kStageRows;
+            seg = seg_rows(a, r);
+            pnt = (seg.len + kStageRows - 1) / kStageRows;
           } while (pnt == 0);
         }
       }
       const int k = kb + lane;
-      const StageRows sr = stage_rows<kStageRows>(a, r, len, i);
-      const int row0 = sr.row0, nvalid = sr.nvalid;
+      const StageRows sr = stage_rows<kStageRows>(a, seg, i);
+      const int nvalid = sr.nvalid, row0 = sr.row(0);
       const int b0 = row0 / P;
       const int nbox = (nvalid + TB - 1) / TB;  // 1 or 2 (two only when P < 32)
-      const int32_t* tbl = a.block_tables + (int64_t)r * a.max_blocks + b0;
-      const int id0 = __ldg(tbl), id1 = nbox > 1 ? __ldg(tbl + 1) : -1;
+      const int32_t* tbl = a.block_tables + (int64_t)r * a.max_blocks;
+      const int id0 = __ldg(tbl + b0);
+      const int id1 = nbox > 1 ? __ldg(tbl + (kWin ? sr.row(TB) / P : b0 + 1)) : -1;
       const int dseg = k - i;  // CTA stage index of the segment's first stage
       const bool end = k == n - 1 || i == pnt - 1;
       const int flags = (k == 0 || i == 0 ? kPieceStart : 0) | (end ? kPieceEnd : 0) |
@@ -422,14 +438,9 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
         prefetch_l2_bulk(static_cast<const TQ*>(a.q) + (qr * a.num_q_heads + (int64_t)h * G) * D,
                          (uint32_t)(G * D * sizeof(TQ)));
       }
-      // the piece's q row rides in the box-count word (nbox is 1 or 2; 3: the
-      // second box alone, the first one's rows are hidden)
-      int code = nbox;
-      if constexpr (kWin) {
-        if (nbox == 2 && sr.hide_lo == 0 && sr.hide_hi >= TB) code = 3;
-      }
+      // the piece's q row rides in the box-count word (nbox is 1 or 2)
       const int qrow = a.q_rows ? __ldg(a.q_rows + r) : r;
-      dA[k & 63] = make_int4(id0, id1, row0 - b0 * P, code | (qrow << 2));
+      dA[k & 63] = make_int4(id0, id1, row0 - b0 * P, nbox | (qrow << 2));
       // with scores, the stage's index in its segment rides above the flags;
       // under a window, its hidden rows
       dB[k & 63] = make_int4(r, h, nvalid,
@@ -442,16 +453,16 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
     ch = __shfl_sync(0xffffffffu, h, 31);
     ci = __shfl_sync(0xffffffffu, i, 31) + 1;
     cpnt = __shfl_sync(0xffffffffu, pnt, 31);
-    cT = __shfl_sync(0xffffffffu, len, 31);
+    cT.len = __shfl_sync(0xffffffffu, seg.len, 31);
+    if constexpr (kWin) cT.skip = __shfl_sync(0xffffffffu, seg.skip, 31);
     __syncwarp();
   };
   // Fill ring slot `st` with the CTA's k-th stage (warp 0, all lanes).
   auto issue_stage = [&](int st, int k) {
     const int4 da = dA[k & 63];
     const int4 db = dB[k & 63];
-    const int nbox = kWin && (da.w & 3) == 3 ? 2 : da.w & 3;
-    const int box0 = kWin && (da.w & 3) == 3 ? 1 : 0;  // the first box to load
-    const bool valid = (box0 == 1 || (da.x >= 0 && (int64_t)da.x < a.num_blocks)) &&
+    const int nbox = da.w & 3;
+    const bool valid = da.x >= 0 && (int64_t)da.x < a.num_blocks &&
                        (nbox < 2 || (da.y >= 0 && (int64_t)da.y < a.num_blocks));
     if (lane == 0) sdesc[st] = db;
     if ((db.w & kPieceStart) && lane == 31)  // refresh the piece's q in L2 shortly before use
@@ -467,21 +478,21 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
     } else {
       if (lane == 0) {
         stage_ok[st] = 1;
-        mbar_arrive_expect_tx(&full[st], 2u * (box_bytes + (kIsMx<T> ? scale_box : 0u)) * (uint32_t)(nbox - box0));
+        mbar_arrive_expect_tx(&full[st], 2u * (box_bytes + (kIsMx<T> ? scale_box : 0u)) * (uint32_t)nbox);
       }
       __syncwarp();
       // one box per lane: lanes 0..nbox-1 load K, lanes 16..16+nbox-1 load V;
       // MXFP8: lanes 8.. and 24.. copy the same boxes' scale rows, which lie
       // contiguously in the head-major scale plane
       const int j = lane & 15;
-      if (j >= box0 && j < nbox) {
+      if (j < nbox) {
         T* dst = tiles + (size_t)st * 2 * L.tile_elems + (lane < 16 ? 0 : L.tile_elems) + j * TB * D;
         tma_load_4d(dst, lane < 16 ? &tmk : &tmv, 0, db.y, j == 0 ? da.z : 0, j == 0 ? da.x : da.y,
                     &full[st]);
       }
       if constexpr (kIsMx<T>) {
         const int js = j - 8;
-        if (js >= box0 && js < nbox) {
+        if (js >= 0 && js < nbox) {
           const int64_t blk = js == 0 ? da.x : da.y;
           const int row = js == 0 ? da.z : 0;
           const uint8_t* src = (lane < 16 ? a.k_scales : a.v_scales) +
@@ -506,8 +517,8 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
       prefetch_tensormap(&tmk);
       prefetch_tensormap(&tmv);
     }
-    cT = plan_len(a, cr, P, false);
-    cpnt = (cT + kStageRows - 1) / kStageRows;
+    cT = seg_rows(a, cr);
+    cpnt = (cT.len + kStageRows - 1) / kStageRows;
     compute_batch(0);  // lengths, block tables and q rows only
   }
   // With plan_before_wait, what the preceding kernel may still write (K/V
@@ -690,11 +701,11 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
   }
 }
 
-template <typename T, int D, int G, bool kScores = false, bool kWin = false>
+template <typename T, int D, int G, bool kScores = false, bool kWin = false, bool kDirect = false>
 cudaError_t launch_partial(const CUtensorMap& tmk, const CUtensorMap& tmv, const DecodeArgsOf<kWin>& a,
                            cudaStream_t stream) {
   const size_t smem = decode_smem_layout(D, (int)sizeof(T), G, a.num_stages).total;
-  auto kern = decode_partial_kernel<T, D, G, kScores, kWin>;
+  auto kern = decode_partial_kernel<T, D, G, kScores, kWin, kDirect>;
   static SmemAttrCache attr_cache;
   cudaError_t e = ensure_smem_limit(kern, (int)smem, attr_cache);
   if (e != cudaSuccess) return e;

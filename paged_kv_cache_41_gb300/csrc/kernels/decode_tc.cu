@@ -162,16 +162,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       prefetch_tensormap(&tmq);
     }
     int r = d0.x, h = d0.y, i = d0.z;
-    int len = plan_len(a, r, P, false);
-    int nt = (len + kTcRows - 1) / kTcRows;
+    SegRows seg = seg_rows(a, r);
+    int nt = (seg.len + kTcRows - 1) / kTcRows;
     while (i >= nt) {  // the plan may name a segment's end: its next non-empty one
       i -= nt;
       if (++h == Hkv) {
         h = 0;
         do {
           ++r;
-          len = plan_len(a, r, P, false);
-          nt = (len + kTcRows - 1) / kTcRows;
+          seg = seg_rows(a, r);
+          nt = (seg.len + kTcRows - 1) / kTcRows;
         } while (nt == 0);
       }
     }
@@ -179,19 +179,19 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // sequence r (0 where the lane has no box), loaded one stage ahead: the
     // table read then overlaps the wait for a free slot
     const int j = lane & 15;
-    auto box_block = [&](int r_, int i_, int len_) -> int {
-      const StageRows sr_ = stage_rows<kTcRows>(a, r_, len_, i_);
-      const int row = sr_.row0 + j * TB;
+    auto box_block = [&](int r_, int i_, SegRows seg_) -> int {
+      const StageRows sr_ = stage_rows<kTcRows>(a, seg_, i_);
+      const int row = sr_.row(j * TB);
       return j * TB < sr_.nvalid
                  ? __ldg(a.block_tables + (int64_t)r_ * a.max_blocks + row / P)
                  : 0;
     };
-    int blk_next = box_block(r, i, len);
+    int blk_next = box_block(r, i, seg);
     if (a.plan_before_wait) pdl_wait();  // the K/V rows and q are read from here on
     int pieces = 0;
     // the previous stage's V boxes: this lane's block and first row, the box
-    // count and the kv head; under a window, the boxes without a seen row
-    int v_blk = 0, v_brow = 0, v_nbox = 0, v_h = 0, v_hide0 = 0, v_hide1 = 0;
+    // count and the kv head
+    int v_blk = 0, v_brow = 0, v_nbox = 0, v_h = 0;
     auto issue_v = [&](int kv) -> bool {
       const int sv = kv % kTcStages;
       if (kv >= kTcStages) {
@@ -202,9 +202,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
       }
-      if (lane == 0) mbar_arrive_expect_tx(&vfull[sv], (uint32_t)((v_nbox - (v_hide1 - v_hide0)) * TB * kTcD * 2));
+      if (lane == 0) mbar_arrive_expect_tx(&vfull[sv], (uint32_t)(v_nbox * TB * kTcD * 2));
       __syncwarp();
-      if (lane >= 16 && j < v_nbox && (j < v_hide0 || j >= v_hide1))
+      if (lane >= 16 && j < v_nbox)
         tma_load_5d(ring + (size_t)sv * 2 * kTcTile + kTcTile + j * TB * kTcD * 2, &tmv, 0, 0, 0, v_h,
                     (int)((int64_t)v_blk * (P / kRowGroup) + v_brow / kRowGroup), &vfull[sv]);
       issued_v = kv + 1;
@@ -226,10 +226,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           break;
         }
       }
-      const StageRows sr = stage_rows<kTcRows>(a, r, len, i);
-      const int t0 = sr.row0, nvalid = sr.nvalid;
-      int hide0 = 0, hide1 = 0;  // boxes that are not loaded
-      if constexpr (kWin) hidden_boxes(sr, TB, &hide0, &hide1);
+      const StageRows sr = stage_rows<kTcRows>(a, seg, i);
+      const int nvalid = sr.nvalid;
       const int dseg = k - i;  // CTA stage index of the segment's first stage
       const bool start = k == 0 || i == 0;
       const bool end = k == n - 1 || i == nt - 1;
@@ -240,9 +238,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
                         (dseg > 0 ? kSlotOne : 0) | (qb << 4) |
                         (kScores ? i << 6 : kWin ? (sr.hide_lo << 8) | (sr.hide_hi << 16) : 0);
       const int nbox = (nvalid + TB - 1) / TB;  // per tensor
-      int brow = (t0 + j * TB) % P;
-      const bool load = j < nbox && (j < hide0 || j >= hide1);
-      const bool bad = load && (blk < 0 || (int64_t)blk >= a.num_blocks);
+      int brow = sr.row(j * TB) % P;
+      const bool bad = j < nbox && (blk < 0 || (int64_t)blk >= a.num_blocks);
       if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.err, PKV_DEVERR_BLOCK);
       if (bad) {
         blk = (int)a.num_blocks;  // zero-filled out-of-range box
@@ -250,10 +247,10 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       }
       if (lane == 0) {
         sdesc[s] = make_int4(r, h, nvalid, flags);
-        mbar_arrive_expect_tx(&kfull[s], (uint32_t)((nbox - (hide1 - hide0)) * TB * kTcD * 2 + (start ? 2 * G * 128 : 0)));
+        mbar_arrive_expect_tx(&kfull[s], (uint32_t)(nbox * TB * kTcD * 2 + (start ? 2 * G * 128 : 0)));
       }
       __syncwarp();
-      if (lane < 16 && load)
+      if (lane < 16 && j < nbox)
         tma_load_5d(ring + (size_t)s * 2 * kTcTile + j * TB * kTcD * 2, &tmk, 0, 0, 0, h,
                     (int)((int64_t)blk * (P / kRowGroup) + brow / kRowGroup), &kfull[s]);
       if (start && lane == 0) {
@@ -270,8 +267,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       v_blk = blk;
       v_brow = brow;
       v_nbox = nbox;
-      v_hide0 = hide0;
-      v_hide1 = hide1;
       v_h = h;
       if (k + 1 < n && ++i == nt) {  // on to the next non-empty segment
         i = 0;
@@ -279,12 +274,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           h = 0;
           do {
             ++r;
-            len = plan_len(a, r, P, false);
-            nt = (len + kTcRows - 1) / kTcRows;
+            seg = seg_rows(a, r);
+            nt = (seg.len + kTcRows - 1) / kTcRows;
           } while (nt == 0);
         }
       }
-      if (k + 1 < n) blk_next = box_block(r, i, len);
+      if (k + 1 < n) blk_next = box_block(r, i, seg);
     }
     if (v_ok) issue_v(n - 1);
   } else if (warp == 1) {
@@ -605,7 +600,7 @@ cudaError_t launch_paged_decode_tc(const CUtensorMap& tmk, const CUtensorMap& tm
     cudaError_t e = ensure_smem_limit(kern, kTcSmem, window_cache);
     if (e != cudaSuccess) return e;
     e = launch_pdl(kern, dim3((unsigned)a.num_ctas), dim3(kTcThreads), kTcSmem, stream, tmk, tmv, tmq,
-                   WindowArgs(a, kTcRows));
+                   WindowArgs(a, a.block_size < kTcRows ? a.block_size : kTcRows));
     if (e != cudaSuccess) return e;
     return launch_decode_reduce(PKV_BF16, kTcD, a, stream);
   }

@@ -149,16 +149,16 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       prefetch_tensormap(&tmq);
     }
     int r = d0.x, h = d0.y, i = d0.z;
-    int len = plan_len(a, r, P, false);
-    int nt = (len + kMxRows - 1) / kMxRows;
+    SegRows seg = seg_rows(a, r);
+    int nt = (seg.len + kMxRows - 1) / kMxRows;
     while (i >= nt) {  // the plan may name a segment's end: its next non-empty one
       i -= nt;
       if (++h == Hkv) {
         h = 0;
         do {
           ++r;
-          len = plan_len(a, r, P, false);
-          nt = (len + kMxRows - 1) / kMxRows;
+          seg = seg_rows(a, r);
+          nt = (seg.len + kMxRows - 1) / kMxRows;
         } while (nt == 0);
       }
     }
@@ -174,10 +174,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       }
-      const StageRows sr = stage_rows<kMxRows>(a, r, len, i);
-      const int t0 = sr.row0, nvalid = sr.nvalid;
-      int hide0 = 0, hide1 = 0;  // boxes that are not loaded
-      if constexpr (kWin) hidden_boxes(sr, TB, &hide0, &hide1);
+      const StageRows sr = stage_rows<kMxRows>(a, seg, i);
+      const int nvalid = sr.nvalid;
       const int dseg = k - i;  // CTA stage index of the segment's first stage
       const bool start = k == 0 || i == 0;
       const bool end = k == n - 1 || i == nt - 1;
@@ -189,22 +187,21 @@ __global__ void __launch_bounds__(kMxThreads, 1)
                         (kScores ? i << 6 : kWin ? (sr.hide_lo << 8) | (sr.hide_hi << 16) : 0);
       const int nbox = (nvalid + TB - 1) / TB;  // per tensor, <= 8
       int blk = 0, brow = 0;
-      const bool load = j < nbox && (j < hide0 || j >= hide1);
-      if (load) {
-        const int row = t0 + j * TB;
+      if (j < nbox) {
+        const int row = sr.row(j * TB);
         const int bi = row / P;
         brow = row - bi * P;
         blk = __ldg(a.block_tables + (int64_t)r * a.max_blocks + bi);
       }
-      const bool bad = load && (blk < 0 || (int64_t)blk >= a.num_blocks);
+      const bool bad = j < nbox && (blk < 0 || (int64_t)blk >= a.num_blocks);
       if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.err, PKV_DEVERR_BLOCK);
       if (lane == 0) {
         sdesc_raw[s] = make_int4(r, h, nvalid, flags);
-        mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * (nbox - (hide1 - hide0)) * TB * (kMxD + kMxD / 32) +
+        mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * nbox * TB * (kMxD + kMxD / 32) +
                                                     (start ? 2 * G * 128 : 0)));
       }
       __syncwarp();
-      if (load) {
+      if (j < nbox) {
         unsigned char* slot = raw + (size_t)s * kRawSlot;
         if (kind == 0 || kind == 2) {
           // a bad block id reads a zero-filled out-of-range box
@@ -233,8 +230,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           h = 0;
           do {
             ++r;
-            len = plan_len(a, r, P, false);
-            nt = (len + kMxRows - 1) / kMxRows;
+            seg = seg_rows(a, r);
+            nt = (seg.len + kMxRows - 1) / kMxRows;
           } while (nt == 0);
         }
       }
@@ -568,7 +565,7 @@ static cudaError_t launch_mx_t(const CUtensorMap& tmk, const CUtensorMap& tmv,
     cudaError_t e = ensure_smem_limit(kern, kMxSmem, window_cache);
     if (e != cudaSuccess) return e;
     return launch_pdl(kern, dim3((unsigned)a.num_ctas), dim3(kMxThreads), kMxSmem, stream, tmk, tmv,
-                      tmq, WindowArgs(a, kMxRows));
+                      tmq, WindowArgs(a, a.block_size < kMxRows ? a.block_size : kMxRows));
   }
   auto kern = a.scores ? decode_tc_mx_kernel<G, true> : decode_tc_mx_kernel<G>;
   static SmemAttrCache attr_cache[2];

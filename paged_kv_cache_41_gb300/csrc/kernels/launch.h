@@ -128,14 +128,22 @@ struct DecodeArgs {
   // ones.  0: every row is.
   int32_t window;
   int32_t num_sinks;
+  // Under a window, 0: the balanced split of plan.cuh; n: CTA c takes the (c %
+  // n)-th n-th of the stages of segment c / n, on the CUDA cores.
+  int32_t parts;
 };
 
 // Arguments of the kernels of a windowed decode: a type of its own, so that
 // the work split counts what is seen (plan.cuh).
 struct WindowArgs : DecodeArgs {
-  int32_t stage_rows = 0;       // rows of one stage
+  int32_t box_rows = 0;         // rows of one TMA box, a power of two
+  int32_t sink_rows = 0;        // ... of the sinks' boxes (INT32_MAX - box_rows at most)
   WindowArgs() = default;
-  WindowArgs(const DecodeArgs& a, int rows) : DecodeArgs(a), stage_rows(rows) {}
+  WindowArgs(const DecodeArgs& a, int rows)
+      : DecodeArgs(a),
+        box_rows(rows),
+        sink_rows(a.num_sinks > INT32_MAX - 2 * rows ? INT32_MAX / rows * rows - rows
+                                                     : (a.num_sinks + rows - 1) / rows * rows) {}
 };
 
 // Partial kernel, then the LSE reduction of cut segments, on one stream.
@@ -148,8 +156,8 @@ cudaError_t launch_decode_partial_scores(int dtype, int head_dim, int group, con
                                          const CUtensorMap& tmv, const DecodeArgs& args,
                                          cudaStream_t stream);
 
-// The partial kernel alone, under a window (decode_window.cu).
-cudaError_t launch_decode_partial_window(int dtype, int head_dim, int group, const CUtensorMap& tmk,
+// The windowed decode on the CUDA cores, merge included (decode_window.cu).
+cudaError_t launch_decode_window(int dtype, int head_dim, int group, const CUtensorMap& tmk,
                                          const CUtensorMap& tmv, const DecodeArgs& args,
                                          cudaStream_t stream);
 

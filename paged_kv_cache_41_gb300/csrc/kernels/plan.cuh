@@ -38,59 +38,83 @@ __device__ __forceinline__ int plan_len(const DecodeArgs& a, int r, int block_si
 }
 __device__ __forceinline__ int plan_heads(const DecodeArgs& a) { return a.num_kv_heads; }
 
-// Under a window a sequence of T rows shows rows t < S (the sinks) and t >= lo =
-// T - W.  Its stages are those that hold a row that is seen: the first ceil(S /
-// R), then, `skip` stages later, those from row lo's on.  They are counted, dealt
-// out and walked like the stages of T - skip R rows; only where a stage's rows
-// lie, and which of them are seen, asks for the window again.
-__device__ __forceinline__ int window_skip(const DecodeArgs& a, int T, int R) {
-  const int lo = T - a.window;
-  if (lo <= a.num_sinks) return 0;  // every row is seen
-  return max(lo / R - (a.num_sinks + R - 1) / R, 0);
-}
-__device__ __forceinline__ int plan_len(const WindowArgs& a, int r, int block_size, bool report) {
-  const int T = effective_len(__ldg(a.seq_lens + r), a.max_blocks, block_size, a.err, report);
-  return T - window_skip(a, T, a.stage_rows) * a.stage_rows;
+// A sequence's rows as the split counts them (plan_len), and, under a window, how
+// many it leaves out.
+struct SegRows {
+  int len, skip;
+};
+__device__ __forceinline__ SegRows seg_rows(const DecodeArgs& a, int r) {
+  return {plan_len(a, r, a.block_size, false), 0};
 }
 
-// The rows of a stage: the first one's place in the sequence, how many there
-// are, and the hidden ones among them, [hide_lo, hide_hi) (none: 0, 0).
+// Under a window a sequence of T rows shows rows t < S (the sinks) and t >= lo =
+// T - W.  Boxes of TB rows without a row that is seen are left out: behind the
+// ceil(S / TB) boxes of the sinks the one that holds row lo follows, `skip` rows
+// further on.  What is left is counted, dealt out and walked as a sequence of T -
+// skip rows ("dense" rows); only where a box lies, and which rows are seen, asks for
+// the window again.
+__device__ __forceinline__ SegRows seg_rows(const WindowArgs& a, int r, bool report = false) {
+  const int T = effective_len(__ldg(a.seq_lens + r), a.max_blocks, a.block_size, a.err, report);
+  const int lo = T - a.window;
+  const int skip = lo <= a.num_sinks ? 0  // every row is seen
+                                     : max((lo & ~(a.box_rows - 1)) - a.sink_rows, 0);
+  return {T - skip, skip};
+}
+__device__ __forceinline__ int plan_len(const WindowArgs& a, int r, int, bool report) {
+  return seg_rows(a, r, report).len;
+}
+
+// The rows of a stage, its dense rows dense0 ..: how many there are, and the
+// hidden ones among them, [hide_lo, hide_hi) (none: 0, 0).
 struct StageRows {
-  int row0, nvalid, hide_lo, hide_hi;
+  int dense0, nvalid, hide_lo, hide_hi;
+  int from, skip;  // dense rows from `from` on lie `skip` rows further on
+  // The place in the sequence of a stage's row (the first one of a box).
+  __device__ __forceinline__ int row(int i) const {
+    return dense0 + i + (dense0 + i >= from ? skip : 0);
+  }
 };
-// Stage i of a sequence r of `len` rows as plan_len counts them.
 template <int R>
-__device__ __forceinline__ StageRows stage_rows(const DecodeArgs& a, int r, int len, int i) {
-  return {i * R, min(R, len - i * R), 0, 0};
+__device__ __forceinline__ StageRows stage_rows(const DecodeArgs&, SegRows seg, int i) {
+  return {i * R, min(R, seg.len - i * R), 0, 0, 0, 0};
 }
 template <int R>
-__device__ __forceinline__ StageRows stage_rows(const WindowArgs& a, int r, int len, int i) {
-  const int T = effective_len(__ldg(a.seq_lens + r), a.max_blocks, a.block_size, a.err, false);
-  const int lo = T - a.window, S = a.num_sinks;
-  StageRows s = {i * R, 0, 0, 0};
-  if (lo > S && i >= (S + R - 1) / R) s.row0 += window_skip(a, T, R) * R;
-  s.nvalid = min(R, T - s.row0);
+__device__ __forceinline__ StageRows stage_rows(const WindowArgs& a, SegRows seg, int i) {
+  const int lo = seg.len + seg.skip - a.window, S = a.num_sinks;
+  StageRows s = {i * R, min(R, seg.len - i * R), 0, 0, a.sink_rows, seg.skip};
   if (lo > S) {
-    const int hs = min(max(S - s.row0, 0), R), he = min(max(lo - s.row0, 0), R);
-    if (hs < he) {
-      if (he >= s.nvalid) {
-        s.nvalid = hs;  // nothing is seen behind the sinks
-      } else {
-        s.hide_lo = hs;
-        s.hide_hi = he;
-      }
+    const int hs = min(max(S - s.dense0, 0), R), he = min(max(lo - seg.skip - s.dense0, 0), R);
+    if (he >= s.nvalid) {
+      s.nvalid = hs;  // nothing is seen behind the sinks
+    } else if (hs < he) {
+      s.hide_lo = hs;
+      s.hide_hi = he;
     }
   }
   return s;
 }
-// Whether row `row` of a stage is seen; the boxes of TB rows that hold no seen
-// row of a stage, [*lo, *hi).
+// Whether row `row` of a stage is seen.
 __device__ __forceinline__ bool row_seen(int row, int nvalid, int hide_lo, int hide_hi) {
   return row < nvalid && (row < hide_lo || row >= hide_hi);
 }
-__device__ __forceinline__ void hidden_boxes(const StageRows& s, int TB, int* lo, int* hi) {
-  *lo = (s.hide_lo + TB - 1) / TB;
-  *hi = max(*lo, s.hide_hi / TB);
+
+// The split without a plan: CTA c takes part c % a.parts of the stages of
+// segment c / a.parts (sequence-major, then kv head), an equal run of them.
+// Returns their number and the (sequence, head, first stage) in *d0; 0: none,
+// -1: none, and it is for this CTA to write an empty segment's result.
+template <int R>
+__device__ __forceinline__ int direct_stages(const WindowArgs& a, int4* d0) {
+  const int seg = blockIdx.x / a.parts, part = blockIdx.x - seg * a.parts;
+  const int r = seg / a.num_kv_heads;
+  const int nt = (plan_len(a, r, a.block_size, part == 0) + R - 1) / R;
+  const int w = (nt + a.parts - 1) / a.parts, i0 = part * w;
+  *d0 = make_int4(r, seg - r * a.num_kv_heads, i0, 0);
+  if (nt == 0) return part == 0 ? -1 : 0;
+  return max(min(w, nt - i0), 0);
+}
+template <int R>
+__device__ __forceinline__ int direct_stages(const DecodeArgs&, int4*) {
+  return 0;
 }
 
 template <bool kWin>

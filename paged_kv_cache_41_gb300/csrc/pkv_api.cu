@@ -246,7 +246,7 @@ pkv_status launch_decode(const pkv_cache_desc* cache, int G, const void* q, cons
   // 69 -> 65.5 us, prefix-tree call 77 -> 72 us, the long-context decode
   // unchanged; a piece worth 1/4, 1/3, 1/2, 3/4, 1 or 2 stages measured no
   // better overall.  The tensor-core decode's 128-row stages dwarf a piece.
-  const bool tc = use_tc_decode(cache, G);
+  const bool tc = use_tc_decode(cache, G) && !a.parts;
   if (cache->dtype == PKV_MXFP8) {  // the scale planes follow the element planes
     a.k_scales = static_cast<const uint8_t*>(k_cache) + mx_plane_bytes(cache);
     a.v_scales = static_cast<const uint8_t*>(v_cache) + mx_plane_bytes(cache);
@@ -523,16 +523,44 @@ size_t pkv_decode_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
 
 namespace {
 
-// Blocks of a sequence that a windowed decode's work list can hold at most
-// (window 0: all).  Its stages are those of the sinks and, the window beginning
-// anywhere in one, those of window + 1 stage's rows.
-int32_t seen_blocks(const pkv_cache_desc* c, int32_t num_q_heads, int32_t max_blocks, int32_t window,
-                    int32_t num_sinks) {
-  if (window <= 0) return max_blocks;
-  const int64_t R = decode_stage_rows(c, num_q_heads / c->num_kv_heads);
-  const int64_t rows = ((int64_t)num_sinks + R - 1) / R * R + ((int64_t)window + 2 * R - 1) / R * R;
+// CTAs of a decode, and the parts of a segment where it takes the direct split
+// of a window (0: the balanced one).
+struct DecodeSplit {
+  int64_t ctas;
+  int32_t parts;
+};
+
+// Rows up to which a window takes the direct split, where its segments alone
+// come near to filling the GPU, and where each is cut into parts.  Measured in us, bf16, block size
+// 16, direct / balanced (eight query heads per kv head: / the tensor cores):
+//   whole segments: 64 x 8 of them, 4 heads: window 128 11.5 / 20.3, 512 32.7 / 40.8,
+//   1024 58.3 / 59.1, 2000 106.7 / 93.7; 256 x 8: 128 43.1 / 51.4, 512 102.4 / 107.0,
+//   2000 233.3 / 213.3; 64 x 8, 8 heads: 128 21.2 / 38.5, 500 56.7 / 61.5, 1024 105.2 / 76.2;
+//   in parts: 8 x 8, 4 heads: 128 8.6 / 12.8, 1024 15.0 / 18.7, 2000 21.7 / 24.0,
+//   4096 33.8 / 31.2; 4 x 8, 8 heads: 128 8.8 / 15.1, 1024 15.7 / 20.3, 2000 20.2 / 21.4.
+constexpr int64_t kDirectRows = 600;
+constexpr int64_t kDirectPartRows = 2200;
+
+DecodeSplit decode_split(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
+                         int32_t max_blocks, int32_t partition_size, int32_t window, int32_t num_sinks) {
+  if (window <= 0) return {decode_ctas(c, num_seqs, num_q_heads, max_blocks, partition_size), 0};
+  const int G = num_q_heads / c->num_kv_heads;
+  // dense rows of a sequence at most: whole boxes of the sinks and, the window
+  // beginning anywhere in one, of the window
+  const int64_t B = c->block_size < pkv::decode_tc_rows() ? c->block_size : pkv::decode_tc_rows();
+  const int64_t seen = ((int64_t)num_sinks + B - 1) / B * B + (int64_t)window + B;
+  const int64_t rows = std::min(seen, (int64_t)max_blocks * c->block_size);
+  const bool tc = use_tc_decode(c, G);
+  if (!(tc && c->dtype == PKV_MXFP8)) {  // eight heads over MXFP8: the tensor cores only
+    int64_t resident = pkv::decode_resident_ctas(c->dtype, c->head_dim, G);
+    if (resident <= 0) resident = 2LL * sm_count();
+    const int64_t segs = (int64_t)num_seqs * c->num_kv_heads;
+    const int64_t stages = (rows + pkv::kStageRows - 1) / pkv::kStageRows;
+    const int64_t parts = std::max<int64_t>(std::min(resident / segs, stages), 1);  // one wave
+    if (rows <= (parts > 1 ? kDirectPartRows : kDirectRows)) return {segs * parts, (int32_t)parts};
+  }
   const int64_t blocks = (rows + c->block_size - 1) / c->block_size;
-  return blocks < max_blocks ? (int32_t)blocks : max_blocks;
+  return {decode_ctas(c, num_seqs, num_q_heads, (int32_t)blocks, 0), 0};
 }
 
 // The paged decode; with `scores` it also leaves every row's base-2 scores
@@ -555,9 +583,9 @@ pkv_status decode_checked(const pkv_cache_desc* cache, void* out, float* lse, co
     return PKV_ERR_INVALID_ARG;
   if (partition_size % cache->block_size != 0) return PKV_ERR_INVALID_ARG;
   const int G = num_q_heads / cache->num_kv_heads;
-  const int64_t C =
-      decode_ctas(cache, num_seqs, num_q_heads,
-                  seen_blocks(cache, num_q_heads, max_blocks_per_seq, window, num_sinks), partition_size);
+  const DecodeSplit split = decode_split(cache, num_seqs, num_q_heads, max_blocks_per_seq,
+                                         partition_size, window, num_sinks);
+  const int64_t C = split.ctas;
   if (C > INT32_MAX) return PKV_ERR_UNSUPPORTED;
   const DecodeWorkspace w = decode_workspace(num_seqs, C, G, cache->head_dim);
   if (workspace_bytes < w.total || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
@@ -590,6 +618,7 @@ pkv_status decode_checked(const pkv_cache_desc* cache, void* out, float* lse, co
   a.scores_rows = scores_rows;
   a.window = window;
   a.num_sinks = num_sinks;
+  a.parts = split.parts;
   return launch_decode(cache, G, q, k_cache, v_cache, a, as_stream(stream));
 }
 
@@ -615,9 +644,9 @@ size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* cache, int32_t nu
       max_blocks_per_seq <= 0 || window <= 0 || num_sinks < 0 ||
       check_attention_shape(cache, num_q_heads) != PKV_OK)
     return 0;
-  return pkv_decode_workspace_bytes(
-      cache, num_seqs, num_q_heads,
-      seen_blocks(cache, num_q_heads, max_blocks_per_seq, window, num_sinks), 0);
+  const DecodeSplit split = decode_split(cache, num_seqs, num_q_heads, max_blocks_per_seq, 0, window,
+                                         num_sinks);
+  return decode_workspace(num_seqs, split.ctas, num_q_heads / cache->num_kv_heads, cache->head_dim).total;
 }
 
 pkv_status pkv_paged_attention_decode_window(

@@ -694,7 +694,8 @@ pkv_status pkv_paged_attention_decode_window(
  *                  in 0 .. D.
  *   q_weight, k_weight: float [D], or NULL: no norm.
  * q, k, v and out are bf16 (fp32 with a PKV_F32 cache); pointers 16-byte aligned,
- * strides whole multiples of 16 bytes.  head_dim 64 or 128; any block_size. */
+ * strides whole multiples of 16 bytes.  head_dim 64 or 128; any block_size; up to
+ * 2^29 head rows of q, k and v together. */
 pkv_status pkv_qk_norm_rope_append(
     const pkv_cache_desc* cache, void* out, void* k_cache, void* v_cache, const void* q,
     int64_t q_stride, const void* k, int64_t k_stride, const void* v, int64_t v_stride,

@@ -1303,8 +1303,7 @@ pkv_status pkv_qk_norm_rope_append(
       !aligned16(k_weight))
     return PKV_ERR_INVALID_ARG;
   const int64_t heads = num_q_heads + 2 * (int64_t)Hkv;
-  if (num_tokens > ((int64_t)1 << 40) / heads || num_tokens * heads / 16 > INT32_MAX - 2)
-    return PKV_ERR_UNSUPPORTED;
+  if (num_tokens > ((int64_t)1 << 29) / heads) return PKV_ERR_UNSUPPORTED;
   pkv::RopeArgs a{};
   if (axis_of)
     for (int j = 0; j < rot / 2; ++j) {

@@ -86,9 +86,12 @@ __device__ __forceinline__ void store_mx(const RopeArgs& a, void* cache, const f
 
 // Group g of D / 8 lanes takes up to kRows head rows of token g / parts: of
 // its parts, the first ceil(Hq / kRows) are q's, then come k's and v's.
+// Four rows of 16-bit elements: 56 registers, nine CTAs an SM (32768 tokens: 138
+// us, 5950 GB/s; with eight or ten CTAs 146); quantising takes eight.
 template <typename T, bool kMx, int D, bool kInter, int kRows>
-// Four rows of 16-bit elements: 56 registers, nine CTAs an SM (eight: 146 us instead of 138 for 32768 tokens; ten, 48 registers: 146); quantising takes eight.
-__global__ void __launch_bounds__(kRopeThreads, kRows == 4 && sizeof(T) == 2 ? (kMx ? 8 : 9) : 1) rope_append_kernel(const RopeArgs a) {
+__global__ void
+__launch_bounds__(kRopeThreads, kRows == 4 && sizeof(T) == 2 ? (kMx ? 8 : 9) : 1)
+    rope_append_kernel(const RopeArgs a) {
   constexpr int LPR = D / 8;  // lanes of a head row
   pdl_launch_dependents();    // a decode after this append may be scheduled now
   const int Hq = a.num_q_heads, Hkv = a.num_kv_heads;

@@ -151,7 +151,7 @@ __device__ __forceinline__ u64 segment_sum(const VfRow& row, int lo, int hi, int
     for (int v0 = lo + lane * 4; v0 < hi; v0 += kRun / 4 * 128) {
       Limbs s = {0, 0, 0};
       const int stop = min(hi, v0 + kRun / 4 * 128);
-#pragma unroll 4
+#pragma unroll 2
       for (int v = v0; v < stop; v += 128) {
         float p[4], q[4];
         load4<kVec, kQ>(row, v, hi, p, q);

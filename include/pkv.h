@@ -738,7 +738,8 @@ pkv_status pkv_qk_norm_rope_append(
  *                  a row of p without any mass.
  * A sequence whose range descends, is longer than max_draft or passes num_rows
  * sets PKV_DEVERR_LENGTH and counts as one without rows.
- * Sums are exact and the result does not depend on the launch.  num_seqs <= 65535. */
+ * Sums are exact and the result does not depend on the launch.  num_seqs <= 65535;
+ * vocab <= 2^30. */
 pkv_status pkv_draft_verify(const float* target_probs, int64_t target_stride,
                             const float* draft_probs, int64_t draft_stride, int32_t vocab,
                             const int32_t* draft_tokens, const int32_t* draft_ptr,

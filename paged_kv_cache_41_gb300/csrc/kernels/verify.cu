@@ -179,14 +179,17 @@ __device__ __forceinline__ u64 segment_sum(const VfRow& row, int lo, int hi, int
 
 // First element of [lo, hi) whose running sum passes `want`, the tokens of
 // `out` (n of them) counting nothing; hi - 1 if none does.  A warp.
-template <bool kVec, bool kQ, bool kOne>
+template <bool kVec>
 __device__ __forceinline__ int segment_find(const VfRow& row, int lo, int hi, int lane, u64 want,
                                             const int* out, int n) {
   u64 before = 0;
   for (int v0 = lo; v0 < hi; v0 += 128) {
     const int v = v0 + lane * 4;
     u64 w[4];
-    weights4<kVec, kQ, kOne>(row, v, hi, w);
+    if (row.q)  // c = 1 like any other: one copy of the code
+      weights4<kVec, true, false>(row, v, hi, w);
+    else
+      weights4<kVec, false, true>(row, v, hi, w);
     for (int k = 0; k < n; ++k) {
       const int d = out[k] - v;
 #pragma unroll
@@ -428,13 +431,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) draft_verify_kernel(const Verif
         to = min(from + sub, to);
       }
       if (warp == 0) {
-        int v;
-        if (!row.q)
-          v = segment_find<kVec, false, true>(row, from, to, lane, left, s_out, taken_out);
-        else if (row.c == one)
-          v = segment_find<kVec, true, true>(row, from, to, lane, left, s_out, 0);
-        else
-          v = segment_find<kVec, true, false>(row, from, to, lane, left, s_out, 0);
+        const int v = segment_find<kVec>(row, from, to, lane, left, s_out, taken_out);
         if (lane == 0) a.next_tokens[r] = max(v, 0);
       }
     }

@@ -523,11 +523,12 @@ size_t pkv_decode_workspace_bytes(const pkv_cache_desc* cache, int32_t num_seqs,
 
 namespace {
 
-// CTAs of a decode, and the parts of a segment where it takes the direct split
-// of a window (0: the balanced one).
+// CTAs of a decode, the parts of a segment where it takes the direct split of
+// a window (0: the balanced one), and the CTAs that leave records to merge.
 struct DecodeSplit {
   int64_t ctas;
   int32_t parts;
+  int64_t recording;
 };
 
 // Rows up to which a window takes the direct split, where its segments alone
@@ -543,7 +544,10 @@ constexpr int64_t kDirectPartRows = 2200;
 
 DecodeSplit decode_split(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
                          int32_t max_blocks, int32_t partition_size, int32_t window, int32_t num_sinks) {
-  if (window <= 0) return {decode_ctas(c, num_seqs, num_q_heads, max_blocks, partition_size), 0};
+  if (window <= 0) {
+    const int64_t C = decode_ctas(c, num_seqs, num_q_heads, max_blocks, partition_size);
+    return {C, 0, C};
+  }
   const int G = num_q_heads / c->num_kv_heads;
   // dense rows of a sequence at most: whole boxes of the sinks and, the window
   // beginning anywhere in one, of the window
@@ -557,10 +561,12 @@ DecodeSplit decode_split(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_
     const int64_t segs = (int64_t)num_seqs * c->num_kv_heads;
     const int64_t stages = (rows + pkv::kStageRows - 1) / pkv::kStageRows;
     const int64_t parts = std::max<int64_t>(std::min(resident / segs, stages), 1);  // one wave
-    if (rows <= (parts > 1 ? kDirectPartRows : kDirectRows)) return {segs * parts, (int32_t)parts};
+    if (rows <= (parts > 1 ? kDirectPartRows : kDirectRows))
+      return {segs * parts, (int32_t)parts, parts > 1 ? segs * parts : 0};
   }
   const int64_t blocks = (rows + c->block_size - 1) / c->block_size;
-  return {decode_ctas(c, num_seqs, num_q_heads, (int32_t)blocks, 0), 0};
+  const int64_t C = decode_ctas(c, num_seqs, num_q_heads, (int32_t)blocks, 0);
+  return {C, 0, C};
 }
 
 // The paged decode; with `scores` it also leaves every row's base-2 scores
@@ -587,7 +593,7 @@ pkv_status decode_checked(const pkv_cache_desc* cache, void* out, float* lse, co
                                          partition_size, window, num_sinks);
   const int64_t C = split.ctas;
   if (C > INT32_MAX) return PKV_ERR_UNSUPPORTED;
-  const DecodeWorkspace w = decode_workspace(num_seqs, C, G, cache->head_dim);
+  const DecodeWorkspace w = decode_workspace(num_seqs, split.recording, G, cache->head_dim);
   if (workspace_bytes < w.total || !workspace || (reinterpret_cast<uintptr_t>(workspace) & 255u))
     return PKV_ERR_INVALID_ARG;
 
@@ -646,7 +652,8 @@ size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* cache, int32_t nu
     return 0;
   const DecodeSplit split = decode_split(cache, num_seqs, num_q_heads, max_blocks_per_seq, 0, window,
                                          num_sinks);
-  return decode_workspace(num_seqs, split.ctas, num_q_heads / cache->num_kv_heads, cache->head_dim).total;
+  return decode_workspace(num_seqs, split.recording, num_q_heads / cache->num_kv_heads, cache->head_dim)
+      .total;
 }
 
 pkv_status pkv_paged_attention_decode_window(
@@ -1356,7 +1363,7 @@ pkv_status pkv_draft_verify(const float* target_probs, int64_t target_stride,
       target_stride < vocab || (draft_probs && draft_stride < vocab))
     return PKV_ERR_INVALID_ARG;
   if (num_seqs == 0) return PKV_OK;
-  if (num_seqs > 65535) return PKV_ERR_UNSUPPORTED;
+  if (num_seqs > 65535 || vocab > (1 << 30)) return PKV_ERR_UNSUPPORTED;
   if (!draft_ptr || !keep || !keep_lens || !next_tokens ||
       (num_rows > 0 && (!target_probs || !draft_tokens || !uniforms)))
     return PKV_ERR_INVALID_ARG;

@@ -108,7 +108,7 @@ def verify(lib, p=A, ps=100, q=A, qs=100, vocab=100, tok=A, ptr=A, masks=A, u=A,
     (dict(p=None), BAD), (dict(tok=None), BAD), (dict(ptr=None), BAD), (dict(u=None), BAD), (dict(keep=None), BAD),
     (dict(kl=None), BAD), (dict(nxt=None), BAD), (dict(ps=99), BAD), (dict(qs=99), BAD), (dict(vocab=0), BAD),
     (dict(b=-1), BAD), (dict(rows=-1), BAD), (dict(n=0), BAD), (dict(n=65), BAD), (dict(b=65536), UNSUP),
-    (dict(b=0), 0)])
+    (dict(vocab=2**30 + 1, ps=2**31, qs=2**31), UNSUP), (dict(b=0), 0)])
 def test_verify_arguments(lib, kw, want):
     assert verify(lib, **kw) == want
 

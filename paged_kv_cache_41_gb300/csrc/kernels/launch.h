@@ -441,6 +441,7 @@ struct RopeArgs {
   int32_t block_size;
   int32_t rot;                  // elements of a head that are rotated
   int32_t axes;
+  int32_t ahead;                // tokens whose rows go into L2 ahead of their turn (the launcher sets it)
   float eps;
   uint32_t uniform;             // bit i: pairs 4 i .. 4 i + 3 are on one axis
   uint8_t axis_of[64];          // the axis of each pair

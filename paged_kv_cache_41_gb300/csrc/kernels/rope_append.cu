@@ -31,8 +31,7 @@ namespace {
 
 constexpr int kRopeThreads = 128;
 // Bytes of q, k and v between a token and the one that its first group asks into
-// L2: about what the resident groups have in hand.  A load that finds its line in
-// L2 waits a third as long, and there were not warps enough to cover DRAM's
+// L2: about what the resident groups have in hand.  There are not warps enough to cover DRAM's
 // latency twice (positions, then angles): 32768 tokens (12 KiB each) take 138 us
 // without, 124.2 / 123.0 / 123.4 / 125.4 with 300 / 600 / 1000 / 1500 of them
 // between, 166 with 3000.

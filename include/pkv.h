@@ -58,8 +58,9 @@
  *     and Hq / Hkv <= 4, on the tensor cores (tiles widened to bf16 in shared
  *     memory) for head_dim 128 and Hq / Hkv = 8 with block_size 16, 32, 64,
  *     128 or 256; other group sizes return PKV_ERR_UNSUPPORTED.  The
- *     decode that weighs rows goes with the decode; the attention of drafted
- *     tokens and the compaction take them in every shape.  The
+ *     decode that weighs rows and the one under a window go with the decode; the
+ *     attention of drafted tokens, the compaction and the append that normalises and
+ *     rotates take them in every shape.  The
  *     shared-prefix kernel and the chunk-first phase take bf16 only (a tree
  *     over MXFP8 pools runs sequence-first).
  *   - Pointers to the caches, q, k, v and out must be 16-byte aligned.

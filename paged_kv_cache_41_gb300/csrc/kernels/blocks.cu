@@ -394,6 +394,9 @@ __global__ void __launch_bounds__(kThreads) blocks_update_kernel(const BlocksArg
     }
   }
   if (t == 0) a.count_out[0] = (int32_t)(avail - used);
+  // The decodes read tables and lengths before they wait for the kernel in
+  // front of them to be complete, so these are visible before this one ends.
+  __threadfence();
   if (!own_rows) return;
   if (single) {
     for (int64_t i = t; i < a.num_rows; i += kThreads) {

@@ -187,6 +187,12 @@ def test_rows_that_are_not_distributions_stay_in_the_vocabulary():
             assert ((nxt >= -1) & (nxt < vocab)).all() and ((lens >= 1) & (lens <= 6)).all()
             if bad not in (2.0 ** -80, 1e-45):
                 v.check((keep, lens, nxt))
+    v = Verify([6, 6], 300, seed=4)   # sums far past what is held exactly
+    v.p[:], v.q[:] = 1.0, 0.0
+    for vocab_rows in (v, Verify([6, 6], 300, sampled=False, seed=4)):
+        vocab_rows.p[:] = 1.0
+        keep, lens, nxt = vocab_rows.call()
+        assert ((nxt >= -1) & (nxt < 300)).all() and ((lens >= 1) & (lens <= 6)).all()
     assert pkv.get_device_error() == 0
 
 

@@ -531,16 +531,24 @@ struct DecodeSplit {
   int64_t recording;
 };
 
-// Rows up to which a window takes the direct split, where its segments alone
-// come near to filling the GPU, and where each is cut into parts.  Measured in us, bf16, block size
-// 16, direct / balanced (eight query heads per kv head: / the tensor cores):
-//   whole segments: 64 x 8 of them, 4 heads: window 128 11.5 / 20.3, 512 32.7 / 40.8,
-//   1024 58.3 / 59.1, 2000 106.7 / 93.7; 256 x 8: 128 43.1 / 51.4, 512 102.4 / 107.0,
-//   2000 233.3 / 213.3; 64 x 8, 8 heads: 128 21.2 / 38.5, 500 56.7 / 61.5, 1024 105.2 / 76.2;
-//   in parts: 8 x 8, 4 heads: 128 8.6 / 12.8, 1024 15.0 / 18.7, 2000 21.7 / 24.0,
-//   4096 33.8 / 31.2; 4 x 8, 8 heads: 128 8.8 / 15.1, 1024 15.7 / 20.3, 2000 20.2 / 21.4.
-constexpr int64_t kDirectRows = 600;
-constexpr int64_t kDirectPartRows = 2200;
+// Which windows take the direct split.  Its CTAs cost no plan and no merge, but
+// the last wave's idle places cost what a segment does: it wins where those,
+// shared out over a wave, come to no more rows than the balanced split's fixed cost is
+// worth.  Measured in us, block size 16, head_dim 128, direct / balanced:
+//   bf16 32/8 heads, 512 segments on 608 places: window 128 11.5 / 20.3, 512 32.7 /
+//   40.8, 1024 58.3 / 59.1, 2000 106.7 / 93.7; 2048 segments: 128 43.1 / 51.4, 512
+//   102.4 / 107.0, 2000 233.3 / 213.3; 8/8 heads, 2400 segments: 1024 192.5 / 215.3;
+//   MXFP8, 512 segments: 128 12.3 / 19.6, 1024 69.7 / 70.7; fp32, 512 on 304 places:
+//   128 21.6 / 24.5, 512 61.1 / 54.6, 1024 113.4 / 94.9; bf16 64/8 heads of 64: 128
+//   15.9 / 19.7, 512 44.1 / 39.6.
+constexpr int64_t kDirectIdleRows = 170;
+// With eight query heads per kv head, against the tensor cores: 512 segments,
+// window 128 21.2 / 38.5, 256 34.2 / 50.1, 500 56.7 / 61.5, 1024 105.2 / 76.2.
+constexpr int64_t kDirectTcRows = 600;
+// And where segments are cut into parts: 8 x 8 segments, 128 8.6 / 12.8, 1024 15.0 /
+// 18.7, 2000 21.7 / 24.0, 4096 33.8 / 31.2; 4 x 8, 8 heads: 128 8.8 / 15.1, 1024 15.7
+// / 20.3, 2000 20.2 / 21.4.
+constexpr int64_t kDirectRows = 2200;
 
 DecodeSplit decode_split(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
                          int32_t max_blocks, int32_t partition_size, int32_t window, int32_t num_sinks) {
@@ -561,8 +569,11 @@ DecodeSplit decode_split(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_
     const int64_t segs = (int64_t)num_seqs * c->num_kv_heads;
     const int64_t stages = (rows + pkv::kStageRows - 1) / pkv::kStageRows;
     const int64_t parts = std::max<int64_t>(std::min(resident / segs, stages), 1);  // one wave
-    if (rows <= (parts > 1 ? kDirectPartRows : kDirectRows))
-      return {segs * parts, (int32_t)parts, parts > 1 ? segs * parts : 0};
+    const int64_t places = (segs + resident - 1) / resident * resident;
+    bool direct = rows <= kDirectRows;
+    if (parts == 1)
+      direct = direct && (tc ? rows <= kDirectTcRows : (places - segs) * rows <= kDirectIdleRows * resident);
+    if (direct) return {segs * parts, (int32_t)parts, parts > 1 ? segs * parts : 0};
   }
   const int64_t blocks = (rows + c->block_size - 1) / c->block_size;
   const int64_t C = decode_ctas(c, num_seqs, num_q_heads, (int32_t)blocks, 0);

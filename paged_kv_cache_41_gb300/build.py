@@ -30,6 +30,7 @@ CUDA_SOURCES = [
     "kernels/decode.cu",
     "kernels/decode_scores.cu",
     "kernels/decode_window.cu",
+    "kernels/window_mma.cu",
     "kernels/decode_tc.cu",
     "kernels/decode_tc_mx.cu",
     "kernels/prefix_tc.cu",
@@ -47,6 +48,7 @@ PER_SOURCE_FLAGS = {
     "kernels/decode.cu": ["--use_fast_math"],
     "kernels/decode_scores.cu": ["--use_fast_math"],
     "kernels/decode_window.cu": ["--use_fast_math"],
+    "kernels/window_mma.cu": ["--use_fast_math"],
     "kernels/decode_tc.cu": ["--use_fast_math"],
     "kernels/decode_tc_mx.cu": ["--use_fast_math"],
     "kernels/prefix_tc.cu": ["--use_fast_math"],

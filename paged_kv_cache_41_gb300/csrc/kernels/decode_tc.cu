@@ -75,12 +75,11 @@ constexpr int kStart = 1, kEnd = 2, kWholeSeg = 4, kSlotOne = 8;
 
 }  // namespace
 
-template <int G, bool kScores = false, bool kWin = false>
+template <int G, bool kScores = false>
 __global__ void __launch_bounds__(kTcThreads, 1)
     decode_tc_kernel(const __grid_constant__ CUtensorMap tmk,
                      const __grid_constant__ CUtensorMap tmv,
-                     const __grid_constant__ CUtensorMap tmq, const DecodeArgsOf<kWin> a) {
-  static_assert(!(kScores && kWin), "the descriptor's flags hold one of the two");
+                     const __grid_constant__ CUtensorMap tmq, const DecodeArgs a) {
   static_assert(G <= kTcN, "at most 16 query heads per kv head");
   constexpr uint32_t kIdQK = tc::idesc_bf16_f32(kTcRows, kTcN, 0, 0);
   constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kTcD, kTcN, 1, 0);
@@ -162,16 +161,16 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       prefetch_tensormap(&tmq);
     }
     int r = d0.x, h = d0.y, i = d0.z;
-    SegRows seg = seg_rows(a, r);
-    int nt = (seg.len + kTcRows - 1) / kTcRows;
+    int len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, P, a.err, false);
+    int nt = (len + kTcRows - 1) / kTcRows;
     while (i >= nt) {  // the plan may name a segment's end: its next non-empty one
       i -= nt;
       if (++h == Hkv) {
         h = 0;
         do {
           ++r;
-          seg = seg_rows(a, r);
-          nt = (seg.len + kTcRows - 1) / kTcRows;
+          len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, P, a.err, false);
+          nt = (len + kTcRows - 1) / kTcRows;
         } while (nt == 0);
       }
     }
@@ -179,14 +178,13 @@ __global__ void __launch_bounds__(kTcThreads, 1)
     // sequence r (0 where the lane has no box), loaded one stage ahead: the
     // table read then overlaps the wait for a free slot
     const int j = lane & 15;
-    auto box_block = [&](int r_, int i_, SegRows seg_) -> int {
-      const StageRows sr_ = stage_rows<kTcRows>(a, seg_, i_);
-      const int row = sr_.row(j * TB);
-      return j * TB < sr_.nvalid
+    auto box_block = [&](int r_, int i_, int len_) -> int {
+      const int row = i_ * kTcRows + j * TB;
+      return row < len_ && j * TB < kTcRows
                  ? __ldg(a.block_tables + (int64_t)r_ * a.max_blocks + row / P)
                  : 0;
     };
-    int blk_next = box_block(r, i, seg);
+    int blk_next = box_block(r, i, len);
     if (a.plan_before_wait) pdl_wait();  // the K/V rows and q are read from here on
     int pieces = 0;
     // the previous stage's V boxes: this lane's block and first row, the box
@@ -226,8 +224,8 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           break;
         }
       }
-      const StageRows sr = stage_rows<kTcRows>(a, seg, i);
-      const int nvalid = sr.nvalid;
+      const int t0 = i * kTcRows;
+      const int nvalid = min(kTcRows, len - t0);
       const int dseg = k - i;  // CTA stage index of the segment's first stage
       const bool start = k == 0 || i == 0;
       const bool end = k == n - 1 || i == nt - 1;
@@ -235,10 +233,9 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       const int qb = (pieces - 1) % kQBufs;
       const int flags = (start ? kStart : 0) | (end ? kEnd : 0) |
                         (end && i == nt - 1 && dseg >= 0 ? kWholeSeg : 0) |
-                        (dseg > 0 ? kSlotOne : 0) | (qb << 4) |
-                        (kScores ? i << 6 : kWin ? (sr.hide_lo << 8) | (sr.hide_hi << 16) : 0);
+                        (dseg > 0 ? kSlotOne : 0) | (qb << 4) | (kScores ? i << 6 : 0);
       const int nbox = (nvalid + TB - 1) / TB;  // per tensor
-      int brow = sr.row(j * TB) % P;
+      int brow = (t0 + j * TB) % P;
       const bool bad = j < nbox && (blk < 0 || (int64_t)blk >= a.num_blocks);
       if (__any_sync(0xffffffffu, bad) && lane == 0) atomicOr(a.err, PKV_DEVERR_BLOCK);
       if (bad) {
@@ -274,12 +271,12 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           h = 0;
           do {
             ++r;
-            seg = seg_rows(a, r);
-            nt = (seg.len + kTcRows - 1) / kTcRows;
+            len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, P, a.err, false);
+            nt = (len + kTcRows - 1) / kTcRows;
           } while (nt == 0);
         }
       }
-      if (k + 1 < n) blk_next = box_block(r, i, seg);
+      if (k + 1 < n) blk_next = box_block(r, i, len);
     }
     if (v_ok) issue_v(n - 1);
   } else if (warp == 1) {
@@ -375,8 +372,6 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       tc::fence_after_sync();
       const int4 dsc = sdesc[s];
       const int nvalid = dsc.z, flags = dsc.w;
-      const int hide_lo = kWin ? (flags >> 8) & 255 : 0, hide_hi = kWin ? flags >> 16 : 0;
-      const bool seen = row_seen(row, nvalid, hide_lo, hide_hi);  // this thread's key row
       if (flags & kStart) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -401,7 +396,7 @@ __global__ void __launch_bounds__(kTcThreads, 1)
       bool pass = false;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        sg[g] = seen ? __uint_as_float(v[g]) * cs : -INFINITY;
+        sg[g] = row < nvalid ? __uint_as_float(v[g]) * cs : -INFINITY;
         pass |= sg[g] > m[g] + 8.0f;
       }
       if constexpr (kScores) {  // stage flags >> 6 of its segment
@@ -484,14 +479,14 @@ __global__ void __launch_bounds__(kTcThreads, 1)
           *reinterpret_cast<__nv_bfloat16*>(at + kQBytes) = lo;
         }
       }
-      // zero the rows of V that are not seen (weight 0, bytes maybe NaN), once
+      // zero the rows of V past the tail (weight 0, bytes maybe NaN), once
       // the stage's V has landed
-      if ((nvalid < kTcRows || hide_hi > 0) &&
+      if (nvalid < kTcRows &&
           !__all_sync(0xffffffffu, mbar_wait(&vfull[s], (k / kTcStages) & 1))) {
         if (lane == 0) atomicOr(a.err, PKV_DEVERR_TIMEOUT);
         break;
       }
-      if (!seen) {
+      if (row >= nvalid) {
         unsigned char* vrow = ring + (size_t)s * 2 * kTcTile + kTcTile +
                               (row / kRowGroup) * kTcGroup + (row % kRowGroup) * 128;
 #pragma unroll
@@ -594,16 +589,6 @@ int decode_tc_resident_ctas() {
 cudaError_t launch_paged_decode_tc(const CUtensorMap& tmk, const CUtensorMap& tmv,
                                    const CUtensorMap& tmq, const DecodeArgs& a,
                                    cudaStream_t stream) {
-  if (a.window) {
-    auto kern = decode_tc_kernel<8, false, true>;
-    static SmemAttrCache window_cache;
-    cudaError_t e = ensure_smem_limit(kern, kTcSmem, window_cache);
-    if (e != cudaSuccess) return e;
-    e = launch_pdl(kern, dim3((unsigned)a.num_ctas), dim3(kTcThreads), kTcSmem, stream, tmk, tmv, tmq,
-                   WindowArgs(a, a.block_size < kTcRows ? a.block_size : kTcRows));
-    if (e != cudaSuccess) return e;
-    return launch_decode_reduce(PKV_BF16, kTcD, a, stream);
-  }
   auto kern = a.scores ? decode_tc_kernel<8, true> : decode_tc_kernel<8>;
   static SmemAttrCache attr_cache[2];
   cudaError_t e = ensure_smem_limit(kern, kTcSmem, attr_cache[a.scores ? 1 : 0]);

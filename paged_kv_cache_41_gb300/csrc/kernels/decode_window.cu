@@ -1,5 +1,7 @@
 // decode_window.cu -- the decode under a sliding window with sinks on the CUDA
-// cores: of T rows the first S and the last W are seen.
+// cores, over fp32 pools and MXFP8 ones of up to four query heads per kv head: of T
+// rows the first S and the last W are seen.  (bf16 pools: window_mma.cu; eight heads over
+// MXFP8: decode_tc_mx.cu.)
 //
 // The work split and the walk count only boxes that hold a row that is seen
 // (plan.cuh); boxes without one are not loaded, so their blocks may have been given
@@ -8,7 +10,7 @@
 //     of the lengths, pieces cut anywhere and the plain decode's reduction;
 //   * direct, for short ones, where no sequence shows many rows: a CTA takes
 //     an equal part of one segment's stages and asks nothing but its length.  There is no
-//     scan, and where segments alone fill the GPU no reduction either: a CTA writes its segment.
+//     scan, and where segments alone fill the GPU no merge either: a CTA writes its segment.
 // A file of its own: it compiles beside decode.cu.
 #include "decode_partial.cuh"
 
@@ -89,13 +91,21 @@ cudaError_t launch_dim(int dtype, int group, const CUtensorMap& tmk, const CUten
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess || a.parts == 1) return e;
-  if (!a.parts) return launch_decode_reduce(dtype, D, a, stream);
+  return a.parts ? launch_window_merge(dtype, D, a, stream) : launch_decode_reduce(dtype, D, a, stream);
+}
+
+template <typename T>
+cudaError_t merge(int head_dim, const WindowArgs& a, cudaStream_t stream) {
   const int64_t rows = (int64_t)a.num_seqs * a.num_q_heads;
-  return launch_pdl(window_merge_kernel<typename IoOf<T>::type, D>, dim3((unsigned)((rows + 3) / 4)),
-                    dim3(128), 0, stream, a);
+  return launch_pdl(head_dim == 128 ? window_merge_kernel<T, 128> : window_merge_kernel<T, 64>,
+                    dim3((unsigned)((rows + 3) / 4)), dim3(128), 0, stream, a);
 }
 
 }  // namespace
+
+cudaError_t launch_window_merge(int dtype, int head_dim, const WindowArgs& a, cudaStream_t stream) {
+  return dtype == PKV_F32 ? merge<float>(head_dim, a, stream) : merge<__nv_bfloat16>(head_dim, a, stream);
+}
 
 cudaError_t launch_decode_window(int dtype, int head_dim, int group, const CUtensorMap& tmk,
                                  const CUtensorMap& tmv, const DecodeArgs& args, cudaStream_t stream) {
@@ -103,9 +113,6 @@ cudaError_t launch_decode_window(int dtype, int head_dim, int group, const CUten
   if (dtype == PKV_MXFP8)
     return head_dim == 128 ? launch_dim<__nv_fp8_e4m3, 128>(dtype, group, tmk, tmv, a, stream)
                            : launch_dim<__nv_fp8_e4m3, 64>(dtype, group, tmk, tmv, a, stream);
-  if (dtype == PKV_BF16)
-    return head_dim == 128 ? launch_dim<__nv_bfloat16, 128>(dtype, group, tmk, tmv, a, stream)
-                           : launch_dim<__nv_bfloat16, 64>(dtype, group, tmk, tmv, a, stream);
   return head_dim == 128 ? launch_dim<float, 128>(dtype, group, tmk, tmv, a, stream)
                          : launch_dim<float, 64>(dtype, group, tmk, tmv, a, stream);
 }

@@ -129,7 +129,7 @@ struct DecodeArgs {
   int32_t window;
   int32_t num_sinks;
   // Under a window, 0: the balanced split of plan.cuh; n: CTA c takes the (c %
-  // n)-th n-th of the stages of segment c / n, on the CUDA cores.
+  // n)-th n-th of the stages of segment c / n.
   int32_t parts;
 };
 
@@ -160,6 +160,15 @@ cudaError_t launch_decode_partial_scores(int dtype, int head_dim, int group, con
 cudaError_t launch_decode_window(int dtype, int head_dim, int group, const CUtensorMap& tmk,
                                          const CUtensorMap& tmv, const DecodeArgs& args,
                                          cudaStream_t stream);
+
+// Its merge of parts (args.parts > 1), by itself.
+cudaError_t launch_window_merge(int dtype, int head_dim, const WindowArgs& args, cudaStream_t stream);
+
+// The direct split over bf16 pools on matrix instructions (window_mma.cu), merge
+// included: tmk / tmv are row-group maps whose box is box_rows_for(P) rows.
+cudaError_t launch_window_mma(int head_dim, int group, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                              const DecodeArgs& args, cudaStream_t stream);
+int window_mma_resident_ctas(int head_dim, int group);
 
 // CTAs of one wave of the partial kernel (resident CTAs per SM x SMs).
 int decode_resident_ctas(int dtype, int head_dim, int group);

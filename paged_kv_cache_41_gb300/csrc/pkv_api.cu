@@ -253,6 +253,13 @@ pkv_status launch_decode(const pkv_cache_desc* cache, int G, const void* q, cons
   }
   a.stage_units = tc ? 1 : 2;
   a.piece_units = tc ? 0 : 3;
+  if (a.parts && cache->dtype == PKV_BF16) {
+    const int rows = pkv::box_rows_for(cache->block_size);
+    if ((st = encode_cache_map_rg(&tmk, cache, k_cache, rows)) != PKV_OK) return st;
+    if ((st = encode_cache_map_rg(&tmv, cache, v_cache, rows)) != PKV_OK) return st;
+    e = pkv::launch_window_mma(cache->head_dim, G, tmk, tmv, a, stream);
+    return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
+  }
   if (tc) {
     const int rows = cache->block_size < pkv::decode_tc_rows() ? cache->block_size
                                                                : pkv::decode_tc_rows();
@@ -531,23 +538,19 @@ struct DecodeSplit {
   int64_t recording;
 };
 
-// Which windows take the direct split.  Its CTAs cost no plan and no merge, but
-// the last wave's idle places cost what a segment does: it wins where those,
-// shared out over a wave, come to no more rows than the balanced split's fixed cost is
-// worth.  Measured in us, block size 16, head_dim 128, direct / balanced:
-//   bf16 32/8 heads, 512 segments on 608 places: window 128 11.5 / 20.3, 512 32.7 /
-//   40.8, 1024 58.3 / 59.1, 2000 106.7 / 93.7; 2048 segments: 128 43.1 / 51.4, 512
-//   102.4 / 107.0, 2000 233.3 / 213.3; 8/8 heads, 2400 segments: 1024 192.5 / 215.3;
-//   MXFP8, 512 segments: 128 12.3 / 19.6, 1024 69.7 / 70.7; fp32, 512 on 304 places:
-//   128 21.6 / 24.5, 512 61.1 / 54.6, 1024 113.4 / 94.9; bf16 64/8 heads of 64: 128
-//   15.9 / 19.7, 512 44.1 / 39.6.
+// Over bf16 pools every window takes the direct split (window_mma.cu): parts
+// enough for one wave, and of no more rows than this, so that one long sequence
+// among short ones is not one CTA's.  Parts of 2048 rows / segments whole where they
+// fill a wave: 64 x 8192 rows, window 4096 163 / 154 us; one sequence of 65536 rows beside 63
+// of 256, window 4096 48 / 85, 65536 101 / 1202 (parts of 1024 rows 117, 4096 127).
+constexpr int64_t kPartRows = 2048;
+// Over the others the direct split wins where its last wave's idle places, shared
+// out over a wave, come to no more rows than the balanced split's plan and merge are
+// worth.  Measured in us, block size 16, head_dim 128, 32/8 heads, direct / balanced:
+//   MXFP8, 512 segments on 608 places: window 128 12.3 / 19.6, 512 37.3 / 42.2, 1024
+//   69.7 / 70.7; 128 segments, in parts: 128 11.8 / 14.3, 1024 25.6 / 26.0; fp32, 512 on 304
+//   places: 128 21.6 / 24.5, 512 61.1 / 54.6, 1024 113.4 / 94.9.
 constexpr int64_t kDirectIdleRows = 170;
-// With eight query heads per kv head, against the tensor cores: 512 segments,
-// window 128 21.2 / 38.5, 256 34.2 / 50.1, 500 56.7 / 61.5, 1024 105.2 / 76.2.
-constexpr int64_t kDirectTcRows = 600;
-// And where segments are cut into parts: 8 x 8 segments, 128 8.6 / 12.8, 1024 15.0 /
-// 18.7, 2000 21.7 / 24.0, 4096 33.8 / 31.2; 4 x 8, 8 heads: 128 8.8 / 15.1, 1024 15.7
-// / 20.3, 2000 20.2 / 21.4.
 constexpr int64_t kDirectRows = 2200;
 
 DecodeSplit decode_split(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_q_heads,
@@ -562,18 +565,24 @@ DecodeSplit decode_split(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_
   const int64_t B = c->block_size < pkv::decode_tc_rows() ? c->block_size : pkv::decode_tc_rows();
   const int64_t seen = ((int64_t)num_sinks + B - 1) / B * B + (int64_t)window + B;
   const int64_t rows = std::min(seen, (int64_t)max_blocks * c->block_size);
-  const bool tc = use_tc_decode(c, G);
-  if (!(tc && c->dtype == PKV_MXFP8)) {  // eight heads over MXFP8: the tensor cores only
+  const int64_t segs = (int64_t)num_seqs * c->num_kv_heads;
+  const int64_t stages = (rows + pkv::kStageRows - 1) / pkv::kStageRows;
+  auto direct = [&](int64_t parts) {
+    return DecodeSplit{segs * parts, (int32_t)parts, parts > 1 ? segs * parts : 0};
+  };
+  if (c->dtype == PKV_BF16) {
+    int64_t resident = pkv::window_mma_resident_ctas(c->head_dim, G);
+    if (resident <= 0) resident = 4LL * sm_count();
+    const int64_t wave = resident / segs, cut = (rows + kPartRows - 1) / kPartRows;
+    return direct(std::max<int64_t>(std::min(std::max(wave, cut), stages), 1));
+  }
+  if (!use_tc_decode(c, G)) {  // eight heads over MXFP8: the tensor cores only
     int64_t resident = pkv::decode_resident_ctas(c->dtype, c->head_dim, G);
     if (resident <= 0) resident = 2LL * sm_count();
-    const int64_t segs = (int64_t)num_seqs * c->num_kv_heads;
-    const int64_t stages = (rows + pkv::kStageRows - 1) / pkv::kStageRows;
     const int64_t parts = std::max<int64_t>(std::min(resident / segs, stages), 1);  // one wave
     const int64_t places = (segs + resident - 1) / resident * resident;
-    bool direct = rows <= kDirectRows;
-    if (parts == 1)
-      direct = direct && (tc ? rows <= kDirectTcRows : (places - segs) * rows <= kDirectIdleRows * resident);
-    if (direct) return {segs * parts, (int32_t)parts, parts > 1 ? segs * parts : 0};
+    if (rows <= kDirectRows && (parts > 1 || (places - segs) * rows <= kDirectIdleRows * resident))
+      return direct(parts);
   }
   const int64_t blocks = (rows + c->block_size - 1) / c->block_size;
   const int64_t C = decode_ctas(c, num_seqs, num_q_heads, (int32_t)blocks, 0);

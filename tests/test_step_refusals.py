@@ -94,7 +94,10 @@ def test_window_workspace_size(lib):
     assert need > 0 and window(lib, wsb=need - 1) == BAD
     # a few rows seen of a long table ask for no more than a short table does
     assert size(c, 2, 4, 100000, 20, 4) == size(c, 2, 4, 8, 20, 4)
-    assert size(c, 2, 4, 100000, 2**31 - 1, 2**31 - 1) == lib.pkv_decode_workspace_bytes(c, 2, 4, 100000, 0)
+    # and a window over everything, where the plain decode's split is taken, what that does
+    f32 = ctypes.byref(desc(dtype=pkv.PKV_F32))
+    assert size(f32, 2, 4, 100000, 2**31 - 1, 2**31 - 1) == lib.pkv_decode_workspace_bytes(f32, 2, 4, 100000, 0)
+    assert size(c, 2, 4, 100000, 2**31 - 1, 2**31 - 1) > need
     for args in ((0, 4, 4, 20, 4), (2, 3, 4, 20, 4), (2, 4, 0, 20, 4), (2, 4, 4, 0, 4), (2, 4, 4, 20, -1)):
         assert size(c, *args) == 0
 

@@ -655,7 +655,9 @@ size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* cache, int32_t nu
  * T = seq_lens[r] rows, row t is seen where t < num_sinks or t >= T - window; out
  * and lse are over the rows that are seen.  Blocks without a seen row are not
  * read, and neither are their table entries' ids: they may be -1
- * (pkv_kv_blocks_update gives such blocks back).
+ * (pkv_kv_blocks_update gives such blocks back).  A NaN score of a row that is
+ * seen makes that head's out and lse NaN; rows whose scores are -infinity weigh
+ * nothing, and a head that sees no other has out 0 and lse -infinity.
  *   window:        >= 1: the newest row is always seen.
  *   num_sinks:     >= 0.
  *   workspace:     at least pkv_decode_window_workspace_bytes bytes, 256-byte

@@ -118,8 +118,9 @@ __global__ void __launch_bounds__(128) decode_reduce_kernel(const DecodeArgs a) 
     return i < n_st ? ext_o + (int64_t)i * D : a.rec_o + piece_rec(i - n_st) * D;
   };
   const float my0 = lane < n ? src_lse(lane) : -INFINITY;
-  float M = my0;
-  for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, src_lse(i));
+  auto top = [](float l) { return l != l ? INFINITY : l; };  // NaN (a window's) is not passed over
+  float M = top(my0);
+  for (int i = lane + 32; i < n; i += 32) M = fmaxf(M, top(src_lse(i)));
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float acc[EPL];
@@ -151,7 +152,7 @@ __global__ void __launch_bounds__(128) decode_reduce_kernel(const DecodeArgs a) 
       }
     }
   }
-  const bool nonempty = Lsum > 0.f;
+  const bool nonempty = a.window ? Lsum != 0.f : Lsum > 0.f;  // a window's NaN stays
   if (!a.out) {  // states only: the merged pieces become the segment's state
     const int64_t slot = rh * a.st_stride + a.st_slot;
     float* so = a.st_o + slot * D + lane * EPL;
@@ -255,7 +256,7 @@ cudaError_t launch_paged_decode(int dtype, int head_dim, int group, const CUtens
                                 const CUtensorMap& tmv, const DecodeArgs& a,
                                 cudaStream_t stream) {
   cudaError_t e;
-  if (a.window) return launch_decode_window(dtype, head_dim, group, tmk, tmv, a, stream);
+  if (a.window) return launch_decode_window(head_dim, group, tmk, tmv, a, stream);  // fp32
   if (a.scores)
     e = launch_decode_partial_scores(dtype, head_dim, group, tmk, tmv, a, stream);
   else if (dtype == PKV_MXFP8)

@@ -242,7 +242,7 @@ __device__ __forceinline__ void decode_chunk(const T* __restrict__ kt, const T* 
       for (int e = 0; e < EP2; ++e) acc[g][e] = __fmul2_rn(acc[g][e], al2);
     }
   }
-  const float p = (kTail && sc == -INFINITY) ? 0.f : exp2f(sc - m_used);
+  const float p = ((kTail || kWin) && sc == -INFINITY) ? 0.f : exp2f(sc - m_used);
   l_run += p;
   // ---- P . V for this half-warp's two rows
   float pg[2][G];
@@ -639,10 +639,11 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
         float Lsum = 0.f, o[EPT];
 #pragma unroll
         for (int i = 0; i < EPT; ++i) o[i] = 0.f;
-        if (M != -INFINITY) {
+        if (kWin || M != -INFINITY) {
+          const float base = M == -INFINITY ? 0.f : M;
 #pragma unroll
           for (int w = 0; w < kConsumerWarps; ++w) {
-            const float wt = exp2f(mm[w * G + g] - M);
+            const float wt = exp2f(mm[w * G + g] - base);
             Lsum = fmaf(wt, ml[w * G + g], Lsum);
             float x[EPT];
             if constexpr (EPT == 1)
@@ -653,7 +654,7 @@ __global__ void __launch_bounds__(kDecodeThreads, (G >= 8 ? 2 : 4))
             for (int i = 0; i < EPT; ++i) o[i] = fmaf(wt, x[i], o[i]);
           }
         }
-        const bool nonempty = Lsum > 0.f;
+        const bool nonempty = kWin ? Lsum != 0.f : Lsum > 0.f;  // a window's NaN stays
         const float inv = nonempty ? 1.f / Lsum : 0.f;
 #pragma unroll
         for (int i = 0; i < EPT; ++i) o[i] *= inv;

@@ -64,12 +64,11 @@ constexpr int kStart = 1, kEnd = 2, kWholeSeg = 4, kSlotOne = 8;
 
 }  // namespace
 
-template <int G, bool kScores = false, bool kWin = false>
+template <int G, bool kScores = false>
 __global__ void __launch_bounds__(kMxThreads, 1)
     decode_tc_mx_kernel(const __grid_constant__ CUtensorMap tmk,
                         const __grid_constant__ CUtensorMap tmv,
-                        const __grid_constant__ CUtensorMap tmq, const DecodeArgsOf<kWin> a) {
-  static_assert(!(kScores && kWin), "the descriptor's flags hold one of the two");
+                        const __grid_constant__ CUtensorMap tmq, const DecodeArgs a) {
   static_assert(G <= kMxN, "at most 16 query heads per kv head");
   constexpr uint32_t kIdQK = tc::idesc_bf16_f32(kMxRows, kMxN, 0, 0);
   constexpr uint32_t kIdPV = tc::idesc_bf16_f32(kMxD, kMxN, 1, 0);
@@ -149,16 +148,16 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       prefetch_tensormap(&tmq);
     }
     int r = d0.x, h = d0.y, i = d0.z;
-    SegRows seg = seg_rows(a, r);
-    int nt = (seg.len + kMxRows - 1) / kMxRows;
+    int len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, P, a.err, false);
+    int nt = (len + kMxRows - 1) / kMxRows;
     while (i >= nt) {  // the plan may name a segment's end: its next non-empty one
       i -= nt;
       if (++h == Hkv) {
         h = 0;
         do {
           ++r;
-          seg = seg_rows(a, r);
-          nt = (seg.len + kMxRows - 1) / kMxRows;
+          len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, P, a.err, false);
+          nt = (len + kMxRows - 1) / kMxRows;
         } while (nt == 0);
       }
     }
@@ -174,8 +173,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         }
         if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       }
-      const StageRows sr = stage_rows<kMxRows>(a, seg, i);
-      const int nvalid = sr.nvalid;
+      const int t0 = i * kMxRows;
+      const int nvalid = min(kMxRows, len - t0);
       const int dseg = k - i;  // CTA stage index of the segment's first stage
       const bool start = k == 0 || i == 0;
       const bool end = k == n - 1 || i == nt - 1;
@@ -183,12 +182,11 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       const int qb = (pieces - 1) % kQBufsMx;
       const int flags = (start ? kStart : 0) | (end ? kEnd : 0) |
                         (end && i == nt - 1 && dseg >= 0 ? kWholeSeg : 0) |
-                        (dseg > 0 ? kSlotOne : 0) | (qb << 4) |
-                        (kScores ? i << 6 : kWin ? (sr.hide_lo << 8) | (sr.hide_hi << 16) : 0);
+                        (dseg > 0 ? kSlotOne : 0) | (qb << 4) | (kScores ? i << 6 : 0);
       const int nbox = (nvalid + TB - 1) / TB;  // per tensor, <= 8
       int blk = 0, brow = 0;
       if (j < nbox) {
-        const int row = sr.row(j * TB);
+        const int row = t0 + j * TB;
         const int bi = row / P;
         brow = row - bi * P;
         blk = __ldg(a.block_tables + (int64_t)r * a.max_blocks + bi);
@@ -230,8 +228,8 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           h = 0;
           do {
             ++r;
-            seg = seg_rows(a, r);
-            nt = (seg.len + kMxRows - 1) / kMxRows;
+            len = effective_len(__ldg(a.seq_lens + r), a.max_blocks, P, a.err, false);
+            nt = (len + kMxRows - 1) / kMxRows;
           } while (nt == 0);
         }
       }
@@ -245,7 +243,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
     // bytes.  Each step a warp widens 4 rows x 8 columns: lane l takes row
     // (l / 8) and the column j = l % 8, so the 8 lanes of a row store to 8
     // bank groups, and odd rows take the other half first, so the 16 lanes of
-    // two rows load from 16 distinct bank pairs.  Rows that are not seen are
+    // two rows load from 16 distinct bank pairs.  Rows past the tail are
     // zeroed (their weight is 0, and 0 * NaN is not).
     constexpr int kRowsW = kMxRows / kWidenWarps;  // rows per warp
     const int wrow0 = (warp - 6) * kRowsW, rsub = lane >> 3, col = lane & 7;
@@ -256,7 +254,6 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         break;
       }
       const int4 dsc = sdesc_raw[s];
-      const int hide_lo = kWin ? (dsc.w >> 8) & 255 : 0, hide_hi = kWin ? dsc.w >> 16 : 0;
       const unsigned char* slot = raw + (size_t)s * kRawSlot;
       bool ok = true;
 #pragma unroll
@@ -274,7 +271,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
         // past 2^7 on any valid row of the warp takes the second multiply
         const int mrow = wrow0 + (lane < kRowsW ? lane : 0);
         const uint32_t scw = *reinterpret_cast<const uint32_t*>(scl + mrow * 4);
-        const bool big = __any_sync(0xffffffffu, lane < kRowsW && row_seen(mrow, dsc.z, hide_lo, hide_hi) &&
+        const bool big = __any_sync(0xffffffffu, lane < kRowsW && mrow < dsc.z &&
                                                      ((scw & 0xffu) > 134u || ((scw >> 8) & 0xffu) > 134u ||
                                                       ((scw >> 16) & 0xffu) > 134u || (scw >> 24) > 134u));
 #pragma unroll
@@ -284,7 +281,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
           const uint32_t sc = __shfl_sync(0xffffffffu, scw, rr);
           const int h = (it & 1) ^ (rsub & 1);
           unsigned char* d = dst + h * kBfHalf + row * 128 + col * 16;
-          if (row_seen(row, dsc.z, hide_lo, hide_hi)) {
+          if (row < dsc.z) {
             const int ch = h * 8 + (col ^ (row & 7));  // chunk of the row
             const uint2 w = *reinterpret_cast<const uint2*>(src + row * kMxD + ch * 8);
             __nv_bfloat162 f1, f2;
@@ -391,7 +388,6 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       tc::fence_after_sync();
       const int4 dsc = sdesc_bf[k & 3];
       const int nvalid = dsc.z, flags = dsc.w;
-      const bool seen = row_seen(row, nvalid, kWin ? (flags >> 8) & 255 : 0, kWin ? flags >> 16 : 0);
       if (flags & kStart) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -411,7 +407,7 @@ __global__ void __launch_bounds__(kMxThreads, 1)
       bool pass = false;
 #pragma unroll
       for (int g = 0; g < G; ++g) {
-        sg[g] = seen ? __uint_as_float(v[g]) * cs : -INFINITY;
+        sg[g] = row < nvalid ? __uint_as_float(v[g]) * cs : -INFINITY;
         pass |= sg[g] > m[g] + 8.0f;
       }
       if constexpr (kScores) {  // stage flags >> 6 of its segment
@@ -559,14 +555,6 @@ bool decode_tc_mx_supported(int dtype, int head_dim, int group, int block_size) 
 template <int G>
 static cudaError_t launch_mx_t(const CUtensorMap& tmk, const CUtensorMap& tmv,
                                const CUtensorMap& tmq, const DecodeArgs& a, cudaStream_t stream) {
-  if (a.window) {
-    auto kern = decode_tc_mx_kernel<G, false, true>;
-    static SmemAttrCache window_cache;
-    cudaError_t e = ensure_smem_limit(kern, kMxSmem, window_cache);
-    if (e != cudaSuccess) return e;
-    return launch_pdl(kern, dim3((unsigned)a.num_ctas), dim3(kMxThreads), kMxSmem, stream, tmk, tmv,
-                      tmq, WindowArgs(a, a.block_size < kMxRows ? a.block_size : kMxRows));
-  }
   auto kern = a.scores ? decode_tc_mx_kernel<G, true> : decode_tc_mx_kernel<G>;
   static SmemAttrCache attr_cache[2];
   cudaError_t e = ensure_smem_limit(kern, kMxSmem, attr_cache[a.scores ? 1 : 0]);

@@ -1,7 +1,6 @@
-// decode_window.cu -- the decode under a sliding window with sinks on the CUDA
-// cores, over fp32 pools and MXFP8 ones of up to four query heads per kv head: of T
-// rows the first S and the last W are seen.  (bf16 pools: window_mma.cu; eight heads over
-// MXFP8: decode_tc_mx.cu.)
+// decode_window.cu -- the decode of fp32 pools under a sliding window with sinks, on
+// the CUDA cores: of T rows the first S and the last W are seen.  (bf16 and MXFP8
+// pools: window_mma.cu.)
 //
 // The work split and the walk count only boxes that hold a row that is seen
 // (plan.cuh); boxes without one are not loaded, so their blocks may have been given
@@ -11,7 +10,8 @@
 //   * direct, for short ones, where no sequence shows many rows: a CTA takes
 //     an equal part of one segment's stages and asks nothing but its length.  There is no
 //     scan, and where segments alone fill the GPU no merge either: a CTA writes its segment.
-// A file of its own: it compiles beside decode.cu.
+// The merge of the direct split's parts serves window_mma.cu too.  A file of its
+// own: it compiles beside decode.cu.
 #include "decode_partial.cuh"
 
 namespace pkv {
@@ -36,7 +36,10 @@ __global__ void __launch_bounds__(128) window_merge_kernel(const WindowArgs a) {
   const int64_t cta = ((int64_t)r * a.num_kv_heads + qh / G) * a.parts;
   auto rec = [&](int i) { return 2 * (cta + i) * G + qh % G; };
   float M = -INFINITY;
-  for (int i = lane; i < n; i += 32) M = fmaxf(M, a.rec_lse[rec(i)]);
+  for (int i = lane; i < n; i += 32) {
+    const float l = a.rec_lse[rec(i)];
+    M = fmaxf(M, l != l ? INFINITY : l);  // NaN is not passed over
+  }
 #pragma unroll
   for (int o = 16; o >= 1; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
   float acc[EPL] = {}, sum = 0.f;
@@ -60,38 +63,33 @@ __global__ void __launch_bounds__(128) window_merge_kernel(const WindowArgs a) {
       }
     }
   }
-  const bool nonempty = sum > 0.f;
+  const bool nonempty = sum != 0.f;  // NaN stays
   T* out = static_cast<T*>(a.out) + rh * D + lane * EPL;
 #pragma unroll
   for (int e = 0; e < EPL; ++e) store_out(out + e, nonempty ? acc[e] / sum : 0.f);
   if (lane == 0 && a.lse_out) a.lse_out[rh] = nonempty ? (M + log2f(sum)) * kLn2 : -INFINITY;
 }
 
-template <typename T, int D, int G>
+template <int D, int G>
 cudaError_t launch_group(const CUtensorMap& tmk, const CUtensorMap& tmv, const WindowArgs& a,
                          cudaStream_t stream) {
-  return a.parts ? launch_partial<T, D, G, false, true, true>(tmk, tmv, a, stream)
-                 : launch_partial<T, D, G, false, true, false>(tmk, tmv, a, stream);
+  return a.parts ? launch_partial<float, D, G, false, true, true>(tmk, tmv, a, stream)
+                 : launch_partial<float, D, G, false, true, false>(tmk, tmv, a, stream);
 }
 
-template <typename T, int D>
-cudaError_t launch_dim(int dtype, int group, const CUtensorMap& tmk, const CUtensorMap& tmv,
-                       const WindowArgs& a, cudaStream_t stream) {
+template <int D>
+cudaError_t launch_dim(int group, const CUtensorMap& tmk, const CUtensorMap& tmv, const WindowArgs& a,
+                       cudaStream_t stream) {
   cudaError_t e;
   switch (group) {
-    case 1: e = launch_group<T, D, 1>(tmk, tmv, a, stream); break;
-    case 2: e = launch_group<T, D, 2>(tmk, tmv, a, stream); break;
-    case 4: e = launch_group<T, D, 4>(tmk, tmv, a, stream); break;
-    case 8:
-      if constexpr (!kIsMx<T>) {
-        e = launch_group<T, D, 8>(tmk, tmv, a, stream);
-        break;
-      }
-      return cudaErrorInvalidValue;
+    case 1: e = launch_group<D, 1>(tmk, tmv, a, stream); break;
+    case 2: e = launch_group<D, 2>(tmk, tmv, a, stream); break;
+    case 4: e = launch_group<D, 4>(tmk, tmv, a, stream); break;
+    case 8: e = launch_group<D, 8>(tmk, tmv, a, stream); break;
     default: return cudaErrorInvalidValue;
   }
   if (e != cudaSuccess || a.parts == 1) return e;
-  return a.parts ? launch_window_merge(dtype, D, a, stream) : launch_decode_reduce(dtype, D, a, stream);
+  return a.parts ? launch_window_merge(PKV_F32, D, a, stream) : launch_decode_reduce(PKV_F32, D, a, stream);
 }
 
 template <typename T>
@@ -107,14 +105,11 @@ cudaError_t launch_window_merge(int dtype, int head_dim, const WindowArgs& a, cu
   return dtype == PKV_F32 ? merge<float>(head_dim, a, stream) : merge<__nv_bfloat16>(head_dim, a, stream);
 }
 
-cudaError_t launch_decode_window(int dtype, int head_dim, int group, const CUtensorMap& tmk,
-                                 const CUtensorMap& tmv, const DecodeArgs& args, cudaStream_t stream) {
+cudaError_t launch_decode_window(int head_dim, int group, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                 const DecodeArgs& args, cudaStream_t stream) {
   const WindowArgs a(args, box_rows_for(args.block_size));
-  if (dtype == PKV_MXFP8)
-    return head_dim == 128 ? launch_dim<__nv_fp8_e4m3, 128>(dtype, group, tmk, tmv, a, stream)
-                           : launch_dim<__nv_fp8_e4m3, 64>(dtype, group, tmk, tmv, a, stream);
-  return head_dim == 128 ? launch_dim<float, 128>(dtype, group, tmk, tmv, a, stream)
-                         : launch_dim<float, 64>(dtype, group, tmk, tmv, a, stream);
+  return head_dim == 128 ? launch_dim<128>(group, tmk, tmv, a, stream)
+                         : launch_dim<64>(group, tmk, tmv, a, stream);
 }
 
 }  // namespace pkv

@@ -156,19 +156,19 @@ cudaError_t launch_decode_partial_scores(int dtype, int head_dim, int group, con
                                          const CUtensorMap& tmv, const DecodeArgs& args,
                                          cudaStream_t stream);
 
-// The windowed decode on the CUDA cores, merge included (decode_window.cu).
-cudaError_t launch_decode_window(int dtype, int head_dim, int group, const CUtensorMap& tmk,
-                                         const CUtensorMap& tmv, const DecodeArgs& args,
-                                         cudaStream_t stream);
+// The windowed decode of fp32 pools on the CUDA cores, merge included (decode_window.cu).
+cudaError_t launch_decode_window(int head_dim, int group, const CUtensorMap& tmk, const CUtensorMap& tmv,
+                                 const DecodeArgs& args, cudaStream_t stream);
 
 // Its merge of parts (args.parts > 1), by itself.
 cudaError_t launch_window_merge(int dtype, int head_dim, const WindowArgs& args, cudaStream_t stream);
 
-// The direct split over bf16 pools on matrix instructions (window_mma.cu), merge
-// included: tmk / tmv are row-group maps whose box is box_rows_for(P) rows.
-cudaError_t launch_window_mma(int head_dim, int group, const CUtensorMap& tmk, const CUtensorMap& tmv,
-                              const DecodeArgs& args, cudaStream_t stream);
-int window_mma_resident_ctas(int head_dim, int group);
+// The direct split over bf16 and MXFP8 pools on matrix instructions (window_mma.cu),
+// merge included.  The maps' boxes are box_rows_for(P) rows: row-group maps for bf16,
+// 4-D ones over the codes, swizzled by the row's bytes, for MXFP8.
+cudaError_t launch_window_mma(int dtype, int head_dim, int group, const CUtensorMap& tmk,
+                              const CUtensorMap& tmv, const DecodeArgs& args, cudaStream_t stream);
+int window_mma_resident_ctas(int dtype, int head_dim, int group);
 
 // CTAs of one wave of the partial kernel (resident CTAs per SM x SMs).
 int decode_resident_ctas(int dtype, int head_dim, int group);

@@ -1,5 +1,5 @@
-// window_mma.cu -- the decode of bf16 pools under a sliding window with sinks,
-// on warp-level matrix instructions.
+// window_mma.cu -- the decode of bf16 and MXFP8 pools under a sliding window with
+// sinks, on warp-level matrix instructions.
 //
 // What it computes: what decode_window.cu computes -- for sequence r and query
 // head h, attention of q[r, h] over the rows t < S and t >= T - W of kv head h /
@@ -29,7 +29,22 @@
 //   * the exponent base moves only when a score passes it by 2^8; rows that are
 //     not seen have weight 0, and their V is cleared in the fragments (0 x NaN);
 //   * the two warps merge through the ring at the end.
+// MXFP8 pools: tiles hold codes, and a warp widens them in its fragments, exactly (an
+// E4M3 value times a power of two is a bf16 value).  ldmatrix moves pairs of codes, so
+// a lane gets four codes of consecutive columns where the fragment wants two and two: K
+// is contracted in that order of columns (q is loaded so), and V's tiles are the even
+// and the odd columns of sixteen.  K's scales multiply the scores of their 32 columns,
+// V's the codes as they are widened.  NaN codes, scales of 2^-127 (K) and above 2^7 (V)
+// cost more instructions; a chunk without one, by a vote, skips them (in every call they
+// made 64 requests, window 1024, 32/8 heads 79 us instead of 51).  A chunk's 900
+// instructions bound it: two warps of matrix work a scheduler, half of its cycles issuing,
+// the ALU pipe 46% busy, 168 registers (at 128, for five CTAs, 77 us).  Against the CUDA cores
+// (one to four heads) and tcgen05's widened tiles (eight), 64 requests, window 128 / 1024:
+//   32/8 heads  9.4 / 51.0 us against 12.3 / 69.7;  64/8   9.9 / 51.8 against 42.5 / 115.7;
+//   8/8         9.1 / 50.5 against 8.8 / 47.4 (head_dim 64: 7.7 / 39.4 against 8.5 / 46.0).
 #include <math.h>
+
+#include <type_traits>
 
 #include "common.cuh"
 #include "launch.h"
@@ -42,10 +57,14 @@ namespace {
 constexpr int kWmRows = 32;             // rows of a stage
 constexpr int kWmThreads = 3 * 32;      // two warps of matrix work, one of loads
 constexpr float kWmLn2 = 0.6931471805599453f;
-// Stages of the ring: 48 KiB, four CTAs an SM.
-constexpr int wm_stages(int d) { return d == 128 ? 3 : 6; }
-constexpr int wm_tile(int d) { return kWmRows * d * 2; }  // bytes of a K (or V) tile
-constexpr int wm_smem(int d) { return wm_stages(d) * 2 * wm_tile(d) + 1024; }  // +1024: alignment
+// Bytes of a K (or V) tile, of its scales, and stages of the ring: 48 KiB (32 for
+// head_dim 64 over MXFP8), four CTAs an SM.
+constexpr int wm_tile(bool mx, int d) { return kWmRows * d * (mx ? 1 : 2); }
+constexpr int wm_scales(bool mx, int d) { return mx ? kWmRows * d / 32 : 0; }
+constexpr int wm_stages(bool mx, int d) { return mx ? (d == 128 ? 6 : 8) : (d == 128 ? 3 : 6); }
+constexpr int wm_smem(bool mx, int d) {
+  return wm_stages(mx, d) * 2 * (wm_tile(mx, d) + wm_scales(mx, d)) + 1024;  // +1024: alignment
+}
 
 __device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
   asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
@@ -65,6 +84,15 @@ __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1
       : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
       : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same onto zeros.
+__device__ __forceinline__ void mma16816_new(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                             uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+      "{%10, %10, %10, %10};"
+      : "=f"(c[0]), "=f"(c[1]), "=f"(c[2]), "=f"(c[3])
+      : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
   const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
   return *reinterpret_cast<const uint32_t*>(&b);
@@ -72,12 +100,42 @@ __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
 
 }  // namespace
 
-template <int D, int G>
+// Two of a word's four codes as the bits of two bf16, times 2^-120: s.eeee.mmm with s
+// at 15, eeeemmm at 10 .. 4.  kHigh: bytes 1 and 3, else 0 and 2.
+template <bool kHigh>
+__device__ __forceinline__ uint32_t place_codes(uint32_t w) {
+  return ((kHigh ? w >> 4 : w << 4) & 0x07f007f0u) | ((kHigh ? w : w << 8) & 0x80008000u);
+}
+// They times f1, as bf16; with kRare also times f2, and with the NaN codes (s.1111.111).
+template <bool kHigh, bool kRare>
+__device__ __forceinline__ uint32_t widen2(uint32_t w, uint32_t f1, uint32_t f2) {
+  const uint32_t x = place_codes<kHigh>(w);
+  __nv_bfloat162 v = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&x), *reinterpret_cast<const __nv_bfloat162*>(&f1));
+  if constexpr (kRare) v = __hmul2(v, *reinterpret_cast<const __nv_bfloat162*>(&f2));
+  uint32_t y = *reinterpret_cast<const uint32_t*>(&v);
+  if constexpr (kRare) {
+    if ((x & 0x07f0u) == 0x07f0u) y |= 0x7fffu;
+    if ((x & 0x07f00000u) == 0x07f00000u) y |= 0x7fff0000u;
+  }
+  return y;
+}
+// Bit 7 of a byte is set ...
+__device__ __forceinline__ uint32_t nan_codes(uint32_t w) {  // ... in NaN codes
+  return (w & 0x7f7f7f7fu) + 0x01010101u;
+}
+__device__ __forceinline__ uint32_t zero_scales(uint32_t s) {  // ... if one is 0 (in some byte)
+  return (s - 0x01010101u) & ~s;
+}
+__device__ __forceinline__ uint32_t large_scales(uint32_t s) {  // ... in scales above 134
+  return ((s & 0x7f7f7f7fu) + 0x79797979u) & s;
+}
+
+template <bool kMx, int D, int G>
 __global__ void __launch_bounds__(kWmThreads, 4)
     window_mma_kernel(const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                       const WindowArgs a) {
-  constexpr int NS = wm_stages(D), kTile = wm_tile(D);
-  constexpr int kAtom = D / 64 * 1024;  // bytes of an 8-row group, both halves
+  constexpr int NS = wm_stages(kMx, D), kTile = wm_tile(kMx, D), kScales = wm_scales(kMx, D);
+  constexpr int kAtom = kMx ? 8 * D : D / 64 * 1024;  // bytes of an 8-row group, all columns
   __shared__ uint64_t full[NS], empty[NS];
   __shared__ float sm_m[2][8], sm_l[2][8];
 
@@ -147,9 +205,22 @@ __global__ void __launch_bounds__(kWmThreads, 4)
       const int nbox = (stage_rows<kWmRows>(a, seg, i0 + k).nvalid + TB - 1) / TB;
       const int from = 2 * (k - x0) + (lane & 1);
       const int my_blk = __shfl_sync(0xffffffffu, blk, from), my_row = __shfl_sync(0xffffffffu, brow, from);
-      if (lane == 0) mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * nbox * TB * D * 2));
+      if (lane == 0)
+        mbar_arrive_expect_tx(&full[s], (uint32_t)(2 * nbox * TB * (kMx ? D + D / 32 : 2 * D)));
       __syncwarp();
-      if (lane < 4 && (lane & 1) < nbox)
+      if constexpr (kMx) {
+        if (lane < 4 && (lane & 1) < nbox) {
+          tma_load_4d(ring + (size_t)s * 2 * kTile + (lane >> 1) * kTile + (lane & 1) * TB * D,
+                      lane < 2 ? &tmk : &tmv, 0, h, my_row, my_blk, &full[s]);
+        } else if (lane < 8 && lane >= 4 && (lane & 1) < nbox) {
+          // the box's scale rows; of a bad block, block 0's (its codes are zeros)
+          const int64_t sb = my_blk < a.num_blocks ? my_blk : 0;
+          const uint8_t* src = (lane < 6 ? a.k_scales : a.v_scales) +
+                               ((sb * a.num_kv_heads + h) * P + my_row) * (D / 32);
+          bulk_load(ring + NS * 2 * kTile + (s * 2 + (lane < 6 ? 0 : 1)) * kScales + (lane & 1) * TB * (D / 32),
+                    src, (uint32_t)(TB * (D / 32)), &full[s]);
+        }
+      } else if (lane < 4 && (lane & 1) < nbox)
         tma_load_5d(ring + (size_t)s * 2 * kTile + (lane >> 1) * kTile + (lane & 1) * TB * D * 2,
                     lane < 2 ? &tmk : &tmv, 0, 0, 0, h,
                     (int)((int64_t)my_blk * (P / kRowGroup) + my_row / kRowGroup), &full[s]);
@@ -169,8 +240,15 @@ __global__ void __launch_bounds__(kWmThreads, 4)
           static_cast<const __nv_bfloat16*>(a.q) + ((int64_t)r * a.num_q_heads + (int64_t)h * G + hd) * D);
 #pragma unroll
       for (int kk = 0; kk < D / 16; ++kk) {
-        q[kk][0] = hd < G ? __ldg(qp + kk * 8 + quad) : 0u;
-        q[kk][1] = hd < G ? __ldg(qp + kk * 8 + 4 + quad) : 0u;
+        if constexpr (kMx) {  // columns 4 quad, + 2 against + 1, + 3
+          const uint32_t w0 = hd < G ? __ldg(qp + kk * 8 + 2 * quad) : 0u;
+          const uint32_t w1 = hd < G ? __ldg(qp + kk * 8 + 2 * quad + 1) : 0u;
+          q[kk][0] = __byte_perm(w0, w1, 0x5410);
+          q[kk][1] = __byte_perm(w0, w1, 0x7632);
+        } else {
+          q[kk][0] = hd < G ? __ldg(qp + kk * 8 + quad) : 0u;
+          q[kk][1] = hd < G ? __ldg(qp + kk * 8 + 4 + quad) : 0u;
+        }
       }
     }
     float o[D / 8][4];
@@ -179,13 +257,18 @@ __global__ void __launch_bounds__(kWmThreads, 4)
 #pragma unroll
       for (int e = 0; e < 4; ++e) o[j][e] = 0.f;
     float m = -INFINITY, l = 0.f;  // of head hd; l: this lane's share
-    // ldmatrix addresses: lane i names row i % 8 of matrix i / 8.  K: matrices
+    // ldmatrix addresses: lane i names row i % 8 of matrix i / 8.  bf16 K: matrices
     // (rows 0-7, columns 0-7), (0-7, 8-15), (8-15, 0-7), (8-15, 8-15); V: (rows
     // 0-7, columns 0-7), (8-15, 0-7), (0-7, 8-15), (8-15, 8-15).
     const int mat = lane >> 3, r8 = lane & 7;
     const uint32_t base = smem_u32(ring) + (uint32_t)(warp * 2 * kAtom);  // this warp's two row groups
-    const uint32_t krow = base + (uint32_t)((mat >> 1) * kAtom + r8 * 128);
-    const uint32_t vrow = base + (uint32_t)(kTile + (mat & 1) * kAtom + r8 * 128);
+    // Codes, K and V: (rows 0-7, 16 columns), (8-15, they), (0-7, the next 16), (8-15, those).
+    const uint32_t krow = base + (uint32_t)(kMx ? (mat & 1) * kAtom + r8 * D : (mat >> 1) * kAtom + r8 * 128);
+    const uint32_t vrow = kMx ? krow + kTile : base + (uint32_t)(kTile + (mat & 1) * kAtom + r8 * 128);
+    // where 16-byte chunk c of a row of codes lies
+    auto code_chunk = [&](int c) -> uint32_t {
+      return (uint32_t)((D == 128 ? c ^ r8 : c ^ (r8 >> 1)) << 4);
+    };
     for (int k = 0; k < n; ++k) {
       const int s = k % NS;
       if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (k / NS) & 1))) {
@@ -203,8 +286,61 @@ __global__ void __launch_bounds__(kWmThreads, 4)
         for (int x = 0; x < 2; ++x)
 #pragma unroll
           for (int e = 0; e < 4; ++e) sc[x][e] = 0.f;
+        // MXFP8: the scales of this lane's four rows
+        uint32_t ksc[4] = {}, vsc[4] = {};
+        if constexpr (kMx) {
+          const unsigned char* at = ring + NS * 2 * kTile + s * 2 * kScales;
 #pragma unroll
-        for (int kk = 0; kk < D / 16; ++kk) {
+          for (int e = 0; e < 4; ++e) {
+            const int row = warp * 16 + (e >> 1) * 8 + quad * 2 + (e & 1);
+            if constexpr (D == 128) {
+              ksc[e] = reinterpret_cast<const uint32_t*>(at)[row];
+              vsc[e] = reinterpret_cast<const uint32_t*>(at + kScales)[row];
+            } else {
+              ksc[e] = reinterpret_cast<const uint16_t*>(at)[row] | 0x01010000u;
+              vsc[e] = reinterpret_cast<const uint16_t*>(at + kScales)[row];
+            }
+          }
+          uint32_t w[D / 32][4], odd = 0;
+#pragma unroll
+          for (int g = 0; g < D / 32; ++g) {
+            ldsm4(krow + off + code_chunk(2 * g + (mat >> 1)), w[g]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) odd |= nan_codes(w[g][i]);
+          }
+#pragma unroll
+          for (int e = 0; e < 4; ++e) odd |= zero_scales(ksc[e]);
+          auto scores = [&](auto rare) {
+            constexpr uint32_t kUp = 0x7b807b80u;  // 2^120: codes as they are placed, to their values
+#pragma unroll
+            for (int g = 0; g < D / 32; ++g) {
+              float part[2][4];
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {  // row group i & 1, chunk 2 g + (i >> 1)
+                const int kk = 2 * g + (i >> 1);
+                const uint32_t b0 = widen2<false, rare.value>(w[g][i], kUp, 0x3f803f80u);
+                const uint32_t b1 = widen2<true, rare.value>(w[g][i], kUp, 0x3f803f80u);
+                if (i < 2)
+                  mma16816_new(part[i], q[kk][0], 0u, q[kk][1], 0u, b0, b1);
+                else
+                  mma16816(part[i & 1], q[kk][0], 0u, q[kk][1], 0u, b0, b1);
+              }
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                const float f = rare.value
+                                    ? e8m0_value((ksc[e] >> (8 * g)) & 0xffu)
+                                    : __uint_as_float((g == 3 ? ksc[e] >> 1 : ksc[e] << (23 - 8 * g)) & 0x7f800000u);
+                sc[e >> 1][e & 1] = fmaf(part[e >> 1][e & 1], f, sc[e >> 1][e & 1]);
+              }
+            }
+          };
+          if (__any_sync(0xffffffffu, (odd & 0x80808080u) != 0))
+            scores(std::true_type{});
+          else
+            scores(std::false_type{});
+        }
+#pragma unroll
+        for (int kk = 0; kk < (kMx ? 0 : D / 16); ++kk) {
           const int c = 2 * kk + (mat & 1);  // 8-column chunk
           uint32_t b[4];
           ldsm4(krow + off + (c >> 3) * 1024 + (((c & 7) ^ r8) << 4), b);
@@ -251,8 +387,57 @@ __global__ void __launch_bounds__(kWmThreads, 4)
           keep0 = (on[0] ? 0xffffu : 0u) | (on[1] ? 0xffff0000u : 0u);
           keep1 = (on[2] ? 0xffffu : 0u) | (on[3] ? 0xffff0000u : 0u);
         }
+        if constexpr (kMx) {
+          uint32_t w[D / 32][4], odd = 0;
 #pragma unroll
-        for (int j = 0; j < D / 8; j += 2) {
+          for (int g = 0; g < D / 32; ++g) {
+            ldsm4_t(vrow + off + code_chunk(2 * g + (mat >> 1)), w[g]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              w[g][i] &= i & 1 ? keep1 : keep0;  // a word's halves are two rows
+              odd |= nan_codes(w[g][i]);
+            }
+          }
+          // scales past 2^7 take the second factor
+#pragma unroll
+          for (int e = 0; e < 4; ++e) odd |= large_scales(vsc[e]);
+          auto values = [&](auto rare) {
+#pragma unroll
+            for (int g = 0; g < D / 32; ++g) {
+              uint32_t f1[2], f2[2];  // of rows 2 quad, + 1, and those 8 further on
+#pragma unroll
+              for (int x = 0; x < 2; ++x) {
+                const uint32_t s2 = __byte_perm(vsc[2 * x], vsc[2 * x + 1], 0x0400u + 0x0101u * g) & 0x00ff00ffu;
+                f1[x] = f2[x] = 0;
+                if constexpr (rare.value) {
+                  const uint32_t m2 = min(s2 & 0xffu, 134u) | min(s2 >> 16, 134u) << 16;
+                  f1[x] = m2 * 0x80u + 0x3C003C00u;          // 2^(m - 7)
+                  f2[x] = (s2 - m2) * 0x80u + 0x3F803F80u;   // 2^(s - m)
+                } else {
+                  f1[x] = s2 * 0x80u + 0x3C003C00u;          // 2^(s - 7)
+                }
+              }
+#pragma unroll
+              for (int y = 0; y < 2; ++y) {  // chunk 2 g + y: tiles of its even and odd columns
+                const int j = 2 * (2 * g + y);
+#pragma unroll
+                for (int z = 0; z < 2; ++z) {
+                  const uint32_t b0 = z ? widen2<true, rare.value>(w[g][2 * y], f1[0], f2[0])
+                                        : widen2<false, rare.value>(w[g][2 * y], f1[0], f2[0]);
+                  const uint32_t b1 = z ? widen2<true, rare.value>(w[g][2 * y + 1], f1[1], f2[1])
+                                        : widen2<false, rare.value>(w[g][2 * y + 1], f1[1], f2[1]);
+                  mma16816(o[j + z], hi0, lo0, hi1, lo1, b0, b1);
+                }
+              }
+            }
+          };
+          if (__any_sync(0xffffffffu, (odd & 0x80808080u) != 0))
+            values(std::true_type{});
+          else
+            values(std::false_type{});
+        }
+#pragma unroll
+        for (int j = 0; j < (kMx ? 0 : D / 8); j += 2) {
           const int c = j + (mat >> 1);
           uint32_t b[4];
           ldsm4_t(vrow + off + (c >> 3) * 1024 + (((c & 7) ^ r8) << 4), b);
@@ -273,10 +458,17 @@ __global__ void __launch_bounds__(kWmThreads, 4)
     named_barrier_sync(1, 64);  // both are done with the ring
     float* om = reinterpret_cast<float*>(ring);  // [2][8][D]
     if (hd < G) {
+      float* to = om + (warp * 8 + hd) * D;
+      if constexpr (kMx) {
 #pragma unroll
-      for (int j = 0; j < D / 8; ++j)
-        *reinterpret_cast<float2*>(om + (warp * 8 + hd) * D + j * 8 + quad * 2) =
-            make_float2(o[j][0] + o[j][2], o[j][1] + o[j][3]);
+        for (int j = 0; j < D / 8; j += 2)  // even and odd columns of sixteen
+          *reinterpret_cast<float4*>(to + j * 8 + quad * 4) =
+              make_float4(o[j][0] + o[j][2], o[j + 1][0] + o[j + 1][2], o[j][1] + o[j][3], o[j + 1][1] + o[j + 1][3]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < D / 8; ++j)
+          *reinterpret_cast<float2*>(to + j * 8 + quad * 2) = make_float2(o[j][0] + o[j][2], o[j][1] + o[j][3]);
+      }
     }
     named_barrier_sync(1, 64);
     if (ok) {
@@ -288,12 +480,12 @@ __global__ void __launch_bounds__(kWmThreads, 4)
         const float m0 = sm_m[0][g], m1 = sm_m[1][g], M = fmaxf(m0, m1);
         const float w0 = M == -INFINITY ? 0.f : exp2f(m0 - M), w1 = M == -INFINITY ? 0.f : exp2f(m1 - M);
         const float sum = fmaf(w0, sm_l[0][g], w1 * sm_l[1][g]);
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum != 0.f ? 1.f / sum : 0.f;  // NaN stays
         const float4 x = *reinterpret_cast<const float4*>(om + g * D + e0);
         const float4 y = *reinterpret_cast<const float4*>(om + (8 + g) * D + e0);
         const float v[4] = {fmaf(w0, x.x, w1 * y.x) * inv, fmaf(w0, x.y, w1 * y.y) * inv,
                             fmaf(w0, x.z, w1 * y.z) * inv, fmaf(w0, x.w, w1 * y.w) * inv};
-        const float lse2 = sum > 0.f ? M + log2f(sum) : -INFINITY;
+        const float lse2 = sum != 0.f ? M + log2f(sum) : -INFINITY;
         if (all) {
           *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
           if (e0 == 0 && lse_out) lse_out[g] = lse2 * kWmLn2;
@@ -306,7 +498,7 @@ __global__ void __launch_bounds__(kWmThreads, 4)
   }
 }
 
-template <int D, int G>
+template <bool kMx, int D, int G>
 static int wm_resident() {
   static std::mutex mu;
   static int cached[64] = {};
@@ -314,10 +506,11 @@ static int wm_resident() {
   if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= 64) return 0;
   std::lock_guard<std::mutex> lock(mu);
   if (!cached[dev]) {
-    auto kern = window_mma_kernel<D, G>;
+    auto kern = window_mma_kernel<kMx, D, G>;
+    constexpr int smem = wm_smem(kMx, D);
     int per_sm = 0, sms = 0;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, wm_smem(D)) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kWmThreads, wm_smem(D)) != cudaSuccess ||
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, kern, kWmThreads, smem) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
       return 0;
     cached[dev] = per_sm * sms;
@@ -325,45 +518,60 @@ static int wm_resident() {
   return cached[dev];
 }
 
-template <int D>
-static int wm_resident_group(int group) {
-  return group == 1 ? wm_resident<D, 1>() : group == 2 ? wm_resident<D, 2>() : group == 4 ? wm_resident<D, 4>()
-                                                                              : wm_resident<D, 8>();
-}
-
-int window_mma_resident_ctas(int head_dim, int group) {
-  return head_dim == 128 ? wm_resident_group<128>(group) : wm_resident_group<64>(group);
-}
-
-template <int D, int G>
+template <bool kMx, int D, int G>
 static cudaError_t launch_wm(const CUtensorMap& tmk, const CUtensorMap& tmv, const WindowArgs& a,
                              cudaStream_t stream) {
-  auto kern = window_mma_kernel<D, G>;
+  auto kern = window_mma_kernel<kMx, D, G>;
+  constexpr int smem = wm_smem(kMx, D);
   static SmemAttrCache attr_cache;
-  cudaError_t e = ensure_smem_limit(kern, wm_smem(D), attr_cache);
+  cudaError_t e = ensure_smem_limit(kern, smem, attr_cache);
   if (e != cudaSuccess) return e;
-  return launch_pdl(kern, dim3((unsigned)a.num_ctas), dim3(kWmThreads), wm_smem(D), stream, tmk, tmv, a);
+  return launch_pdl(kern, dim3((unsigned)a.num_ctas), dim3(kWmThreads), smem, stream, tmk, tmv, a);
 }
 
-template <int D>
-static cudaError_t launch_wm_group(int group, const CUtensorMap& tmk, const CUtensorMap& tmv,
-                                   const WindowArgs& a, cudaStream_t stream) {
-  switch (group) {
-    case 1: return launch_wm<D, 1>(tmk, tmv, a, stream);
-    case 2: return launch_wm<D, 2>(tmk, tmv, a, stream);
-    case 4: return launch_wm<D, 4>(tmk, tmv, a, stream);
-    case 8: return launch_wm<D, 8>(tmk, tmv, a, stream);
+// Call f.operator()<kMx, D, G>() for the sizes of a call.
+template <bool kMx, int D, class F>
+static auto wm_group(int group, F&& f) {
+  return group == 1   ? f.template operator()<kMx, D, 1>()
+         : group == 2 ? f.template operator()<kMx, D, 2>()
+         : group == 4 ? f.template operator()<kMx, D, 4>()
+                      : f.template operator()<kMx, D, 8>();
+}
+template <class F>
+static auto wm_sizes(int dtype, int head_dim, int group, F&& f) {
+  if (dtype == PKV_MXFP8)
+    return head_dim == 128 ? wm_group<true, 128>(group, f) : wm_group<true, 64>(group, f);
+  return head_dim == 128 ? wm_group<false, 128>(group, f) : wm_group<false, 64>(group, f);
+}
+
+namespace {
+struct ResidentCall {
+  template <bool kMx, int D, int G>
+  int operator()() const {
+    return wm_resident<kMx, D, G>();
   }
-  return cudaErrorInvalidValue;
+};
+struct LaunchCall {
+  const CUtensorMap &tmk, &tmv;
+  const WindowArgs& a;
+  cudaStream_t stream;
+  template <bool kMx, int D, int G>
+  cudaError_t operator()() const {
+    return launch_wm<kMx, D, G>(tmk, tmv, a, stream);
+  }
+};
+}  // namespace
+
+int window_mma_resident_ctas(int dtype, int head_dim, int group) {
+  return wm_sizes(dtype, head_dim, group, ResidentCall{});
 }
 
-cudaError_t launch_window_mma(int head_dim, int group, const CUtensorMap& tmk, const CUtensorMap& tmv,
-                              const DecodeArgs& args, cudaStream_t stream) {
+cudaError_t launch_window_mma(int dtype, int head_dim, int group, const CUtensorMap& tmk,
+                              const CUtensorMap& tmv, const DecodeArgs& args, cudaStream_t stream) {
   const WindowArgs a(args, box_rows_for(args.block_size));
-  cudaError_t e = head_dim == 128 ? launch_wm_group<128>(group, tmk, tmv, a, stream)
-                                  : launch_wm_group<64>(group, tmk, tmv, a, stream);
+  cudaError_t e = wm_sizes(dtype, head_dim, group, LaunchCall{tmk, tmv, a, stream});
   if (e != cudaSuccess || a.parts == 1) return e;
-  return launch_window_merge(PKV_BF16, head_dim, a, stream);
+  return launch_window_merge(dtype, head_dim, a, stream);
 }
 
 }  // namespace pkv

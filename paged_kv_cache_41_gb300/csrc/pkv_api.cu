@@ -147,8 +147,8 @@ pkv_status check_attention_shape(const pkv_cache_desc* c, int32_t num_q_heads) {
 
 // 4-D map over the pool [NB, P, Hkv, D] whose box is one kv head x `rows`
 // token rows x head_dim.
-pkv_status encode_cache_map(CUtensorMap* map, const pkv_cache_desc* c, const void* base,
-                            int rows) {
+pkv_status encode_cache_map(CUtensorMap* map, const pkv_cache_desc* c, const void* base, int rows,
+                            CUtensorMapSwizzle swizzle = CU_TENSOR_MAP_SWIZZLE_NONE) {
   const cuuint64_t es = (cuuint64_t)elem_bytes(c->dtype);
   cuuint64_t dims[4] = {(cuuint64_t)c->head_dim, (cuuint64_t)c->num_kv_heads,
                         (cuuint64_t)c->block_size, (cuuint64_t)c->num_blocks};
@@ -158,8 +158,7 @@ pkv_status encode_cache_map(CUtensorMap* map, const pkv_cache_desc* c, const voi
                                 : c->dtype == PKV_MXFP8 ? CU_TENSOR_MAP_DATA_TYPE_UINT8
                                                         : CU_TENSOR_MAP_DATA_TYPE_FLOAT32;
   CUresult r = encode_tiled_cached(map, dt,
-                                   4, const_cast<void*>(base), dims, strides, box,
-                                   CU_TENSOR_MAP_SWIZZLE_NONE);
+                                   4, const_cast<void*>(base), dims, strides, box, swizzle);
   if (r == CUDA_ERROR_NOT_INITIALIZED) return PKV_ERR_CUDA;
   return r == CUDA_SUCCESS ? PKV_OK : PKV_ERR_UNSUPPORTED;
 }
@@ -253,11 +252,17 @@ pkv_status launch_decode(const pkv_cache_desc* cache, int G, const void* q, cons
   }
   a.stage_units = tc ? 1 : 2;
   a.piece_units = tc ? 0 : 3;
-  if (a.parts && cache->dtype == PKV_BF16) {
+  if (a.parts && cache->dtype != PKV_F32) {
     const int rows = pkv::box_rows_for(cache->block_size);
-    if ((st = encode_cache_map_rg(&tmk, cache, k_cache, rows)) != PKV_OK) return st;
-    if ((st = encode_cache_map_rg(&tmv, cache, v_cache, rows)) != PKV_OK) return st;
-    e = pkv::launch_window_mma(cache->head_dim, G, tmk, tmv, a, stream);
+    if (cache->dtype == PKV_MXFP8) {  // a row of codes is the swizzle's span
+      const CUtensorMapSwizzle sw = cache->head_dim == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+      if ((st = encode_cache_map(&tmk, cache, k_cache, rows, sw)) != PKV_OK) return st;
+      if ((st = encode_cache_map(&tmv, cache, v_cache, rows, sw)) != PKV_OK) return st;
+    } else {
+      if ((st = encode_cache_map_rg(&tmk, cache, k_cache, rows)) != PKV_OK) return st;
+      if ((st = encode_cache_map_rg(&tmv, cache, v_cache, rows)) != PKV_OK) return st;
+    }
+    e = pkv::launch_window_mma(cache->dtype, cache->head_dim, G, tmk, tmv, a, stream);
     return e == cudaSuccess ? PKV_OK : PKV_ERR_CUDA;
   }
   if (tc) {
@@ -538,18 +543,16 @@ struct DecodeSplit {
   int64_t recording;
 };
 
-// Over bf16 pools every window takes the direct split (window_mma.cu): parts
-// enough for one wave, and of no more rows than this, so that one long sequence
+// Over bf16 and MXFP8 pools every window takes the direct split (window_mma.cu):
+// parts enough for one wave, and of no more rows than this, so that one long sequence
 // among short ones is not one CTA's.  Parts of 2048 rows / segments whole where they
 // fill a wave: 64 x 8192 rows, window 4096 163 / 154 us; one sequence of 65536 rows beside 63
 // of 256, window 4096 48 / 85, 65536 101 / 1202 (parts of 1024 rows 117, 4096 127).
 constexpr int64_t kPartRows = 2048;
-// Over the others the direct split wins where its last wave's idle places, shared
+// Over fp32 pools the direct split wins where its last wave's idle places, shared
 // out over a wave, come to no more rows than the balanced split's plan and merge are
-// worth.  Measured in us, block size 16, head_dim 128, 32/8 heads, direct / balanced:
-//   MXFP8, 512 segments on 608 places: window 128 12.3 / 19.6, 512 37.3 / 42.2, 1024
-//   69.7 / 70.7; 128 segments, in parts: 128 11.8 / 14.3, 1024 25.6 / 26.0; fp32, 512 on 304
-//   places: 128 21.6 / 24.5, 512 61.1 / 54.6, 1024 113.4 / 94.9.
+// worth: 512 segments on 304 places, window 128 21.6 us against 24.5 balanced, 512
+// 61.1 / 54.6, 1024 113.4 / 94.9.
 constexpr int64_t kDirectIdleRows = 170;
 constexpr int64_t kDirectRows = 2200;
 
@@ -570,20 +573,18 @@ DecodeSplit decode_split(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_
   auto direct = [&](int64_t parts) {
     return DecodeSplit{segs * parts, (int32_t)parts, parts > 1 ? segs * parts : 0};
   };
-  if (c->dtype == PKV_BF16) {
-    int64_t resident = pkv::window_mma_resident_ctas(c->head_dim, G);
+  if (c->dtype != PKV_F32) {
+    int64_t resident = pkv::window_mma_resident_ctas(c->dtype, c->head_dim, G);
     if (resident <= 0) resident = 4LL * sm_count();
     const int64_t wave = resident / segs, cut = (rows + kPartRows - 1) / kPartRows;
     return direct(std::max<int64_t>(std::min(std::max(wave, cut), stages), 1));
   }
-  if (!use_tc_decode(c, G)) {  // eight heads over MXFP8: the tensor cores only
-    int64_t resident = pkv::decode_resident_ctas(c->dtype, c->head_dim, G);
-    if (resident <= 0) resident = 2LL * sm_count();
-    const int64_t parts = std::max<int64_t>(std::min(resident / segs, stages), 1);  // one wave
-    const int64_t places = (segs + resident - 1) / resident * resident;
-    if (rows <= kDirectRows && (parts > 1 || (places - segs) * rows <= kDirectIdleRows * resident))
-      return direct(parts);
-  }
+  int64_t resident = pkv::decode_resident_ctas(c->dtype, c->head_dim, G);
+  if (resident <= 0) resident = 2LL * sm_count();
+  const int64_t parts = std::max<int64_t>(std::min(resident / segs, stages), 1);  // one wave
+  const int64_t places = (segs + resident - 1) / resident * resident;
+  if (rows <= kDirectRows && (parts > 1 || (places - segs) * rows <= kDirectIdleRows * resident))
+    return direct(parts);
   const int64_t blocks = (rows + c->block_size - 1) / c->block_size;
   const int64_t C = decode_ctas(c, num_seqs, num_q_heads, (int32_t)blocks, 0);
   return {C, 0, C};

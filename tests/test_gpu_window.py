@@ -215,3 +215,73 @@ def test_the_scores_of_hidden_rows_do_not_matter():
     out, lse = w.call()
     assert torch.equal(out, good)
     w.check(out, lse)
+
+
+@pytest.mark.parametrize("hq,d", [(1, 64), (4, 128), (8, 128)])
+def test_scales_and_codes_at_the_ends_of_mxfp8(hq, d):
+    # K scales of 2^-127, V scales past 2^7 (up to 2^14) in single groups: the ones
+    # that chunks of rows without them do not pay for
+    w = Window([5, 40, 64, 300], 120, 3, dtype="mxfp8", hq=hq, hkv=1, d=d, seed=hq)
+    rng = np.random.default_rng(d)
+    for pool, bytes_ in ((w.c.k, [0]), (w.c.v, [134, 135, 141])):
+        scales = pool.scales.view(-1)
+        at = torch.from_numpy(rng.choice(scales.numel(), scales.numel() // 12, replace=False)).cuda()
+        scales[at] = torch.from_numpy(rng.choice(bytes_, at.numel())).to(torch.uint8).cuda()
+    w.k64, w.v64 = zip(*(w.c.rows64(r, n) for r, n in enumerate(w.lens)))
+    w.run()
+    # a NaN code in a row that is seen: its column of V, every column by K
+    good, _ = w.call()
+    row = int(w.c.slots(3, np.array([250]))[0])
+    v, k = w.c.v.elements.view(-1, d), w.c.k.elements.view(-1, d)
+    was = int(v[row, 37])
+    v[row, 37] = 0xFF
+    out, _ = w.call()
+    assert torch.isnan(out[3, :, 37]).all()
+    out[3, :, 37] = good[3, :, 37]
+    assert torch.equal(out, good)
+    v[row, 37] = was
+    k[row, 5] = 0x7F
+    out, _ = w.call()
+    assert torch.isnan(out[3]).all() and torch.equal(out[:3], good[:3])
+
+
+@pytest.mark.parametrize("dtype,hq", [("bf16", 1), ("bf16", 8), ("f32", 1), ("f32", 8), ("mxfp8", 8)])
+@pytest.mark.parametrize("window,lens", [(120, [5, 300]), (120, [5, 300] + [0] * 400), (2500, [5, 2600])])
+def test_nan_scores_stay(dtype, hq, window, lens):
+    # one CTA a segment, several, and (fp32) pieces of the balanced split
+    w = Window(lens, window, 3, dtype=dtype, hq=hq, hkv=1, d=128, seed=hq)
+    good, good_lse = w.call()
+    row = int(w.c.slots(1, np.array([lens[1] - 30]))[0])
+    if dtype == "mxfp8":
+        w.c.k.elements.view(-1, 128)[row, 5] = 0x7F
+    else:
+        w.c.k.view(-1, 128)[row, 5] = float("nan")
+    out, lse = w.call()
+    assert torch.isnan(out[1]).all() and torch.isnan(lse[1]).all()
+    assert torch.equal(out[0], good[0]) and torch.equal(lse[0], good_lse[0])
+    assert torch.equal(out[2:], good[2:]) and torch.equal(lse[2:], good_lse[2:])
+    # every row that is seen
+    rows = torch.from_numpy(w.c.slots(0, np.arange(5))).cuda()
+    if dtype == "mxfp8":
+        w.c.k.elements.view(-1, 128)[rows] = 0x7F
+    else:
+        w.c.k.view(-1, 128)[rows] = float("nan")
+    out, lse = w.call()
+    assert torch.isnan(out[:2]).all() and torch.isnan(lse[:2]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+@pytest.mark.parametrize("window,n", [(120, 300), (2500, 2600)])
+def test_scores_of_minus_infinity_weigh_nothing(dtype, window, n):
+    w = Window([n, 3], window, 0, dtype=dtype, hq=1, hkv=1, d=64, seed=n)
+    w.q[:, 0, 7] = 1.0
+    off = np.concatenate([np.arange(n - window, n - window + 70), [n - 20]])
+    pool = w.c.k.view(-1, 64)
+    pool[torch.from_numpy(w.c.slots(0, off)).cuda(), 7] = float("-inf")
+    pool[torch.from_numpy(w.c.slots(1, np.arange(3))).cuda(), 7] = float("-inf")
+    w.seen[0][off] = False  # what is left of the formula
+    w.seen[1][:] = False
+    out, lse = w.call()
+    assert pkv.get_device_error() == 0
+    w.check(out, lse)
+    assert (out[1] == 0).all() and torch.isneginf(lse[1]).all()

@@ -18,9 +18,9 @@ namespace pkv {
 
 namespace {
 
-// Merge the parts of each (sequence, query head)'s segment by log-sum-exp, a
-// warp each; segments that one CTA had whole, and empty ones, are written
-// already.
+// Merge the parts of each (sequence, query head)'s segment, or what its clusters
+// made of them, by log-sum-exp, a warp each; segments that one CTA or cluster had
+// whole, and empty ones, are written already.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) window_merge_kernel(const WindowArgs a) {
   constexpr int EPL = D / 32;
@@ -31,10 +31,12 @@ __global__ void __launch_bounds__(128) window_merge_kernel(const WindowArgs a) {
   const int r = (int)(rh / a.num_q_heads), qh = (int)(rh - (int64_t)r * a.num_q_heads);
   const int G = a.num_q_heads / a.num_kv_heads;
   const int nt = (plan_len(a, r, a.block_size, false) + kStageRows - 1) / kStageRows;
-  const int w = (nt + a.parts - 1) / a.parts, n = nt ? (nt + w - 1) / w : 0;  // as direct_stages
+  // a record of each part (as direct_stages), or of each cluster of them
+  const int w = (nt + a.parts - 1) / a.parts, each = max(a.cluster, 1);
+  const int n = nt ? (nt + w * each - 1) / (w * each) : 0;
   if (n < 2) return;
-  const int64_t cta = ((int64_t)r * a.num_kv_heads + qh / G) * a.parts;
-  auto rec = [&](int i) { return 2 * (cta + i) * G + qh % G; };
+  const int64_t rec0 = ((int64_t)r * a.num_kv_heads + qh / G) * (a.parts / each);
+  auto rec = [&](int i) { return 2 * (rec0 + i) * G + qh % G; };
   float M = -INFINITY;
   for (int i = lane; i < n; i += 32) {
     const float l = a.rec_lse[rec(i)];

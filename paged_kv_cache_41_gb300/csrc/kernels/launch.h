@@ -48,6 +48,33 @@ cudaError_t launch_pdl(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t sme
   return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
 }
 
+inline cudaLaunchAttribute cluster_attr(int size) {
+  cudaLaunchAttribute a = {};
+  a.id = cudaLaunchAttributeClusterDimension;
+  a.val.clusterDim.x = (unsigned)size;
+  a.val.clusterDim.y = 1;
+  a.val.clusterDim.z = 1;
+  return a;
+}
+
+// The same in clusters of `size` CTAs.
+template <typename... KArgs, typename... Args>
+cudaError_t launch_pdl_clusters(void (*kern)(KArgs...), dim3 grid, dim3 block, size_t smem,
+                                cudaStream_t stream, int size, Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  cudaLaunchAttribute attr[2];
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
+  attr[1] = cluster_attr(size);
+  cfg.attrs = attr;
+  cfg.numAttrs = 2;
+  return cudaLaunchKernelEx(&cfg, kern, std::forward<Args>(args)...);
+}
+
 cudaError_t launch_kv_append(void* k_cache, void* v_cache, const void* k, const void* v,
                              const int64_t* slots, int64_t num_tokens, int64_t num_slots,
                              int64_t row_bytes, unsigned int* err, cudaStream_t stream);
@@ -131,6 +158,9 @@ struct DecodeArgs {
   // Under a window, 0: the balanced split of plan.cuh; n: CTA c takes the (c %
   // n)-th n-th of the stages of segment c / n.
   int32_t parts;
+  // So many parts are a cluster (window_mma.cu, up to 8, a divisor of parts) and merge
+  // their results into one, a segment's output or a record; 0: each CTA leaves a record.
+  int32_t cluster;
 };
 
 // Arguments of the kernels of a windowed decode: a type of its own, so that
@@ -169,6 +199,8 @@ cudaError_t launch_window_merge(int dtype, int head_dim, const WindowArgs& args,
 cudaError_t launch_window_mma(int dtype, int head_dim, int group, const CUtensorMap& tmk,
                               const CUtensorMap& tmv, const DecodeArgs& args, cudaStream_t stream);
 int window_mma_resident_ctas(int dtype, int head_dim, int group);
+// Clusters of `size` (<= 8) of its CTAs that can be resident at once.
+int window_mma_resident_clusters(int dtype, int head_dim, int group, int size);
 
 // CTAs of one wave of the partial kernel (resident CTAs per SM x SMs).
 int decode_resident_ctas(int dtype, int head_dim, int group);

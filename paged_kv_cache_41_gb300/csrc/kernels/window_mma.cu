@@ -19,7 +19,7 @@
 // carries the second term (a weight within 2^-16 of itself).  A 16-row chunk is 32
 // matrix instructions and, loads and waits among them, 340 in all, where the CUDA-core
 // kernel takes 920 for four heads.  Measured: 64 requests, 1024 + 4 rows,
-// 32/8 heads 43.0 us, 6170 GB/s, 91% of a copy's rate; 2000 + 4 rows 97%.
+// 32/8 heads 43.8 us, 6050 GB/s, 89% of a copy's rate; 2000 + 4 rows 78.5 us, 98%.
 //   * warp 2 fetches block ids sixteen stages at a time and fills a ring of 32-row
 //     stages by TMA (the row-group tiles of launch.h, 128-byte swizzle, which
 //     ldmatrix reads without bank conflicts);
@@ -28,7 +28,11 @@
 //     A operand of P V, so they never leave registers;
 //   * the exponent base moves only when a score passes it by 2^8; rows that are
 //     not seen have weight 0, and their V is cleared in the fragments (0 x NaN);
-//   * the two warps merge through the ring at the end.
+//   * the two warps merge through the ring at the end, and the CTAs that share a
+//     segment through distributed shared memory: up to eight parts are a cluster, each CTA
+//     of it merges a share of the outputs, and one launch does the whole decode (one chat
+//     of 516 rows 4.8 us, 8.9 with records and a merging launch; 8 x 16,448 rows, 64/8 heads 81 / 90).
+//     CTAs without a stage leave; the cluster's barriers wait for those that are there.
 // MXFP8 pools: tiles hold codes, and a warp widens them in its fragments, exactly (an
 // E4M3 value times a power of two is a bf16 value).  ldmatrix moves pairs of codes, so
 // a lane gets four codes of consecutive columns where the fragment wants two and two: K
@@ -42,6 +46,7 @@
 // (one to four heads) and tcgen05's widened tiles (eight), 64 requests, window 128 / 1024:
 //   32/8 heads  9.4 / 51.0 us against 12.3 / 69.7;  64/8   9.9 / 51.8 against 42.5 / 115.7;
 //   8/8         9.1 / 50.5 against 8.8 / 47.4 (head_dim 64: 7.7 / 39.4 against 8.5 / 46.0).
+#include <cooperative_groups.h>
 #include <math.h>
 
 #include <type_traits>
@@ -52,10 +57,13 @@
 
 namespace pkv {
 
+namespace cg = cooperative_groups;
+
 namespace {
 
 constexpr int kWmRows = 32;             // rows of a stage
 constexpr int kWmThreads = 3 * 32;      // two warps of matrix work, one of loads
+constexpr int kWmCluster = 8;           // CTAs of a cluster at most
 constexpr float kWmLn2 = 0.6931471805599453f;
 // Bytes of a K (or V) tile, of its scales, and stages of the ring: 48 KiB (32 for
 // head_dim 64 over MXFP8), four CTAs an SM.
@@ -138,6 +146,7 @@ __global__ void __launch_bounds__(kWmThreads, 4)
   constexpr int kAtom = kMx ? 8 * D : D / 64 * 1024;  // bytes of an 8-row group, all columns
   __shared__ uint64_t full[NS], empty[NS];
   __shared__ float sm_m[2][8], sm_l[2][8];
+  __shared__ float sm_lse[8];  // of this part
 
   if (!a.plan_before_wait) pdl_wait();
   pdl_launch_dependents();
@@ -166,6 +175,9 @@ __global__ void __launch_bounds__(kWmThreads, 4)
   }
   __syncthreads();
 
+  const int nt = (seg.len + kWmRows - 1) / kWmRows;
+  const bool all = i0 == 0 && n == nt;
+  float* const om = reinterpret_cast<float*>(ring);  // [2][8][D], later also the part's [G][D]
   bool ok = true;
   int issued = 0;  // stages whose copies warp 2 started
   if (warp == 2) {
@@ -456,7 +468,6 @@ __global__ void __launch_bounds__(kWmThreads, 4)
       sm_l[warp][hd] = l;
     }
     named_barrier_sync(1, 64);  // both are done with the ring
-    float* om = reinterpret_cast<float*>(ring);  // [2][8][D]
     if (hd < G) {
       float* to = om + (warp * 8 + hd) * D;
       if constexpr (kMx) {
@@ -472,9 +483,6 @@ __global__ void __launch_bounds__(kWmThreads, 4)
     }
     named_barrier_sync(1, 64);
     if (ok) {
-      const int nt = (seg.len + kWmRows - 1) / kWmRows;
-      const bool all = i0 == 0 && n == nt;
-      const int64_t rec = 2 * (int64_t)blockIdx.x * G;
       for (int i = t * 4; i < G * D; i += 64 * 4) {
         const int g = i / D, e0 = i % D;
         const float m0 = sm_m[0][g], m1 = sm_m[1][g], M = fmaxf(m0, m1);
@@ -490,12 +498,59 @@ __global__ void __launch_bounds__(kWmThreads, 4)
           *reinterpret_cast<uint2*>(out + i) = make_uint2(pack_bf16(v[0], v[1]), pack_bf16(v[2], v[3]));
           if (e0 == 0 && lse_out) lse_out[g] = lse2 * kWmLn2;
         } else {
-          *reinterpret_cast<float4*>(a.rec_o + rec * D + i) = make_float4(v[0], v[1], v[2], v[3]);
-          if (e0 == 0) a.rec_lse[rec + g] = lse2;
+          *reinterpret_cast<float4*>(om + 16 * D + i) = make_float4(v[0], v[1], v[2], v[3]);
+          if (e0 == 0) sm_lse[g] = lse2;
         }
       }
     }
   }
+  if (all) return;
+  // ---- merge the cluster's parts, each CTA a share of the outputs; CTAs without a
+  // stage have left
+  const int w = (nt + a.parts - 1) / a.parts, parts = (nt + w - 1) / w;  // as direct_stages
+  const int part = blockIdx.x % a.parts, rank = part % a.cluster, np = min(parts - (part - rank), a.cluster);
+  const int64_t rec = 2 * (int64_t)(blockIdx.x / a.cluster) * G;
+  cg::cluster_group cluster = cg::this_cluster();
+  __syncwarp();
+  cluster.sync();
+  for (int u = rank * kWmThreads + t; u < G * D / 4; u += np * kWmThreads) {
+    const int g = u * 4 / D;
+    float l[kWmCluster], M = -INFINITY;
+    float4 x[kWmCluster];
+#pragma unroll
+    for (int i = 0; i < kWmCluster; ++i) {
+      l[i] = -INFINITY;
+      if (i < np) {
+        l[i] = cluster.map_shared_rank(sm_lse, i)[g];
+        x[i] = *reinterpret_cast<const float4*>(cluster.map_shared_rank(om, i) + 16 * D + u * 4);
+      }
+      M = fmaxf(M, l[i] != l[i] ? INFINITY : l[i]);  // NaN is not passed over
+    }
+    float sum = 0.f, y[4] = {};
+#pragma unroll
+    for (int i = 0; i < kWmCluster; ++i) {
+      if (i >= np || l[i] == -INFINITY) continue;
+      const float wt = exp2f(l[i] - M);
+      sum += wt;
+      y[0] = fmaf(wt, x[i].x, y[0]);
+      y[1] = fmaf(wt, x[i].y, y[1]);
+      y[2] = fmaf(wt, x[i].z, y[2]);
+      y[3] = fmaf(wt, x[i].w, y[3]);
+    }
+    const float inv = sum != 0.f ? 1.f / sum : 0.f;
+    const float lse2 = sum != 0.f ? M + log2f(sum) : -INFINITY;
+    if (parts <= a.cluster) {
+      *reinterpret_cast<uint2*>(out + u * 4) =
+          make_uint2(pack_bf16(y[0] * inv, y[1] * inv), pack_bf16(y[2] * inv, y[3] * inv));
+      if (u * 4 % D == 0 && lse_out) lse_out[g] = lse2 * kWmLn2;
+    } else {
+      *reinterpret_cast<float4*>(a.rec_o + rec * D + u * 4) =
+          make_float4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv);
+      if (u * 4 % D == 0) a.rec_lse[rec + g] = lse2;
+    }
+  }
+  __syncwarp();
+  cluster.sync();  // its shared memory has been read
 }
 
 template <bool kMx, int D, int G>
@@ -518,6 +573,30 @@ static int wm_resident() {
   return cached[dev];
 }
 
+// Clusters of `size` CTAs that can be resident at once.
+template <bool kMx, int D, int G>
+static int wm_clusters(int size) {
+  static std::mutex mu;
+  static int cached[64][kWmCluster + 1] = {};  // + 1
+  int dev = 0;
+  if (wm_resident<kMx, D, G>() <= 0 || cudaGetDevice(&dev) != cudaSuccess) return 0;
+  std::lock_guard<std::mutex> lock(mu);
+  int& c = cached[dev][size];
+  if (!c) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)size);
+    cfg.blockDim = dim3(kWmThreads);
+    cfg.dynamicSmemBytes = wm_smem(kMx, D);
+    cudaLaunchAttribute attr = cluster_attr(size);
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    int n = 0;
+    if (cudaOccupancyMaxActiveClusters(&n, window_mma_kernel<kMx, D, G>, &cfg) != cudaSuccess) return 0;
+    c = n + 1;
+  }
+  return c - 1;
+}
+
 template <bool kMx, int D, int G>
 static cudaError_t launch_wm(const CUtensorMap& tmk, const CUtensorMap& tmv, const WindowArgs& a,
                              cudaStream_t stream) {
@@ -526,6 +605,9 @@ static cudaError_t launch_wm(const CUtensorMap& tmk, const CUtensorMap& tmv, con
   static SmemAttrCache attr_cache;
   cudaError_t e = ensure_smem_limit(kern, smem, attr_cache);
   if (e != cudaSuccess) return e;
+  if (a.cluster > 1)
+    return launch_pdl_clusters(kern, dim3((unsigned)a.num_ctas), dim3(kWmThreads), smem, stream, a.cluster, tmk,
+                               tmv, a);
   return launch_pdl(kern, dim3((unsigned)a.num_ctas), dim3(kWmThreads), smem, stream, tmk, tmv, a);
 }
 
@@ -551,6 +633,13 @@ struct ResidentCall {
     return wm_resident<kMx, D, G>();
   }
 };
+struct ClustersCall {
+  int size;
+  template <bool kMx, int D, int G>
+  int operator()() const {
+    return wm_clusters<kMx, D, G>(size);
+  }
+};
 struct LaunchCall {
   const CUtensorMap &tmk, &tmv;
   const WindowArgs& a;
@@ -566,11 +655,15 @@ int window_mma_resident_ctas(int dtype, int head_dim, int group) {
   return wm_sizes(dtype, head_dim, group, ResidentCall{});
 }
 
+int window_mma_resident_clusters(int dtype, int head_dim, int group, int size) {
+  return wm_sizes(dtype, head_dim, group, ClustersCall{size});
+}
+
 cudaError_t launch_window_mma(int dtype, int head_dim, int group, const CUtensorMap& tmk,
                               const CUtensorMap& tmv, const DecodeArgs& args, cudaStream_t stream) {
   const WindowArgs a(args, box_rows_for(args.block_size));
   cudaError_t e = wm_sizes(dtype, head_dim, group, LaunchCall{tmk, tmv, a, stream});
-  if (e != cudaSuccess || a.parts == 1) return e;
+  if (e != cudaSuccess || a.parts == a.cluster) return e;
   return launch_window_merge(dtype, head_dim, a, stream);
 }
 

@@ -541,13 +541,26 @@ struct DecodeSplit {
   int64_t ctas;
   int32_t parts;
   int64_t recording;
+  int32_t cluster;  // parts that merge in a cluster (window_mma.cu)
 };
 
-// Over bf16 and MXFP8 pools every window takes the direct split (window_mma.cu):
-// parts enough for one wave, and of no more rows than this, so that one long sequence
-// among short ones is not one CTA's.  Parts of 2048 rows / segments whole where they
-// fill a wave: 64 x 8192 rows, window 4096 163 / 154 us; one sequence of 65536 rows beside 63
-// of 256, window 4096 48 / 85, 65536 101 / 1202 (parts of 1024 rows 117, 4096 127).
+// Over bf16 and MXFP8 pools every window takes the direct split (window_mma.cu), its
+// parts in clusters of up to kClusterParts CTAs that merge among themselves; several
+// clusters to a segment leave a record each for another launch.  Measured in us, block
+// size 16, head_dim 128, 32/8 heads:
+//   * one cluster against that launch after parts enough for a wave, each leaving a
+//     record: 1 sequence, window 512 4.9 / 9.0, 4096 12.5 / 20.2; 8 sequences, window
+//     512 6.7 / 10.2, 2048 15.1 / 19.9; 32, window 128 6.7 / 9.5;
+constexpr int64_t kClusterParts = 8;
+//   * several where they take more rows than this, per part, off the longest CTA: 1
+//     sequence, window 2048 (232 rows) 10.7 / one cluster 8.0, 4096 (459) 11.0 / 12.5, 8192 12.6 /
+//     21.7; 4, 4096 (258) 19.4 / 17.4; MXFP8, whose rows cost more: 1024 (116) 9.7 / 8.8, 2048 (231)
+//     11.1 / 12.7; 4 sequences, 2048 (130) 15.4 / 16.6;
+constexpr int64_t kGroupRows = 320, kGroupRowsMx = 120;
+//   * and, though it be several waves, enough that a part has no more than about so many rows, so that
+//     one long sequence among short ones is not one cluster's: in parts of 1024, 2048 and 4096
+//     rows, 64 x 8192, window 4096 165 / 156 / 156; 1 sequence of 65536 rows beside 63 of 256, window
+//     16384 74 / 55 / 90, 65536 134 / 109 / 102 (8192 rows: 171).
 constexpr int64_t kPartRows = 2048;
 // Over fp32 pools the direct split wins where its last wave's idle places, shared
 // out over a wave, come to no more rows than the balanced split's plan and merge are
@@ -560,24 +573,39 @@ DecodeSplit decode_split(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_
                          int32_t max_blocks, int32_t partition_size, int32_t window, int32_t num_sinks) {
   if (window <= 0) {
     const int64_t C = decode_ctas(c, num_seqs, num_q_heads, max_blocks, partition_size);
-    return {C, 0, C};
+    return {C, 0, C, 0};
   }
   const int G = num_q_heads / c->num_kv_heads;
   // dense rows of a sequence at most: whole boxes of the sinks and, the window
   // beginning anywhere in one, of the window
-  const int64_t B = c->block_size < pkv::decode_tc_rows() ? c->block_size : pkv::decode_tc_rows();
+  const int64_t B = pkv::box_rows_for(c->block_size);
   const int64_t seen = ((int64_t)num_sinks + B - 1) / B * B + (int64_t)window + B;
   const int64_t rows = std::min(seen, (int64_t)max_blocks * c->block_size);
   const int64_t segs = (int64_t)num_seqs * c->num_kv_heads;
   const int64_t stages = (rows + pkv::kStageRows - 1) / pkv::kStageRows;
   auto direct = [&](int64_t parts) {
-    return DecodeSplit{segs * parts, (int32_t)parts, parts > 1 ? segs * parts : 0};
+    return DecodeSplit{segs * parts, (int32_t)parts, parts > 1 ? segs * parts : 0, 0};
   };
   if (c->dtype != PKV_F32) {
     int64_t resident = pkv::window_mma_resident_ctas(c->dtype, c->head_dim, G);
     if (resident <= 0) resident = 4LL * sm_count();
-    const int64_t wave = resident / segs, cut = (rows + kPartRows - 1) / kPartRows;
-    return direct(std::max<int64_t>(std::min(std::max(wave, cut), stages), 1));
+    auto fit = [&](int64_t size) -> int64_t {  // clusters a segment can have in one wave
+      if (size == 1) return resident / segs;
+      const int n = pkv::window_mma_resident_clusters(c->dtype, c->head_dim, G, (int)size);
+      return (n > 0 ? n : resident * 7 / 8 / size) / segs;
+    };
+    int64_t size = std::min(stages, kClusterParts), groups = fit(size);
+    groups = std::min(groups, (stages + size - 1) / size);
+    if (rows * (groups - 1) <= (c->dtype == PKV_MXFP8 ? kGroupRowsMx : kGroupRows) * size * groups)
+      groups = std::min<int64_t>(groups, 1);
+    for (; groups == 0 && size > 1; groups = fit(size)) --size;
+    groups = std::max<int64_t>(groups, 1);
+    const int64_t cut = (rows + kPartRows * 3 / 4) / kPartRows;  // a quarter more is borne
+    if (size * groups < cut) {
+      size = std::min(cut, kClusterParts);
+      groups = (cut + size - 1) / size;
+    }
+    return {segs * size * groups, (int32_t)(size * groups), groups > 1 ? segs * groups : 0, (int32_t)size};
   }
   int64_t resident = pkv::decode_resident_ctas(c->dtype, c->head_dim, G);
   if (resident <= 0) resident = 2LL * sm_count();
@@ -587,7 +615,7 @@ DecodeSplit decode_split(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_
     return direct(parts);
   const int64_t blocks = (rows + c->block_size - 1) / c->block_size;
   const int64_t C = decode_ctas(c, num_seqs, num_q_heads, (int32_t)blocks, 0);
-  return {C, 0, C};
+  return {C, 0, C, 0};
 }
 
 // The paged decode; with `scores` it also leaves every row's base-2 scores
@@ -646,6 +674,7 @@ pkv_status decode_checked(const pkv_cache_desc* cache, void* out, float* lse, co
   a.window = window;
   a.num_sinks = num_sinks;
   a.parts = split.parts;
+  a.cluster = split.cluster;
   return launch_decode(cache, G, q, k_cache, v_cache, a, as_stream(stream));
 }
 

@@ -285,3 +285,16 @@ def test_scores_of_minus_infinity_weigh_nothing(dtype, window, n):
     assert pkv.get_device_error() == 0
     w.check(out, lse)
     assert (out[1] == 0).all() and torch.isneginf(lse[1]).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "mxfp8"])
+@pytest.mark.parametrize("hq,hkv,d", [(4, 1, 128), (8, 1, 128), (2, 2, 64), (16, 2, 128)])
+@pytest.mark.parametrize("window", [20, 100, 250, 1000, 6000])
+def test_segments_of_several_ctas(dtype, hq, hkv, d, window):
+    # parts of one cluster, of several, and sequences too short to have them all
+    Window([7000, 0, 1, 33, 300, 5000, 255, 257], window, 5, dtype=dtype, hq=hq, hkv=hkv, d=d, seed=window).run()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "mxfp8"])
+def test_segments_of_several_ctas_in_several_waves(dtype):
+    Window([9000] + [40] * 700, 8000, 3, dtype=dtype, hq=4, hkv=1, d=64, seed=5).run()

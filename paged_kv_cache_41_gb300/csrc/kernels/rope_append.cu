@@ -107,7 +107,7 @@ __launch_bounds__(kRopeThreads, kRows == 4 && sizeof(T) == 2 ? (kMx ? 8 : 9) : 1
   const int Hq = a.num_q_heads, Hkv = a.num_kv_heads;
   const int qparts = (Hq + kRows - 1) / kRows, kparts = (Hkv + kRows - 1) / kRows;
   const int parts = qparts + 2 * kparts;
-  const unsigned g = (blockIdx.x * (unsigned)kRopeThreads + threadIdx.x) / LPR;  // below 2^31
+  const unsigned g = blockIdx.x * (unsigned)(kRopeThreads / LPR) + threadIdx.x / LPR;  // at most 2^29
   const int l = threadIdx.x % LPR;
   const unsigned lanes = (LPR == 32 ? 0xffffffffu : ((1u << LPR) - 1)) << ((threadIdx.x & 31) / LPR * LPR);
   const unsigned tok32 = g / (unsigned)parts;

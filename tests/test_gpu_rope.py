@@ -300,3 +300,20 @@ def test_large_offsets():
     got = kc.view(-1, 8, 128)[torch.from_numpy(r.slots).cuda()]
     assert torch.equal(got, small.kc.view(-1, 8, 128)[[2, 0, 1]])
     assert torch.equal(vc.view(-1, 8, 128)[torch.from_numpy(r.slots).cuda()], r.v)
+
+
+def test_more_lanes_than_32_bits_count():
+    # three groups of sixteen lanes a token; all tokens but the ends are padding
+    n, ends = (1 << 28) // 3 + 1000, 6
+    if torch.cuda.mem_get_info()[0] < 90 << 30:
+        pytest.skip("69 GB of rows")
+    r = Rope(2 * ends, hq=1, hkv=1, d=128, seed=11)
+    q, k, v = (torch.empty(n, 1, 128, dtype=torch.bfloat16, device="cuda") for _ in range(3))
+    slots = torch.full((n,), -1, dtype=torch.int64, device="cuda")
+    pos = torch.full((n,), -1, dtype=torch.int32, device="cuda")
+    for big, small in ((q, r.q), (k, r.k), (v, r.v), (slots, torch.from_numpy(r.slots)), (pos, torch.from_numpy(r.pos[0]))):
+        big[:ends], big[-ends:] = small[:ends].to(big.device), small[ends:].to(big.device)
+    pkv.qk_norm_rope_append(q, k, v, r.kc, r.vc, slots, pos, torch.from_numpy(r.table).cuda(), q_weight=r.wq,
+                            k_weight=r.wk, eps=r.eps, out=q)
+    assert pkv.get_device_error() == 0
+    r.check(torch.cat([q[:ends], q[-ends:]]))

@@ -562,6 +562,10 @@ constexpr int64_t kGroupRows = 320, kGroupRowsMx = 120;
 //     rows, 64 x 8192, window 4096 165 / 156 / 156; 1 sequence of 65536 rows beside 63 of 256, window
 //     16384 74 / 55 / 90, 65536 134 / 109 / 102 (8192 rows: 171).
 constexpr int64_t kPartRows = 2048;
+//   * but no more of them than about so many waves: a table may be wide for sequences that
+//     are short, and CTAs without a stage cost time too (64 of 256 rows in a table for
+//     1,600,000, every row seen: 60 us with the limit, 452 without).
+constexpr int64_t kPartWaves = 8;
 // Over fp32 pools the direct split wins where its last wave's idle places, shared
 // out over a wave, come to no more rows than the balanced split's plan and merge are
 // worth: 512 segments on 304 places, window 128 21.6 us against 24.5 balanced, 512
@@ -600,7 +604,8 @@ DecodeSplit decode_split(const pkv_cache_desc* c, int32_t num_seqs, int32_t num_
       groups = std::min<int64_t>(groups, 1);
     for (; groups == 0 && size > 1; groups = fit(size)) --size;
     groups = std::max<int64_t>(groups, 1);
-    const int64_t cut = (rows + kPartRows * 3 / 4) / kPartRows;  // a quarter more is borne
+    const int64_t cut = std::min((rows + kPartRows * 3 / 4) / kPartRows,  // a quarter more is borne
+                                 kPartWaves * resident / segs);
     if (size * groups < cut) {
       size = std::min(cut, kClusterParts);
       groups = (cut + size - 1) / size;

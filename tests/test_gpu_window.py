@@ -298,3 +298,8 @@ def test_segments_of_several_ctas(dtype, hq, hkv, d, window):
 @pytest.mark.parametrize("dtype", ["bf16", "mxfp8"])
 def test_segments_of_several_ctas_in_several_waves(dtype):
     Window([9000] + [40] * 700, 8000, 3, dtype=dtype, hq=4, hkv=1, d=64, seed=5).run()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32", "mxfp8"])
+def test_wide_tables(dtype):
+    Window([100, 0, 900] + [20] * 30, 2**31 - 1, 0, dtype=dtype, hq=4, hkv=1, d=64, width=100000, seed=6).run()

@@ -644,6 +644,12 @@ def kv_compact(k_cache, v_cache, block_tables, seq_lens, keep, keep_lens, *, bas
         "pkv_kv_compact")
 
 
+def _window_sizes(window, num_sinks):
+    """Check what ctypes would cut to 32 bits."""
+    if not (window < 2**31 and num_sinks < 2**31):
+        raise ValueError(f"window and num_sinks must be below 2**31, got {window} and {num_sinks}")
+
+
 def kv_blocks_update(k_cache, block_tables, seq_lens, add, free_ids, free_count, *, base_lens=None,
                      num_sinks=0, window=0, num_rows=None, out_lens=None, row_ptr=None, slots=None,
                      positions=None, free_count_out=None, stream=None):
@@ -660,6 +666,7 @@ def kv_blocks_update(k_cache, block_tables, seq_lens, add, free_ids, free_count,
     [B], row_ptr int32 [B + 1], slots int64 [num_rows], positions int32
     [num_rows]); out_lens must not be one of the inputs."""
     desc = cache_desc(k_cache)
+    _window_sizes(window, num_sinks)
     b, max_blocks = block_tables.shape
     _dense("block_tables", block_tables, torch.int32, (b, max_blocks))
     _dense("seq_lens", seq_lens, torch.int32, (b,))
@@ -706,6 +713,7 @@ def kv_blocks_update(k_cache, block_tables, seq_lens, add, free_ids, free_count,
 def decode_window_workspace_bytes(k_cache, num_seqs, num_q_heads, max_blocks_per_seq, window,
                                   num_sinks=0) -> int:
     desc = cache_desc(k_cache)
+    _window_sizes(window, num_sinks)
     return load_library().pkv_decode_window_workspace_bytes(
         ctypes.byref(desc), num_seqs, num_q_heads, max_blocks_per_seq, window, num_sinks)
 
@@ -717,6 +725,7 @@ def paged_attention_decode_window(q, k_cache, v_cache, block_tables, seq_lens, s
     without one may have been given back.  Returns out (and writes lse [B, Hq] float32 when
     given)."""
     desc = _pair_desc(k_cache, v_cache)
+    _window_sizes(window, num_sinks)
     b, hq, d = q.shape
     _, max_blocks = block_tables.shape
     _dense("q", q, _io_dtype(desc), (b, hq, desc.head_dim))

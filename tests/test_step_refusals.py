@@ -174,3 +174,17 @@ def test_binding_refuses_host_tensors_and_wrong_shapes(lib):
         with pytest.raises(ValueError) as e:
             f(**o)
         assert "current CUDA device" not in str(e.value), o
+
+
+@pytest.mark.parametrize("size", [2**31, 2**32 + 7, 2**40])
+def test_binding_refuses_windows_past_32_bits(lib, size):
+    i32 = lambda *s: torch.zeros(s, dtype=torch.int32)
+    kc = torch.zeros(4, 16, 2, 64)
+    q = torch.zeros(1, 4, 64)
+    for kw in (dict(window=size), dict(window=5, num_sinks=size)):
+        with pytest.raises(ValueError, match="2\\*\\*31"):
+            pkv.paged_attention_decode_window(q, kc, kc, i32(1, 2), i32(1), 1.0, **kw)
+        with pytest.raises(ValueError, match="2\\*\\*31"):
+            pkv.decode_window_workspace_bytes(kc, 1, 4, 2, kw["window"], kw.get("num_sinks", 0))
+        with pytest.raises(ValueError, match="2\\*\\*31"):
+            pkv.kv_blocks_update(kc, i32(1, 2), i32(1), i32(1), i32(4), i32(1), num_rows=1, **kw)

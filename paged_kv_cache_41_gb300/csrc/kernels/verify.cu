@@ -383,6 +383,7 @@ __global__ void __launch_bounds__(kVfThreads, 4) draft_verify_kernel(const Verif
     return sum;
   };
   if (taken_out) {
+    __syncthreads();  // every warp has added all[] up
     if (t < S) {
       const int from = (int)min((int64_t)t * per, (int64_t)V);
       all[t] -= out_of(from, min(from + per, V));

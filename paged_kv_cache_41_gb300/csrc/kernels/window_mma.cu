@@ -16,7 +16,7 @@
 //   S [16 x 16 rows]  = Q [16 heads x D] K^T,     heads 8 .. 15 zero
 //   O [16 x D]       += P [16 x 16 rows] V,       heads 0 .. 7 the upper bf16 term
 // of the weights, 8 .. 15 what it leaves of them, so that the unused half of the tile
-// carries the second term (a weight within 2^-16 of itself).  A 16-row chunk is 32
+// carries the second term (a weight within 2^-16 + 2^-23 of itself).  A 16-row chunk is 32
 // matrix instructions and, loads and waits among them, 340 in all, where the CUDA-core
 // kernel takes 920 for four heads.  Measured: 64 requests, 1024 + 4 rows,
 // 32/8 heads 43.8 us, 6050 GB/s, 89% of a copy's rate; 2000 + 4 rows 78.5 us, 98%.
@@ -387,12 +387,14 @@ __global__ void __launch_bounds__(kWmThreads, 4)
           p[e] = p[e] == -INFINITY ? 0.f : exp2f(p[e] - m);
           l += p[e];
         }
-        // two bf16 terms: a weight's upper half, cut off (so that neither term is
-        // negative and an infinity of V stays one), and what that leaves
+        // two bf16 terms: a weight's upper half, cut off, and what that leaves of p (1 +
+        // 2^-23).  Neither is negative, nor 0 (above 2^-103) unless the weight is, so
+        // that an infinity of V stays one in both products.
+        constexpr float kMore = 1.f + 0x1p-23f;
         const uint32_t hi0 = __byte_perm(__float_as_uint(p[0]), __float_as_uint(p[1]), 0x7632);
         const uint32_t hi1 = __byte_perm(__float_as_uint(p[2]), __float_as_uint(p[3]), 0x7632);
-        const uint32_t lo0 = pack_bf16(p[0] - bf16lo(hi0), p[1] - bf16hi(hi0));
-        const uint32_t lo1 = pack_bf16(p[2] - bf16lo(hi1), p[3] - bf16hi(hi1));
+        const uint32_t lo0 = pack_bf16(fmaf(p[0], kMore, -bf16lo(hi0)), fmaf(p[1], kMore, -bf16hi(hi0)));
+        const uint32_t lo1 = pack_bf16(fmaf(p[2], kMore, -bf16lo(hi1)), fmaf(p[3], kMore, -bf16hi(hi1)));
         // ---- P V; V of rows that are not seen is cleared
         uint32_t keep0 = 0xffffffffu, keep1 = 0xffffffffu;
         if (!whole) {

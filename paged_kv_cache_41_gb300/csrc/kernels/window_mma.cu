@@ -34,7 +34,7 @@
 //     of 516 rows 4.8 us, 8.9 with records and a merging launch; 8 x 16,448 rows, 64/8 heads 81 / 90).
 //     CTAs without a stage leave; the cluster's barriers wait for those that are there.
 // MXFP8 pools: tiles hold codes, and a warp widens them in its fragments, exactly (an
-// E4M3 value times a power of two is a bf16 value).  ldmatrix moves pairs of codes, so
+// E4M3 value times a power of two is a bf16 value, those from 2^-126 up).  ldmatrix moves pairs of codes, so
 // a lane gets four codes of consecutive columns where the fragment wants two and two: K
 // is contracted in that order of columns (q is loaded so), and V's tiles are the even
 // and the odd columns of sixteen.  K's scales multiply the scores of their 32 columns,
@@ -339,10 +339,12 @@ __global__ void __launch_bounds__(kWmThreads, 4)
               }
 #pragma unroll
               for (int e = 0; e < 4; ++e) {
-                const float f = rare.value
-                                    ? e8m0_value((ksc[e] >> (8 * g)) & 0xffu)
-                                    : __uint_as_float((g == 3 ? ksc[e] >> 1 : ksc[e] << (23 - 8 * g)) & 0x7f800000u);
-                sc[e >> 1][e & 1] = fmaf(part[e >> 1][e & 1], f, sc[e >> 1][e & 1]);
+                // 0 is 2^-127, which fp32 here takes for 0: 2^-126 and a half of it
+                const bool least = rare.value && ((ksc[e] >> (8 * g)) & 0xffu) == 0;
+                const float f = least ? 0x1p-126f
+                                      : __uint_as_float((g == 3 ? ksc[e] >> 1 : ksc[e] << (23 - 8 * g)) & 0x7f800000u);
+                const float x = part[e >> 1][e & 1];
+                sc[e >> 1][e & 1] = fmaf(least ? 0.5f * x : x, f, sc[e >> 1][e & 1]);
               }
             }
           };

@@ -1,5 +1,5 @@
-"""pkv_paged_attention_decode_window: infinities of V in rows that are seen, and
-the two bf16 terms that a weight is held in."""
+"""pkv_paged_attention_decode_window: infinities of V in rows that are seen, the two
+bf16 terms that a weight is held in, and the smallest K scale."""
 import numpy as np
 import pytest
 import torch
@@ -105,3 +105,18 @@ def test_few_keys_of_opposite_values(dtype, hq):
             w.c.v.view(-1, 2, 128)[b] = -w.c.v.view(-1, 2, 128)[a]
     w.reread()
     w.run()
+
+
+@pytest.mark.parametrize("hq,d", [(1, 64), (2, 64), (4, 128), (8, 128)])
+@pytest.mark.parametrize("lens,window", [([3, 50, 200], 70), ([3000, 1], 2500)])
+def test_keys_of_the_smallest_scale(hq, d, lens, window):
+    # K scales of 2^-127 against queries of about 2^112: scores of ordinary size
+    w = Exact(lens, window, 2, dtype="mxfp8", hq=hq, hkv=1, d=d, seed=d)
+    w.c.k.scales.zero_()
+    w.q.copy_((w.q.float() * 2.0 ** 112).to(w.q.dtype))
+    w.scale = 6.0
+    w.reread()
+    out, lse = w.call()
+    assert pkv.get_device_error() == 0
+    w.check(out, lse)
+    assert (lse[1].exp() / min(lens[1], window + 2) - 1).abs().max() > 1e-3 or lens[1] < 3  # not all of score 0

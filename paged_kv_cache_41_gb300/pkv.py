@@ -646,8 +646,8 @@ def kv_compact(k_cache, v_cache, block_tables, seq_lens, keep, keep_lens, *, bas
 
 def _window_sizes(window, num_sinks):
     """Check what ctypes would cut to 32 bits."""
-    if not (window < 2**31 and num_sinks < 2**31):
-        raise ValueError(f"window and num_sinks must be below 2**31, got {window} and {num_sinks}")
+    if not (-2**31 <= window < 2**31 and -2**31 <= num_sinks < 2**31):
+        raise ValueError(f"window and num_sinks must be within +-2**31, got {window} and {num_sinks}")
 
 
 def kv_blocks_update(k_cache, block_tables, seq_lens, add, free_ids, free_count, *, base_lens=None,

@@ -644,10 +644,11 @@ def kv_compact(k_cache, v_cache, block_tables, seq_lens, keep, keep_lens, *, bas
         "pkv_kv_compact")
 
 
-def _window_sizes(window, num_sinks):
+def _sizes(**sizes):
     """Check what ctypes would cut to 32 bits."""
-    if not (-2**31 <= window < 2**31 and -2**31 <= num_sinks < 2**31):
-        raise ValueError(f"window and num_sinks must be within +-2**31, got {window} and {num_sinks}")
+    for name, x in sizes.items():
+        if not -2**31 <= x < 2**31:
+            raise ValueError(f"{name} must be within +-2**31, got {x}")
 
 
 def kv_blocks_update(k_cache, block_tables, seq_lens, add, free_ids, free_count, *, base_lens=None,
@@ -666,8 +667,8 @@ def kv_blocks_update(k_cache, block_tables, seq_lens, add, free_ids, free_count,
     [B], row_ptr int32 [B + 1], slots int64 [num_rows], positions int32
     [num_rows]); out_lens must not be one of the inputs."""
     desc = cache_desc(k_cache)
-    _window_sizes(window, num_sinks)
     b, max_blocks = block_tables.shape
+    _sizes(window=window, num_sinks=num_sinks, max_blocks=max_blocks)
     _dense("block_tables", block_tables, torch.int32, (b, max_blocks))
     _dense("seq_lens", seq_lens, torch.int32, (b,))
     _dense("add", add, torch.int32, (b,))
@@ -713,7 +714,8 @@ def kv_blocks_update(k_cache, block_tables, seq_lens, add, free_ids, free_count,
 def decode_window_workspace_bytes(k_cache, num_seqs, num_q_heads, max_blocks_per_seq, window,
                                   num_sinks=0) -> int:
     desc = cache_desc(k_cache)
-    _window_sizes(window, num_sinks)
+    _sizes(window=window, num_sinks=num_sinks, num_seqs=num_seqs, num_q_heads=num_q_heads,
+           max_blocks_per_seq=max_blocks_per_seq)
     return load_library().pkv_decode_window_workspace_bytes(
         ctypes.byref(desc), num_seqs, num_q_heads, max_blocks_per_seq, window, num_sinks)
 
@@ -725,9 +727,9 @@ def paged_attention_decode_window(q, k_cache, v_cache, block_tables, seq_lens, s
     without one may have been given back.  Returns out (and writes lse [B, Hq] float32 when
     given)."""
     desc = _pair_desc(k_cache, v_cache)
-    _window_sizes(window, num_sinks)
     b, hq, d = q.shape
     _, max_blocks = block_tables.shape
+    _sizes(window=window, num_sinks=num_sinks, max_blocks=max_blocks)
     _dense("q", q, _io_dtype(desc), (b, hq, desc.head_dim))
     _dense("block_tables", block_tables, torch.int32, (b, max_blocks))
     _dense("seq_lens", seq_lens, torch.int32, (b,))
@@ -790,6 +792,7 @@ def qk_norm_rope_append(q, k, v, k_cache, v_cache, slot_mapping, positions, cos_
     rot = 0
     if cos_sin is not None:
         rot = cos_sin.shape[-1]
+        _sizes(rot=rot, positions=cos_sin.shape[0])
         _dense("cos_sin", cos_sin, torch.float32, (cos_sin.shape[0], rot))
     if axis_of is not None:
         axis_of = bytes(axis_of)
@@ -837,6 +840,7 @@ def draft_verify(target_probs, draft_tokens, draft_ptr, uniforms, *, max_draft, 
     kv_compact; keep_lens int32 [B]; next_tokens int32 [B])."""
     rows, vocab = target_probs.shape
     b = draft_ptr.shape[0] - 1
+    _sizes(max_draft=max_draft, vocab=vocab, rows=rows)
     target_stride = _prob_rows("target_probs", target_probs, rows, vocab)
     draft_stride = 0 if draft_probs is None else _prob_rows("draft_probs", draft_probs, rows, vocab)
     _dense("draft_tokens", draft_tokens, torch.int32, (rows,))

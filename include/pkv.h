@@ -631,9 +631,10 @@ pkv_status pkv_kv_compact(const pkv_cache_desc* cache, void* k_cache, void* v_ca
  *                  tree are rotated by their depth instead).
  * A request whose growth does not find free blocks (requests are served in
  * order; those that need none always are), or whose rows pass num_rows, keeps its length
- * and table, its rows (below num_rows) get -1, and PKV_DEVERR_POOL or
- * PKV_DEVERR_LENGTH is set; so does one whose lengths are negative or pass its
- * table row (PKV_DEVERR_LENGTH; it has no rows).  An id outside the pool sets
+ * and the blocks that a decode at it sees (those behind the window go all the same,
+ * before it is known who is served), its rows (below num_rows) get -1, and
+ * PKV_DEVERR_POOL or PKV_DEVERR_LENGTH is set.  One whose lengths are negative or pass
+ * its table row keeps its length and whole table and has no rows (PKV_DEVERR_LENGTH).  An id outside the pool sets
  * PKV_DEVERR_BLOCK: given back it is dropped, taken it becomes -1.
  * Exact and deterministic.  Any block_size; num_blocks and num_rows <= INT32_MAX;
  * num_seqs <= 65535. */

@@ -27,8 +27,18 @@ namespace pkv {
 namespace {
 
 constexpr int kBlRowThreads = 256;
-// Rows whose slots the one CTA writes itself.
-constexpr int64_t kBlOwnRows = 4096;
+// Rows whose slots the one CTA writes itself; more are a second launch's.  By itself
+// against that, 1024 threads, us: 8 requests, 1024 rows 5.4 / 6.1, 2048 6.8 / 6.2,
+// 4096 9.1 / 6.6; 64 requests, 2048 6.9 / 7.3, 2560 7.9 / 7.4; 256, 2048 5.8 / 7.0, 2560
+// 8.2 / 8.2; 512, 2048 6.1 / 7.4, 3072 7.1 / 7.5, 4096 8.2 / 7.3.
+constexpr int64_t kBlOwnRows = 2048;
+// Requests (one a thread, one pass) and rows of a call that 128 threads take; 1024
+// take any other.  128 against 1024, us: 1 request, 128 rows 4.0 / 5.2, 256 4.7 / 5.2, 320
+// 5.6 / 5.4, 512 6.3 / 5.6; 64 requests, 128 rows 3.4 / 4.3, 256 4.0 / 4.2, 320 4.8 /
+// 4.4, 512 5.5 / 4.4; 128 requests, 256 rows 4.2 / 4.4, 384 4.8 / 4.4; 192 requests, 192
+// rows (two passes) 7.6 / 4.2.
+constexpr int kBlFewSeqs = 128;
+constexpr int64_t kBlFewRows = 256;
 
 struct Sum3 {
   long long a, b, c;
@@ -415,10 +425,9 @@ __global__ void __launch_bounds__(kThreads) blocks_update_kernel(const BlocksArg
 
 cudaError_t launch_blocks_update(const BlocksArgs& a, cudaStream_t stream) {
   const int own = a.num_rows <= kBlOwnRows ? 1 : 0;
-  // a step of few requests and rows; a call without rows gives ids back, of
-  // which there may be thousands
-  if (a.num_seqs <= 128 && a.num_rows > 0 && a.num_rows <= 1024)
-    blocks_update_kernel<128><<<1, 128, 0, stream>>>(a, own);
+  // a call without rows gives ids back, of which there may be thousands
+  if (a.num_seqs <= kBlFewSeqs && a.num_rows > 0 && a.num_rows <= kBlFewRows)
+    blocks_update_kernel<kBlFewSeqs><<<1, kBlFewSeqs, 0, stream>>>(a, own);
   else
     blocks_update_kernel<1024><<<1, 1024, 0, stream>>>(a, own);
   cudaError_t e = cudaGetLastError();

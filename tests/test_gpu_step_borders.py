@@ -1,0 +1,18 @@
+"""The step's operators on either side of the sizes where another kernel takes over."""
+import numpy as np
+import pytest
+
+from test_gpu_blocks import Step
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("batch", [1, 127, 128, 129])
+@pytest.mark.parametrize("rows", [255, 256, 257, 2047, 2048, 2049])
+def test_block_updates_of_so_many_rows(batch, rows):
+    rng = np.random.default_rng(rows + batch)
+    s = Step(rng.integers(0, 60, batch), 2100 // 16 + 60 // 16 + 2, spare=rows // 16 + batch + 1, seed=batch)
+    add = np.bincount(rng.integers(0, batch, rows - 2), minlength=batch)
+    old = s.lens_np.copy()
+    s.update("lens", add, rows)                    # two rows of padding
+    s.update(old, add // 2, 0)

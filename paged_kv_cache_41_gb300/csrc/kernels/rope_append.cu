@@ -36,6 +36,15 @@ constexpr int kRopeThreads = 128;
 // without, 124.2 / 123.0 / 123.4 / 125.4 with 300 / 600 / 1000 / 1500 of them
 // between, 166 with 3000.
 constexpr int64_t kRopeAheadBytes = 8 << 20;
+// Elements of q, k and v up to which a group of lanes takes one head row, so that
+// every SM has some; above, four, so that a token's weights and angles are multiplied
+// once for four.  One against four, us, 32/8 heads, by millions of elements:
+//   bf16, head_dim 128: 0.75 2.6 / 2.9, 1 2.90 / 2.91, 1.25 3.4 / 3.2, 2.5 4.9 / 3.7;
+//   64/8 heads, head_dim 64: 1 2.9 / 3.1, 1.25 3.2 / 3.2, 2.5 4.7 / 3.6;
+//   fp32, head_dim 128: 0.75 3.07 / 3.10, 1 3.3 / 3.2, 2.5 5.2 / 4.0; 64: 1 3.1 / 3.1, 1.25 3.4 / 3.3;
+//   MXFP8, head_dim 128: 1 3.4 / 4.4, 2 4.8 / 4.9, 2.5 5.4 / 5.1, 5 8.6 / 7.6;
+//   64: 1 3.0 / 5.3, 4 7.1 / 7.9, 8 13.0 / 13.3, 16 25.6 / 23.7; 64/8 heads 4 7.0 / 7.1, 8 13.2 / 12.1.
+constexpr int64_t rope_few(bool mx, int d) { return mx ? (d == 128 ? 2200000 : 6000000) : 1100000; }
 
 // Four consecutive elements as they lie in memory.
 template <typename T>
@@ -98,8 +107,9 @@ __device__ __forceinline__ void store_mx(const RopeArgs& a, void* cache, const f
 // its parts, the first ceil(Hq / kRows) are q's, then come k's and v's.
 // kWhole: the whole head is rotated (rot = D), so that no lane asks whether its
 // elements are: 32768 tokens 123.8 us, 125.2 where they ask.
-// Four rows of 16-bit elements: 56 registers, nine CTAs an SM (32768 tokens: 138
-// us; with eight or ten CTAs 146); quantising takes eight.
+// Four rows of 16-bit elements: 56 registers, nine CTAs an SM (32768 tokens 122 us; with
+// eight CTAs 127, ten 125); quantising takes eight (8192 tokens 44.3 us; with seven
+// 45.3).
 template <typename T, bool kMx, int D, bool kInter, int kRows, bool kWhole>
 __global__ void
 __launch_bounds__(kRopeThreads, kRows == 4 && sizeof(T) == 2 ? (kMx ? 8 : 9) : 1)
@@ -323,9 +333,7 @@ static cudaError_t launch_rope_t(const RopeArgs& args, cudaStream_t stream) {
   RopeArgs a = args;
   const int64_t H = a.num_q_heads + 2 * (int64_t)a.num_kv_heads;
   const int per_cta = kRopeThreads / (D / 8);
-  // Few rows: one a group, so that every SM has some.  Many: four, so that a
-  // token's angles are read once for four.
-  const bool few = a.num_tokens * H <= 20000;
+  const bool few = a.num_tokens * H * D <= rope_few(kMx, D);
   const int64_t groups =
       a.num_tokens * (few ? H : (a.num_q_heads + 3) / 4 + 2 * ((a.num_kv_heads + 3) / 4));
   const unsigned grid = (unsigned)((groups + per_cta - 1) / per_cta);

@@ -3,6 +3,7 @@ import numpy as np
 import pytest
 
 from test_gpu_blocks import Step
+from test_gpu_rope import Rope
 
 pytestmark = pytest.mark.gpu
 
@@ -16,3 +17,12 @@ def test_block_updates_of_so_many_rows(batch, rows):
     old = s.lens_np.copy()
     s.update("lens", add, rows)                    # two rows of padding
     s.update(old, add // 2, 0)
+
+
+@pytest.mark.parametrize("dtype,d,border", [("bf16", 128, 1100000), ("bf16", 64, 1100000), ("f32", 128, 1100000),
+                                            ("f32", 64, 1100000), ("mxfp8", 128, 2200000), ("mxfp8", 64, 6000000)])
+@pytest.mark.parametrize("rot", [0, 32, None])
+def test_rotations_of_so_many_elements(dtype, d, border, rot):
+    n = border // (d * 12)       # 8/2 heads: one head row a group of lanes up to here
+    for tokens in (n, n + 1):
+        Rope(tokens, dtype=dtype, hq=8, hkv=2, d=d, rot=rot, seed=tokens).run()

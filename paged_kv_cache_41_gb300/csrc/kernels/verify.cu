@@ -40,6 +40,7 @@ namespace {
 constexpr int kVfThreads = 256;
 constexpr int kVfWarps = kVfThreads / 32;
 constexpr int kVfMaxCluster = 8;
+constexpr int kVfWave = 560;  // CTAs that run at once; clusters of eight do not fill all 608 places
 constexpr int kVfNodes = 64;  // PKV_MAX_DRAFT
 static_assert(kVfWarps * kVfMaxCluster <= 64, "a warp holds two segments' sums a lane");
 typedef unsigned long long u64;
@@ -450,10 +451,16 @@ __global__ void __launch_bounds__(kVfThreads, 4) draft_verify_kernel(const Verif
 }
 
 cudaError_t launch_draft_verify(const VerifyArgs& a, cudaStream_t stream) {
-  // CTAs of a request: enough to fill the GPU about three times over with few
-  // requests, but no segment below a warp's four loads
+  // CTAs of a request: no more than run at once (four an SM, in clusters), and no warp's
+  // segment below 64 elements of the vocabulary (each is whole steps of 128, so some may
+  // be empty).  With 1 / 2 / 4 / 8 CTAs, us, chains of 3:
+  //   131072 words: 64 requests 58 / 33 / 22 / 17.0, 70 58 / 33 / 22 / 17.5, 76 59 / 34 / 23 /
+  //   24, 140 64 / 39 / 28 / 32, 152 65 / 40 / 41 / 39; 32000 words: 256 22 / 17.2 / 22 / 32,
+  //   304 23.1 / 18.6 / 28 / 40, 330 24.6 / 27.2 / 30 / 42;
+  //   16 requests: 600 words 5.5 / 5.6 / 5.5 / 5.8, 1200 6.4 / 5.8 / 6.0 / 5.9, 2400 6.6 / 6.4 / 5.9 /
+  //   5.9, 5000 7.4 / 7.0 / 6.4 / 5.9; 64 requests: 600 5.6 / 5.8 / 6.2 / 7.1, 2400 6.8 / 6.8 / 6.2 / 7.2.
   int C = 1;
-  while (C < kVfMaxCluster && (int64_t)a.num_seqs * C * 2 <= 512 && (int64_t)C * kVfThreads * 8 < a.vocab)
+  while (C < kVfMaxCluster && (int64_t)a.num_seqs * C * 2 <= kVfWave && C * 4 * kVfThreads < a.vocab)
     C *= 2;
   const bool vec = a.target_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(a.target) & 15u) == 0 &&
                    (!a.draft || (a.draft_stride % 4 == 0 && (reinterpret_cast<uintptr_t>(a.draft) & 15u) == 0));

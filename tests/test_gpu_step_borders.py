@@ -4,6 +4,7 @@ import pytest
 
 from test_gpu_blocks import Step
 from test_gpu_rope import Rope
+from test_gpu_verify import Verify
 
 pytestmark = pytest.mark.gpu
 
@@ -26,3 +27,15 @@ def test_rotations_of_so_many_elements(dtype, d, border, rot):
     n = border // (d * 12)       # 8/2 heads: one head row a group of lanes up to here
     for tokens in (n, n + 1):
         Rope(tokens, dtype=dtype, hq=8, hkv=2, d=d, rot=rot, seed=tokens).run()
+
+
+@pytest.mark.parametrize("vocab", [1023, 1024, 1025, 2047, 2048, 2049, 4096, 4097])
+@pytest.mark.parametrize("sampled", [False, True])
+def test_verifications_over_so_many_words(vocab, sampled):
+    # one CTA a request, two, four, eight
+    Verify([3, 1, 4], vocab, sampled=sampled, peak=1.0, seed=vocab).run()
+
+
+@pytest.mark.parametrize("batch,vocab", [(70, 4100), (71, 4100), (140, 2100), (141, 2100), (280, 1100), (281, 1100)])
+def test_verifications_of_so_many_requests(batch, vocab):
+    Verify([1] * (batch - 2) + [3, 0], vocab, seed=batch).run()

@@ -681,7 +681,8 @@ pkv_status pkv_paged_attention_decode_window(
  *   (x_a, x_b) <- (x_a c - x_b s, x_b c + x_a s)      for the pairs j < rot / 2:
  * (a, b) = (j, j + rot / 2), or (2 j, 2 j + 1) where interleaved; c and s are
  * cos_sin[p, j] and cos_sin[p, rot / 2 + j] at the token's position p on the axis
- * of pair j.  q goes to out; k, and v as it is, go to slot slots[i] of the pools
+ * of pair j; elements from rot on are not rotated, and no other one goes into them but
+ * by the mean.  q goes to out; k, and v as it is, go to slot slots[i] of the pools
  * (an MXFP8 pool: quantised from the fp32 values, as pkv_kv_append does).
  *   q, k, v:       [num_tokens, Hq or Hkv, D], head rows contiguous and *_stride
  *                  elements from token to token (a packed projection's parts).

@@ -282,7 +282,11 @@ __device__ __forceinline__ int plan_cta_stages(const Args& a, long long* wsum, i
   const long long S = U * Hkv;
   const long long w = units_per_cta(S, C, su);
   const long long lo = min((long long)c * w, S), hi = min(lo + w, S);
-  if (lo >= hi) return 0;  // uniform over the CTA
+  if (lo >= hi) {  // uniform over the CTA
+    // where no CTA has a stage, the grid still ends behind what it was launched behind
+    if (S == 0) pdl_wait();
+    return 0;
+  }
   // ---- find the stage counts at lo and hi (hi == S: every stage); with
   // units that are stages, the count is hi - lo and only lo is searched
   const bool want_hi = weighted && hi < S;

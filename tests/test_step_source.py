@@ -22,3 +22,16 @@ def test_sums_are_changed_behind_a_barrier():
     for at in writes:
         barrier = max(kernel.rfind("__syncthreads()", 0, at), kernel.rfind("cluster.sync()", 0, at))
         assert barrier > max([r for r in reads if r < at] + [0])
+
+
+def test_a_decode_of_empty_sequences_waits_too():
+    # a kernel that is launched early has to wait for the one in front of it, or it
+    # may be over, and the next one begin, before that is: CTAs without work may
+    # leave, but not all of them
+    leave = re.search(r"if \(lo >= hi\)(.*?)return 0;", source("plan.cuh"), flags=re.S).group(1)
+    assert "if (S == 0) pdl_wait();" in leave
+    # and in the split without a plan the first CTA of each sequence, which has its
+    # result to write
+    for name in ("window_mma.cu", "decode_partial.cuh"):
+        text = source(name)
+        assert re.search(r"if \(n < 0\) \{\s*if \(a\.plan_before_wait\) pdl_wait\(\);", text[:text.index("if (n <= 0)")])

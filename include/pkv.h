@@ -658,7 +658,8 @@ size_t pkv_decode_window_workspace_bytes(const pkv_cache_desc* cache, int32_t nu
  * read, and neither are their table entries' ids: they may be -1
  * (pkv_kv_blocks_update gives such blocks back).  A NaN score of a row that is
  * seen makes that head's out and lse NaN; rows whose scores are -infinity weigh
- * nothing, and a head that sees no other has out 0 and lse -infinity.  Over bf16 and
+ * 0 (times a V that is not finite, NaN), and a head that sees no other has out 0 and
+ * lse -infinity.  Over bf16 and
  * MXFP8 pools a weight meets V in two bf16 terms, within 2^-16 + 2^-23 of itself (lse
  * comes of the fp32 weights); an infinity of V in a row that is seen stays one,
  * unless the row's weight is below 2^-103 of the largest.

@@ -30,7 +30,7 @@ constexpr int kBlRowThreads = 256;
 // Rows whose slots the one CTA writes itself; more are a second launch's.  By itself
 // against that, 1024 threads, us: 8 requests, 1024 rows 5.4 / 6.1, 2048 6.8 / 6.2,
 // 4096 9.1 / 6.6; 64 requests, 2048 6.9 / 7.3, 2560 7.9 / 7.4; 256, 2048 5.8 / 7.0, 2560
-// 8.2 / 8.2; 512, 2048 6.1 / 7.4, 3072 7.1 / 7.5, 4096 8.2 / 7.3.
+// 8.2 / 8.2; 512, 2048 6.1 / 7.4, 4096 8.2 / 7.3.
 constexpr int64_t kBlOwnRows = 2048;
 // Requests (one a thread, one pass) and rows of a call that 128 threads take; 1024
 // take any other.  128 against 1024, us: 1 request, 128 rows 4.0 / 5.2, 256 4.7 / 5.2, 320
